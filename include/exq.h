@@ -81,7 +81,8 @@ typedef enum {
   EXQ_ERR_INVALID_ARG = 1, /* bad pointer, size, alignment or layout        */
   EXQ_ERR_UNSUPPORTED = 2, /* valid, but outside what this build handles    */
   EXQ_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed          */
-  EXQ_ERR_TIMEOUT = 4      /* a device-side wait gave up (from the device)  */
+  EXQ_ERR_TIMEOUT = 4,     /* a device-side wait gave up (from the device)  */
+  EXQ_ERR_FULL = 5         /* the page pool has too few free pages          */
 } exq_status;
 
 typedef enum { EXQ_FMT_GPTQ4 = 1, EXQ_FMT_EXL2 = 2, EXQ_FMT_EXL2_QSCALE = 3 } exq_format;
@@ -365,6 +366,213 @@ exq_status exq_kv_quantize(const uint16_t* x, int64_t n_groups, int32_t D, int32
 exq_status exq_kv_dequantize(const uint32_t* codes, const uint16_t* scales, int64_t n_groups, int32_t D,
                              int32_t bits, uint16_t* x_out, void* stream);
 
+/* ---------------------------------------------------------------- rotary positions */
+
+/* Rotary position embedding of the first R values of a head: the R/2 pairs
+ * (x1, x2) are turned by the angle position * f_j of pair j,
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s,
+ * EXQ_ROPE_HALF pairs values (j, j + R/2), EXQ_ROPE_INTERLEAVED (2j, 2j + 1);
+ * values R .. D-1 pass through. */
+typedef enum { EXQ_ROPE_HALF = 0, EXQ_ROPE_INTERLEAVED = 1 } exq_rope_layout;
+
+/* How frequencies are stretched for contexts longer than the trained one:
+ *  NONE    f_j = base^(-2j/R)
+ *  LINEAR  f_j / factor
+ *  NTK     base * factor^(R/(R-2)) in place of base (R > 2)
+ *  YARN    pairs that turn more than `high` times over orig_ctx tokens keep
+ *          f_j, those that turn less than `low` times get f_j / factor, with
+ *          a linear ramp over the pair index between the two (its ends
+ *          rounded outwards to whole pairs); cos and sin are scaled by
+ *          gain = 0.1 ln(factor) + 1 (1 for factor <= 1)
+ *  BANDS   with t = orig_ctx f_j / 2 pi turns over orig_ctx:
+ *          m = clamp((t - low) / (high - low), 0, 1),
+ *          f_j' = (1 - m) f_j / factor + m f_j */
+typedef enum {
+  EXQ_ROPE_SCALE_NONE = 0,
+  EXQ_ROPE_SCALE_LINEAR = 1,
+  EXQ_ROPE_SCALE_NTK = 2,
+  EXQ_ROPE_SCALE_YARN = 3,
+  EXQ_ROPE_SCALE_BANDS = 4
+} exq_rope_scaling;
+
+/* exq_rope_freqs -- host-only, synchronous: the R/2 frequencies in radians
+ * per position (host double [R/2]) and the gain (host double). orig_ctx, low
+ * and high are read for YARN and BANDS only, factor not for NONE.
+ * EXQ_ERR_INVALID_ARG for NULL outputs, R < 2 or odd, base <= 1, factor <= 0,
+ * NTK with R = 2, orig_ctx <= 0, low <= 0 or high <= low, an unknown scaling. */
+exq_status exq_rope_freqs(int32_t R, double base, int32_t scaling, double factor, double orig_ctx, double low,
+                          double high, double* inv_freq_out, double* gain_out);
+
+/* exq_rope_steps -- host-only, synchronous: frequencies (radians per
+ * position) as fixed-point turns, steps_out[j] = frac(f_j / 2 pi) in units of
+ * 2^-64. The kernels multiply a step by the position in 64-bit integers, and
+ * the overflow drops whole turns, so far positions lose no precision.
+ * EXQ_ERR_INVALID_ARG for NULL buffers, n <= 0 or a frequency that is not
+ * finite. */
+exq_status exq_rope_steps(const double* inv_freq, int32_t n, uint64_t* steps_out);
+
+/* Rotary parameters of a device call. */
+typedef struct {
+  const uint64_t* steps; /* device [R/2], see exq_rope_steps                  */
+  int32_t R;             /* values of a head that turn: even, 2 .. D           */
+  int32_t layout;        /* exq_rope_layout                                   */
+  double gain;           /* factor on cos and sin (1 unless exq_rope_freqs says) */
+} exq_rope_params;
+
+/* fp16 rows of D values per (token, head): token t's head h starts at
+ * data + t * token_stride + h * head_stride (strides in values, multiples of
+ * 8; the D values are contiguous). Inputs are only read. */
+typedef struct {
+  uint16_t* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} exq_rows;
+
+/* exq_rope -- device, asynchronous: y = x turned. cos and sin are computed in
+ * fp64 and rounded once (times gain) to fp32; products, sums (fp32) and the
+ * result (fp16) are each rounded to nearest, so the result is a function of
+ * the inputs alone, bit for bit.
+ *   x, y  rows of n_heads heads; y may be x itself (same strides), else they
+ *         must not overlap
+ *   pos   device int32 [n_tokens], any sign (4-byte aligned)
+ *   grad  0: as above. 1: the transposed map (the angle negated, the same
+ *         gain), which takes the gradient at y to the gradient at x; with
+ *         gain 1 it is also the inverse.
+ * D % 8 == 0, D <= 512, else EXQ_ERR_UNSUPPORTED; n_tokens = 0 or n_heads = 0
+ * launches nothing. EXQ_ERR_INVALID_ARG for bad pointers, strides, R, layout
+ * or a gain that is not finite. */
+exq_status exq_rope(const exq_rope_params* rope, const exq_rows* x, int64_t n_tokens, int32_t n_heads, int32_t D,
+                    const int32_t* pos, const exq_rows* y, int32_t grad, void* stream);
+
+/* ---------------------------------------------------------------- paged KV cache */
+
+/* A cache of n_layers x n_pages pages of page_size token slots. For every
+ * (layer, page, KV head, slot) it holds one group of D values of K and one of
+ * V: with bits 4, 6 or 8 the codec's codes and scale of exq_kv_quantize, with
+ * bits 16 the fp16 values themselves (no scales). Arrays, all device memory:
+ *   k_codes, v_codes    uint32 [n_layers, n_pages, n_kv_heads, page_size, D * bits / 32]
+ *   k_scales, v_scales  fp16   [n_layers, n_pages, n_kv_heads, page_size]; NULL for bits 16
+ * A page id names the same page in every layer. D is 64, 128 or 256;
+ * page_size 16, 32, 64, 128 or 256. The (page, head) block of a layer is
+ * contiguous, and exq_kv_dequantize reads any run of groups as it is. */
+typedef struct {
+  int32_t bits, D, n_kv_heads, page_size, n_pages, n_layers;
+  uint32_t* k_codes;
+  uint16_t* k_scales;
+  uint32_t* v_codes;
+  uint16_t* v_scales;
+} exq_kv_cache;
+
+/* The sequences of one step, new tokens packed one sequence after the other.
+ * Lengths and tables are device memory (4-byte aligned), so a captured graph
+ * can be replayed with other contents. n_tokens, max_q_len and max_kv_len are
+ * host bounds: no sequence may have more (a longer one is reported as below).
+ * Sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1 and hold its
+ * last positions, kv_len[b] - (q_start[b+1] - q_start[b]) .. kv_len[b] - 1.
+ * Position p of sequence b is slot p % page_size of page
+ * page_table[b * max_pages + p / page_size]; entries past its last token are
+ * not read. What the kernels find out of range (a page id outside the cache,
+ * a length above its bound, q_start that falls) they skip and report as
+ * EXQ_ERR_INVALID_ARG in the device error word; results of that sequence are
+ * then unspecified. */
+typedef struct {
+  int32_t n_seqs, n_tokens, max_q_len, max_kv_len, max_pages;
+  const int32_t* q_start;    /* [n_seqs + 1], from 0; rows q_start[n_seqs] and up are padding */
+  const int32_t* kv_len;     /* [n_seqs] cached tokens, the new ones among them */
+  const int32_t* page_table; /* [n_seqs, max_pages]                           */
+} exq_kv_batch;
+
+/* exq_kv_append -- device, asynchronous: writes the new tokens' K and V to
+ * their slots of one layer, with rotary positions and the codec on the way.
+ *   k, v   rows of n_kv_heads heads, n_tokens tokens
+ *   rope   NULL: k is written as it is. Else k is turned as by exq_rope
+ *          (fp16-rounded), then coded; bit for bit what exq_rope and
+ *          exq_kv_quantize give.
+ *   pos    device int32 [n_tokens], the rotary positions, or NULL for the
+ *          tokens' positions in their sequences
+ *   q, q_out  rows of n_heads heads, turned in the same launch (q_out may be
+ *          q itself, with the same strides); both NULL: none (n_heads is
+ *          then ignored); they need rope
+ * Two tokens of a call must not share a slot. Padding rows are left alone.
+ * Status rules as for exq_rope and the cache above; EXQ_ERR_UNSUPPORTED for a
+ * D, bits or page_size outside the sets. n_tokens = 0 launches nothing. */
+exq_status exq_kv_append(const exq_kv_cache* cache, int32_t layer, const exq_kv_batch* batch, const exq_rows* k,
+                         const exq_rows* v, const exq_rope_params* rope, const int32_t* pos, const exq_rows* q,
+                         const exq_rows* q_out, int32_t n_heads, void* stream);
+
+/* Bytes of device workspace exq_paged_attn needs on the current device for
+ * this cache, batch and number of query heads; 0 for arguments it would
+ * refuse. It depends on the batch's bounds only, not on device contents. */
+size_t exq_paged_attn_workspace_size(const exq_kv_cache* cache, const exq_kv_batch* batch, int32_t n_heads);
+
+/* exq_paged_attn -- device, asynchronous: attention of the new tokens over
+ * the cached ones, which hold them already (exq_kv_append). For query head h
+ * of row i at position p of its sequence, over the cached positions t it sees,
+ *   o = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale q . k_t),
+ * with k_t, v_t of KV head h / (n_heads / n_kv_heads); a quantised value is
+ * (u - z) s exactly, not rounded to fp16.
+ *   q       rows of n_heads heads (a multiple of n_kv_heads)
+ *   causal  1: row i sees t <= p. 0: all of its sequence's cached tokens.
+ *   window  0, or the number of latest tokens seen: t > p - window
+ *   scale   finite; commonly 1 / sqrt(D)
+ *   out     rows of n_heads heads, fp16; must not overlap q
+ *   lse     NULL or device fp32 [n_tokens, n_heads]: ln sum_t w_t
+ * A row that sees nothing (an empty sequence, or more new tokens than
+ * cached ones) gives zeros and an lse of -inf. Slots past a sequence's last
+ * token may hold anything, NaN included. Scores, the softmax's maximum and
+ * sum and the output's sums are fp32; the weights are rounded to fp16 for
+ * the matrix instructions (V's scales multiplied in before that rounding).
+ *   workspace  at least exq_paged_attn_workspace_size() bytes, 256-byte
+ *          aligned, its first 64 KB ZERO before the first use; a call that
+ *          completes leaves them zero, and the counters exq_gemv keeps there
+ *          too, so one workspace serves both on one stream. The rest is
+ *          scratch. Calls that may overlap need separate workspaces.
+ * Deterministic: the same inputs give the same bits on the same device.
+ * n_tokens = 0 or n_seqs = 0 launches nothing. */
+exq_status exq_paged_attn(const exq_kv_cache* cache, int32_t layer, const exq_kv_batch* batch, const exq_rows* q,
+                          int32_t n_heads, float scale, int32_t causal, int32_t window, const exq_rows* out, float* lse,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* exq_kv_copy_pages -- device, asynchronous: for every pair (src, dst) of
+ * page ids and every layer, page dst becomes a copy of page src (codes and
+ * scales, K and V).
+ *   pairs  device int32 [n_pairs, 2] (4-byte aligned). No page may be dst of
+ *          two pairs, or dst of one and src of another. An id outside the
+ *          cache skips its pair and is reported in the device error word. */
+exq_status exq_kv_copy_pages(const exq_kv_cache* cache, const int32_t* pairs, int64_t n_pairs, void* stream);
+
+/* Page bookkeeping -- host-only, synchronous, no CUDA. refs is the caller's
+ * host int32 [n_pages]: how many sequences hold each page (0 = free). The
+ * calls check everything first: one that fails changes nothing. */
+
+/* exq_pages_alloc -- takes the n lowest free pages (refs 0 -> 1) into
+ * ids_out [n]; EXQ_ERR_FULL if there are fewer. */
+exq_status exq_pages_alloc(int32_t* refs, int32_t n_pages, int32_t n, int32_t* ids_out);
+
+/* exq_pages_free -- gives up one hold on each of ids [n]. EXQ_ERR_INVALID_ARG
+ * if an id is outside the pool, or named more often than it is held. */
+exq_status exq_pages_free(int32_t* refs, int32_t n_pages, const int32_t* ids, int32_t n);
+
+/* exq_pages_fork -- a second sequence that shares the first n_tokens cached
+ * tokens of one whose pages are ids: its page ids go to ids_out
+ * [ceil(n_tokens / page_size)]. Whole pages are shared (one more hold each);
+ * a partly filled last page, into which both will append, is given a page of
+ * its own, and pair_out [2] = (src, dst) for exq_kv_copy_pages, *n_pairs_out
+ * = 1 (else 0). EXQ_ERR_FULL if that needs a page and none is free. */
+exq_status exq_pages_fork(int32_t* refs, int32_t n_pages, int32_t page_size, const int32_t* ids, int32_t n_tokens,
+                          int32_t* ids_out, int32_t* pair_out, int32_t* n_pairs_out);
+
+/* exq_pages_compact -- moves the held pages to the ids 0 .. held - 1: the
+ * highest held page to the lowest free id, and so on. refs and every id in
+ * tables [n_entries] (all sequences' tables; negative entries are passed over)
+ * are rewritten; pairs_out gets the (src, dst) pairs for exq_kv_copy_pages,
+ * which must run before the pages are used again (room for 2 *
+ * floor(n_pages / 2) int32), *n_pairs_out their number.
+ * EXQ_ERR_INVALID_ARG for a table entry that is outside the pool or names a
+ * free page. */
+exq_status exq_pages_compact(int32_t* refs, int32_t n_pages, int32_t* tables, int64_t n_entries, int32_t* pairs_out,
+                             int32_t* n_pairs_out);
+
 /* ---------------------------------------------------------------- EXL2 conversion */
 
 /* Converting an fp16 weight to EXL2 without calibration data (ExLlamaV2 blog
@@ -425,7 +633,8 @@ const char* exq_status_string(exq_status s);
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: EXQ_OK, EXQ_ERR_TIMEOUT (a kernel gave up waiting) or
  * EXQ_ERR_INVALID_ARG (a kernel met an EXL2 segment width outside the set or
- * past the end of qweight, or a permutation entry outside [0, K)).
+ * past the end of qweight, a permutation entry outside [0, K), or a page id
+ * or length of a paged cache out of range).
  * Returns EXQ_ERR_CUDA if the synchronisation itself fails. */
 exq_status exq_get_last_device_error(void* stream);
 

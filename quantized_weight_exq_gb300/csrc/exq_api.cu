@@ -1,6 +1,7 @@
 // Host entry points of libexq: argument checks, dispatch, status codes.
 // Every check here runs before any launch and has no side effects.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -233,6 +234,136 @@ extern "C" exq_status exq_kv_dequantize(const uint32_t* codes, const uint16_t* s
 }
 
 namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+exq_status check_rows(const exq_rows* r) {
+  if (!r || !r->data || !aligned16(r->data) || r->token_stride % 8 || r->head_stride % 8) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+// rows that are overwritten by a call that reads `in`: in's own rows, or other ones
+exq_status check_in_place(const exq_rows& in, const exq_rows& out) {
+  if (in.data == out.data && (in.token_stride != out.token_stride || in.head_stride != out.head_stride))
+    return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+exq_status check_rope(const exq_rope_params* r, int D) {
+  if (!r || !r->steps || (reinterpret_cast<uintptr_t>(r->steps) & 7u) || r->R < 2 || r->R % 2 || r->R > D)
+    return EXQ_ERR_INVALID_ARG;
+  if (r->layout != EXQ_ROPE_HALF && r->layout != EXQ_ROPE_INTERLEAVED) return EXQ_ERR_INVALID_ARG;
+  if (!std::isfinite(r->gain)) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+exq_status check_cache(const exq_kv_cache* c) {
+  if (!c || c->n_kv_heads <= 0 || c->n_pages <= 0 || c->n_layers <= 0) return EXQ_ERR_INVALID_ARG;
+  if (c->D != 64 && c->D != 128 && c->D != 256) return EXQ_ERR_UNSUPPORTED;
+  if (c->bits != 4 && c->bits != 6 && c->bits != 8 && c->bits != 16) return EXQ_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return EXQ_ERR_UNSUPPORTED;
+  if (c->n_kv_heads > 1024) return EXQ_ERR_UNSUPPORTED;
+  if (!c->k_codes || !c->v_codes || !aligned16(c->k_codes) || !aligned16(c->v_codes)) return EXQ_ERR_INVALID_ARG;
+  if (c->bits == 16) return c->k_scales || c->v_scales ? EXQ_ERR_INVALID_ARG : EXQ_OK;
+  if (!c->k_scales || !c->v_scales || !aligned16(c->k_scales) || !aligned16(c->v_scales)) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+exq_status check_batch(const exq_kv_cache& c, const exq_kv_batch* b) {
+  if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_q_len < 0 || b->max_kv_len < 0 || b->max_pages < 0)
+    return EXQ_ERR_INVALID_ARG;
+  if (b->max_kv_len > static_cast<long long>(b->max_pages) * c.page_size) return EXQ_ERR_INVALID_ARG;
+  if (b->n_seqs == 0 || b->n_tokens == 0) return EXQ_OK;  // nothing to do, the arrays are not looked at
+  if (!b->q_start || !b->kv_len || !aligned4(b->q_start) || !aligned4(b->kv_len)) return EXQ_ERR_INVALID_ARG;
+  if (b->max_pages > 0 && (!b->page_table || !aligned4(b->page_table))) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+int current_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return device_info(dev).sm_count;
+}
+}  // namespace
+
+extern "C" exq_status exq_rope(const exq_rope_params* rope, const exq_rows* x, int64_t n_tokens, int32_t n_heads,
+                               int32_t D, const int32_t* pos, const exq_rows* y, int32_t grad, void* stream) {
+  if (n_tokens < 0 || n_heads < 0 || D <= 0 || (grad != 0 && grad != 1)) return EXQ_ERR_INVALID_ARG;
+  if (D % 8 || D > 512) return EXQ_ERR_UNSUPPORTED;
+  exq_status st = check_rope(rope, D);
+  if (st != EXQ_OK) return st;
+  if (n_tokens == 0 || n_heads == 0) return EXQ_OK;
+  if ((st = check_rows(x)) != EXQ_OK || (st = check_rows(y)) != EXQ_OK || (st = check_in_place(*x, *y)) != EXQ_OK) return st;
+  if (!pos || !aligned4(pos)) return EXQ_ERR_INVALID_ARG;
+  if (current_cc() < 100) return EXQ_ERR_CUDA;
+  return launch_rope(*rope, *x, n_tokens, n_heads, D, pos, *y, grad != 0, current_sms(), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" exq_status exq_kv_append(const exq_kv_cache* cache, int32_t layer, const exq_kv_batch* batch,
+                                    const exq_rows* k, const exq_rows* v, const exq_rope_params* rope,
+                                    const int32_t* pos, const exq_rows* q, const exq_rows* q_out, int32_t n_heads,
+                                    void* stream) {
+  exq_status st = check_cache(cache);
+  if (st != EXQ_OK || (st = check_batch(*cache, batch)) != EXQ_OK) return st;
+  if (layer < 0 || layer >= cache->n_layers) return EXQ_ERR_INVALID_ARG;
+  if (rope ? (st = check_rope(rope, cache->D)) != EXQ_OK : pos != nullptr) return EXQ_ERR_INVALID_ARG;
+  if (!aligned4(pos) || (q == nullptr) != (q_out == nullptr) || (q && (!rope || n_heads <= 0))) return EXQ_ERR_INVALID_ARG;
+  if (batch->n_tokens == 0 || batch->n_seqs == 0) return EXQ_OK;
+  if ((st = check_rows(k)) != EXQ_OK || (st = check_rows(v)) != EXQ_OK) return st;
+  if (q && ((st = check_rows(q)) != EXQ_OK || (st = check_rows(q_out)) != EXQ_OK ||
+            (st = check_in_place(*q, *q_out)) != EXQ_OK))
+    return st;
+  if (current_cc() < 100) return EXQ_ERR_CUDA;
+  return launch_kv_append(*cache, layer, *batch, *k, *v, rope, pos, q, q_out, n_heads, current_sms(),
+                          static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+exq_status check_attn(const exq_kv_cache* cache, const exq_kv_batch* batch, int n_heads) {
+  exq_status st = check_cache(cache);
+  if (st != EXQ_OK || (st = check_batch(*cache, batch)) != EXQ_OK) return st;
+  if (n_heads <= 0 || n_heads % cache->n_kv_heads) return EXQ_ERR_INVALID_ARG;
+  if (n_heads > 4096) return EXQ_ERR_UNSUPPORTED;
+  return EXQ_OK;
+}
+}  // namespace
+
+extern "C" size_t exq_paged_attn_workspace_size(const exq_kv_cache* cache, const exq_kv_batch* batch, int32_t n_heads) {
+  const int sms = current_sms();
+  if (check_attn(cache, batch, n_heads) != EXQ_OK || sms <= 0) return 0;
+  return paged_attn_workspace_bytes(*cache, *batch, n_heads, sms);
+}
+
+extern "C" exq_status exq_paged_attn(const exq_kv_cache* cache, int32_t layer, const exq_kv_batch* batch,
+                                     const exq_rows* q, int32_t n_heads, float scale, int32_t causal, int32_t window,
+                                     const exq_rows* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  exq_status st = check_attn(cache, batch, n_heads);
+  if (st != EXQ_OK) return st;
+  if (layer < 0 || layer >= cache->n_layers || !std::isfinite(scale) || (causal != 0 && causal != 1) || window < 0 ||
+      !aligned4(lse))
+    return EXQ_ERR_INVALID_ARG;
+  if (batch->n_tokens == 0 || batch->n_seqs == 0) return EXQ_OK;
+  if ((st = check_rows(q)) != EXQ_OK || (st = check_rows(out)) != EXQ_OK) return st;
+  if (q->data == out->data) return EXQ_ERR_INVALID_ARG;
+  const int sms = current_sms();
+  if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      ws_bytes < paged_attn_workspace_bytes(*cache, *batch, n_heads, sms))
+    return EXQ_ERR_INVALID_ARG;
+  const AttnCall call{cache, layer, batch, *q, *out, n_heads, scale, causal != 0, window, lse, workspace};
+  return launch_paged_attn(call, sms, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" exq_status exq_kv_copy_pages(const exq_kv_cache* cache, const int32_t* pairs, int64_t n_pairs, void* stream) {
+  const exq_status st = check_cache(cache);
+  if (st != EXQ_OK) return st;
+  if (n_pairs < 0) return EXQ_ERR_INVALID_ARG;
+  if (n_pairs == 0) return EXQ_OK;
+  if (!pairs || !aligned4(pairs)) return EXQ_ERR_INVALID_ARG;
+  if (current_cc() < 100) return EXQ_ERR_CUDA;
+  return launch_kv_copy(*cache, pairs, n_pairs, current_sms(), static_cast<cudaStream_t>(stream));
+}
+
+namespace {
 exq_status check_convert(const uint16_t* W, const int32_t* perm, int K, int N) {
   if (!W || !aligned16(W) || (perm && !aligned16(perm))) return EXQ_ERR_INVALID_ARG;
   if (K <= 0 || N <= 0 || K % 32 || N % 8) return EXQ_ERR_INVALID_ARG;
@@ -277,6 +408,7 @@ extern "C" const char* exq_status_string(exq_status s) {
     case EXQ_ERR_UNSUPPORTED: return "unsupported shape or format";
     case EXQ_ERR_CUDA: return "CUDA error";
     case EXQ_ERR_TIMEOUT: return "device wait timed out";
+    case EXQ_ERR_FULL: return "no free page left";
   }
   return "unknown status";
 }
@@ -284,11 +416,11 @@ extern "C" const char* exq_status_string(exq_status s) {
 extern "C" exq_status exq_get_last_device_error(void* stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned a = take_gemv_errors(s), b = take_dequant_errors(s), c = take_gemm_errors(s),
-                 d = take_convert_errors(s);
-  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u) return EXQ_ERR_CUDA;
-  const unsigned v = a | b | c | d;
+                 d = take_convert_errors(s), e = take_kv_errors(s), f = take_attn_errors(s);
+  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u || e == ~0u || f == ~0u) return EXQ_ERR_CUDA;
+  const unsigned v = a | b | c | d | e | f;
   if (v & kDevErrTimeout) return EXQ_ERR_TIMEOUT;
-  if (v & (kDevErrBadSegment | kDevErrBadPerm)) return EXQ_ERR_INVALID_ARG;
+  if (v & (kDevErrBadSegment | kDevErrBadPerm | kDevErrBadPage)) return EXQ_ERR_INVALID_ARG;
   return EXQ_OK;
 }
 

@@ -14,6 +14,7 @@ enum : unsigned {
   kDevErrTimeout = 1u,      // a bounded wait gave up
   kDevErrBadSegment = 2u,   // an EXL2 segment width outside {2,3,4,5,6,8} or past the end
   kDevErrBadPerm = 4u,      // a permutation entry outside [0, K)
+  kDevErrBadPage = 8u,      // a page id, length or row range of a paged cache out of range
 };
 
 // failure-detection test hook (exq_testing.h): 0 = off, else the wait bound
@@ -63,6 +64,31 @@ exq_status launch_kv_quantize(const uint16_t* x, long long n_groups, int D, int 
 exq_status launch_kv_dequantize(const uint32_t* codes, const uint16_t* scales, long long n_groups, int D, int b,
                                 uint16_t* x_out, cudaStream_t stream);
 
+// rotary positions (arguments checked by the caller)
+exq_status launch_rope(const exq_rope_params& rope, const exq_rows& x, long long n_tokens, int n_heads, int D,
+                       const int32_t* pos, const exq_rows& y, bool grad, int sms, cudaStream_t stream);
+
+// paged KV cache (arguments checked by the caller; rope, pos, q and q_out may be NULL)
+exq_status launch_kv_append(const exq_kv_cache& c, int layer, const exq_kv_batch& batch, const exq_rows& k,
+                            const exq_rows& v, const exq_rope_params* rope, const int32_t* pos, const exq_rows* q,
+                            const exq_rows* q_out, int n_heads, int sms, cudaStream_t stream);
+exq_status launch_kv_copy(const exq_kv_cache& c, const int32_t* pairs, long long n_pairs, int sms, cudaStream_t stream);
+
+struct AttnCall {
+  const exq_kv_cache* cache;
+  int layer;
+  const exq_kv_batch* batch;
+  exq_rows q, out;
+  int n_heads;
+  float scale;
+  bool causal;
+  int window;
+  float* lse;
+  void* workspace;
+};
+exq_status launch_paged_attn(const AttnCall& c, int sms, cudaStream_t stream);
+size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& batch, int n_heads, int sms);
+
 // EXL2 conversion: RTN quantiser into the EXL2 layout, and the error table
 exq_status launch_rtn_quantize(const uint16_t* W, const int32_t* perm, int K, int N, const uint32_t* seg_off,
                                int n_word_rows, uint32_t* qweight, uint16_t* scales, cudaStream_t stream);
@@ -76,5 +102,7 @@ unsigned take_gemv_errors(cudaStream_t stream);
 unsigned take_dequant_errors(cudaStream_t stream);
 unsigned take_gemm_errors(cudaStream_t stream);
 unsigned take_convert_errors(cudaStream_t stream);
+unsigned take_kv_errors(cudaStream_t stream);
+unsigned take_attn_errors(cudaStream_t stream);
 
 }  // namespace exq

@@ -19,10 +19,15 @@
 // as one contiguous block (D * 2 bytes of fp16, D * b / 8 bytes of codes); all
 // of a warp's loads are issued before any of its arithmetic, to keep enough
 // bytes in flight per SM.
+//
+// Below the codec: the append to a paged cache, which runs the same codec on
+// rotated keys, and the copy of pages.
+#include <algorithm>
 #include <type_traits>
 
 #include "exq_device.cuh"
 #include "exq_internal.h"
+#include "exq_rope.cuh"
 
 namespace exq {
 namespace {
@@ -136,14 +141,62 @@ __device__ __forceinline__ void store_words(unsigned long long chunk, uint32_t* 
   }
 }
 
+// One group from the lanes' values (fp16 bits h): codes and scale.
+template <int VPL, int B>
+__device__ __forceinline__ void quantize_group(const uint32_t (&h)[VPL], uint32_t* __restrict__ dst,
+                                               uint16_t* __restrict__ scale, int lane) {
+  constexpr int kWords = VPL * B;      // words of a group: 32 VPL values of B bits
+  constexpr int kChunk = VPL * B;      // bits of one lane (8..64)
+  constexpr int kQmax = (1 << (B - 1)) - 1;
+  float xf[VPL];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    xf[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(h[i])));
+    amax = fmaxf(amax, fabsf(xf[i]));
+  }
+  // non-negative floats order as their bit patterns
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  static_assert(kQmax == 7 || kQmax == 31 || kQmax == 127, "div_by_const is checked for these only");
+  const __half s16 = __float2half_rn(div_by_const<kQmax>(amax));
+  const float s = __half2float(s16);
+  const float inv = s != 0.f ? rcp_approx(s) : 0.f;  // s = 0: every q is 0
+
+  // q = rint(fp32_RN(x / s)): from x * inv, except where that lies within
+  // 2^-14 of a half-integer; one test per lane for its VPL values
+  int q[VPL];
+  bool near_tie = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float r = xf[i] * inv;
+    q[i] = __float2int_rn(r);
+    near_tie |= fabsf(r - static_cast<float>(q[i])) > 0.5f - 0x1p-14f;
+  }
+  if (near_tie)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) q[i] = __float2int_rn(__fdiv_rn(xf[i], s));
+  // A normal fp16 s is within 2^-11 (plus the fp32 quotient's 2^-24) of
+  // amax / qmax, so |x / s| < qmax (1 + 2^-10) < qmax + 1/2 and every q is
+  // already in range; only a subnormal s (amax < 2^-14 qmax), with fewer
+  // significant bits, needs the clamp. The test is the same for the whole
+  // warp (s is the group's).
+  if (s < 0x1p-14f)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) q[i] = max(-kQmax - 1, min(kQmax, q[i]));
+  using Chunk = std::conditional_t<(kChunk <= 32), uint32_t, unsigned long long>;
+  Chunk chunk = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) chunk |= static_cast<Chunk>(q[i] + (1 << (B - 1))) << (i * B);
+  store_words<kChunk, kWords>(chunk, dst, lane);
+  if (lane == 0) *scale = __half_as_ushort(s16);
+}
+
 template <int VPL, int B, int GPW>
 __global__ void __launch_bounds__(kWarps * 32)
     kv_quantize_kernel(const uint16_t* __restrict__ x, long long n_groups, uint32_t* __restrict__ codes,
                        uint16_t* __restrict__ scales) {
   constexpr int D = 32 * VPL;
   constexpr int kWords = D * B / 32;   // words of a group
-  constexpr int kChunk = VPL * B;      // bits of one lane (8..64)
-  constexpr int kQmax = (1 << (B - 1)) - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the block's groups: k * kWarps + warp, k < GPW (each k a contiguous run of kWarps groups)
   const long long g0 = static_cast<long long>(blockIdx.x) * kWarps * GPW + warp;
@@ -162,47 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (g >= n_groups) break;  // warp-uniform
     uint32_t h[VPL];
     unpack_halves<VPL>(raw[k], h);
-    float xf[VPL];
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      xf[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(h[i])));
-      amax = fmaxf(amax, fabsf(xf[i]));
-    }
-    // non-negative floats order as their bit patterns
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    static_assert(kQmax == 7 || kQmax == 31 || kQmax == 127, "div_by_const is checked for these only");
-    const __half s16 = __float2half_rn(div_by_const<kQmax>(amax));
-    const float s = __half2float(s16);
-    const float inv = s != 0.f ? rcp_approx(s) : 0.f;  // s = 0: every q is 0
-
-    // q = rint(fp32_RN(x / s)): from x * inv, except where that lies within
-    // 2^-14 of a half-integer; one test per lane for its VPL values
-    int q[VPL];
-    bool near_tie = false;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float r = xf[i] * inv;
-      q[i] = __float2int_rn(r);
-      near_tie |= fabsf(r - static_cast<float>(q[i])) > 0.5f - 0x1p-14f;
-    }
-    if (near_tie)
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) q[i] = __float2int_rn(__fdiv_rn(xf[i], s));
-    // A normal fp16 s is within 2^-11 (plus the fp32 quotient's 2^-24) of
-    // amax / qmax, so |x / s| < qmax (1 + 2^-10) < qmax + 1/2 and every q is
-    // already in range; only a subnormal s (amax < 2^-14 qmax), with fewer
-    // significant bits, needs the clamp. The test is the same for the whole
-    // warp (s is the group's).
-    if (s < 0x1p-14f)
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) q[i] = max(-kQmax - 1, min(kQmax, q[i]));
-    using Chunk = std::conditional_t<(kChunk <= 32), uint32_t, unsigned long long>;
-    Chunk chunk = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) chunk |= static_cast<Chunk>(q[i] + (1 << (B - 1))) << (i * B);
-    store_words<kChunk, kWords>(chunk, codes + g * kWords, lane);
-    if (lane == 0) scales[g] = __half_as_ushort(s16);
+    quantize_group<VPL, B>(h, codes + g * kWords, scales + g, lane);
   }
 }
 
@@ -252,6 +265,241 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
+// ---------------------------------------------------------------- paged cache: append
+
+__device__ unsigned g_kv_err;
+
+struct AppendArgs {
+  // batch
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int n_seqs, n_tokens, max_pages, max_q_len, max_kv_len;
+  // cache, its arrays at the layer
+  uint32_t* codes[2];   // K, V
+  uint16_t* scales[2];
+  int n_kv_heads, page_size, n_pages, D;
+  // rows
+  const uint16_t* in[3];  // q, k, v
+  uint16_t* q_out;
+  long long ts[4], hs[4]; // strides of q, k, v, q_out
+  int n_q;                // query heads (0: none)
+  // rotary
+  const uint64_t* steps;
+  const int32_t* pos;
+  double gain;
+  int R, interleaved;
+  int shift;              // log2 of the tokens of a block
+  int rows_per;           // rows (q, k and v heads) of a token that one block does
+};
+
+struct TokenPlace {
+  int pos;        // rotary position
+  int block;      // page, or -1: nothing to do for this token
+  int slot;
+};
+
+// Where token t goes, by one warp: its sequence is the last with
+// q_start <= t (counted by the lanes over all sequences).
+__device__ __forceinline__ TokenPlace find_place(const AppendArgs& a, int t, int lane) {
+  int n = 0;
+  for (int b = lane; b < a.n_seqs; b += 32) n += __ldg(a.q_start + b) <= t ? 1 : 0;
+  const int b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n))) - 1;
+  TokenPlace p{0, -1, 0};
+  const int end = __ldg(a.q_start + a.n_seqs);
+  if (t >= end) return p;  // padding
+  const int first = b >= 0 ? __ldg(a.q_start + b) : 0, next = b >= 0 ? __ldg(a.q_start + b + 1) : 0;
+  bool ok = b >= 0 && next > t && next - first <= a.max_q_len;  // else q_start falls somewhere, or a bound is wrong
+  if (ok) {
+    const int len = __ldg(a.kv_len + b), at = len - (next - t);
+    ok = len <= a.max_kv_len && at >= 0;  // max_kv_len <= max_pages * page_size
+    if (ok) {
+      const int page = __ldg(a.page_table + static_cast<long long>(b) * a.max_pages + at / a.page_size);
+      ok = page >= 0 && page < a.n_pages;
+      if (ok) {
+        p.pos = a.pos ? __ldg(a.pos + t) : at;
+        p.block = page;
+        p.slot = at % a.page_size;
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicOr(&g_kv_err, kDevErrBadPage);
+  return p;
+}
+
+// A lane's values [lane VPL, lane VPL + VPL) of a row, turned. Partners of
+// HALF pairs come from the lane that holds them (R/2 a multiple of VPL), or
+// are read from the row in memory.
+template <int VPL>
+__device__ __forceinline__ void rotate_lane(uint32_t (&h)[VPL], const uint16_t* row, const float2* cs, int R,
+                                            bool interleaved, int lane) {
+  const int half = R / 2, d0 = lane * VPL;
+  uint32_t other[VPL];
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) other[i] = h[i ^ 1];
+  } else if (half % VPL == 0) {  // the same for all lanes
+    const int src = d0 < half ? lane + half / VPL : lane - half / VPL;
+#pragma unroll
+    for (int i = 0; i < VPL; i += 2) {
+      const uint32_t two = __shfl_sync(0xffffffffu, h[i] | (h[i + 1] << 16), src & 31);
+      other[i] = two & 0xFFFFu;
+      other[i + 1] = two >> 16;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int d = d0 + i;
+      other[i] = d < R ? row[d < half ? d + half : d - half] : 0u;
+    }
+    __syncwarp();  // q_out may be the row itself: every partner is read before any lane writes
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int d = d0 + i;
+    if (d >= R) continue;
+    const bool first = interleaved ? (i & 1) == 0 : d < half;
+    const float2 c = cs[interleaved ? d / 2 : first ? d : d - half];
+    const float x = half_bits_to_float(h[i]), o = half_bits_to_float(other[i]);
+    h[i] = float_to_half_bits(first ? rope_first(x, o, c) : rope_second(o, x, c));
+  }
+}
+
+// Bound by HBM for many tokens (2 bytes read a value, 2 or B / 8 written), by
+// latency for one: a block holds 1 .. 8 tokens, each done by 8 / tokens of
+// its warps, and where tokens are few the rows of a token are split over
+// blocks. A warp does a row (one head of q, k or v) at a time, four rows'
+// loads ahead of their arithmetic; cos and sin are computed once per block.
+template <int VPL, int B>
+__global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  extern __shared__ float2 cs[];
+  __shared__ TokenPlace places[kWarps];
+  constexpr int D = 32 * VPL;
+  constexpr int kU = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tokens = 1 << a.shift;
+  const int t0 = blockIdx.x << a.shift;
+  if (warp < tokens) {
+    TokenPlace p{0, -1, 0};
+    if (t0 + warp < a.n_tokens) p = find_place(a, t0 + warp, lane);
+    if (lane == 0) places[warp] = p;
+  }
+  __syncthreads();
+  const int half = a.R / 2;
+  for (int i = threadIdx.x; i < tokens * half; i += kWarps * 32) {  // R = 0: no rotary positions
+    const int tk = i / half, j = i - tk * half;
+    if (places[tk].block >= 0)
+      cs[i] = rope_cos_sin(__ldg(reinterpret_cast<const unsigned long long*>(a.steps) + j), places[tk].pos, a.gain, false);
+  }
+  __syncthreads();
+
+  const int tk = warp & (tokens - 1), stride = kWarps >> a.shift;
+  const TokenPlace p = places[tk];
+  if (p.block < 0) return;  // warp-uniform
+  const long long t = t0 + tk;
+  const float2* table = cs + tk * half;
+  const int rows = a.n_q + 2 * a.n_kv_heads;
+  const int r1 = min(rows, static_cast<int>(blockIdx.y + 1) * a.rows_per);
+  using V = typename Vec<VPL>::T;
+  for (int r0 = blockIdx.y * a.rows_per + (warp >> a.shift); r0 < r1; r0 += kU * stride) {
+    V raw[kU];
+    const uint16_t* src[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int r = r0 + k * stride;
+      if (r < r1) {
+        const int which = r < a.n_q ? 0 : r < a.n_q + a.n_kv_heads ? 1 : 2;
+        const int head = which == 0 ? r : which == 1 ? r - a.n_q : r - a.n_q - a.n_kv_heads;
+        const uint16_t* base = which == 0 ? a.in[0] : which == 1 ? a.in[1] : a.in[2];
+        const long long ts = which == 0 ? a.ts[0] : which == 1 ? a.ts[1] : a.ts[2];
+        const long long hs = which == 0 ? a.hs[0] : which == 1 ? a.hs[1] : a.hs[2];
+        src[k] = base + t * ts + head * hs;
+        raw[k] = *reinterpret_cast<const V*>(src[k] + lane * VPL);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int r = r0 + k * stride;
+      if (r >= r1) break;  // warp-uniform
+      uint32_t h[VPL];
+      unpack_halves<VPL>(raw[k], h);
+      if (half > 0 && r < a.n_q + a.n_kv_heads) rotate_lane<VPL>(h, src[k], table, a.R, a.interleaved, lane);
+      uint16_t* dst16 = nullptr;
+      if (r < a.n_q) {
+        dst16 = a.q_out + t * a.ts[3] + r * a.hs[3];
+      } else {
+        const int v = r < a.n_q + a.n_kv_heads ? 0 : 1;
+        const int head = r - a.n_q - (v ? a.n_kv_heads : 0);
+        const long long g = (static_cast<long long>(p.block) * a.n_kv_heads + head) * a.page_size + p.slot;
+        if constexpr (B == 16)
+          dst16 = reinterpret_cast<uint16_t*>(v ? a.codes[1] : a.codes[0]) + g * D;
+        else
+          quantize_group<VPL, B>(h, (v ? a.codes[1] : a.codes[0]) + g * (VPL * B),
+                                 (v ? a.scales[1] : a.scales[0]) + g, lane);
+      }
+      if (dst16) {
+        uint32_t out[VPL / 2];
+#pragma unroll
+        for (int i = 0; i < VPL / 2; ++i) out[i] = h[2 * i] | (h[2 * i + 1] << 16);
+        *reinterpret_cast<V*>(dst16 + lane * VPL) = *reinterpret_cast<const V*>(out);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- paged cache: copies
+
+struct CopyArgs {
+  uint8_t* base[4];          // k_codes, v_codes, k_scales, v_scales
+  long long page_bytes[4];   // 0: absent
+  int pieces[4];             // pieces of kCopyPiece bytes of a page of each
+  int per_page;              // their sum
+  const int32_t* pairs;
+  long long n_pairs;
+  int n_pages, n_layers;
+};
+
+constexpr int kCopyPiece = 256 * 16 * 4;  // four 16-byte loads in flight a thread
+
+// Bound by HBM: a block takes pieces of 16 KB, of any (pair, layer, array) in
+// turn, and issues a piece's loads before its stores.
+__global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
+  const long long total = a.n_pairs * a.n_layers * a.per_page;
+  for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+    const long long pl = w / a.per_page;
+    int piece = static_cast<int>(w - pl * a.per_page);
+    const int layer = static_cast<int>(pl % a.n_layers);
+    const long long pair = pl / a.n_layers;
+    const int src = __ldg(a.pairs + 2 * pair), dst = __ldg(a.pairs + 2 * pair + 1);
+    if (src < 0 || src >= a.n_pages || dst < 0 || dst >= a.n_pages) {
+      if (threadIdx.x == 0) atomicOr(&g_kv_err, kDevErrBadPage);
+      continue;
+    }
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (k == i && piece >= a.pieces[i]) {
+        piece -= a.pieces[i];
+        k = i + 1;
+      }
+    const long long bytes = k == 0 ? a.page_bytes[0] : k == 1 ? a.page_bytes[1] : k == 2 ? a.page_bytes[2] : a.page_bytes[3];
+    uint8_t* base = k == 0 ? a.base[0] : k == 1 ? a.base[1] : k == 2 ? a.base[2] : a.base[3];
+    const long long layer0 = static_cast<long long>(layer) * a.n_pages;
+    const uint4* from = reinterpret_cast<const uint4*>(base + (layer0 + src) * bytes);
+    uint4* to = reinterpret_cast<uint4*>(base + (layer0 + dst) * bytes);
+    const long long i0 = static_cast<long long>(piece) * (kCopyPiece / 16) + threadIdx.x, n = bytes / 16;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + 256 * j < n) v[j] = __ldcs(from + i0 + 256 * j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i0 + 256 * j < n) __stcs(to + i0 + 256 * j, v[j]);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
 constexpr int kGpw = 4;  // groups per warp
 
 using QuantFn = void (*)(const uint16_t*, long long, uint32_t*, uint16_t*);
@@ -289,6 +537,99 @@ exq_status launch_kv_dequantize(const uint32_t* codes, const uint16_t* scales, l
       D == 64 ? dequant_for_bits<2>(b) : D == 128 ? dequant_for_bits<4>(b) : dequant_for_bits<8>(b);
   fn<<<grid_for(n_groups), kWarps * 32, 0, stream>>>(codes, scales, n_groups, x_out);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
+namespace {
+
+template <int VPL>
+void (*append_for_bits(int b))(const AppendArgs) {
+  return b == 4 ? kv_append_kernel<VPL, 4>
+                : b == 6 ? kv_append_kernel<VPL, 6> : b == 8 ? kv_append_kernel<VPL, 8> : kv_append_kernel<VPL, 16>;
+}
+
+}  // namespace
+
+exq_status launch_kv_append(const exq_kv_cache& c, int layer, const exq_kv_batch& batch, const exq_rows& k,
+                            const exq_rows& v, const exq_rope_params* rope, const int32_t* pos, const exq_rows* q,
+                            const exq_rows* q_out, int n_heads, int sms, cudaStream_t stream) {
+  AppendArgs a{};
+  a.q_start = batch.q_start;
+  a.kv_len = batch.kv_len;
+  a.page_table = batch.page_table;
+  a.n_seqs = batch.n_seqs;
+  a.n_tokens = batch.n_tokens;
+  a.max_pages = batch.max_pages;
+  a.max_q_len = batch.max_q_len;
+  a.max_kv_len = batch.max_kv_len;
+  const long long groups = static_cast<long long>(c.n_pages) * c.n_kv_heads * c.page_size * layer;  // before the layer
+  a.codes[0] = c.k_codes + groups * (c.D * c.bits / 32);
+  a.codes[1] = c.v_codes + groups * (c.D * c.bits / 32);
+  if (c.bits != 16) {
+    a.scales[0] = c.k_scales + groups;
+    a.scales[1] = c.v_scales + groups;
+  }
+  a.n_kv_heads = c.n_kv_heads;
+  a.page_size = c.page_size;
+  a.n_pages = c.n_pages;
+  a.D = c.D;
+  const exq_rows* rows[3] = {q, &k, &v};
+  for (int i = 0; i < 3; ++i)
+    if (rows[i]) {
+      a.in[i] = rows[i]->data;
+      a.ts[i] = rows[i]->token_stride;
+      a.hs[i] = rows[i]->head_stride;
+    }
+  if (q) {
+    a.q_out = q_out->data;
+    a.ts[3] = q_out->token_stride;
+    a.hs[3] = q_out->head_stride;
+    a.n_q = n_heads;
+  }
+  if (rope) {
+    a.steps = rope->steps;
+    a.pos = pos;
+    a.gain = rope->gain;
+    a.R = rope->R;
+    a.interleaved = rope->layout == EXQ_ROPE_INTERLEAVED;
+  }
+  // tokens of a block: about one cos and sin a thread, and enough blocks to fill the SMs
+  const int all = a.n_q + 2 * a.n_kv_heads;
+  while (a.shift < 3 && (a.R / 2) << (a.shift + 1) <= kWarps * 32 && (a.n_tokens >> (a.shift + 1)) >= 2 * sms) ++a.shift;
+  const int gx = static_cast<int>((static_cast<long long>(a.n_tokens) + (1 << a.shift) - 1) >> a.shift);
+  const int splits = std::min(std::max(1, (2 * sms + gx - 1) / gx), (all + kWarps - 1) / kWarps);
+  a.rows_per = (all + splits - 1) / splits;
+  const dim3 grid(gx, (all + a.rows_per - 1) / a.rows_per);
+  const size_t smem = (static_cast<size_t>(a.R / 2) << a.shift) * sizeof(float2);
+  auto fn = c.D == 64 ? append_for_bits<2>(c.bits) : c.D == 128 ? append_for_bits<4>(c.bits) : append_for_bits<8>(c.bits);
+  fn<<<grid, kWarps * 32, smem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
+exq_status launch_kv_copy(const exq_kv_cache& c, const int32_t* pairs, long long n_pairs, int sms, cudaStream_t stream) {
+  CopyArgs a{};
+  const long long slots = static_cast<long long>(c.n_kv_heads) * c.page_size;
+  void* base[4] = {c.k_codes, c.v_codes, c.k_scales, c.v_scales};
+  for (int i = 0; i < 4; ++i) {
+    a.base[i] = static_cast<uint8_t*>(base[i]);
+    a.page_bytes[i] = i < 2 ? slots * c.D * c.bits / 8 : c.bits == 16 ? 0 : slots * 2;
+    a.pieces[i] = static_cast<int>((a.page_bytes[i] + kCopyPiece - 1) / kCopyPiece);
+    a.per_page += a.pieces[i];
+  }
+  a.pairs = pairs;
+  a.n_pairs = n_pairs;
+  a.n_pages = c.n_pages;
+  a.n_layers = c.n_layers;
+  const long long total = n_pairs * c.n_layers * a.per_page;
+  kv_copy_kernel<<<static_cast<unsigned>(std::min<long long>(total, 8ll * sms)), 256, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
+unsigned take_kv_errors(cudaStream_t stream) {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, g_kv_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return ~0u;
+  if (cudaMemcpyToSymbolAsync(g_kv_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess) return ~0u;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return ~0u;
+  return v;
 }
 
 }  // namespace exq

@@ -22,10 +22,14 @@ EXQ_ERR_INVALID_ARG = 1
 EXQ_ERR_UNSUPPORTED = 2
 EXQ_ERR_CUDA = 3
 EXQ_ERR_TIMEOUT = 4
+EXQ_ERR_FULL = 5
 
 EXQ_FMT_GPTQ4 = 1
 EXQ_FMT_EXL2 = 2
 EXQ_FMT_EXL2_QSCALE = 3
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN, ROPE_SCALE_BANDS = range(5)
 
 # every symbol include/exq.h declares
 EXPORTED = (
@@ -34,6 +38,8 @@ EXPORTED = (
     "exq_gemv", "exq_gemv_multi_workspace_size", "exq_gemv_multi", "exq_gemm_workspace_size", "exq_gemm", "exq_gemm_multi_workspace_size", "exq_gemm_multi", "exq_gemm_noalloc", "exq_status_string",
     "exq_get_last_device_error", "exq_kv_quantize", "exq_kv_dequantize",
     "exq_quantize_exl2", "exq_measure_exl2_workspace_size", "exq_measure_exl2", "exq_solve_exl2_bits",
+    "exq_rope_freqs", "exq_rope_steps", "exq_rope", "exq_kv_append", "exq_paged_attn_workspace_size", "exq_paged_attn",
+    "exq_kv_copy_pages", "exq_pages_alloc", "exq_pages_free", "exq_pages_fork", "exq_pages_compact",
     "exq_testing_starve",
 )
 
@@ -60,13 +66,31 @@ class exq_weight(ctypes.Structure):
     ]
 
 
+class exq_rope_params(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_void_p), ("R", ctypes.c_int32), ("layout", ctypes.c_int32), ("gain", ctypes.c_double)]
+
+
+class exq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class exq_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("bits", "D", "n_kv_heads", "page_size", "n_pages", "n_layers")] + [
+        (n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")]
+
+
+class exq_kv_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_tokens", "max_q_len", "max_kv_len", "max_pages")] + [
+        (n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")]
+
+
 def _load():
     if not _LIB_PATH.exists():
         raise ImportError(f"{_LIB_PATH} is not built; run quantized_weight_exq_gb300/build.py "
                           "(or __graft_entry__.build())")
     lib = ctypes.CDLL(str(_LIB_PATH))
     P, i32, i64, sz, st = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
-    W = ctypes.POINTER(exq_weight)
+    W, dbl = ctypes.POINTER(exq_weight), ctypes.c_double
     sig = {
         "exq_pack_gptq": (st, [P, P, P, i32, i32, i32, P, P, P]),
         "exq_pack_exl2": (st, [P, P, i32, i32, P, P]),
@@ -89,6 +113,17 @@ def _load():
         "exq_measure_exl2_workspace_size": (sz, [i32, i32]),
         "exq_measure_exl2": (st, [P, P, i32, i32, P, P, sz, P]),
         "exq_solve_exl2_bits": (st, [P, i32, i64, P]),
+        "exq_rope_freqs": (st, [i32, dbl, i32, dbl, dbl, dbl, dbl, P, P]),
+        "exq_rope_steps": (st, [P, i32, P]),
+        "exq_rope": (st, [P, P, i64, i32, i32, P, P, i32, P]),
+        "exq_kv_append": (st, [P, i32, P, P, P, P, P, P, P, i32, P]),
+        "exq_paged_attn_workspace_size": (sz, [P, P, i32]),
+        "exq_paged_attn": (st, [P, i32, P, P, i32, ctypes.c_float, i32, i32, P, P, P, sz, P]),
+        "exq_kv_copy_pages": (st, [P, P, i64, P]),
+        "exq_pages_alloc": (st, [P, i32, i32, P]),
+        "exq_pages_free": (st, [P, i32, P, i32]),
+        "exq_pages_fork": (st, [P, i32, i32, P, i32, P, P, P]),
+        "exq_pages_compact": (st, [P, i32, P, i64, P, P]),
         "exq_status_string": (ctypes.c_char_p, [st]),
         "exq_get_last_device_error": (st, [P]),
         "exq_testing_starve": (None, [i32]),
@@ -392,6 +427,228 @@ def exq_kv_dequantize(codes, scales, D: int, bits: int, out=None, stream=None):
     _check(_lib.exq_kv_dequantize(codes.data_ptr(), scales.data_ptr(), G, D, bits, out.data_ptr(),
                                   _stream_ptr(stream)), "exq_kv_dequantize")
     return out
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def exq_rope_freqs(R: int, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE, factor: float = 1.0,
+                   orig_ctx: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """Host: (frequencies float64 [R/2] in radians per position, gain)."""
+    out = np.empty(max(int(R) // 2, 1), dtype=np.float64)
+    gain = ctypes.c_double()
+    _check(_lib.exq_rope_freqs(R, base, scaling, factor, orig_ctx, low, high, _np_ptr(out), ctypes.byref(gain)),
+           "exq_rope_freqs")
+    return out, gain.value
+
+
+def exq_rope_steps(inv_freq: np.ndarray) -> np.ndarray:
+    """Host: frequencies (radians per position) -> uint64 turns per position in units of 2^-64."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    out = np.empty(f.size, dtype=np.uint64)
+    _check(_lib.exq_rope_steps(_np_ptr(f), f.size, _np_ptr(out)), "exq_rope_steps")
+    return out
+
+
+class Rope:
+    """Rotary parameters on the GPU: steps int64 [R/2] (uint64 bits, exq_rope_steps), the layout and the gain."""
+
+    def __init__(self, steps, R: int, layout: int = ROPE_HALF, gain: float = 1.0):
+        if steps.numel() < R // 2 or steps.element_size() != 8 or not steps.is_contiguous():
+            raise ExqError(EXQ_ERR_INVALID_ARG, "Rope")
+        self.steps, self.R, self.layout, self.gain = steps, R, layout, gain
+        self._desc = exq_rope_params(steps.data_ptr(), R, layout, gain)
+
+
+def rope_table(R: int, layout: int = ROPE_HALF, device="cuda", **freqs) -> Rope:
+    """A Rope from exq_rope_freqs(R, **freqs) and exq_rope_steps."""
+    import torch
+    f, gain = exq_rope_freqs(R, **freqs)
+    return Rope(torch.from_numpy(exq_rope_steps(f).view(np.int64)).to(device), R, layout, gain)
+
+
+def _rows(x, where: str, D: Optional[int] = None, heads: Optional[int] = None, tokens: Optional[int] = None):
+    """Descriptor of fp16 [tokens, heads, D] with a contiguous last axis."""
+    t, h, d = x.shape
+    if (x.element_size() != 2 or not x.is_floating_point() or (D is not None and d != D) or (heads is not None and h != heads)
+            or (tokens is not None and t < tokens)):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    st, sh, sd = x.stride()
+    if sd != 1 and d > 1:
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    return exq_rows(x.data_ptr(), st, sh)
+
+
+def exq_rope(x, pos, rope: Rope, out=None, grad: bool = False, stream=None):
+    """x fp16 [tokens, heads, D] turned by the positions pos int32 [tokens] (grad: the transposed map, from the gradient at
+    the result to the gradient at x). ``out`` may be x."""
+    import torch
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty(T, H, D, dtype=torch.float16, device=x.device)
+    if pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ExqError(EXQ_ERR_INVALID_ARG, "exq_rope")
+    xr, yr = _rows(x, "exq_rope"), _rows(out, "exq_rope", D, H, T)
+    _check(_lib.exq_rope(ctypes.byref(rope._desc), ctypes.byref(xr), T, H, D, pos.data_ptr(), ctypes.byref(yr), int(grad),
+                         _stream_ptr(stream)), "exq_rope")
+    return out
+
+
+# ---------------------------------------------------------------- paged KV cache
+
+class KVCache:
+    """A paged cache on the GPU: k_codes, v_codes int32 [layers, pages, KV heads, page_size, D * bits / 32] (uint32 words;
+    fp16 pairs for bits 16), k_scales, v_scales fp16 [layers, pages, KV heads, page_size] (None for bits 16)."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, bits: int):
+        L, P, H, S, W = k_codes.shape
+        for t, n in ((k_codes, 4), (v_codes, 4), (k_scales, 2), (v_scales, 2)):
+            if t is None:
+                continue
+            if t.element_size() != n or tuple(t.shape[:4]) != (L, P, H, S) or not t.is_contiguous():
+                raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
+        if v_codes.shape != k_codes.shape or W * 32 % bits or (k_scales is None) != (v_scales is None):
+            raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.bits, self.D, self.n_kv_heads, self.page_size, self.n_pages, self.n_layers = bits, W * 32 // bits, H, S, P, L
+        self._desc = exq_kv_cache(bits, self.D, H, S, P, L, k_codes.data_ptr(),
+                                  None if k_scales is None else k_scales.data_ptr(), v_codes.data_ptr(),
+                                  None if v_scales is None else v_scales.data_ptr())
+
+
+def kv_cache(n_layers: int, n_pages: int, n_kv_heads: int, page_size: int, D: int, bits: int, device="cuda") -> KVCache:
+    """A KVCache with memory of its own (contents undefined until exq_kv_append writes them)."""
+    import torch
+    shape = (n_layers, n_pages, n_kv_heads, page_size)
+    codes = [torch.empty(*shape, D * bits // 32, dtype=torch.int32, device=device) for _ in range(2)]
+    scales = [None if bits == 16 else torch.empty(shape, dtype=torch.float16, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales, bits)
+
+
+class KVBatch:
+    """The sequences of one step: q_start int32 [B + 1], kv_len int32 [B], page_table int32 [B, max_pages] on the GPU, and
+    the host's bounds on new and cached tokens of any sequence (see exq_kv_batch). n_tokens: rows of q, k and v."""
+
+    def __init__(self, q_start, kv_len, page_table, max_q_len: int, max_kv_len: int, n_tokens: Optional[int] = None):
+        B, pages = page_table.shape
+        for t in (q_start, kv_len, page_table):
+            if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+                raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
+        if q_start.numel() != B + 1 or kv_len.numel() != B:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
+        self.q_start, self.kv_len, self.page_table, self.n_tokens = q_start, kv_len, page_table, n_tokens
+        self._desc = exq_kv_batch(B, n_tokens or 0, max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(),
+                                  page_table.data_ptr())
+
+    def desc(self, rows: int) -> exq_kv_batch:
+        if self.n_tokens is None:
+            self._desc.n_tokens = rows
+        return self._desc
+
+
+def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[Rope] = None, pos=None, q_out=None,
+                  layer: int = 0, stream=None):
+    """Writes the new tokens' k and v, fp16 [tokens, KV heads, D], to their slots of one layer, k (and q, fp16 [tokens,
+    heads, D], where given) turned by ``rope``. Returns the turned q (``q_out``, which may be q) or None."""
+    import torch
+    where = "exq_kv_append"
+    T, H, D = k.shape[0], cache.n_kv_heads, cache.D
+    if batch.n_tokens is not None:
+        if batch.n_tokens > T:
+            raise ExqError(EXQ_ERR_INVALID_ARG, where)
+        T = batch.n_tokens
+    kr, vr = _rows(k, where, D, H), _rows(v, where, D, H, T)
+    qp = op = None
+    heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        qp, op = ctypes.byref(_rows(q, where, D, None, T)), ctypes.byref(_rows(q_out, where, D, heads, T))
+    if pos is not None and (pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    _check(_lib.exq_kv_append(ctypes.byref(cache._desc), layer, ctypes.byref(batch.desc(T)), ctypes.byref(kr),
+                              ctypes.byref(vr), None if rope is None else ctypes.byref(rope._desc),
+                              None if pos is None else pos.data_ptr(), qp, op, heads, _stream_ptr(stream)), where)
+    return q_out if q is not None else None
+
+
+def exq_paged_attn_workspace_size(cache: KVCache, batch: KVBatch, n_heads: int, n_tokens: int) -> int:
+    return int(_lib.exq_paged_attn_workspace_size(ctypes.byref(cache._desc), ctypes.byref(batch.desc(n_tokens)), n_heads))
+
+
+def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[float] = None, causal: bool = True,
+                   window: int = 0, lse=None, layer: int = 0, workspace=None, stream=None):
+    """Attention of the new tokens' q, fp16 [tokens, heads, D], over the cached tokens of their sequences, the new ones
+    among them (exq_kv_append first). scale: 1 / sqrt(D) unless given; lse: fp32 [tokens, heads] to fill, or None.
+    Without ``workspace`` the zero-filled one of the device that exq_gemv uses too is taken: for calls on one stream."""
+    import torch
+    where = "exq_paged_attn"
+    T, H, D = q.shape
+    if batch.n_tokens is not None:
+        if batch.n_tokens > T:
+            raise ExqError(EXQ_ERR_INVALID_ARG, where)
+        T = batch.n_tokens
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    c, b = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T))
+    if workspace is None:
+        workspace = _shared_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)))
+    _check(_lib.exq_paged_attn(c, layer, b, ctypes.byref(qr), H, D ** -0.5 if scale is None else scale, int(causal), window,
+                               ctypes.byref(orow), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+    return out
+
+
+def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
+    """Copies pages pairs int32 [n, 2] of (src, dst) on the GPU, in every layer."""
+    if pairs.element_size() != 4 or pairs.is_floating_point() or not pairs.is_contiguous() or pairs.numel() % 2:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "exq_kv_copy_pages")
+    _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2, _stream_ptr(stream)),
+           "exq_kv_copy_pages")
+
+
+def _i32(a, where: str) -> np.ndarray:
+    if not isinstance(a, np.ndarray) or a.dtype != np.int32 or not a.flags.c_contiguous:
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    return a
+
+
+def exq_pages_alloc(refs: np.ndarray, n: int) -> np.ndarray:
+    """Host: the n lowest free pages of refs int32 [pages], now held once."""
+    out = np.empty(max(n, 0), dtype=np.int32)
+    _check(_lib.exq_pages_alloc(_np_ptr(_i32(refs, "exq_pages_alloc")), refs.size, n, _np_ptr(out)), "exq_pages_alloc")
+    return out
+
+
+def exq_pages_free(refs: np.ndarray, ids) -> None:
+    """Host: gives up one hold on each page of ids."""
+    ids = np.ascontiguousarray(ids, dtype=np.int32)
+    _check(_lib.exq_pages_free(_np_ptr(_i32(refs, "exq_pages_free")), refs.size, _np_ptr(ids), ids.size), "exq_pages_free")
+
+
+def exq_pages_fork(refs: np.ndarray, ids, n_tokens: int, page_size: int):
+    """Host: (page ids of a second sequence sharing the first n_tokens, pairs int32 [0 or 1, 2] to copy)."""
+    ids = np.ascontiguousarray(ids, dtype=np.int32)
+    n = -(-n_tokens // page_size) if page_size > 0 and n_tokens > 0 else 0
+    if ids.size < n:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "exq_pages_fork")
+    out, pair, count = np.empty(n, np.int32), np.empty((1, 2), np.int32), ctypes.c_int32()
+    _check(_lib.exq_pages_fork(_np_ptr(_i32(refs, "exq_pages_fork")), refs.size, page_size, _np_ptr(ids), n_tokens,
+                               _np_ptr(out), _np_ptr(pair), ctypes.byref(count)), "exq_pages_fork")
+    return out, pair[:count.value]
+
+
+def exq_pages_compact(refs: np.ndarray, tables: np.ndarray) -> np.ndarray:
+    """Host: moves the held pages to the lowest ids in refs and tables (int32, both rewritten); the pairs int32 [n, 2] to
+    copy."""
+    where = "exq_pages_compact"
+    pairs, count = np.empty((max(refs.size // 2, 1), 2), np.int32), ctypes.c_int32()
+    _check(_lib.exq_pages_compact(_np_ptr(_i32(refs, where)), refs.size, _np_ptr(_i32(tables, where)), tables.size,
+                                  _np_ptr(pairs), ctypes.byref(count)), where)
+    return pairs[:count.value]
 
 
 def exq_solve_exl2_bits(err: np.ndarray, budget: int) -> np.ndarray:

@@ -1,0 +1,304 @@
+// What the paged attention kernels share: their arguments, the division of
+// the work over CTAs, the join of split units, and PTX wrappers.
+//
+// Work is cut into units: a block of query rows of one sequence and KV head
+// (row r of a sequence and KV head is new token r / group, query head
+// r % group of it, so the rows of one token lie together), over the tiles of
+// cached tokens that some row of the block sees. The tiles of all units, one
+// unit after the other, are divided evenly over the CTAs, whatever the
+// sequences' lengths: a CTA may end a unit that another began, do several
+// whole units, and begin another. Lengths are read on the device. A unit that
+// several CTAs share is joined by the last of them to finish, in the CTAs'
+// order, so the result does not depend on which one that is.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "exq_device.cuh"
+#include "exq_internal.h"
+#include "exq_rope.cuh"
+
+namespace exq {
+
+struct AttnArgs {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int n_seqs, n_tokens, max_pages, max_q_len, max_kv_len;
+  const uint32_t* codes[2];   // K, V of the layer
+  const uint16_t* scales[2];
+  int n_kv_heads, page_size, n_pages, group;  // group: query heads of a KV head
+  exq_rows q, out;
+  int n_heads;
+  float scale_log2;           // scale * log2(e)
+  int causal, window;
+  float* lse;
+  int row_blocks;             // blocks of rows a sequence may need (host bound)
+  int min_tiles;              // fewest tiles worth a CTA
+  unsigned* counters;         // [CTAs], zero between calls
+  float* partial;             // [CTAs][2][rows * (D + 2)]
+  unsigned* err;              // the device error word
+  int wait_limit;
+  int starve;
+};
+
+constexpr size_t kAttnCounterBytes = 64 << 10;
+constexpr int kAttnMaxCtas = static_cast<int>(kAttnCounterBytes / sizeof(unsigned));
+
+// Geometry of a block of rows: sequence b, its new tokens and lengths, the
+// rows, and the tiles [tile0, tile0 + tiles) of cached tokens [begin, end).
+struct AttnUnit {
+  int b, q0, n, len;   // sequence, its first row of q, new tokens, cached tokens
+  int r0, rows;        // first row of the block, rows of it
+  int begin, end;      // cached tokens that some row sees
+  int tile0, tiles;    // tiles >= 1 where rows > 0 (one, empty, where nothing is seen)
+};
+
+template <int ROWS, int TILE>
+__device__ __forceinline__ AttnUnit attn_unit(const AttnArgs& a, int pair) {
+  AttnUnit u{};
+  u.b = a.row_blocks == 1 ? pair : pair / a.row_blocks;
+  const int rb = a.row_blocks == 1 ? 0 : pair - u.b * a.row_blocks;
+  u.q0 = __ldg(a.q_start + u.b);
+  u.n = __ldg(a.q_start + u.b + 1) - u.q0;
+  u.len = __ldg(a.kv_len + u.b);
+  if (u.q0 < 0 || u.n < 0 || u.n > a.max_q_len || u.q0 > a.n_tokens - u.n || u.len < 0 || u.len > a.max_kv_len) {
+    atomicOr(a.err, kDevErrBadPage);
+    return u;
+  }
+  u.r0 = rb * ROWS;
+  u.rows = min(ROWS, u.n * a.group - u.r0);
+  if (u.rows <= 0) {
+    u.rows = 0;
+    return u;
+  }
+  const int first = u.len - u.n + u.r0 / a.group, last = u.len - u.n + (u.r0 + u.rows - 1) / a.group;  // positions
+  u.end = a.causal ? min(u.len, max(0, last + 1)) : u.len;
+  u.begin = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  if (u.begin >= u.end) {
+    u.begin = u.end = u.tile0 = 0;
+    u.tiles = 1;
+  } else {
+    u.tile0 = u.begin / TILE;
+    u.tiles = (u.end + TILE - 1) / TILE - u.tile0;
+  }
+  return u;
+}
+
+// A CTA's share of the tiles: [begin, end) of `total`, and where it starts.
+struct AttnShare {
+  long long total, begin, end;
+  long long pair_start;  // tiles before the first pair, all heads
+  int pair;
+  int ctas;              // CTAs that have work
+};
+
+// Every thread of the block (a multiple of 32) calls it; `scratch` is shared
+// memory of at least 34 long longs.
+template <int ROWS, int TILE>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, long long* scratch) {
+  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = a.n_seqs * a.row_blocks;
+  const int per = (pairs + nt - 1) / nt, p0 = min(tid * per, pairs), p1 = min(p0 + per, pairs);
+  long long sum = 0;
+  for (int p = p0; p < p1; ++p) sum += attn_unit<ROWS, TILE>(a, p).tiles;
+  long long inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += v;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  long long before = 0, all = 0;
+  for (int w = 0; w < nt / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    all += scratch[w];
+  }
+  AttnShare s;
+  s.total = all * a.n_kv_heads;
+  s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + a.min_tiles - 1) / a.min_tiles));
+  s.begin = s.end = s.pair_start = 0;
+  s.pair = 0;
+  if (static_cast<int>(blockIdx.x) >= s.ctas) return s;
+  s.begin = s.total * blockIdx.x / s.ctas;
+  s.end = s.total * (blockIdx.x + 1) / s.ctas;
+  long long at = (before + inc - sum) * a.n_kv_heads;  // tiles before this thread's pairs
+  if (at <= s.begin && s.begin < at + sum * a.n_kv_heads) {
+    for (int p = p0; p < p1; ++p) {
+      const long long tiles = static_cast<long long>(attn_unit<ROWS, TILE>(a, p).tiles) * a.n_kv_heads;
+      if (s.begin < at + tiles) {
+        scratch[32] = at;
+        scratch[33] = p;
+        break;
+      }
+      at += tiles;
+    }
+  }
+  __syncthreads();
+  s.pair_start = scratch[32];
+  s.pair = static_cast<int>(scratch[33]);
+  return s;
+}
+
+// The CTA whose share holds tile x: share c is [total c / ctas, total (c + 1) / ctas).
+__device__ __forceinline__ int attn_cta_of(const AttnShare& s, long long x) {
+  return static_cast<int>(((x + 1) * s.ctas - 1) / s.total);
+}
+
+// A CTA's piece of a unit, in order.
+struct AttnPiece {
+  AttnUnit u;
+  int head;            // KV head
+  int t0, t1;          // tiles of the piece, counted from cached token 0
+  long long first;     // the unit's first tile in the division
+  bool whole;
+};
+
+struct AttnWalk {
+  AttnShare s;
+  long long at;        // next tile of the share
+  long long pair_start;
+  int pair;
+};
+
+template <int ROWS, int TILE>
+__device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w, AttnPiece& p) {
+  if (w.at >= w.s.end) return false;
+  p.u = attn_unit<ROWS, TILE>(a, w.pair);
+  while (w.at >= w.pair_start + static_cast<long long>(p.u.tiles) * a.n_kv_heads) {  // pairs without rows are passed
+    w.pair_start += static_cast<long long>(p.u.tiles) * a.n_kv_heads;
+    p.u = attn_unit<ROWS, TILE>(a, ++w.pair);
+  }
+  const int off = static_cast<int>(w.at - w.pair_start);
+  p.head = off / p.u.tiles;
+  const int o = off - p.head * p.u.tiles;
+  p.first = w.at - o;
+  const int n = static_cast<int>(min(w.s.end - w.at, static_cast<long long>(p.u.tiles - o)));
+  p.t0 = p.u.tile0 + o;
+  p.t1 = p.t0 + n;
+  p.whole = n == p.u.tiles;
+  w.at += n;
+  return true;
+}
+
+// The partial result of CTA c in a unit: its second slot where the unit
+// begins in the CTA's share, its first where it began before. Row-major
+// [rows][D] sums, then [rows] maxima (log2) and [rows] sums of weights.
+__device__ __forceinline__ float* attn_slot(const AttnArgs& a, int cta, bool begins, int floats) {
+  return a.partial + (static_cast<size_t>(cta) * 2 + (begins ? 1 : 0)) * floats;
+}
+
+__device__ __forceinline__ void attn_row_of(const AttnArgs& a, const AttnPiece& p, int r, int& token, int& head) {
+  const int rr = p.u.r0 + r;
+  const int t = rr / a.group;
+  token = p.u.q0 + t;
+  head = p.head * a.group + (rr - t * a.group);
+}
+
+__device__ __forceinline__ void attn_store_lse(const AttnArgs& a, int token, int head, float m, float l) {
+  if (a.lse)
+    a.lse[static_cast<long long>(token) * a.n_heads + head] =
+        l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Joins the pieces of a unit that CTAs c0 .. c1 share and writes its rows.
+// `threads` threads with ids `tid` call it, in the one CTA that came last.
+template <int ROWS, int D>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnPiece& p, int c0, int c1, int tid, int threads) {
+  constexpr int kFloats = ROWS * (D + 2);
+  constexpr int kCols = D / 4;
+  for (int e = tid; e < p.u.rows * kCols; e += threads) {
+    const int r = e / kCols, col = e - r * kCols;
+    float m = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+      const float* s = attn_slot(a, c, c == c0, kFloats) + ROWS * D;
+      if (__ldcg(s + ROWS + r) > 0.f) m = fmaxf(m, __ldcg(s + r));
+    }
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float* s = attn_slot(a, c, c == c0, kFloats);
+      const float li = __ldcg(s + ROWS * D + ROWS + r);
+      const float f = li > 0.f ? exp2_fast(__ldcg(s + ROWS * D + r) - m) : 0.f;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D) + col);
+      l += li * f;
+      y.x += v.x * f;
+      y.y += v.y * f;
+      y.z += v.z * f;
+      y.w += v.w * f;
+    }
+    int token, head;
+    attn_row_of(a, p, r, token, head);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2 o;
+    o.x = float_to_half_bits(y.x * inv) | (float_to_half_bits(y.y * inv) << 16);
+    o.y = float_to_half_bits(y.z * inv) | (float_to_half_bits(y.w * inv) << 16);
+    *reinterpret_cast<uint2*>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * col) = o;
+    if (col == 0) attn_store_lse(a, token, head, m, l);
+  }
+}
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait of one thread; false (and a recorded timeout) if the phase
+// never completes, or if another role of the CTA gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const AttnArgs& a) {
+  for (int i = 0; i < a.wait_limit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  atomicOr(a.err, kDevErrTimeout);
+  *abort_flag = 1;
+  return false;
+}
+
+// Bounded wait of a whole warp: all lanes leave in the same round.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, const AttnArgs& a) {
+  for (int i = 0; i < a.wait_limit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+  }
+  if ((threadIdx.x & 31) == 0) atomicOr(a.err, kDevErrTimeout);
+  *abort_flag = 1;
+  return false;
+}
+
+// host: launches of one (bits, D) family
+exq_status launch_attn_split(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+size_t attn_split_workspace(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms);
+
+}  // namespace exq

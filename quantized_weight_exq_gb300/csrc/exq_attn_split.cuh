@@ -1,0 +1,710 @@
+// Attention of few rows over the paged cache (decoded tokens, drafts): HBM is
+// the bound, the cache is read once, as packed codes.
+//
+//   S^T = K Q^T and O^T = V^T P^T on mma.sync.m16n8k16: the cache is the A
+//   operand, 16 tokens (or 16 dims) a fragment, and the query rows are B's 8
+//   columns, so 8 rows cost one instruction per 256 cached values.
+//
+// Codes become the small integers (u - z), exact in fp16, and the groups'
+// scales stay outside the products, in fp32:
+//   q . k_t = s_t sum_d q_d (u_td - z),   sum_t (p_t s_t) (u_td - z),
+// so a pair of codes costs an AND-OR that plants them in the mantissa of 1024
+// and one exact fp16x2 subtraction (and part of a shift), the same as the
+// weights of the GEMV. Leaving the zero point in (multiplying by u, planted
+// or as a subnormal, and subtracting z sum_t p_t s_t after) would save the
+// subtraction, but the tensor cores align products by their operands'
+// exponents and keep about 24 bits: for weights of mixed size the sums were
+// off by up to 2^-14 of the largest.
+// K and V differ in how their fragments are gathered: K's words come by
+// ldmatrix as they lie; V needs two tokens' codes of one dim in a register,
+// which ldmatrix.trans gives for 16-bit units of 4 (Q4), 2 (Q8) or 1 (fp16)
+// values; Q6's codes straddle such units and take plain loads and byte
+// permutes. The order of dims within a fragment follows the packing; Q is
+// loaded, and O stored, in that order.
+//
+// A CTA is 4 warps that each take 16 tokens of a 64-token tile, with softmax
+// statistics and sums of their own until the unit ends, and a producer warp
+// that fills a ring of stages by TMA: one box per page (or 64 tokens of it),
+// swizzled so that ldmatrix is free of bank conflicts, and the scales beside
+// it. Slots past the last token are masked in S, and V's (fp16) zeroed.
+#pragma once
+
+#include <algorithm>
+#include <mutex>
+
+#include "exq_attn.cuh"
+
+namespace exq {
+namespace split {
+
+constexpr int kTile = 64;
+constexpr int kConsumers = 4;
+constexpr int kThreads = (kConsumers + 1) * 32;
+
+template <int B, int D, int NT>
+struct Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRowBytes = D * B / 8;
+  // parts of a row as TMA boxes; 128-byte parts at most where rows are swizzled
+  static constexpr int kPartBytes = B == 6 ? kRowBytes : kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kParts = kRowBytes / kPartBytes;
+  static constexpr int kArray = kTile * kRowBytes;        // K or V of a stage
+  static constexpr int kScale = B == 16 ? 0 : kTile * 2;  // scales of K or V
+  static constexpr int kStage = ((2 * kArray + 2 * kScale + 1023) / 1024) * 1024;
+  static constexpr int kRegions = kRows * D <= 2048 ? kConsumers : 1;
+  static constexpr int kMerge = kRegions * kRows * D * 4 + 2 * kConsumers * kRows * 4;
+  static constexpr int kCtas = kStage > 40 * 1024 ? 1 : kStage > 20 * 1024 || D * NT > 128 ? 2 : D * NT > 64 ? 3 : 4;  // an SM: by stages, registers
+  static constexpr int kBudget = (224 * 1024) / kCtas - 1024 - kMerge - 1024;
+  static constexpr int kFit = kBudget / kStage;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kSmem = 1024 + kStages * kStage + ((kMerge + 15) / 16) * 16 + 512;
+  static_assert(kStages >= 2, "at least two stages");
+  static constexpr int kFloats = kRows * (D + 2);
+};
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+
+// Byte offset of 16-byte chunk `ch` of token row `row` in a stage's K or V,
+// where TMA put it: its swizzle XORs the chunk's index in a 128-, 64- or
+// 32-byte row with address bits 7 and up.
+template <typename C>
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
+  constexpr int kPer = C::kPartBytes / 16;  // 8, 4 or 2
+  const int part = ch / kPer, in = ch % kPer;
+  const int x = kPer == 8 ? row & 7 : kPer == 4 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return part * (kTile * C::kPartBytes) + row * C::kPartBytes + ((in ^ x) << 4);
+}
+
+// The token of a 16-token slice at fragment index i: as they lie, except for
+// Q6, whose plain loads of V then touch four neighbouring tokens at a time.
+template <int B>
+__device__ __forceinline__ int token_at(int i) {
+  if constexpr (B == 6) return (i & 8) + ((i >> 1) & 3) + 4 * (i & 1);
+  return i;
+}
+
+// (u - z) of Q8 codes planted in 1024
+__device__ __forceinline__ uint32_t q8_pair(uint32_t w, uint32_t sel) {
+  return hadd2(prmt(w, 0x64646464u, sel), pack2(f16_bits(-(1024 + 128)), f16_bits(-(1024 + 128))));
+}
+
+// (u_i - z) of two tokens a, b from 48 bits of Q6 codes of each
+__device__ __forceinline__ void q6_two(uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t (&v)[8]) {
+  const uint32_t x01 = prmt(alo, blo, 0x5410), x12 = prmt(alo, blo, 0x6521), x23 = prmt(alo, blo, 0x7632);
+  const uint32_t wa = fshr(alo, ahi, 16), wb = fshr(blo, bhi, 16);
+  const uint32_t y = prmt(wa, wb, 0x6521), z = prmt(wa, wb, 0x7632);
+  v[0] = unbias<0, 0, 32>(and_or(x01, 0x003F003Fu, kMagic));
+  v[1] = unbias<4, 4, 32>(and_or(x01 >> 2, 0x03F003F0u, kMagic));
+  v[2] = unbias<4, 4, 32>(and_or(x12, 0x03F003F0u, kMagic));
+  v[3] = unbias<2, 2, 32>(and_or(x23, 0x00FC00FCu, kMagic));
+  v[4] = unbias<0, 0, 32>(and_or(y, 0x003F003Fu, kMagic));
+  v[5] = unbias<4, 4, 32>(and_or(y >> 2, 0x03F003F0u, kMagic));
+  v[6] = unbias<4, 4, 32>(and_or(z, 0x03F003F0u, kMagic));
+  v[7] = unbias<2, 2, 32>(and_or(z >> 8, 0x00FC00FCu, kMagic));
+}
+
+// O's dim of (16-dim tile, half of its rows, lane group g)
+template <int B, int D>
+__device__ __forceinline__ int dim_of(int mt, int half, int g) {
+  if constexpr (B == 4) return 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) + half;
+  if constexpr (B == 6) return g * (D / 8) + 2 * mt + half;
+  if constexpr (B == 8) return 16 * mt + 2 * g + half;
+  return 16 * mt + 8 * half + g;
+}
+
+template <int B, int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
+    attn_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
+  using C = Cfg<B, D, NT>;
+  constexpr bool kQuant = B != 16;
+  constexpr int kSteps = D / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+  float* stat_m = merge + C::kRegions * C::kRows * D;
+  float* stat_l = stat_m + kConsumers * C::kRows;
+  uint8_t* tail = smem + C::kStages * C::kStage + ((C::kMerge + 15) / 16) * 16;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + C::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
+  int* is_last = const_cast<int*>(abort_flag) + 1;
+  long long* scratch = reinterpret_cast<long long*>(merge);  // free until the first unit ends
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), kConsumers);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  AttnWalk walk;
+  walk.s = attn_share<C::kRows, kTile>(a, scratch);  // its barriers cover the initialisation above
+  if (walk.s.begin >= walk.s.end) return;            // the whole CTA
+  __syncthreads();                                   // scratch has been read
+  walk.at = walk.s.begin;
+  walk.pair = walk.s.pair;
+  walk.pair_start = walk.s.pair_start;
+  AttnPiece p;
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    if (a.starve) return;  // test hook: the consumers' waits run out
+    const int box = min(kTile, a.page_size);      // tokens of a TMA box
+    const int boxes = kTile / box;                // of a tile
+    int st = 0;
+    uint32_t ph = 0;
+    long long issued = 0;
+    bool ok = true;
+    while (ok && attn_next<C::kRows, kTile>(a, walk, p)) {
+      const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
+      const int b0 = p.t0 * boxes, b1 = p.t1 * boxes;  // boxes of the piece
+      const auto page_of = [&](int bx) {               // -1: nothing to copy
+        const int tok = bx * box;
+        if (bx >= b1 || tok >= p.u.end) return -1;
+        const int page = __ldg(table + tok / a.page_size);
+        if (page < 0 || page >= a.n_pages) {
+          atomicOr(a.err, kDevErrBadPage);
+          return -1;
+        }
+        return page;
+      };
+      int have = b0, page = page_of(b0 + lane), next = page_of(b0 + 32 + lane);
+      for (int t = p.t0; t < p.t1; ++t) {
+        if (t * boxes >= have + 32) {
+          have += 32;
+          page = next;
+          next = page_of(have + 32 + lane);
+        }
+        const int mine = __shfl_sync(0xffffffffu, page, (t * boxes - have + (lane & (boxes - 1))) & 31);
+        const bool copy = lane < boxes && mine >= 0;
+        const unsigned n = __popc(__ballot_sync(0xffffffffu, copy));
+        ok = mbar_wait_warp(smem_u32(&empty[st]), ph ^ 1, abort_flag, a);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&full[st]);
+        const uint32_t base = smem_u32(smem + st * C::kStage);
+        if (lane == 0) mbar_expect_tx(bar, n * box * (2 * C::kRowBytes + (kQuant ? 4 : 0)));
+        __syncwarp();
+        if (copy) {
+          const int tok = t * kTile + lane * box, slot = tok & (a.page_size - 1), block = mine * a.n_kv_heads + p.head;
+#pragma unroll
+          for (int i = 0; i < C::kParts; ++i) {
+            const uint32_t off = i * (kTile * C::kPartBytes) + lane * box * C::kPartBytes;
+            tma_load_3d(base + off, &maps.k, i * (C::kPartBytes / 4), slot, block, bar);
+            tma_load_3d(base + C::kArray + off, &maps.v, i * (C::kPartBytes / 4), slot, block, bar);
+          }
+          if constexpr (kQuant) {
+            const long long g = static_cast<long long>(block) * a.page_size + slot;
+            bulk_load(base + 2 * C::kArray + lane * box * 2, a.scales[0] + g, box * 2, bar);
+            bulk_load(base + 2 * C::kArray + C::kScale + lane * box * 2, a.scales[1] + g, box * 2, bar);
+          }
+        }
+        ++issued;
+        if (++st == C::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    // every stage's copies land before the CTA may go
+    for (long long i = max(0ll, issued - C::kStages); i < issued; ++i)
+      for (int r = 0; r < a.wait_limit; ++r)
+        if (mbar_try_wait(smem_u32(&full[i % C::kStages]), (i / C::kStages) & 1)) break;
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  const int row0 = warp * 16;                        // the warp's tokens in a tile
+  const int tokA = row0 + token_at<B>(g), tokB = row0 + token_at<B>(g + 8);
+  int st = 0;
+  uint32_t ph = 0;
+  while (attn_next<C::kRows, kTile>(a, walk, p)) {
+    // Q as B fragments: column g of tile nt is row 8 nt + g
+    uint32_t bq[NT][kSteps][2];
+    int lo[NT][2], hi[NT][2];  // cached tokens that rows 2c, 2c + 1 of a tile see
+    int all_lo = 0, all_hi = p.u.end;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const bool has = r < p.u.rows;
+      int token = 0, head = 0;
+      if (has) attn_row_of(a, p, r, token, head);
+      const uint16_t* q = a.q.data + token * a.q.token_stride + head * a.q.head_stride;
+      if constexpr (B == 4 || B == 6) {  // 8 neighbouring dims are two steps, in the unpackers' order of pairs
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          const int d = B == 4 ? 32 * i + 8 * c : c * (D / 4) + 8 * i;
+          const uint4 v = has ? __ldg(reinterpret_cast<const uint4*>(q + d)) : make_uint4(0, 0, 0, 0);
+          bq[nt][2 * i][0] = prmt(v.x, v.z, 0x5410);      // 0, 4
+          bq[nt][2 * i][1] = prmt(v.x, v.z, 0x7632);      // 1, 5
+          bq[nt][2 * i + 1][0] = prmt(v.y, v.w, 0x5410);  // 2, 6
+          bq[nt][2 * i + 1][1] = prmt(v.y, v.w, 0x7632);  // 3, 7
+        }
+      } else if constexpr (B == 8) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint2 v = has ? __ldg(reinterpret_cast<const uint2*>(q + 16 * i + 4 * c)) : make_uint2(0, 0);
+          bq[nt][i][0] = v.x;
+          bq[nt][i][1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          bq[nt][i][0] = has ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * i + 2 * c)) : 0u;
+          bq[nt][i][1] = has ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * i + 8 + 2 * c)) : 0u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = p.u.r0 + min(8 * nt + 2 * c + i, p.u.rows - 1), pos = p.u.len - p.u.n + rr / a.group;
+        hi[nt][i] = a.causal ? min(pos + 1, p.u.len) : p.u.len;
+        lo[nt][i] = a.window > 0 ? pos - a.window + 1 : 0;
+        all_lo = max(all_lo, lo[nt][i]);
+        all_hi = min(all_hi, hi[nt][i]);
+      }
+    }
+    // bounds of the tokens that all rows see, over the warp
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+    float o[NT][kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[nt][i] = 0.f, m[nt][i] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+    int kexp = -1;        // V's scales are read times 2^(15 - kexp)
+
+    for (int t = p.t0; t < p.t1; ++t) {
+      // a wait that gave up leaves the unit as it is, but no barrier below:
+      // all warps go through the same ones, whichever of them saw the flag
+      if (!mbar_wait_warp(smem_u32(&full[st]), ph, abort_flag, a)) break;
+      const uint32_t kbase = smem_u32(smem + st * C::kStage), vbase = kbase + C::kArray, sbase = vbase + C::kArray;
+      const int first = t * kTile + row0;
+      const int tA = t * kTile + tokA, tB = t * kTile + tokB;
+      if (first < p.u.end && first + 16 > p.u.begin) {  // some token of the slice is seen
+        // ---------------------------------------------------------- S^T = K Q^T
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
+        if constexpr (B == 6) {
+          constexpr int kWin = D / 32;  // 48-bit windows of a lane's D / 4 codes
+          constexpr int kW = kWin * 3 / 2;
+          uint32_t wa[kW], wb[kW];
+#pragma unroll
+          for (int i = 0; i < kW; ++i) {
+            wa[i] = lds32(kbase + tokA * C::kRowBytes + c * (kW * 4) + 4 * i);
+            wb[i] = lds32(kbase + tokB * C::kRowBytes + c * (kW * 4) + 4 * i);
+          }
+#pragma unroll
+          for (int i = 0; i < kWin; ++i) {
+            const int w = (i / 2) * 3 + (i & 1);
+            uint32_t pa[4], pb[4];
+            if (i & 1) {
+              unpack8<6>(fshr(wa[w], wa[w + 1], 16), wa[w + 1] >> 16, pa);
+              unpack8<6>(fshr(wb[w], wb[w + 1], 16), wb[w + 1] >> 16, pb);
+            } else {
+              unpack8<6>(wa[w], wa[w + 1], pa);
+              unpack8<6>(wb[w], wb[w + 1], pb);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][2 * i][0], bq[nt][2 * i][1]);
+              mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][2 * i + 1][0], bq[nt][2 * i + 1][1]);
+            }
+          }
+        } else {
+          constexpr int kChunks = C::kRowBytes / 16;
+          const int lrow = row0 + (lane & 15), lch = lane >> 4;
+#pragma unroll
+          for (int q = 0; q < kChunks; q += 2) {
+            uint32_t r[4];
+            ldsm4<false>(kbase + chunk_at<C>(lrow, q + lch), r);
+            if constexpr (B == 4) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t pa[4], pb[4];
+                unpack8<4>(r[2 * h], 0u, pa);
+                unpack8<4>(r[2 * h + 1], 0u, pb);
+                const int i = 2 * (q + h);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][i][0], bq[nt][i][1]);
+                  mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][i + 1][0], bq[nt][i + 1][1]);
+                }
+              }
+            } else if constexpr (B == 8) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
+                const uint32_t a0 = q8_pair(w0, 0x4140), a1 = q8_pair(w1, 0x4140), a2 = q8_pair(w0, 0x4342),
+                               a3 = q8_pair(w1, 0x4342);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(h ? s2[nt] : s[nt], a0, a1, a2, a3, bq[nt][q + h][0], bq[nt][q + h][1]);
+              }
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma((q & 2) ? s2[nt] : s[nt], r[0], r[1], r[2], r[3], bq[nt][q / 2][0], bq[nt][q / 2][1]);
+            }
+          }
+        }
+        // ---------------------------------------------------------- softmax
+        const bool all_see = first >= all_lo && first + 16 <= all_hi;
+        float ksA = a.scale_log2, ksB = a.scale_log2, vsA = 1.f, vsB = 1.f;
+        if constexpr (kQuant) {
+          ksA *= half_bits_to_float(lds16(sbase + 2 * tokA));
+          ksB *= half_bits_to_float(lds16(sbase + 2 * tokB));
+          uint32_t va = lds16(sbase + C::kScale + 2 * tokA), vb = lds16(sbase + C::kScale + 2 * tokB);
+          if (tA >= p.u.end) va = 0;  // whatever the slots past the end hold
+          if (tB >= p.u.end) vb = 0;
+          // V's scales are brought near 1, or their products with small
+          // weights would leave fp16's normal range: times 2^(15 - kexp),
+          // kexp the (biased) exponent of the largest so far, moved only when
+          // one is 2^6 above it
+          const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, max(va, vb)) >> 10) & 31;
+          if (kexp < 0) {
+            kexp = e;
+          } else if (e > kexp + 6) {
+            const float f = __uint_as_float(static_cast<uint32_t>(127 + kexp - e) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[nt][i][j] *= f;
+            kexp = e;
+          }
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + 15 - kexp) << 23);
+          vsA = half_bits_to_float(va) * f;
+          vsB = half_bits_to_float(vb) * f;
+        }
+        uint32_t pb0[NT], pb1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = (s[nt][i] + s2[nt][i]) * (i < 2 ? ksA : ksB);
+            const int tt = i < 2 ? tA : tB;
+            if (!all_see && (tt < lo[nt][i & 1] || tt >= hi[nt][i & 1])) x[i] = -INFINITY;
+          }
+          float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          const bool more = m0 > m[nt][0] || m1 > m[nt][1];
+          if (__any_sync(0xffffffffu, more)) {
+            const float n0 = fmaxf(m[nt][0], m0), n1 = fmaxf(m[nt][1], m1);
+            const float f0 = n0 == -INFINITY ? 1.f : exp2_fast(m[nt][0] - n0), f1 = n1 == -INFINITY ? 1.f : exp2_fast(m[nt][1] - n1);
+            m[nt][0] = n0, m[nt][1] = n1;
+            l[nt][0] *= f0, l[nt][1] *= f1;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              o[nt][i][0] *= f0, o[nt][i][1] *= f1;
+              o[nt][i][2] *= f0, o[nt][i][3] *= f1;
+            }
+          }
+          const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float w0 = exp2_fast(x[0] - b0), w1 = exp2_fast(x[1] - b1), w2 = exp2_fast(x[2] - b0), w3 = exp2_fast(x[3] - b1);
+          l[nt][0] += w0 + w2;
+          l[nt][1] += w1 + w3;
+          const __half2 h0 = __floats2half2_rn(w0 * vsA, w1 * vsA), h1 = __floats2half2_rn(w2 * vsB, w3 * vsB);
+          pb0[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&h0));
+          pb1[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&h1));
+        }
+        // ---------------------------------------------------------- O^T += V^T P^T
+        if constexpr (B == 6) {
+          // tokens (c, 4 + c) and (8 + c, 12 + c) of the slice, D / 8 codes from dim g D / 8
+          constexpr int kWin = D / 64;
+          const int ta = row0 + c;
+#pragma unroll
+          for (int i = 0; i < kWin; ++i) {
+            uint32_t w[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int bit = g * (D / 8 * 6) + 48 * i;  // of the row
+              const uint32_t at = vbase + (ta + 4 * j) * C::kRowBytes + (bit >> 5) * 4;
+              const uint32_t x = lds32(at), y = lds32(at + 4);
+              w[j][0] = fshr(x, y, bit & 16);
+              w[j][1] = y >> (bit & 16);
+            }
+            uint32_t va[8], vb[8];
+            q6_two(w[0][0], w[0][1], w[1][0], w[1][1], va);
+            q6_two(w[2][0], w[2][1], w[3][0], w[3][1], vb);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(o[nt][4 * i + j], va[2 * j], va[2 * j + 1], vb[2 * j], vb[2 * j + 1], pb0[nt], pb1[nt]);
+          }
+        } else {
+          constexpr int kChunks = C::kRowBytes / 16;
+          const int lrow = row0 + (lane & 15), lch = lane >> 4;
+          uint32_t zA = 0xFFFFFFFFu, zB = 0xFFFFFFFFu;  // V's tokens past the end, as zeros
+          bool ragged = false;
+          if constexpr (!kQuant) {
+            ragged = first + 16 > p.u.end;
+            const int x = first + 2 * c, y = x + 8;
+            zA = (x < p.u.end ? 0xFFFFu : 0u) | (x + 1 < p.u.end ? 0xFFFF0000u : 0u);
+            zB = (y < p.u.end ? 0xFFFFu : 0u) | (y + 1 < p.u.end ? 0xFFFF0000u : 0u);
+          }
+#pragma unroll
+          for (int q = 0; q < kChunks; q += 2) {
+            uint32_t r[4];
+            ldsm4<true>(vbase + chunk_at<C>(lrow, q + lch), r);
+            if constexpr (B == 4) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                // the unpacker's pairs are here (token a, token b) of dims 4g .. 4g + 3
+                uint32_t va[4], vb[4];
+                unpack8<4>(r[2 * h], 0u, va);
+                unpack8<4>(r[2 * h + 1], 0u, vb);
+                const int i = 2 * (q + h);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma(o[nt][i], va[0], va[1], vb[0], vb[1], pb0[nt], pb1[nt]);
+                  mma(o[nt][i + 1], va[2], va[3], vb[2], vb[3], pb0[nt], pb1[nt]);
+                }
+              }
+            } else if constexpr (B == 8) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
+                const uint32_t a0 = q8_pair(w0, 0x4240), a1 = q8_pair(w0, 0x4341), a2 = q8_pair(w1, 0x4240),
+                               a3 = q8_pair(w1, 0x4341);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma(o[nt][q + h], a0, a1, a2, a3, pb0[nt], pb1[nt]);
+              }
+            } else {
+              if (ragged) r[0] &= zA, r[2] &= zA, r[1] &= zB, r[3] &= zB;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma(o[nt][q / 2], r[0], r[2], r[1], r[3], pb0[nt], pb1[nt]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+
+    // -------------------------------------------------------------- the warps' results to one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
+        if (g == 0) {
+          stat_m[warp * C::kRows + 8 * nt + 2 * c + i] = m[nt][i];
+          stat_l[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i];
+        }
+      }
+    consumer_sync();
+    const float back = kQuant ? __uint_as_float(static_cast<uint32_t>(127 - 15 + max(kexp, 0)) << 23) : 1.f;
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, stat_m[w * C::kRows + 8 * nt + 2 * c + i]);
+        f[nt][i] = m[nt][i] == -INFINITY ? 0.f : exp2_fast(m[nt][i] - mm) * back;
+      }
+    const auto put = [&](float* region, bool add) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float y = o[nt][i][2 * h + j] * f[nt][j];
+              float* at = region + (8 * nt + 2 * c + j) * D + dim_of<B, D>(i, h, g);
+              *at = add ? *at + y : y;
+            }
+    };
+    if constexpr (C::kRegions > 1) {
+      put(merge + warp * C::kRows * D, false);
+      consumer_sync();
+    } else {
+      for (int w = 0; w < kConsumers; ++w) {
+        if (w == warp) put(merge, w > 0);
+        consumer_sync();
+      }
+    }
+    // 128 threads: 4 dims of a row each
+    const int c0 = p.whole ? 0 : attn_cta_of(walk.s, p.first), c1 = p.whole ? 0 : attn_cta_of(walk.s, p.first + p.u.tiles - 1);
+    const int me = blockIdx.x;
+    float* slot = p.whole ? nullptr : attn_slot(a, me, me == c0, C::kFloats);
+    for (int e = threadIdx.x; e < p.u.rows * (D / 4); e += kConsumers * 32) {
+      const int r = e / (D / 4), col = e % (D / 4);
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, stat_m[w * C::kRows + r]);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) {
+        const float mw = stat_m[w * C::kRows + r];
+        if (mw != -INFINITY) ll += stat_l[w * C::kRows + r] * exp2_fast(mw - mm);
+      }
+      float4 y = *reinterpret_cast<const float4*>(merge + r * D + 4 * col);
+#pragma unroll
+      for (int w = 1; w < C::kRegions; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(merge + (w * C::kRows + r) * D + 4 * col);
+        y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+      }
+      if (p.whole) {
+        int token, head;
+        attn_row_of(a, p, r, token, head);
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        uint2 out;
+        out.x = float_to_half_bits(y.x * inv) | (float_to_half_bits(y.y * inv) << 16);
+        out.y = float_to_half_bits(y.z * inv) | (float_to_half_bits(y.w * inv) << 16);
+        *reinterpret_cast<uint2*>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * col) = out;
+        if (col == 0) attn_store_lse(a, token, head, mm, ll);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * D + 4 * col) = y;
+        if (col == 0) slot[C::kRows * D + r] = mm, slot[C::kRows * D + C::kRows + r] = ll;
+      }
+    }
+    if (!p.whole) {
+      __threadfence();
+      consumer_sync();
+      if (threadIdx.x == 0) {
+        const int last = atomicAdd(a.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+        if (last) a.counters[c0] = 0u;
+        *is_last = last;
+      }
+      consumer_sync();
+      if (*is_last) {
+        __threadfence();
+        attn_join<C::kRows, D>(a, p, c0, c1, threadIdx.x, kConsumers * 32);
+      }
+    }
+    consumer_sync();  // merge and the statistics are free again
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+inline bool encode_cache(CUtensorMap* map, const void* base, const exq_kv_cache& c, int part_words,
+                         CUtensorMapSwizzle swizzle) {
+  EncodeTiled enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t words = static_cast<cuuint64_t>(c.D) * c.bits / 32;
+  const cuuint64_t dims[3] = {words, static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.n_pages) * c.n_kv_heads};
+  const cuuint64_t strides[2] = {words * 4, words * 4 * c.page_size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(part_words), static_cast<cuuint32_t>(std::min(kTile, c.page_size)), 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int B, int D, int NT>
+exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t stream) {
+  using C = Cfg<B, D, NT>;
+  Maps maps;
+  constexpr CUtensorMapSwizzle kSwizzle = B == 6                ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                          : C::kPartBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                          : C::kPartBytes == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
+  if (!encode_cache(&maps.k, a.codes[0], *call.cache, C::kPartBytes / 4, kSwizzle) ||
+      !encode_cache(&maps.v, a.codes[1], *call.cache, C::kPartBytes / 4, kSwizzle))
+    return EXQ_ERR_CUDA;
+  auto fn = attn_split_kernel<B, D, NT>;
+  static std::once_flag once;
+  std::call_once(once, [&] { cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+  fn<<<std::min(sms * C::kCtas, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a);
+  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
+template <int B>
+exq_status launch_bits(const AttnCall& call, AttnArgs& a, int sms, cudaStream_t stream) {
+  const bool one = static_cast<long long>(call.batch->max_q_len) * a.group <= 8;
+  switch (call.cache->D) {
+    case 64: return one ? launch<B, 64, 1>(call, a, sms, stream) : launch<B, 64, 2>(call, a, sms, stream);
+    case 128: return one ? launch<B, 128, 1>(call, a, sms, stream) : launch<B, 128, 2>(call, a, sms, stream);
+    default: return launch<B, 256, 1>(call, a, sms, stream);
+  }
+}
+
+// rows of a unit, by the same rule
+inline int rows_of(int D, long long rows) { return D == 256 || rows <= 8 ? 8 : 16; }
+
+}  // namespace split
+
+exq_status launch_attn_split4(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_split6(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_split8(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_split16(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+
+}  // namespace exq

@@ -1,0 +1,10 @@
+// The few-row attention kernels of fp16 pages (one translation unit per format: they compile side by side).
+#include "exq_attn_split.cuh"
+
+namespace exq {
+
+exq_status launch_attn_split16(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream) {
+  return split::launch_bits<16>(c, a, sms, stream);
+}
+
+}  // namespace exq

@@ -17,7 +17,8 @@ BUILD = PKG / "_build"
 LIB = PKG / "libexq.so"
 
 SOURCES = ["exq_api.cu", "exq_gemv.cu", "exq_dequant.cu", "exq_gemm.cu", "exq_kv.cu", "exq_convert.cu", "exq_rope.cu",
-           "exq_attn.cu", "exq_attn_split4.cu", "exq_attn_split6.cu", "exq_attn_split8.cu", "exq_attn_split16.cu", "exq_pack.cpp", "exq_pages.cpp"]
+           "exq_attn.cu", *(f"exq_attn_{kind}{bits}.cu" for kind in ("split", "chunk") for bits in (4, 6, 8, 16)),
+           "exq_pack.cpp", "exq_pages.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,7 +1,7 @@
 // Attention of new tokens over a paged (quantised) KV cache: the launch.
 //   o = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale q . k_t - m),
 // over the cached tokens t a row sees, m the running maximum.
-#include "exq_attn_split.cuh"
+#include "exq_attn_chunk.cuh"
 
 namespace exq {
 namespace {
@@ -27,11 +27,17 @@ unsigned* error_word(int dev) {
 
 constexpr int kWaitLimit = 1 << 22;  // try_wait rounds before giving up
 
+// More query rows a KV head than this go to the tensor-memory kernel, whose
+// units have 256 (128) of them; fewer to the packed-code kernel, which reads
+// the cache again for every 16 (8).
+bool many_rows(long long rows) { return rows > 32; }
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms) {
-  const int rows = split::rows_of(c.D, static_cast<long long>(b.max_q_len) * (n_heads / c.n_kv_heads));
-  const size_t ctas = std::min(4 * sms, kAttnMaxCtas);
+  const long long all = static_cast<long long>(b.max_q_len) * (n_heads / c.n_kv_heads);
+  const int rows = many_rows(all) ? chunk::rows_of(c.D) : split::rows_of(c.D, all);
+  const size_t ctas = std::min(many_rows(all) ? sms : 4 * sms, kAttnMaxCtas);
   return kAttnCounterBytes + ctas * 2 * rows * (c.D + 2) * sizeof(float);
 }
 
@@ -75,12 +81,19 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   a.wait_limit = starve > 0 ? starve : kWaitLimit;
   a.starve = starve > 0 ? 1 : 0;
   const long long rows = static_cast<long long>(b.max_q_len) * a.group;
-  const int per = split::rows_of(c.D, rows);
+  const bool many = many_rows(rows);
+  const int per = many ? chunk::rows_of(c.D) : split::rows_of(c.D, rows);
   const long long blocks = (rows + per - 1) / per;
   if (blocks * b.n_seqs > 0x7FFFFFFFll) return EXQ_ERR_UNSUPPORTED;
   if (blocks == 0) return EXQ_OK;
   a.row_blocks = static_cast<int>(blocks);
   a.min_tiles = 2;
+  if (many) switch (c.bits) {
+      case 4: return launch_attn_chunk4(call, a, sms, stream);
+      case 6: return launch_attn_chunk6(call, a, sms, stream);
+      case 8: return launch_attn_chunk8(call, a, sms, stream);
+      default: return launch_attn_chunk16(call, a, sms, stream);
+    }
   switch (c.bits) {
     case 4: return launch_attn_split4(call, a, sms, stream);
     case 6: return launch_attn_split6(call, a, sms, stream);

@@ -1,0 +1,10 @@
+// The many-row attention kernels of fp16 pages (one translation unit per format: they compile side by side).
+#include "exq_attn_chunk.cuh"
+
+namespace exq {
+
+exq_status launch_attn_chunk16(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream) {
+  return chunk::launch_bits<16>(c, a, sms, stream);
+}
+
+}  // namespace exq

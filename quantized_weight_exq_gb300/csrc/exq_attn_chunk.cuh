@@ -3,25 +3,28 @@
 // memory. The multiplications are the bound.
 //
 // A unit is 256 rows (128 for D = 256) of one KV head: two M = 128 tiles, each
-// with its own S and O in tensor memory, so that one tile's softmax runs
-// while the tensor cores work on the other (for D = 256 one tile with two S).
-// Roles of a CTA, one per SM:
+// with its own O and two S buffers of 64 cached tokens in tensor memory, all
+// 512 columns of it for D = 128. The scores of the next tile are computed
+// while a tile's softmax runs, so the softmax never waits for the round trip
+// through the tensor cores (with one S of 128 tokens, its 2000 cycles and the
+// round trip's 2300 came one after the other). Roles of a CTA, one per SM:
 //
-//   warps 0-7   softmax, a thread a row: S from tensor memory in two passes
-//               (the maximum; the weights, which go back as fp16 over S as
-//               the A operand of P V), the sums of weights, and the
-//               epilogue. O is only rescaled when a row's maximum rises by
-//               more than 2^8 over the one in use: weights up to 2^8 have the
-//               same relative precision in fp16.
-//   warps 8-11  loaders: quantised pages come in by plain 16-byte loads one
-//               tile ahead, become the integers (u - z), exact in fp16, and go
-//               to shared memory in the MMA's 128-byte swizzle; fp16 pages
-//               come by TMA. Dequantising once per tile serves 256 rows. The
-//               groups' scales stay in fp32 beside the tile and multiply S's
-//               columns (K) and the weights (V) in the softmax: rounding
-//               (u - z) s to fp16 here instead would be one rounding more per
-//               cached value. Slots past the end are zeros.
+//   warps 0-7   softmax: S once into registers; the weights go back as fp16
+//               over S, the A operand of P V; the sums of weights; the
+//               epilogue. A row's reference is raised, and O rescaled, only
+//               when a score exceeds it by more than 8 (in log2): weights up
+//               to 2^8 have the same relative precision in fp16. So most
+//               tiles need no row maximum over lanes, one vote does.
+//   warps 8-11  dequantisers: packed tiles in shared memory become the
+//               integers (u - z), exact in fp16, in the MMA's 128-byte
+//               swizzle, once for all rows of the unit. The groups' scales
+//               stay in fp32 beside the tile and multiply S's columns (K) and
+//               the weights (V) in the softmax: rounding (u - z) s to fp16
+//               here instead would be one rounding more per cached value. For
+//               fp16 pages, which TMA brings in place, they only put zeros in
+//               V's slots past the end. They also bring Q.
 //   warp 12     issues the MMAs.
+//   warp 13     issues the TMA copies.
 //
 // K is K-major (tokens x 64 dims per 128-byte swizzled row); V has the same
 // layout and is the MN-major B operand, so nothing is transposed.
@@ -29,6 +32,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "exq_attn_split.cuh"
 
@@ -36,34 +40,55 @@ namespace exq {
 namespace chunk {
 
 constexpr int kSoftmaxThreads = 256;
-constexpr int kLoaderThreads = 128;
-constexpr int kThreads = kSoftmaxThreads + kLoaderThreads + 32;
-constexpr int kMmaWarp = 12;
+constexpr int kDequantThreads = 128;
+constexpr int kThreads = 512;  // registers move between whole groups of 4 warps
+constexpr int kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kTile = split::kTile;
+
+// Registers a thread: the block is launched with kLaunchRegs and hands those
+// of the MMA's group to the softmax. The shares may not add up to more than
+// the launch's, or an increase would never be granted.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kDequantRegs = 112, kIssueRegs = 64;
+static_assert(2 * kSoftmaxRegs + kDequantRegs + kIssueRegs <= 4 * kLaunchRegs, "register shares");
+
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int B, int D>
 struct Cfg {
+  using Packed = split::Cfg<B, D, 1>;                // the packed tile's layout, as TMA writes it
   static constexpr int kStreams = D == 256 ? 1 : 2;  // M = 128 tiles of a unit
   static constexpr int kRows = 128 * kStreams;
-  static constexpr int kTile = D == 256 ? 64 : 128;  // cached tokens
-  static constexpr int kSBufs = 2;                   // S buffers: one a stream, or two of the one stream
   static constexpr int kSlabs = D / 64;              // 64 dims: one 128-byte swizzled row
   static constexpr int kArray = kTile * D * 2;       // K or V of a stage, fp16
-  static constexpr int kOffV = 0;                    // two stages each
-  static constexpr int kOffK = 2 * kArray;
-  static constexpr int kOffQ = 4 * kArray;
-  static constexpr int kOffScale = kOffQ + kRows * D * 2;              // [stage][sk, sv][kTile] fp32
-  static constexpr int kOffBar = kOffScale + 2 * 2 * kTile * 4 + 2 * 16;  // and [stage][4] of V's exponents
+  static constexpr int kStages = D == 256 && B == 8 ? 1 : B == 16 && D < 256 ? 4 : 2;  // as many as fit
+  static constexpr int kOffV = 0;
+  static constexpr int kOffK = kStages * kArray;
+  static constexpr int kOffQ = 2 * kStages * kArray;
+  static constexpr int kOffPacked = kOffQ + kRows * D * 2;
+  static constexpr int kPacked = B == 16 ? 0 : Packed::kStage;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 - 512;
+  static constexpr int kPackedFit = B == 16 ? 0 : kRoom / kPacked;
+  static constexpr int kPackedStages = kPackedFit > 4 ? 4 : kPackedFit;
+  static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32
+  static constexpr int kOffExps = kOffScale + 4 * 2 * kTile * 4;          // [4][2]: V's exponents
+  static constexpr int kOffBar = kOffExps + 64;
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static constexpr int kFloats = kRows * (D + 2);
+  static_assert(B == 16 || kPackedStages >= 1, "a packed stage");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // tensor memory columns
-  static constexpr int kTmemS = 0;                   // kSBufs x kTile
-  static constexpr int kTmemO = 256;                 // kStreams x D
+  static constexpr int kTmemS = 0;                   // [stream][2][kTile]
+  static constexpr int kTmemO = 256;                 // [stream][D]
 };
 
-struct Maps {
-  CUtensorMap k, v;  // fp16 pages only
-};
+using split::Maps;
 
 struct Extra {
   float scale;       // |scale| log2(e); 0 is passed as 2^-126
@@ -73,8 +98,15 @@ struct Extra {
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The MMA warp issues as a whole, one lane elected in each instruction: the
+// operands then stay in uniform registers. Issued from a branch that only
+// lane 0 takes, an M = 128, N = 128, K = 16 product took 90 to 140 cycles
+// beside busy softmax warps; this way 64, the tensor cores' own time.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // shared-memory descriptor, 128-byte swizzle: `lead` is the stride between
@@ -92,16 +124,18 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool b_mn_major, bool nega
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// the same value in every lane, known as such to the compiler
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -123,22 +157,59 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 lanes x 64 columns as the fragments of mma.sync: register 4 j + 2 i + k is
+// row lane / 4 + 8 i, column 8 j + 2 (lane % 4) + k
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// and 16 lanes x 16 columns, loaded, scaled by the rows' factors and stored back
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f0, float f1) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * ((i >> 1) & 1 ? f1 : f0));
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 lanes x 32 columns of fp16 pairs: register 2 j + i is row lane / 4 + 8 i, column 4 j + lane % 4
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
-      : "memory");
+// both halves of a warp's 32 rows
+__device__ __forceinline__ void tmem_wait_frag(uint32_t (&r)[2][32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]), "+r"(r[0][5]),
+                 "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]), "+r"(r[0][10]), "+r"(r[0][11]),
+                 "+r"(r[0][12]), "+r"(r[0][13]), "+r"(r[0][14]), "+r"(r[0][15]), "+r"(r[0][16]), "+r"(r[0][17]),
+                 "+r"(r[0][18]), "+r"(r[0][19]), "+r"(r[0][20]), "+r"(r[0][21]), "+r"(r[0][22]), "+r"(r[0][23]),
+                 "+r"(r[0][24]), "+r"(r[0][25]), "+r"(r[0][26]), "+r"(r[0][27]), "+r"(r[0][28]), "+r"(r[0][29]),
+                 "+r"(r[0][30]), "+r"(r[0][31])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]),
+                 "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]), "+r"(r[1][9]), "+r"(r[1][10]), "+r"(r[1][11]),
+                 "+r"(r[1][12]), "+r"(r[1][13]), "+r"(r[1][14]), "+r"(r[1][15]), "+r"(r[1][16]), "+r"(r[1][17]),
+                 "+r"(r[1][18]), "+r"(r[1][19]), "+r"(r[1][20]), "+r"(r[1][21]), "+r"(r[1][22]), "+r"(r[1][23]),
+                 "+r"(r[1][24]), "+r"(r[1][25]), "+r"(r[1][26]), "+r"(r[1][27]), "+r"(r[1][28]), "+r"(r[1][29]),
+                 "+r"(r[1][30]), "+r"(r[1][31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -186,81 +257,66 @@ __device__ __forceinline__ uint32_t operand_at(int rows, int row, int ch) {
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
 
-// ---- loaders of quantised pages: an item is the codes of one 12- or 16-byte
-// piece of a token's row; consecutive threads hold 8 tokens of one piece, so
-// that their 16-byte stores fall on different banks
+// ---- dequantisers: an item is the codes of one 12- (Q6) or 16-byte piece of
+// a token's row; consecutive threads hold 8 tokens of one piece, so that the
+// loads (TMA's swizzle) and the 16-byte stores (the MMA's) fall on different
+// banks
 template <int B, int D>
 struct Item {
   static constexpr int kWords = B == 6 ? 3 : 4;
   static constexpr int kCodes = kWords * 32 / B;            // 32 or 16
   static constexpr int kPerRow = D / kCodes;
-  static constexpr int kItems = Cfg<B, D>::kTile * kPerRow / kLoaderThreads;
+  static constexpr int kItems = kTile * kPerRow / kDequantThreads;
 };
-
-template <int B, int D>
-__device__ __forceinline__ int item_token(int it, int tid) {
-  const int i = it * kLoaderThreads + tid;
-  return (i & 7) + 8 * (i / (8 * Item<B, D>::kPerRow));
-}
-template <int B, int D>
-__device__ __forceinline__ int item_piece(int it, int tid) {
-  return ((it * kLoaderThreads + tid) >> 3) % Item<B, D>::kPerRow;
-}
-
-template <int B, int D>
-__device__ __forceinline__ void load_items(const AttnArgs& a, int which, const int (&pages)[Item<B, D>::kItems], int head,
-                                           int t, int tid, uint32_t (&w)[Item<B, D>::kItems][Item<B, D>::kWords]) {
-  using I = Item<B, D>;
-#pragma unroll
-  for (int it = 0; it < I::kItems; ++it) {
-#pragma unroll
-    for (int j = 0; j < I::kWords; ++j) w[it][j] = 0;
-    if (pages[it] < 0) continue;
-    const int slot = (t * Cfg<B, D>::kTile + item_token<B, D>(it, tid)) & (a.page_size - 1);
-    const long long g = (static_cast<long long>(pages[it]) * a.n_kv_heads + head) * a.page_size + slot;
-    const uint32_t* src = a.codes[which] + g * (D * B / 32) + item_piece<B, D>(it, tid) * I::kWords;
-    if constexpr (B == 6) {
-#pragma unroll
-      for (int j = 0; j < 3; ++j) w[it][j] = __ldg(src + j);
-    } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-      w[it][0] = v.x, w[it][1] = v.y, w[it][2] = v.z, w[it][3] = v.w;
-    }
-  }
-}
 
 // Each 8 codes become a 16-byte chunk of (u - z): Q8 in the dims' order, Q4
 // and Q6 as the unpackers' pairs (0 4 1 5 2 6 3 7), the order in which Q is
 // loaded and O stored
 template <int B, int D>
-__device__ __forceinline__ void store_items(uint32_t base, int tid, const uint32_t (&w)[Item<B, D>::kItems][Item<B, D>::kWords]) {
+__device__ __forceinline__ void dequant(uint32_t src, uint32_t dst, int tid) {
   using I = Item<B, D>;
+  using P = typename Cfg<B, D>::Packed;
 #pragma unroll
   for (int it = 0; it < I::kItems; ++it) {
-    const int row = item_token<B, D>(it, tid), ch = item_piece<B, D>(it, tid) * (I::kCodes / 8);
+    const int i = it * kDequantThreads + tid;
+    const int row = (i & 7) + 8 * (i / (8 * I::kPerRow)), piece = (i >> 3) % I::kPerRow;
+    uint32_t w[4];
+    if constexpr (B == 6) {
+#pragma unroll
+      for (int j = 0; j < 3; ++j) w[j] = split::lds32(src + row * P::kRowBytes + piece * 12 + 4 * j);
+    } else {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(src + split::chunk_at<P>(row, piece)));
+    }
+    const int ch = piece * (I::kCodes / 8);
 #pragma unroll
     for (int j = 0; j < I::kCodes / 8; ++j) {
       uint32_t v[4];
       if constexpr (B == 4) {
-        unpack8<4>(w[it][j], 0u, v);
+        unpack8<4>(w[j], 0u, v);
       } else if constexpr (B == 8) {
-        v[0] = split::q8_pair(w[it][2 * j], 0x4140), v[1] = split::q8_pair(w[it][2 * j], 0x4342);
-        v[2] = split::q8_pair(w[it][2 * j + 1], 0x4140), v[3] = split::q8_pair(w[it][2 * j + 1], 0x4342);
+        v[0] = split::q8_pair(w[2 * j], 0x4140), v[1] = split::q8_pair(w[2 * j], 0x4342);
+        v[2] = split::q8_pair(w[2 * j + 1], 0x4140), v[3] = split::q8_pair(w[2 * j + 1], 0x4342);
       } else {
-        if (j == 0) unpack8<6>(w[it][0], w[it][1], v);
-        else unpack8<6>(fshr(w[it][1], w[it][2], 16), w[it][2] >> 16, v);
+        if (j == 0) unpack8<6>(w[0], w[1], v);
+        else unpack8<6>(fshr(w[1], w[2], 16), w[2] >> 16, v);
       }
-      sts128(base + operand_at(Cfg<B, D>::kTile, row, ch + j), v[0], v[1], v[2], v[3]);
+      sts128(dst + operand_at(kTile, row, ch + j), v[0], v[1], v[2], v[3]);
     }
   }
 }
 
-struct Phase {  // a ring position of two stages, or the parity of one barrier
+// A position in a ring of N stages and the parity of its pass.
+template <int N>
+struct Ring {
   int st = 0;
   uint32_t ph = 0;
   __device__ __forceinline__ void next() {
-    st ^= 1;
-    if (st == 0) ph ^= 1;
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
   }
 };
 
@@ -268,42 +324,45 @@ template <int B, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, const __grid_constant__ Extra x) {
   using C = Cfg<B, D>;
+  using P = typename C::Packed;
   constexpr bool kQuant = B != 16;
   constexpr bool kPairs = B == 4 || B == 6;  // dims in the unpackers' order
-  constexpr int T = C::kTile;
+  constexpr int T = kTile;
+  constexpr int kNP = kQuant ? C::kPackedStages : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
-  int* exps = reinterpret_cast<int*>(scales + 4 * T);
+  int* exps = reinterpret_cast<int*>(smem + C::kOffExps);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  // barriers
-  const uint32_t k_full = smem_u32(bars), k_empty = k_full + 16, v_full = k_full + 32, v_empty = k_full + 48,
-                 s_full = k_full + 64, p_full = k_full + 80, o_full = k_full + 96 /* one a stream */, q_full = k_full + 112,
-                 q_empty = k_full + 120, k_tma = k_full + 128, v_tma = k_full + 144, drain = k_full + 160,
-                 pv_done = k_full + 168;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 23);
-  int* is_last = reinterpret_cast<int*>(bars + 24);
+  const uint32_t bar0 = smem_u32(bars);
+  const auto bar = [bar0](int group, int i) { return bar0 + 8 * (4 * group + i); };
+  enum { kKFull, kKEmpty, kVFull, kVEmpty, kVTma, kPFull /* packed */, kPEmpty, kSFull /* 2 stream + buffer */, kWFull /* weights */, kPvDone /* stream */, kOne };
+  const uint32_t o_full = bar(kOne, 0) /* one a stream */, q_full = bar(kOne, 2), q_empty = bar(kOne, 3), drain = bar(kOne + 1, 0);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * (kOne + 1) + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* is_last = reinterpret_cast<int*>(tmem_slot + 2);
   long long* scratch = reinterpret_cast<long long*>(smem);  // before the first tile
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + 8 * i, kQuant ? kLoaderThreads : 1);
-      mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, kLoaderThreads);
-      mbar_init(v_empty + 8 * i, 1);
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 128);
-      mbar_init(o_full + 8 * i, 1);
-      mbar_init(k_tma + 8 * i, 1);
-      mbar_init(v_tma + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kKFull, i), kQuant ? kDequantThreads : 1);
+      mbar_init(bar(kKEmpty, i), 1);
+      mbar_init(bar(kVFull, i), kDequantThreads);
+      mbar_init(bar(kVEmpty, i), 1);
+      mbar_init(bar(kVTma, i), 1);
+      mbar_init(bar(kPFull, i), 1);
+      mbar_init(bar(kPEmpty, i), kDequantThreads);
+      mbar_init(bar(kSFull, i), 1);
+      mbar_init(bar(kWFull, i), 128);
+      mbar_init(bar(kPvDone, i), 1);
     }
-    mbar_init(q_full, kLoaderThreads);
+    mbar_init(o_full, 1);
+    mbar_init(o_full + 8, 1);
+    mbar_init(q_full, kDequantThreads);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
-    mbar_init(pv_done, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -324,405 +383,415 @@ __global__ void __launch_bounds__(kThreads, 1)
   walk.pair_start = walk.s.pair_start;
   AttnPiece p;
 
-  if (warp == kMmaWarp) {
-    // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t id_qk = instr_desc(T, false, x.negate != 0), id_pv = instr_desc(D, true, false);
-      Phase kr, vr;                       // ring positions of the next QK and PV
-      uint32_t p_ph[2] = {0, 0}, q_ph = 0;
-      const auto qk = [&](int s, int buf) {  // S = Q K^T, to buffer `buf`
-        const uint32_t qa = sbase + C::kOffQ + s * (128 * D * 2), ka = sbase + C::kOffK + kr.st * C::kArray;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + C::kTmemS + buf * T, smem_desc(qa + (i >> 2) * (128 * 128) + (i & 3) * 32, 16),
-                 smem_desc(ka + (i >> 2) * (T * 128) + (i & 3) * 32, 16), id_qk, i > 0);
-        tc_commit(s_full + 8 * buf);
-      };
-      const auto pv = [&](int s, int buf, bool first) {  // O += P V
-        const uint32_t va = sbase + C::kOffV + vr.st * C::kArray;
-#pragma unroll
-        for (int i = 0; i < T / 16; ++i)
-          mma_ts(tmem + C::kTmemO + s * D, tmem + C::kTmemS + buf * T + 8 * i, smem_desc(va + i * 2048, T * 128), id_pv,
-                 !(first && i == 0));
-      };
+  if (warp >= kMmaWarp) {
+    fewer_regs<kIssueRegs>();
+    if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t id_qk = uniform(instr_desc(T, false, x.negate != 0)), id_pv = uniform(instr_desc(D, true, false));
+      const uint32_t tm = uniform(tmem), sb = uniform(sbase);
+      Ring<C::kStages> kr, vr;           // of the next QK and PV
+      uint32_t g[2] = {0, 0};            // tiles of each stream so far whose QK was issued
+      uint32_t w[2] = {0, 0};            // and whose PV was
+      uint32_t q_ph = 0;
       bool ok = true;
       while (ok && attn_next<C::kRows, T>(a, walk, p)) {
-        const int n = p.t1 - p.t0, ns = p.u.rows > 128 ? C::kStreams : 1;
-        ok = mbar_wait(q_full, q_ph, abort_flag, a);
+        const int n = uniform(p.t1 - p.t0), ns = uniform(p.u.rows) > 128 ? C::kStreams : 1;
+        ok = mbar_wait_warp(q_full, q_ph, abort_flag, a);
         q_ph ^= 1;
-        if (!ok) break;
-        tc_after();
-        if constexpr (C::kStreams == 2) {
-          ok = mbar_wait(k_full + 8 * kr.st, kr.ph, abort_flag, a);
-          if (!ok) break;
-          tc_after();
-          for (int s = 0; s < ns; ++s) qk(s, s);
-          tc_commit(k_empty + 8 * kr.st);
-          kr.next();
-          if (n == 1) tc_commit(q_empty);
-          for (int j = 0; j < n && ok; ++j) {
-            for (int s = 0; s < ns && ok; ++s) {
-              ok = mbar_wait(p_full + 8 * s, p_ph[s], abort_flag, a);
-              p_ph[s] ^= 1;
-              if (ok && s == 0) ok = mbar_wait(v_full + 8 * vr.st, vr.ph, abort_flag, a);
-              if (!ok) break;
-              tc_after();
-              pv(s, s, j == 0);
-              if (s == ns - 1) tc_commit(v_empty + 8 * vr.st);
-              if (j + 1 < n) {
-                if (s == 0) ok = mbar_wait(k_full + 8 * kr.st, kr.ph, abort_flag, a);
-                if (!ok) break;
-                tc_after();
-                qk(s, s);
-                if (s == ns - 1) {
-                  tc_commit(k_empty + 8 * kr.st);
-                  kr.next();
-                  if (j + 2 == n) tc_commit(q_empty);
-                }
-              } else {
-                tc_commit(o_full + 8 * s);
-              }
+        for (int j = -1; j < n && ok; ++j) {
+          if (j + 1 < n) {  // S of tile j + 1; its buffer's last weights were read by the P V issued before
+            ok = mbar_wait_warp(bar(kKFull, kr.st), kr.ph, abort_flag, a);
+            if (!ok) break;
+            tc_after();
+            const uint64_t kd = smem_desc(sb + C::kOffK + uniform(kr.st) * C::kArray, 16);
+#pragma unroll
+            for (int s = 0; s < C::kStreams; ++s) {
+              if (s >= ns) break;
+              const uint64_t qd = smem_desc(sb + C::kOffQ + s * (128 * D * 2), 16);
+              const uint32_t buf = 2 * s + uniform(g[s] & 1);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+                mma_ss(tm + C::kTmemS + buf * T, qd + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
+                       kd + ((i >> 2) * (T * 128) + (i & 3) * 32) / 16, id_qk, i > 0);
+              tc_commit(bar(kSFull, buf));
+              ++g[s];
             }
-            vr.next();
+            tc_commit(bar(kKEmpty, kr.st));
+            kr.next();
+            if (j + 2 == n) tc_commit(q_empty);
           }
-        } else {
-          for (int j = 0; j < n + 1 && ok; ++j) {  // QK of tile j, then PV of tile j - 1
-            if (j < n) {
-              ok = mbar_wait(k_full + 8 * kr.st, kr.ph, abort_flag, a);
+          if (j >= 0) {
+            ok = mbar_wait_warp(bar(kVFull, vr.st), vr.ph, abort_flag, a);
+            const uint64_t vd = smem_desc(sb + C::kOffV + uniform(vr.st) * C::kArray, T * 128);
+#pragma unroll
+            for (int s = 0; s < C::kStreams; ++s) {
+              if (s >= ns || !ok) break;
+              const uint32_t buf = 2 * s + uniform(w[s] & 1);
+              ok = mbar_wait_warp(bar(kWFull, buf), (w[s] >> 1) & 1, abort_flag, a);
               if (!ok) break;
               tc_after();
-              qk(0, j & 1);  // its P was read by PV of tile j - 2, issued before
-              tc_commit(k_empty + 8 * kr.st);
-              kr.next();
-              if (j + 1 == n) tc_commit(q_empty);
+#pragma unroll
+              for (int i = 0; i < T / 16; ++i)
+                mma_ts(tm + C::kTmemO + s * D, tm + C::kTmemS + buf * T + 8 * i, vd + i * 128, id_pv, i > 0 ? 1 : j > 0);
+              tc_commit(bar(kPvDone, s));
+              if (j + 1 == n) tc_commit(o_full + 8 * s);
+              ++w[s];
             }
-            if (j > 0) {
-              const int buf = (j - 1) & 1;
-              ok = mbar_wait(p_full + 8 * buf, p_ph[buf], abort_flag, a);
-              p_ph[buf] ^= 1;
-              if (ok) ok = mbar_wait(v_full + 8 * vr.st, vr.ph, abort_flag, a);
-              if (!ok) break;
-              tc_after();
-              pv(0, buf, j == 1);
-              tc_commit(v_empty + 8 * vr.st);
-              vr.next();
-              tc_commit(pv_done);
-              if (j == n) tc_commit(o_full);
-            }
+            if (!ok) break;
+            tc_commit(bar(kVEmpty, vr.st));
+            vr.next();
           }
         }
       }
       // nothing may be in flight when tensor memory is freed
       tc_commit(drain);
       for (int r = 0; r < a.wait_limit; ++r)
-        if (mbar_try_wait(drain, 0)) break;
+        if (__all_sync(0xffffffffu, mbar_try_wait(drain, 0))) break;
+    } else if (warp == kTmaWarp && a.starve == 0) {  // test hook: the other roles' waits run out
+      // ------------------------------------------------------------ TMA producer
+      const int box = min(T, a.page_size), boxes = T / box;  // tokens of a box, boxes of a tile
+      Ring<kNP> pr;
+      Ring<C::kStages> kr;
+      long long issued = 0;
+      bool ok = true;
+      while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+        const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
+        const int b0 = p.t0 * boxes, b1 = p.t1 * boxes;
+        const auto page_of = [&](int bx) {  // -1: nothing to copy
+          const int tok = bx * box;
+          if (bx >= b1 || tok >= p.u.end) return -1;
+          const int page = __ldg(table + tok / a.page_size);
+          if (page < 0 || page >= a.n_pages) {
+            atomicOr(a.err, kDevErrBadPage);
+            return -1;
+          }
+          return page;
+        };
+        int have = b0, page = page_of(b0 + lane), next = page_of(b0 + 32 + lane);
+        for (int t = p.t0; t < p.t1; ++t) {
+          if (t * boxes >= have + 32) {
+            have += 32;
+            page = next;
+            next = page_of(have + 32 + lane);
+          }
+          const int mine = __shfl_sync(0xffffffffu, page, (t * boxes - have + (lane & (boxes - 1))) & 31);
+          const bool copy = lane < boxes && mine >= 0;
+          const unsigned n = __popc(__ballot_sync(0xffffffffu, copy));
+          const int slot = (t * T + lane * box) & (a.page_size - 1), block = mine * a.n_kv_heads + p.head;
+          if constexpr (kQuant) {
+            ok = mbar_wait_warp(bar(kPEmpty, pr.st), pr.ph ^ 1, abort_flag, a);
+            if (!ok) break;
+            const uint32_t full = bar(kPFull, pr.st), base = sbase + C::kOffPacked + pr.st * C::kPacked;
+            if (lane == 0) mbar_expect_tx(full, n * box * (2 * P::kRowBytes + 4));
+            __syncwarp();
+            if (copy) {
+#pragma unroll
+              for (int i = 0; i < P::kParts; ++i) {
+                const uint32_t off = i * (T * P::kPartBytes) + lane * box * P::kPartBytes;
+                split::tma_load_3d(base + off, &maps.k, i * (P::kPartBytes / 4), slot, block, full);
+                split::tma_load_3d(base + P::kArray + off, &maps.v, i * (P::kPartBytes / 4), slot, block, full);
+              }
+              const long long grp = static_cast<long long>(block) * a.page_size + slot;
+              split::bulk_load(base + 2 * P::kArray + lane * box * 2, a.scales[0] + grp, box * 2, full);
+              split::bulk_load(base + 2 * P::kArray + P::kScale + lane * box * 2, a.scales[1] + grp, box * 2, full);
+            }
+            pr.next();
+          } else {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              ok = ok && mbar_wait_warp(bar(which ? kVEmpty : kKEmpty, kr.st), kr.ph ^ 1, abort_flag, a);
+              if (!ok) break;
+              const uint32_t full = bar(which ? kVTma : kKFull, kr.st);
+              if (lane == 0) mbar_expect_tx(full, n * box * D * 2);
+              __syncwarp();
+              if (copy) {
+                const uint32_t base = sbase + (which ? C::kOffV : C::kOffK) + kr.st * C::kArray + lane * box * 128;
+#pragma unroll
+                for (int i = 0; i < C::kSlabs; ++i)
+                  split::tma_load_3d(base + i * (T * 128), which ? &maps.v : &maps.k, i * 32, slot, block, full);
+              }
+            }
+            if (!ok) break;
+            kr.next();
+          }
+          ++issued;
+        }
+      }
+      // every copy lands before the CTA may go
+      constexpr int kRing = kQuant ? kNP : C::kStages;
+      for (long long i = max(0ll, issued - kRing); i < issued; ++i) {
+        const int st = static_cast<int>(i % kRing);
+        const uint32_t ph = (i / kRing) & 1;
+        for (int r = 0; r < a.wait_limit; ++r)
+          if (mbar_try_wait(bar(kQuant ? kPFull : kKFull, st), ph)) break;
+        if constexpr (!kQuant)
+          for (int r = 0; r < a.wait_limit; ++r)
+            if (mbar_try_wait(bar(kVTma, st), ph)) break;
+      }
     }
   } else if (warp >= kSoftmaxThreads / 32) {
-    // -------------------------------------------------------------- loaders
+    // -------------------------------------------------------------- dequantisers
+    fewer_regs<kDequantRegs>();
     const int tid = threadIdx.x - kSoftmaxThreads;
-    Phase kr, vr;
+    Ring<kNP> pr;
+    Ring<C::kStages> r;
+    Ring<4> sr;
     uint32_t q_ph = 0;
-    bool ok = a.starve == 0;  // test hook: the other roles' waits run out
-    long long issued_k = 0, issued_v = 0;
+    bool ok = true;
     while (ok && attn_next<C::kRows, T>(a, walk, p)) {
       // ---- Q: [M tile][slab][128 rows][128 bytes]; rows past the unit are zeros
       ok = mbar_wait_warp(q_empty, q_ph ^ 1, abort_flag, a);
       q_ph ^= 1;
       if (!ok) break;
       const int q_rows = p.u.rows > 128 ? C::kRows : 128;
-      for (int i = tid; i < q_rows * (D / 8); i += kLoaderThreads) {
-        const int row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < p.u.rows) {
-          int token, head;
-          attn_row_of(a, p, row, token, head);
-          v = __ldg(reinterpret_cast<const uint4*>(a.q.data + token * a.q.token_stride + head * a.q.head_stride + 8 * ch));
+      // consecutive threads hold 8 rows of one chunk (their stores fall on different banks); 8 loads at a time
+      for (int i0 = tid; i0 < q_rows * (D / 8); i0 += 8 * kDequantThreads) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = i0 + j * kDequantThreads, row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (row < p.u.rows) {
+            int token, head;
+            attn_row_of(a, p, row, token, head);
+            v[j] = __ldg(reinterpret_cast<const uint4*>(a.q.data + token * a.q.token_stride + head * a.q.head_stride + 8 * ch));
+          }
         }
-        if constexpr (kPairs)
-          v = make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
-        sts128(sbase + C::kOffQ + (row >> 7) * (128 * D * 2) + operand_at(128, row & 127, ch), v.x, v.y, v.z, v.w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = i0 + j * kDequantThreads, row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
+          uint4 u = v[j];
+          if constexpr (kPairs)
+            u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
+          sts128(sbase + C::kOffQ + (row >> 7) * (128 * D * 2) + operand_at(128, row & 127, ch), u.x, u.y, u.z, u.w);
+        }
       }
       async_fence();
       mbar_arrive(q_full);
 
-      const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
-      const auto page_of = [&](int tok) {  // -1: zeros
-        if (tok >= p.u.end) return -1;
-        const int page = __ldg(table + tok / a.page_size);
-        if (page < 0 || page >= a.n_pages) {
-          atomicOr(a.err, kDevErrBadPage);
-          return -1;
-        }
-        return page;
-      };
-      if constexpr (kQuant) {
-        using I = Item<B, D>;
-        // a tile ahead: page ids; a K or V ahead: codes and scales
-        int pages[I::kItems], next_pages[I::kItems], spage, next_spage;
-        uint32_t w[I::kItems][I::kWords];
-        const int stok = tid & (T - 1);
-        uint32_t scale_bits = 0;
-        const auto get_pages = [&](int t, int (&pg)[I::kItems], int& sp) {
-#pragma unroll
-          for (int it = 0; it < I::kItems; ++it) pg[it] = t < p.t1 ? page_of(t * T + item_token<B, D>(it, tid)) : -1;
-          sp = t < p.t1 ? page_of(t * T + stok) : -1;
-        };
-        const auto get_scale = [&](int which, int t) {
-          if (spage < 0) return 0u;
-          const long long g = (static_cast<long long>(spage) * a.n_kv_heads + p.head) * a.page_size +
-                              ((t * T + stok) & (a.page_size - 1));
-          return static_cast<uint32_t>(__ldg(a.scales[which] + g));
-        };
-        get_pages(p.t0, pages, spage);
-        load_items<B, D>(a, 0, pages, p.head, p.t0, tid, w);
-        scale_bits = get_scale(0, p.t0);
-        for (int t = p.t0; t < p.t1 && ok; ++t) {
-          get_pages(t + 1, next_pages, next_spage);
-          // K
-          ok = mbar_wait_warp(k_empty + 8 * kr.st, kr.ph ^ 1, abort_flag, a);
+      for (int t = p.t0; t < p.t1 && ok; ++t) {
+        const int keep = p.u.end - t * T;  // tokens of the tile that exist
+        if constexpr (kQuant) {
+          ok = mbar_wait_warp(bar(kPFull, pr.st), pr.ph, abort_flag, a);
+          if (ok) ok = mbar_wait_warp(bar(kKEmpty, r.st), r.ph ^ 1, abort_flag, a);
           if (!ok) break;
-          store_items<B, D>(sbase + C::kOffK + kr.st * C::kArray, tid, w);
-          // K's scales are read by the softmax of this tile, which ends
-          // before V's stage of the tile is released: the V ring guards both
-          ok = mbar_wait_warp(v_empty + 8 * vr.st, vr.ph ^ 1, abort_flag, a);
+          const uint32_t src = sbase + C::kOffPacked + pr.st * C::kPacked;
+          dequant<B, D>(src, sbase + C::kOffK + r.st * C::kArray, tid);
+          // Scales: threads 0-63 K's, 64-127 V's (zero past the end). Four
+          // tiles' are kept: K's stage being free says that S of two tiles
+          // ago is done, its MMA comes after P V of the tile four ago, and
+          // that after the softmax that read these
+          {
+            const int tok = tid & 63;
+            uint32_t bits = split::lds16(src + 2 * P::kArray + (tid >> 6) * P::kScale + 2 * tok);
+            if (tok >= keep) bits = 0;
+            scales[(2 * sr.st + (tid >> 6)) * T + tok] = half_bits_to_float(bits) * (tid < 64 ? x.scale : 1.f);
+            const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
+            if (tid >= 64 && lane == 0) exps[2 * sr.st + ((tid >> 5) & 1)] = e;
+          }
+          async_fence();
+          mbar_arrive(bar(kKFull, r.st));
+          ok = mbar_wait_warp(bar(kVEmpty, r.st), r.ph ^ 1, abort_flag, a);
           if (!ok) break;
-          if (tid < T) scales[(vr.st * 2) * T + stok] = half_bits_to_float(scale_bits) * x.scale;
-          load_items<B, D>(a, 1, pages, p.head, t, tid, w);
-          scale_bits = get_scale(1, t);
-          const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, scale_bits) >> 10) & 31;
-          if (tid < T) scales[(vr.st * 2 + 1) * T + stok] = half_bits_to_float(scale_bits);
-          if (lane == 0) exps[vr.st * 4 + (tid >> 5)] = e;
+          dequant<B, D>(src + P::kArray, sbase + C::kOffV + r.st * C::kArray, tid);
           async_fence();
-          mbar_arrive(k_full + 8 * kr.st);
-          kr.next();
-          // V
-          store_items<B, D>(sbase + C::kOffV + vr.st * C::kArray, tid, w);
-#pragma unroll
-          for (int it = 0; it < I::kItems; ++it) pages[it] = next_pages[it];
-          spage = next_spage;
-          load_items<B, D>(a, 0, pages, p.head, t + 1, tid, w);
-          scale_bits = get_scale(0, t + 1);
-          async_fence();
-          mbar_arrive(v_full + 8 * vr.st);
-          vr.next();
+          mbar_arrive(bar(kVFull, r.st));
+          mbar_arrive(bar(kPEmpty, pr.st));
+          pr.next();
+          sr.next();
+        } else {
+          ok = mbar_wait_warp(bar(kVTma, r.st), r.ph, abort_flag, a);
+          if (!ok) break;
+          if (keep < T) {  // V's slots past the end may hold anything
+            const int from = max(keep, 0);
+            for (int i = tid; i < (T - from) * (D / 8); i += kDequantThreads)
+              sts128(sbase + C::kOffV + r.st * C::kArray + operand_at(T, from + i / (D / 8), i % (D / 8)), 0, 0, 0, 0);
+            async_fence();
+          }
+          mbar_arrive(bar(kVFull, r.st));
         }
-      } else {
-        const int box = min(T, a.page_size), boxes = T / box;
-        int page = tid < boxes ? page_of(p.t0 * T + tid * box) : -1, last_page = -1;
-        const auto issue = [&](const CUtensorMap* map, uint32_t dst, uint32_t bar, int t, int pg) {  // warp 8
-          const unsigned n = __popc(__ballot_sync(0xffffffffu, pg >= 0));
-          if (lane == 0) mbar_expect_tx(bar, n * box * D * 2);
-          __syncwarp();
-          if (pg >= 0) {
-            const int slot = (t * T + lane * box) & (a.page_size - 1);
-#pragma unroll
-            for (int i = 0; i < C::kSlabs; ++i)
-              split::tma_load_3d(dst + i * (T * 128) + lane * box * 128, map, i * 32, slot, pg * a.n_kv_heads + p.head, bar);
-          }
-        };
-        // K of tile t, then V of tile t - 1 handed on, then V of tile t
-        for (int t = p.t0; t <= p.t1 && ok; ++t) {
-          if (t < p.t1) {
-            ok = mbar_wait_warp(k_empty + 8 * kr.st, kr.ph ^ 1, abort_flag, a);
-            if (!ok) break;
-            if (tid < 32) issue(&maps.k, sbase + C::kOffK + kr.st * C::kArray, k_full + 8 * kr.st, t, page);
-            ++issued_k;
-            kr.next();
-          }
-          if (t > p.t0) {
-            const int st = vr.st ^ 1;  // V of tile t - 1
-            ok = mbar_wait_warp(v_tma + 8 * st, st == 0 ? vr.ph : vr.ph ^ 1, abort_flag, a);
-            if (!ok) break;
-            const int keep = p.u.end - (t - 1) * T;  // tokens of the tile that exist
-            if (keep < T) {
-              for (int i = tid; i < (T - keep) * (D / 8); i += kLoaderThreads)
-                sts128(sbase + C::kOffV + st * C::kArray + operand_at(T, keep + i / (D / 8), i % (D / 8)), 0, 0, 0, 0);
-              async_fence();
-            }
-            mbar_arrive(v_full + 8 * st);
-          }
-          if (t < p.t1) {
-            last_page = page;
-            page = tid < boxes && t + 1 < p.t1 ? page_of((t + 1) * T + tid * box) : -1;
-            ok = mbar_wait_warp(v_empty + 8 * vr.st, vr.ph ^ 1, abort_flag, a);
-            if (!ok) break;
-            if (tid < 32) issue(&maps.v, sbase + C::kOffV + vr.st * C::kArray, v_tma + 8 * vr.st, t, last_page);
-            ++issued_v;
-            vr.next();
-          }
-        }
+        r.next();
       }
-    }
-    if constexpr (!kQuant) {  // every copy lands before the CTA may go
-      for (long long i = max(0ll, issued_k - 2); i < issued_k; ++i)
-        for (int r = 0; r < a.wait_limit; ++r)
-          if (mbar_try_wait(k_full + 8 * (i & 1), (i >> 1) & 1)) break;
-      for (long long i = max(0ll, issued_v - 2); i < issued_v; ++i)
-        for (int r = 0; r < a.wait_limit; ++r)
-          if (mbar_try_wait(v_tma + 8 * (i & 1), (i >> 1) & 1)) break;
     }
   } else {
     // -------------------------------------------------------------- softmax
+    more_regs<kSoftmaxRegs>();
+    // A warp has 32 rows (its lanes of tensor memory). S is read as fragments:
+    // a thread holds 4 rows (k: 8 k + lane / 4) and, of each 8 columns, two, so
+    // that a pair of scales out of shared memory serves 4 rows.
     const int s = C::kStreams == 2 ? warp >> 2 : 0;
     const bool works = C::kStreams == 2 || warp < 4;
-    const int row = s * 128 + (warp & 3) * 32 + lane;     // of the unit
+    const int row0 = s * 128 + (warp & 3) * 32;           // the warp's first row of the unit
+    const int row = row0 + lane;                          // the epilogue's
+    const int col2 = 2 * (lane & 3);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    constexpr uint32_t kHalf = 16u << 16;                 // 16 lanes on
     const uint32_t t_o = tmem + lane_base + C::kTmemO + s * D;
-    uint32_t s_ph[2] = {0, 0}, o_ph = 0, pv_ph = 0;
-    Phase sr;                                             // the scales' ring (V's)
+    uint32_t g = 0, o_ph = 0;                             // tiles of the stream so far
+    uint32_t tiles = 0;                                   // tiles of the CTA so far (the scales' ring)
     bool ok = true;
     while (attn_next<C::kRows, T>(a, walk, p)) {
       const bool active = works && s * 128 < p.u.rows;    // warp-uniform, the same for the stream's warps
-      float m = -INFINITY, l = 0.f, base = 0.f;
-      int kexp = -1;
+      float m[4], nbase[4];                               // references, and -(m - (15 - kexp)), see below
+      uint64_t sum[4];                                    // of weights, even and odd columns
+      int lo[4], hi[4];
+      int kexp = 15;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = -INFINITY, nbase[k] = 0.f, sum[k] = 0;
       if (active) {
-        const int rr = p.u.r0 + min(row, p.u.rows - 1), pos = p.u.len - p.u.n + rr / a.group;
-        const int hi = a.causal ? min(pos + 1, p.u.len) : p.u.len, lo = a.window > 0 ? pos - a.window + 1 : 0;
-        const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+        int all_lo = 0, all_hi = p.u.end;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = p.u.r0 + min(row0 + 8 * k + (lane >> 2), p.u.rows - 1), pos = p.u.len - p.u.n + rr / a.group;
+          hi[k] = a.causal ? min(pos + 1, p.u.len) : p.u.len;
+          lo[k] = a.window > 0 ? pos - a.window + 1 : 0;
+          all_lo = max(all_lo, lo[k]);
+          all_hi = min(all_hi, hi[k]);
+        }
+        all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+        all_hi = __reduce_min_sync(0xffffffffu, all_hi);
         for (int t = p.t0; t < p.t1 && ok; ++t) {
-          const int buf = C::kStreams == 2 ? s : (t - p.t0) & 1;
-          ok = mbar_wait_warp(s_full + 8 * buf, s_ph[buf], abort_flag, a);
-          s_ph[buf] ^= 1;
+          const int buf = 2 * s + (g & 1);
+          ok = mbar_wait_warp(bar(kSFull, buf), (g >> 1) & 1, abort_flag, a);
           if (!ok) break;
           tc_after();
           const uint32_t t_s = tmem + lane_base + C::kTmemS + buf * T;
-          const float* sk = scales + sr.st * 2 * T;
+          const int st = (tiles + (t - p.t0)) & 3;
+          const float* sk = scales + 2 * st * T + col2;
           const float* sv = sk + T;
-          const bool masked = t * T < all_lo || (t + 1) * T > all_hi;  // warp-uniform
-          const int c_lo = lo - t * T, c_hi = hi - t * T;              // the row's columns
-          // ---- maximum
-          float mx = -INFINITY;
-          {
-            uint32_t r[2][32];
-            tmem_ld32(t_s, r[0]);
-#pragma unroll
-            for (int c = 0; c < T / 32; ++c) {
-              tmem_wait_ld(r[c & 1]);
-              if (c + 1 < T / 32) tmem_ld32(t_s + 32 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float v[4];
-                if constexpr (kQuant) {
-                  const float4 k4 = *reinterpret_cast<const float4*>(sk + 32 * c + i);
-                  const float2 u0 = unpack_f2(mul_f2(pack_f2(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1])), pack_f2(k4.x, k4.y)));
-                  const float2 u1 = unpack_f2(mul_f2(pack_f2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3])), pack_f2(k4.z, k4.w)));
-                  v[0] = u0.x, v[1] = u0.y, v[2] = u1.x, v[3] = u1.y;
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r[c & 1][i + j]);
-                }
-                if (masked) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if (32 * c + i + j < c_lo || 32 * c + i + j >= c_hi) v[j] = -INFINITY;
-                }
-                mx = fmaxf(mx, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-              }
-            }
-          }
-          if constexpr (!kQuant) mx = mx == -INFINITY ? mx : mx * x.scale;
-          // ---- the reference `base` = m - (15 - kexp): V's scales are near
-          // 2^(kexp - 15), and weights times scales near 1
-          int e = kexp;
+          const int first = t * T + col2;
+          uint32_t r[2][32];
+          tmem_ld_frag(t_s, r[0]);
+          tmem_ld_frag(t_s + kHalf, r[1]);
+          uint64_t k2[T / 8];
           if constexpr (kQuant) {
-            const int4 e4 = *reinterpret_cast<const int4*>(exps + sr.st * 4);
-            const int tile_e = max(max(e4.x, e4.y), max(e4.z, e4.w));
-            if (kexp < 0 || tile_e > kexp + 4) e = tile_e;
+#pragma unroll
+            for (int j = 0; j < T / 8; ++j) k2[j] = *reinterpret_cast<const uint64_t*>(sk + 8 * j);
           }
-          const float m1 = mx > m + 8.f ? mx : m;  // m = -inf: mx, where anything is seen
-          const float shift = kQuant ? static_cast<float>(15 - e) : 0.f;
-          const float base1 = (m1 == -INFINITY ? 0.f : m1) - shift;
-          const bool moved = t > p.t0 && base1 != base && m != -INFINITY;  // else O is all zeros or not begun
-          if constexpr (C::kStreams == 1) {
-            // P V of the tile before has to be over before O is touched
-            if (t > p.t0) {
-              ok = mbar_wait_warp(pv_done, pv_ph, abort_flag, a);
-              pv_ph ^= 1;
+          tmem_wait_frag(r);
+          // ---- scores (times K's scales), masked, and each thread's maxima;
+          // masked or not is two bodies: a branch a value would leave no
+          // independent work between the links of each value's chain
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const auto scores = [&](auto with_mask) {
+            constexpr bool kMask = decltype(with_mask)::value;
+#pragma unroll
+            for (int j = 0; j < T / 8; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
+                float2 u = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                if constexpr (kQuant) u = unpack_f2(mul_f2(pack_f2(u.x, u.y), k2[j]));
+                if constexpr (kMask) {
+                  if (first + 8 * j < lo[k] || first + 8 * j >= hi[k]) u.x = -INFINITY;
+                  if (first + 8 * j + 1 < lo[k] || first + 8 * j + 1 >= hi[k]) u.y = -INFINITY;
+                }
+                if constexpr (kQuant || kMask) v[0] = __float_as_uint(u.x), v[1] = __float_as_uint(u.y);
+                mx[k] = fmaxf(mx[k], fmaxf(u.x, u.y));
+              }
+          };
+          if (t * T < all_lo || (t + 1) * T > all_hi) scores(std::true_type{});
+          else scores(std::false_type{});
+          // ---- raise the references where a score exceeds one by more than
+          // 8, or V's scales the exponent in use by more than 2^4: V's scales
+          // are near 2^(kexp - 15), and weights 2^(15 - kexp) times larger
+          // keep the products with them near 1
+          int tile_e = 15;
+          if constexpr (kQuant) {
+            const int2 e2 = *reinterpret_cast<const int2*>(exps + 2 * st);
+            tile_e = max(e2.x, e2.y);
+          }
+          bool raise = kQuant && (t == p.t0 || tile_e > kexp + 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (!kQuant) mx[k] = mx[k] == -INFINITY ? mx[k] : mx[k] * x.scale;
+            raise |= mx[k] > m[k] + 8.f;
+          }
+          if (__any_sync(0xffffffffu, raise)) {
+            if (kQuant && (t == p.t0 || tile_e > kexp + 4)) kexp = tile_e;
+            float f[4];
+            bool any = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+              const float m1 = mx[k] > m[k] + 8.f ? mx[k] : m[k];  // m = -inf: mx, where anything is seen
+              const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
+              const bool moved = nb1 != nbase[k] && m[k] != -INFINITY;  // else the row's O is zeros, or not begun
+              f[k] = moved ? exp2_fast(nb1 - nbase[k]) : 1.f;
+              any |= moved;
+              m[k] = m1;
+              nbase[k] = nb1;
+              sum[k] = mul_f2(sum[k], pack_f2(f[k], f[k]));
+            }
+            if (t > p.t0 && __any_sync(0xffffffffu, any)) {
+              // P V of the tile before has to be over before O is touched. (Of
+              // the tile before that it is: S of this tile was issued after it,
+              // so the parity is not ambiguous.)
+              ok = mbar_wait_warp(bar(kPvDone, s), (g - 1) & 1, abort_flag, a);
               if (!ok) break;
               tc_after();
-            }
-          }
-          if (__any_sync(0xffffffffu, moved)) {
-            const float f = moved ? exp2_fast(base - base1) : 1.f;
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(t_o + 32 * c, r);
-              tmem_wait_ld(r);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-              tmem_st32(t_o + 32 * c, r);
-            }
-            tmem_wait_st();
-          }
-          m = m1;
-          kexp = e;
-          base = base1;
-          // ---- weights
-          {
-            const uint64_t nb = pack_f2(-base, -base), sc = pack_f2(x.scale, x.scale);
-            uint64_t sum0 = 0, sum1 = 0;
-            uint32_t r[2][32];
-            tmem_ld32(t_s, r[0]);
-#pragma unroll
-            for (int c = 0; c < T / 32; ++c) {
-              tmem_wait_ld(r[c & 1]);
-              if (c + 1 < T / 32) tmem_ld32(t_s + 32 * (c + 1), r[(c + 1) & 1]);
-              uint32_t out[16];
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                uint64_t u0 = pack_f2(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1]));
-                uint64_t u1 = pack_f2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
-                if constexpr (kQuant) {
-                  const float4 k4 = *reinterpret_cast<const float4*>(sk + 32 * c + i);
-                  u0 = add_f2(mul_f2(u0, pack_f2(k4.x, k4.y)), nb);
-                  u1 = add_f2(mul_f2(u1, pack_f2(k4.z, k4.w)), nb);
-                } else {
-                  u0 = fma_f2(u0, sc, nb);
-                  u1 = fma_f2(u1, sc, nb);
-                }
-                const float2 f0 = unpack_f2(u0), f1 = unpack_f2(u1);
-                float v[4] = {f0.x, f0.y, f1.x, f1.y};
-                if (masked) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if (32 * c + i + j < c_lo || 32 * c + i + j >= c_hi) v[j] = -INFINITY;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = exp2_fast(v[j]);
-                u0 = pack_f2(v[0], v[1]);
-                u1 = pack_f2(v[2], v[3]);
-                sum0 = add_f2(sum0, u0);
-                sum1 = add_f2(sum1, u1);
-                if constexpr (kQuant) {
-                  const float4 v4 = *reinterpret_cast<const float4*>(sv + 32 * c + i);
-                  u0 = mul_f2(u0, pack_f2(v4.x, v4.y));
-                  u1 = mul_f2(u1, pack_f2(v4.z, v4.w));
-                }
-                const float2 g0 = unpack_f2(u0), g1 = unpack_f2(u1);
-                out[i / 2] = half2_bits(g0.x, g0.y);
-                out[i / 2 + 1] = half2_bits(g1.x, g1.y);
+#pragma unroll 2
+              for (int c = 0; c < D / 16; ++c) {  // few registers: the scores stay where they are
+                tmem_scale16(t_o + 16 * c, f[0], f[1]);
+                tmem_scale16(t_o + kHalf + 16 * c, f[2], f[3]);
               }
-              tmem_st16(t_s + 16 * c, out);  // S's columns below 32 (c + 1) have been read
+              tmem_wait_st();
             }
-            const float2 a0 = unpack_f2(add_f2(sum0, sum1));
-            l += a0.x + a0.y;
+          }
+          // ---- weights, to where the scores were
+          {
+            const uint64_t sc = pack_f2(x.scale, x.scale);
+            uint64_t nb[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nb[k] = pack_f2(nbase[k], nbase[k]);
+            uint32_t out[2][16];
+#pragma unroll
+            for (int j = 0; j < T / 8; ++j) {
+              uint64_t v2 = 0;
+              if constexpr (kQuant) v2 = *reinterpret_cast<const uint64_t*>(sv + 8 * j);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
+                uint64_t u = pack_f2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                if constexpr (kQuant)
+                  u = add_f2(u, nb[k]);
+                else
+                  u = fma_f2(u, sc, nb[k]);
+                float2 e = unpack_f2(u);
+                u = pack_f2(exp2_fast(e.x), exp2_fast(e.y));
+                sum[k] = add_f2(sum[k], u);
+                if constexpr (kQuant) u = mul_f2(u, v2);
+                e = unpack_f2(u);
+                out[k >> 1][2 * j + (k & 1)] = half2_bits(e.x, e.y);
+              }
+            }
+            tmem_st_pairs(t_s, out[0]);
+            tmem_st_pairs(t_s + kHalf, out[1]);
           }
           tmem_wait_st();
           tc_before();
-          mbar_arrive(p_full + 8 * buf);
-          sr.next();
+          mbar_arrive(bar(kWFull, buf));
+          ++g;
         }
         if (ok) {
           ok = mbar_wait_warp(o_full + 8 * s, o_ph, abort_flag, a);
           o_ph ^= 1;
-          if constexpr (C::kStreams == 1) pv_ph ^= 1;  // the last P V's
           tc_after();
         }
-      } else {
-        // the ring of scales moves on with the other stream's tiles
-        if ((p.t1 - p.t0) & 1) sr.next();
+      }
+      tiles += p.t1 - p.t0;
+      // the statistics of the thread's row `lane` of the warp: slot lane / 8 of
+      // the lanes from 4 (lane % 8)
+      float row_l = 0.f, row_base = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v2 = unpack_f2(sum[k]);
+        float v = v2.x + v2.y;
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        const float a1 = __shfl_sync(0xffffffffu, v, 4 * (lane & 7)), b1 = __shfl_sync(0xffffffffu, -nbase[k], 4 * (lane & 7));
+        if ((lane >> 3) == k) row_l = a1, row_base = b1;
       }
       // ---- epilogue: a thread holds its row's D values
       const int c0 = p.whole ? 0 : attn_cta_of(walk.s, p.first), c1 = p.whole ? 0 : attn_cta_of(walk.s, p.first + p.u.tiles - 1);
@@ -732,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (has) attn_row_of(a, p, row, token, head);
         uint16_t* dst = a.out.data + token * a.out.token_stride + head * a.out.head_stride;
         float* slot = p.whole ? nullptr : attn_slot(a, blockIdx.x, static_cast<int>(blockIdx.x) == c0, C::kFloats);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = row_l > 0.f ? 1.f / row_l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
@@ -746,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) {
               // 0 4 1 5 2 6 3 7 back to the dims' order
               const int at = kPairs ? (j < 4 ? 2 * j : 2 * (j - 4) + 1) : j;
-              y[j] = l > 0.f ? __uint_as_float(r[i + at]) : 0.f;
+              y[j] = row_l > 0.f ? __uint_as_float(r[i + at]) : 0.f;
             }
             if (p.whole) {
               uint4 o;
@@ -766,9 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (has) {
           if (p.whole)
-            attn_store_lse(a, token, head, base, l);
+            attn_store_lse(a, token, head, row_base, row_l);
           else
-            slot[C::kRows * D + row] = base, slot[C::kRows * D + C::kRows + row] = l;
+            slot[C::kRows * D + row] = row_base, slot[C::kRows * D + C::kRows + row] = row_l;
         }
         tc_before();  // the next unit's first P V, ordered by p_full, overwrites O
       }
@@ -803,16 +872,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int B, int D>
 exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t stream) {
   using C = Cfg<B, D>;
-  Maps maps{};
-  if constexpr (B == 16) {
-    if (!split::encode_cache(&maps.k, a.codes[0], *call.cache, 32, CU_TENSOR_MAP_SWIZZLE_128B, C::kTile) ||
-        !split::encode_cache(&maps.v, a.codes[1], *call.cache, 32, CU_TENSOR_MAP_SWIZZLE_128B, C::kTile))
-      return EXQ_ERR_CUDA;
-  }
+  Maps maps;
+  constexpr int kPart = B == 16 ? 128 : C::Packed::kPartBytes;
+  constexpr CUtensorMapSwizzle kSwizzle = B == 6        ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                          : kPart == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                          : kPart == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                         : CU_TENSOR_MAP_SWIZZLE_32B;
+  if (!split::encode_cache(&maps.k, a.codes[0], *call.cache, kPart / 4, kSwizzle) ||
+      !split::encode_cache(&maps.v, a.codes[1], *call.cache, kPart / 4, kSwizzle))
+    return EXQ_ERR_CUDA;
   const Extra x{std::fmax(std::fabs(a.scale_log2), 0x1p-126f), a.scale_log2 < 0};
   auto fn = attn_chunk_kernel<B, D>;
   static std::once_flag once;
-  std::call_once(once, [&] { cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+  static bool usable = false;
+  std::call_once(once, [&] {
+    cudaFuncAttributes at{};
+    usable = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess &&
+             cudaFuncGetAttributes(&at, fn) == cudaSuccess && (at.numRegs + 7) / 8 * 8 == kLaunchRegs;
+  });
+  if (!usable) return EXQ_ERR_CUDA;
   fn<<<std::min(sms, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a, x);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }

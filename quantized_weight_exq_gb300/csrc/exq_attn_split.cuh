@@ -656,13 +656,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
 // ---------------------------------------------------------------- host
 
 inline bool encode_cache(CUtensorMap* map, const void* base, const exq_kv_cache& c, int part_words,
-                         CUtensorMapSwizzle swizzle, int tile) {
+                         CUtensorMapSwizzle swizzle) {
   EncodeTiled enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t words = static_cast<cuuint64_t>(c.D) * c.bits / 32;
   const cuuint64_t dims[3] = {words, static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.n_pages) * c.n_kv_heads};
   const cuuint64_t strides[2] = {words * 4, words * 4 * c.page_size};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(part_words), static_cast<cuuint32_t>(std::min(tile, c.page_size)), 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(part_words), static_cast<cuuint32_t>(std::min(kTile, c.page_size)), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -677,8 +677,8 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
                                           : C::kPartBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                           : C::kPartBytes == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
                                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
-  if (!encode_cache(&maps.k, a.codes[0], *call.cache, C::kPartBytes / 4, kSwizzle, kTile) ||
-      !encode_cache(&maps.v, a.codes[1], *call.cache, C::kPartBytes / 4, kSwizzle, kTile))
+  if (!encode_cache(&maps.k, a.codes[0], *call.cache, C::kPartBytes / 4, kSwizzle) ||
+      !encode_cache(&maps.v, a.codes[1], *call.cache, C::kPartBytes / 4, kSwizzle))
     return EXQ_ERR_CUDA;
   auto fn = attn_split_kernel<B, D, NT>;
   static std::once_flag once;

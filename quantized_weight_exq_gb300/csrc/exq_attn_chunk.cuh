@@ -67,15 +67,16 @@ struct Cfg {
   static constexpr int kRows = 128 * kStreams;
   static constexpr int kSlabs = D / 64;              // 64 dims: one 128-byte swizzled row
   static constexpr int kArray = kTile * D * 2;       // K or V of a stage, fp16
-  static constexpr int kStages = D == 256 && B == 8 ? 1 : B == 16 && D < 256 ? 4 : 2;  // as many as fit
+  static constexpr int kStages = D == 256 ? 2 : B == 16 ? 4 : 3;  // of K and V together
   static constexpr int kOffV = 0;
   static constexpr int kOffK = kStages * kArray;
   static constexpr int kOffQ = 2 * kStages * kArray;
   static constexpr int kOffPacked = kOffQ + kRows * D * 2;
-  static constexpr int kPacked = B == 16 ? 0 : Packed::kStage;
+  // a packed stage is one tile of K or of V with its scales
+  static constexpr int kPacked = B == 16 ? 0 : (Packed::kArray + Packed::kScale + 1023) / 1024 * 1024;
   static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 - 512;
   static constexpr int kPackedFit = B == 16 ? 0 : kRoom / kPacked;
-  static constexpr int kPackedStages = kPackedFit > 4 ? 4 : kPackedFit;
+  static constexpr int kPackedStages = kPackedFit > 8 ? 8 : kPackedFit;
   static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32
   static constexpr int kOffExps = kOffScale + 4 * 2 * kTile * 4;          // [4][2]: V's exponents
   static constexpr int kOffBar = kOffExps + 64;
@@ -329,17 +330,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kPairs = B == 4 || B == 6;  // dims in the unpackers' order
   constexpr int T = kTile;
   constexpr int kNP = kQuant ? C::kPackedStages : 1;
+  constexpr int kNS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   float* scales = reinterpret_cast<float*>(smem + C::kOffScale);
   int* exps = reinterpret_cast<int*>(smem + C::kOffExps);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  // Barriers. Tiles are counted over the CTA's whole share; S and P V of tile
+  // i complete phase i / 4 of barrier i % 4 of their kinds. Commits cost the
+  // issuing warp some 100 cycles each, so there is one a tile for each kind:
+  // S also says that K has been read, P V that the stage and the weights have.
   const uint32_t bar0 = smem_u32(bars);
-  const auto bar = [bar0](int group, int i) { return bar0 + 8 * (4 * group + i); };
-  enum { kKFull, kKEmpty, kVFull, kVEmpty, kVTma, kPFull /* packed */, kPEmpty, kSFull /* 2 stream + buffer */, kWFull /* weights */, kPvDone /* stream */, kOne };
-  const uint32_t o_full = bar(kOne, 0) /* one a stream */, q_full = bar(kOne, 2), q_empty = bar(kOne, 3), drain = bar(kOne + 1, 0);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * (kOne + 1) + 1);
+  const auto s_full = [bar0](uint32_t tile) { return bar0 + 8 * (tile & 3); };
+  const auto pv_done = [bar0](uint32_t tile) { return bar0 + 32 + 8 * (tile & 3); };
+  const auto w_full = [bar0](int stream, int buf) { return bar0 + 64 + 8 * (2 * stream + buf); };  // weights are there
+  const auto kv_full = [bar0](int st) { return bar0 + 96 + 8 * st; };
+  const auto packed_full = [bar0](int st) { return bar0 + 128 + 8 * st; };
+  const auto packed_empty = [bar0](int st) { return bar0 + 192 + 8 * st; };
+  const uint32_t q_full = bar0 + 256, v_zeroed = bar0 + 264, drain = bar0 + 272;
+  const auto phase4 = [](uint32_t tile) { return (tile >> 2) & 1; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* is_last = reinterpret_cast<int*>(tmem_slot + 2);
   long long* scratch = reinterpret_cast<long long*>(smem);  // before the first tile
@@ -347,21 +358,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(kKFull, i), kQuant ? kDequantThreads : 1);
-      mbar_init(bar(kKEmpty, i), 1);
-      mbar_init(bar(kVFull, i), kDequantThreads);
-      mbar_init(bar(kVEmpty, i), 1);
-      mbar_init(bar(kVTma, i), 1);
-      mbar_init(bar(kPFull, i), 1);
-      mbar_init(bar(kPEmpty, i), kDequantThreads);
-      mbar_init(bar(kSFull, i), 1);
-      mbar_init(bar(kWFull, i), 128);
-      mbar_init(bar(kPvDone, i), 1);
+      mbar_init(s_full(i), 1);
+      mbar_init(pv_done(i), 1);
+      mbar_init(w_full(i >> 1, i & 1), 128);
+      mbar_init(kv_full(i), kQuant ? kDequantThreads : 1);
     }
-    mbar_init(o_full, 1);
-    mbar_init(o_full + 8, 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(packed_full(i), 1);
+      mbar_init(packed_empty(i), kDequantThreads);
+    }
     mbar_init(q_full, kDequantThreads);
-    mbar_init(q_empty, 1);
+    mbar_init(v_zeroed, kDequantThreads);
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -389,57 +396,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ MMA issuer
       const uint32_t id_qk = uniform(instr_desc(T, false, x.negate != 0)), id_pv = uniform(instr_desc(D, true, false));
       const uint32_t tm = uniform(tmem), sb = uniform(sbase);
-      Ring<C::kStages> kr, vr;           // of the next QK and PV
-      uint32_t g[2] = {0, 0};            // tiles of each stream so far whose QK was issued
-      uint32_t w[2] = {0, 0};            // and whose PV was
-      uint32_t q_ph = 0;
+      Ring<kNS> kr, vr;                  // of the next QK and PV
+      uint32_t gq = 0, gp = 0;           // their tiles
+      uint32_t w_ph = 0, q_ph = 0, z_ph = 0;
       bool ok = true;
       while (ok && attn_next<C::kRows, T>(a, walk, p)) {
         const int n = uniform(p.t1 - p.t0), ns = uniform(p.u.rows) > 128 ? C::kStreams : 1;
+        // the tile whose V the dequantisers zero past the end (fp16 pages), if it is in the piece
+        const int ragged = kQuant || p.t1 * T <= p.u.end ? -1 : uniform(n - 1);
         ok = mbar_wait_warp(q_full, q_ph, abort_flag, a);
         q_ph ^= 1;
         for (int j = -1; j < n && ok; ++j) {
           if (j + 1 < n) {  // S of tile j + 1; its buffer's last weights were read by the P V issued before
-            ok = mbar_wait_warp(bar(kKFull, kr.st), kr.ph, abort_flag, a);
+            ok = mbar_wait_warp(kv_full(kr.st), kr.ph, abort_flag, a);
             if (!ok) break;
             tc_after();
             const uint64_t kd = smem_desc(sb + C::kOffK + uniform(kr.st) * C::kArray, 16);
+            const uint32_t ts = tm + C::kTmemS + uniform(gq & 1) * T;
 #pragma unroll
             for (int s = 0; s < C::kStreams; ++s) {
               if (s >= ns) break;
               const uint64_t qd = smem_desc(sb + C::kOffQ + s * (128 * D * 2), 16);
-              const uint32_t buf = 2 * s + uniform(g[s] & 1);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i)
-                mma_ss(tm + C::kTmemS + buf * T, qd + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
+                mma_ss(ts + s * 2 * T, qd + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
                        kd + ((i >> 2) * (T * 128) + (i & 3) * 32) / 16, id_qk, i > 0);
-              tc_commit(bar(kSFull, buf));
-              ++g[s];
             }
-            tc_commit(bar(kKEmpty, kr.st));
+            tc_commit(s_full(gq));
             kr.next();
-            if (j + 2 == n) tc_commit(q_empty);
+            ++gq;
           }
           if (j >= 0) {
-            ok = mbar_wait_warp(bar(kVFull, vr.st), vr.ph, abort_flag, a);
+            if (j == ragged) {
+              ok = mbar_wait_warp(v_zeroed, z_ph, abort_flag, a);
+              z_ph ^= 1;
+            }
             const uint64_t vd = smem_desc(sb + C::kOffV + uniform(vr.st) * C::kArray, T * 128);
+            const uint32_t buf = uniform(gp & 1);
 #pragma unroll
             for (int s = 0; s < C::kStreams; ++s) {
               if (s >= ns || !ok) break;
-              const uint32_t buf = 2 * s + uniform(w[s] & 1);
-              ok = mbar_wait_warp(bar(kWFull, buf), (w[s] >> 1) & 1, abort_flag, a);
+              ok = mbar_wait_warp(w_full(s, buf), (w_ph >> (2 * s + buf)) & 1, abort_flag, a);
+              w_ph ^= 1u << (2 * s + buf);
               if (!ok) break;
               tc_after();
 #pragma unroll
               for (int i = 0; i < T / 16; ++i)
-                mma_ts(tm + C::kTmemO + s * D, tm + C::kTmemS + buf * T + 8 * i, vd + i * 128, id_pv, i > 0 ? 1 : j > 0);
-              tc_commit(bar(kPvDone, s));
-              if (j + 1 == n) tc_commit(o_full + 8 * s);
-              ++w[s];
+                mma_ts(tm + C::kTmemO + s * D, tm + C::kTmemS + (2 * s + buf) * T + 8 * i, vd + i * 128, id_pv,
+                       i > 0 ? 1 : j > 0);
             }
             if (!ok) break;
-            tc_commit(bar(kVEmpty, vr.st));
+            tc_commit(pv_done(gp));
             vr.next();
+            ++gp;
           }
         }
       }
@@ -451,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ TMA producer
       const int box = min(T, a.page_size), boxes = T / box;  // tokens of a box, boxes of a tile
       Ring<kNP> pr;
-      Ring<C::kStages> kr;
-      long long issued = 0;
+      Ring<kNS> r;
+      uint32_t g = 0;          // tiles
+      long long issued = 0;    // stages filled
       bool ok = true;
       while (ok && attn_next<C::kRows, T>(a, walk, p)) {
         const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return page;
         };
         int have = b0, page = page_of(b0 + lane), next = page_of(b0 + 32 + lane);
-        for (int t = p.t0; t < p.t1; ++t) {
+        for (int t = p.t0; t < p.t1; ++t, ++g) {
           if (t * boxes >= have + 32) {
             have += 32;
             page = next;
@@ -479,54 +489,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned n = __popc(__ballot_sync(0xffffffffu, copy));
           const int slot = (t * T + lane * box) & (a.page_size - 1), block = mine * a.n_kv_heads + p.head;
           if constexpr (kQuant) {
-            ok = mbar_wait_warp(bar(kPEmpty, pr.st), pr.ph ^ 1, abort_flag, a);
-            if (!ok) break;
-            const uint32_t full = bar(kPFull, pr.st), base = sbase + C::kOffPacked + pr.st * C::kPacked;
-            if (lane == 0) mbar_expect_tx(full, n * box * (2 * P::kRowBytes + 4));
-            __syncwarp();
-            if (copy) {
-#pragma unroll
-              for (int i = 0; i < P::kParts; ++i) {
-                const uint32_t off = i * (T * P::kPartBytes) + lane * box * P::kPartBytes;
-                split::tma_load_3d(base + off, &maps.k, i * (P::kPartBytes / 4), slot, block, full);
-                split::tma_load_3d(base + P::kArray + off, &maps.v, i * (P::kPartBytes / 4), slot, block, full);
-              }
-              const long long grp = static_cast<long long>(block) * a.page_size + slot;
-              split::bulk_load(base + 2 * P::kArray + lane * box * 2, a.scales[0] + grp, box * 2, full);
-              split::bulk_load(base + 2 * P::kArray + P::kScale + lane * box * 2, a.scales[1] + grp, box * 2, full);
-            }
-            pr.next();
-          } else {
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
-              ok = ok && mbar_wait_warp(bar(which ? kVEmpty : kKEmpty, kr.st), kr.ph ^ 1, abort_flag, a);
+              ok = ok && mbar_wait_warp(packed_empty(pr.st), pr.ph ^ 1, abort_flag, a);
               if (!ok) break;
-              const uint32_t full = bar(which ? kVTma : kKFull, kr.st);
-              if (lane == 0) mbar_expect_tx(full, n * box * D * 2);
+              const uint32_t full = packed_full(pr.st), base = sbase + C::kOffPacked + pr.st * C::kPacked;
+              if (lane == 0) mbar_expect_tx(full, n * box * (P::kRowBytes + 2));
               __syncwarp();
               if (copy) {
-                const uint32_t base = sbase + (which ? C::kOffV : C::kOffK) + kr.st * C::kArray + lane * box * 128;
 #pragma unroll
-                for (int i = 0; i < C::kSlabs; ++i)
-                  split::tma_load_3d(base + i * (T * 128), which ? &maps.v : &maps.k, i * 32, slot, block, full);
+                for (int i = 0; i < P::kParts; ++i)
+                  split::tma_load_3d(base + i * (T * P::kPartBytes) + lane * box * P::kPartBytes, which ? &maps.v : &maps.k,
+                                     i * (P::kPartBytes / 4), slot, block, full);
+                split::bulk_load(base + P::kArray + lane * box * 2,
+                                 a.scales[which] + static_cast<long long>(block) * a.page_size + slot, box * 2, full);
               }
+              pr.next();
+              ++issued;
             }
             if (!ok) break;
-            kr.next();
+          } else {
+            if (g >= kNS) ok = mbar_wait_warp(pv_done(g - kNS), phase4(g - kNS), abort_flag, a);
+            if (!ok) break;
+            const uint32_t full = kv_full(r.st);
+            if (lane == 0) mbar_expect_tx(full, n * box * D * 4);
+            __syncwarp();
+            if (copy) {
+              const uint32_t at = sbase + r.st * C::kArray + lane * box * 128;
+#pragma unroll
+              for (int i = 0; i < C::kSlabs; ++i) {
+                split::tma_load_3d(at + C::kOffK + i * (T * 128), &maps.k, i * 32, slot, block, full);
+                split::tma_load_3d(at + C::kOffV + i * (T * 128), &maps.v, i * 32, slot, block, full);
+              }
+            }
+            r.next();
+            ++issued;
           }
-          ++issued;
         }
       }
       // every copy lands before the CTA may go
-      constexpr int kRing = kQuant ? kNP : C::kStages;
+      constexpr int kRing = kQuant ? kNP : kNS;
       for (long long i = max(0ll, issued - kRing); i < issued; ++i) {
         const int st = static_cast<int>(i % kRing);
-        const uint32_t ph = (i / kRing) & 1;
-        for (int r = 0; r < a.wait_limit; ++r)
-          if (mbar_try_wait(bar(kQuant ? kPFull : kKFull, st), ph)) break;
-        if constexpr (!kQuant)
-          for (int r = 0; r < a.wait_limit; ++r)
-            if (mbar_try_wait(bar(kVTma, st), ph)) break;
+        for (int k = 0; k < a.wait_limit; ++k)
+          if (mbar_try_wait(kQuant ? packed_full(st) : kv_full(st), (i / kRing) & 1)) break;
       }
     }
   } else if (warp >= kSoftmaxThreads / 32) {
@@ -534,14 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fewer_regs<kDequantRegs>();
     const int tid = threadIdx.x - kSoftmaxThreads;
     Ring<kNP> pr;
-    Ring<C::kStages> r;
-    Ring<4> sr;
-    uint32_t q_ph = 0;
+    Ring<kNS> r;
+    uint32_t g = 0;  // tiles
     bool ok = true;
     while (ok && attn_next<C::kRows, T>(a, walk, p)) {
-      // ---- Q: [M tile][slab][128 rows][128 bytes]; rows past the unit are zeros
-      ok = mbar_wait_warp(q_empty, q_ph ^ 1, abort_flag, a);
-      q_ph ^= 1;
+      // ---- Q: [M tile][slab][128 rows][128 bytes]; rows past the unit are
+      // zeros. The last S of the unit before has been computed.
+      if (g > 0) ok = mbar_wait_warp(s_full(g - 1), phase4(g - 1), abort_flag, a);
       if (!ok) break;
       const int q_rows = p.u.rows > 128 ? C::kRows : 128;
       // consecutive threads hold 8 rows of one chunk (their stores fall on different banks); 8 loads at a time
@@ -569,46 +574,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       async_fence();
       mbar_arrive(q_full);
 
-      for (int t = p.t0; t < p.t1 && ok; ++t) {
+      for (int t = p.t0; t < p.t1 && ok; ++t, ++g) {
         const int keep = p.u.end - t * T;  // tokens of the tile that exist
         if constexpr (kQuant) {
-          ok = mbar_wait_warp(bar(kPFull, pr.st), pr.ph, abort_flag, a);
-          if (ok) ok = mbar_wait_warp(bar(kKEmpty, r.st), r.ph ^ 1, abort_flag, a);
-          if (!ok) break;
-          const uint32_t src = sbase + C::kOffPacked + pr.st * C::kPacked;
-          dequant<B, D>(src, sbase + C::kOffK + r.st * C::kArray, tid);
-          // Scales: threads 0-63 K's, 64-127 V's (zero past the end). Four
-          // tiles' are kept: K's stage being free says that S of two tiles
-          // ago is done, its MMA comes after P V of the tile four ago, and
-          // that after the softmax that read these
-          {
-            const int tok = tid & 63;
-            uint32_t bits = split::lds16(src + 2 * P::kArray + (tid >> 6) * P::kScale + 2 * tok);
-            if (tok >= keep) bits = 0;
-            scales[(2 * sr.st + (tid >> 6)) * T + tok] = half_bits_to_float(bits) * (tid < 64 ? x.scale : 1.f);
-            const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
-            if (tid >= 64 && lane == 0) exps[2 * sr.st + ((tid >> 5) & 1)] = e;
+          if (g >= kNS) ok = mbar_wait_warp(pv_done(g - kNS), phase4(g - kNS), abort_flag, a);
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            ok = ok && mbar_wait_warp(packed_full(pr.st), pr.ph, abort_flag, a);
+            if (!ok) break;
+            const uint32_t src = sbase + C::kOffPacked + pr.st * C::kPacked;
+            dequant<B, D>(src, sbase + (which ? C::kOffV : C::kOffK) + r.st * C::kArray, tid);
+            // scales, zero past the end. Four tiles' are kept, and P V of the
+            // tile kNS <= 3 ago, so every weight of the one four ago, is done
+            if (tid < T) {
+              uint32_t bits = split::lds16(src + P::kArray + 2 * tid);
+              if (tid >= keep) bits = 0;
+              scales[(2 * (g & 3) + which) * T + tid] = half_bits_to_float(bits) * (which ? 1.f : x.scale);
+              if (which) {
+                const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
+                if (lane == 0) exps[2 * (g & 3) + (tid >> 5)] = e;
+              }
+            }
+            mbar_arrive(packed_empty(pr.st));
+            pr.next();
           }
-          async_fence();
-          mbar_arrive(bar(kKFull, r.st));
-          ok = mbar_wait_warp(bar(kVEmpty, r.st), r.ph ^ 1, abort_flag, a);
           if (!ok) break;
-          dequant<B, D>(src + P::kArray, sbase + C::kOffV + r.st * C::kArray, tid);
           async_fence();
-          mbar_arrive(bar(kVFull, r.st));
-          mbar_arrive(bar(kPEmpty, pr.st));
-          pr.next();
-          sr.next();
+          mbar_arrive(kv_full(r.st));
         } else {
-          ok = mbar_wait_warp(bar(kVTma, r.st), r.ph, abort_flag, a);
+          ok = mbar_wait_warp(kv_full(r.st), r.ph, abort_flag, a);
           if (!ok) break;
           if (keep < T) {  // V's slots past the end may hold anything
             const int from = max(keep, 0);
             for (int i = tid; i < (T - from) * (D / 8); i += kDequantThreads)
               sts128(sbase + C::kOffV + r.st * C::kArray + operand_at(T, from + i / (D / 8), i % (D / 8)), 0, 0, 0, 0);
             async_fence();
+            mbar_arrive(v_zeroed);
           }
-          mbar_arrive(bar(kVFull, r.st));
         }
         r.next();
       }
@@ -627,8 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     constexpr uint32_t kHalf = 16u << 16;                 // 16 lanes on
     const uint32_t t_o = tmem + lane_base + C::kTmemO + s * D;
-    uint32_t g = 0, o_ph = 0;                             // tiles of the stream so far
-    uint32_t tiles = 0;                                   // tiles of the CTA so far (the scales' ring)
+    uint32_t g = 0;                                       // tiles
     bool ok = true;
     while (attn_next<C::kRows, T>(a, walk, p)) {
       const bool active = works && s * 128 < p.u.rows;    // warp-uniform, the same for the stream's warps
@@ -650,85 +651,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
         all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-        for (int t = p.t0; t < p.t1 && ok; ++t) {
-          const int buf = 2 * s + (g & 1);
-          ok = mbar_wait_warp(bar(kSFull, buf), (g >> 1) & 1, abort_flag, a);
+        bool begun = false;  // every row of the thread has a reference
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++g) {
+          ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
           if (!ok) break;
           tc_after();
-          const uint32_t t_s = tmem + lane_base + C::kTmemS + buf * T;
-          const int st = (tiles + (t - p.t0)) & 3;
-          const float* sk = scales + 2 * st * T + col2;
+          const int buf = g & 1;
+          const uint32_t t_s = tmem + lane_base + C::kTmemS + (2 * s + buf) * T;
+          const float* sk = scales + 2 * (g & 3) * T + col2;
           const float* sv = sk + T;
-          const int first = t * T + col2;
           uint32_t r[2][32];
           tmem_ld_frag(t_s, r[0]);
           tmem_ld_frag(t_s + kHalf, r[1]);
-          uint64_t k2[T / 8];
-          if constexpr (kQuant) {
-#pragma unroll
-            for (int j = 0; j < T / 8; ++j) k2[j] = *reinterpret_cast<const uint64_t*>(sk + 8 * j);
-          }
           tmem_wait_frag(r);
-          // ---- scores (times K's scales), masked, and each thread's maxima;
-          // masked or not is two bodies: a branch a value would leave no
-          // independent work between the links of each value's chain
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          const auto scores = [&](auto with_mask) {
+          // ---- exponents: scores (times K's scales) less the rows'
+          // references, masked, and the thread's largest; masked or not is two
+          // bodies: a branch a value would leave no independent work between
+          // the links of each value's chain
+          const int first = t * T + col2;
+          float top = -INFINITY;
+          const auto exponents = [&](auto with_mask) {
             constexpr bool kMask = decltype(with_mask)::value;
+            const uint64_t sc = pack_f2(x.scale, x.scale);
 #pragma unroll
-            for (int j = 0; j < T / 8; ++j)
+            for (int j = 0; j < T / 8; ++j) {
+              uint64_t k2 = sc;
+              if constexpr (kQuant) k2 = *reinterpret_cast<const uint64_t*>(sk + 8 * j);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
-                float2 u = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                if constexpr (kQuant) u = unpack_f2(mul_f2(pack_f2(u.x, u.y), k2[j]));
+                float2 u = unpack_f2(fma_f2(pack_f2(__uint_as_float(v[0]), __uint_as_float(v[1])), k2, pack_f2(nbase[k], nbase[k])));
                 if constexpr (kMask) {
                   if (first + 8 * j < lo[k] || first + 8 * j >= hi[k]) u.x = -INFINITY;
                   if (first + 8 * j + 1 < lo[k] || first + 8 * j + 1 >= hi[k]) u.y = -INFINITY;
                 }
-                if constexpr (kQuant || kMask) v[0] = __float_as_uint(u.x), v[1] = __float_as_uint(u.y);
-                mx[k] = fmaxf(mx[k], fmaxf(u.x, u.y));
+                v[0] = __float_as_uint(u.x), v[1] = __float_as_uint(u.y);
+                top = fmaxf(top, fmaxf(u.x, u.y));
               }
+            }
           };
-          if (t * T < all_lo || (t + 1) * T > all_hi) scores(std::true_type{});
-          else scores(std::false_type{});
+          if (t * T < all_lo || (t + 1) * T > all_hi) exponents(std::true_type{});
+          else exponents(std::false_type{});
           // ---- raise the references where a score exceeds one by more than
           // 8, or V's scales the exponent in use by more than 2^4: V's scales
           // are near 2^(kexp - 15), and weights 2^(15 - kexp) times larger
           // keep the products with them near 1
           int tile_e = 15;
           if constexpr (kQuant) {
-            const int2 e2 = *reinterpret_cast<const int2*>(exps + 2 * st);
+            const int2 e2 = *reinterpret_cast<const int2*>(exps + 2 * (g & 3));
             tile_e = max(e2.x, e2.y);
           }
-          bool raise = kQuant && (t == p.t0 || tile_e > kexp + 4);
+          const bool new_e = kQuant && (t == p.t0 || tile_e > kexp + 4);
+          if (__any_sync(0xffffffffu, !begun || new_e || top > 8.f + static_cast<float>(15 - kexp))) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (!kQuant) mx[k] = mx[k] == -INFINITY ? mx[k] : mx[k] * x.scale;
-            raise |= mx[k] > m[k] + 8.f;
-          }
-          if (__any_sync(0xffffffffu, raise)) {
-            if (kQuant && (t == p.t0 || tile_e > kexp + 4)) kexp = tile_e;
+            for (int j = 0; j < T / 8; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
+                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1])));
+              }
+            if (new_e) kexp = tile_e;
             float f[4];
             bool any = false;
+            begun = true;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-              const float m1 = mx[k] > m[k] + 8.f ? mx[k] : m[k];  // m = -inf: mx, where anything is seen
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2)) - nbase[k];  // the largest score
+              const float m1 = mx[k] > m[k] + 8.f ? mx[k] : m[k];  // m = -inf: the score, where anything is seen
               const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
               const bool moved = nb1 != nbase[k] && m[k] != -INFINITY;  // else the row's O is zeros, or not begun
               f[k] = moved ? exp2_fast(nb1 - nbase[k]) : 1.f;
               any |= moved;
+              const uint64_t d2 = pack_f2(nb1 - nbase[k], nb1 - nbase[k]);
+#pragma unroll
+              for (int j = 0; j < T / 8; ++j) {
+                uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
+                const float2 u = unpack_f2(add_f2(pack_f2(__uint_as_float(v[0]), __uint_as_float(v[1])), d2));
+                v[0] = __float_as_uint(u.x), v[1] = __float_as_uint(u.y);
+              }
               m[k] = m1;
               nbase[k] = nb1;
+              begun &= m1 != -INFINITY;
               sum[k] = mul_f2(sum[k], pack_f2(f[k], f[k]));
             }
             if (t > p.t0 && __any_sync(0xffffffffu, any)) {
-              // P V of the tile before has to be over before O is touched. (Of
-              // the tile before that it is: S of this tile was issued after it,
-              // so the parity is not ambiguous.)
-              ok = mbar_wait_warp(bar(kPvDone, s), (g - 1) & 1, abort_flag, a);
+              // P V of the tile before has to be over before O is touched
+              ok = mbar_wait_warp(pv_done(g - 1), phase4(g - 1), abort_flag, a);
               if (!ok) break;
               tc_after();
 #pragma unroll 2
@@ -741,10 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---- weights, to where the scores were
           {
-            const uint64_t sc = pack_f2(x.scale, x.scale);
-            uint64_t nb[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) nb[k] = pack_f2(nbase[k], nbase[k]);
             uint32_t out[2][16];
 #pragma unroll
             for (int j = 0; j < T / 8; ++j) {
@@ -753,16 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
-                uint64_t u = pack_f2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                if constexpr (kQuant)
-                  u = add_f2(u, nb[k]);
-                else
-                  u = fma_f2(u, sc, nb[k]);
-                float2 e = unpack_f2(u);
-                u = pack_f2(exp2_fast(e.x), exp2_fast(e.y));
+                uint64_t u = pack_f2(exp2_fast(__uint_as_float(v[0])), exp2_fast(__uint_as_float(v[1])));
                 sum[k] = add_f2(sum[k], u);
                 if constexpr (kQuant) u = mul_f2(u, v2);
-                e = unpack_f2(u);
+                const float2 e = unpack_f2(u);
                 out[k >> 1][2 * j + (k & 1)] = half2_bits(e.x, e.y);
               }
             }
@@ -771,16 +771,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
           tc_before();
-          mbar_arrive(bar(kWFull, buf));
-          ++g;
+          mbar_arrive(w_full(s, buf));
         }
         if (ok) {
-          ok = mbar_wait_warp(o_full + 8 * s, o_ph, abort_flag, a);
-          o_ph ^= 1;
+          ok = mbar_wait_warp(pv_done(g - 1), phase4(g - 1), abort_flag, a);
           tc_after();
         }
+      } else if (works) {
+        // stays in step with the tiles, so that no phase is missed
+        for (int t = p.t0; t < p.t1 && ok; ++t, ++g) ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
       }
-      tiles += p.t1 - p.t0;
       // the statistics of the thread's row `lane` of the warp: slot lane / 8 of
       // the lanes from 4 (lane % 8)
       float row_l = 0.f, row_base = 0.f;

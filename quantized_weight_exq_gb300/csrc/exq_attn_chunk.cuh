@@ -23,7 +23,12 @@
 //               here instead would be one rounding more per cached value. For
 //               fp16 pages, which TMA brings in place, they only put zeros in
 //               V's slots past the end. They also bring Q.
-//   warp 12     issues the MMAs.
+//   warp 12     issues S = Q K^T, warps 14 and 15 O += P V of the two M tiles.
+//               An MMA is accepted about when the one before is done, so a
+//               warp's wait on a barrier (100 to 300 cycles beside busy warps,
+//               even if it is complete) leaves the tensor cores idle; with
+//               three issuers another's MMAs fill the gap (one issuer: 2500
+//               cycles a tile, of which 1260 were MMAs).
 //   warp 13     issues the TMA copies.
 //
 // K is K-major (tokens x 64 dims per 128-byte swizzled row); V has the same
@@ -42,7 +47,7 @@ namespace chunk {
 constexpr int kSoftmaxThreads = 256;
 constexpr int kDequantThreads = 128;
 constexpr int kThreads = 512;  // registers move between whole groups of 4 warps
-constexpr int kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kScoreWarp = 12, kTmaWarp = 13, kValueWarp = 14;
 constexpr int kTile = split::kTile;
 
 // Registers a thread: the block is launched with kLaunchRegs and hands those
@@ -338,9 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* exps = reinterpret_cast<int*>(smem + C::kOffExps);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   // Barriers. Tiles are counted over the CTA's whole share; S and P V of tile
-  // i complete phase i / 4 of barrier i % 4 of their kinds. Commits cost the
-  // issuing warp some 100 cycles each, so there is one a tile for each kind:
-  // S also says that K has been read, P V that the stage and the weights have.
+  // i complete phase i / 4 of barrier i % 4 of their kinds. P V says too that
+  // the stage of K and V and the weights (S's buffer) have been read.
   const uint32_t bar0 = smem_u32(bars);
   const auto s_full = [bar0](uint32_t tile) { return bar0 + 8 * (tile & 3); };
   const auto pv_done = [bar0](uint32_t tile) { return bar0 + 32 + 8 * (tile & 3); };
@@ -348,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto kv_full = [bar0](int st) { return bar0 + 96 + 8 * st; };
   const auto packed_full = [bar0](int st) { return bar0 + 128 + 8 * st; };
   const auto packed_empty = [bar0](int st) { return bar0 + 192 + 8 * st; };
-  const uint32_t q_full = bar0 + 256, v_zeroed = bar0 + 264, drain = bar0 + 272;
+  const auto v_ready = [bar0](uint32_t tile) { return bar0 + 256 + 8 * (tile & 3); };  // fp16 pages: zeros past the end
+  const uint32_t q_full = bar0 + 288, drain = bar0 + 296 /* of warps 12, 14, 15 */;
   const auto phase4 = [](uint32_t tile) { return (tile >> 2) & 1; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 36);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 40);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* is_last = reinterpret_cast<int*>(tmem_slot + 2);
   long long* scratch = reinterpret_cast<long long*>(smem);  // before the first tile
@@ -359,24 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(pv_done(i), 1);
+      mbar_init(pv_done(i), C::kStreams);
       mbar_init(w_full(i >> 1, i & 1), 128);
       mbar_init(kv_full(i), kQuant ? kDequantThreads : 1);
+      mbar_init(v_ready(i), kDequantThreads);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(packed_full(i), 1);
       mbar_init(packed_empty(i), kDequantThreads);
     }
     mbar_init(q_full, kDequantThreads);
-    mbar_init(v_zeroed, kDequantThreads);
-    mbar_init(drain, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(drain + 8 * i, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   AttnWalk walk;
   walk.s = attn_share<C::kRows, T>(a, scratch);
   if (walk.s.begin >= walk.s.end) return;  // the whole CTA
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -390,72 +395,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   walk.pair_start = walk.s.pair_start;
   AttnPiece p;
 
-  if (warp >= kMmaWarp) {
+  if (warp >= kScoreWarp) {
     fewer_regs<kIssueRegs>();
-    if (warp == kMmaWarp) {
-      // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_qk = uniform(instr_desc(T, false, x.negate != 0)), id_pv = uniform(instr_desc(D, true, false));
-      const uint32_t tm = uniform(tmem), sb = uniform(sbase);
-      Ring<kNS> kr, vr;                  // of the next QK and PV
-      uint32_t gq = 0, gp = 0;           // their tiles
-      uint32_t w_ph = 0, q_ph = 0, z_ph = 0;
+    if (warp == kScoreWarp) {
+      // ------------------------------------------------------------ S = Q K^T
+      const uint32_t idesc = uniform(instr_desc(T, false, x.negate != 0));
+      const uint32_t tm = uniform(tmem + C::kTmemS), sb = uniform(sbase);
+      Ring<kNS> r;
+      uint32_t g = 0, q_ph = 0;
       bool ok = true;
       while (ok && attn_next<C::kRows, T>(a, walk, p)) {
         const int n = uniform(p.t1 - p.t0), ns = uniform(p.u.rows) > 128 ? C::kStreams : 1;
-        // the tile whose V the dequantisers zero past the end (fp16 pages), if it is in the piece
-        const int ragged = kQuant || p.t1 * T <= p.u.end ? -1 : uniform(n - 1);
         ok = mbar_wait_warp(q_full, q_ph, abort_flag, a);
         q_ph ^= 1;
-        for (int j = -1; j < n && ok; ++j) {
-          if (j + 1 < n) {  // S of tile j + 1; its buffer's last weights were read by the P V issued before
-            ok = mbar_wait_warp(kv_full(kr.st), kr.ph, abort_flag, a);
-            if (!ok) break;
-            tc_after();
-            const uint64_t kd = smem_desc(sb + C::kOffK + uniform(kr.st) * C::kArray, 16);
-            const uint32_t ts = tm + C::kTmemS + uniform(gq & 1) * T;
+        for (int j = 0; j < n && ok; ++j, ++g) {
+          ok = mbar_wait_warp(kv_full(r.st), r.ph, abort_flag, a);
+          if (ok && g >= 2) ok = mbar_wait_warp(pv_done(g - 2), phase4(g - 2), abort_flag, a);  // the buffer's last weights
+          if (!ok) break;
+          tc_after();
+          const uint64_t kd = smem_desc(sb + C::kOffK + uniform(r.st) * C::kArray, 16);
+          const uint32_t ts = tm + uniform(g & 1) * T;
 #pragma unroll
-            for (int s = 0; s < C::kStreams; ++s) {
-              if (s >= ns) break;
-              const uint64_t qd = smem_desc(sb + C::kOffQ + s * (128 * D * 2), 16);
+          for (int s = 0; s < C::kStreams; ++s) {
+            if (s >= ns) break;
+            const uint64_t qd = smem_desc(sb + C::kOffQ + s * (128 * D * 2), 16);
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                mma_ss(ts + s * 2 * T, qd + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
-                       kd + ((i >> 2) * (T * 128) + (i & 3) * 32) / 16, id_qk, i > 0);
-            }
-            tc_commit(s_full(gq));
-            kr.next();
-            ++gq;
+            for (int i = 0; i < D / 16; ++i)
+              mma_ss(ts + s * 2 * T, qd + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
+                     kd + ((i >> 2) * (T * 128) + (i & 3) * 32) / 16, idesc, i > 0);
           }
-          if (j >= 0) {
-            if (j == ragged) {
-              ok = mbar_wait_warp(v_zeroed, z_ph, abort_flag, a);
-              z_ph ^= 1;
-            }
-            const uint64_t vd = smem_desc(sb + C::kOffV + uniform(vr.st) * C::kArray, T * 128);
-            const uint32_t buf = uniform(gp & 1);
-#pragma unroll
-            for (int s = 0; s < C::kStreams; ++s) {
-              if (s >= ns || !ok) break;
-              ok = mbar_wait_warp(w_full(s, buf), (w_ph >> (2 * s + buf)) & 1, abort_flag, a);
-              w_ph ^= 1u << (2 * s + buf);
-              if (!ok) break;
-              tc_after();
-#pragma unroll
-              for (int i = 0; i < T / 16; ++i)
-                mma_ts(tm + C::kTmemO + s * D, tm + C::kTmemS + (2 * s + buf) * T + 8 * i, vd + i * 128, id_pv,
-                       i > 0 ? 1 : j > 0);
-            }
-            if (!ok) break;
-            tc_commit(pv_done(gp));
-            vr.next();
-            ++gp;
-          }
+          tc_commit(s_full(g));
+          r.next();
         }
       }
-      // nothing may be in flight when tensor memory is freed
       tc_commit(drain);
-      for (int r = 0; r < a.wait_limit; ++r)
-        if (__all_sync(0xffffffffu, mbar_try_wait(drain, 0))) break;
+    } else if (warp >= kValueWarp && warp - kValueWarp < C::kStreams) {
+      // ------------------------------------------------------------ O += P V of one M tile
+      const uint32_t s = uniform(warp - kValueWarp), idesc = uniform(instr_desc(D, true, false));
+      const uint32_t to = uniform(tmem + C::kTmemO + s * D), tp = uniform(tmem + C::kTmemS + 2 * s * T), sb = uniform(sbase);
+      Ring<kNS> r;
+      uint32_t g = 0, w_ph = 0;
+      bool ok = true;
+      while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+        const int n = uniform(p.t1 - p.t0);
+        const bool active = uniform(p.u.rows) > 128 * s;
+        for (int j = 0; j < n && ok; ++j, ++g, r.next()) {
+          if (!active) {  // keeps the phases whole
+            ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
+            if (ok && lane == 0) mbar_arrive(pv_done(g));
+            continue;
+          }
+          const uint32_t buf = uniform(g & 1);
+          if (!kQuant) ok = mbar_wait_warp(v_ready(g), phase4(g), abort_flag, a);
+          ok = ok && mbar_wait_warp(w_full(s, buf), (w_ph >> buf) & 1, abort_flag, a);
+          w_ph ^= 1u << buf;
+          if (!ok) break;
+          tc_after();
+          const uint64_t vd = smem_desc(sb + C::kOffV + uniform(r.st) * C::kArray, T * 128);
+#pragma unroll
+          for (int i = 0; i < T / 16; ++i) mma_ts(to, tp + buf * T + 8 * i, vd + i * 128, idesc, i > 0 ? 1 : j > 0);
+          tc_commit(pv_done(g));
+        }
+      }
+      tc_commit(drain + 8 * (1 + s));
     } else if (warp == kTmaWarp && a.starve == 0) {  // test hook: the other roles' waits run out
       // ------------------------------------------------------------ TMA producer
       const int box = min(T, a.page_size), boxes = T / box;  // tokens of a box, boxes of a tile
@@ -609,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = tid; i < (T - from) * (D / 8); i += kDequantThreads)
               sts128(sbase + C::kOffV + r.st * C::kArray + operand_at(T, from + i / (D / 8), i % (D / 8)), 0, 0, 0, 0);
             async_fence();
-            mbar_arrive(v_zeroed);
           }
+          mbar_arrive(v_ready(g));
         }
         r.next();
       }
@@ -859,9 +861,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  // nothing may be in flight when tensor memory is freed
+  if (warp == kScoreWarp)
+    for (int i = 0; i < 1 + C::kStreams; ++i)
+      for (int r = 0; r < a.wait_limit; ++r)
+        if (__all_sync(0xffffffffu, mbar_try_wait(drain + 8 * i, 0))) break;
   tc_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }

@@ -323,15 +323,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
-    float o[NT][kSteps][4], m[NT][2], l[NT][2];
+    float o[NT][kSteps][4], l[NT][2];
+    float m[NT][2], nbase[NT][2];  // the rows' references, and -(m - (15 - kexp)), see below
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) l[nt][i] = 0.f, m[nt][i] = -INFINITY;
+      for (int i = 0; i < 2; ++i) l[nt][i] = 0.f, m[nt][i] = -INFINITY, nbase[nt][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
-    int kexp = -1;        // V's scales are read times 2^(15 - kexp)
+    int kexp = 15;        // V's scales are near 2^(kexp - 15)
+    bool begun = false;   // every row of the lane has a reference
+    bool started = false; // kexp is set
 
     for (int t = p.t0; t < p.t1; ++t) {
       // a wait that gave up leaves the unit as it is, but no barrier below:
@@ -412,63 +415,75 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         // ---------------------------------------------------------- softmax
         const bool all_see = first >= all_lo && first + 16 <= all_hi;
         float ksA = a.scale_log2, ksB = a.scale_log2, vsA = 1.f, vsB = 1.f;
+        uint32_t vtop = 0;
         if constexpr (kQuant) {
           ksA *= half_bits_to_float(lds16(sbase + 2 * tokA));
           ksB *= half_bits_to_float(lds16(sbase + 2 * tokB));
           uint32_t va = lds16(sbase + C::kScale + 2 * tokA), vb = lds16(sbase + C::kScale + 2 * tokB);
-          if (tA >= p.u.end) va = 0;  // whatever the slots past the end hold
-          if (tB >= p.u.end) vb = 0;
-          // V's scales are brought near 1, or their products with small
-          // weights would leave fp16's normal range: times 2^(15 - kexp),
-          // kexp the (biased) exponent of the largest so far, moved only when
-          // one is 2^6 above it
-          const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, max(va, vb)) >> 10) & 31;
-          if (kexp < 0) {
-            kexp = e;
-          } else if (e > kexp + 6) {
-            const float f = __uint_as_float(static_cast<uint32_t>(127 + kexp - e) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[nt][i][j] *= f;
-            kexp = e;
+          if (first + 16 > p.u.end) {  // whatever the slots past the end hold
+            if (tA >= p.u.end) va = 0;
+            if (tB >= p.u.end) vb = 0;
           }
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + 15 - kexp) << 23);
-          vsA = half_bits_to_float(va) * f;
-          vsB = half_bits_to_float(vb) * f;
+          vtop = max(va, vb);
+          vsA = half_bits_to_float(va);
+          vsB = half_bits_to_float(vb);
+        }
+        // exponents: scores less the rows' references, and the lane's largest
+        float x[NT][4], top = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[nt][i] = fmaf(s[nt][i] + s2[nt][i], i < 2 ? ksA : ksB, nbase[nt][i & 1]);
+            const int tt = i < 2 ? tA : tB;
+            if (!all_see && (tt < lo[nt][i & 1] || tt >= hi[nt][i & 1])) x[nt][i] = -INFINITY;
+            top = fmaxf(top, x[nt][i]);
+          }
+        // A row's reference is raised only where a score exceeds it by more
+        // than 8 (weights up to 2^8 have the same relative precision in fp16),
+        // and the exponent that stands for V's scales where one is 2^4 above
+        // it: weights are kept 2^(15 - kexp) larger, so that their products
+        // with V's scales stay in fp16's normal range. Most steps need no
+        // maximum over lanes, one vote does.
+        if (__any_sync(0xffffffffu, !begun || top > 8.f + static_cast<float>(15 - kexp) ||
+                                        (kQuant && static_cast<int>(vtop >> 10) > kexp + 4))) {
+          if constexpr (kQuant) {
+            const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, vtop) >> 10) & 31;
+            if (!started || e > kexp + 4) kexp = e;  // the same in all lanes
+            started = true;
+          }
+          begun = true;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mx = fmaxf(x[nt][i], x[nt][i + 2]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              mx -= nbase[nt][i];  // the largest score
+              const float m1 = mx > m[nt][i] + 8.f ? mx : m[nt][i];  // m = -inf: the score, where anything is seen
+              const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
+              const float d = nb1 - nbase[nt][i];
+              f[i] = m[nt][i] == -INFINITY ? 1.f : exp2_fast(d);  // -inf: o and l are zeros
+              x[nt][i] += d;
+              x[nt][i + 2] += d;
+              m[nt][i] = m1;
+              nbase[nt][i] = nb1;
+              begun &= m1 != -INFINITY;
+              l[nt][i] *= f[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              o[nt][i][0] *= f[0], o[nt][i][1] *= f[1];
+              o[nt][i][2] *= f[0], o[nt][i][3] *= f[1];
+            }
+          }
         }
         uint32_t pb0[NT], pb1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = (s[nt][i] + s2[nt][i]) * (i < 2 ? ksA : ksB);
-            const int tt = i < 2 ? tA : tB;
-            if (!all_see && (tt < lo[nt][i & 1] || tt >= hi[nt][i & 1])) x[i] = -INFINITY;
-          }
-          float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-          }
-          const bool more = m0 > m[nt][0] || m1 > m[nt][1];
-          if (__any_sync(0xffffffffu, more)) {
-            const float n0 = fmaxf(m[nt][0], m0), n1 = fmaxf(m[nt][1], m1);
-            const float f0 = n0 == -INFINITY ? 1.f : exp2_fast(m[nt][0] - n0), f1 = n1 == -INFINITY ? 1.f : exp2_fast(m[nt][1] - n1);
-            m[nt][0] = n0, m[nt][1] = n1;
-            l[nt][0] *= f0, l[nt][1] *= f1;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              o[nt][i][0] *= f0, o[nt][i][1] *= f1;
-              o[nt][i][2] *= f0, o[nt][i][3] *= f1;
-            }
-          }
-          const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float w0 = exp2_fast(x[0] - b0), w1 = exp2_fast(x[1] - b1), w2 = exp2_fast(x[2] - b0), w3 = exp2_fast(x[3] - b1);
+          const float w0 = exp2_fast(x[nt][0]), w1 = exp2_fast(x[nt][1]), w2 = exp2_fast(x[nt][2]), w3 = exp2_fast(x[nt][3]);
           l[nt][0] += w0 + w2;
           l[nt][1] += w1 + w3;
           const __half2 h0 = __floats2half2_rn(w0 * vsA, w1 * vsA), h1 = __floats2half2_rn(w2 * vsB, w3 * vsB);
@@ -562,12 +577,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
         if (g == 0) {
-          stat_m[warp * C::kRows + 8 * nt + 2 * c + i] = m[nt][i];
+          stat_m[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i] > 0.f ? -nbase[nt][i] : -INFINITY;
           stat_l[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i];
         }
       }
     consumer_sync();
-    const float back = kQuant ? __uint_as_float(static_cast<uint32_t>(127 - 15 + max(kexp, 0)) << 23) : 1.f;
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, stat_m[w * C::kRows + 8 * nt + 2 * c + i]);
-        f[nt][i] = m[nt][i] == -INFINITY ? 0.f : exp2_fast(m[nt][i] - mm) * back;
+        f[nt][i] = l[nt][i] > 0.f ? exp2_fast(-nbase[nt][i] - mm) : 0.f;
       }
     const auto put = [&](float* region, bool add) {
 #pragma unroll

@@ -161,7 +161,8 @@ def _np_ptr(a: Optional[np.ndarray]):
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without the Stream object around it (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -453,7 +454,7 @@ class Rope:
     """Rotary parameters on the GPU: steps int64 [R/2] (uint64 bits, exq_rope_steps), the layout and the gain."""
 
     def __init__(self, steps, R: int, layout: int = ROPE_HALF, gain: float = 1.0):
-        if steps.numel() < R // 2 or steps.element_size() != 8 or not steps.is_contiguous():
+        if steps.numel() < R // 2 or steps.element_size() != 8 or steps.is_floating_point() or not steps.is_contiguous():
             raise ExqError(EXQ_ERR_INVALID_ARG, "Rope")
         self.steps, self.R, self.layout, self.gain = steps, R, layout, gain
         self._desc = exq_rope_params(steps.data_ptr(), R, layout, gain)
@@ -468,12 +469,11 @@ def rope_table(R: int, layout: int = ROPE_HALF, device="cuda", **freqs) -> Rope:
 
 def _rows(x, where: str, D: Optional[int] = None, heads: Optional[int] = None, tokens: Optional[int] = None):
     """Descriptor of fp16 [tokens, heads, D] with a contiguous last axis."""
+    import torch
     t, h, d = x.shape
-    if (x.element_size() != 2 or not x.is_floating_point() or (D is not None and d != D) or (heads is not None and h != heads)
-            or (tokens is not None and t < tokens)):
-        raise ExqError(EXQ_ERR_INVALID_ARG, where)
     st, sh, sd = x.stride()
-    if sd != 1 and d > 1:
+    if (x.dtype != torch.float16 or (sd != 1 and d > 1) or (D is not None and d != D) or (heads is not None and h != heads)
+            or (tokens is not None and t < tokens)):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     return exq_rows(x.data_ptr(), st, sh)
 
@@ -500,13 +500,17 @@ class KVCache:
     fp16 pairs for bits 16), k_scales, v_scales fp16 [layers, pages, KV heads, page_size] (None for bits 16)."""
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales, bits: int):
-        L, P, H, S, W = k_codes.shape
-        for t, n in ((k_codes, 4), (v_codes, 4), (k_scales, 2), (v_scales, 2)):
-            if t is None:
-                continue
-            if t.element_size() != n or tuple(t.shape[:4]) != (L, P, H, S) or not t.is_contiguous():
-                raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
-        if v_codes.shape != k_codes.shape or W * 32 % bits or (k_scales is None) != (v_scales is None):
+        import torch
+        shape = k_codes.shape
+        L, P, H, S, W = shape
+        quantised = bits != 16
+        if (k_codes.dtype != torch.int32 or v_codes.dtype != torch.int32 or v_codes.shape != shape or W * 32 % bits
+                or not k_codes.is_contiguous() or not v_codes.is_contiguous()
+                or (k_scales is not None) != quantised or (v_scales is not None) != quantised):
+            raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
+        if quantised and (k_scales.dtype != torch.float16 or v_scales.dtype != torch.float16
+                          or k_scales.shape != shape[:4] or v_scales.shape != shape[:4]
+                          or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.bits, self.D, self.n_kv_heads, self.page_size, self.n_pages, self.n_layers = bits, W * 32 // bits, H, S, P, L
@@ -530,10 +534,11 @@ class KVBatch:
 
     def __init__(self, q_start, kv_len, page_table, max_q_len: int, max_kv_len: int, n_tokens: Optional[int] = None):
         B, pages = page_table.shape
-        for t in (q_start, kv_len, page_table):
-            if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
-                raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
-        if q_start.numel() != B + 1 or kv_len.numel() != B:
+        import torch
+        i32 = torch.int32
+        if (q_start.dtype != i32 or kv_len.dtype != i32 or page_table.dtype != i32 or q_start.shape != (B + 1,)
+                or kv_len.shape != (B,) or not q_start.is_contiguous() or not kv_len.is_contiguous()
+                or not page_table.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
         self.q_start, self.kv_len, self.page_table, self.n_tokens = q_start, kv_len, page_table, n_tokens
         self._desc = exq_kv_batch(B, n_tokens or 0, max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(),
@@ -604,7 +609,8 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
 
 def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
     """Copies pages pairs int32 [n, 2] of (src, dst) on the GPU, in every layer."""
-    if pairs.element_size() != 4 or pairs.is_floating_point() or not pairs.is_contiguous() or pairs.numel() % 2:
+    import torch
+    if pairs.dtype != torch.int32 or not pairs.is_contiguous() or pairs.numel() % 2:
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_kv_copy_pages")
     _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2, _stream_ptr(stream)),
            "exq_kv_copy_pages")

@@ -90,12 +90,20 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnArgs& a, int pair) {
 }
 
 // A CTA's share of the tiles: [begin, end) of `total`, and where it starts.
+// The first `extra` CTAs have per + 1 tiles, the others per.
 struct AttnShare {
   long long total, begin, end;
   long long pair_start;  // tiles before the first pair, all heads
+  long long per;
+  int extra;
   int pair;
   int ctas;              // CTAs that have work
 };
+
+// quotients of non-negative numbers, by the short division where it does
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 
 // Every thread of the block (a multiple of 32) calls it; `scratch` is shared
 // memory of at least 34 long longs.
@@ -121,12 +129,15 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, long long* sc
   }
   AttnShare s;
   s.total = all * a.n_kv_heads;
-  s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (s.total + a.min_tiles - 1) / a.min_tiles));
-  s.begin = s.end = s.pair_start = 0;
-  s.pair = 0;
-  if (static_cast<int>(blockIdx.x) >= s.ctas) return s;
-  s.begin = s.total * blockIdx.x / s.ctas;
-  s.end = s.total * (blockIdx.x + 1) / s.ctas;
+  s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), quotient(s.total + a.min_tiles - 1, a.min_tiles)));
+  s.begin = s.end = s.pair_start = s.per = 0;
+  s.pair = s.extra = 0;
+  const int cta = blockIdx.x;
+  if (cta >= s.ctas) return s;
+  s.per = quotient(s.total, s.ctas);
+  s.extra = static_cast<int>(s.total - s.per * s.ctas);
+  s.begin = cta * s.per + min(cta, s.extra);
+  s.end = s.begin + s.per + (cta < s.extra ? 1 : 0);
   long long at = (before + inc - sum) * a.n_kv_heads;  // tiles before this thread's pairs
   if (at <= s.begin && s.begin < at + sum * a.n_kv_heads) {
     for (int p = p0; p < p1; ++p) {
@@ -145,9 +156,10 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, long long* sc
   return s;
 }
 
-// The CTA whose share holds tile x: share c is [total c / ctas, total (c + 1) / ctas).
+// The CTA whose share holds tile x.
 __device__ __forceinline__ int attn_cta_of(const AttnShare& s, long long x) {
-  return static_cast<int>(((x + 1) * s.ctas - 1) / s.total);
+  const long long longer = s.extra * (s.per + 1);  // tiles of the CTAs that have one more
+  return static_cast<int>(x < longer ? quotient(x, s.per + 1) : s.extra + quotient(x - longer, s.per));
 }
 
 // A CTA's piece of a unit, in order.
@@ -212,41 +224,72 @@ __device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, 0 f
   return y;
 }
 
-// Joins the pieces of a unit that CTAs c0 .. c1 share and writes its rows.
-// `threads` threads with ids `tid` call it, in the one CTA that came last.
+// Joins the pieces of a unit that CTAs c0 .. c1 share, in their order, and
+// writes its rows, in the one CTA that came last. `threads` threads with ids
+// `tid` call it. The loads of 8 pieces are in flight at a time, for two
+// places (a row, 4 columns) a thread.
 template <int ROWS, int D>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnPiece& p, int c0, int c1, int tid, int threads) {
   constexpr int kFloats = ROWS * (D + 2);
   constexpr int kCols = D / 4;
-  for (int e = tid; e < p.u.rows * kCols; e += threads) {
-    const int r = e / kCols, col = e - r * kCols;
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = attn_slot(a, c, c == c0, kFloats) + ROWS * D;
-      if (__ldcg(s + ROWS + r) > 0.f) m = fmaxf(m, __ldcg(s + r));
+  constexpr int kKeep = 2, kBatch = 8;
+  const int places = p.u.rows * kCols;
+  for (int e0 = tid; e0 < places; e0 += kKeep * threads) {
+    float4 y[kKeep];
+    float l[kKeep], m[kKeep];
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f), l[k] = 0.f, m[k] = -INFINITY;
+    for (int b0 = c0; b0 <= c1; b0 += kBatch) {
+      float4 v[kKeep][kBatch];
+      float mi[kKeep][kBatch], li[kKeep][kBatch];
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k) {
+        const int e = min(e0 + k * threads, places - 1), r = e / kCols, col = e - r * kCols;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = min(b0 + i, c1);
+          const float* s = attn_slot(a, c, c == c0, kFloats);
+          v[k][i] = __ldcg(reinterpret_cast<const float4*>(s + r * D) + col);
+          mi[k][i] = __ldcg(s + ROWS * D + r);
+          li[k][i] = b0 + i <= c1 ? __ldcg(s + ROWS * D + ROWS + r) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k) {
+        float top = m[k];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = li[k][i] > 0.f ? fmaxf(top, mi[k][i]) : top;
+        const float old = m[k] == -INFINITY ? 0.f : exp2_fast(m[k] - top);
+        l[k] *= old;
+        y[k].x *= old, y[k].y *= old, y[k].z *= old, y[k].w *= old;
+        m[k] = top;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float f = li[k][i] > 0.f ? exp2_fast(mi[k][i] - top) : 0.f;
+          l[k] += li[k][i] * f;
+          if (f > 0.f) {
+            y[k].x += v[k][i].x * f;
+            y[k].y += v[k][i].y * f;
+            y[k].z += v[k][i].z * f;
+            y[k].w += v[k][i].w * f;
+          }
+        }
+      }
     }
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* s = attn_slot(a, c, c == c0, kFloats);
-      const float li = __ldcg(s + ROWS * D + ROWS + r);
-      const float f = li > 0.f ? exp2_fast(__ldcg(s + ROWS * D + r) - m) : 0.f;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D) + col);
-      l += li * f;
-      y.x += v.x * f;
-      y.y += v.y * f;
-      y.z += v.z * f;
-      y.w += v.w * f;
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+      const int e = e0 + k * threads;
+      if (e >= places) break;
+      const int r = e / kCols, col = e - r * kCols;
+      int token, head;
+      attn_row_of(a, p, r, token, head);
+      const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
+      uint2 o;
+      o.x = float_to_half_bits(y[k].x * inv) | (float_to_half_bits(y[k].y * inv) << 16);
+      o.y = float_to_half_bits(y[k].z * inv) | (float_to_half_bits(y[k].w * inv) << 16);
+      *reinterpret_cast<uint2*>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * col) = o;
+      if (col == 0) attn_store_lse(a, token, head, m[k], l[k]);
     }
-    int token, head;
-    attn_row_of(a, p, r, token, head);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2 o;
-    o.x = float_to_half_bits(y.x * inv) | (float_to_half_bits(y.y * inv) << 16);
-    o.y = float_to_half_bits(y.z * inv) | (float_to_half_bits(y.w * inv) << 16);
-    *reinterpret_cast<uint2*>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * col) = o;
-    if (col == 0) attn_store_lse(a, token, head, m, l);
   }
 }
 

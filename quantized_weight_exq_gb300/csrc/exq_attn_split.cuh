@@ -22,8 +22,10 @@
 // permutes. The order of dims within a fragment follows the packing; Q is
 // loaded, and O stored, in that order.
 //
-// A CTA is 4 warps that each take 16 tokens of a 64-token tile, with softmax
-// statistics and sums of their own until the unit ends, and a producer warp
+// A CTA is two pairs of warps that take the 64-token tiles in turn, each warp
+// 32 tokens as two slices of 16 side by side (so that a wait and a vote serve
+// 32 tokens, and the slices' chains overlap), with softmax statistics and
+// sums of their own until the unit ends, and a producer warp
 // that fills a ring of stages by TMA: one box per page (or 64 tokens of it),
 // swizzled so that ldmatrix is free of bank conflicts, and the scales beside
 // it. Slots past the last token are masked in S, and V's (fp16) zeroed.
@@ -51,14 +53,28 @@ struct Cfg {
   static constexpr int kArray = kTile * kRowBytes;        // K or V of a stage
   static constexpr int kScale = B == 16 ? 0 : kTile * 2;  // scales of K or V
   static constexpr int kStage = ((2 * kArray + 2 * kScale + 1023) / 1024) * 1024;
-  static constexpr int kRegions = kRows * D <= 2048 ? kConsumers : 1;
-  static constexpr int kMerge = kRegions * kRows * D * 4 + 2 * kConsumers * kRows * 4;
-  static constexpr int kCtas = kStage > 40 * 1024 ? 1 : kStage > 20 * 1024 || D * NT > 128 ? 2 : D * NT > 64 ? 3 : 4;  // an SM: by stages, registers
-  static constexpr int kBudget = (224 * 1024) / kCtas - 1024 - kMerge - 1024;
-  static constexpr int kFit = kBudget / kStage;
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  // the warps' sums meet in `regions` copies (4: one barrier, 1: four)
+  static constexpr int merge_bytes(int regions) { return regions * kRows * D * 4 + 2 * kConsumers * kRows * 4; }
+  static constexpr int fit(int ctas, int regions) {
+    return ((224 * 1024) / ctas - 2048 - merge_bytes(regions)) / kStage;
+  }
+  // CTAs of an SM: as registers allow, fewer until each has 4 stages
+  static constexpr int kByRegs = D * NT > 128 ? 2 : D * NT > 64 ? 3 : 4;
+  static constexpr int kCtas = fit(kByRegs, 1) >= 4 ? kByRegs : kByRegs > 2 && fit(2, 1) >= 4 ? 2 : 1;
+  // Two pairs of warps take tiles in turn. The stages are even in number, so
+  // a stage always belongs to the same pair: a warp that met a stage only now
+  // and then could take the phase before last for the last. Where 4 stages do
+  // not fit (fp16, D = 256), all warps share every tile.
+  static constexpr bool kAlternate = fit(kCtas, 1) >= 4;
+  static constexpr int even(int n) { return n > 8 ? 8 : n & ~1; }
+  static constexpr int kWide = even(fit(kCtas, kConsumers));
+  static constexpr int kRegions = kAlternate && (kWide == even(fit(kCtas, 1)) || kWide >= 6) ? kConsumers : 1;
+  static constexpr int kStages = kAlternate ? even(fit(kCtas, kRegions)) : fit(kCtas, kRegions);
+  static constexpr int kMerge = merge_bytes(kRegions);
+  static constexpr int kSlices = kAlternate ? 2 : 1;  // of 16 tokens, of a warp in a tile
   static constexpr int kSmem = 1024 + kStages * kStage + ((kMerge + 15) / 16) * 16 + 512;
-  static_assert(kStages >= 2, "at least two stages");
+  static_assert(kStages >= 2 && (!kAlternate || kStages % 2 == 0), "stages");
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
   static constexpr int kFloats = kRows * (D + 2);
 };
 
@@ -166,6 +182,155 @@ __device__ __forceinline__ int dim_of(int mt, int half, int g) {
   return 16 * mt + 8 * half + g;
 }
 
+// S^T += K Q^T of 16 tokens from row `row0` of a stage, in two chains of sums
+template <int B, int D, int NT>
+__device__ __forceinline__ void scores(uint32_t kbase, int row0, int lane, const uint32_t (&bq)[NT][D / 16][2],
+                                       float (&s)[NT][4], float (&s2)[NT][4]) {
+  using C = Cfg<B, D, NT>;
+  const int g = lane >> 2, c = lane & 3;
+  const int tok_a = row0 + token_at<B>(g), tok_b = row0 + token_at<B>(g + 8);
+  if constexpr (B == 6) {
+    constexpr int kWin = D / 32;  // 48-bit windows of a lane's D / 4 codes
+    constexpr int kW = kWin * 3 / 2;
+    uint32_t wa[kW], wb[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      wa[i] = lds32(kbase + tok_a * C::kRowBytes + c * (kW * 4) + 4 * i);
+      wb[i] = lds32(kbase + tok_b * C::kRowBytes + c * (kW * 4) + 4 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < kWin; ++i) {
+      const int w = (i / 2) * 3 + (i & 1);
+      uint32_t pa[4], pb[4];
+      if (i & 1) {
+        unpack8<6>(fshr(wa[w], wa[w + 1], 16), wa[w + 1] >> 16, pa);
+        unpack8<6>(fshr(wb[w], wb[w + 1], 16), wb[w + 1] >> 16, pb);
+      } else {
+        unpack8<6>(wa[w], wa[w + 1], pa);
+        unpack8<6>(wb[w], wb[w + 1], pb);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][2 * i][0], bq[nt][2 * i][1]);
+        mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][2 * i + 1][0], bq[nt][2 * i + 1][1]);
+      }
+    }
+  } else {
+    constexpr int kChunks = C::kRowBytes / 16;
+    const int lrow = row0 + (lane & 15), lch = lane >> 4;
+#pragma unroll
+    for (int q = 0; q < kChunks; q += 2) {
+      uint32_t r[4];
+      ldsm4<false>(kbase + chunk_at<C>(lrow, q + lch), r);
+      if constexpr (B == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pa[4], pb[4];
+          unpack8<4>(r[2 * h], 0u, pa);
+          unpack8<4>(r[2 * h + 1], 0u, pb);
+          const int i = 2 * (q + h);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][i][0], bq[nt][i][1]);
+            mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][i + 1][0], bq[nt][i + 1][1]);
+          }
+        }
+      } else if constexpr (B == 8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
+          const uint32_t a0 = q8_pair(w0, 0x4140), a1 = q8_pair(w1, 0x4140), a2 = q8_pair(w0, 0x4342),
+                         a3 = q8_pair(w1, 0x4342);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(h ? s2[nt] : s[nt], a0, a1, a2, a3, bq[nt][q + h][0], bq[nt][q + h][1]);
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma((q & 2) ? s2[nt] : s[nt], r[0], r[1], r[2], r[3], bq[nt][q / 2][0], bq[nt][q / 2][1]);
+      }
+    }
+  }
+}
+
+// O^T += V^T P^T of the same; `first` is the first token's position, fp16 values from `end` on are taken as zeros
+template <int B, int D, int NT>
+__device__ __forceinline__ void values(uint32_t vbase, int row0, int first, int end, int lane, const uint32_t (&pb)[NT][2],
+                                       float (&o)[NT][D / 16][4]) {
+  using C = Cfg<B, D, NT>;
+  constexpr bool kQuant = B != 16;
+  const int g = lane >> 2, c = lane & 3;
+  if constexpr (B == 6) {
+    // tokens (c, 4 + c) and (8 + c, 12 + c) of the slice, D / 8 codes from dim g D / 8
+    constexpr int kWin = D / 64;
+    const int ta = row0 + c;
+#pragma unroll
+    for (int i = 0; i < kWin; ++i) {
+      uint32_t w[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int bit = g * (D / 8 * 6) + 48 * i;  // of the row
+        const uint32_t at = vbase + (ta + 4 * j) * C::kRowBytes + (bit >> 5) * 4;
+        const uint32_t x = lds32(at), y = lds32(at + 4);
+        w[j][0] = fshr(x, y, bit & 16);
+        w[j][1] = y >> (bit & 16);
+      }
+      uint32_t va[8], vb[8];
+      q6_two(w[0][0], w[0][1], w[1][0], w[1][1], va);
+      q6_two(w[2][0], w[2][1], w[3][0], w[3][1], vb);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma(o[nt][4 * i + j], va[2 * j], va[2 * j + 1], vb[2 * j], vb[2 * j + 1], pb[nt][0], pb[nt][1]);
+    }
+  } else {
+    constexpr int kChunks = C::kRowBytes / 16;
+    const int lrow = row0 + (lane & 15), lch = lane >> 4;
+    uint32_t zA = 0xFFFFFFFFu, zB = 0xFFFFFFFFu;  // V's tokens past the end, as zeros
+    bool ragged = false;
+    if constexpr (!kQuant) {
+      ragged = first + 16 > end;
+      const int x = first + 2 * c, y = x + 8;
+      zA = (x < end ? 0xFFFFu : 0u) | (x + 1 < end ? 0xFFFF0000u : 0u);
+      zB = (y < end ? 0xFFFFu : 0u) | (y + 1 < end ? 0xFFFF0000u : 0u);
+    }
+#pragma unroll
+    for (int q = 0; q < kChunks; q += 2) {
+      uint32_t r[4];
+      ldsm4<true>(vbase + chunk_at<C>(lrow, q + lch), r);
+      if constexpr (B == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // the unpacker's pairs are here (token a, token b) of dims 4g .. 4g + 3
+          uint32_t va[4], vb[4];
+          unpack8<4>(r[2 * h], 0u, va);
+          unpack8<4>(r[2 * h + 1], 0u, vb);
+          const int i = 2 * (q + h);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(o[nt][i], va[0], va[1], vb[0], vb[1], pb[nt][0], pb[nt][1]);
+            mma(o[nt][i + 1], va[2], va[3], vb[2], vb[3], pb[nt][0], pb[nt][1]);
+          }
+        }
+      } else if constexpr (B == 8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
+          const uint32_t a0 = q8_pair(w0, 0x4240), a1 = q8_pair(w0, 0x4341), a2 = q8_pair(w1, 0x4240),
+                         a3 = q8_pair(w1, 0x4341);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(o[nt][q + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        }
+      } else {
+        if (ragged) r[0] &= zA, r[2] &= zA, r[1] &= zB, r[3] &= zB;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma(o[nt][q / 2], r[0], r[2], r[1], r[3], pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+}
+
 template <int B, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     attn_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
@@ -188,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), kConsumers);
+      mbar_init(smem_u32(&empty[s]), C::kAlternate ? kConsumers / 2 : kConsumers);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -270,9 +435,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const int row0 = warp * 16;                        // the warp's tokens in a tile
-  const int tokA = row0 + token_at<B>(g), tokB = row0 + token_at<B>(g + 8);
-  int st = 0;
+  constexpr int kSlices = C::kSlices;
+  const int row0 = C::kAlternate ? (warp & 1) * 32 : warp * 16;  // the warp's tokens in a tile
+  const int turn = warp >> 1;                                    // its pair's tiles: even or odd ones of the CTA's
+  int st = 0, tile = 0;
   uint32_t ph = 0;
   while (attn_next<C::kRows, kTile>(a, walk, p)) {
     // Q as B fragments: column g of tile nt is row 8 nt + g
@@ -336,108 +502,68 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     bool begun = false;   // every row of the lane has a reference
     bool started = false; // kexp is set
 
-    for (int t = p.t0; t < p.t1; ++t) {
+    for (int t = p.t0; t < p.t1; ++t, ++tile) {
+      const int here = st;
+      const uint32_t parity = ph;
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+      if (C::kAlternate && (tile & 1) != turn) continue;
       // a wait that gave up leaves the unit as it is, but no barrier below:
       // all warps go through the same ones, whichever of them saw the flag
-      if (!mbar_wait_warp(smem_u32(&full[st]), ph, abort_flag, a)) break;
-      const uint32_t kbase = smem_u32(smem + st * C::kStage), vbase = kbase + C::kArray, sbase = vbase + C::kArray;
+      if (!mbar_wait_warp(smem_u32(&full[here]), parity, abort_flag, a)) break;
+      const uint32_t kbase = smem_u32(smem + here * C::kStage), vbase = kbase + C::kArray, sbase = vbase + C::kArray;
       const int first = t * kTile + row0;
-      const int tA = t * kTile + tokA, tB = t * kTile + tokB;
-      if (first < p.u.end && first + 16 > p.u.begin) {  // some token of the slice is seen
+      if (first < p.u.end && first + 16 * kSlices > p.u.begin) {  // some token of the slices is seen
         // ---------------------------------------------------------- S^T = K Q^T
-        float s[NT][4], s2[NT][4];
+        float s[kSlices][NT][4];
+        {
+          float s2[kSlices][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int h = 0; h < kSlices; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
-        if constexpr (B == 6) {
-          constexpr int kWin = D / 32;  // 48-bit windows of a lane's D / 4 codes
-          constexpr int kW = kWin * 3 / 2;
-          uint32_t wa[kW], wb[kW];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < kW; ++i) {
-            wa[i] = lds32(kbase + tokA * C::kRowBytes + c * (kW * 4) + 4 * i);
-            wb[i] = lds32(kbase + tokB * C::kRowBytes + c * (kW * 4) + 4 * i);
-          }
+              for (int i = 0; i < 4; ++i) s[h][nt][i] = s2[h][nt][i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < kWin; ++i) {
-            const int w = (i / 2) * 3 + (i & 1);
-            uint32_t pa[4], pb[4];
-            if (i & 1) {
-              unpack8<6>(fshr(wa[w], wa[w + 1], 16), wa[w + 1] >> 16, pa);
-              unpack8<6>(fshr(wb[w], wb[w + 1], 16), wb[w + 1] >> 16, pb);
-            } else {
-              unpack8<6>(wa[w], wa[w + 1], pa);
-              unpack8<6>(wb[w], wb[w + 1], pb);
-            }
+          for (int h = 0; h < kSlices; ++h) scores<B, D, NT>(kbase, row0 + 16 * h, lane, bq, s[h], s2[h]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][2 * i][0], bq[nt][2 * i][1]);
-              mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][2 * i + 1][0], bq[nt][2 * i + 1][1]);
-            }
-          }
-        } else {
-          constexpr int kChunks = C::kRowBytes / 16;
-          const int lrow = row0 + (lane & 15), lch = lane >> 4;
+          for (int h = 0; h < kSlices; ++h)
 #pragma unroll
-          for (int q = 0; q < kChunks; q += 2) {
-            uint32_t r[4];
-            ldsm4<false>(kbase + chunk_at<C>(lrow, q + lch), r);
-            if constexpr (B == 4) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t pa[4], pb[4];
-                unpack8<4>(r[2 * h], 0u, pa);
-                unpack8<4>(r[2 * h + 1], 0u, pb);
-                const int i = 2 * (q + h);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma(s[nt], pa[0], pb[0], pa[1], pb[1], bq[nt][i][0], bq[nt][i][1]);
-                  mma(s2[nt], pa[2], pb[2], pa[3], pb[3], bq[nt][i + 1][0], bq[nt][i + 1][1]);
-                }
-              }
-            } else if constexpr (B == 8) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
-                const uint32_t a0 = q8_pair(w0, 0x4140), a1 = q8_pair(w1, 0x4140), a2 = q8_pair(w0, 0x4342),
-                               a3 = q8_pair(w1, 0x4342);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(h ? s2[nt] : s[nt], a0, a1, a2, a3, bq[nt][q + h][0], bq[nt][q + h][1]);
-              }
-            } else {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma((q & 2) ? s2[nt] : s[nt], r[0], r[1], r[2], r[3], bq[nt][q / 2][0], bq[nt][q / 2][1]);
-            }
-          }
+              for (int i = 0; i < 4; ++i) s[h][nt][i] += s2[h][nt][i];
         }
         // ---------------------------------------------------------- softmax
-        const bool all_see = first >= all_lo && first + 16 <= all_hi;
-        float ksA = a.scale_log2, ksB = a.scale_log2, vsA = 1.f, vsB = 1.f;
+        const bool all_see = first >= all_lo && first + 16 * kSlices <= all_hi;
+        float vs[kSlices][2];
         uint32_t vtop = 0;
-        if constexpr (kQuant) {
-          ksA *= half_bits_to_float(lds16(sbase + 2 * tokA));
-          ksB *= half_bits_to_float(lds16(sbase + 2 * tokB));
-          uint32_t va = lds16(sbase + C::kScale + 2 * tokA), vb = lds16(sbase + C::kScale + 2 * tokB);
-          if (first + 16 > p.u.end) {  // whatever the slots past the end hold
-            if (tA >= p.u.end) va = 0;
-            if (tB >= p.u.end) vb = 0;
-          }
-          vtop = max(va, vb);
-          vsA = half_bits_to_float(va);
-          vsB = half_bits_to_float(vb);
-        }
+        float top = -INFINITY;
         // exponents: scores less the rows' references, and the lane's largest
-        float x[NT][4], top = -INFINITY;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < kSlices; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[nt][i] = fmaf(s[nt][i] + s2[nt][i], i < 2 ? ksA : ksB, nbase[nt][i & 1]);
-            const int tt = i < 2 ? tA : tB;
-            if (!all_see && (tt < lo[nt][i & 1] || tt >= hi[nt][i & 1])) x[nt][i] = -INFINITY;
-            top = fmaxf(top, x[nt][i]);
+          for (int e = 0; e < 2; ++e) {  // the lane's two tokens of a slice
+            const int tok = row0 + 16 * h + token_at<B>(g + 8 * e), at = t * kTile + tok;
+            float ks = a.scale_log2;
+            vs[h][e] = 1.f;
+            if constexpr (kQuant) {
+              ks *= half_bits_to_float(lds16(sbase + 2 * tok));
+              uint32_t v = lds16(sbase + C::kScale + 2 * tok);
+              if (at >= p.u.end) v = 0;  // whatever the slots past the end hold
+              vtop = max(vtop, v);
+              vs[h][e] = half_bits_to_float(v);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float x = fmaf(s[h][nt][2 * e + i], ks, nbase[nt][i]);
+                if (!all_see && (at < lo[nt][i] || at >= hi[nt][i])) x = -INFINITY;
+                s[h][nt][2 * e + i] = x;
+                top = fmaxf(top, x);
+              }
           }
         // A row's reference is raised only where a score exceeds it by more
         // than 8 (weights up to 2^8 have the same relative precision in fp16),
@@ -458,7 +584,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float mx = fmaxf(x[nt][i], x[nt][i + 2]);
+              float mx = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < kSlices; ++h) mx = fmaxf(mx, fmaxf(s[h][nt][i], s[h][nt][i + 2]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               mx -= nbase[nt][i];  // the largest score
@@ -466,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
               const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
               const float d = nb1 - nbase[nt][i];
               f[i] = m[nt][i] == -INFINITY ? 1.f : exp2_fast(d);  // -inf: o and l are zeros
-              x[nt][i] += d;
-              x[nt][i + 2] += d;
+#pragma unroll
+              for (int h = 0; h < kSlices; ++h) s[h][nt][i] += d, s[h][nt][i + 2] += d;
               m[nt][i] = m1;
               nbase[nt][i] = nb1;
               begun &= m1 != -INFINITY;
@@ -480,93 +608,26 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             }
           }
         }
-        uint32_t pb0[NT], pb1[NT];
+        uint32_t pb[kSlices][NT][2];  // weights times V's scales, as B fragments
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float w0 = exp2_fast(x[nt][0]), w1 = exp2_fast(x[nt][1]), w2 = exp2_fast(x[nt][2]), w3 = exp2_fast(x[nt][3]);
-          l[nt][0] += w0 + w2;
-          l[nt][1] += w1 + w3;
-          const __half2 h0 = __floats2half2_rn(w0 * vsA, w1 * vsA), h1 = __floats2half2_rn(w2 * vsB, w3 * vsB);
-          pb0[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&h0));
-          pb1[nt] = transpose8(*reinterpret_cast<const uint32_t*>(&h1));
-        }
+        for (int h = 0; h < kSlices; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float w0 = exp2_fast(s[h][nt][2 * e]), w1 = exp2_fast(s[h][nt][2 * e + 1]);
+              l[nt][0] += w0;
+              l[nt][1] += w1;
+              const __half2 w = __floats2half2_rn(w0 * vs[h][e], w1 * vs[h][e]);
+              pb[h][nt][e] = transpose8(*reinterpret_cast<const uint32_t*>(&w));
+            }
         // ---------------------------------------------------------- O^T += V^T P^T
-        if constexpr (B == 6) {
-          // tokens (c, 4 + c) and (8 + c, 12 + c) of the slice, D / 8 codes from dim g D / 8
-          constexpr int kWin = D / 64;
-          const int ta = row0 + c;
 #pragma unroll
-          for (int i = 0; i < kWin; ++i) {
-            uint32_t w[4][2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int bit = g * (D / 8 * 6) + 48 * i;  // of the row
-              const uint32_t at = vbase + (ta + 4 * j) * C::kRowBytes + (bit >> 5) * 4;
-              const uint32_t x = lds32(at), y = lds32(at + 4);
-              w[j][0] = fshr(x, y, bit & 16);
-              w[j][1] = y >> (bit & 16);
-            }
-            uint32_t va[8], vb[8];
-            q6_two(w[0][0], w[0][1], w[1][0], w[1][1], va);
-            q6_two(w[2][0], w[2][1], w[3][0], w[3][1], vb);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma(o[nt][4 * i + j], va[2 * j], va[2 * j + 1], vb[2 * j], vb[2 * j + 1], pb0[nt], pb1[nt]);
-          }
-        } else {
-          constexpr int kChunks = C::kRowBytes / 16;
-          const int lrow = row0 + (lane & 15), lch = lane >> 4;
-          uint32_t zA = 0xFFFFFFFFu, zB = 0xFFFFFFFFu;  // V's tokens past the end, as zeros
-          bool ragged = false;
-          if constexpr (!kQuant) {
-            ragged = first + 16 > p.u.end;
-            const int x = first + 2 * c, y = x + 8;
-            zA = (x < p.u.end ? 0xFFFFu : 0u) | (x + 1 < p.u.end ? 0xFFFF0000u : 0u);
-            zB = (y < p.u.end ? 0xFFFFu : 0u) | (y + 1 < p.u.end ? 0xFFFF0000u : 0u);
-          }
-#pragma unroll
-          for (int q = 0; q < kChunks; q += 2) {
-            uint32_t r[4];
-            ldsm4<true>(vbase + chunk_at<C>(lrow, q + lch), r);
-            if constexpr (B == 4) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                // the unpacker's pairs are here (token a, token b) of dims 4g .. 4g + 3
-                uint32_t va[4], vb[4];
-                unpack8<4>(r[2 * h], 0u, va);
-                unpack8<4>(r[2 * h + 1], 0u, vb);
-                const int i = 2 * (q + h);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mma(o[nt][i], va[0], va[1], vb[0], vb[1], pb0[nt], pb1[nt]);
-                  mma(o[nt][i + 1], va[2], va[3], vb[2], vb[3], pb0[nt], pb1[nt]);
-                }
-              }
-            } else if constexpr (B == 8) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t w0 = r[2 * h], w1 = r[2 * h + 1];
-                const uint32_t a0 = q8_pair(w0, 0x4240), a1 = q8_pair(w0, 0x4341), a2 = q8_pair(w1, 0x4240),
-                               a3 = q8_pair(w1, 0x4341);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma(o[nt][q + h], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-              }
-            } else {
-              if (ragged) r[0] &= zA, r[2] &= zA, r[1] &= zB, r[3] &= zB;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma(o[nt][q / 2], r[0], r[2], r[1], r[3], pb0[nt], pb1[nt]);
-            }
-          }
-        }
+        for (int h = 0; h < kSlices; ++h)
+          values<B, D, NT>(vbase, row0 + 16 * h, t * kTile + row0 + 16 * h, p.u.end, lane, pb[h], o);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
-      if (++st == C::kStages) {
-        st = 0;
-        ph ^= 1;
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&empty[here]));
     }
 
     // -------------------------------------------------------------- the warps' results to one

@@ -4,12 +4,14 @@
 // Work is cut into units: a block of query rows of one sequence and KV head
 // (row r of a sequence and KV head is new token r / group, query head
 // r % group of it, so the rows of one token lie together), over the tiles of
-// cached tokens that some row of the block sees. The tiles of all units, one
-// unit after the other, are divided evenly over the CTAs, whatever the
-// sequences' lengths: a CTA may end a unit that another began, do several
-// whole units, and begin another. Lengths are read on the device. A unit that
-// several CTAs share is joined by the last of them to finish, in the CTAs'
-// order, so the result does not depend on which one that is.
+// cached tokens that some row of the block sees. What a unit costs beside its
+// tiles (loading its queries, bringing its sums together) counts as
+// `unit_cost` tiles before its first. All units, one after the other, are
+// divided evenly over the CTAs, whatever the sequences' lengths: a CTA may end
+// a unit that another began, do several whole units, and begin another.
+// Lengths are read on the device. A unit that several CTAs share is joined by
+// the last of them to finish, in the CTAs' order, so the result does not
+// depend on which one that is.
 #pragma once
 
 #include <cuda.h>
@@ -38,6 +40,7 @@ struct AttnArgs {
   int causal, window;
   float* lse;
   int row_blocks;             // blocks of rows a sequence may need (host bound)
+  int unit_cost;              // what a unit costs beside its tiles, in tiles
   int min_tiles;              // fewest tiles worth a CTA
   unsigned* counters;         // [CTAs], zero between calls
   float* partial;             // [CTAs][2][rows * (D + 2)]
@@ -89,11 +92,16 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnArgs& a, int pair) {
   return u;
 }
 
-// A CTA's share of the tiles: [begin, end) of `total`, and where it starts.
-// The first `extra` CTAs have per + 1 tiles, the others per.
+// Places of a unit in the division.
+__device__ __forceinline__ long long attn_places(const AttnArgs& a, const AttnUnit& u) {
+  return u.tiles > 0 ? u.tiles + a.unit_cost : 0;
+}
+
+// A CTA's share of the places: [begin, end) of `total`, and where it starts.
+// The first `extra` CTAs have per + 1 places, the others per.
 struct AttnShare {
   long long total, begin, end;
-  long long pair_start;  // tiles before the first pair, all heads
+  long long pair_start;  // places before the first pair, all heads
   long long per;
   int extra;
   int pair;
@@ -105,30 +113,23 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
-// Every thread of the block (a multiple of 32) calls it; `scratch` is shared
-// memory of at least 34 long longs.
+// Every warp works it out for itself, each lane for its part of the pairs:
+// no shared memory, no barrier.
 template <int ROWS, int TILE>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, long long* scratch) {
-  const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& a) {
+  const int lane = threadIdx.x & 31;
   const int pairs = a.n_seqs * a.row_blocks;
-  const int per = (pairs + nt - 1) / nt, p0 = min(tid * per, pairs), p1 = min(p0 + per, pairs);
+  const int per = (pairs + 31) >> 5, p0 = min(lane * per, pairs), p1 = min(p0 + per, pairs);
   long long sum = 0;
-  for (int p = p0; p < p1; ++p) sum += attn_unit<ROWS, TILE>(a, p).tiles;
+  for (int p = p0; p < p1; ++p) sum += attn_places(a, attn_unit<ROWS, TILE>(a, p));
   long long inc = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += v;
   }
-  if (lane == 31) scratch[warp] = inc;
-  __syncthreads();
-  long long before = 0, all = 0;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    all += scratch[w];
-  }
   AttnShare s;
-  s.total = all * a.n_kv_heads;
+  s.total = __shfl_sync(0xffffffffu, inc, 31) * a.n_kv_heads;
   s.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), quotient(s.total + a.min_tiles - 1, a.min_tiles)));
   s.begin = s.end = s.pair_start = s.per = 0;
   s.pair = s.extra = 0;
@@ -138,27 +139,24 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a, long long* sc
   s.extra = static_cast<int>(s.total - s.per * s.ctas);
   s.begin = cta * s.per + min(cta, s.extra);
   s.end = s.begin + s.per + (cta < s.extra ? 1 : 0);
-  long long at = (before + inc - sum) * a.n_kv_heads;  // tiles before this thread's pairs
-  if (at <= s.begin && s.begin < at + sum * a.n_kv_heads) {
-    for (int p = p0; p < p1; ++p) {
-      const long long tiles = static_cast<long long>(attn_unit<ROWS, TILE>(a, p).tiles) * a.n_kv_heads;
-      if (s.begin < at + tiles) {
-        scratch[32] = at;
-        scratch[33] = p;
-        break;
-      }
+  long long at = (inc - sum) * a.n_kv_heads;  // places before this lane's pairs
+  const bool mine = at <= s.begin && s.begin < at + sum * a.n_kv_heads;
+  int pair = p0;
+  if (mine && per > 1)
+    for (; pair < p1 - 1; ++pair) {
+      const long long tiles = attn_places(a, attn_unit<ROWS, TILE>(a, pair)) * a.n_kv_heads;
+      if (s.begin < at + tiles) break;
       at += tiles;
     }
-  }
-  __syncthreads();
-  s.pair_start = scratch[32];
-  s.pair = static_cast<int>(scratch[33]);
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;  // one lane
+  s.pair_start = __shfl_sync(0xffffffffu, at, from);
+  s.pair = __shfl_sync(0xffffffffu, pair, from);
   return s;
 }
 
-// The CTA whose share holds tile x.
+// The CTA whose share holds place x.
 __device__ __forceinline__ int attn_cta_of(const AttnShare& s, long long x) {
-  const long long longer = s.extra * (s.per + 1);  // tiles of the CTAs that have one more
+  const long long longer = s.extra * (s.per + 1);  // places of the CTAs that have one more
   return static_cast<int>(x < longer ? quotient(x, s.per + 1) : s.extra + quotient(x - longer, s.per));
 }
 
@@ -167,34 +165,70 @@ struct AttnPiece {
   AttnUnit u;
   int head;            // KV head
   int t0, t1;          // tiles of the piece, counted from cached token 0
-  long long first;     // the unit's first tile in the division
+  long long first;     // the place of the unit's first tile
   bool whole;
 };
 
-struct AttnWalk {
+// A warp's place in its CTA's share and the piece it is at. It lies in shared
+// memory, one for each warp (all of a CTA's warps go through the same pieces):
+// in registers it would be carried, and spilled, through the loops over tiles.
+struct AttnState {
   AttnShare s;
-  long long at;        // next tile of the share
+  long long at;          // next place of the share
   long long pair_start;
   int pair;
+  AttnPiece p;
 };
 
 template <int ROWS, int TILE>
-__device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnWalk& w, AttnPiece& p) {
-  if (w.at >= w.s.end) return false;
-  p.u = attn_unit<ROWS, TILE>(a, w.pair);
-  while (w.at >= w.pair_start + static_cast<long long>(p.u.tiles) * a.n_kv_heads) {  // pairs without rows are passed
-    w.pair_start += static_cast<long long>(p.u.tiles) * a.n_kv_heads;
-    p.u = attn_unit<ROWS, TILE>(a, ++w.pair);
+__device__ __forceinline__ bool attn_begin(const AttnArgs& a, AttnState& st) {
+  const AttnShare s = attn_share<ROWS, TILE>(a);
+  if ((threadIdx.x & 31) == 0) {
+    st.s = s;
+    st.at = s.begin;
+    st.pair = s.pair;
+    st.pair_start = s.pair_start;
   }
-  const int off = static_cast<int>(w.at - w.pair_start);
-  p.head = off / p.u.tiles;
-  const int o = off - p.head * p.u.tiles;
-  p.first = w.at - o;
-  const int n = static_cast<int>(min(w.s.end - w.at, static_cast<long long>(p.u.tiles - o)));
-  p.t0 = p.u.tile0 + o;
-  p.t1 = p.t0 + n;
-  p.whole = n == p.u.tiles;
-  w.at += n;
+  __syncwarp();
+  return s.begin < s.end;
+}
+
+// The next piece, to st.p; false when there is none. Called by whole warps.
+template <int ROWS, int TILE>
+__device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnState& st) {
+  long long at = st.at, pair_start = st.pair_start;
+  const long long end = st.s.end;
+  int pair = st.pair;
+  AttnPiece p;
+  for (;;) {
+    if (at >= end) return false;  // the same for all lanes
+    p.u = attn_unit<ROWS, TILE>(a, pair);
+    int places = static_cast<int>(attn_places(a, p.u));
+    while (at >= pair_start + static_cast<long long>(places) * a.n_kv_heads) {  // pairs that are done or have no rows
+      pair_start += static_cast<long long>(places) * a.n_kv_heads;
+      p.u = attn_unit<ROWS, TILE>(a, ++pair);
+      places = static_cast<int>(attn_places(a, p.u));
+    }
+    const int off = static_cast<int>(at - pair_start);
+    p.head = off / places;
+    const int o = off - p.head * places;  // the share's first place in the unit
+    const int n = static_cast<int>(min(end - at, static_cast<long long>(places - o)));
+    const int from = max(o - a.unit_cost, 0), to = max(o + n - a.unit_cost, 0);
+    p.first = at - o + a.unit_cost;
+    p.t0 = p.u.tile0 + from;
+    p.t1 = p.u.tile0 + to;
+    p.whole = to - from == p.u.tiles;
+    at += n;
+    if (to > from) break;  // else only the unit's cost fell to this CTA
+  }
+  __syncwarp();  // every lane has read the state
+  if ((threadIdx.x & 31) == 0) {
+    st.at = at;
+    st.pair = pair;
+    st.pair_start = pair_start;
+    st.p = p;
+  }
+  __syncwarp();
   return true;
 }
 

@@ -53,7 +53,7 @@ constexpr int kTile = split::kTile;
 // Registers a thread: the block is launched with kLaunchRegs and hands those
 // of the MMA's group to the softmax. The shares may not add up to more than
 // the launch's, or an increase would never be granted.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kDequantRegs = 112, kIssueRegs = 64;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kDequantRegs = 112, kIssueRegs = 96;
 static_assert(2 * kSoftmaxRegs + kDequantRegs + kIssueRegs <= 4 * kLaunchRegs, "register shares");
 
 template <int N>
@@ -79,12 +79,14 @@ struct Cfg {
   static constexpr int kOffPacked = kOffQ + kRows * D * 2;
   // a packed stage is one tile of K or of V with its scales
   static constexpr int kPacked = B == 16 ? 0 : (Packed::kArray + Packed::kScale + 1023) / 1024 * 1024;
-  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 - 512;
+  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 -
+                               kThreads / 32 * static_cast<int>(sizeof(AttnState)) - 512;
   static constexpr int kPackedFit = B == 16 ? 0 : kRoom / kPacked;
   static constexpr int kPackedStages = kPackedFit > 8 ? 8 : kPackedFit;
   static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32
   static constexpr int kOffExps = kOffScale + 4 * 2 * kTile * 4;          // [4][2]: V's exponents
-  static constexpr int kOffBar = kOffExps + 64;
+  static constexpr int kOffState = kOffExps + 64;                  // a warp's place each
+  static constexpr int kOffBar = kOffState + kThreads / 32 * static_cast<int>(sizeof(AttnState));
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static constexpr int kFloats = kRows * (D + 2);
   static_assert(B == 16 || kPackedStages >= 1, "a packed stage");
@@ -140,8 +142,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// the same value in every lane, known as such to the compiler
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+using split::uniform;
+// Copies that the lane of a box issues on its own. Issued by the whole warp
+// (as in the packed-code kernel) this kernel took 20 % longer on quantised
+// pages: the copies have time here, and the warp's issue slots have not.
+__device__ __forceinline__ void lane_tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void lane_bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -358,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 40);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* is_last = reinterpret_cast<int*>(tmem_slot + 2);
-  long long* scratch = reinterpret_cast<long long*>(smem);  // before the first tile
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -378,9 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  AttnWalk walk;
-  walk.s = attn_share<C::kRows, T>(a, scratch);
-  if (walk.s.begin >= walk.s.end) return;  // the whole CTA
+  AttnState& state = reinterpret_cast<AttnState*>(smem + C::kOffState)[warp];
+  if (!attn_begin<C::kRows, T>(a, state)) return;  // the whole CTA
   if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
@@ -390,10 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_slot;
-  walk.at = walk.s.begin;
-  walk.pair = walk.s.pair;
-  walk.pair_start = walk.s.pair_start;
-  AttnPiece p;
+  const AttnPiece& p = state.p;
 
   if (warp >= kScoreWarp) {
     fewer_regs<kIssueRegs>();
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<kNS> r;
       uint32_t g = 0, q_ph = 0;
       bool ok = true;
-      while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+      while (ok && attn_next<C::kRows, T>(a, state)) {
         const int n = uniform(p.t1 - p.t0), ns = uniform(p.u.rows) > 128 ? C::kStreams : 1;
         ok = mbar_wait_warp(q_full, q_ph, abort_flag, a);
         q_ph ^= 1;
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<kNS> r;
       uint32_t g = 0, w_ph = 0;
       bool ok = true;
-      while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+      while (ok && attn_next<C::kRows, T>(a, state)) {
         const int n = uniform(p.t1 - p.t0);
         const bool active = uniform(p.u.rows) > 128 * s;
         for (int j = 0; j < n && ok; ++j, ++g, r.next()) {
@@ -466,12 +477,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;          // tiles
       long long issued = 0;    // stages filled
       bool ok = true;
-      while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+      while (ok && attn_next<C::kRows, T>(a, state)) {
         const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
-        const int b0 = p.t0 * boxes, b1 = p.t1 * boxes;
+        const int t0 = p.t0, t1 = p.t1, head = p.head, end = p.u.end;
+        const int b0 = t0 * boxes, b1 = t1 * boxes;
         const auto page_of = [&](int bx) {  // -1: nothing to copy
           const int tok = bx * box;
-          if (bx >= b1 || tok >= p.u.end) return -1;
+          if (bx >= b1 || tok >= end) return -1;
           const int page = __ldg(table + tok / a.page_size);
           if (page < 0 || page >= a.n_pages) {
             atomicOr(a.err, kDevErrBadPage);
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return page;
         };
         int have = b0, page = page_of(b0 + lane), next = page_of(b0 + 32 + lane);
-        for (int t = p.t0; t < p.t1; ++t, ++g) {
+        for (int t = t0; t < t1; ++t, ++g) {
           if (t * boxes >= have + 32) {
             have += 32;
             page = next;
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int mine = __shfl_sync(0xffffffffu, page, (t * boxes - have + (lane & (boxes - 1))) & 31);
           const bool copy = lane < boxes && mine >= 0;
           const unsigned n = __popc(__ballot_sync(0xffffffffu, copy));
-          const int slot = (t * T + lane * box) & (a.page_size - 1), block = mine * a.n_kv_heads + p.head;
+          const int slot = (t * T + lane * box) & (a.page_size - 1), block = mine * a.n_kv_heads + head;
           if constexpr (kQuant) {
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
@@ -501,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (copy) {
 #pragma unroll
                 for (int i = 0; i < P::kParts; ++i)
-                  split::tma_load_3d(base + i * (T * P::kPartBytes) + lane * box * P::kPartBytes, which ? &maps.v : &maps.k,
+                  lane_tma_load_3d(base + i * (T * P::kPartBytes) + lane * box * P::kPartBytes, which ? &maps.v : &maps.k,
                                      i * (P::kPartBytes / 4), slot, block, full);
-                split::bulk_load(base + P::kArray + lane * box * 2,
+                lane_bulk_load(base + P::kArray + lane * box * 2,
                                  a.scales[which] + static_cast<long long>(block) * a.page_size + slot, box * 2, full);
               }
               pr.next();
@@ -520,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t at = sbase + r.st * C::kArray + lane * box * 128;
 #pragma unroll
               for (int i = 0; i < C::kSlabs; ++i) {
-                split::tma_load_3d(at + C::kOffK + i * (T * 128), &maps.k, i * 32, slot, block, full);
-                split::tma_load_3d(at + C::kOffV + i * (T * 128), &maps.v, i * 32, slot, block, full);
+                lane_tma_load_3d(at + C::kOffK + i * (T * 128), &maps.k, i * 32, slot, block, full);
+                lane_tma_load_3d(at + C::kOffV + i * (T * 128), &maps.v, i * 32, slot, block, full);
               }
             }
             r.next();
@@ -545,12 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kNS> r;
     uint32_t g = 0;  // tiles
     bool ok = true;
-    while (ok && attn_next<C::kRows, T>(a, walk, p)) {
+    while (ok && attn_next<C::kRows, T>(a, state)) {
       // ---- Q: [M tile][slab][128 rows][128 bytes]; rows past the unit are
       // zeros. The last S of the unit before has been computed.
       if (g > 0) ok = mbar_wait_warp(s_full(g - 1), phase4(g - 1), abort_flag, a);
       if (!ok) break;
-      const int q_rows = p.u.rows > 128 ? C::kRows : 128;
+      const int rows = p.u.rows, q_rows = rows > 128 ? C::kRows : 128;
       // consecutive threads hold 8 rows of one chunk (their stores fall on different banks); 8 loads at a time
       for (int i0 = tid; i0 < q_rows * (D / 8); i0 += 8 * kDequantThreads) {
         uint4 v[8];
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 8; ++j) {
           const int i = i0 + j * kDequantThreads, row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
           v[j] = make_uint4(0, 0, 0, 0);
-          if (row < p.u.rows) {
+          if (row < rows) {
             int token, head;
             attn_row_of(a, p, row, token, head);
             v[j] = __ldg(reinterpret_cast<const uint4*>(a.q.data + token * a.q.token_stride + head * a.q.head_stride + 8 * ch));
@@ -576,8 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       async_fence();
       mbar_arrive(q_full);
 
-      for (int t = p.t0; t < p.t1 && ok; ++t, ++g) {
-        const int keep = p.u.end - t * T;  // tokens of the tile that exist
+      const int t1 = p.t1, end = p.u.end;
+      for (int t = p.t0; t < t1 && ok; ++t, ++g) {
+        const int keep = end - t * T;  // tokens of the tile that exist
         if constexpr (kQuant) {
           if (g >= kNS) ok = mbar_wait_warp(pv_done(g - kNS), phase4(g - kNS), abort_flag, a);
 #pragma unroll
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = tmem + lane_base + C::kTmemO + s * D;
     uint32_t g = 0;                                       // tiles
     bool ok = true;
-    while (attn_next<C::kRows, T>(a, walk, p)) {
+    while (attn_next<C::kRows, T>(a, state)) {
       const bool active = works && s * 128 < p.u.rows;    // warp-uniform, the same for the stream's warps
       float m[4], nbase[4];                               // references, and -(m - (15 - kexp)), see below
       uint64_t sum[4];                                    // of weights, even and odd columns
@@ -654,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
         all_hi = __reduce_min_sync(0xffffffffu, all_hi);
         bool begun = false;  // every row of the thread has a reference
-        for (int t = p.t0; t < p.t1 && ok; ++t, ++g) {
+        const int t0 = p.t0, t1 = p.t1;
+        for (int t = t0; t < t1 && ok; ++t, ++g) {
           ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
           if (!ok) break;
           tc_after();
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int2 e2 = *reinterpret_cast<const int2*>(exps + 2 * (g & 3));
             tile_e = max(e2.x, e2.y);
           }
-          const bool new_e = kQuant && (t == p.t0 || tile_e > kexp + 4);
+          const bool new_e = kQuant && (t == t0 || tile_e > kexp + 4);
           if (__any_sync(0xffffffffu, !begun || new_e || top > 8.f + static_cast<float>(15 - kexp))) {
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -738,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               begun &= m1 != -INFINITY;
               sum[k] = mul_f2(sum[k], pack_f2(f[k], f[k]));
             }
-            if (t > p.t0 && __any_sync(0xffffffffu, any)) {
+            if (t > t0 && __any_sync(0xffffffffu, any)) {
               // P V of the tile before has to be over before O is touched
               ok = mbar_wait_warp(pv_done(g - 1), phase4(g - 1), abort_flag, a);
               if (!ok) break;
@@ -781,7 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (works) {
         // stays in step with the tiles, so that no phase is missed
-        for (int t = p.t0; t < p.t1 && ok; ++t, ++g) ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
+        const int n = p.t1 - p.t0;
+        for (int t = 0; t < n && ok; ++t, ++g) ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
       }
       // the statistics of the thread's row `lane` of the warp: slot lane / 8 of
       // the lanes from 4 (lane % 8)
@@ -796,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((lane >> 3) == k) row_l = a1, row_base = b1;
       }
       // ---- epilogue: a thread holds its row's D values
-      const int c0 = p.whole ? 0 : attn_cta_of(walk.s, p.first), c1 = p.whole ? 0 : attn_cta_of(walk.s, p.first + p.u.tiles - 1);
+      const int c0 = p.whole ? 0 : attn_cta_of(state.s, p.first), c1 = p.whole ? 0 : attn_cta_of(state.s, p.first + p.u.tiles - 1);
       if (active && ok) {
         const bool has = row < p.u.rows;
         int token = 0, head = 0;

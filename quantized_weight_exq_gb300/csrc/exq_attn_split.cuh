@@ -56,7 +56,7 @@ struct Cfg {
   // the warps' sums meet in `regions` copies (4: one barrier, 1: four)
   static constexpr int merge_bytes(int regions) { return regions * kRows * D * 4 + 2 * kConsumers * kRows * 4; }
   static constexpr int fit(int ctas, int regions) {
-    return ((224 * 1024) / ctas - 2048 - merge_bytes(regions)) / kStage;
+    return ((227 * 1024) / ctas - 2048 - 256 - 5 * static_cast<int>(sizeof(AttnState)) - merge_bytes(regions)) / kStage;
   }
   // CTAs of an SM: as registers allow, fewer until each has 4 stages
   static constexpr int kByRegs = D * NT > 128 ? 2 : D * NT > 64 ? 3 : 4;
@@ -72,7 +72,7 @@ struct Cfg {
   static constexpr int kStages = kAlternate ? even(fit(kCtas, kRegions)) : fit(kCtas, kRegions);
   static constexpr int kMerge = merge_bytes(kRegions);
   static constexpr int kSlices = kAlternate ? 2 : 1;  // of 16 tokens, of a warp in a tile
-  static constexpr int kSmem = 1024 + kStages * kStage + ((kMerge + 15) / 16) * 16 + 512;
+  static constexpr int kSmem = 1024 + kStages * kStage + ((kMerge + 15) / 16) * 16 + 256 + 5 * sizeof(AttnState);
   static_assert(kStages >= 2 && (!kAlternate || kStages % 2 == 0), "stages");
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
   static constexpr int kFloats = kRows * (D + 2);
@@ -82,18 +82,34 @@ struct Maps {
   CUtensorMap k, v;
 };
 
+// Copies are issued by a whole warp with the same operands, one lane elected
+// in the instruction: the operands stay in uniform registers. Each issued by
+// some lane on its own took 200 cycles, and the producer was the bound.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+      : "memory");
 }
+
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+      : "memory");
+}
+
+// the same value in every lane, known as such to the compiler
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -347,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
   uint64_t* empty = full + C::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
   int* is_last = const_cast<int*>(abort_flag) + 1;
-  long long* scratch = reinterpret_cast<long long*>(merge);  // free until the first unit ends
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -358,14 +373,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  AttnWalk walk;
-  walk.s = attn_share<C::kRows, kTile>(a, scratch);  // its barriers cover the initialisation above
-  if (walk.s.begin >= walk.s.end) return;            // the whole CTA
-  __syncthreads();                                   // scratch has been read
-  walk.at = walk.s.begin;
-  walk.pair = walk.s.pair;
-  walk.pair_start = walk.s.pair_start;
-  AttnPiece p;
+  AttnState& state = reinterpret_cast<AttnState*>(tail + 256)[warp];
+  if (!attn_begin<C::kRows, kTile>(a, state)) return;  // the whole CTA
+  __syncthreads();                                      // the barriers are initialised
+  const AttnPiece& p = state.p;
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
@@ -376,12 +387,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     uint32_t ph = 0;
     long long issued = 0;
     bool ok = true;
-    while (ok && attn_next<C::kRows, kTile>(a, walk, p)) {
+    while (ok && attn_next<C::kRows, kTile>(a, state)) {
       const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
-      const int b0 = p.t0 * boxes, b1 = p.t1 * boxes;  // boxes of the piece
+      const int t0 = p.t0, t1 = p.t1, head = p.head, end = p.u.end;
+      const int b0 = t0 * boxes, b1 = t1 * boxes;      // boxes of the piece
       const auto page_of = [&](int bx) {               // -1: nothing to copy
         const int tok = bx * box;
-        if (bx >= b1 || tok >= p.u.end) return -1;
+        if (bx >= b1 || tok >= end) return -1;
         const int page = __ldg(table + tok / a.page_size);
         if (page < 0 || page >= a.n_pages) {
           atomicOr(a.err, kDevErrBadPage);
@@ -390,33 +402,33 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         return page;
       };
       int have = b0, page = page_of(b0 + lane), next = page_of(b0 + 32 + lane);
-      for (int t = p.t0; t < p.t1; ++t) {
+      for (int t = t0; t < t1; ++t) {
         if (t * boxes >= have + 32) {
           have += 32;
           page = next;
           next = page_of(have + 32 + lane);
         }
-        const int mine = __shfl_sync(0xffffffffu, page, (t * boxes - have + (lane & (boxes - 1))) & 31);
-        const bool copy = lane < boxes && mine >= 0;
-        const unsigned n = __popc(__ballot_sync(0xffffffffu, copy));
+        const int at = t * boxes - have;  // the tile's boxes are those of lanes at .. at + boxes - 1
+        const unsigned there = (__ballot_sync(0xffffffffu, page >= 0) >> at) & ((1u << boxes) - 1u);
         ok = mbar_wait_warp(smem_u32(&empty[st]), ph ^ 1, abort_flag, a);
         if (!ok) break;
-        const uint32_t bar = smem_u32(&full[st]);
-        const uint32_t base = smem_u32(smem + st * C::kStage);
-        if (lane == 0) mbar_expect_tx(bar, n * box * (2 * C::kRowBytes + (kQuant ? 4 : 0)));
-        __syncwarp();
-        if (copy) {
-          const int tok = t * kTile + lane * box, slot = tok & (a.page_size - 1), block = mine * a.n_kv_heads + p.head;
+        const uint32_t bar = uniform(smem_u32(&full[st])), base = uniform(smem_u32(smem + st * C::kStage));
+        expect_tx(bar, uniform(__popc(there) * box * (2 * C::kRowBytes + (kQuant ? 4 : 0))));
+        for (int i = 0; i < boxes; ++i) {
+          if (!((there >> i) & 1u)) continue;
+          const int block = __shfl_sync(0xffffffffu, page, at + i) * a.n_kv_heads + head;
+          const uint32_t slot = uniform((t * kTile + i * box) & (a.page_size - 1)), blk = uniform(block);
+          const uint32_t off = base + uniform(i * box) * C::kPartBytes;
 #pragma unroll
-          for (int i = 0; i < C::kParts; ++i) {
-            const uint32_t off = i * (kTile * C::kPartBytes) + lane * box * C::kPartBytes;
-            tma_load_3d(base + off, &maps.k, i * (C::kPartBytes / 4), slot, block, bar);
-            tma_load_3d(base + C::kArray + off, &maps.v, i * (C::kPartBytes / 4), slot, block, bar);
+          for (int k = 0; k < C::kParts; ++k) {
+            tma_load_3d(off + k * (kTile * C::kPartBytes), &maps.k, k * (C::kPartBytes / 4), slot, blk, bar);
+            tma_load_3d(off + C::kArray + k * (kTile * C::kPartBytes), &maps.v, k * (C::kPartBytes / 4), slot, blk, bar);
           }
           if constexpr (kQuant) {
-            const long long g = static_cast<long long>(block) * a.page_size + slot;
-            bulk_load(base + 2 * C::kArray + lane * box * 2, a.scales[0] + g, box * 2, bar);
-            bulk_load(base + 2 * C::kArray + C::kScale + lane * box * 2, a.scales[1] + g, box * 2, bar);
+            const long long grp = static_cast<long long>(blk) * a.page_size + slot;
+            const uint32_t sc = base + 2 * C::kArray + uniform(i * box) * 2;
+            bulk_load(sc, a.scales[0] + grp, box * 2, bar);
+            bulk_load(sc + C::kScale, a.scales[1] + grp, box * 2, bar);
           }
         }
         ++issued;
@@ -440,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
   const int turn = warp >> 1;                                    // its pair's tiles: even or odd ones of the CTA's
   int st = 0, tile = 0;
   uint32_t ph = 0;
-  while (attn_next<C::kRows, kTile>(a, walk, p)) {
+  while (attn_next<C::kRows, kTile>(a, state)) {
+    const int t0 = p.t0, t1 = p.t1, begin = p.u.begin, end = p.u.end;
     // Q as B fragments: column g of tile nt is row 8 nt + g
     uint32_t bq[NT][kSteps][2];
     int lo[NT][2], hi[NT][2];  // cached tokens that rows 2c, 2c + 1 of a tile see
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     bool begun = false;   // every row of the lane has a reference
     bool started = false; // kexp is set
 
-    for (int t = p.t0; t < p.t1; ++t, ++tile) {
+    for (int t = t0; t < t1; ++t, ++tile) {
       const int here = st;
       const uint32_t parity = ph;
       if (++st == C::kStages) {
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       if (!mbar_wait_warp(smem_u32(&full[here]), parity, abort_flag, a)) break;
       const uint32_t kbase = smem_u32(smem + here * C::kStage), vbase = kbase + C::kArray, sbase = vbase + C::kArray;
       const int first = t * kTile + row0;
-      if (first < p.u.end && first + 16 * kSlices > p.u.begin) {  // some token of the slices is seen
+      if (first < end && first + 16 * kSlices > begin) {  // some token of the slices is seen
         // ---------------------------------------------------------- S^T = K Q^T
         float s[kSlices][NT][4];
         {
@@ -551,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             if constexpr (kQuant) {
               ks *= half_bits_to_float(lds16(sbase + 2 * tok));
               uint32_t v = lds16(sbase + C::kScale + 2 * tok);
-              if (at >= p.u.end) v = 0;  // whatever the slots past the end hold
+              if (at >= end) v = 0;  // whatever the slots past the end hold
               vtop = max(vtop, v);
               vs[h][e] = half_bits_to_float(v);
             }
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         // ---------------------------------------------------------- O^T += V^T P^T
 #pragma unroll
         for (int h = 0; h < kSlices; ++h)
-          values<B, D, NT>(vbase, row0 + 16 * h, t * kTile + row0 + 16 * h, p.u.end, lane, pb[h], o);
+          values<B, D, NT>(vbase, row0 + 16 * h, t * kTile + row0 + 16 * h, end, lane, pb[h], o);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[here]));
@@ -677,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       }
     }
     // 128 threads: 4 dims of a row each
-    const int c0 = p.whole ? 0 : attn_cta_of(walk.s, p.first), c1 = p.whole ? 0 : attn_cta_of(walk.s, p.first + p.u.tiles - 1);
+    const int c0 = p.whole ? 0 : attn_cta_of(state.s, p.first), c1 = p.whole ? 0 : attn_cta_of(state.s, p.first + p.u.tiles - 1);
     const int me = blockIdx.x;
     float* slot = p.whole ? nullptr : attn_slot(a, me, me == c0, C::kFloats);
     for (int e = threadIdx.x; e < p.u.rows * (D / 4); e += kConsumers * 32) {

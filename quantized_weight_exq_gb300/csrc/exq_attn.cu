@@ -87,7 +87,7 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   if (blocks * b.n_seqs > 0x7FFFFFFFll) return EXQ_ERR_UNSUPPORTED;
   if (blocks == 0) return EXQ_OK;
   a.row_blocks = static_cast<int>(blocks);
-  a.unit_cost = many ? 8 : 6;
+  a.unit_cost = many ? 12 : 6;
   a.min_tiles = 2;
   if (many) switch (c.bits) {
       case 4: return launch_attn_chunk4(call, a, sms, stream);

@@ -79,13 +79,14 @@ struct Cfg {
   static constexpr int kOffPacked = kOffQ + kRows * D * 2;
   // a packed stage is one tile of K or of V with its scales
   static constexpr int kPacked = B == 16 ? 0 : (Packed::kArray + Packed::kScale + 1023) / 1024 * 1024;
-  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 -
+  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 - kStreams * 4 * 2048 -
                                kThreads / 32 * static_cast<int>(sizeof(AttnState)) - 512;
   static constexpr int kPackedFit = B == 16 ? 0 : kRoom / kPacked;
   static constexpr int kPackedStages = kPackedFit > 8 ? 8 : kPackedFit;
   static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32
   static constexpr int kOffExps = kOffScale + 4 * 2 * kTile * 4;          // [4][2]: V's exponents
-  static constexpr int kOffState = kOffExps + 64;                  // a warp's place each
+  static constexpr int kOffStage = kOffExps + 64;                         // 32 rows of 64 bytes a softmax warp
+  static constexpr int kOffState = kOffStage + kStreams * 4 * 2048;       // a warp's place each
   static constexpr int kOffBar = kOffState + kThreads / 32 * static_cast<int>(sizeof(AttnState));
   static constexpr int kSmem = 1024 + kOffBar + 512;
   static constexpr int kFloats = kRows * (D + 2);
@@ -563,26 +564,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g > 0) ok = mbar_wait_warp(s_full(g - 1), phase4(g - 1), abort_flag, a);
       if (!ok) break;
       const int rows = p.u.rows, q_rows = rows > 128 ? C::kRows : 128;
-      // consecutive threads hold 8 rows of one chunk (their stores fall on different banks); 8 loads at a time
-      for (int i0 = tid; i0 < q_rows * (D / 8); i0 += 8 * kDequantThreads) {
-        uint4 v[8];
+      {
+        // A thread's chunk of the dims (for D = 256 also the one 16 on) and
+        // its first row; its rows step by kStep. Eight threads hold
+        // neighbouring rows of one chunk, so that their stores fall on
+        // different banks; 8 loads at a time.
+        constexpr int kPer = D == 256 ? 2 : 1, kStep = D == 64 ? 16 : 8, kBatch = 8 / kPer;
+        const int ch = (tid >> 3) & (D == 64 ? 7 : 15);
+        int row = (tid & 7) + (D == 64 ? 8 * (tid >> 6) : 0);
+        const int group = a.group, down = kStep / group, over = kStep - down * group;
+        const long long ts = a.q.token_stride, hs = a.q.head_stride;
+        int head = (p.u.r0 + row) % group;
+        const uint16_t* src = a.q.data + (p.u.q0 + (p.u.r0 + row) / group) * ts + (p.head * group + head) * hs + 8 * ch;
+        const long long step = down * ts + over * hs, wrap = ts - group * hs;  // and from the last head to the next token
+        for (int i0 = 0; i0 < q_rows; i0 += kBatch * kStep) {
+          uint4 v[kBatch][kPer];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + j * kDequantThreads, row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
-          v[j] = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            int token, head;
-            attn_row_of(a, p, row, token, head);
-            v[j] = __ldg(reinterpret_cast<const uint4*>(a.q.data + token * a.q.token_stride + head * a.q.head_stride + 8 * ch));
+          for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+              v[j][k] = row + j * kStep < rows ? __ldg(reinterpret_cast<const uint4*>(src + 128 * k)) : make_uint4(0, 0, 0, 0);
+            src += step;
+            head += over;
+            if (head >= group) {
+              head -= group;
+              src += wrap;
+            }
           }
-        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + j * kDequantThreads, row = (i & 7) + 8 * (i / D), ch = (i >> 3) % (D / 8);
-          uint4 u = v[j];
-          if constexpr (kPairs)
-            u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
-          sts128(sbase + C::kOffQ + (row >> 7) * (128 * D * 2) + operand_at(128, row & 127, ch), u.x, u.y, u.z, u.w);
+          for (int j = 0; j < kBatch; ++j) {
+            const int r = row + j * kStep;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              uint4 u = v[j][k];
+              if constexpr (kPairs)
+                u = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410), prmt(u.y, u.w, 0x7632));
+              sts128(sbase + C::kOffQ + (r >> 7) * (128 * D * 2) + operand_at(128, r & 127, ch + 16 * k), u.x, u.y, u.z, u.w);
+            }
+          }
+          row += kBatch * kStep;
         }
       }
       async_fence();
@@ -816,15 +836,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool has = row < p.u.rows;
         int token = 0, head = 0;
         if (has) attn_row_of(a, p, row, token, head);
-        uint16_t* dst = a.out.data + token * a.out.token_stride + head * a.out.head_stride;
         float* slot = p.whole ? nullptr : attn_slot(a, blockIdx.x, static_cast<int>(blockIdx.x) == c0, C::kFloats);
-        const float inv = row_l > 0.f ? 1.f / row_l : 0.f;
+        const float inv = !p.whole ? 1.f : row_l > 0.f ? 1.f / row_l : 0.f;
+        // where the lane's row goes
+        const unsigned long long out =
+            p.whole ? reinterpret_cast<unsigned long long>(a.out.data + token * a.out.token_stride + head * a.out.head_stride)
+                    : reinterpret_cast<unsigned long long>(slot + row * D);
+        // Rows go out through shared memory, 64 bytes of each at a time, so
+        // that four lanes write 64 neighbouring bytes of a row and a store
+        // touches 8 lines and not 32 (a unit's rows took 8500 cycles that way).
+        const uint32_t stage = sbase + C::kOffStage + (s * 4 + (warp & 3)) * 2048;
+        const uint32_t put = stage + lane * 64, put_x = (lane >> 1) & 3;
+        const bool whole = p.whole;
+        const int last = min(32, p.u.rows - row0);  // rows of the warp
+        const auto flush = [&](int byte) {          // the staged 64 bytes to byte `byte` of each row
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), ch = lane & 3;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
+            const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
+            if (rr < last) *reinterpret_cast<uint4*>(to + byte + 16 * ch) = v;
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
           tmem_ld32(t_o + 32 * c, r);
           tmem_wait_ld(r);
-          if (has) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             float y[8];
@@ -832,23 +875,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) {
               // 0 4 1 5 2 6 3 7 back to the dims' order
               const int at = kPairs ? (j < 4 ? 2 * j : 2 * (j - 4) + 1) : j;
-              y[j] = row_l > 0.f ? __uint_as_float(r[i + at]) : 0.f;
+              y[j] = row_l > 0.f ? __uint_as_float(r[i + at]) * inv : 0.f;
             }
-            if (p.whole) {
-              uint4 o;
-              o.x = half2_bits(y[0] * inv, y[1] * inv);
-              o.y = half2_bits(y[2] * inv, y[3] * inv);
-              o.z = half2_bits(y[4] * inv, y[5] * inv);
-              o.w = half2_bits(y[6] * inv, y[7] * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * c + i) = o;
+            if (whole) {
+              sts128(put + (((i >> 3) ^ put_x) << 4), half2_bits(y[0], y[1]), half2_bits(y[2], y[3]), half2_bits(y[4], y[5]),
+                     half2_bits(y[6], y[7]));
             } else {
-              float4* at = reinterpret_cast<float4*>(slot + row * D + 32 * c + i);
-              at[0] = make_float4(y[0], y[1], y[2], y[3]);
-              at[1] = make_float4(y[4], y[5], y[6], y[7]);
+              sts128(put + ((((i >> 2) & 3) ^ put_x) << 4), __float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                     __float_as_uint(y[3]));
+              sts128(put + (((((i >> 2) + 1) & 3) ^ put_x) << 4), __float_as_uint(y[4]), __float_as_uint(y[5]),
+                     __float_as_uint(y[6]), __float_as_uint(y[7]));
+              if (i & 8) flush((32 * c + i - 8) * 4);
             }
           }
-          }
-          __syncwarp();
+          if (whole) flush(32 * c * 2);
         }
         if (has) {
           if (p.whole)

@@ -849,46 +849,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t put = stage + lane * 64, put_x = (lane >> 1) & 3;
         const bool whole = p.whole;
         const int last = min(32, p.u.rows - row0);  // rows of the warp
-        const auto flush = [&](int byte) {          // the staged 64 bytes to byte `byte` of each row
+        // the rows that the lane writes a quarter of, and its places in them
+        const int get_row = lane >> 2, get_ch = lane & 3;
+        unsigned long long to[4];
+        uint32_t get[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + get_row;
+          to[i] = __shfl_sync(0xffffffffu, out, rr) + 16 * get_ch;
+          get[i] = stage + rr * 64 + ((get_ch ^ ((rr >> 1) & 3)) << 4);
+        }
+        const auto flush = [&](int byte) {  // the staged 64 bytes to byte `byte` of each row
+          uint4 v[4];
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), ch = lane & 3;
-            uint4 v;
+          for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
-            const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
-            if (rr < last) *reinterpret_cast<uint4*>(to + byte + 16 * ch) = v;
-          }
+                         : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                         : "r"(get[i]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * i + get_row < last) *reinterpret_cast<uint4*>(to[i] + byte) = v[i];
           __syncwarp();
         };
-#pragma unroll 1
+        uint32_t r[2][32];
+        tmem_ld32(t_o, r[0]);
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(t_o + 32 * c, r);
-          tmem_wait_ld(r);
+          tmem_wait_ld(r[c & 1]);
+          if (c + 1 < D / 32) tmem_ld32(t_o + 32 * (c + 1), r[(c + 1) & 1]);
+          float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float y[8];
+          for (int i = 0; i < 32; ++i) {
+            // 0 4 1 5 2 6 3 7 back to the dims' order
+            const int at = kPairs ? (i & ~7) + 2 * (i & 3) + ((i >> 2) & 1) : i;
+            y[i] = row_l > 0.f ? __uint_as_float(r[c & 1][at]) * inv : 0.f;
+          }
+          if (whole) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              // 0 4 1 5 2 6 3 7 back to the dims' order
-              const int at = kPairs ? (j < 4 ? 2 * j : 2 * (j - 4) + 1) : j;
-              y[j] = row_l > 0.f ? __uint_as_float(r[i + at]) * inv : 0.f;
-            }
-            if (whole) {
-              sts128(put + (((i >> 3) ^ put_x) << 4), half2_bits(y[0], y[1]), half2_bits(y[2], y[3]), half2_bits(y[4], y[5]),
-                     half2_bits(y[6], y[7]));
-            } else {
-              sts128(put + ((((i >> 2) & 3) ^ put_x) << 4), __float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                     __float_as_uint(y[3]));
-              sts128(put + (((((i >> 2) + 1) & 3) ^ put_x) << 4), __float_as_uint(y[4]), __float_as_uint(y[5]),
-                     __float_as_uint(y[6]), __float_as_uint(y[7]));
-              if (i & 8) flush((32 * c + i - 8) * 4);
+            for (int i = 0; i < 4; ++i)
+              sts128(put + ((i ^ put_x) << 4), half2_bits(y[8 * i], y[8 * i + 1]), half2_bits(y[8 * i + 2], y[8 * i + 3]),
+                     half2_bits(y[8 * i + 4], y[8 * i + 5]), half2_bits(y[8 * i + 6], y[8 * i + 7]));
+            flush(64 * c);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sts128(put + ((i ^ put_x) << 4), __float_as_uint(y[16 * h + 4 * i]), __float_as_uint(y[16 * h + 4 * i + 1]),
+                       __float_as_uint(y[16 * h + 4 * i + 2]), __float_as_uint(y[16 * h + 4 * i + 3]));
+              flush(128 * c + 64 * h);
             }
           }
-          if (whole) flush(32 * c * 2);
         }
         if (has) {
           if (p.whole)

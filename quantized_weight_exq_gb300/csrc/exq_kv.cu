@@ -327,58 +327,117 @@ __device__ __forceinline__ TokenPlace find_place(const AppendArgs& a, int t, int
   return p;
 }
 
-// A lane's values [lane VPL, lane VPL + VPL) of a row, turned. Partners of
-// HALF pairs come from the lane that holds them (R/2 a multiple of VPL), or
-// are read from the row in memory.
+// What a lane needs to turn its values [lane VPL, lane VPL + VPL) of any row
+// of a token: y = x c + o s with its partner's value o, products and sum each
+// rounded (s is negated for the first of a pair, which is exact, so both
+// values of a pair come out as by rope_first and rope_second).
 template <int VPL>
-__device__ __forceinline__ void rotate_lane(uint32_t (&h)[VPL], const uint16_t* row, const float2* cs, int R,
-                                            bool interleaved, int lane) {
+struct Turn {
+  float c[VPL], s[VPL];
+  int from;         // lane that holds the partners of HALF pairs; -1: read them from memory
+  bool all, some;   // all / some of the lane's values turn
+};
+
+template <int VPL>
+__device__ __forceinline__ void load_turn(Turn<VPL>& t, const float2* cs, int R, bool interleaved, int lane) {
   const int half = R / 2, d0 = lane * VPL;
+  t.all = d0 + VPL <= R;
+  t.some = d0 < R;
+  t.from = half % VPL == 0 ? (d0 < half ? lane + half / VPL : lane - half / VPL) & 31 : -1;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int d = d0 + i;
+    const bool first = interleaved ? (i & 1) == 0 : d < half;
+    const float2 v = d < R ? cs[interleaved ? d / 2 : first ? d : d - half] : make_float2(1.f, 0.f);
+    t.c[i] = v.x;
+    t.s[i] = first ? -v.y : v.y;
+  }
+}
+
+// The lane's values turned. Partners of HALF pairs come from the lane that
+// holds them (R/2 a multiple of VPL), or from the row in memory.
+template <int VPL>
+__device__ __forceinline__ void rotate_lane(uint32_t (&h)[VPL], const Turn<VPL>& t, const uint16_t* row, int R,
+                                            bool interleaved, int lane) {
   uint32_t other[VPL];
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) other[i] = h[i ^ 1];
-  } else if (half % VPL == 0) {  // the same for all lanes
-    const int src = d0 < half ? lane + half / VPL : lane - half / VPL;
+  } else if (t.from >= 0) {  // the same for all lanes
 #pragma unroll
     for (int i = 0; i < VPL; i += 2) {
-      const uint32_t two = __shfl_sync(0xffffffffu, h[i] | (h[i + 1] << 16), src & 31);
+      const uint32_t two = __shfl_sync(0xffffffffu, h[i] | (h[i + 1] << 16), t.from);
       other[i] = two & 0xFFFFu;
       other[i + 1] = two >> 16;
     }
   } else {
+    const int half = R / 2;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int d = d0 + i;
+      const int d = lane * VPL + i;
       other[i] = d < R ? row[d < half ? d + half : d - half] : 0u;
     }
     __syncwarp();  // q_out may be the row itself: every partner is read before any lane writes
   }
+  if (!t.some) return;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int d = d0 + i;
-    if (d >= R) continue;
-    const bool first = interleaved ? (i & 1) == 0 : d < half;
-    const float2 c = cs[interleaved ? d / 2 : first ? d : d - half];
-    const float x = half_bits_to_float(h[i]), o = half_bits_to_float(other[i]);
-    h[i] = float_to_half_bits(first ? rope_first(x, o, c) : rope_second(o, x, c));
+    const uint32_t y = float_to_half_bits(
+        __fadd_rn(__fmul_rn(half_bits_to_float(h[i]), t.c[i]), __fmul_rn(half_bits_to_float(other[i]), t.s[i])));
+    h[i] = t.all || lane * VPL + i < R ? y : h[i];
   }
 }
 
 // Bound by HBM for many tokens (2 bytes read a value, 2 or B / 8 written), by
 // latency for one: a block holds 1 .. 8 tokens, each done by 8 / tokens of
 // its warps, and where tokens are few the rows of a token are split over
-// blocks. A warp does a row (one head of q, k or v) at a time, four rows'
-// loads ahead of their arithmetic; cos and sin are computed once per block.
+// blocks. A warp does a row (one head of q, k or v) at a time, with the loads
+// of kU rows of each of q, k and v in flight before their arithmetic, the first ones while the
+// token's place is looked up; cos and sin are computed once per block, and a
+// lane keeps those of its values in registers for all rows.
 template <int VPL, int B>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, VPL <= 4 ? 3 : 2) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   extern __shared__ float2 cs[];
   __shared__ TokenPlace places[kWarps];
   constexpr int D = 32 * VPL;
-  constexpr int kU = 4;
+  constexpr int kU = VPL <= 4 ? 4 : 2;
+  using V = typename Vec<VPL>::T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens = 1 << a.shift;
   const int t0 = blockIdx.x << a.shift;
+  const int tk = warp & (tokens - 1), stride = kWarps >> a.shift;
+  const long long t = t0 + tk;
+  // the block's rows of the token, heads of q, k and v one after the other
+  const int begin = blockIdx.y * a.rows_per, end = begin + a.rows_per;
+
+  // heads [first, last) of q, k or v, every `stride`-th from the warp's own
+  struct Part {
+    int first, last;
+    const uint16_t* src;  // of head `first`
+    long long step;
+  };
+  const auto part_of = [&](int which, int start, int heads) {
+    Part p;
+    int r = begin + (warp >> a.shift);  // the warp's rows are begin + warp / tokens + i stride
+    if (r < start) r += (start - r + stride - 1) / stride * stride;
+    p.first = r - start;
+    p.last = t < a.n_tokens ? min(heads, end - start) : 0;
+    p.src = a.in[which] + t * a.ts[which] + p.first * a.hs[which] + lane * VPL;  // (not read where there are no rows)
+    p.step = stride * a.hs[which];
+    return p;
+  };
+  const auto fetch = [&](V (&v)[kU], const Part& p, int head, const uint16_t* src) {
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (head + k * stride < p.last) v[k] = *reinterpret_cast<const V*>(src + k * p.step);
+  };
+  const Part pk = part_of(1, a.n_q, a.n_kv_heads), pv = part_of(2, a.n_q + a.n_kv_heads, a.n_kv_heads);
+  const Part pq = part_of(0, 0, a.n_q);
+  V vk[kU], vv[kU], next[kU];
+  fetch(vk, pk, pk.first, pk.src);
+  fetch(vv, pv, pv.first, pv.src);
+  fetch(next, pq, pq.first, pq.src);
+
   if (warp < tokens) {
     TokenPlace p{0, -1, 0};
     if (t0 + warp < a.n_tokens) p = find_place(a, t0 + warp, lane);
@@ -387,62 +446,64 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_con
   __syncthreads();
   const int half = a.R / 2;
   for (int i = threadIdx.x; i < tokens * half; i += kWarps * 32) {  // R = 0: no rotary positions
-    const int tk = i / half, j = i - tk * half;
-    if (places[tk].block >= 0)
-      cs[i] = rope_cos_sin(__ldg(reinterpret_cast<const unsigned long long*>(a.steps) + j), places[tk].pos, a.gain, false);
+    const int of = i / half, j = i - of * half;
+    if (places[of].block >= 0)
+      cs[i] = rope_cos_sin(__ldg(reinterpret_cast<const unsigned long long*>(a.steps) + j), places[of].pos, a.gain, false);
   }
   __syncthreads();
+  const TokenPlace place = places[tk];
+  if (place.block < 0) return;  // warp-uniform
+  Turn<VPL> turn;
+  if (half > 0) load_turn<VPL>(turn, cs + tk * half, a.R, a.interleaved, lane);
 
-  const int tk = warp & (tokens - 1), stride = kWarps >> a.shift;
-  const TokenPlace p = places[tk];
-  if (p.block < 0) return;  // warp-uniform
-  const long long t = t0 + tk;
-  const float2* table = cs + tk * half;
-  const int rows = a.n_q + 2 * a.n_kv_heads;
-  const int r1 = min(rows, static_cast<int>(blockIdx.y + 1) * a.rows_per);
-  using V = typename Vec<VPL>::T;
-  for (int r0 = blockIdx.y * a.rows_per + (warp >> a.shift); r0 < r1; r0 += kU * stride) {
-    V raw[kU];
-    const uint16_t* src[kU];
+  const auto store16 = [&](uint16_t* dst, const uint32_t (&h)[VPL]) {
+    uint32_t out[VPL / 2];
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const int r = r0 + k * stride;
-      if (r < r1) {
-        const int which = r < a.n_q ? 0 : r < a.n_q + a.n_kv_heads ? 1 : 2;
-        const int head = which == 0 ? r : which == 1 ? r - a.n_q : r - a.n_q - a.n_kv_heads;
-        const uint16_t* base = which == 0 ? a.in[0] : which == 1 ? a.in[1] : a.in[2];
-        const long long ts = which == 0 ? a.ts[0] : which == 1 ? a.ts[1] : a.ts[2];
-        const long long hs = which == 0 ? a.hs[0] : which == 1 ? a.hs[1] : a.hs[2];
-        src[k] = base + t * ts + head * hs;
-        raw[k] = *reinterpret_cast<const V*>(src[k] + lane * VPL);
+    for (int i = 0; i < VPL / 2; ++i) out[i] = h[2 * i] | (h[2 * i + 1] << 16);
+    *reinterpret_cast<V*>(dst + lane * VPL) = *reinterpret_cast<const V*>(out);
+  };
+  // K (turned) and V to the page
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const Part& p = which ? pv : pk;
+    V (&v)[kU] = which ? vv : vk;
+    const uint16_t* src = p.src;
+    for (int head = p.first; head < p.last; head += kU * stride, src += kU * p.step) {
+      if (head != p.first) fetch(v, p, head, src);
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const int hd = head + k * stride;
+        if (hd >= p.last) break;  // warp-uniform
+        uint32_t h[VPL];
+        unpack_halves<VPL>(v[k], h);
+        if (which == 0 && half > 0) rotate_lane<VPL>(h, turn, src + k * p.step - lane * VPL, a.R, a.interleaved, lane);
+        const long long g = (static_cast<long long>(place.block) * a.n_kv_heads + hd) * a.page_size + place.slot;
+        if constexpr (B == 16)
+          store16(reinterpret_cast<uint16_t*>(a.codes[which]) + g * D, h);
+        else
+          quantize_group<VPL, B>(h, a.codes[which] + g * (VPL * B), a.scales[which] + g, lane);
       }
     }
+  }
+  // Q
+  if (a.n_q == 0) return;
+  const uint16_t* src = pq.src;
+  uint16_t* dst = a.q_out + t * a.ts[3] + pq.first * a.hs[3];
+  for (int head = pq.first; head < pq.last; head += kU * stride) {
+    V v[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) v[k] = next[k];
+    const uint16_t* at = src;
+    src += kU * pq.step;
+    fetch(next, pq, head + kU * stride, src);
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int r = r0 + k * stride;
-      if (r >= r1) break;  // warp-uniform
+      if (head + k * stride >= pq.last) break;  // warp-uniform
       uint32_t h[VPL];
-      unpack_halves<VPL>(raw[k], h);
-      if (half > 0 && r < a.n_q + a.n_kv_heads) rotate_lane<VPL>(h, src[k], table, a.R, a.interleaved, lane);
-      uint16_t* dst16 = nullptr;
-      if (r < a.n_q) {
-        dst16 = a.q_out + t * a.ts[3] + r * a.hs[3];
-      } else {
-        const int v = r < a.n_q + a.n_kv_heads ? 0 : 1;
-        const int head = r - a.n_q - (v ? a.n_kv_heads : 0);
-        const long long g = (static_cast<long long>(p.block) * a.n_kv_heads + head) * a.page_size + p.slot;
-        if constexpr (B == 16)
-          dst16 = reinterpret_cast<uint16_t*>(v ? a.codes[1] : a.codes[0]) + g * D;
-        else
-          quantize_group<VPL, B>(h, (v ? a.codes[1] : a.codes[0]) + g * (VPL * B),
-                                 (v ? a.scales[1] : a.scales[0]) + g, lane);
-      }
-      if (dst16) {
-        uint32_t out[VPL / 2];
-#pragma unroll
-        for (int i = 0; i < VPL / 2; ++i) out[i] = h[2 * i] | (h[2 * i + 1] << 16);
-        *reinterpret_cast<V*>(dst16 + lane * VPL) = *reinterpret_cast<const V*>(out);
-      }
+      unpack_halves<VPL>(v[k], h);
+      rotate_lane<VPL>(h, turn, at + k * pq.step - lane * VPL, a.R, a.interleaved, lane);
+      store16(dst, h);
+      dst += stride * a.hs[3];
     }
   }
 }

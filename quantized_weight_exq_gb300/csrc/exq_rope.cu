@@ -64,8 +64,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   constexpr int kU = 4;
   if (u >= turning) {  // passes through
     const int d = a.R + 8 * (u - turning);
-    for (int h = h0 + hl; h < h1; h += head_lanes)
-      *reinterpret_cast<uint4*>(y + h * a.yh + d) = *reinterpret_cast<const uint4*>(x + h * a.xh + d);
+    for (int h = h0 + hl; h < h1; h += kU * head_lanes) {
+      uint4 v[kU];
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (h + k * head_lanes < h1) v[k] = *reinterpret_cast<const uint4*>(x + (h + k * head_lanes) * a.xh + d);
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (h + k * head_lanes < h1) *reinterpret_cast<uint4*>(y + (h + k * head_lanes) * a.yh + d) = v[k];
+    }
     return;
   }
   constexpr int kPairs = HALF ? 8 : 4;
@@ -165,7 +172,12 @@ exq_status launch_rope(const exq_rope_params& rope, const exq_rows& x, long long
     a.units = rope.R / 2 + (in_place ? 0 : D - rope.R);
   int tokens = std::max(1, kThreads / (rope.R / 2));
   if (vec) tokens = std::min(tokens, kThreads / a.units);
-  a.tokens_per = static_cast<int>(std::min<long long>(std::min(tokens, 8), n_tokens));
+  // at most 4 tokens a block (8 left a second, part-filled wave of blocks: 77
+  // for 54 us at 8000 tokens of 64 half-turned heads), fewer while there is
+  // not a block for each SM twice over
+  tokens = std::min(tokens, 4);
+  while (tokens > 1 && n_tokens < 2ll * sms * tokens) tokens /= 2;
+  a.tokens_per = tokens;
   const long long gx = (n_tokens + a.tokens_per - 1) / a.tokens_per;
   if (gx > 0x7FFFFFFFll) return EXQ_ERR_UNSUPPORTED;
   // few tokens: the heads are split over blocks until two blocks an SM have work

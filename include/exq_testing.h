@@ -13,8 +13,8 @@
 extern "C" {
 #endif
 
-/* exq_testing_starve -- while wait_rounds > 0, every exq_gemv, exq_gemv_multi
- * and exq_gemm launch runs with its producer issuing no copies at all, and
+/* exq_testing_starve -- while wait_rounds > 0, every exq_gemv, exq_gemv_multi,
+ * exq_gemm and exq_paged_attn launch runs with its producer issuing no copies at all, and
  * every mbarrier wait of those kernels gives up after wait_rounds polling
  * rounds instead of the built-in bound. The consumers then wait for data that
  * never comes; their bounded waits run out, the kernel records

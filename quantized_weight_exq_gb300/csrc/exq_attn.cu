@@ -27,17 +27,22 @@ unsigned* error_word(int dev) {
 
 constexpr int kWaitLimit = 1 << 22;  // try_wait rounds before giving up
 
-// More query rows a KV head than this go to the tensor-memory kernel, whose
+// More query rows a KV head than these go to the tensor-memory kernel, whose
 // units have 256 (128) of them; fewer to the packed-code kernel, which reads
-// the cache again for every 16 (8).
-bool many_rows(long long rows) { return rows > 32; }
+// the cache again for every 16 (8). Measured on 8 sequences of up to 4000
+// tokens, packed-code against tensor-memory kernel, us: D = 128, Q4: 31 / 39
+// at 32 rows, 42 / 42 at 40, 45 / 40 at 64; fp16: 63 / 35 at 32; D = 64, Q4:
+// 22 / 27 at 64; D = 256, Q4: 40 / 36 at 32.
+bool many_rows(const exq_kv_cache& c, long long rows) {
+  return rows > (c.bits == 16 || c.D == 256 ? 16 : c.D == 64 ? 64 : 32);
+}
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms) {
   const long long all = static_cast<long long>(b.max_q_len) * (n_heads / c.n_kv_heads);
-  const int rows = many_rows(all) ? chunk::rows_of(c.D) : split::rows_of(c.D, all);
-  const size_t ctas = std::min(many_rows(all) ? sms : 4 * sms, kAttnMaxCtas);
+  const int rows = many_rows(c, all) ? chunk::rows_of(c.D) : split::rows_of(c.D, all);
+  const size_t ctas = std::min(many_rows(c, all) ? sms : 4 * sms, kAttnMaxCtas);
   return kAttnCounterBytes + ctas * 2 * rows * (c.D + 2) * sizeof(float);
 }
 
@@ -81,12 +86,16 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   a.wait_limit = starve > 0 ? starve : kWaitLimit;
   a.starve = starve > 0 ? 1 : 0;
   const long long rows = static_cast<long long>(b.max_q_len) * a.group;
-  const bool many = many_rows(rows);
+  const bool many = many_rows(c, rows);
   const int per = many ? chunk::rows_of(c.D) : split::rows_of(c.D, rows);
   const long long blocks = (rows + per - 1) / per;
   if (blocks * b.n_seqs > 0x7FFFFFFFll) return EXQ_ERR_UNSUPPORTED;
   if (blocks == 0) return EXQ_OK;
   a.row_blocks = static_cast<int>(blocks);
+  // A unit's queries, joins and stores take about as long as these many tiles
+  // (32 ragged sequences Q4: 61 us at 0, 45 at 4 to 8; prompts of 3500 tokens
+  // in a window: 360 us at 0, 245 at 12). Two tiles a CTA at least: 10 us for
+  // one sequence of 500 tokens, 15 at ten.
   a.unit_cost = many ? 12 : 6;
   a.min_tiles = 2;
   if (many) switch (c.bits) {

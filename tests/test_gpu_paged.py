@@ -417,3 +417,69 @@ def test_copy_pages(env, bits, D, page, KH, layers, moves):
     for a in c.words + [s for s in c.scales if s is not None]:
         a[:, pairs[:, 1]] = a[:, pairs[:, 0]]
     c.same(cache)
+
+
+# ---------------------------------------------------------------- failure detection, types
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_wait_runs_out_then_recovers(env, bits, new):
+    # the producer issues no copies: every wait runs out, the call ends in a timeout, the next one is right again
+    exq, torch = env
+    c = Case(exq, torch, bits, 128, 64, 2, [700, 90], [new, new], seed=6).fill()
+    cache, batch = c.cache(), c.batch()
+    q = torch.randn(2 * new, 8, 128, device="cuda").half()
+    ws = torch.zeros(exq.exq_paged_attn_workspace_size(cache, batch, 8, 2 * new), dtype=torch.uint8, device="cuda")
+    want = exq.exq_paged_attn(cache, batch, q, workspace=ws)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    exq.exq_testing_starve(64)
+    try:
+        exq.exq_paged_attn(cache, batch, q, workspace=ws)
+        assert exq.exq_get_last_device_error() == exq.EXQ_ERR_TIMEOUT
+    finally:
+        exq.exq_testing_starve(0)
+    ws.zero_()
+    got = exq.exq_paged_attn(cache, batch, q, workspace=ws)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    assert torch.equal(got, want)
+
+
+def test_binding_refuses_other_types(env):
+    exq, torch = env
+    c = Case(exq, torch, 4, 64, 16, 2, [20], [1], seed=3).fill()
+    cache, batch = c.cache(), c.batch()
+    q = torch.randn(1, 8, 64, device="cuda").bfloat16()
+    for call in (lambda: exq.exq_paged_attn(cache, batch, q), lambda: exq.exq_kv_append(cache, batch, q[:, :2], q[:, :2]),
+                 lambda: exq.KVCache(cache.k_codes, cache.v_codes, None, cache.v_scales, 4),
+                 lambda: exq.KVCache(cache.k_codes, cache.v_codes.float(), cache.k_scales, cache.v_scales, 4),
+                 lambda: exq.KVCache(cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, 16),
+                 lambda: exq.KVBatch(batch.q_start, batch.kv_len.float(), batch.page_table, 1, 20),
+                 lambda: exq.KVBatch(batch.q_start, batch.kv_len.long(), batch.page_table, 1, 20),
+                 lambda: exq.exq_kv_copy_pages(cache, torch.zeros(1, 2, device="cuda"))):
+        with pytest.raises(exq.ExqError):
+            call()
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64), (16, 128)])
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+def test_attention_scales_of_any_sign(env, bits, D, scale):
+    exq, torch = env
+    for new in (1, 50):
+        c = Case(exq, torch, bits, D, 16, 1, [150], [new], seed=D).fill()
+        q = c.rng.standard_normal((new, 4, D)).astype(np.float16)
+        out = exq.exq_paged_attn(c.cache(), c.batch(), torch.from_numpy(q).cuda(), scale=scale)
+        k, v = c.dense[0]
+        qd = q.astype(np.float64)
+        ref, _, spread, total = O.attention(qd, k, v, np.arange(150 - new, 150), float(np.float32(scale)))
+        assert np.all(np.abs(_np(out).astype(np.float64) - ref) <= _bound(ref, spread, total, qd, k, v, scale, 150, D))
+
+
+def test_attention_of_many_short_and_empty_sequences(env):
+    # more sequences than lanes, most of them empty or one tile long: shares that begin and end inside many units
+    exq, torch = env
+    rng = np.random.default_rng(11)
+    lens = [int(n) for n in rng.choice([0, 0, 1, 5, 64, 65, 200], 150)]
+    for new in (1, 3):
+        _check_attention(env, (4, 64, 16, 1, 6, lens, [min(new, n) for n in lens], True, 0), seed=3)
+    _check_attention(env, (16, 64, 16, 1, 6, [n for n in lens[:60]], [min(9, n) for n in lens[:60]], True, 0), seed=3)

@@ -37,10 +37,15 @@ bool many_rows(const exq_kv_cache& c, long long rows) {
   return rows > (c.bits == 16 || c.D == 256 ? 16 : c.D == 64 ? 64 : 32);
 }
 
+// Rows a KV head of one sequence at most.
+long long most_rows(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads) {
+  return static_cast<long long>(std::min(b.max_q_len, b.n_tokens)) * (n_heads / c.n_kv_heads);
+}
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms) {
-  const long long all = static_cast<long long>(b.max_q_len) * (n_heads / c.n_kv_heads);
+  const long long all = most_rows(c, b, n_heads);
   const int rows = many_rows(c, all) ? chunk::rows_of(c.D) : split::rows_of(c.D, all);
   const size_t ctas = std::min(many_rows(c, all) ? sms : 4 * sms, kAttnMaxCtas);
   return kAttnCounterBytes + ctas * 2 * rows * (c.D + 2) * sizeof(float);
@@ -78,18 +83,18 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   a.n_heads = call.n_heads;
   a.scale_log2 = static_cast<float>(call.scale * 1.4426950408889634);
   a.causal = call.causal;
-  a.window = call.window;
+  a.window = call.window < b.max_kv_len ? call.window : 0;  // no position reaches that far: no limit, no overflow
   a.lse = call.lse;
   a.counters = static_cast<unsigned*>(call.workspace);
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(call.workspace) + kAttnCounterBytes);
   const int starve = testing_starve_rounds();
   a.wait_limit = starve > 0 ? starve : kWaitLimit;
   a.starve = starve > 0 ? 1 : 0;
-  const long long rows = static_cast<long long>(b.max_q_len) * a.group;
+  const long long rows = most_rows(c, b, call.n_heads);
   const bool many = many_rows(c, rows);
   const int per = many ? chunk::rows_of(c.D) : split::rows_of(c.D, rows);
   const long long blocks = (rows + per - 1) / per;
-  if (blocks * b.n_seqs > 0x7FFFFFFFll) return EXQ_ERR_UNSUPPORTED;
+  if (rows > 0x7FFFFF00ll || blocks * b.n_seqs > 0x7FFFFF00ll) return EXQ_ERR_UNSUPPORTED;  // 32-bit row and block numbers
   if (blocks == 0) return EXQ_OK;
   a.row_blocks = static_cast<int>(blocks);
   // A unit's queries, joins and stores take about as long as these many tiles

@@ -92,6 +92,13 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnArgs& a, int pair) {
   return u;
 }
 
+// The pair after one whose unit is u. Blocks past a sequence's rows are passed
+// over together: one prompt chunk among many single tokens gives every
+// sequence as many blocks as the chunk.
+__device__ __forceinline__ int attn_after(const AttnArgs& a, int pair, const AttnUnit& u) {
+  return u.rows > 0 ? pair + 1 : (u.b + 1) * a.row_blocks;
+}
+
 // Places of a unit in the division.
 __device__ __forceinline__ long long attn_places(const AttnArgs& a, const AttnUnit& u) {
   return u.tiles > 0 ? u.tiles + a.unit_cost : 0;
@@ -121,7 +128,11 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a) {
   const int pairs = a.n_seqs * a.row_blocks;
   const int per = (pairs + 31) >> 5, p0 = min(lane * per, pairs), p1 = min(p0 + per, pairs);
   long long sum = 0;
-  for (int p = p0; p < p1; ++p) sum += attn_places(a, attn_unit<ROWS, TILE>(a, p));
+  for (int p = p0; p < p1;) {
+    const AttnUnit u = attn_unit<ROWS, TILE>(a, p);
+    sum += attn_places(a, u);
+    p = attn_after(a, p, u);
+  }
   long long inc = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -143,10 +154,12 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& a) {
   const bool mine = at <= s.begin && s.begin < at + sum * a.n_kv_heads;
   int pair = p0;
   if (mine && per > 1)
-    for (; pair < p1 - 1; ++pair) {
-      const long long tiles = attn_places(a, attn_unit<ROWS, TILE>(a, pair)) * a.n_kv_heads;
-      if (s.begin < at + tiles) break;
-      at += tiles;
+    while (pair < p1 - 1) {
+      const AttnUnit u = attn_unit<ROWS, TILE>(a, pair);
+      const long long places = attn_places(a, u) * a.n_kv_heads;
+      if (s.begin < at + places) break;
+      at += places;
+      pair = attn_after(a, pair, u);
     }
   const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;  // one lane
   s.pair_start = __shfl_sync(0xffffffffu, at, from);
@@ -206,7 +219,8 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnState& st) {
     int places = static_cast<int>(attn_places(a, p.u));
     while (at >= pair_start + static_cast<long long>(places) * a.n_kv_heads) {  // pairs that are done or have no rows
       pair_start += static_cast<long long>(places) * a.n_kv_heads;
-      p.u = attn_unit<ROWS, TILE>(a, ++pair);
+      pair = attn_after(a, pair, p.u);
+      p.u = attn_unit<ROWS, TILE>(a, pair);
       places = static_cast<int>(attn_places(a, p.u));
     }
     const int off = static_cast<int>(at - pair_start);

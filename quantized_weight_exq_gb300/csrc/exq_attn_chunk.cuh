@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             slot[C::kRows * D + row] = row_base, slot[C::kRows * D + C::kRows + row] = row_l;
         }
-        tc_before();  // the next unit's first P V, ordered by p_full, overwrites O
+        tc_before();  // the next unit's first P V, ordered by its weights, overwrites O
       }
       if (!p.whole) {
         __threadfence();

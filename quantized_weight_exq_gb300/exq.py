@@ -454,7 +454,8 @@ class Rope:
     """Rotary parameters on the GPU: steps int64 [R/2] (uint64 bits, exq_rope_steps), the layout and the gain."""
 
     def __init__(self, steps, R: int, layout: int = ROPE_HALF, gain: float = 1.0):
-        if steps.numel() < R // 2 or steps.element_size() != 8 or steps.is_floating_point() or not steps.is_contiguous():
+        if (not steps.is_cuda or steps.numel() < R // 2 or steps.element_size() != 8 or steps.is_floating_point()
+                or not steps.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "Rope")
         self.steps, self.R, self.layout, self.gain = steps, R, layout, gain
         self._desc = exq_rope_params(steps.data_ptr(), R, layout, gain)
@@ -468,12 +469,12 @@ def rope_table(R: int, layout: int = ROPE_HALF, device="cuda", **freqs) -> Rope:
 
 
 def _rows(x, where: str, D: Optional[int] = None, heads: Optional[int] = None, tokens: Optional[int] = None):
-    """Descriptor of fp16 [tokens, heads, D] with a contiguous last axis."""
+    """Descriptor of fp16 [tokens, heads, D] on the GPU with a contiguous last axis."""
     import torch
     t, h, d = x.shape
     st, sh, sd = x.stride()
-    if (x.dtype != torch.float16 or (sd != 1 and d > 1) or (D is not None and d != D) or (heads is not None and h != heads)
-            or (tokens is not None and t < tokens)):
+    if (not x.is_cuda or x.dtype != torch.float16 or (sd != 1 and d > 1) or (D is not None and d != D)
+            or (heads is not None and h != heads) or (tokens is not None and t < tokens)):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     return exq_rows(x.data_ptr(), st, sh)
 
@@ -485,7 +486,7 @@ def exq_rope(x, pos, rope: Rope, out=None, grad: bool = False, stream=None):
     T, H, D = x.shape
     if out is None:
         out = torch.empty(T, H, D, dtype=torch.float16, device=x.device)
-    if pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
+    if not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_rope")
     xr, yr = _rows(x, "exq_rope"), _rows(out, "exq_rope", D, H, T)
     _check(_lib.exq_rope(ctypes.byref(rope._desc), ctypes.byref(xr), T, H, D, pos.data_ptr(), ctypes.byref(yr), int(grad),
@@ -504,11 +505,13 @@ class KVCache:
         shape = k_codes.shape
         L, P, H, S, W = shape
         quantised = bits != 16
-        if (k_codes.dtype != torch.int32 or v_codes.dtype != torch.int32 or v_codes.shape != shape or W * 32 % bits
+        if (not k_codes.is_cuda or not v_codes.is_cuda or k_codes.dtype != torch.int32 or v_codes.dtype != torch.int32
+                or v_codes.shape != shape or W * 32 % bits
                 or not k_codes.is_contiguous() or not v_codes.is_contiguous()
                 or (k_scales is not None) != quantised or (v_scales is not None) != quantised):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
-        if quantised and (k_scales.dtype != torch.float16 or v_scales.dtype != torch.float16
+        if quantised and (not k_scales.is_cuda or not v_scales.is_cuda
+                          or k_scales.dtype != torch.float16 or v_scales.dtype != torch.float16
                           or k_scales.shape != shape[:4] or v_scales.shape != shape[:4]
                           or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
@@ -536,7 +539,8 @@ class KVBatch:
         B, pages = page_table.shape
         import torch
         i32 = torch.int32
-        if (q_start.dtype != i32 or kv_len.dtype != i32 or page_table.dtype != i32 or q_start.shape != (B + 1,)
+        if (not (q_start.is_cuda and kv_len.is_cuda and page_table.is_cuda) or q_start.dtype != i32
+                or kv_len.dtype != i32 or page_table.dtype != i32 or q_start.shape != (B + 1,)
                 or kv_len.shape != (B,) or not q_start.is_contiguous() or not kv_len.is_contiguous()
                 or not page_table.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
@@ -569,7 +573,7 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
         qp, op = ctypes.byref(_rows(q, where, D, None, T)), ctypes.byref(_rows(q_out, where, D, heads, T))
-    if pos is not None and (pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
+    if pos is not None and (not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_kv_append(ctypes.byref(cache._desc), layer, ctypes.byref(batch.desc(T)), ctypes.byref(kr),
                               ctypes.byref(vr), None if rope is None else ctypes.byref(rope._desc),
@@ -585,7 +589,8 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
                    window: int = 0, lse=None, layer: int = 0, workspace=None, stream=None):
     """Attention of the new tokens' q, fp16 [tokens, heads, D], over the cached tokens of their sequences, the new ones
     among them (exq_kv_append first). scale: 1 / sqrt(D) unless given; lse: fp32 [tokens, heads] to fill, or None.
-    Without ``workspace`` the zero-filled one of the device that exq_gemv uses too is taken: for calls on one stream."""
+    Without ``workspace`` the zero-filled one of the device that exq_gemv uses too is taken: for calls on one stream. A
+    call that a graph captures needs one of its own, for as long as the graph is replayed."""
     import torch
     where = "exq_paged_attn"
     T, H, D = q.shape
@@ -596,11 +601,15 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
     qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
+    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     c, b = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T))
     if workspace is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise ExqError(EXQ_ERR_INVALID_ARG, where)
         workspace = _shared_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)))
+    elif not workspace.is_cuda:
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_paged_attn(c, layer, b, ctypes.byref(qr), H, D ** -0.5 if scale is None else scale, int(causal), window,
                                ctypes.byref(orow), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
@@ -610,7 +619,7 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
 def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
     """Copies pages pairs int32 [n, 2] of (src, dst) on the GPU, in every layer."""
     import torch
-    if pairs.dtype != torch.int32 or not pairs.is_contiguous() or pairs.numel() % 2:
+    if not pairs.is_cuda or pairs.dtype != torch.int32 or not pairs.is_contiguous() or pairs.numel() % 2:
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_kv_copy_pages")
     _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2, _stream_ptr(stream)),
            "exq_kv_copy_pages")

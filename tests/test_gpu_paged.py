@@ -483,3 +483,17 @@ def test_attention_of_many_short_and_empty_sequences(env):
     for new in (1, 3):
         _check_attention(env, (4, 64, 16, 1, 6, lens, [min(new, n) for n in lens], True, 0), seed=3)
     _check_attention(env, (16, 64, 16, 1, 6, [n for n in lens[:60]], [min(9, n) for n in lens[:60]], True, 0), seed=3)
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64), (16, 64)])
+def test_attention_of_a_prompt_chunk_among_single_tokens(env, bits, D):
+    # every sequence is given as many blocks of rows as the longest one needs, and has one or none
+    lens, new = [1, 40, 0, 700, 5, 0, 90, 33], [1, 1, 0, 650, 2, 0, 1, 33]
+    for causal in (True, False):
+        _check_attention(env, (bits, D, 32, 1, 4, lens, new, causal, 0), seed=D)
+
+
+@pytest.mark.parametrize("new", [5, 60])
+def test_attention_in_the_longest_window(env, new):
+    # a window no position reaches, beside more new tokens than cached ones: positions below zero
+    _check_attention(env, (4, 64, 16, 1, 2, [2, new, 45], [5, new, 1], True, 2**31 - 1), seed=4)

@@ -242,3 +242,17 @@ def test_copy_pages_validates_on_host(exq):
         assert call(cache=kw) == exq.EXQ_ERR_INVALID_ARG, kw
     assert call(pairs=None) == exq.EXQ_ERR_INVALID_ARG and call(pairs=0x1002) == exq.EXQ_ERR_INVALID_ARG
     assert call(n=-1) == exq.EXQ_ERR_INVALID_ARG and call(n=0, pairs=None) == exq.EXQ_OK
+
+
+def test_binding_refuses_host_tensors(exq):
+    # a tensor that is not on the GPU is an error on the host, before any launch
+    import torch
+    i32, f16 = torch.int32, torch.float16
+    z = lambda *s, dtype=i32: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    for call in (lambda: exq.Rope(z(32, dtype=torch.int64), 64), lambda: exq.KVBatch(z(2), z(1), z(1, 4), 1, 64),
+                 lambda: exq.KVCache(z(1, 4, 2, 16, 16), z(1, 4, 2, 16, 16), z(1, 4, 2, 16, dtype=f16), z(1, 4, 2, 16, dtype=f16), 4),
+                 lambda: exq.exq_rope(z(1, 2, 64, dtype=f16), z(1), None), lambda: exq.exq_kv_copy_pages(None, z(2, 2)),
+                 lambda: exq.kv_cache(1, 4, 2, 16, 128, 4, device="cpu")):
+        with pytest.raises(exq.ExqError) as e:
+            call()
+        assert e.value.status == exq.EXQ_ERR_INVALID_ARG

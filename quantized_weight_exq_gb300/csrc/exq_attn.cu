@@ -27,28 +27,49 @@ unsigned* error_word(int dev) {
 
 constexpr int kWaitLimit = 1 << 22;  // try_wait rounds before giving up
 
-// More query rows a KV head than these go to the tensor-memory kernel, whose
-// units have 256 (128) of them; fewer to the packed-code kernel, which reads
-// the cache again for every 16 (8). Measured on 8 sequences of up to 4000
-// tokens, packed-code against tensor-memory kernel, us: D = 128, Q4: 31 / 39
-// at 32 rows, 42 / 42 at 40, 45 / 40 at 64; fp16: 63 / 35 at 32; D = 64, Q4:
-// 22 / 27 at 64; D = 256, Q4: 40 / 36 at 32.
-bool many_rows(const exq_kv_cache& c, long long rows) {
-  return rows > (c.bits == 16 || c.D == 256 ? 16 : c.D == 64 ? 64 : 32);
-}
+// Sequences of more query rows a KV head than these go to the tensor-memory
+// kernel, whose units have 256 (128) of them; those of fewer to the
+// packed-code kernel, which reads the cache again for every 16 (8). Measured
+// on 8 sequences of up to 4000 tokens, packed-code against tensor-memory
+// kernel, us: D = 128, Q4: 31 / 39 at 32 rows, 42 / 42 at 40, 45 / 40 at 64;
+// fp16: 63 / 35 at 32; D = 64, Q4: 22 / 27 at 64; D = 256, Q4: 40 / 36 at 32.
+int few_rows(const exq_kv_cache& c) { return c.bits == 16 || c.D == 256 ? 16 : c.D == 64 ? 64 : 32; }
 
-// Rows a KV head of one sequence at most.
-long long most_rows(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads) {
-  return static_cast<long long>(std::min(b.max_q_len, b.n_tokens)) * (n_heads / c.n_kv_heads);
+// The launches of a call, by the host's bounds.
+struct Plan {
+  long long rows;             // rows a KV head of one sequence at most
+  int few;                    // the limit of the packed-code kernel
+  bool split, chunk;
+  int split_rows, chunk_rows; // rows of their units
+};
+
+Plan plan_of(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads) {
+  const int group = n_heads / c.n_kv_heads;
+  Plan p{};
+  p.rows = static_cast<long long>(std::min(b.max_q_len, b.n_tokens)) * group;
+  p.few = few_rows(c);
+  p.chunk = p.rows > p.few;
+  // Sequences of both kinds, as far as the host can tell: each launch passes
+  // over the other's. A chunk of 2048 tokens with 63 single tokens over 4000
+  // cached (Q4, 8 KV heads): 265 us, 423 with all of them in the
+  // tensor-memory kernel; with 31 of 32 KV heads: 225 us, 583. Prompts of mixed
+  // lengths pay 4 us for the second launch.
+  const bool mixed = p.chunk && b.n_tokens < static_cast<long long>(b.n_seqs) * b.max_q_len && b.n_seqs > 1;
+  p.split = !p.chunk || mixed;
+  // beside prompt chunks the short sequences are mostly single tokens (units
+  // of 16 rows there: 305 and 298 us)
+  p.split_rows = split::rows_of(c.D, mixed ? group : p.rows);
+  p.chunk_rows = chunk::rows_of(c.D);
+  return p;
 }
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms) {
-  const long long all = most_rows(c, b, n_heads);
-  const int rows = many_rows(c, all) ? chunk::rows_of(c.D) : split::rows_of(c.D, all);
-  const size_t ctas = std::min(many_rows(c, all) ? sms : 4 * sms, kAttnMaxCtas);
-  return kAttnCounterBytes + ctas * 2 * rows * (c.D + 2) * sizeof(float);
+  const Plan p = plan_of(c, b, n_heads);
+  const size_t split = p.split ? static_cast<size_t>(std::min(4 * sms, kAttnMaxCtas)) * p.split_rows : 0;
+  const size_t chunk = p.chunk ? static_cast<size_t>(std::min(sms, kAttnMaxCtas)) * p.chunk_rows : 0;
+  return kAttnCounterBytes + std::max(split, chunk) * 2 * (c.D + 2) * sizeof(float);
 }
 
 exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream) {
@@ -90,30 +111,34 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   const int starve = testing_starve_rounds();
   a.wait_limit = starve > 0 ? starve : kWaitLimit;
   a.starve = starve > 0 ? 1 : 0;
-  const long long rows = most_rows(c, b, call.n_heads);
-  const bool many = many_rows(c, rows);
-  const int per = many ? chunk::rows_of(c.D) : split::rows_of(c.D, rows);
-  const long long blocks = (rows + per - 1) / per;
-  if (rows > 0x7FFFFF00ll || blocks * b.n_seqs > 0x7FFFFF00ll) return EXQ_ERR_UNSUPPORTED;  // 32-bit row and block numbers
-  if (blocks == 0) return EXQ_OK;
-  a.row_blocks = static_cast<int>(blocks);
-  // A unit's queries, joins and stores take about as long as these many tiles
-  // (32 ragged sequences Q4: 61 us at 0, 45 at 4 to 8; prompts of 3500 tokens
-  // in a window: 360 us at 0, 245 at 12). Two tiles a CTA at least: 10 us for
-  // one sequence of 500 tokens, 15 at ten.
-  a.unit_cost = many ? 12 : 6;
-  a.min_tiles = 2;
-  if (many) switch (c.bits) {
-      case 4: return launch_attn_chunk4(call, a, sms, stream);
-      case 6: return launch_attn_chunk6(call, a, sms, stream);
-      case 8: return launch_attn_chunk8(call, a, sms, stream);
-      default: return launch_attn_chunk16(call, a, sms, stream);
-    }
+  const Plan plan = plan_of(c, b, call.n_heads);
+  if (plan.rows > 0x7FFFFF00ll || plan.rows / 8 * b.n_seqs > 0x7FFFFF00ll)
+    return EXQ_ERR_UNSUPPORTED;  // row and block numbers have 32 bits
+  a.min_tiles = 2;  // 10 us for one sequence of 500 tokens, 15 at ten
+  // What a unit's queries, joins and stores take, in tiles: packed-code kernel,
+  // 32 ragged sequences Q4: 61 us at 0, 45 at 4 to 8; tensor-memory kernel,
+  // prompts of 3500 tokens in a window: 360 us at 0, 245 at 12.
+  if (plan.chunk) {
+    a.rows_above = plan.split ? plan.few : 0;
+    a.rows_upto = static_cast<int>(plan.rows);
+    a.row_blocks = static_cast<int>((plan.rows + plan.chunk_rows - 1) / plan.chunk_rows);
+    a.unit_cost = 12;
+    const exq_status st = c.bits == 4   ? launch_attn_chunk4(call, a, sms, stream)
+                          : c.bits == 6 ? launch_attn_chunk6(call, a, sms, stream)
+                          : c.bits == 8 ? launch_attn_chunk8(call, a, sms, stream)
+                                        : launch_attn_chunk16(call, a, sms, stream);
+    if (st != EXQ_OK || !plan.split) return st;
+  }
+  a.rows_above = 0;
+  a.rows_upto = static_cast<int>(std::min<long long>(plan.rows, plan.few));
+  a.row_blocks = (a.rows_upto + plan.split_rows - 1) / plan.split_rows;
+  a.unit_cost = 6;
+  if (a.row_blocks == 0) return EXQ_OK;
   switch (c.bits) {
-    case 4: return launch_attn_split4(call, a, sms, stream);
-    case 6: return launch_attn_split6(call, a, sms, stream);
-    case 8: return launch_attn_split8(call, a, sms, stream);
-    default: return launch_attn_split16(call, a, sms, stream);
+    case 4: return launch_attn_split4(call, a, plan.split_rows, sms, stream);
+    case 6: return launch_attn_split6(call, a, plan.split_rows, sms, stream);
+    case 8: return launch_attn_split8(call, a, plan.split_rows, sms, stream);
+    default: return launch_attn_split16(call, a, plan.split_rows, sms, stream);
   }
 }
 

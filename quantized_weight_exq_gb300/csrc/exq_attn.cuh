@@ -39,7 +39,8 @@ struct AttnArgs {
   float scale_log2;           // scale * log2(e)
   int causal, window;
   float* lse;
-  int row_blocks;             // blocks of rows a sequence may need (host bound)
+  int rows_above, rows_upto;  // the launch serves sequences of rows_above < rows <= rows_upto a KV head
+  int row_blocks;             // blocks of rows such a sequence may need (host bound)
   int unit_cost;              // what a unit costs beside its tiles, in tiles
   int min_tiles;              // fewest tiles worth a CTA
   unsigned* counters;         // [CTAs], zero between calls
@@ -73,8 +74,9 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnArgs& a, int pair) {
     atomicOr(a.err, kDevErrBadPage);
     return u;
   }
+  const int all = u.n * a.group;
   u.r0 = rb * ROWS;
-  u.rows = min(ROWS, u.n * a.group - u.r0);
+  u.rows = all > a.rows_above && all <= a.rows_upto ? min(ROWS, all - u.r0) : 0;
   if (u.rows <= 0) {
     u.rows = 0;
     return u;

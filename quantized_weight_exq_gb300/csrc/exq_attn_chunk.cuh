@@ -970,7 +970,7 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
 }
 
 template <int B>
-exq_status launch_bits(const AttnCall& call, AttnArgs& a, int sms, cudaStream_t stream) {
+exq_status launch_bits(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t stream) {
   switch (call.cache->D) {
     case 64: return launch<B, 64>(call, a, sms, stream);
     case 128: return launch<B, 128>(call, a, sms, stream);
@@ -982,9 +982,9 @@ inline int rows_of(int D) { return D == 256 ? 128 : 256; }
 
 }  // namespace chunk
 
-exq_status launch_attn_chunk4(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_chunk6(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_chunk8(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_chunk16(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_chunk4(const AttnCall& c, const AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_chunk6(const AttnCall& c, const AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_chunk8(const AttnCall& c, const AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_chunk16(const AttnCall& c, const AttnArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace exq

@@ -3,7 +3,7 @@
 
 namespace exq {
 
-exq_status launch_attn_chunk6(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream) {
+exq_status launch_attn_chunk6(const AttnCall& c, const AttnArgs& a, int sms, cudaStream_t stream) {
   return chunk::launch_bits<6>(c, a, sms, stream);
 }
 

@@ -776,8 +776,8 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
 }
 
 template <int B>
-exq_status launch_bits(const AttnCall& call, AttnArgs& a, int sms, cudaStream_t stream) {
-  const bool one = static_cast<long long>(call.batch->max_q_len) * a.group <= 8;
+exq_status launch_bits(const AttnCall& call, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream) {
+  const bool one = unit_rows == 8;
   switch (call.cache->D) {
     case 64: return one ? launch<B, 64, 1>(call, a, sms, stream) : launch<B, 64, 2>(call, a, sms, stream);
     case 128: return one ? launch<B, 128, 1>(call, a, sms, stream) : launch<B, 128, 2>(call, a, sms, stream);
@@ -785,14 +785,14 @@ exq_status launch_bits(const AttnCall& call, AttnArgs& a, int sms, cudaStream_t 
   }
 }
 
-// rows of a unit, by the same rule
+// unit_rows for sequences of `rows` rows
 inline int rows_of(int D, long long rows) { return D == 256 || rows <= 8 ? 8 : 16; }
 
 }  // namespace split
 
-exq_status launch_attn_split4(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_split6(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_split8(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-exq_status launch_attn_split16(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
+exq_status launch_attn_split4(const AttnCall& c, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream);
+exq_status launch_attn_split6(const AttnCall& c, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream);
+exq_status launch_attn_split8(const AttnCall& c, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream);
+exq_status launch_attn_split16(const AttnCall& c, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream);
 
 }  // namespace exq

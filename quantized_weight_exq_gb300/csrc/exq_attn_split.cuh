@@ -29,6 +29,11 @@
 // that fills a ring of stages by TMA: one box per page (or 64 tokens of it),
 // swizzled so that ldmatrix is free of bank conflicts, and the scales beside
 // it. Slots past the last token are masked in S, and V's (fp16) zeroed.
+//
+// 8 KV heads of 128, 8 query heads each: one sequence of 131072 tokens Q8 (273
+// MB) 66 us, 4.1 TB/s, 62 % of the copy rate; 32 ragged ones up to 8192
+// Q4 (152 MB) 44 us, half of it at the copy rate, the rest unpacking, starts
+// and joins; one of 500 tokens 10 us.
 #pragma once
 
 #include <algorithm>

@@ -31,7 +31,7 @@
 // it. Slots past the last token are masked in S, and V's (fp16) zeroed.
 //
 // 8 KV heads of 128, 8 query heads each: one sequence of 131072 tokens Q8 (273
-// MB) 66 us, 4.1 TB/s, 62 % of the copy rate; 32 ragged ones up to 8192
+// MB) 61 us, 4.5 TB/s, 67 % of the copy rate; 32 ragged ones up to 8192
 // Q4 (152 MB) 44 us, half of it at the copy rate, the rest unpacking, starts
 // and joins; one of 500 tokens 10 us.
 #pragma once
@@ -776,7 +776,12 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
   auto fn = attn_split_kernel<B, D, NT>;
   static std::once_flag once;
   std::call_once(once, [&] { cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
-  fn<<<std::min(sms * C::kCtas, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a);
+  // Units cut into more than 32 pieces take two CTAs an SM: fewer pieces to
+  // join (131072 tokens of 8 KV heads: Q8 61 us, 65 with three; Q4 48, 50). With
+  // 16 sequences' units instead two cost more than they gain (23 us against 22).
+  const long long units = static_cast<long long>(a.n_seqs) * a.row_blocks * a.n_kv_heads;
+  const int ctas = units * 32 < static_cast<long long>(sms) * C::kCtas ? std::min(C::kCtas, 2) : C::kCtas;
+  fn<<<std::min(sms * ctas, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 

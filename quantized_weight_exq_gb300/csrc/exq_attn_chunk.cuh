@@ -456,16 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = uniform(p.t1 - p.t0);
         const bool active = uniform(p.u.rows) > 128 * s;
         for (int j = 0; j < n && ok; ++j, ++g, r.next()) {
-          if (!active) {  // keeps the phases whole
-            ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
-            if (ok && lane == 0) mbar_arrive(pv_done(g));
-            continue;
-          }
           const uint32_t buf = uniform(g & 1);
-          if (!kQuant) ok = mbar_wait_warp(v_ready(g), phase4(g), abort_flag, a);
+          if (!kQuant && active) ok = mbar_wait_warp(v_ready(g), phase4(g), abort_flag, a);
           ok = ok && mbar_wait_warp(w_full(s, buf), (w_ph >> buf) & 1, abort_flag, a);
           w_ph ^= 1u << buf;
           if (!ok) break;
+          if (!active) {  // no rows: keeps the phases whole, and its softmax warps in step
+            if (lane == 0) mbar_arrive(pv_done(g));
+            continue;
+          }
           tc_after();
           const uint64_t vd = smem_desc(sb + C::kOffV + uniform(r.st) * C::kArray, T * 128);
 #pragma unroll
@@ -818,9 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_after();
         }
       } else if (works) {
-        // stays in step with the tiles, so that no phase is missed
+        // An M tile without rows: the warps say that they have seen each tile's
+        // scores, and the scores two tiles on wait for that by way of P V. A
+        // warp that only watched could fall four tiles behind, and wait for a
+        // phase that has gone by.
         const int n = p.t1 - p.t0;
-        for (int t = 0; t < n && ok; ++t, ++g) ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
+        for (int t = 0; t < n && ok; ++t, ++g) {
+          ok = mbar_wait_warp(s_full(g), phase4(g), abort_flag, a);
+          if (ok) mbar_arrive(w_full(s, g & 1));
+        }
       }
       // the statistics of the thread's row `lane` of the warp: slot lane / 8 of
       // the lanes from 4 (lane % 8)

@@ -530,3 +530,10 @@ def test_attention_of_both_kinds_in_a_graph(env, bits, D, kvh, heads):
             ref, _, spread, total = O.attention(qb, k, v, np.arange(L - n, L), scale)
             assert np.all(np.abs(_np(want[at:at + n]).astype(np.float64) - ref) <= _bound(ref, spread, total, qb, k, v, scale, L, D))
         at += n
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (16, 128), (8, 64)])
+def test_attention_of_units_with_and_without_a_second_tile_of_rows(env, bits, D):
+    # 200 and 90 rows a KV head in turn, several units a CTA: the second M tile has rows, has none, has some again
+    lens = [int(n) for n in np.random.default_rng(5).integers(100, 700, 24)]
+    _check_attention(env, (bits, D, 64, 8, 16, lens, [100 if b % 2 == 0 else 45 for b in range(24)], True, 0), seed=12)

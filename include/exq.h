@@ -518,8 +518,10 @@ size_t exq_paged_attn_workspace_size(const exq_kv_cache* cache, const exq_kv_bat
  *   out     rows of n_heads heads, fp16; must not overlap q
  *   lse     NULL or device fp32 [n_tokens, n_heads]: ln sum_t w_t
  * A row that sees nothing (an empty sequence, or more new tokens than
- * cached ones) gives zeros and an lse of -inf. Slots past a sequence's last
- * token may hold anything, NaN included. Scores, the softmax's maximum and
+ * cached ones), or whose scores are all -inf, gives zeros and an lse of -inf.
+ * One with a score of NaN or +inf gives NaN in both; the scores of a K group
+ * whose scale is not finite are NaN. Slots past a sequence's
+ * last token may hold anything, NaN included. Scores, the softmax's maximum and
  * sum and the output's sums are fp32; the weights are rounded to fp16 for
  * the matrix instructions (V's scales multiplied in before that rounding).
  *   workspace  at least exq_paged_attn_workspace_size() bytes, 256-byte

@@ -262,10 +262,21 @@ __device__ __forceinline__ void attn_row_of(const AttnArgs& a, const AttnPiece& 
   head = p.head * a.group + (rr - t * a.group);
 }
 
+// A K scale as it multiplies its group's products. An infinite one gives NaN,
+// as its values do: those of zero codes are NaN, the others infinities of both
+// signs.
+__device__ __forceinline__ float attn_key_scale(uint32_t half_bits) {
+  const float s = half_bits_to_float(half_bits);
+  return fmaf(s, 0.f, s);
+}
+
+// A sum of weights of 0 is that of a row that has seen nothing (yet). A NaN
+// score makes it NaN, which every step keeps: tests of it are `l != 0`, true
+// for NaN.
 __device__ __forceinline__ void attn_store_lse(const AttnArgs& a, int token, int head, float m, float l) {
   if (a.lse)
     a.lse[static_cast<long long>(token) * a.n_heads + head] =
-        l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, 0 for -inf
@@ -308,16 +319,16 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnPiece& p,
       for (int k = 0; k < kKeep; ++k) {
         float top = m[k];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = li[k][i] > 0.f ? fmaxf(top, mi[k][i]) : top;
+        for (int i = 0; i < kBatch; ++i) top = li[k][i] != 0.f ? fmaxf(top, mi[k][i]) : top;
         const float old = m[k] == -INFINITY ? 0.f : exp2_fast(m[k] - top);
         l[k] *= old;
         y[k].x *= old, y[k].y *= old, y[k].z *= old, y[k].w *= old;
         m[k] = top;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const float f = li[k][i] > 0.f ? exp2_fast(mi[k][i] - top) : 0.f;
-          l[k] += li[k][i] * f;
-          if (f > 0.f) {
+          if (li[k][i] != 0.f) {
+            const float f = exp2_fast(mi[k][i] - top);
+            l[k] += li[k][i] * f;
             y[k].x += v[k][i].x * f;
             y[k].y += v[k][i].y * f;
             y[k].z += v[k][i].z * f;
@@ -333,7 +344,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnPiece& p,
       const int r = e / kCols, col = e - r * kCols;
       int token, head;
       attn_row_of(a, p, r, token, head);
-      const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
+      const float inv = l[k] != 0.f ? 1.f / l[k] : 0.f;
       uint2 o;
       o.x = float_to_half_bits(y[k].x * inv) | (float_to_half_bits(y[k].y * inv) << 16);
       o.y = float_to_half_bits(y[k].z * inv) | (float_to_half_bits(y[k].w * inv) << 16);

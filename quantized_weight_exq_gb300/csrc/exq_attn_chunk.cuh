@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tid < T) {
               uint32_t bits = split::lds16(src + P::kArray + 2 * tid);
               if (tid >= keep) bits = 0;
-              scales[(2 * (g & 3) + which) * T + tid] = half_bits_to_float(bits) * (which ? 1.f : x.scale);
+              scales[(2 * (g & 3) + which) * T + tid] = which ? half_bits_to_float(bits) : attn_key_scale(bits) * x.scale;
               if (which) {
                 const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
                 if (lane == 0) exps[2 * (g & 3) + (tid >> 5)] = e;
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int token = 0, head = 0;
         if (has) attn_row_of(a, p, row, token, head);
         float* slot = p.whole ? nullptr : attn_slot(a, blockIdx.x, static_cast<int>(blockIdx.x) == c0, C::kFloats);
-        const float inv = !p.whole ? 1.f : row_l > 0.f ? 1.f / row_l : 0.f;
+        const float inv = !p.whole ? 1.f : row_l != 0.f ? 1.f / row_l : 0.f;
         // where the lane's row goes
         const unsigned long long out =
             p.whole ? reinterpret_cast<unsigned long long>(a.out.data + token * a.out.token_stride + head * a.out.head_stride)
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) {
             // 0 4 1 5 2 6 3 7 back to the dims' order
             const int at = kPairs ? (i & ~7) + 2 * (i & 3) + ((i >> 2) & 1) : i;
-            y[i] = row_l > 0.f ? __uint_as_float(r[c & 1][at]) * inv : 0.f;
+            y[i] = row_l != 0.f ? __uint_as_float(r[c & 1][at]) * inv : 0.f;
           }
           if (whole) {
 #pragma unroll

@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             float ks = a.scale_log2;
             vs[h][e] = 1.f;
             if constexpr (kQuant) {
-              ks *= half_bits_to_float(lds16(sbase + 2 * tok));
+              ks *= attn_key_scale(lds16(sbase + 2 * tok));
               uint32_t v = lds16(sbase + C::kScale + 2 * tok);
               if (at >= end) v = 0;  // whatever the slots past the end hold
               vtop = max(vtop, v);
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
         if (g == 0) {
-          stat_m[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i] > 0.f ? -nbase[nt][i] : -INFINITY;
+          stat_m[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i] != 0.f ? -nbase[nt][i] : -INFINITY;
           stat_l[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i];
         }
       }
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, stat_m[w * C::kRows + 8 * nt + 2 * c + i]);
-        f[nt][i] = l[nt][i] > 0.f ? exp2_fast(-nbase[nt][i] - mm) : 0.f;
+        f[nt][i] = l[nt][i] != 0.f ? exp2_fast(-nbase[nt][i] - mm) : 0.f;
       }
     const auto put = [&](float* region, bool add) {
 #pragma unroll
@@ -705,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       for (int w = 0; w < kConsumers; ++w) mm = fmaxf(mm, stat_m[w * C::kRows + r]);
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) {
-        const float mw = stat_m[w * C::kRows + r];
-        if (mw != -INFINITY) ll += stat_l[w * C::kRows + r] * exp2_fast(mw - mm);
+        const float lw = stat_l[w * C::kRows + r];
+        if (lw != 0.f) ll += lw * exp2_fast(stat_m[w * C::kRows + r] - mm);
       }
       float4 y = *reinterpret_cast<const float4*>(merge + r * D + 4 * col);
 #pragma unroll
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       if (p.whole) {
         int token, head;
         attn_row_of(a, p, r, token, head);
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = ll != 0.f ? 1.f / ll : 0.f;
         uint2 out;
         out.x = float_to_half_bits(y.x * inv) | (float_to_half_bits(y.y * inv) << 16);
         out.y = float_to_half_bits(y.z * inv) | (float_to_half_bits(y.w * inv) << 16);

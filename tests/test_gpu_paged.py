@@ -78,6 +78,15 @@ class Case:
         self.scales[i][self.layer, pages, :, slots] = s.reshape(n, self.KH)
         return O.kv_values(w, s, self.bits, self.D).reshape(n, self.KH, self.D)
 
+    def read(self, b, i):
+        """What sequence b's cached tokens of K (i = 0) or V (1) stand for, from the pool as it is: float64 [n, KV heads, D]."""
+        pos = np.arange(self.lens[b])
+        at = self.layer, self.table[b, pos // self.page], slice(None), pos % self.page
+        s = self.scales[i] if self.scales[i] is None else self.scales[i][at].reshape(-1)
+        with np.errstate(all="ignore"):
+            v = O.kv_values(self.words[i][at].reshape(-1, self.words[i].shape[-1]), s, self.bits, self.D)
+        return v.reshape(-1, self.KH, self.D)
+
     def cache(self):
         t = self.torch
         words = [t.from_numpy(w.view(np.int32)).cuda() for w in self.words]
@@ -537,3 +546,81 @@ def test_attention_of_units_with_and_without_a_second_tile_of_rows(env, bits, D)
     # 200 and 90 rows a KV head in turn, several units a CTA: the second M tile has rows, has none, has some again
     lens = [int(n) for n in np.random.default_rng(5).integers(100, 700, 24)]
     _check_attention(env, (bits, D, 64, 8, 16, lens, [100 if b % 2 == 0 else 45 for b in range(24)], True, 0), seed=12)
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+def _check_not_finite(env, case, spoil_cache=None, spoil_q=None, seed=0):
+    """A result that the definition leaves not finite is the same one here, and every other is as near as ever. spoil_cache(c)
+    may change words and scales of a filled case; spoil_q(q) some queries."""
+    exq, torch = env
+    bits, D, page, KH, H, lens, news, causal, window = case
+    c = Case(exq, torch, bits, D, page, KH, lens, news, seed=seed + D).fill()
+    q = c.rng.standard_normal((sum(news), H, D)).astype(np.float16)
+    if spoil_cache:
+        spoil_cache(c)
+    if spoil_q:
+        spoil_q(q)
+    lse = torch.full((sum(news), H), 7.0, device="cuda")
+    out = exq.exq_paged_attn(c.cache(), c.batch(), torch.from_numpy(q).cuda(), causal=causal, window=window, lse=lse)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    got, got_lse = _np(out).astype(np.float64), _np(lse).astype(np.float64)
+    scale, bad = float(np.float32(D ** -0.5)), 0
+    for b, (n, L) in enumerate(zip(news, lens)):
+        r = slice(c.start[b], c.start[b + 1])
+        k, v = (c.read(b, i) for i in range(2))
+        qb = q[r].astype(np.float64)
+        with np.errstate(all="ignore"):
+            ref, ref_lse, spread, total = O.attention(qb, k, v, np.arange(L - n, L), scale, causal, window)
+        finite = lambda a: np.where(np.isfinite(a), a, 0.0)  # noqa: E731
+        tol = _bound(finite(ref), finite(spread), np.maximum(finite(total), 1.0), finite(qb), finite(k), finite(v), scale, L, D)
+        ok = np.isfinite(ref)
+        assert np.array_equal(np.isnan(got[r]), np.isnan(ref)), b
+        assert np.array_equal(got[r][np.isinf(ref)], ref[np.isinf(ref)]), b
+        off = np.abs(got[r][ok] - ref[ok])
+        assert np.all(off <= tol[ok]), (b, off.max())
+        assert np.array_equal(np.isnan(got_lse[r]), np.isnan(ref_lse))
+        assert np.array_equal(np.isneginf(got_lse[r]), np.isneginf(ref_lse))
+        there = np.isfinite(ref_lse)
+        big = np.abs(finite(qb)).sum(-1).max() * np.abs(finite(k)).max() * scale   # as in _check_attention
+        lse_tol = (D + 8) * 2.0 ** -24 * big + L * 2.0 ** -23 + 2.0 ** -20 * np.abs(ref_lse[there]) + 2.0 ** -20
+        assert np.all(np.abs(got_lse[r][there] - ref_lse[there]) <= lse_tol)
+        bad += (~ok).sum()
+    return bad
+
+
+def _set_key(c, i, b, pos, head, value):
+    """K's (i = 0) or V's (1) group of a cached token: its scale (codes), or one fp16 value."""
+    page, slot = c.table[b, pos // c.page], pos % c.page
+    if c.bits == 16:
+        c.words[i].view(np.float16)[c.layer, page, head, slot, 3] = value
+    else:
+        c.scales[i].view(np.float16)[c.layer, page, head, slot] = value
+
+
+# one token and chunks of new ones; sequences of one CTA and of many
+NOT_FINITE = [(4, 128, 64, 2, 16, [300, 9000, 40], [1, 1, 1], True, 0), (16, 128, 16, 1, 4, [200, 9000], [2, 2], True, 0),
+              (8, 64, 32, 2, 8, [90, 6000], [1, 1], True, 0), (6, 256, 16, 1, 4, [70, 5000], [1, 1], True, 0),
+              (4, 128, 64, 1, 8, [150, 2500], [45, 45], True, 0), (16, 64, 16, 2, 8, [140, 2500], [60, 33], True, 0),
+              (8, 256, 64, 1, 8, [100, 1500], [20, 40], True, 0), (6, 128, 32, 1, 8, [150, 1200], [50, 45], True, 0)]
+NOT_FINITE_IDS = ["-".join(map(str, (*c[:5], max(c[6])))) for c in NOT_FINITE]
+
+
+@pytest.mark.parametrize("case", NOT_FINITE, ids=NOT_FINITE_IDS)
+def test_attention_of_queries_that_are_not_finite(env, case):
+    def spoil(q):
+        q[0, 1, 5] = np.nan
+        q[-1, 2, 7] = np.inf
+        q[-1, 0, :] = 60000.0            # finite queries beside them
+    assert _check_not_finite(env, case, spoil_q=spoil) > 0
+
+
+@pytest.mark.parametrize("value", [np.inf, np.nan])
+@pytest.mark.parametrize("case", NOT_FINITE, ids=NOT_FINITE_IDS)
+def test_attention_of_seen_keys_that_are_not_finite(env, case, value):
+    # an infinite score among finite ones: its weight is NaN, or 0 where it is negative; whichever piece of a unit holds it
+    def spoil(c):
+        for b, L in enumerate(c.lens):
+            _set_key(c, 0, b, min(37, L - 1), 0, value)
+            _set_key(c, 0, b, L - 1, c.KH - 1, value)
+    assert _check_not_finite(env, case, spoil_cache=spoil) > 0

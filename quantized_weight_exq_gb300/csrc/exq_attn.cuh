@@ -326,9 +326,9 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnPiece& p,
         m[k] = top;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          if (li[k][i] != 0.f) {
-            const float f = exp2_fast(mi[k][i] - top);
-            l[k] += li[k][i] * f;
+          const float f = li[k][i] != 0.f ? exp2_fast(mi[k][i] - top) : 0.f;
+          l[k] += li[k][i] * f;
+          if (f != 0.f) {
             y[k].x += v[k][i].x * f;
             y[k].y += v[k][i].y * f;
             y[k].z += v[k][i].z * f;

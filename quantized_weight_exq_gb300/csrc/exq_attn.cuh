@@ -270,6 +270,30 @@ __device__ __forceinline__ float attn_key_scale(uint32_t half_bits) {
   return fmaf(s, 0.f, s);
 }
 
+// References of the softmax. Weights are multiplied by V's scales and rounded
+// to fp16 for the matrix instructions, so what has to stay in fp16's normal
+// range is that product: a row's reference is the largest score plus the
+// exponent of its token's V scale (0 for fp16 pages), over the tokens that the
+// row sees, and is raised where one exceeds it by more than attn_lag. Weights
+// up to 2^lag have the same relative precision; those whose product falls
+// below 2^-14 lose some, 2^-25 of the row's largest product at most each. Most
+// tiles need no maximum over lanes: one vote, on the lane's largest score plus
+// the largest exponent of all its tokens, says that no reference moves.
+// (Reference and exponent apart, with the exponent of the largest V scale met,
+// let a large scale that a row does not see, or hardly weighs, push the row's
+// other products below fp16's range.)
+template <int B>
+__device__ __forceinline__ constexpr float attn_lag() {
+  return B == 16 ? 8.f : 12.f;
+}
+
+// The exponent of a V scale (an fp16 value): 2^e <= |v| < 2^(e + 1), within
+// fp16's range also for zeros and infinities.
+__device__ __forceinline__ float attn_value_exponent(float v) {
+  const int e = static_cast<int>((__float_as_uint(v) >> 23) & 255u) - 127;
+  return static_cast<float>(max(-24, min(16, e)));
+}
+
 // A sum of weights of 0 is that of a row that has seen nothing (yet). A NaN
 // score makes it NaN, which every step keeps: tests of it are `l != 0`, true
 // for NaN.

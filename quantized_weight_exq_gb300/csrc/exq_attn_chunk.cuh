@@ -12,9 +12,8 @@
 //   warps 0-7   softmax: S once into registers; the weights go back as fp16
 //               over S, the A operand of P V; the sums of weights; the
 //               epilogue. A row's reference is raised, and O rescaled, only
-//               when a score exceeds it by more than 8 (in log2): weights up
-//               to 2^8 have the same relative precision in fp16. So most
-//               tiles need no row maximum over lanes, one vote does.
+//               when a score exceeds it by more than attn_lag. So most tiles
+//               need no row maximum over lanes, one vote does.
 //   warps 8-11  dequantisers: packed tiles in shared memory become the
 //               integers (u - z), exact in fp16, in the MMA's 128-byte
 //               swizzle, once for all rows of the unit. The groups' scales
@@ -671,10 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (attn_next<C::kRows, T>(a, state)) {
       const bool active = works && s * 128 < p.u.rows;    // warp-uniform, the same for the stream's warps
-      float m[4], nbase[4];                               // references, and -(m - (15 - kexp)), see below
+      float m[4], nbase[4];                               // references, and -m (0 before there is one)
       uint64_t sum[4];                                    // of weights, even and odd columns
       int lo[4], hi[4];
-      int kexp = 15;
 #pragma unroll
       for (int k = 0; k < 4; ++k) m[k] = -INFINITY, nbase[k] = 0.f, sum[k] = 0;
       if (active) {
@@ -731,35 +729,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           if (t * T < all_lo || (t + 1) * T > all_hi) exponents(std::true_type{});
           else exponents(std::false_type{});
-          // ---- raise the references where a score exceeds one by more than
-          // 8, or V's scales the exponent in use by more than 2^4: V's scales
-          // are near 2^(kexp - 15), and weights 2^(15 - kexp) times larger
-          // keep the products with them near 1
-          int tile_e = 15;
+          // ---- references, see attn_lag
+          constexpr float kLag = attn_lag<B>();
+          float tile_e = 0.f;  // the largest exponent of the tile's V scales
           if constexpr (kQuant) {
             const int2 e2 = *reinterpret_cast<const int2*>(exps + 2 * (g & 3));
-            tile_e = max(e2.x, e2.y);
+            tile_e = static_cast<float>(max(e2.x, e2.y) - 15);
           }
-          const bool new_e = kQuant && (t == t0 || tile_e > kexp + 4);
-          if (__any_sync(0xffffffffu, !begun || new_e || top > 8.f + static_cast<float>(15 - kexp))) {
+          if (__any_sync(0xffffffffu, !begun || top + tile_e > kLag)) {
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < T / 8; ++j)
+            for (int j = 0; j < T / 8; ++j) {
+              float2 ex;
+              if constexpr (kQuant) {
+                const float2 v2 = *reinterpret_cast<const float2*>(sv + 8 * j);
+                ex = make_float2(attn_value_exponent(v2.x), attn_value_exponent(v2.y));
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
-                mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1])));
+                float2 u = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                if constexpr (kQuant) u.x += ex.x, u.y += ex.y;
+                mx[k] = fmaxf(mx[k], fmaxf(u.x, u.y));
               }
-            if (new_e) kexp = tile_e;
+            }
             float f[4];
             bool any = false;
             begun = true;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2)) - nbase[k];  // the largest score
-              const float m1 = mx[k] > m[k] + 8.f ? mx[k] : m[k];  // m = -inf: the score, where anything is seen
-              const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2)) - nbase[k];  // the largest score and exponent
+              const float m1 = mx[k] > m[k] + kLag ? mx[k] : m[k];  // m = -inf: mx, where anything is seen
+              const float nb1 = m1 == -INFINITY ? 0.f : -m1;
               const bool moved = nb1 != nbase[k] && m[k] != -INFINITY;  // else the row's O is zeros, or not begun
               f[k] = moved ? exp2_fast(nb1 - nbase[k]) : 1.f;
               any |= moved;

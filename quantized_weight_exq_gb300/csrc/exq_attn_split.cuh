@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
     float o[NT][kSteps][4], l[NT][2];
-    float m[NT][2], nbase[NT][2];  // the rows' references, and -(m - (15 - kexp)), see below
+    float m[NT][2], nbase[NT][2];  // the rows' references, and -m (0 before there is one)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -516,9 +516,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
-    int kexp = 15;        // V's scales are near 2^(kexp - 15)
-    bool begun = false;   // every row of the lane has a reference
-    bool started = false; // kexp is set
+    bool begun = false;            // every row of the lane has a reference
 
     for (int t = t0; t < t1; ++t, ++tile) {
       const int here = st;
@@ -583,19 +581,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
                 top = fmaxf(top, x);
               }
           }
-        // A row's reference is raised only where a score exceeds it by more
-        // than 8 (weights up to 2^8 have the same relative precision in fp16),
-        // and the exponent that stands for V's scales where one is 2^4 above
-        // it: weights are kept 2^(15 - kexp) larger, so that their products
-        // with V's scales stay in fp16's normal range. Most steps need no
-        // maximum over lanes, one vote does.
-        if (__any_sync(0xffffffffu, !begun || top > 8.f + static_cast<float>(15 - kexp) ||
-                                        (kQuant && static_cast<int>(vtop >> 10) > kexp + 4))) {
-          if constexpr (kQuant) {
-            const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, vtop) >> 10) & 31;
-            if (!started || e > kexp + 4) kexp = e;  // the same in all lanes
-            started = true;
-          }
+        // ---- references, see attn_lag
+        constexpr float kLag = attn_lag<B>();
+        const float ve = kQuant ? static_cast<float>(static_cast<int>(vtop >> 10) - 15) : 0.f;
+        if (__any_sync(0xffffffffu, !begun || top + ve > kLag)) {
           begun = true;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -604,12 +593,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             for (int i = 0; i < 2; ++i) {
               float mx = -INFINITY;
 #pragma unroll
-              for (int h = 0; h < kSlices; ++h) mx = fmaxf(mx, fmaxf(s[h][nt][i], s[h][nt][i + 2]));
+              for (int h = 0; h < kSlices; ++h)
+                if constexpr (kQuant)
+                  mx = fmaxf(mx, fmaxf(s[h][nt][i] + attn_value_exponent(vs[h][0]),
+                                       s[h][nt][i + 2] + attn_value_exponent(vs[h][1])));
+                else
+                  mx = fmaxf(mx, fmaxf(s[h][nt][i], s[h][nt][i + 2]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              mx -= nbase[nt][i];  // the largest score
-              const float m1 = mx > m[nt][i] + 8.f ? mx : m[nt][i];  // m = -inf: the score, where anything is seen
-              const float nb1 = (m1 == -INFINITY ? 0.f : -m1) + static_cast<float>(15 - kexp);
+              mx -= nbase[nt][i];  // the largest score and exponent
+              const float m1 = mx > m[nt][i] + kLag ? mx : m[nt][i];  // m = -inf: mx, where anything is seen
+              const float nb1 = m1 == -INFINITY ? 0.f : -m1;
               const float d = nb1 - nbase[nt][i];
               f[i] = m[nt][i] == -INFINITY ? 1.f : exp2_fast(d);  // -inf: o and l are zeros
 #pragma unroll

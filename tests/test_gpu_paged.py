@@ -624,3 +624,51 @@ def test_attention_of_seen_keys_that_are_not_finite(env, case, value):
             _set_key(c, 0, b, min(37, L - 1), 0, value)
             _set_key(c, 0, b, L - 1, c.KH - 1, value)
     assert _check_not_finite(env, case, spoil_cache=spoil) > 0
+
+
+# ---------------------------------------------------------------- V of very different sizes
+
+def _bound_by_row(ref, spread, w, vs, bits, q, k, scale, D):
+    """_bound for one row, from what the row sees alone: w its weights (the largest is 1) and vs V's scales. Products below
+    fp16's normal range lose 2^-25 of the row's largest product each, times a code."""
+    n = w.size
+    score = (D + 8) * 2.0 ** -24 * np.abs(q).sum() * np.abs(k).max() * scale
+    tiny = n * 2.0 ** -25 * (w * vs).max() * 2.0 ** (bits - 1) / w.sum()
+    return 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2 * score + n * 2.0 ** -23) * spread + tiny + 2.0 ** -24
+
+
+@pytest.mark.parametrize("place", ["later", "before the window", "of no weight"])
+@pytest.mark.parametrize("bits,D,new", [(4, 128, 4), (8, 64, 8), (6, 256, 4), (4, 128, 60), (8, 64, 70), (6, 256, 40)])
+def test_attention_beside_values_of_another_size(env, bits, D, new, place):
+    # V of the tokens is about 2^-8, of one token 2^10: rows that do not see it, or whose weight of it is 2^-50 or less, are as
+    # near to their result as if it were not there
+    exq, torch = env
+    L, window = 210, 100 if place == "before the window" else 0
+    c = Case(exq, torch, bits, D, 16, 1, [L], [new], seed=bits + new).fill()
+    c.put(0, 1, (c.rng.standard_normal((L, 1, D)) * 2.0 ** -8).astype(np.float16), np.arange(L))
+    q = c.rng.standard_normal((new, 1, D)).astype(np.float16)
+    q[:] = q[:1] + np.float16(0.125) * q           # queries alike: one key far from all of them
+    at = np.array([{"later": L - 2, "before the window": L - new // 2 - window, "of no weight": 130}[place]])
+    c.put(0, 1, (c.rng.standard_normal((1, 1, D)) * 2.0 ** 10).astype(np.float16), at)
+    if place == "of no weight":
+        c.put(0, 0, (q[:1] * np.float16(-60 / (D ** -0.5 * (q[0].astype(np.float64) ** 2).sum()))).astype(np.float16), at)
+    out = _np(exq.exq_paged_attn(c.cache(), c.batch(), torch.from_numpy(q).cuda(), window=window)).astype(np.float64)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    k, v = c.read(0, 0)[:, 0], c.read(0, 1)[:, 0]
+    vs = c.scales[1].view(np.float16)[0, c.table[0, np.arange(L) // 16], 0, np.arange(L) % 16].astype(np.float64)
+    scale, clear = float(np.float32(D ** -0.5)), 0
+    for i in range(new):
+        pos = L - new + i
+        seen = np.arange(max(0, pos - window + 1) if window else 0, pos + 1)
+        qi = q[i, 0].astype(np.float64)
+        x = k[seen] @ qi * scale
+        w = np.exp(x - x.max())
+        if at[0] in seen:
+            if place != "of no weight":
+                continue                            # its own rows are its size
+            assert w[seen == at[0]] < 2.0 ** -50
+        ref, spread = w @ v[seen] / w.sum(), w @ np.abs(v[seen]) / w.sum()
+        tol = _bound_by_row(ref, spread, w, vs[seen], bits, qi, k[seen], scale, D)
+        assert np.all(np.abs(out[i, 0] - ref) <= tol), (i, np.abs(out[i, 0] - ref).max(), tol.max())
+        clear += 1
+    assert clear >= new // 2 - 2 and clear > 0

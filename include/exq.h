@@ -519,11 +519,14 @@ size_t exq_paged_attn_workspace_size(const exq_kv_cache* cache, const exq_kv_bat
  *   lse     NULL or device fp32 [n_tokens, n_heads]: ln sum_t w_t
  * A row that sees nothing (an empty sequence, or more new tokens than
  * cached ones), or whose scores are all -inf, gives zeros and an lse of -inf.
- * One with a score of NaN or +inf gives NaN in both; the scores of a K group
- * whose scale is not finite are NaN. Slots past a sequence's
- * last token may hold anything, NaN included. Scores, the softmax's maximum and
- * sum and the output's sums are fp32; the weights are rounded to fp16 for
- * the matrix instructions (V's scales multiplied in before that rounding).
+ * One with a score of NaN or +inf gives NaN in both; so does one that sees a
+ * token whose K or V group has a scale that is not finite. A value of fp16 V
+ * that is not finite gives results that are not finite (an infinity whose
+ * weight is below fp16's range gives NaN) in its dim of the rows that see it.
+ * What a row does not see does not reach it: other slots of the sequence's
+ * pages may hold anything, NaN included. Scores, the softmax's maximum and sum
+ * and the output's sums are fp32; the weights are rounded to fp16 for the
+ * matrix instructions (V's scales multiplied in before that rounding).
  *   workspace  at least exq_paged_attn_workspace_size() bytes, 256-byte
  *          aligned, its first 64 KB ZERO before the first use; a call that
  *          completes leaves them zero, and the counters exq_gemv keeps there

@@ -192,6 +192,7 @@ struct AttnState {
   long long at;          // next place of the share
   long long pair_start;
   int pair;
+  int number;            // of the piece, from 1
   AttnPiece p;
 };
 
@@ -201,6 +202,7 @@ __device__ __forceinline__ bool attn_begin(const AttnArgs& a, AttnState& st) {
   if ((threadIdx.x & 31) == 0) {
     st.s = s;
     st.at = s.begin;
+    st.number = 0;
     st.pair = s.pair;
     st.pair_start = s.pair_start;
   }
@@ -242,6 +244,7 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& a, AttnState& st) {
     st.at = at;
     st.pair = pair;
     st.pair_start = pair_start;
+    ++st.number;
     st.p = p;
   }
   __syncwarp();
@@ -262,12 +265,84 @@ __device__ __forceinline__ void attn_row_of(const AttnArgs& a, const AttnPiece& 
   head = p.head * a.group + (rr - t * a.group);
 }
 
+__device__ __forceinline__ bool attn_finite(uint32_t half_bits) { return (half_bits & 0x7C00u) != 0x7C00u; }
+
 // A K scale as it multiplies its group's products. An infinite one gives NaN,
 // as its values do: those of zero codes are NaN, the others infinities of both
 // signs.
 __device__ __forceinline__ float attn_key_scale(uint32_t half_bits) {
   const float s = half_bits_to_float(half_bits);
   return fmaf(s, 0.f, s);
+}
+
+// ---- values that are not finite, at positions that only some rows see
+//
+// A weight of 0 does not keep an infinity or a NaN of V out of a product. A V
+// scale that is not finite is therefore taken as 0 and its token's scores as
+// NaN: rows that see the token are NaN, and no others. (Leaving it out where
+// the weight is 0 instead would keep the log-sum-exp finite: 893 us for 882 of
+// a prompt chunk Q4, 926 for 900 Q8.) fp16 pages go into the matrix product as they are, so their
+// tiles with tokens that not every row of the unit sees are cleaned: such a
+// token's values are taken as zeros where they are not finite, tokens that no
+// row sees as zeros altogether. What was taken out marks the unit, and is
+// added again to the rows that do see it when they have been stored, from the
+// cache. (The weight of a seen token counts as above 0 there, also where its
+// exponential is not: infinity times it is infinity.)
+
+// The cached tokens that every row of the unit sees.
+struct AttnSpan {
+  int lo, hi;
+};
+__device__ __forceinline__ AttnSpan attn_seen_by_all(const AttnArgs& a, const AttnUnit& u) {
+  const int first = u.len - u.n + u.r0 / a.group, last = u.len - u.n + (u.r0 + u.rows - 1) / a.group;  // positions
+  return {a.window > 0 ? max(0, last - a.window + 1) : 0, a.causal ? min(u.len, max(0, first + 1)) : u.len};
+}
+
+// the halves of two fp16 values that are not finite, and of those that `among` has the top bit of, as a mask
+__device__ __forceinline__ uint32_t attn_not_finite(uint32_t two, uint32_t among) {
+  const uint32_t t = ((two & 0x7C007C00u) + 0x04000400u) & 0x80008000u & among;
+  return (t >> 15) * 0xFFFFu;
+}
+
+// What the cleaning took out of dims [d, d + 4) of fp16 V for row r of the piece: the sum of the values that are not finite,
+// of the tokens that row r sees and not every row does. 0: nothing.
+template <int D>
+__device__ __forceinline__ float4 attn_taken_out(const AttnArgs& a, const AttnPiece& p, int tile, int r, int d) {
+  const AttnSpan all = attn_seen_by_all(a, p.u);
+  const int pos = p.u.len - p.u.n + (p.u.r0 + r) / a.group;
+  const int lo = max(p.t0 * tile, a.window > 0 ? max(0, pos - a.window + 1) : 0);
+  const int hi = min(p.t1 * tile, a.causal ? min(p.u.len, pos + 1) : p.u.len);
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int t = lo; t < hi; ++t) {
+    if (t >= all.lo && t < all.hi) t = all.hi;
+    if (t >= hi) break;
+    const int page = __ldg(a.page_table + static_cast<long long>(p.u.b) * a.max_pages + t / a.page_size);
+    if (page < 0 || page >= a.n_pages) continue;
+    const long long g = (static_cast<long long>(page) * a.n_kv_heads + p.head) * a.page_size + t % a.page_size;
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.codes[1] + (g * D + d) / 2));
+    const uint32_t h[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!attn_finite(h[i])) y[i] += half_bits_to_float(h[i]);
+  }
+  return make_float4(y[0], y[1], y[2], y[3]);
+}
+
+// Adds it to a stored row: fp16 results (`out`), or a piece's fp32 sums (`slot`, not NULL).
+template <int D>
+__device__ __forceinline__ void attn_put_back(const AttnArgs& a, const AttnPiece& p, int tile, int r, int d, uint16_t* out,
+                                              float* slot) {
+  const float4 z = attn_taken_out<D>(a, p, tile, r, d);
+  const float add[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (add[i] == 0.f) continue;
+    if (slot)
+      slot[d + i] += add[i];
+    else
+      out[d + i] = static_cast<uint16_t>(float_to_half_bits(half_bits_to_float(out[d + i]) + add[i]));
+  }
 }
 
 // References of the softmax. Weights are multiplied by V's scales and rounded

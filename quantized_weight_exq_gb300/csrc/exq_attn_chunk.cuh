@@ -20,8 +20,8 @@
 //               stay in fp32 beside the tile and multiply S's columns (K) and
 //               the weights (V) in the softmax: rounding (u - z) s to fp16
 //               here instead would be one rounding more per cached value. For
-//               fp16 pages, which TMA brings in place, they only put zeros in
-//               V's slots past the end. They also bring Q.
+//               fp16 pages, which TMA brings in place, they only clean V's
+//               tokens that not every row sees. They also bring Q.
 //   warp 12     issues S = Q K^T, warps 14 and 15 O += P V of the two M tiles.
 //               An MMA is accepted about when the one before is done, so a
 //               warp's wait on a barrier (100 to 300 cycles beside busy warps,
@@ -275,6 +275,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
 // byte offset of the 16-byte chunk of dims [8 ch, 8 ch + 8) of row `row` in an
 // operand of `rows` rows: 64-dim slabs of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t operand_at(int rows, int row, int ch) {
@@ -346,6 +350,17 @@ struct Ring {
   }
 };
 
+// attn_put_back for a whole row of a unit. Rare, so a call of its own.
+template <int D, int FLOATS>
+__device__ __noinline__ void put_back_row(const AttnArgs& a, const AttnPiece& p, int row, bool begins) {
+  int tk, hd;
+  attn_row_of(a, p, row, tk, hd);
+#pragma unroll 1
+  for (int d = 0; d < D; d += 4)
+    attn_put_back<D>(a, p, kTile, row, d, a.out.data + tk * a.out.token_stride + hd * a.out.head_stride,
+                     p.whole ? nullptr : attn_slot(a, blockIdx.x, begins, FLOATS) + row * D);
+}
+
 template <int B, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, const __grid_constant__ Extra x) {
@@ -372,12 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto kv_full = [bar0](int st) { return bar0 + 96 + 8 * st; };
   const auto packed_full = [bar0](int st) { return bar0 + 128 + 8 * st; };
   const auto packed_empty = [bar0](int st) { return bar0 + 192 + 8 * st; };
-  const auto v_ready = [bar0](uint32_t tile) { return bar0 + 256 + 8 * (tile & 3); };  // fp16 pages: zeros past the end
+  const auto v_ready = [bar0](uint32_t tile) { return bar0 + 256 + 8 * (tile & 3); };  // fp16 pages: V is clean
   const uint32_t q_full = bar0 + 288, drain = bar0 + 296 /* of warps 12, 14, 15 */;
   const auto phase4 = [](uint32_t tile) { return (tile >> 2) & 1; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 40);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* is_last = reinterpret_cast<int*>(tmem_slot + 2);
+  // The last pieces' numbers (from 1) whose V was cleaned. The dequantisers may
+  // be three pieces ahead of the epilogue: the scores of two tiles and their
+  // queries are.
+  volatile int* cleaned = reinterpret_cast<volatile int*>(tmem_slot + 3);  // [4]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -395,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, kDequantThreads);
     for (int i = 0; i < 3; ++i) mbar_init(drain + 8 * i, 1);
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) cleaned[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   AttnState& state = reinterpret_cast<AttnState*>(smem + C::kOffState)[warp];
@@ -611,8 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(q_full);
 
       const int t1 = p.t1, end = p.u.end;
+      AttnSpan all;
+      if constexpr (!kQuant) all = attn_seen_by_all(a, p.u);
       for (int t = p.t0; t < t1 && ok; ++t, ++g) {
-        const int keep = end - t * T;  // tokens of the tile that exist
         if constexpr (kQuant) {
           if (g >= kNS) ok = mbar_wait_warp(pv_done(g - kNS), phase4(g - kNS), abort_flag, a);
 #pragma unroll
@@ -620,16 +641,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && mbar_wait_warp(packed_full(pr.st), pr.ph, abort_flag, a);
             if (!ok) break;
             const uint32_t src = sbase + C::kOffPacked + pr.st * C::kPacked;
+            uint32_t bits = tid < T ? split::lds16(src + P::kArray + 2 * tid) : 0;  // ahead of its use
             dequant<B, D>(src, sbase + (which ? C::kOffV : C::kOffK) + r.st * C::kArray, tid);
             // scales, zero past the end. Four tiles' are kept, and P V of the
             // tile kNS <= 3 ago, so every weight of the one four ago, is done
             if (tid < T) {
-              uint32_t bits = split::lds16(src + P::kArray + 2 * tid);
-              if (tid >= keep) bits = 0;
+              if (tid >= end - t * T) bits = 0;
               scales[(2 * (g & 3) + which) * T + tid] = which ? half_bits_to_float(bits) : attn_key_scale(bits) * x.scale;
               if (which) {
                 const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
                 if (lane == 0) exps[2 * (g & 3) + (tid >> 5)] = e;
+                if (!attn_finite(bits)) {
+                  scales[2 * (g & 3) * T + tid] = NAN;
+                  scales[(2 * (g & 3) + 1) * T + tid] = 0.f;
+                }
               }
             }
             mbar_arrive(packed_empty(pr.st));
@@ -641,11 +666,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           ok = mbar_wait_warp(kv_full(r.st), r.ph, abort_flag, a);
           if (!ok) break;
-          if (keep < T) {  // V's slots past the end may hold anything
-            const int from = max(keep, 0);
-            for (int i = tid; i < (T - from) * (D / 8); i += kDequantThreads)
-              sts128(sbase + C::kOffV + r.st * C::kArray + operand_at(T, from + i / (D / 8), i % (D / 8)), 0, 0, 0, 0);
-            async_fence();
+          if (t * T < all.lo || (t + 1) * T > all.hi) {  // tokens that not every row sees
+            // A thread has one or two 16-byte chunks of every kStep-th row.
+            // Tiles whose tokens are all seen by some row are looked over
+            // first (x 0 + 0 is NaN where x is not finite): most are clean.
+            constexpr int kPer = D == 64 ? 8 : 16, kStep = kDequantThreads / kPer, kParts = D / 8 / kPer;
+            const int row0 = tid / kPer;
+            const uint32_t own = sbase + C::kOffV + r.st * C::kArray + operand_at(T, row0, tid % kPer);
+            uint32_t sum = 0;
+            const int begin = p.u.begin;
+            const bool all_there = t * T >= begin && (t + 1) * T <= end;
+            if (all_there) {
+#pragma unroll
+              for (int i = 0; i < T / kStep * kParts; ++i) {
+                uint32_t v[4];
+                lds128(own + (i % kParts) * (2 * T * 128) + i / kParts * (kStep * 128), v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum = hfma2(v[j], 0u, sum);
+              }
+            }
+            if (!all_there || sum != 0) {
+#pragma unroll 1
+              for (int i = 0; i < T / kStep * kParts; ++i) {
+                const int at = t * T + row0 + i / kParts * kStep;
+                if (at >= all.lo && at < all.hi) continue;
+                const uint32_t to = own + (i % kParts) * (2 * T * 128) + i / kParts * (kStep * 128);
+                uint32_t v[4] = {0, 0, 0, 0}, out = 1;
+                if (at >= begin && at < end) {
+                  lds128(to, v);
+                  out = 0;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const uint32_t m = attn_not_finite(v[j], 0x80008000u);
+                    v[j] &= ~m;
+                    out |= m;
+                  }
+                  if (out) cleaned[state.number & 3] = state.number;
+                }
+                if (out) sts128(to, v[0], v[1], v[2], v[3]);
+              }
+              async_fence();
+            }
           }
           mbar_arrive(v_ready(g));
         }
@@ -920,6 +981,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             slot[C::kRows * D + row] = row_base, slot[C::kRows * D + C::kRows + row] = row_l;
         }
         tc_before();  // the next unit's first P V, ordered by its weights, overwrites O
+        if constexpr (!kQuant) {
+          if (cleaned[state.number & 3] == state.number && row < p.u.rows)
+            put_back_row<D, C::kFloats>(a, p, row, static_cast<int>(blockIdx.x) == c0);
+        }
       }
       if (!p.whole) {
         __threadfence();

@@ -274,12 +274,29 @@ __device__ __forceinline__ void scores(uint32_t kbase, int row0, int lane, const
   }
 }
 
-// O^T += V^T P^T of the same; `first` is the first token's position, fp16 values from `end` on are taken as zeros
+// Which of a lane's fp16 values of V are to be cleaned: bits of tokens that are
+// taken as they are or cleaned (`keep`), and of those that are cleaned (`some`).
+struct Clean {
+  uint32_t keep, some;
+  __device__ __forceinline__ void two(int x, int begin, int end, int all_lo, int all_hi) {  // tokens x and x + 1
+    const auto seen = [&](int t) { return t >= begin && t < end; };
+    const auto shared = [&](int t) { return t >= all_lo && t < all_hi; };
+    keep = (seen(x) ? 0xFFFFu : 0u) | (seen(x + 1) ? 0xFFFF0000u : 0u);
+    some = keep & ((shared(x) ? 0u : 0x8000u) | (shared(x + 1) ? 0u : 0x80000000u));
+  }
+  __device__ __forceinline__ void apply(uint32_t& v, bool& taken) const {
+    v &= keep;
+    const uint32_t out = attn_not_finite(v, some);
+    v &= ~out;
+    taken |= out != 0;
+  }
+};
+
+// O^T += V^T P^T of the same; fp16 values of tokens c, c + 1 (a) and c + 8, c + 9 (b) are cleaned where `clean` says so
 template <int B, int D, int NT>
-__device__ __forceinline__ void values(uint32_t vbase, int row0, int first, int end, int lane, const uint32_t (&pb)[NT][2],
-                                       float (&o)[NT][D / 16][4]) {
+__device__ __forceinline__ void values(uint32_t vbase, int row0, int lane, bool clean, const Clean& a, const Clean& b, bool& taken,
+                                       const uint32_t (&pb)[NT][2], float (&o)[NT][D / 16][4]) {
   using C = Cfg<B, D, NT>;
-  constexpr bool kQuant = B != 16;
   const int g = lane >> 2, c = lane & 3;
   if constexpr (B == 6) {
     // tokens (c, 4 + c) and (8 + c, 12 + c) of the slice, D / 8 codes from dim g D / 8
@@ -308,14 +325,6 @@ __device__ __forceinline__ void values(uint32_t vbase, int row0, int first, int 
   } else {
     constexpr int kChunks = C::kRowBytes / 16;
     const int lrow = row0 + (lane & 15), lch = lane >> 4;
-    uint32_t zA = 0xFFFFFFFFu, zB = 0xFFFFFFFFu;  // V's tokens past the end, as zeros
-    bool ragged = false;
-    if constexpr (!kQuant) {
-      ragged = first + 16 > end;
-      const int x = first + 2 * c, y = x + 8;
-      zA = (x < end ? 0xFFFFu : 0u) | (x + 1 < end ? 0xFFFF0000u : 0u);
-      zB = (y < end ? 0xFFFFu : 0u) | (y + 1 < end ? 0xFFFF0000u : 0u);
-    }
 #pragma unroll
     for (int q = 0; q < kChunks; q += 2) {
       uint32_t r[4];
@@ -344,7 +353,7 @@ __device__ __forceinline__ void values(uint32_t vbase, int row0, int first, int 
           for (int nt = 0; nt < NT; ++nt) mma(o[nt][q + h], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
         }
       } else {
-        if (ragged) r[0] &= zA, r[2] &= zA, r[1] &= zB, r[3] &= zB;
+        if (clean) a.apply(r[0], taken), a.apply(r[2], taken), b.apply(r[1], taken), b.apply(r[3], taken);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma(o[nt][q / 2], r[0], r[2], r[1], r[3], pb[nt][0], pb[nt][1]);
       }
@@ -368,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
   uint64_t* empty = full + C::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
   int* is_last = const_cast<int*>(abort_flag) + 1;
+  int* cleaned = is_last + 1;  // of each consumer warp: something was taken out of V in the unit
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -517,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
     bool begun = false;            // every row of the lane has a reference
+    bool taken = false;            // values of V that are not finite were taken out
 
     for (int t = t0; t < t1; ++t, ++tile) {
       const int here = st;
@@ -553,29 +564,42 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
         }
         // ---------------------------------------------------------- softmax
         const bool all_see = first >= all_lo && first + 16 * kSlices <= all_hi;
-        float vs[kSlices][2];
+        float ks[kSlices][2], vs[kSlices][2];
         uint32_t vtop = 0;
         float top = -INFINITY;
-        // exponents: scores less the rows' references, and the lane's largest
 #pragma unroll
         for (int h = 0; h < kSlices; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {  // the lane's two tokens of a slice
-            const int tok = row0 + 16 * h + token_at<B>(g + 8 * e), at = t * kTile + tok;
-            float ks = a.scale_log2;
+            ks[h][e] = a.scale_log2;
             vs[h][e] = 1.f;
             if constexpr (kQuant) {
-              ks *= attn_key_scale(lds16(sbase + 2 * tok));
+              const int tok = row0 + 16 * h + token_at<B>(g + 8 * e);
+              ks[h][e] *= attn_key_scale(lds16(sbase + 2 * tok));
               uint32_t v = lds16(sbase + C::kScale + 2 * tok);
-              if (at >= end) v = 0;  // whatever the slots past the end hold
+              if (t * kTile + tok >= end) v = 0;  // whatever the slots past the end hold
               vtop = max(vtop, v);
               vs[h][e] = half_bits_to_float(v);
             }
+          }
+        if (kQuant && vtop >= 0x7C00u) {  // one of them is not finite (or below 0, which no codec gives)
+#pragma unroll
+          for (int h = 0; h < kSlices; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(fabsf(vs[h][e]) < INFINITY)) ks[h][e] = NAN, vs[h][e] = 0.f;
+        }
+        // exponents: scores less the rows' references, and the lane's largest
+#pragma unroll
+        for (int h = 0; h < kSlices; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = first + 16 * h + token_at<B>(g + 8 * e);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                float x = fmaf(s[h][nt][2 * e + i], ks, nbase[nt][i]);
+                float x = fmaf(s[h][nt][2 * e + i], ks[h][e], nbase[nt][i]);
                 if (!all_see && (at < lo[nt][i] || at >= hi[nt][i])) x = -INFINITY;
                 s[h][nt][2 * e + i] = x;
                 top = fmaxf(top, x);
@@ -635,8 +659,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
             }
         // ---------------------------------------------------------- O^T += V^T P^T
 #pragma unroll
-        for (int h = 0; h < kSlices; ++h)
-          values<B, D, NT>(vbase, row0 + 16 * h, t * kTile + row0 + 16 * h, end, lane, pb[h], o);
+        for (int h = 0; h < kSlices; ++h) {
+          Clean ca, cb;
+          if (B == 16 && !all_see) {
+            const int x = first + 16 * h + 2 * c;
+            ca.two(x, begin, end, all_lo, all_hi);
+            cb.two(x + 8, begin, end, all_lo, all_hi);
+          }
+          values<B, D, NT>(vbase, row0 + 16 * h, lane, !all_see, ca, cb, taken, pb[h], o);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty[here]));
@@ -654,6 +685,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
           stat_l[warp * C::kRows + 8 * nt + 2 * c + i] = l[nt][i];
         }
       }
+    if constexpr (!kQuant) {
+      taken = __any_sync(0xffffffffu, taken);
+      if (lane == 0) cleaned[warp] = taken;
+    }
     consumer_sync();
     float f[NT][2];
 #pragma unroll
@@ -720,6 +755,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
       } else {
         *reinterpret_cast<float4*>(slot + r * D + 4 * col) = y;
         if (col == 0) slot[C::kRows * D + r] = mm, slot[C::kRows * D + C::kRows + r] = ll;
+      }
+    }
+    if (!kQuant && (cleaned[0] | cleaned[1] | cleaned[2] | cleaned[3])) {
+      __syncwarp();  // the stores above come first, whatever their types
+      for (int e = threadIdx.x; e < p.u.rows * (D / 4); e += kConsumers * 32) {  // each its own stores
+        const int r = e / (D / 4), d = 4 * (e % (D / 4));
+        int token, head;
+        attn_row_of(a, p, r, token, head);
+        attn_put_back<D>(a, p, kTile, r, d, a.out.data + token * a.out.token_stride + head * a.out.head_stride,
+                         p.whole ? nullptr : slot + r * D);
       }
     }
     if (!p.whole) {

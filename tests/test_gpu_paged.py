@@ -550,9 +550,10 @@ def test_attention_of_units_with_and_without_a_second_tile_of_rows(env, bits, D)
 
 # ---------------------------------------------------------------- values that are not finite
 
-def _check_not_finite(env, case, spoil_cache=None, spoil_q=None, seed=0):
+def _check_not_finite(env, case, spoil_cache=None, spoil_q=None, seed=0, values=False):
     """A result that the definition leaves not finite is the same one here, and every other is as near as ever. spoil_cache(c)
-    may change words and scales of a filled case; spoil_q(q) some queries."""
+    may change words and scales of a filled case; spoil_q(q) some queries. values: of V, where infinity may become NaN,
+    and codes make the log-sum-exp NaN too."""
     exq, torch = env
     bits, D, page, KH, H, lens, news, causal, window = case
     c = Case(exq, torch, bits, D, page, KH, lens, news, seed=seed + D).fill()
@@ -575,8 +576,13 @@ def _check_not_finite(env, case, spoil_cache=None, spoil_q=None, seed=0):
         finite = lambda a: np.where(np.isfinite(a), a, 0.0)  # noqa: E731
         tol = _bound(finite(ref), finite(spread), np.maximum(finite(total), 1.0), finite(qb), finite(k), finite(v), scale, L, D)
         ok = np.isfinite(ref)
-        assert np.array_equal(np.isnan(got[r]), np.isnan(ref)), b
-        assert np.array_equal(got[r][np.isinf(ref)], ref[np.isinf(ref)]), b
+        if values and bits != 16:
+            ref_lse = np.where(ok.all(-1), ref_lse, np.nan)                      # such a token's scores are NaN
+        if values:
+            assert np.array_equal(np.isfinite(got[r]), ok), (b, np.argwhere(np.isfinite(got[r]) != ok)[:8])
+        else:
+            assert np.array_equal(np.isnan(got[r]), np.isnan(ref)), b
+            assert np.array_equal(got[r][np.isinf(ref)], ref[np.isinf(ref)]), b
         off = np.abs(got[r][ok] - ref[ok])
         assert np.all(off <= tol[ok]), (b, off.max())
         assert np.array_equal(np.isnan(got_lse[r]), np.isnan(ref_lse))
@@ -672,3 +678,48 @@ def test_attention_beside_values_of_another_size(env, bits, D, new, place):
         assert np.all(np.abs(out[i, 0] - ref) <= tol), (i, np.abs(out[i, 0] - ref).max(), tol.max())
         clear += 1
     assert clear >= new // 2 - 2 and clear > 0
+
+
+# beside NOT_FINITE: windows, of one token and of many, and rows that see everything
+NOT_FINITE_V = NOT_FINITE + [(4, 128, 16, 2, 16, [300, 9000, 40], [1, 1, 1], True, 70), (16, 128, 16, 1, 4, [200, 900], [3, 2], True, 65),
+                             (16, 64, 16, 2, 2, [500, 300], [300, 70], True, 90), (8, 128, 32, 1, 4, [500, 700], [90, 200], True, 33),
+                             (16, 256, 16, 1, 4, [130, 700], [5, 3], True, 50), (16, 256, 16, 1, 4, [330, 700], [60, 30], True, 50),
+                             (16, 128, 64, 1, 4, [200, 90], [40, 3], False, 0), (6, 64, 64, 1, 4, [200, 90], [40, 3], False, 20)]
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("case", NOT_FINITE_V, ids=["-".join(map(str, (*c[:5], max(c[6]), c[7], c[8]))) for c in NOT_FINITE_V])
+def test_attention_of_values_that_are_not_finite(env, case, value):
+    # the newest token (seen by the last rows alone), one in the middle of the new ones, one that the window leaves on the
+    # way; in the last head one that no row sees, or that all see: rows that do not see one are untouched
+    bits, D, page, KH, H, lens, news, causal, window = case
+
+    def spoil(c):
+        for b, (L, n) in enumerate(zip(lens, news)):
+            for at in {L - 1, L - n // 2 - 1} | ({max(L - n // 2 - window, 0)} if window else set()):
+                _set_key(c, 1, b, at, 0, value)
+            if window and L - n - window >= 0:
+                _set_key(c, 1, b, L - n - window, KH - 1, value)             # just before every row's window
+            elif KH > 1:
+                _set_key(c, 1, b, 0, KH - 1, value)
+    assert _check_not_finite(env, case, spoil_cache=spoil, values=True) > 0
+
+
+@pytest.mark.parametrize("bits,D,new", [(4, 128, 1), (8, 64, 3), (16, 128, 2), (6, 128, 50), (16, 64, 80), (4, 256, 40)])
+def test_attention_beside_slots_that_hold_nan(env, bits, D, new):
+    # every token before the window and after the row is NaN, K and V: row by row the same as a sequence without them
+    exq, torch = env
+    L, window, page = 400, 90, 16
+    case = (bits, D, page, 1, 2, [L], [new], True, window)
+    c = Case(exq, torch, *case[:4], [L], [new], seed=5).fill()
+    q = torch.from_numpy(c.rng.standard_normal((new, 2, D)).astype(np.float16)).cuda()
+    want = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
+    for i in range(2):
+        for at in range(0, L - new - window + 1):
+            _set_key(c, i, 0, at, 0, np.nan)
+    assert torch.equal(exq.exq_paged_attn(c.cache(), c.batch(), q, window=window), want)
+    for i in range(2):
+        for at in range(L - new + 1, L):
+            _set_key(c, i, 0, at, 0, np.nan)
+    got = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
+    assert torch.equal(got[:1], want[:1]) and exq.exq_get_last_device_error() == exq.EXQ_OK

@@ -470,9 +470,11 @@ typedef struct {
  * Sequence b's new tokens are rows q_start[b] .. q_start[b+1] - 1 and hold its
  * last positions, kv_len[b] - (q_start[b+1] - q_start[b]) .. kv_len[b] - 1.
  * Position p of sequence b is slot p % page_size of page
- * page_table[b * max_pages + p / page_size]; entries past its last token are
- * not read. What the kernels find out of range (a page id outside the cache,
- * a length above its bound, q_start that falls) they skip and report as
+ * page_table[b * max_pages + p / page_size]. Entries past its last token are
+ * not read, nor, with a window, those of pages that it has left behind for all
+ * of the sequence's new tokens: such pages may be free, or hold others' tokens.
+ * What the kernels find out of range (a page id outside the cache, a length
+ * above its bound, q_start that falls) they skip and report as
  * EXQ_ERR_INVALID_ARG in the device error word; results of that sequence are
  * then unspecified. */
 typedef struct {

@@ -404,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<B, D, NT>::kCtas))
     bool ok = true;
     while (ok && attn_next<C::kRows, kTile>(a, state)) {
       const int32_t* table = a.page_table + static_cast<long long>(p.u.b) * a.max_pages;
-      const int t0 = p.t0, t1 = p.t1, head = p.head, end = p.u.end;
+      const int t0 = p.t0, t1 = p.t1, head = p.head, begin = p.u.begin, end = p.u.end;
       const int b0 = t0 * boxes, b1 = t1 * boxes;      // boxes of the piece
       const auto page_of = [&](int bx) {               // -1: nothing to copy
         const int tok = bx * box;
-        if (bx >= b1 || tok >= end) return -1;
+        if (bx >= b1 || tok >= end || tok + box <= begin) return -1;
         const int page = __ldg(table + tok / a.page_size);
         if (page < 0 || page >= a.n_pages) {
           atomicOr(a.err, kDevErrBadPage);

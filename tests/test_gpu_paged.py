@@ -723,3 +723,27 @@ def test_attention_beside_slots_that_hold_nan(env, bits, D, new):
             _set_key(c, i, 0, at, 0, np.nan)
     got = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
     assert torch.equal(got[:1], want[:1]) and exq.exq_get_last_device_error() == exq.EXQ_OK
+
+
+@pytest.mark.parametrize("bits,D,page,new,window", [(4, 128, 16, 1, 100), (8, 64, 32, 3, 70), (16, 128, 16, 2, 130), (6, 256, 16, 1, 33),
+                                                    (4, 128, 16, 50, 100), (16, 64, 32, 80, 100), (16, 256, 16, 40, 50), (8, 128, 64, 1, 64),
+                                                    (6, 128, 32, 45, 20)])
+def test_attention_after_the_pages_before_the_window_are_gone(env, bits, D, page, new, window):
+    # pages that lie before every new token's window are not read: their entries name no page
+    exq, torch = env
+    lens = [400, 333, 77]
+    c = Case(exq, torch, bits, D, page, 2, lens, [new] * 3, seed=window).fill()
+    q = torch.from_numpy(c.rng.standard_normal((3 * new, 4, D)).astype(np.float16)).cuda()
+    want = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
+    gone = 0
+    for b, L in enumerate(lens):
+        n = max(0, L - new - window + 1) // page
+        for i in range(2):                                       # whoever has the pages now
+            c.words[i][:, c.table[b, :n]] = 0x7E007E00
+            if bits != 16:
+                c.scales[i][:, c.table[b, :n]] = 0x7E00
+        c.table[b, :n] = -1
+        gone += n
+    got = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK and gone > 0
+    assert torch.equal(got, want)

@@ -39,7 +39,6 @@
 #pragma once
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "exq_attn_split.cuh"
@@ -1033,14 +1032,14 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
     return EXQ_ERR_CUDA;
   const Extra x{std::fmax(std::fabs(a.scale_log2), 0x1p-126f), a.scale_log2 < 0};
   auto fn = attn_chunk_kernel<B, D>;
-  static std::once_flag once;
-  static bool usable = false;
-  std::call_once(once, [&] {
-    cudaFuncAttributes at{};
-    usable = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess &&
-             cudaFuncGetAttributes(&at, fn) == cudaSuccess && (at.numRegs + 7) / 8 * 8 == kLaunchRegs;
-  });
-  if (!usable) return EXQ_ERR_CUDA;
+  static PerDevice state;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || !state.once(dev, [&] {
+        cudaFuncAttributes at{};
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess &&
+               cudaFuncGetAttributes(&at, fn) == cudaSuccess && (at.numRegs + 7) / 8 * 8 == kLaunchRegs;
+      }))
+    return EXQ_ERR_CUDA;
   fn<<<std::min(sms, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a, x);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }

@@ -37,7 +37,6 @@
 #pragma once
 
 #include <algorithm>
-#include <mutex>
 
 #include "exq_attn.cuh"
 
@@ -813,8 +812,12 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
       !encode_cache(&maps.v, a.codes[1], *call.cache, C::kPartBytes / 4, kSwizzle))
     return EXQ_ERR_CUDA;
   auto fn = attn_split_kernel<B, D, NT>;
-  static std::once_flag once;
-  std::call_once(once, [&] { cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+  static PerDevice state;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || !state.once(dev, [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) == cudaSuccess;
+      }))
+    return EXQ_ERR_CUDA;
   // Units cut into more than 32 pieces take two CTAs an SM: fewer pieces to
   // join (131072 tokens of 8 KV heads: Q8 61 us, 65 with three; Q4 48, 50). With
   // 16 sequences' units instead two cost more than they gain (23 us against 22).

@@ -800,9 +800,12 @@ exq_status launch_tiles(EncodeTiled enc, const exq_weight* w, int n, const uint1
             : w0.format == EXQ_FMT_EXL2
                 ? (xp_mode ? gemm_kernel<EXQ_FMT_EXL2, true> : gemm_kernel<EXQ_FMT_EXL2, false>)
                 : (xp_mode ? gemm_kernel<EXQ_FMT_EXL2_QSCALE, true> : gemm_kernel<EXQ_FMT_EXL2_QSCALE, false>);
-  static std::once_flag attr_once[6];
-  std::call_once(attr_once[2 * (w0.format - 1) + (xp_mode ? 1 : 0)],
-                 [&] { cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); });
+  static PerDevice attr[6];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || !attr[2 * (w0.format - 1) + (xp_mode ? 1 : 0)].once(dev, [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) == cudaSuccess;
+      }))
+    return EXQ_ERR_CUDA;
   {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((M + BT - 1) / BT, tiles, plan.split);

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "exq.h"
+#include "exq_per_device.h"
 
 namespace exq {
 

@@ -8,6 +8,7 @@ module raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 from pathlib import Path
@@ -168,6 +169,16 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _on(stream, device):
+    """The context in which ``stream`` (a torch stream, a handle, or None: the current one) is the current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 # ---------------------------------------------------------------- host packers
 
 def exq_pack_gptq(q: np.ndarray, z: np.ndarray, g_idx: Optional[np.ndarray], group_size: int):
@@ -306,7 +317,8 @@ def exq_gemv_workspace_size(w: Weight, M: int) -> int:
     return int(_lib.exq_gemv_workspace_size(ctypes.byref(w.desc()), M))
 
 
-_gemv_ws = {}  # device index -> zero-filled uint8 workspace shared by calls on one stream
+_gemv_ws = {}       # device index -> zero-filled uint8 workspace shared by calls on one stream
+_gemv_ws_outgrown = []  # smaller ones from before: graphs captured with them keep their addresses
 
 
 def gemv_workspace(w: Weight, M: int):
@@ -322,8 +334,29 @@ def _shared_workspace(need: int):
     dev = torch.cuda.current_device()
     buf = _gemv_ws.get(dev)
     if buf is None or buf.numel() < need:
-        buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
+        if buf is not None:
+            _gemv_ws_outgrown.append(buf)
+        buf = torch.zeros(max(need, 1 << 20, 2 * buf.numel() if buf is not None else 0), dtype=torch.uint8, device=f"cuda:{dev}")
         _gemv_ws[dev] = buf
+    return buf
+
+
+_attn_ws = {}  # (device index, stream handle) -> zero-filled uint8 workspace of exq_paged_attn
+
+
+def _attn_workspace(need: int, stream):
+    """The default exq_paged_attn workspace of the launch's stream, zeroed in that stream's order; kept and grown across calls.
+    Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
+    import torch
+    dev = torch.cuda.current_device()
+    with _on(stream, dev):
+        if torch.cuda.is_current_stream_capturing():
+            raise ExqError(EXQ_ERR_INVALID_ARG, "exq_paged_attn")
+        key = (dev, _stream_ptr(stream))
+        buf = _attn_ws.get(key)
+        if buf is None or buf.numel() < need:
+            # (the outgrown one goes back to the stream's own pool: what runs on the stream still has it)
+            buf = _attn_ws[key] = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
     return buf
 
 
@@ -589,8 +622,8 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
                    window: int = 0, lse=None, layer: int = 0, workspace=None, stream=None):
     """Attention of the new tokens' q, fp16 [tokens, heads, D], over the cached tokens of their sequences, the new ones
     among them (exq_kv_append first). scale: 1 / sqrt(D) unless given; lse: fp32 [tokens, heads] to fill, or None.
-    Without ``workspace`` the zero-filled one of the device that exq_gemv uses too is taken: for calls on one stream. A
-    call that a graph captures needs one of its own, for as long as the graph is replayed."""
+    Without ``workspace`` one is kept for each stream that calls are launched on. A call that a graph captures needs one
+    of its own, for as long as the graph is replayed."""
     import torch
     where = "exq_paged_attn"
     T, H, D = q.shape
@@ -605,9 +638,7 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     c, b = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T))
     if workspace is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise ExqError(EXQ_ERR_INVALID_ARG, where)
-        workspace = _shared_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)))
+        workspace = _attn_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)), stream)
     elif not workspace.is_cuda:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_paged_attn(c, layer, b, ctypes.byref(qr), H, D ** -0.5 if scale is None else scale, int(causal), window,

@@ -174,9 +174,24 @@ def _on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_ptr(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that a kernel launched on ``stream`` may write at once, and that the current stream may go on to use: of the
+    allocator's pool for ``stream``, where what it held before was used in that stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with _on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if torch.cuda.current_stream(device) != current:
+            t.record_stream(current)
+    return t
 
 
 # ---------------------------------------------------------------- host packers
@@ -415,7 +430,7 @@ def exq_gemm_multi(ws, x, ys, workspace=None, stream=None):
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_gemm_multi")
     need = exq_gemm_multi_workspace_size(ws, x.shape[0])
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream)
     ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     yp = (ctypes.c_void_p * len(ys))(*[y.data_ptr() for y in ys])
@@ -444,9 +459,9 @@ def exq_kv_quantize(x, bits: int, codes=None, scales=None, stream=None):
     D = x.shape[-1]
     G = x.numel() // D if D else 0
     if codes is None:
-        codes = torch.empty(G, D * bits // 32, dtype=torch.int32, device=x.device)
+        codes = _empty((G, D * bits // 32), torch.int32, x.device, stream)
     if scales is None:
-        scales = torch.empty(G, dtype=torch.float16, device=x.device)
+        scales = _empty(G, torch.float16, x.device, stream)
     _check(_lib.exq_kv_quantize(x.data_ptr(), G, D, bits, codes.data_ptr(), scales.data_ptr(), _stream_ptr(stream)),
            "exq_kv_quantize")
     return codes, scales
@@ -457,7 +472,7 @@ def exq_kv_dequantize(codes, scales, D: int, bits: int, out=None, stream=None):
     import torch
     G = scales.numel()
     if out is None:
-        out = torch.empty(G, D, dtype=torch.float16, device=scales.device)
+        out = _empty((G, D), torch.float16, scales.device, stream)
     _check(_lib.exq_kv_dequantize(codes.data_ptr(), scales.data_ptr(), G, D, bits, out.data_ptr(),
                                   _stream_ptr(stream)), "exq_kv_dequantize")
     return out
@@ -518,7 +533,7 @@ def exq_rope(x, pos, rope: Rope, out=None, grad: bool = False, stream=None):
     import torch
     T, H, D = x.shape
     if out is None:
-        out = torch.empty(T, H, D, dtype=torch.float16, device=x.device)
+        out = _empty((T, H, D), torch.float16, x.device, stream)
     if not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_rope")
     xr, yr = _rows(x, "exq_rope"), _rows(out, "exq_rope", D, H, T)
@@ -604,7 +619,7 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
     if q is not None:
         heads = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+            q_out = _empty(q.shape, torch.float16, q.device, stream)
         qp, op = ctypes.byref(_rows(q, where, D, None, T)), ctypes.byref(_rows(q_out, where, D, heads, T))
     if pos is not None and (not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
@@ -632,7 +647,7 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
             raise ExqError(EXQ_ERR_INVALID_ARG, where)
         T = batch.n_tokens
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        out = _empty(q.shape, torch.float16, q.device, stream)
     qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
     if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
@@ -711,9 +726,9 @@ def exq_measure_exl2(W, perm=None, stream=None):
     """RTN error table fp32 [K/32, 6] of an fp16 weight [K, N] (device)."""
     import torch
     K, N = W.shape
-    err = torch.empty(K // 32, 6, dtype=torch.float32, device=W.device)
+    err = _empty((K // 32, 6), torch.float32, W.device, stream)
     nws = int(_lib.exq_measure_exl2_workspace_size(K, N))
-    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=W.device)
+    ws = _empty(max(nws, 16), torch.uint8, W.device, stream)
     _check(_lib.exq_measure_exl2(W.data_ptr(), None if perm is None else perm.data_ptr(), K, N, err.data_ptr(),
                                  ws.data_ptr(), nws, _stream_ptr(stream)), "exq_measure_exl2")
     return err
@@ -727,8 +742,8 @@ def exq_quantize_exl2(W, bits, perm=None, stream=None) -> Weight:
     off = exq_exl2_seg_word_off(bits)
     rows = int(off[-1])
     off_d = torch.from_numpy(off.view(np.int32)).to(W.device)
-    qw = torch.empty(rows, N, dtype=torch.int32, device=W.device)
-    sc = torch.empty(K // 32, N, dtype=torch.float16, device=W.device)
+    qw = _empty((rows, N), torch.int32, W.device, stream)
+    sc = _empty((K // 32, N), torch.float16, W.device, stream)
     _check(_lib.exq_quantize_exl2(W.data_ptr(), None if perm is None else perm.data_ptr(), K, N, off_d.data_ptr(),
                                   rows, qw.data_ptr(), sc.data_ptr(), _stream_ptr(stream)), "exq_quantize_exl2")
     return Weight(EXQ_FMT_EXL2, K, N, 32, qw, sc, None, perm, off_d)

@@ -110,3 +110,31 @@ def test_attention_refuses_capture_of_the_stream_it_is_given(env):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("what", ["rope", "append", "attention", "dequantize"])
+def test_results_on_another_stream_do_not_meet_pending_work_on_this_one(env, what):
+    # the current stream still has a write to memory that has been given back: a result that is written on another stream
+    # must not be put there
+    exq, torch = env
+    cache, batch, q = _long_sequence(exq, torch, tokens=256, new=256)
+    k, v = (torch.randn(256, 2, 128, device="cuda").half() for _ in range(2))
+    rope, pos = exq.rope_table(128), torch.arange(256, dtype=torch.int32, device="cuda")
+    codes, scales = exq.exq_kv_quantize(q, 4)
+    ws = torch.zeros(exq.exq_paged_attn_workspace_size(cache, batch, 16, 256), dtype=torch.uint8, device="cuda")
+    call = {"rope": lambda **kw: exq.exq_rope(q, pos, rope, **kw),
+            "append": lambda **kw: exq.exq_kv_append(cache, batch, k, v, q=q, rope=rope, **kw),
+            "attention": lambda **kw: exq.exq_paged_attn(cache, batch, q, workspace=ws, **kw),
+            "dequantize": lambda **kw: exq.exq_kv_dequantize(codes, scales, 128, 4, **kw)}[what]
+    want = call()
+    s = torch.cuda.Stream()
+    call(stream=s)
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        gone = torch.empty_like(want)
+        torch.cuda._sleep(40_000_000)                    # about 20 ms: the write below is still to come
+        gone.fill_(7.0)
+        del gone
+        got = call(stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), what

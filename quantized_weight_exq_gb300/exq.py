@@ -597,9 +597,12 @@ class KVBatch:
                                   page_table.data_ptr())
 
     def desc(self, rows: int) -> exq_kv_batch:
-        if self.n_tokens is None:
-            self._desc.n_tokens = rows
-        return self._desc
+        """The call's own descriptor: another thread's call with the same batch may have other rows."""
+        if self.n_tokens is not None:
+            return self._desc
+        d = exq_kv_batch.from_buffer_copy(self._desc)
+        d.n_tokens = rows
+        return d
 
 
 def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[Rope] = None, pos=None, q_out=None,

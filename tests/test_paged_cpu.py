@@ -256,3 +256,54 @@ def test_binding_refuses_host_tensors(exq):
         with pytest.raises(exq.ExqError) as e:
             call()
         assert e.value.status == exq.EXQ_ERR_INVALID_ARG
+
+
+class _Tensor:
+    """What the binding asks of a tensor, without a GPU."""
+
+    def __init__(self, shape, dtype, device=0):
+        import math
+        self.shape, self.dtype, self.device_index, self.is_cuda = tuple(shape), dtype, device, device >= 0
+        self._strides = [math.prod(self.shape[i + 1:]) for i in range(len(self.shape))]
+
+    def stride(self):
+        return tuple(self._strides)
+
+    def numel(self):
+        import math
+        return math.prod(self.shape)
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_floating_point(self):
+        return self.dtype.is_floating_point
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+    def get_device(self):
+        return self.device_index
+
+    @property
+    def device(self):
+        import torch
+        return torch.device("cuda", self.device_index) if self.is_cuda else torch.device("cpu")
+
+
+def _batch(exq, device=0, n_tokens=None):
+    import torch
+    z = lambda *s: _Tensor(s, torch.int32, device)  # noqa: E731
+    return exq.KVBatch(z(3), z(2), z(2, 8), 4, 100, n_tokens)
+
+
+def test_batch_descriptors_of_two_calls_are_their_own(exq):
+    # two threads with one batch and other rows: neither passes the other's count
+    batch = _batch(exq)
+    a = batch.desc(3)
+    b = batch.desc(5)
+    assert (a.n_tokens, b.n_tokens) == (3, 5) and a.n_seqs == b.n_seqs == 2 and a.max_kv_len == 100
+    assert _batch(exq, n_tokens=7).desc(9).n_tokens == 7

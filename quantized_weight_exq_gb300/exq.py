@@ -480,6 +480,15 @@ def exq_kv_dequantize(codes, scales, D: int, bits: int, out=None, stream=None):
 
 # ---------------------------------------------------------------- rotary positions
 
+def _here(where: str, *devices: int) -> None:
+    """Refuses tensors (their get_device()) of different devices, of the host, or of another device than the current one,
+    which the launch goes to: its kernels could not read them."""
+    import torch
+    d = devices[0]
+    if d < 0 or any(x != d for x in devices) or d != torch.cuda.current_device():
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+
+
 def exq_rope_freqs(R: int, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE, factor: float = 1.0,
                    orig_ctx: float = 0.0, low: float = 1.0, high: float = 32.0):
     """Host: (frequencies float64 [R/2] in radians per position, gain)."""
@@ -532,10 +541,11 @@ def exq_rope(x, pos, rope: Rope, out=None, grad: bool = False, stream=None):
     the result to the gradient at x). ``out`` may be x."""
     import torch
     T, H, D = x.shape
-    if out is None:
-        out = _empty((T, H, D), torch.float16, x.device, stream)
     if not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_rope")
+    _here("exq_rope", x.get_device(), pos.get_device(), rope.steps.get_device(), *(() if out is None else (out.get_device(),)))
+    if out is None:
+        out = _empty((T, H, D), torch.float16, x.device, stream)
     xr, yr = _rows(x, "exq_rope"), _rows(out, "exq_rope", D, H, T)
     _check(_lib.exq_rope(ctypes.byref(rope._desc), ctypes.byref(xr), T, H, D, pos.data_ptr(), ctypes.byref(yr), int(grad),
                          _stream_ptr(stream)), "exq_rope")
@@ -562,6 +572,9 @@ class KVCache:
                           or k_scales.dtype != torch.float16 or v_scales.dtype != torch.float16
                           or k_scales.shape != shape[:4] or v_scales.shape != shape[:4]
                           or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
+            raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
+        self.device = k_codes.get_device()
+        if any(t is not None and t.get_device() != self.device for t in (v_codes, k_scales, v_scales)):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.bits, self.D, self.n_kv_heads, self.page_size, self.n_pages, self.n_layers = bits, W * 32 // bits, H, S, P, L
@@ -592,6 +605,9 @@ class KVBatch:
                 or kv_len.shape != (B,) or not q_start.is_contiguous() or not kv_len.is_contiguous()
                 or not page_table.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
+        self.device = q_start.get_device()
+        if kv_len.get_device() != self.device or page_table.get_device() != self.device:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
         self.q_start, self.kv_len, self.page_table, self.n_tokens = q_start, kv_len, page_table, n_tokens
         self._desc = exq_kv_batch(B, n_tokens or 0, max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(),
                                   page_table.data_ptr())
@@ -616,6 +632,8 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
         if batch.n_tokens > T:
             raise ExqError(EXQ_ERR_INVALID_ARG, where)
         T = batch.n_tokens
+    _here(where, cache.device, batch.device, k.get_device(), v.get_device(),
+          *(t.get_device() for t in (q, q_out, pos, rope and rope.steps) if t is not None))
     kr, vr = _rows(k, where, D, H), _rows(v, where, D, H, T)
     qp = op = None
     heads = 0
@@ -649,6 +667,8 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
         if batch.n_tokens > T:
             raise ExqError(EXQ_ERR_INVALID_ARG, where)
         T = batch.n_tokens
+    _here(where, cache.device, batch.device, q.get_device(),
+          *(t.get_device() for t in (out, lse, workspace) if t is not None))
     if out is None:
         out = _empty(q.shape, torch.float16, q.device, stream)
     qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
@@ -657,8 +677,6 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
     c, b = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T))
     if workspace is None:
         workspace = _attn_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)), stream)
-    elif not workspace.is_cuda:
-        raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_paged_attn(c, layer, b, ctypes.byref(qr), H, D ** -0.5 if scale is None else scale, int(causal), window,
                                ctypes.byref(orow), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
@@ -670,6 +688,7 @@ def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
     import torch
     if not pairs.is_cuda or pairs.dtype != torch.int32 or not pairs.is_contiguous() or pairs.numel() % 2:
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_kv_copy_pages")
+    _here("exq_kv_copy_pages", cache.device, pairs.get_device())
     _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2, _stream_ptr(stream)),
            "exq_kv_copy_pages")
 

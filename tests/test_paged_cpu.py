@@ -307,3 +307,52 @@ def test_batch_descriptors_of_two_calls_are_their_own(exq):
     b = batch.desc(5)
     assert (a.n_tokens, b.n_tokens) == (3, 5) and a.n_seqs == b.n_seqs == 2 and a.max_kv_len == 100
     assert _batch(exq, n_tokens=7).desc(9).n_tokens == 7
+
+
+def test_binding_refuses_tensors_of_several_devices(exq, monkeypatch):
+    # all of a call's tensors are on one device, and it is the current one: anything else is an error before any launch
+    import torch
+    i32, f16, i64 = torch.int32, torch.float16, torch.int64
+    T = _Tensor
+    here = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: here[0])
+
+    def cache(d=0, vd=None, sd=None):
+        codes = lambda dev: T((1, 8, 2, 16, 8), i32, dev)  # noqa: E731
+        scales = lambda dev: T((1, 8, 2, 16), f16, dev)  # noqa: E731
+        return exq.KVCache(codes(d), codes(d if vd is None else vd), scales(d), scales(d if sd is None else sd), 4)
+
+    def rope(d=0):
+        return exq.Rope(T((32,), i64, d), 64)
+
+    rows = lambda heads, d=0: T((3, heads, 64), f16, d)  # noqa: E731
+    pos = lambda d=0: T((3,), i32, d)  # noqa: E731
+    bad = [lambda: cache(vd=1), lambda: cache(sd=1),
+           lambda: exq.KVBatch(T((3,), i32, 0), T((2,), i32, 1), T((2, 8), i32, 0), 4, 100),
+           lambda: exq.KVBatch(T((3,), i32, 0), T((2,), i32, 0), T((2, 8), i32, 1), 4, 100),
+           lambda: exq.exq_rope(rows(4, 1), pos(), rope()), lambda: exq.exq_rope(rows(4), pos(1), rope()),
+           lambda: exq.exq_rope(rows(4), pos(), rope(1)), lambda: exq.exq_rope(rows(4), pos(), rope(), out=rows(4, 1)),
+           lambda: exq.exq_rope(rows(4, -1), pos(), rope()),
+           lambda: exq.exq_kv_append(cache(), _batch(exq, 1), rows(2), rows(2)),
+           lambda: exq.exq_kv_append(cache(1), _batch(exq), rows(2), rows(2)),
+           lambda: exq.exq_kv_append(cache(), _batch(exq), rows(2), rows(2, 1)),
+           lambda: exq.exq_kv_append(cache(), _batch(exq), rows(2), rows(2), q=rows(4, 1), rope=rope(), q_out=rows(4)),
+           lambda: exq.exq_kv_append(cache(), _batch(exq), rows(2), rows(2), q=rows(4), rope=rope(1), q_out=rows(4)),
+           lambda: exq.exq_kv_append(cache(), _batch(exq), rows(2), rows(2), rope=rope(), pos=pos(1)),
+           lambda: exq.exq_paged_attn(cache(), _batch(exq), rows(4, 1)),
+           lambda: exq.exq_paged_attn(cache(), _batch(exq), rows(4), out=rows(4, 1)),
+           lambda: exq.exq_paged_attn(cache(), _batch(exq), rows(4), out=rows(4), lse=T((3, 4), torch.float32, 1)),
+           lambda: exq.exq_paged_attn(cache(), _batch(exq), rows(4), out=rows(4), workspace=T((1 << 20,), torch.uint8, -1)),
+           lambda: exq.exq_kv_copy_pages(cache(), T((1, 2), i32, 1))]
+    for i, call in enumerate(bad):
+        with pytest.raises(exq.ExqError) as e:
+            call()
+        assert e.value.status == exq.EXQ_ERR_INVALID_ARG, i
+    here[0] = 1                                          # everything on device 0, the launch would go to 1
+    for i, call in enumerate([lambda: exq.exq_rope(rows(4), pos(), rope(), out=rows(4)),
+                              lambda: exq.exq_kv_append(cache(), _batch(exq), rows(2), rows(2)),
+                              lambda: exq.exq_paged_attn(cache(), _batch(exq), rows(4), out=rows(4)),
+                              lambda: exq.exq_kv_copy_pages(cache(), T((1, 2), i32))]):
+        with pytest.raises(exq.ExqError) as e:
+            call()
+        assert e.value.status == exq.EXQ_ERR_INVALID_ARG, i

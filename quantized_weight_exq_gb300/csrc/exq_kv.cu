@@ -278,7 +278,7 @@ struct AppendArgs {
   // cache, its arrays at the layer
   uint32_t* codes[2];   // K, V
   uint16_t* scales[2];
-  int n_kv_heads, page_size, n_pages, D;
+  int n_kv_heads, page_size, n_pages;
   // rows
   const uint16_t* in[3];  // q, k, v
   uint16_t* q_out;
@@ -300,16 +300,23 @@ struct TokenPlace {
 };
 
 // Where token t goes, by one warp: its sequence is the last with
-// q_start <= t (counted by the lanes over all sequences).
+// q_start <= t (counted by the lanes over all sequences, which also see whether
+// q_start falls anywhere: then no token's sequence is certain).
 __device__ __forceinline__ TokenPlace find_place(const AppendArgs& a, int t, int lane) {
   int n = 0;
-  for (int b = lane; b < a.n_seqs; b += 32) n += __ldg(a.q_start + b) <= t ? 1 : 0;
+  bool falls = false;
+  for (int b = lane; b < a.n_seqs; b += 32) {
+    const int start = __ldg(a.q_start + b);
+    n += start <= t ? 1 : 0;
+    falls |= __ldg(a.q_start + b + 1) < start;
+  }
+  falls = __any_sync(0xffffffffu, falls);
   const int b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n))) - 1;
   TokenPlace p{0, -1, 0};
   const int end = __ldg(a.q_start + a.n_seqs);
-  if (t >= end) return p;  // padding
+  if (t >= end && !falls) return p;  // padding
   const int first = b >= 0 ? __ldg(a.q_start + b) : 0, next = b >= 0 ? __ldg(a.q_start + b + 1) : 0;
-  bool ok = b >= 0 && next > t && next - first <= a.max_q_len;  // else q_start falls somewhere, or a bound is wrong
+  bool ok = !falls && b >= 0 && next > t && next - first <= a.max_q_len;  // else q_start is wrong, or a bound
   if (ok) {
     const int len = __ldg(a.kv_len + b), at = len - (next - t);
     ok = len <= a.max_kv_len && at >= 0;  // max_kv_len <= max_pages * page_size
@@ -635,7 +642,6 @@ exq_status launch_kv_append(const exq_kv_cache& c, int layer, const exq_kv_batch
   a.n_kv_heads = c.n_kv_heads;
   a.page_size = c.page_size;
   a.n_pages = c.n_pages;
-  a.D = c.D;
   const exq_rows* rows[3] = {q, &k, &v};
   for (int i = 0; i < 3; ++i)
     if (rows[i]) {

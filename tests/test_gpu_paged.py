@@ -747,3 +747,16 @@ def test_attention_after_the_pages_before_the_window_are_gone(env, bits, D, page
     got = exq.exq_paged_attn(c.cache(), c.batch(), q, window=window)
     assert exq.exq_get_last_device_error() == exq.EXQ_OK and gone > 0
     assert torch.equal(got, want)
+
+
+def test_append_reports_a_q_start_that_falls(env):
+    # every token finds a sequence with room for it, but not its own: nothing is written
+    exq, torch = env
+    k = torch.randn(20, 2, 64, device="cuda").half()
+    for start in ([1, 9, 9, 0, 20], [0, 20, 20, 20, 3], [0, 9, 8, 8, 20]):
+        c = Case(exq, torch, 8, 64, 16, 2, [40, 40, 40, 40], [5, 5, 5, 5], seed=3)
+        c.start[:] = start
+        cache = c.cache()
+        exq.exq_kv_append(cache, c.batch(max_q_len=20), k, k)
+        assert exq.exq_get_last_device_error() == exq.EXQ_ERR_INVALID_ARG, start
+        c.same(cache)

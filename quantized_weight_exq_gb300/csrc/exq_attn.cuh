@@ -477,19 +477,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait of one thread; false (and a recorded timeout) if the phase
-// never completes, or if another role of the CTA gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const AttnArgs& a) {
-  for (int i = 0; i < a.wait_limit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  atomicOr(a.err, kDevErrTimeout);
-  *abort_flag = 1;
-  return false;
-}
-
-// Bounded wait of a whole warp: all lanes leave in the same round.
+// Bounded wait of a whole warp, all lanes leave in the same round; false (and a
+// recorded timeout) if the phase never completes, or if another role of the
+// CTA gave up.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, const AttnArgs& a) {
   for (int i = 0; i < a.wait_limit; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -499,9 +489,5 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   *abort_flag = 1;
   return false;
 }
-
-// host: launches of one (bits, D) family
-exq_status launch_attn_split(const AttnCall& c, AttnArgs& a, int sms, cudaStream_t stream);
-size_t attn_split_workspace(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads, int sms);
 
 }  // namespace exq

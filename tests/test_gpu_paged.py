@@ -760,3 +760,15 @@ def test_append_reports_a_q_start_that_falls(env):
         exq.exq_kv_append(cache, c.batch(max_q_len=20), k, k)
         assert exq.exq_get_last_device_error() == exq.EXQ_ERR_INVALID_ARG, start
         c.same(cache)
+
+
+MANY_HEADS = [(4, 128, 64, 1, 64, [500, 77], [1, 1], True, 0), (16, 128, 16, 1, 64, [300], [1], True, 100),
+              (8, 64, 32, 2, 142, [90, 200], [1, 3], True, 0), (6, 256, 16, 1, 33, [200], [1], True, 0),
+              (4, 64, 16, 1, 40, [3000], [1], True, 0), (16, 256, 64, 1, 24, [150, 70], [1, 1], True, 0),
+              (8, 128, 256, 1, 300, [140], [5], True, 70)]
+
+
+@pytest.mark.parametrize("case", MANY_HEADS, ids=["-".join(map(str, (*c[:5], max(c[6])))) for c in MANY_HEADS])
+def test_attention_of_many_query_heads_a_kv_head(env, case):
+    # more query heads than a unit of the few-row kernel has rows: several units, or the kernel of many rows for one token
+    _check_attention(env, case, seed=21)

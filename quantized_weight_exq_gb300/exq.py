@@ -159,11 +159,12 @@ def _np_ptr(a: Optional[np.ndarray]):
     return None if a is None else a.ctypes.data
 
 
-def _stream_ptr(stream) -> Optional[int]:
+def _stream_ptr(stream, device: Optional[int] = None) -> Optional[int]:
+    """The handle of ``stream``, or of the current one (of ``device``, where the caller knows that it is the current device)."""
     if stream is None:
         import torch
         # the current stream's handle without the Stream object around it (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -359,19 +360,19 @@ def _shared_workspace(need: int):
 _attn_ws = {}  # (device index, stream handle) -> zero-filled uint8 workspace of exq_paged_attn
 
 
-def _attn_workspace(need: int, stream):
+def _attn_workspace(need: int, dev: int, stream, handle: int):
     """The default exq_paged_attn workspace of the launch's stream, zeroed in that stream's order; kept and grown across calls.
     Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
     import torch
-    dev = torch.cuda.current_device()
-    with _on(stream, dev):
-        if torch.cuda.is_current_stream_capturing():
-            raise ExqError(EXQ_ERR_INVALID_ARG, "exq_paged_attn")
-        key = (dev, _stream_ptr(stream))
-        buf = _attn_ws.get(key)
-        if buf is None or buf.numel() < need:
-            # (the outgrown one goes back to the stream's own pool: what runs on the stream still has it)
-            buf = _attn_ws[key] = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
+    if stream is not None:
+        with _on(stream, dev):
+            return _attn_workspace(need, dev, None, handle)
+    if torch.cuda.is_current_stream_capturing():
+        raise ExqError(EXQ_ERR_INVALID_ARG, "exq_paged_attn")
+    buf = _attn_ws.get((dev, handle))
+    if buf is None or buf.numel() < need:
+        # (the outgrown one goes back to the stream's own pool: what runs on the stream still has it)
+        buf = _attn_ws[dev, handle] = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
     return buf
 
 
@@ -485,7 +486,7 @@ def _here(where: str, *devices: int) -> None:
     which the launch goes to: its kernels could not read them."""
     import torch
     d = devices[0]
-    if d < 0 or any(x != d for x in devices) or d != torch.cuda.current_device():
+    if d < 0 or devices.count(d) != len(devices) or d != torch.cuda.current_device():
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
 
 
@@ -543,12 +544,13 @@ def exq_rope(x, pos, rope: Rope, out=None, grad: bool = False, stream=None):
     T, H, D = x.shape
     if not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_rope")
-    _here("exq_rope", x.get_device(), pos.get_device(), rope.steps.get_device(), *(() if out is None else (out.get_device(),)))
+    dev = x.get_device()
+    _here("exq_rope", dev, pos.get_device(), rope.steps.get_device(), dev if out is None else out.get_device())
     if out is None:
         out = _empty((T, H, D), torch.float16, x.device, stream)
     xr, yr = _rows(x, "exq_rope"), _rows(out, "exq_rope", D, H, T)
     _check(_lib.exq_rope(ctypes.byref(rope._desc), ctypes.byref(xr), T, H, D, pos.data_ptr(), ctypes.byref(yr), int(grad),
-                         _stream_ptr(stream)), "exq_rope")
+                         _stream_ptr(stream, dev)), "exq_rope")
     return out
 
 
@@ -574,7 +576,8 @@ class KVCache:
                           or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
         self.device = k_codes.get_device()
-        if any(t is not None and t.get_device() != self.device for t in (v_codes, k_scales, v_scales)):
+        if v_codes.get_device() != self.device or (quantised and (k_scales.get_device() != self.device
+                                                                  or v_scales.get_device() != self.device)):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.bits, self.D, self.n_kv_heads, self.page_size, self.n_pages, self.n_layers = bits, W * 32 // bits, H, S, P, L
@@ -609,15 +612,18 @@ class KVBatch:
         if kv_len.get_device() != self.device or page_table.get_device() != self.device:
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
         self.q_start, self.kv_len, self.page_table, self.n_tokens = q_start, kv_len, page_table, n_tokens
-        self._desc = exq_kv_batch(B, n_tokens or 0, max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(),
-                                  page_table.data_ptr())
+        self._rest = max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()
+        self._last = -1, None
 
     def desc(self, rows: int) -> exq_kv_batch:
-        """The call's own descriptor: another thread's call with the same batch may have other rows."""
+        """The descriptor of a call with ``rows`` rows. One that has been handed out is not written again: another thread's
+        call with the same batch may have other rows."""
         if self.n_tokens is not None:
-            return self._desc
-        d = exq_kv_batch.from_buffer_copy(self._desc)
-        d.n_tokens = rows
+            rows = self.n_tokens
+        last, d = self._last
+        if last != rows:
+            d = exq_kv_batch(self.kv_len.shape[0], rows, *self._rest)
+            self._last = rows, d
         return d
 
 
@@ -632,8 +638,10 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
         if batch.n_tokens > T:
             raise ExqError(EXQ_ERR_INVALID_ARG, where)
         T = batch.n_tokens
-    _here(where, cache.device, batch.device, k.get_device(), v.get_device(),
-          *(t.get_device() for t in (q, q_out, pos, rope and rope.steps) if t is not None))
+    dev = cache.device
+    _here(where, dev, batch.device, k.get_device(), v.get_device(), dev if q is None else q.get_device(),
+          dev if q_out is None else q_out.get_device(), dev if pos is None else pos.get_device(),
+          dev if rope is None else rope.steps.get_device())
     kr, vr = _rows(k, where, D, H), _rows(v, where, D, H, T)
     qp = op = None
     heads = 0
@@ -646,7 +654,7 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_kv_append(ctypes.byref(cache._desc), layer, ctypes.byref(batch.desc(T)), ctypes.byref(kr),
                               ctypes.byref(vr), None if rope is None else ctypes.byref(rope._desc),
-                              None if pos is None else pos.data_ptr(), qp, op, heads, _stream_ptr(stream)), where)
+                              None if pos is None else pos.data_ptr(), qp, op, heads, _stream_ptr(stream, dev)), where)
     return q_out if q is not None else None
 
 
@@ -667,19 +675,20 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
         if batch.n_tokens > T:
             raise ExqError(EXQ_ERR_INVALID_ARG, where)
         T = batch.n_tokens
-    _here(where, cache.device, batch.device, q.get_device(),
-          *(t.get_device() for t in (out, lse, workspace) if t is not None))
+    dev = cache.device
+    _here(where, dev, batch.device, q.get_device(), dev if out is None else out.get_device(),
+          dev if lse is None else lse.get_device(), dev if workspace is None else workspace.get_device())
     if out is None:
         out = _empty(q.shape, torch.float16, q.device, stream)
     qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
     if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
-    c, b = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T))
+    c, b, handle = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T)), _stream_ptr(stream, dev)
     if workspace is None:
-        workspace = _attn_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)), stream)
+        workspace = _attn_workspace(int(_lib.exq_paged_attn_workspace_size(c, b, H)), dev, stream, handle)
     _check(_lib.exq_paged_attn(c, layer, b, ctypes.byref(qr), H, D ** -0.5 if scale is None else scale, int(causal), window,
                                ctypes.byref(orow), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+                               workspace.numel() * workspace.element_size(), handle), where)
     return out
 
 
@@ -689,7 +698,8 @@ def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
     if not pairs.is_cuda or pairs.dtype != torch.int32 or not pairs.is_contiguous() or pairs.numel() % 2:
         raise ExqError(EXQ_ERR_INVALID_ARG, "exq_kv_copy_pages")
     _here("exq_kv_copy_pages", cache.device, pairs.get_device())
-    _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2, _stream_ptr(stream)),
+    _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2,
+                                  _stream_ptr(stream, cache.device)),
            "exq_kv_copy_pages")
 
 

@@ -362,11 +362,10 @@ __device__ __forceinline__ constexpr float attn_lag() {
   return B == 16 ? 8.f : 12.f;
 }
 
-// The exponent of a V scale (an fp16 value): 2^e <= |v| < 2^(e + 1), within
-// fp16's range also for zeros and infinities.
+// The exponent of a V scale (an fp16 value): 2^e <= |v| < 2^(e + 1), -24 (fp16's
+// least) for 0; planted in the mantissa of 2^23 rather than converted.
 __device__ __forceinline__ float attn_value_exponent(float v) {
-  const int e = static_cast<int>((__float_as_uint(v) >> 23) & 255u) - 127;
-  return static_cast<float>(max(-24, min(16, e)));
+  return fmaxf(-24.f, __uint_as_float(0x4B000000u | ((__float_as_uint(v) >> 23) & 255u)) - (8388608.f + 127.f));
 }
 
 // A sum of weights of 0 is that of a row that has seen nothing (yet). A NaN

@@ -81,12 +81,12 @@ struct Cfg {
   static constexpr int kOffPacked = kOffQ + kRows * D * 2;
   // a packed stage is one tile of K or of V with its scales
   static constexpr int kPacked = B == 16 ? 0 : (Packed::kArray + Packed::kScale + 1023) / 1024 * 1024;
-  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 2 * kTile * 4 - 64 - kStreams * 4 * 2048 -
+  static constexpr int kRoom = 227 * 1024 - 1024 - kOffPacked - 4 * 3 * kTile * 4 - 64 - kStreams * 4 * 2048 -
                                kThreads / 32 * static_cast<int>(sizeof(AttnState)) - 512;
   static constexpr int kPackedFit = B == 16 ? 0 : kRoom / kPacked;
   static constexpr int kPackedStages = kPackedFit > 8 ? 8 : kPackedFit;
-  static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32
-  static constexpr int kOffExps = kOffScale + 4 * 2 * kTile * 4;          // [4][2]: V's exponents
+  static constexpr int kOffScale = kOffPacked + kPackedStages * kPacked;  // [4][sk, sv][kTile] fp32, [4][kTile] sv's exponents
+  static constexpr int kOffExps = kOffScale + 4 * 3 * kTile * 4;          // [4][2]: V's largest exponents
   static constexpr int kOffStage = kOffExps + 64;                         // 32 rows of 64 bytes a softmax warp
   static constexpr int kOffState = kOffStage + kStreams * 4 * 2048;       // a warp's place each
   static constexpr int kOffBar = kOffState + kThreads / 32 * static_cast<int>(sizeof(AttnState));
@@ -650,6 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (which) {
                 const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, bits) >> 10) & 31;
                 if (lane == 0) exps[2 * (g & 3) + (tid >> 5)] = e;
+                // once here: computed in the softmax, code that a unit runs once or
+                // twice, a prompt of 2048 tokens took 149 us for 142 (Q4)
+                scales[(8 + (g & 3)) * T + tid] = attn_value_exponent(half_bits_to_float(bits));
                 if (!attn_finite(bits)) {
                   scales[2 * (g & 3) * T + tid] = NAN;
                   scales[(2 * (g & 3) + 1) * T + tid] = 0.f;
@@ -802,14 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < T / 8; ++j) {
               float2 ex;
               if constexpr (kQuant) {
-                const float2 v2 = *reinterpret_cast<const float2*>(sv + 8 * j);
-                ex = make_float2(attn_value_exponent(v2.x), attn_value_exponent(v2.y));
+                ex = *reinterpret_cast<const float2*>(scales + (8 + (g & 3)) * T + col2 + 8 * j);
               }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t* v = &r[k >> 1][4 * j + 2 * (k & 1)];
                 float2 u = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                if constexpr (kQuant) u.x += ex.x, u.y += ex.y;
+                if constexpr (kQuant) u = unpack_f2(add_f2(pack_f2(u.x, u.y), pack_f2(ex.x, ex.y)));
                 mx[k] = fmaxf(mx[k], fmaxf(u.x, u.y));
               }
             }

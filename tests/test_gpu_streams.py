@@ -138,3 +138,23 @@ def test_results_on_another_stream_do_not_meet_pending_work_on_this_one(env, wha
         got = call(stream=handle)
         torch.cuda.synchronize()
         assert torch.equal(got, want), what
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_the_default_workspace_survives_a_timeout(env, new):
+    # a call whose waits run out leaves the counters of shared units as it found them: the next one needs no fresh workspace
+    exq, torch = env
+    cache, batch, q = _long_sequence(exq, torch, tokens=3000, new=new)
+    want = exq.exq_paged_attn(cache, batch, q)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    exq.exq_testing_starve(64)
+    try:
+        exq.exq_paged_attn(cache, batch, q)
+        assert exq.exq_get_last_device_error() == exq.EXQ_ERR_TIMEOUT
+    finally:
+        exq.exq_testing_starve(0)
+    kept = exq.exq._attn_ws[0, torch.cuda.current_stream().cuda_stream]
+    assert int(kept[:65536].count_nonzero()) == 0
+    for _ in range(2):
+        assert torch.equal(exq.exq_paged_attn(cache, batch, q), want)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK

@@ -527,11 +527,11 @@ def rope_table(R: int, layout: int = ROPE_HALF, device="cuda", **freqs) -> Rope:
 
 
 def _rows(x, where: str, D: Optional[int] = None, heads: Optional[int] = None, tokens: Optional[int] = None):
-    """Descriptor of fp16 [tokens, heads, D] on the GPU with a contiguous last axis."""
+    """Descriptor of fp16 [tokens, heads, D] with a contiguous last axis, on the device that _here has seen."""
     import torch
     t, h, d = x.shape
     st, sh, sd = x.stride()
-    if (not x.is_cuda or x.dtype != torch.float16 or (sd != 1 and d > 1) or (D is not None and d != D)
+    if (x.dtype != torch.float16 or (sd != 1 and d > 1) or (D is not None and d != D)
             or (heads is not None and h != heads) or (tokens is not None and t < tokens)):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     return exq_rows(x.data_ptr(), st, sh)
@@ -565,19 +565,16 @@ class KVCache:
         shape = k_codes.shape
         L, P, H, S, W = shape
         quantised = bits != 16
-        if (not k_codes.is_cuda or not v_codes.is_cuda or k_codes.dtype != torch.int32 or v_codes.dtype != torch.int32
+        self.device = dev = k_codes.get_device()
+        if (dev < 0 or v_codes.get_device() != dev or k_codes.dtype != torch.int32 or v_codes.dtype != torch.int32
                 or v_codes.shape != shape or W * 32 % bits
                 or not k_codes.is_contiguous() or not v_codes.is_contiguous()
                 or (k_scales is not None) != quantised or (v_scales is not None) != quantised):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
-        if quantised and (not k_scales.is_cuda or not v_scales.is_cuda
+        if quantised and (k_scales.get_device() != dev or v_scales.get_device() != dev
                           or k_scales.dtype != torch.float16 or v_scales.dtype != torch.float16
                           or k_scales.shape != shape[:4] or v_scales.shape != shape[:4]
                           or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
-            raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
-        self.device = k_codes.get_device()
-        if v_codes.get_device() != self.device or (quantised and (k_scales.get_device() != self.device
-                                                                  or v_scales.get_device() != self.device)):
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVCache")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.bits, self.D, self.n_kv_heads, self.page_size, self.n_pages, self.n_layers = bits, W * 32 // bits, H, S, P, L
@@ -603,13 +600,11 @@ class KVBatch:
         B, pages = page_table.shape
         import torch
         i32 = torch.int32
-        if (not (q_start.is_cuda and kv_len.is_cuda and page_table.is_cuda) or q_start.dtype != i32
+        self.device = dev = q_start.get_device()
+        if (dev < 0 or kv_len.get_device() != dev or page_table.get_device() != dev or q_start.dtype != i32
                 or kv_len.dtype != i32 or page_table.dtype != i32 or q_start.shape != (B + 1,)
                 or kv_len.shape != (B,) or not q_start.is_contiguous() or not kv_len.is_contiguous()
                 or not page_table.is_contiguous()):
-            raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
-        self.device = q_start.get_device()
-        if kv_len.get_device() != self.device or page_table.get_device() != self.device:
             raise ExqError(EXQ_ERR_INVALID_ARG, "KVBatch")
         self.q_start, self.kv_len, self.page_table, self.n_tokens = q_start, kv_len, page_table, n_tokens
         self._rest = max_q_len, max_kv_len, pages, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()
@@ -650,7 +645,7 @@ def exq_kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Optional[R
         if q_out is None:
             q_out = _empty(q.shape, torch.float16, q.device, stream)
         qp, op = ctypes.byref(_rows(q, where, D, None, T)), ctypes.byref(_rows(q_out, where, D, heads, T))
-    if pos is not None and (not pos.is_cuda or pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
+    if pos is not None and (pos.numel() < T or pos.dtype != torch.int32 or not pos.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_kv_append(ctypes.byref(cache._desc), layer, ctypes.byref(batch.desc(T)), ctypes.byref(kr),
                               ctypes.byref(vr), None if rope is None else ctypes.byref(rope._desc),
@@ -681,7 +676,7 @@ def exq_paged_attn(cache: KVCache, batch: KVBatch, q, out=None, scale: Optional[
     if out is None:
         out = _empty(q.shape, torch.float16, q.device, stream)
     qr, orow = _rows(q, where, cache.D), _rows(out, where, cache.D, H, T)
-    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() < T * H or not lse.is_contiguous()):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     c, b, handle = ctypes.byref(cache._desc), ctypes.byref(batch.desc(T)), _stream_ptr(stream, dev)
     if workspace is None:

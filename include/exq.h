@@ -406,7 +406,9 @@ exq_status exq_rope_freqs(int32_t R, double base, int32_t scaling, double factor
 /* exq_rope_steps -- host-only, synchronous: frequencies (radians per
  * position) as fixed-point turns, steps_out[j] = frac(f_j / 2 pi) in units of
  * 2^-64. The kernels multiply a step by the position in 64-bit integers, and
- * the overflow drops whole turns, so far positions lose no precision.
+ * the overflow drops whole turns, so that the product is exact for the step as
+ * it is, however far the position. The step itself carries the rounding of
+ * f / 2 pi in doubles (2^-53 of it and 2^-53 turns at most), times the position.
  * EXQ_ERR_INVALID_ARG for NULL buffers, n <= 0 or a frequency that is not
  * finite. */
 exq_status exq_rope_steps(const double* inv_freq, int32_t n, uint64_t* steps_out);

@@ -51,7 +51,7 @@ Plan plan_of(const exq_kv_cache& c, const exq_kv_batch& b, int n_heads) {
   p.chunk = p.rows > p.few;
   // Sequences of both kinds, as far as the host can tell: each launch passes
   // over the other's. A chunk of 2048 tokens with 63 single tokens over 4000
-  // cached (Q4, 8 KV heads): 265 us, 423 with all of them in the
+  // cached (Q4, 8 KV heads): 267 us, 423 with all of them in the
   // tensor-memory kernel; with 31 of 32 KV heads: 225 us, 583. Prompts of mixed
   // lengths pay 4 us for the second launch.
   const bool mixed = p.chunk && b.n_tokens < static_cast<long long>(b.n_seqs) * b.max_q_len && b.n_seqs > 1;
@@ -115,9 +115,11 @@ exq_status launch_paged_attn(const AttnCall& call, int sms, cudaStream_t stream)
   if (plan.rows > 0x7FFFFF00ll || plan.rows / 8 * b.n_seqs > 0x7FFFFF00ll)
     return EXQ_ERR_UNSUPPORTED;  // row and block numbers have 32 bits
   a.min_tiles = 2;  // 10 us for one sequence of 500 tokens, 15 at ten
-  // What a unit's queries, joins and stores take, in tiles: packed-code kernel,
-  // 32 ragged sequences Q4: 61 us at 0, 45 at 4 to 8; tensor-memory kernel,
-  // prompts of 3500 tokens in a window: 360 us at 0, 245 at 12.
+  // What a unit's queries, joins and stores take, in tiles. Packed-code kernel,
+  // us at 3, 6 and 12: 32 ragged sequences Q4 48, 44, 46 (61 at 0); 16 of 4000,
+  // 32 KV heads 48, 47, 49; 40 of 3000, D = 64 Q8 19, 18, 18; 24 of 5000 fp16 62,
+  // 56, 56. Tensor-memory kernel at 6, 12 and 24: prompts of 3500 in a window
+  // 233, 230, 239 (360 at 0); 4 of 3000, D = 64 Q8 88, 86, 97; 3 of 900 Q4 84, 85, 81.
   if (plan.chunk) {
     a.rows_above = plan.split ? plan.few : 0;
     a.rows_upto = static_cast<int>(plan.rows);

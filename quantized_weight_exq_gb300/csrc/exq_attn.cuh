@@ -346,8 +346,11 @@ __device__ __forceinline__ void attn_put_back(const AttnArgs& a, const AttnPiece
 }
 
 // References of the softmax. Weights are multiplied by V's scales and rounded
-// to fp16 for the matrix instructions, so what has to stay in fp16's normal
-// range is that product: a row's reference is the largest score plus the
+// to fp16 for the matrix instructions: the one rounding to fewer than 32 bits
+// before the result's own. (Results are 2.4e-4 to 3.1e-4 of their size off the
+// 64-bit ones, 2.1e-4 with their own rounding alone; a second product with the
+// remainders would take the matrix instructions of P V twice.) What has to stay
+// in fp16's normal range is that product: a row's reference is the largest score plus the
 // exponent of its token's V scale (0 for fp16 pages), over the tokens that the
 // row sees, and is raised where one exceeds it by more than attn_lag. Weights
 // up to 2^lag have the same relative precision; those whose product falls

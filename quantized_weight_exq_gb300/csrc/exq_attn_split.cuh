@@ -31,7 +31,7 @@
 // it. Slots past the last token are masked in S, and V's (fp16) zeroed.
 //
 // 8 KV heads of 128, 8 query heads each: one sequence of 131072 tokens Q8 (273
-// MB) 61 us, 4.5 TB/s, 67 % of the copy rate; 32 ragged ones up to 8192
+// MB) 61 us, 4.4 TB/s, 66 % of the copy rate; 32 ragged ones up to 8192
 // Q4 (152 MB) 44 us, half of it at the copy rate, the rest unpacking, starts
 // and joins; one of 500 tokens 10 us.
 #pragma once
@@ -819,8 +819,11 @@ exq_status launch(const AttnCall& call, const AttnArgs& a, int sms, cudaStream_t
       }))
     return EXQ_ERR_CUDA;
   // Units cut into more than 32 pieces take two CTAs an SM: fewer pieces to
-  // join (131072 tokens of 8 KV heads: Q8 61 us, 65 with three; Q4 48, 50). With
-  // 16 sequences' units instead two cost more than they gain (23 us against 22).
+  // join. us with two and with all, D = 128 (three): 8 units of 131072 tokens Q8
+  // 62 / 66, Q4 48.5 / 49.4, of 16384 Q4 20 / 26; past the limit 16 units of up
+  // to 131072 Q4 66 / 64, Q8 88 / 90, 32 units of 32768 Q4 43.6 / 40.3. D = 64
+  // (four), Q4: 4 units of 131072 37 / 51, 12 40 / 43, 16 53 / 49 (of 16384 18 /
+  // 25); past the limit 24 of 65536 32 / 33.
   const long long units = static_cast<long long>(a.n_seqs) * a.row_blocks * a.n_kv_heads;
   const int ctas = units * 32 < static_cast<long long>(sms) * C::kCtas ? std::min(C::kCtas, 2) : C::kCtas;
   fn<<<std::min(sms * ctas, kAttnMaxCtas), kThreads, C::kSmem, stream>>>(maps, a);

@@ -395,9 +395,11 @@ __device__ __forceinline__ void rotate_lane(uint32_t (&h)[VPL], const Turn<VPL>&
   }
 }
 
-// 2 bytes read a value, 2 or B / 8 written: bound by instruction issue for
-// many tokens (4 sequences of up to 2048, 64 + 8 + 8 heads of 128, Q8: 60 us
-// for 177 MB, 59 % of the issue slots), by latency for one (7 us): a block
+// 2 bytes read a value, 2 or B / 8 written. Many tokens (4 sequences of up to
+// 2048, 64 + 8 + 8 heads of 128, Q8) take 60 us for 177 MB, 2.9 TB/s: neither
+// HBM nor the issue slots (59 %) are full, a warp waits for loads and for the
+// steps of a row's codec, maximum, quotient, exchange, one after the other.
+// One token takes 7 us, the launch and its dependent steps: a block
 // holds 1 .. 8 tokens, each done by 8 / tokens of its warps, and where tokens
 // are few the rows of a token are split over blocks. A warp does a row (one
 // head of q, k or v) at a time, with the loads of kU rows of each of q, k and

@@ -175,8 +175,10 @@ exq_status launch_rope(const exq_rope_params& rope, const exq_rows& x, long long
   int tokens = std::max(1, kThreads / (rope.R / 2));
   if (vec) tokens = std::min(tokens, kThreads / a.units);
   // at most 4 tokens a block (8 left a second, part-filled wave of blocks: 77
-  // for 54 us at 8000 tokens of 64 half-turned heads), fewer while there is
-  // not a block for each SM twice over
+  // for 54 us at 8000 tokens of 64 half-turned heads; fully turned 50 and 50,
+  // 55 with two; 8 heads of 64, 16000 tokens: 37 with four, 28 with eight; 16 of
+  // 256, 4000: 26 and 28), fewer while there is not a block for each SM twice
+  // over
   tokens = std::min(tokens, 4);
   while (tokens > 1 && n_tokens < 2ll * sms * tokens) tokens /= 2;
   a.tokens_per = tokens;

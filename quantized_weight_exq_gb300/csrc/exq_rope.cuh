@@ -12,7 +12,7 @@ namespace exq {
 // turn is split into the nearest quarter q and a remainder |r| <= 1/8 turn,
 // and cos, sin of x = 2 pi r, |x| <= pi/4, come from their Taylor polynomials
 // in fp64: up to x^13 for sin and x^14 for cos, whose first dropped terms are
-// below 2^-45 and 2^-49 of the result. fp64 because the rounding to fp32 then
+// at most 2^-44.9 and 2^-49 of the result. fp64 because the rounding to fp32 then
 // agrees with the correctly rounded one but for about one angle in 2^20: the
 // rotated values, and with them the KV codes, are the same bits wherever they
 // are computed. The kernels evaluate each (token, pair) once per block, in

@@ -782,6 +782,6 @@ def exq_get_last_device_error(stream=None) -> int:
 
 def exq_testing_starve(wait_rounds: int) -> None:
     """Failure-detection test hook (include/exq_testing.h): while wait_rounds
-    > 0, GEMV / GEMM launches issue no copies and their bounded waits give up
+    > 0, GEMV / GEMM / paged attention launches issue no copies and their bounded waits give up
     after wait_rounds rounds, so the call ends in EXQ_ERR_TIMEOUT; 0 = off."""
     _lib.exq_testing_starve(int(wait_rounds))

@@ -45,6 +45,7 @@ def test_a_graph_keeps_the_default_workspace_it_was_captured_with(env):
     w = _layer(exq, 512, 256)
     x = torch.from_numpy(synth.activations(1, 512, seed=1)).cuda()
     y = torch.empty(1, 256, dtype=torch.float16, device="cuda")
+    before = mod._gemv_ws.pop(0, None)                   # whatever earlier tests have grown it to
     exq.exq_gemv(w, x, y)
     want = y.clone()
     held = mod._gemv_ws[0]
@@ -63,7 +64,7 @@ def test_a_graph_keeps_the_default_workspace_it_was_captured_with(env):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
-    del ones
+    del ones, before
 
 
 def test_attention_on_several_streams_without_a_workspace(env):

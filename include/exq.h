@@ -634,6 +634,150 @@ exq_status exq_measure_exl2(const uint16_t* W, const int32_t* perm, int32_t K, i
  * budget below 2 * S. */
 exq_status exq_solve_exl2_bits(const double* err, int32_t S, int64_t budget, uint8_t* bits_out);
 
+/* ---------------------------------------------------------------- microscaled 4-bit floating point */
+
+/* A matrix [rows, K] of e2m1 codes (bit 3 the sign; magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 for codes 0..7) with one scale byte for each block along K:
+ *  E4M3  blocks of 16, the scale an e4m3 number (without sign), and one fp32
+ *        factor for the whole matrix: value = e2m1(code) * scale * factor
+ *  E8M0  blocks of 32, the scale 2^(byte - 127): value = e2m1(code) * scale
+ * A NaN scale (e4m3 0x7f, e8m0 0xff) makes its block NaN. Layout:
+ *  - codes uint8 [rows, K/2]: byte j holds k = 2j in its low and 2j + 1 in its
+ *    high half.
+ *  - scales uint8, tiles of 128 rows x 4 blocks (512 bytes): row r and block j
+ *    of a tile are its byte (r % 32) * 16 + (r / 32) * 4 + j. The tiles of the
+ *    first 128 rows come first, in order of K. Where a tile reaches over the
+ *    matrix its bytes are zero (exq_pack_fp4 and exq_fp4_quantize write them).
+ * K % 32 == 0 (a row's codes are then a multiple of 16 bytes). */
+typedef enum { EXQ_FP4_E4M3 = 1, EXQ_FP4_E8M0 = 2 } exq_fp4_format;
+
+typedef struct {
+  int32_t format; /* exq_fp4_format                                            */
+  int32_t rows;
+  int32_t K;
+  float factor;   /* E4M3: of the whole matrix, 2^-60 .. 2^60; E8M0: 1            */
+  uint8_t* codes; /* device [rows, K/2]                                        */
+  uint8_t* scales;/* device, exq_fp4_scale_bytes(format, rows, K)              */
+} exq_fp4_matrix;
+
+/* Bytes of a matrix's scales: 512 * ceil(rows / 128) * ceil(K / (4 * block)).
+ * 0 for an unknown format, rows <= 0, K <= 0 or K % 32. */
+size_t exq_fp4_scale_bytes(int32_t format, int32_t rows, int32_t K);
+
+/* exq_pack_fp4 -- host-only, synchronous: codes uint8 [rows, K] (0..15) and
+ * scale bytes uint8 [rows, K / block] to the layout above.
+ * EXQ_ERR_INVALID_ARG for NULL buffers, bad sizes, a code above 15 or an e4m3
+ * scale with its sign set; outputs are then unspecified. */
+exq_status exq_pack_fp4(const uint8_t* codes, const uint8_t* scales, int32_t format, int32_t rows, int32_t K,
+                        uint8_t* codes_out, uint8_t* scales_out);
+
+/* exq_fp4_quantize -- device, asynchronous: x fp16 [rows, K] into out's codes
+ * and scales (out's format, sizes and factor are given, its memory is written
+ * whole). With a the largest magnitude of a block:
+ *  E4M3  s = the e4m3 number nearest to a / (6 factor), ties to even, at most
+ *        448, at least 2^-9 (0 for a block of zeros)
+ *  E8M0  s = 2^(floor(log2 a) - 2) (2^-127 for a block of zeros)
+ * and each code is the e2m1 number nearest to x / (s factor), ties to the even
+ * code, at most 6 in magnitude, with x's sign. Both are decided exactly, not
+ * on rounded quotients. A block that holds a NaN or an infinity gets the NaN
+ * scale and codes 0. rows = 0 launches nothing.
+ * EXQ_ERR_INVALID_ARG for bad pointers (16 bytes), sizes or a factor out of range. */
+exq_status exq_fp4_quantize(const uint16_t* x, const exq_fp4_matrix* out, void* stream);
+
+/* exq_fp4_dequantize -- device, asynchronous: out fp16 [rows, K],
+ * fp16_RNE(fp32_RNE(value)); the same rules. */
+exq_status exq_fp4_dequantize(const exq_fp4_matrix* m, uint16_t* out, void* stream);
+
+/* Bytes of device workspace exq_fp4_gemm needs (0 if none): fp32 partial sums
+ * of a split along K, where there are fewer output tiles than SMs. */
+size_t exq_fp4_gemm_workspace_size(const exq_fp4_matrix* a, const exq_fp4_matrix* w);
+
+/* exq_fp4_gemm -- device, asynchronous: y fp16 [a.rows, w.rows],
+ *   y[m][n] = fp16_RNE(a.factor * w.factor * sum_k a[m][k] w[n][k]),
+ * on the block-scaled tcgen05 tensor cores, sums in fp32. a and w have one
+ * format and one K; any a.rows (0 launches nothing), w.rows % 8 == 0.
+ *   workspace  at least exq_fp4_gemm_workspace_size() bytes, 256-byte aligned
+ *              (NULL when that is 0); scratch. Calls that may overlap on the
+ *              GPU need separate workspaces.
+ * A row of a (w) with a NaN scale has a NaN row (column) of y, no other.
+ * Deterministic: the same inputs give the same bits on the same device.
+ * EXQ_ERR_INVALID_ARG for bad pointers, sizes, formats or a short workspace. */
+exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/* The workspaces of exq_fp4_gemv and exq_moe start with counters: ZERO-FILL
+ * this many bytes before the first use. Every call that completes leaves them
+ * zero, so that one workspace serves any sequence of calls of either on one
+ * stream; one that ended in EXQ_ERR_TIMEOUT may not: zero-fill them again. */
+#define EXQ_FP4_COUNTER_BYTES ((size_t)128 << 10)
+
+/* Bytes of device workspace exq_fp4_gemv needs on the current device; 0 for an
+ * invalid matrix or M outside 1..16. */
+size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M);
+
+/* exq_fp4_gemv -- device, asynchronous: y fp16 [M, w.rows] = x . w^T for a few
+ * rows x fp16 [M, K] as they are (not quantised), 1 <= M <= 16; products and
+ * sums in fp32, w.factor and one rounding at the end. The codes are read once.
+ *   workspace  as above, 256-byte aligned; calls that may overlap on the GPU
+ *              need separate ones.
+ * w.rows % 8 == 0. Deterministic on the same device. EXQ_ERR_UNSUPPORTED for
+ * M > 16 (use exq_fp4_gemm) or more than 4,194,176 rows; EXQ_ERR_INVALID_ARG for
+ * M < 1, bad pointers, sizes or workspace. */
+exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, int32_t M, uint16_t* y, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- mixture of experts, few tokens */
+
+/* One matrix [rows, K] for each expert, in the 4-bit layout above: expert e's
+ * codes at codes + e * rows * K / 2, its scales at scales + e *
+ * exq_fp4_scale_bytes(format, rows, K). */
+typedef struct {
+  int32_t format, n_experts, rows, K;
+  const uint8_t* codes;  /* device [n_experts, rows, K/2]                      */
+  const uint8_t* scales; /* device                                            */
+  const float* factors;  /* device fp32 [n_experts], or NULL: all 1 (E8M0: NULL) */
+} exq_fp4_experts;
+
+/* What the gate's product goes through before it is multiplied by up's. */
+typedef enum { EXQ_ACT_SILU = 0, EXQ_ACT_GELU_TANH = 1 } exq_activation;
+
+typedef struct {
+  exq_fp4_experts gate, up, down; /* [I, D], [I, D], [D, I], one format          */
+  const uint16_t* router;         /* device fp16 [n_experts, D], or NULL         */
+  int32_t top_k;                  /* experts of a token, 1 .. min(16, n_experts) */
+  int32_t renorm;                 /* 1: weights are a softmax over the chosen logits, 0: over all */
+  int32_t act;                    /* exq_activation                             */
+} exq_moe_layer;
+
+/* Bytes of device workspace exq_moe needs on the current device; 0 for an
+ * invalid layer or T outside 1..16. */
+size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T);
+
+/* exq_moe -- device, asynchronous: a layer of experts for a few tokens x fp16
+ * [T, D], 1 <= T <= 16:
+ *   logits = x . router^T (fp32); ids[t] = the top_k largest, largest first,
+ *   ties (and NaNs, which count as -infinity) to the lowest index;
+ *   weights[t][j] = exp(logit - max) / sum (see renorm);
+ *   y[t] = fp16_RNE(sum_j weights[t][j] * (act(x gate^T) * (x up^T)) down^T)
+ * with the experts' products over x as it is and fp32 sums. What lies between
+ * the products is held as the sum of two fp16 numbers times a power of two for
+ * each 128 values (22 bits of the largest); weights and factors are applied in
+ * fp32 after the sums.
+ *   ids      device int32 [T, top_k], weights device fp32 [T, top_k]: written
+ *            when the layer has a router, read when it has none. An id of -1
+ *            is an unused place; one that repeats counts each time; another
+ *            one outside 0 .. n_experts - 1 is skipped and reported as
+ *            EXQ_ERR_INVALID_ARG in the device error word. A token without
+ *            experts gets zeros.
+ *   y        device fp16 [T, D], fully overwritten
+ *   workspace  as for exq_fp4_gemv.
+ * Only the chosen experts are read, each once. D % 32 == 0, I % 32 == 0, at
+ * most 512 experts. Deterministic on the same device. EXQ_ERR_UNSUPPORTED for
+ * T > 16, more than 512 experts, top_k > 16 or sizes whose tiles outnumber the counters;
+ * EXQ_ERR_INVALID_ARG for anything else out of range. */
+exq_status exq_moe(const exq_moe_layer* layer, const uint16_t* x, int32_t T, int32_t* ids, float* weights, uint16_t* y,
+                   void* workspace, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Static, NUL-terminated description of a status code. */
@@ -642,8 +786,8 @@ const char* exq_status_string(exq_status s);
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device: EXQ_OK, EXQ_ERR_TIMEOUT (a kernel gave up waiting) or
  * EXQ_ERR_INVALID_ARG (a kernel met an EXL2 segment width outside the set or
- * past the end of qweight, a permutation entry outside [0, K), or a page id
- * or length of a paged cache out of range).
+ * past the end of qweight, a permutation entry outside [0, K), a page id or
+ * length of a paged cache out of range, or an expert's index out of range).
  * Returns EXQ_ERR_CUDA if the synchronisation itself fails. */
 exq_status exq_get_last_device_error(void* stream);
 

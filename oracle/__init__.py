@@ -5,3 +5,4 @@ reference legs may import this package. The product path never does.
 """
 from .exq_oracle import *  # noqa: F401,F403
 from .paged_oracle import *  # noqa: F401,F403
+from .fp4_oracle import *  # noqa: F401,F403

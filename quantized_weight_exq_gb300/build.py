@@ -18,7 +18,7 @@ LIB = PKG / "libexq.so"
 
 SOURCES = ["exq_api.cu", "exq_gemv.cu", "exq_dequant.cu", "exq_gemm.cu", "exq_kv.cu", "exq_convert.cu", "exq_rope.cu",
            "exq_attn.cu", *(f"exq_attn_{kind}{bits}.cu" for kind in ("split", "chunk") for bits in (4, 6, 8, 16)),
-           "exq_pack.cpp", "exq_pages.cpp"]
+           "exq_fp4_quant.cu", "exq_fp4_gemm.cu", "exq_fp4_stream.cu", "exq_pack.cpp", "exq_pages.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

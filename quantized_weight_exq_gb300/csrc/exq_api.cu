@@ -42,7 +42,8 @@ EncodeTiled tensor_map_encoder() {
 }
 
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
-               uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapL2promotion promotion) {
+               uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapL2promotion promotion,
+               CUtensorMapSwizzle swizzle) {
   EncodeTiled enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t gdim[2] = {inner, outer};
@@ -50,7 +51,7 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uin
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t es[2] = {1, 1};
   return enc(map, type, 2, const_cast<void*>(base), gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_NONE, promotion,
+             swizzle, promotion,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -401,6 +402,143 @@ extern "C" exq_status exq_measure_exl2(const uint16_t* W, const int32_t* perm, i
   return launch_rtn_measure(W, perm, K, N, err_out, workspace, static_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------- microscaled 4-bit floating point
+
+namespace {
+
+// block size of a format, 0 for an unknown one
+int fp4_block_of(int format) { return format == EXQ_FP4_E4M3 ? 16 : format == EXQ_FP4_E8M0 ? 32 : 0; }
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+exq_status check_fp4(const exq_fp4_matrix* m) {
+  if (!m || !fp4_block_of(m->format) || m->rows < 0 || m->K <= 0 || m->K % 32) return EXQ_ERR_INVALID_ARG;
+  if (m->format == EXQ_FP4_E8M0 ? m->factor != 1.f : !(m->factor >= 0x1p-60f && m->factor <= 0x1p60f))
+    return EXQ_ERR_INVALID_ARG;
+  if (m->rows == 0) return EXQ_OK;  // its memory is not looked at
+  if (!m->codes || !m->scales || !aligned16(m->codes) || !aligned16(m->scales)) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+exq_status check_fp4_product(const exq_fp4_matrix* a, const exq_fp4_matrix* w) {
+  exq_status st = check_fp4(w);
+  if (st != EXQ_OK || (st = check_fp4(a)) != EXQ_OK) return st;
+  if (w->rows <= 0 || w->rows % 8 || a->format != w->format || a->K != w->K) return EXQ_ERR_INVALID_ARG;
+  return EXQ_OK;
+}
+
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+}  // namespace
+
+extern "C" size_t exq_fp4_scale_bytes(int32_t format, int32_t rows, int32_t K) {
+  const int block = fp4_block_of(format);
+  if (!block || rows <= 0 || K <= 0 || K % 32) return 0;
+  return static_cast<size_t>(512) * ((static_cast<size_t>(rows) + 127) / 128) * ((static_cast<size_t>(K) + 4 * block - 1) / (4 * block));
+}
+
+extern "C" exq_status exq_fp4_quantize(const uint16_t* x, const exq_fp4_matrix* out, void* stream) {
+  const exq_status st = check_fp4(out);
+  if (st != EXQ_OK || out->rows == 0) return st;
+  if (!x || !aligned16(x)) return EXQ_ERR_INVALID_ARG;
+  if (current_cc() < 100) return EXQ_ERR_CUDA;
+  return launch_fp4_quantize(x, *out, current_sms(), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" exq_status exq_fp4_dequantize(const exq_fp4_matrix* m, uint16_t* out, void* stream) {
+  const exq_status st = check_fp4(m);
+  if (st != EXQ_OK || m->rows == 0) return st;
+  if (!out || !aligned16(out)) return EXQ_ERR_INVALID_ARG;
+  if (current_cc() < 100) return EXQ_ERR_CUDA;
+  return launch_fp4_dequantize(*m, out, current_sms(), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t exq_fp4_gemm_workspace_size(const exq_fp4_matrix* a, const exq_fp4_matrix* w) {
+  const int sms = current_sms();
+  if (check_fp4_product(a, w) != EXQ_OK || a->rows == 0 || sms <= 0) return 0;
+  return fp4_gemm_workspace_bytes(*a, *w, sms);
+}
+
+extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  const exq_status st = check_fp4_product(a, w);
+  if (st != EXQ_OK || a->rows == 0) return st;
+  if (!y || !aligned16(y)) return EXQ_ERR_INVALID_ARG;
+  const int sms = current_sms();
+  if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
+  const size_t need = fp4_gemm_workspace_bytes(*a, *w, sms);
+  if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return EXQ_ERR_INVALID_ARG;
+  return launch_fp4_gemm(*a, *w, y, workspace, ws_bytes, sms, current_device(), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M) {
+  const int sms = current_sms();
+  if (check_fp4(w) != EXQ_OK || w->rows <= 0 || w->rows % 8 || M < 1 || M > 16 || sms <= 0) return 0;
+  return fp4_gemv_workspace_bytes(M, sms);
+}
+
+extern "C" exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, int32_t M, uint16_t* y, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  const exq_status st = check_fp4(w);
+  if (st != EXQ_OK) return st;
+  if (w->rows <= 0 || w->rows % 8 || M < 1 || !x || !y || !aligned16(x) || !aligned16(y)) return EXQ_ERR_INVALID_ARG;
+  if (M > 16 || !fp4_gemv_fits(w->rows)) return EXQ_ERR_UNSUPPORTED;
+  const int sms = current_sms();
+  if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
+  if (!workspace || !aligned256(workspace) || ws_bytes < fp4_gemv_workspace_bytes(M, sms)) return EXQ_ERR_INVALID_ARG;
+  return launch_fp4_gemv(*w, x, M, y, workspace, sms, current_device(), static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- mixture of experts
+
+namespace {
+
+exq_status check_experts(const exq_fp4_experts& p, int format, int n, int rows, int K) {
+  if (p.format != format || p.n_experts != n || p.rows != rows || p.K != K) return EXQ_ERR_INVALID_ARG;
+  if (!p.codes || !p.scales || !aligned16(p.codes) || !aligned16(p.scales) || !aligned4(p.factors)) return EXQ_ERR_INVALID_ARG;
+  if (format == EXQ_FP4_E8M0 && p.factors) return EXQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(n) * rows > 0x7FFFFF00LL) return EXQ_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+  return EXQ_OK;
+}
+
+exq_status check_moe(const exq_moe_layer* l, int T) {
+  if (!l || T < 1) return EXQ_ERR_INVALID_ARG;
+  const int n = l->gate.n_experts, I = l->gate.rows, D = l->gate.K;
+  if (!fp4_block_of(l->gate.format) || n <= 0 || I <= 0 || I % 32 || D <= 0 || D % 32) return EXQ_ERR_INVALID_ARG;
+  exq_status st = check_experts(l->gate, l->gate.format, n, I, D);
+  if (st != EXQ_OK || (st = check_experts(l->up, l->gate.format, n, I, D)) != EXQ_OK ||
+      (st = check_experts(l->down, l->gate.format, n, D, I)) != EXQ_OK)
+    return st;
+  if (l->top_k < 1 || l->top_k > n || (l->renorm != 0 && l->renorm != 1) ||
+      (l->act != EXQ_ACT_SILU && l->act != EXQ_ACT_GELU_TANH) || !aligned16(l->router))
+    return EXQ_ERR_INVALID_ARG;
+  if (T > 16 || l->top_k > 16 || n > 512 || !moe_fits(*l, T)) return EXQ_ERR_UNSUPPORTED;
+  return EXQ_OK;
+}
+
+}  // namespace
+
+extern "C" size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T) {
+  const int sms = current_sms();
+  if (check_moe(layer, T) != EXQ_OK || sms <= 0) return 0;
+  return moe_workspace_bytes(*layer, T, sms);
+}
+
+extern "C" exq_status exq_moe(const exq_moe_layer* layer, const uint16_t* x, int32_t T, int32_t* ids, float* weights,
+                              uint16_t* y, void* workspace, size_t ws_bytes, void* stream) {
+  const exq_status st = check_moe(layer, T);
+  if (st != EXQ_OK) return st;
+  if (!x || !y || !ids || !weights || !aligned16(x) || !aligned16(y) || !aligned4(ids) || !aligned4(weights))
+    return EXQ_ERR_INVALID_ARG;
+  const int sms = current_sms();
+  if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
+  if (!workspace || !aligned256(workspace) || ws_bytes < moe_workspace_bytes(*layer, T, sms)) return EXQ_ERR_INVALID_ARG;
+  return launch_moe(*layer, x, T, ids, weights, y, workspace, sms, current_device(), static_cast<cudaStream_t>(stream));
+}
+
 extern "C" const char* exq_status_string(exq_status s) {
   switch (s) {
     case EXQ_OK: return "ok";
@@ -416,11 +554,12 @@ extern "C" const char* exq_status_string(exq_status s) {
 extern "C" exq_status exq_get_last_device_error(void* stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned a = take_gemv_errors(s), b = take_dequant_errors(s), c = take_gemm_errors(s),
-                 d = take_convert_errors(s), e = take_kv_errors(s), f = take_attn_errors(s);
-  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u || e == ~0u || f == ~0u) return EXQ_ERR_CUDA;
-  const unsigned v = a | b | c | d | e | f;
+                 d = take_convert_errors(s), e = take_kv_errors(s), f = take_attn_errors(s),
+                 g = take_fp4_stream_errors(s), h = take_fp4_gemm_errors(s);
+  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u || e == ~0u || f == ~0u || g == ~0u || h == ~0u) return EXQ_ERR_CUDA;
+  const unsigned v = a | b | c | d | e | f | g | h;
   if (v & kDevErrTimeout) return EXQ_ERR_TIMEOUT;
-  if (v & (kDevErrBadSegment | kDevErrBadPerm | kDevErrBadPage)) return EXQ_ERR_INVALID_ARG;
+  if (v & (kDevErrBadSegment | kDevErrBadPerm | kDevErrBadPage | kDevErrBadExpert)) return EXQ_ERR_INVALID_ARG;
   return EXQ_OK;
 }
 

@@ -16,6 +16,7 @@ enum : unsigned {
   kDevErrBadSegment = 2u,   // an EXL2 segment width outside {2,3,4,5,6,8} or past the end
   kDevErrBadPerm = 4u,      // a permutation entry outside [0, K)
   kDevErrBadPage = 8u,      // a page id, length or row range of a paged cache out of range
+  kDevErrBadExpert = 16u,   // an expert's index outside [-1, n_experts)
 };
 
 // failure-detection test hook (exq_testing.h): 0 = off, else the wait bound
@@ -37,13 +38,14 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled tensor_map_encoder();
 
-// A 2-D tiled tensor map without swizzle: dims {inner, outer} elements, the
-// outer stride in bytes, box {box_inner, box_outer}; elements outside the
-// tensor read as zero; `promotion` sets how much L2 fetches around each
-// access. False if the driver rejects it.
+// A 2-D tiled tensor map: dims {inner, outer} elements, the outer stride in
+// bytes, box {box_inner, box_outer}; elements outside the tensor read as zero;
+// `promotion` sets how much L2 fetches around each access. False if the driver
+// rejects it.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
                uint64_t outer_stride_bytes, uint32_t box_inner, uint32_t box_outer,
-               CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+               CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // n layers (1..EXQ_GEMV_MAX_LAYERS) of one format and K that share x
 exq_status launch_gemv(const exq_weight* w, int n, const uint16_t* x, int M, uint16_t* const* y, void* workspace,
@@ -90,6 +92,21 @@ struct AttnCall {
 exq_status launch_paged_attn(const AttnCall& c, int sms, cudaStream_t stream);
 size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& batch, int n_heads, int sms);
 
+// microscaled 4-bit floating point (arguments checked by the caller)
+exq_status launch_fp4_quantize(const uint16_t* x, const exq_fp4_matrix& m, int sms, cudaStream_t stream);
+exq_status launch_fp4_dequantize(const exq_fp4_matrix& m, uint16_t* out, int sms, cudaStream_t stream);
+exq_status launch_fp4_gemm(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uint16_t* y, void* workspace,
+                           size_t ws_bytes, int sms, int device, cudaStream_t stream);
+size_t fp4_gemm_workspace_bytes(const exq_fp4_matrix& a, const exq_fp4_matrix& w, int sms);
+exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, uint16_t* y, void* workspace, int sms,
+                           int device, cudaStream_t stream);
+size_t fp4_gemv_workspace_bytes(int M, int sms);
+bool fp4_gemv_fits(int rows);  // whether the row tiles have counters
+exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t* ids, float* weights, uint16_t* y,
+                      void* workspace, int sms, int device, cudaStream_t stream);
+size_t moe_workspace_bytes(const exq_moe_layer& l, int T, int sms);
+bool moe_fits(const exq_moe_layer& l, int T);
+
 // EXL2 conversion: RTN quantiser into the EXL2 layout, and the error table
 exq_status launch_rtn_quantize(const uint16_t* W, const int32_t* perm, int K, int N, const uint32_t* seg_off,
                                int n_word_rows, uint32_t* qweight, uint16_t* scales, cudaStream_t stream);
@@ -105,5 +122,7 @@ unsigned take_gemm_errors(cudaStream_t stream);
 unsigned take_convert_errors(cudaStream_t stream);
 unsigned take_kv_errors(cudaStream_t stream);
 unsigned take_attn_errors(cudaStream_t stream);
+unsigned take_fp4_stream_errors(cudaStream_t stream);
+unsigned take_fp4_gemm_errors(cudaStream_t stream);
 
 }  // namespace exq

@@ -10,6 +10,7 @@
 //
 // EXL2: 32-row segments at widths {2,3,4,5,6,8} (README, "EXL2
 // quantization"); each segment-column is a 32*b-bit little-endian stream.
+#include <algorithm>
 #include <queue>
 #include <utility>
 #include <vector>
@@ -140,6 +141,28 @@ extern "C" exq_status exq_pack_exl2_qscale(const uint8_t* codes, int32_t S, int3
         word |= static_cast<uint32_t>(v) << (4 * i);
       }
       q_scale_out[s * (N / 8) + k] = word;
+    }
+  return EXQ_OK;
+}
+
+// The 4-bit floating point format: codes two to a byte, scale bytes in tiles of
+// 128 rows x 4 blocks, zero where a tile reaches over the matrix.
+extern "C" exq_status exq_pack_fp4(const uint8_t* codes, const uint8_t* scales, int32_t format, int32_t rows, int32_t K,
+                                   uint8_t* codes_out, uint8_t* scales_out) {
+  const size_t bytes = exq_fp4_scale_bytes(format, rows, K);
+  if (!codes || !scales || !codes_out || !scales_out || bytes == 0) return EXQ_ERR_INVALID_ARG;
+  const int64_t n = static_cast<int64_t>(rows) * K;
+  for (int64_t i = 0; i < n; i += 2) {
+    if (codes[i] > 15 || codes[i + 1] > 15) return EXQ_ERR_INVALID_ARG;
+    codes_out[i / 2] = static_cast<uint8_t>(codes[i] | codes[i + 1] << 4);
+  }
+  const int64_t blocks = K / (format == EXQ_FP4_E4M3 ? 16 : 32), across = (blocks + 3) / 4;
+  std::fill(scales_out, scales_out + bytes, static_cast<uint8_t>(0));
+  for (int64_t r = 0; r < rows; ++r)
+    for (int64_t j = 0; j < blocks; ++j) {
+      const uint8_t s = scales[r * blocks + j];
+      if (format == EXQ_FP4_E4M3 && s > 0x7F) return EXQ_ERR_INVALID_ARG;
+      scales_out[(r / 128 * across + j / 4) * 512 + r % 32 * 16 + r % 128 / 32 * 4 + j % 4] = s;
     }
   return EXQ_OK;
 }

@@ -29,6 +29,9 @@ EXQ_FMT_GPTQ4 = 1
 EXQ_FMT_EXL2 = 2
 EXQ_FMT_EXL2_QSCALE = 3
 
+FP4_E4M3, FP4_E8M0 = 1, 2
+ACT_SILU, ACT_GELU_TANH = 0, 1
+
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN, ROPE_SCALE_BANDS = range(5)
 
@@ -41,6 +44,8 @@ EXPORTED = (
     "exq_quantize_exl2", "exq_measure_exl2_workspace_size", "exq_measure_exl2", "exq_solve_exl2_bits",
     "exq_rope_freqs", "exq_rope_steps", "exq_rope", "exq_kv_append", "exq_paged_attn_workspace_size", "exq_paged_attn",
     "exq_kv_copy_pages", "exq_pages_alloc", "exq_pages_free", "exq_pages_fork", "exq_pages_compact",
+    "exq_fp4_scale_bytes", "exq_pack_fp4", "exq_fp4_quantize", "exq_fp4_dequantize", "exq_fp4_gemm_workspace_size", "exq_fp4_gemm",
+    "exq_fp4_gemv_workspace_size", "exq_fp4_gemv", "exq_moe_workspace_size", "exq_moe",
     "exq_testing_starve",
 )
 
@@ -85,6 +90,21 @@ class exq_kv_batch(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")]
 
 
+class exq_fp4_matrix(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("format", "rows", "K")] + [
+        ("factor", ctypes.c_float), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class exq_fp4_experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("format", "n_experts", "rows", "K")] + [
+        (n, ctypes.c_void_p) for n in ("codes", "scales", "factors")]
+
+
+class exq_moe_layer(ctypes.Structure):
+    _fields_ = [(n, exq_fp4_experts) for n in ("gate", "up", "down")] + [("router", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("top_k", "renorm", "act")]
+
+
 def _load():
     if not _LIB_PATH.exists():
         raise ImportError(f"{_LIB_PATH} is not built; run quantized_weight_exq_gb300/build.py "
@@ -125,6 +145,16 @@ def _load():
         "exq_pages_free": (st, [P, i32, P, i32]),
         "exq_pages_fork": (st, [P, i32, i32, P, i32, P, P, P]),
         "exq_pages_compact": (st, [P, i32, P, i64, P, P]),
+        "exq_fp4_scale_bytes": (sz, [i32, i32, i32]),
+        "exq_pack_fp4": (st, [P, P, i32, i32, i32, P, P]),
+        "exq_fp4_quantize": (st, [P, P, P]),
+        "exq_fp4_dequantize": (st, [P, P, P]),
+        "exq_fp4_gemm_workspace_size": (sz, [P, P]),
+        "exq_fp4_gemm": (st, [P, P, P, P, sz, P]),
+        "exq_fp4_gemv_workspace_size": (sz, [P, i32]),
+        "exq_fp4_gemv": (st, [P, P, i32, P, P, sz, P]),
+        "exq_moe_workspace_size": (sz, [P, i32]),
+        "exq_moe": (st, [P, P, i32, P, P, P, P, sz, P]),
         "exq_status_string": (ctypes.c_char_p, [st]),
         "exq_get_last_device_error": (st, [P]),
         "exq_testing_starve": (None, [i32]),
@@ -696,6 +726,249 @@ def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
     _check(_lib.exq_kv_copy_pages(ctypes.byref(cache._desc), pairs.data_ptr(), pairs.numel() // 2,
                                   _stream_ptr(stream, cache.device)),
            "exq_kv_copy_pages")
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floating point
+
+FP4_COUNTER_BYTES = 128 << 10  # EXQ_FP4_COUNTER_BYTES
+
+_fp4_ws = {}  # (device index, stream handle) -> workspace of exq_fp4_gemv and exq_moe, its counters zero between calls
+
+
+def _fp4_workspace(need: int, dev: int, stream, handle: int, where: str):
+    """The default workspace of the launch's stream, its counters zeroed in that stream's order; kept and grown across calls.
+    Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
+    import torch
+    if stream is not None:
+        with _on(stream, dev):
+            return _fp4_workspace(need, dev, None, handle, where)
+    if torch.cuda.is_current_stream_capturing():
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    buf = _fp4_ws.get((dev, handle))
+    if buf is None or buf.numel() < need:
+        buf = torch.empty(max(need, 4 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
+        buf[:FP4_COUNTER_BYTES].zero_()
+        _fp4_ws[dev, handle] = buf
+    return buf
+
+
+def exq_fp4_scale_bytes(format: int, rows: int, K: int) -> int:
+    return int(_lib.exq_fp4_scale_bytes(format, rows, K))
+
+
+def _fp4_tensors(where: str, codes, scales, lead: tuple, format: int):
+    """(rows, K) of codes uint8 [*lead, rows, K / 2] with scales uint8 [*lead, bytes], both contiguous and on one device."""
+    import torch
+    if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != len(lead) + 2 or codes.get_device() < 0
+            or scales.get_device() != codes.get_device() or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    rows, K = codes.shape[-2], 2 * codes.shape[-1]
+    if codes.shape[:-2] != lead or (rows and tuple(scales.shape) != (*lead, exq_fp4_scale_bytes(format, rows, K))):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    return rows, K
+
+
+class Fp4Matrix:
+    """A matrix [rows, K] in the 4-bit format on the GPU: codes uint8 [rows, K / 2], scales uint8 [exq_fp4_scale_bytes] in tiles
+    (exq_pack_fp4, exq_fp4_quantize), and the factor of an E4M3 one."""
+
+    def __init__(self, codes, scales, format: int, factor: float = 1.0):
+        self.rows, self.K = _fp4_tensors("Fp4Matrix", codes, scales, (), format)
+        self.codes, self.scales, self.format, self.factor = codes, scales, format, factor
+        self.device = codes.get_device()
+        self._desc = exq_fp4_matrix(format, self.rows, self.K, factor, codes.data_ptr(), scales.data_ptr())
+        self._ref = ctypes.byref(self._desc)
+
+
+def exq_pack_fp4(codes: np.ndarray, scales: np.ndarray, format: int):
+    """Host: codes uint8 [rows, K] (0..15) and scale bytes uint8 [rows, K / block] -> (codes uint8 [rows, K / 2], scales uint8
+    [exq_fp4_scale_bytes]) as the matrices of the library have them."""
+    codes, scales = np.ascontiguousarray(codes, dtype=np.uint8), np.ascontiguousarray(scales, dtype=np.uint8)
+    rows, K = codes.shape
+    if format not in (FP4_E4M3, FP4_E8M0) or scales.shape != (rows, K // (16 if format == FP4_E4M3 else 32)):
+        raise ExqError(EXQ_ERR_INVALID_ARG, "exq_pack_fp4")
+    out, tiles = np.empty((rows, K // 2), np.uint8), np.empty(exq_fp4_scale_bytes(format, rows, K), np.uint8)
+    _check(_lib.exq_pack_fp4(_np_ptr(codes), _np_ptr(scales), format, rows, K, _np_ptr(out), _np_ptr(tiles)), "exq_pack_fp4")
+    return out, tiles
+
+
+def fp4_matrix(codes: np.ndarray, scales: np.ndarray, format: int, factor: float = 1.0, device="cuda") -> Fp4Matrix:
+    """An Fp4Matrix of host codes [rows, K] and scale bytes [rows, K / block]."""
+    import torch
+    return Fp4Matrix(*(torch.from_numpy(a).to(device) for a in exq_pack_fp4(codes, scales, format)), format, factor)
+
+
+def _fp16_rows(x, where: str):
+    """Refuses what is not a contiguous fp16 [rows, K]."""
+    import torch
+    if x.dtype != torch.float16 or x.dim() != 2 or not x.is_contiguous():
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+
+
+def exq_fp4_quantize(x, format: int, factor: float = 1.0, out: Optional[Fp4Matrix] = None, stream=None) -> Fp4Matrix:
+    """x fp16 [rows, K] in the 4-bit format: a new Fp4Matrix, or ``out`` (whose format and factor are taken) with its contents
+    replaced."""
+    import torch
+    where = "exq_fp4_quantize"
+    _fp16_rows(x, where)
+    rows, K = x.shape
+    dev = x.get_device()
+    _here(where, dev, dev if out is None else out.device)
+    if out is None:
+        bytes_ = exq_fp4_scale_bytes(format, rows, K)
+        if rows and not bytes_:
+            raise ExqError(EXQ_ERR_INVALID_ARG, where)
+        out = Fp4Matrix(_empty((rows, K // 2), torch.uint8, x.device, stream), _empty(bytes_, torch.uint8, x.device, stream),
+                        format, factor)
+    elif out.rows != rows or out.K != K:
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    _check(_lib.exq_fp4_quantize(x.data_ptr(), out._ref, _stream_ptr(stream, dev)), where)
+    return out
+
+
+def exq_fp4_dequantize(m: Fp4Matrix, out=None, stream=None):
+    """The matrix as fp16 [rows, K]."""
+    import torch
+    where = "exq_fp4_dequantize"
+    _here(where, m.device, m.device if out is None else out.get_device())
+    if out is None:
+        out = _empty((m.rows, m.K), torch.float16, m.codes.device, stream)
+    _fp16_rows(out, where)
+    if out.shape != (m.rows, m.K):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    _check(_lib.exq_fp4_dequantize(m._ref, out.data_ptr(), _stream_ptr(stream, m.device)), where)
+    return out
+
+
+def exq_fp4_gemm_workspace_size(a: Fp4Matrix, w: Fp4Matrix) -> int:
+    return int(_lib.exq_fp4_gemm_workspace_size(a._ref, w._ref))
+
+
+def _space(workspace, where: str):
+    """(address, bytes) of a workspace tensor."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def exq_fp4_gemm(a: Fp4Matrix, w: Fp4Matrix, out=None, workspace=None, stream=None):
+    """a . w^T as fp16 [a.rows, w.rows], both in the 4-bit format."""
+    import torch
+    where = "exq_fp4_gemm"
+    dev = a.device
+    _here(where, dev, w.device, dev if out is None else out.get_device(), dev if workspace is None else workspace.get_device())
+    if out is None:
+        out = _empty((a.rows, w.rows), torch.float16, a.codes.device, stream)
+    _fp16_rows(out, where)
+    if out.shape != (a.rows, w.rows):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    if workspace is None:
+        need = exq_fp4_gemm_workspace_size(a, w)
+        if need:
+            workspace = _empty(need, torch.uint8, a.codes.device, stream)
+    ws, n = _space(workspace, where)
+    _check(_lib.exq_fp4_gemm(a._ref, w._ref, out.data_ptr(), ws, n, _stream_ptr(stream, dev)), where)
+    return out
+
+
+def exq_fp4_gemv_workspace_size(w: Fp4Matrix, M: int) -> int:
+    return int(_lib.exq_fp4_gemv_workspace_size(w._ref, M))
+
+
+def exq_fp4_gemv(w: Fp4Matrix, x, out=None, workspace=None, stream=None):
+    """x . w^T as fp16 [M, w.rows] for up to 16 rows x fp16 [M, K], which are not quantised. Without ``workspace`` one is kept for
+    each stream that calls are launched on. A call that a graph captures needs one of its own, its first FP4_COUNTER_BYTES zero,
+    for as long as the graph is replayed."""
+    import torch
+    where = "exq_fp4_gemv"
+    dev = w.device
+    _here(where, dev, x.get_device(), dev if out is None else out.get_device(), dev if workspace is None else workspace.get_device())
+    _fp16_rows(x, where)
+    M = x.shape[0]
+    if out is None:
+        out = _empty((M, w.rows), torch.float16, x.device, stream)
+    _fp16_rows(out, where)
+    if x.shape[1] != w.K or out.shape != (M, w.rows):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    handle = _stream_ptr(stream, dev)
+    if workspace is None:
+        workspace = _fp4_workspace(exq_fp4_gemv_workspace_size(w, M), dev, stream, handle, where)
+    ws, n = _space(workspace, where)
+    _check(_lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle), where)
+    return out
+
+
+# ---------------------------------------------------------------- mixture of experts
+
+class Fp4Experts:
+    """One matrix [rows, K] for each expert, in the 4-bit format on the GPU: codes uint8 [experts, rows, K / 2], scales uint8
+    [experts, exq_fp4_scale_bytes], factors fp32 [experts] (E4M3) or None."""
+
+    def __init__(self, codes, scales, format: int, factors=None):
+        import torch
+        where = "Fp4Experts"
+        self.rows, self.K = _fp4_tensors(where, codes, scales, (codes.shape[0],), format)
+        self.n_experts, self.device = codes.shape[0], codes.get_device()
+        if factors is not None and (factors.dtype != torch.float32 or factors.shape != (self.n_experts,)
+                                    or factors.get_device() != self.device or not factors.is_contiguous()):
+            raise ExqError(EXQ_ERR_INVALID_ARG, where)
+        self.codes, self.scales, self.format, self.factors = codes, scales, format, factors
+        self._desc = exq_fp4_experts(format, self.n_experts, self.rows, self.K, codes.data_ptr(), scales.data_ptr(),
+                                     None if factors is None else factors.data_ptr())
+
+
+class MoeLayer:
+    """A layer of experts: gate and up [I, D], down [D, I] of each, the router fp16 [experts, D] (None: the calls bring ids and
+    weights), how many experts a token has, and whether their weights add up to one."""
+
+    def __init__(self, gate: Fp4Experts, up: Fp4Experts, down: Fp4Experts, top_k: int, router=None, renorm: bool = True,
+                 act: int = ACT_SILU):
+        import torch
+        self.device, self.D, self.top_k = gate.device, gate.K, top_k
+        if (up.device != self.device or down.device != self.device or
+                (router is not None and (router.dtype != torch.float16 or router.shape != (gate.n_experts, gate.K)
+                                         or router.get_device() != self.device or not router.is_contiguous()))):
+            raise ExqError(EXQ_ERR_INVALID_ARG, "MoeLayer")
+        self.gate, self.up, self.down, self.router = gate, up, down, router
+        self._desc = exq_moe_layer(gate._desc, up._desc, down._desc, None if router is None else router.data_ptr(), top_k,
+                                   int(renorm), act)
+        self._ref = ctypes.byref(self._desc)
+
+
+def exq_moe_workspace_size(layer: MoeLayer, T: int) -> int:
+    return int(_lib.exq_moe_workspace_size(layer._ref, T))
+
+
+def exq_moe(layer: MoeLayer, x, ids=None, weights=None, out=None, workspace=None, stream=None):
+    """(y fp16 [T, D], ids int32 [T, top_k], weights fp32 [T, top_k]) of up to 16 tokens x fp16 [T, D]. ids and weights are filled
+    where the layer has a router, and read, so that both must be given, where it has none. The workspace is as exq_fp4_gemv's."""
+    import torch
+    where = "exq_moe"
+    dev = layer.device
+    _here(where, dev, x.get_device(), *(t.get_device() for t in (ids, weights, out, workspace) if t is not None))
+    _fp16_rows(x, where)
+    T = x.shape[0]
+    if layer.router is None and (ids is None or weights is None):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    if ids is None:
+        ids = _empty((T, layer.top_k), torch.int32, x.device, stream)
+    if weights is None:
+        weights = _empty((T, layer.top_k), torch.float32, x.device, stream)
+    if out is None:
+        out = _empty((T, layer.D), torch.float16, x.device, stream)
+    _fp16_rows(out, where)
+    shape = (T, layer.top_k)
+    if (x.shape[1] != layer.D or out.shape != x.shape or ids.shape != shape or weights.shape != shape or ids.dtype != torch.int32
+            or weights.dtype != torch.float32 or not ids.is_contiguous() or not weights.is_contiguous()):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    handle = _stream_ptr(stream, dev)
+    if workspace is None:
+        workspace = _fp4_workspace(exq_moe_workspace_size(layer, T), dev, stream, handle, where)
+    ws, n = _space(workspace, where)
+    _check(_lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle), where)
+    return out, ids, weights
 
 
 def _i32(a, where: str) -> np.ndarray:

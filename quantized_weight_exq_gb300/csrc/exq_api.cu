@@ -477,7 +477,7 @@ extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix
 extern "C" size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M) {
   const int sms = current_sms();
   if (check_fp4(w) != EXQ_OK || w->rows <= 0 || w->rows % 8 || M < 1 || M > 16 || sms <= 0) return 0;
-  return fp4_gemv_workspace_bytes(M, sms);
+  return fp4_gemv_workspace_bytes(*w, M, sms);
 }
 
 extern "C" exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, int32_t M, uint16_t* y, void* workspace,
@@ -488,7 +488,7 @@ extern "C" exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, i
   if (M > 16 || !fp4_gemv_fits(w->rows)) return EXQ_ERR_UNSUPPORTED;
   const int sms = current_sms();
   if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
-  if (!workspace || !aligned256(workspace) || ws_bytes < fp4_gemv_workspace_bytes(M, sms)) return EXQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned256(workspace) || ws_bytes < fp4_gemv_workspace_bytes(*w, M, sms)) return EXQ_ERR_INVALID_ARG;
   return launch_fp4_gemv(*w, x, M, y, workspace, sms, current_device(), static_cast<cudaStream_t>(stream));
 }
 

@@ -47,6 +47,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   return r;
 }
 
+// the e2m1 number nearest to q (|q| <= 6) and its code
+__device__ __forceinline__ void e2m1_nearest(float q, uint32_t& code, float& value) {
+  uint32_t both;
+  asm("{\n\t.reg .b8 b, z;\n\t.reg .b32 f;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, 0f00000000, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(code), "=r"(both)
+      : "f"(q));
+  value = __half2float(__ushort_as_half(static_cast<unsigned short>(both)));
+}
+
 // two e4m3 bytes (the low 16 bits) as fp16, exact; 0x7f is NaN
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t bytes) {
   uint32_t r;

@@ -1,37 +1,41 @@
-// Products of a few fp16 rows with matrices of the microscaled 4-bit format:
-// the decode product (one matrix) and the two products of an expert layer.
+// Products of a few fp16 rows with matrices of the microscaled 4-bit format on
+// the block-scaled tcgen05 tensor cores: the decode product (one matrix) and
+// the two products of an expert layer.
 //
 //   out[t][n] = sum_k x[t][k] w[n][k],   t < 16
 //
-// Every code is read once, so the floor is the codes' and scales' bytes; the
-// kernel is a stream through shared memory with just enough arithmetic behind
-// it. Work is cut into units of 128 rows x 256 k of one matrix (16 KB of
-// codes, 2 or 1 KB of scales). The units of a call, in an order in which those
-// of one output tile follow one another, are divided evenly over the CTAs, one
-// CTA an SM: no wave is left part-filled, whatever the shape.
+// Every code is read once, so the floor is the codes' and scales' bytes. At
+// 6.8 TB/s an SM gets 47 codes a clock: turning them into fp16 in registers
+// costs more instructions than it has (a first kernel on mma.sync reached 2.4
+// TB/s, its integer pipe full). So the codes are never turned into anything:
+// the tensor cores multiply them as they are, and x is brought to their form.
 //
-//   warp 16     producer: for each unit the codes as one 2-D box (128-byte
-//               rows, 128-byte swizzle), the scale tiles as one copy (they are
-//               contiguous along K) and 512 bytes of each x row, all
-//               completing on the stage's mbarrier.
-//   warps 0-15  eight groups of 16 rows times the two halves of the unit's k.
-//               Per 32 k: one word of codes a lane and row (8 codes of its
-//               row), 16 bytes of x, two mma.sync.m16n8k16 with the weights
-//               as A (16 rows) and x as B (8 tokens). The k within 32 go to
-//               the MMA's places in an order of our own, the same for both
-//               operands: lane t of a quad holds k 8t .. 8t + 7.
-//               E4M3: code times scale is exact in fp16 (6 bits) and is what
-//               the MMA sees. E8M0: the scale's range is beyond fp16, so the
-//               codes go in as they are and the block's sum (the two MMAs
-//               cover just one block of 32) is scaled in fp32.
-//   end of tile the halves of k meet in shared memory. A tile whose units lie
-//               in several CTAs goes through the workspace: each writes its
-//               part, the last to arrive (a counter) adds them in CTA order,
-//               so that the result does not depend on who it is.
+// A row of x as eight 4-bit rows: with s a power of two, |x| <= 4 s for all of
+// a block, part 0 is the e2m1 number nearest to q = x / s, part p + 1 that
+// nearest to 8 times what part p left, and
+//   x = s (p0 + p1 / 8 + p2 / 64 + ...)
+// e2m1's steps up to 4 are at most 1, so that at most 1/2 is left, times 8 at
+// most 4 again: every step is exact in fp32, and after eight parts at most
+// 2^-23 of the block's bound is left. The eight rows share their scales, lie
+// beside one another as columns of the product, and the epilogue adds them
+// with weights 8^-p. 16 tokens are 128 columns: a third of what the tensor
+// cores could do while the codes arrive.
 //
-// mma.sync and not tcgen05: with 8 or 16 tokens the arithmetic is far below
-// either's rate, and registers take the dequantised A operand without a trip
-// through tensor memory.
+// Work is cut into units of 128 rows x 256 k of one matrix (16 KB of codes, 2
+// or 1 KB of scales). The units of a call, those of one output tile in a row,
+// are divided evenly over the CTAs, one an SM: no wave is left part-filled.
+//
+//   warp 0     producer: for each unit the codes as one 2-D box (128-byte
+//              rows, 128-byte swizzle), the scale tiles as one copy, and of
+//              each token its 8 rows of parts (1 KB: one swizzle atom) and
+//              their scales.
+//   warp 1     one lane copies scales to tensor memory and issues the MMAs
+//              (M = 128 rows of the matrix, N = 8 columns a token, K = 64).
+//   warps 2-5  drain the sums: a lane is a row.
+//
+// A tile whose units lie in several CTAs goes through the workspace: each
+// writes its part, the last to arrive (a counter) adds them in CTA order, so
+// that the result does not depend on who it is.
 #pragma once
 
 #include "exq_fp4.cuh"
@@ -43,50 +47,53 @@ static __device__ unsigned g_stream_err;
 
 enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
-constexpr int kRows = 128;           // rows of a unit
+constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
-constexpr int kConsumers = 16;       // warps
-constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kCodeBytes = kRows * kUnitK / 2;
-constexpr int kScaleRoom = 2048;     // 4 tiles (E4M3) or 2 (E8M0)
-constexpr int kXStride = kUnitK * 2 + 64;  // x rows 64 bytes apart modulo 128: two rows' quads hit all banks
+constexpr int kThreads = 6 * 32;
+constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
 constexpr int kMaxPairs = 256;       // tokens x experts of each
 constexpr int kMaxExperts = 512;
-constexpr int kSmemMost = 227 * 1024;
+constexpr int kMaxStages = 10;
 
-// What lies between the two products of an expert, h, as up leaves and down
-// reads it: for each (token, expert) and 256 values a piece of the first fp16
-// parts, the second ones and the factors of the two halves of 128 (times which
-// the sums of the parts are h).
-constexpr int kHPiece = kUnitK * 4 + 16;
-constexpr int kHStride = kHPiece + 48;     // in shared memory: 64 bytes apart modulo 128, as the x rows
+// a stage: codes, scale tiles, the tokens' parts, their scales
+constexpr int kOffScales = kRows * kUnitK / 2;
+constexpr int kOffX = kOffScales + 2048;
+static_assert(kOffX % 1024 == 0, "swizzle atoms");
+// An expert's tokens are picked one by one. Their scales of a unit are 8 lines
+// of 16 bytes (a line a row, its first word the scales) for each scale tile:
+// four such pieces, one a token, are what one copy to tensor memory takes, so
+// that MMAs are made for up to four tokens at a time.
+constexpr int kLines = 8 * 16;
+__host__ __device__ constexpr int unit_tiles(int fmt) { return kUnitK / fp4_tile_k(fmt); }
+__host__ __device__ constexpr int token_lines(int fmt) { return unit_tiles(fmt) * kLines; }
 
-__host__ __device__ constexpr int x_stride(int mode) { return mode == kDown ? kHStride : kXStride; }
-__host__ __device__ constexpr int stage_bytes(int mode, int nt) {
-  return (kCodeBytes + kScaleRoom + 8 * nt * x_stride(mode) + 1023) / 1024 * 1024;
-}
-// accumulators of a lane: 4 for each 8 tokens (and matrix)
-__host__ __device__ constexpr int accs(int mode, int nt) { return 4 * nt * (mode == kUp ? 2 : 1); }
-__host__ __device__ constexpr int meet_bytes(int mode, int nt) { return 2 * 8 * 32 * accs(mode, nt) * 4; }
-constexpr int kRest = 10240 + 1024;  // barriers, the experts' tables, alignment
-__host__ __device__ constexpr int stages(int mode, int nt) {
-  const int n = (kSmemMost - kRest - meet_bytes(mode, nt)) / stage_bytes(mode, nt);
-  return n < 8 ? n : 8;
-}
-__host__ __device__ constexpr int smem_bytes(int mode, int nt) {
-  return stages(mode, nt) * stage_bytes(mode, nt) + meet_bytes(mode, nt) + kRest;
-}
-// floats of one CTA's part of a tile
-__host__ __device__ constexpr int part_floats(int mode, int nt) { return 8 * 32 * accs(mode, nt); }
+constexpr int kSmemTotal = 226 * 1024;
+constexpr int kRest = 20 * 1024;     // barriers, the experts' tables, sums, alignment
+constexpr int kRing = kSmemTotal - kRest;
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemScales = 432;         // 16 columns of the matrix's, then 16 for each four tokens
+constexpr int kMaxBuffers = 4;
+
+// Scale of a block of x: 2^(e - 1) for a largest magnitude in [2^e, 2^(e + 1)).
+// An e4m3 scale has 18 powers of two: for fp16 the largest is 2^14 (times 2^-6
+// that is 2^8, e4m3's largest power), and a block whose scale would be under
+// the smallest takes that one, 2^-3: its eighth part counts 2^-25 then, half of
+// fp16's smallest number. What lies between the experts' products is brought
+// to [1, 2) first, for each 128 rows and token.
+constexpr int kXTop = 14, kHTop = -1;          // exponents of the largest scales
+__host__ __device__ constexpr int e4m3_shift(int top) { return top - 8; }
 
 struct Args {
   const uint8_t* sc0;      // scale tiles of the matrix, or of expert 0's gate or down
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
-  const uint16_t* x;       // [M, K]; down: h, [pairs, k_units] pieces
-  uint16_t* out;           // [M, rows]; up: h, [pairs, h_units] pieces
-  const float *f0, *f1, *f2;  // experts' factors of gate, up and down, or NULL
+  const uint8_t* x_scales; // gemv: scale tiles of the parts; else token_lines for each [token or pair, unit]
+  uint16_t* y;             // gemv [M, rows], down [M, rows]
+  uint8_t* h_codes;        // up: parts of h, [pairs * 8, rows / 2]
+  uint8_t* h_scales;       // up: token_lines for each [pair, h_units]
+  const float *f0, *f1;    // experts' factors of gate and up, or of down, or NULL
   const int32_t* ids;      // [M, top_k]
   const float* weights;
   unsigned* counters;
@@ -98,144 +105,162 @@ struct Args {
   int wait_limit, starve;
 };
 
+// floats of one CTA's part of a tile: a value for each row, token (and matrix)
+__host__ __device__ constexpr int part_floats(int mode) { return kRows * kMaxTokens * (mode == kUp ? 2 : 1); }
+
 // The experts of a call, the same in every CTA: those that some token chose,
 // ascending, with the tokens of each and the place of (expert, token) in ids.
 struct Experts {
-  int n, pad[3];
+  int n, most_tokens, pad[2];
   int expert[kMaxPairs];
   unsigned tokens[kMaxPairs];                 // a bit each
   uint8_t place[kMaxPairs][kMaxTokens];       // the first, where an id repeats
   int ids[kMaxPairs];
   float weight[kMaxPairs];                    // by that place: those of an id that repeats are added up
-  float most[8][kMaxTokens];                  // up: the groups' largest h
+  float most[4][kMaxTokens];                  // up: the warps' largest h
 };
-static_assert(sizeof(Experts) + 256 <= 10240, "shared memory budget");
+static_assert(sizeof(Experts) + kRows * kMaxTokens * 4 + 512 + 1024 <= kRest, "shared memory budget");
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// ---------------------------------------------------------------- parts
+
+// The e-1 of a block's scale 2^(e-1) from the bits of its largest magnitude
+// (fp32, finite), and the byte that the format has for it.
+template <int FMT>
+__device__ __forceinline__ int part_exponent(float most, int top) {
+  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 128;  // -128 for zero and subnormals
+  if constexpr (FMT == EXQ_FP4_E4M3) return min(max(e, top - 17), top);
+  return max(e, -126);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t part_scale_byte(int e, int top) {
+  if constexpr (FMT == EXQ_FP4_E8M0) return static_cast<uint32_t>(e + 127);
+  const int p = e - e4m3_shift(top);  // -9 .. 8
+  return p >= -6 ? static_cast<uint32_t>(p + 7) << 3 : 1u << (p + 9);
+}
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {  // K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// 32 lines of 16 bytes, groups of 8 lines `stride` bytes apart, no swizzle
+__device__ __forceinline__ uint64_t lines_desc(uint32_t addr, uint32_t stride) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46);
+}
+
+__device__ __forceinline__ uint32_t idesc_for(int fmt, int n) {  // e2m1 operands, K-major, M = 128
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((fmt == EXQ_FP4_E8M0 ? 1u : 0u) << 23) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           uint32_t accumulate) {
+  if constexpr (FMT == EXQ_FP4_E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+  uint32_t u[16];
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// a token's sum from those of its parts
+__device__ __forceinline__ float join_parts(const float* d) {
+  float v = d[7];
+#pragma unroll
+  for (int p = 6; p >= 0; --p) v = fmaf(v, 0.125f, d[p]);
+  return v;
 }
 
-// One warp's 16 rows times 128 k (half kh) of a stage, added to acc.
-template <int FMT, int MODE, int NT>
-__device__ __forceinline__ void consume(const uint8_t* st, int chunks, unsigned tokens, int rg, int kh, int lane,
-                                        float (*acc)[4]) {
-  const int g = lane >> 2, t = lane & 3;
-  const int r0 = rg * 16 + g;  // and r0 + 8: both are g modulo 8
-  const uint8_t* row0 = st + r0 * 128 + 4 * t;
-  const uint8_t* sc = st + kCodeBytes;
-  const uint8_t* x0 = st + kCodeBytes + kScaleRoom + g * x_stride(MODE) + 16 * t;
-  constexpr int kTilesHalf = FMT == EXQ_FP4_E4M3 ? 2 : 1;  // scale tiles of 128 k
-  uint32_t sw[2][kTilesHalf];
-#pragma unroll
-  for (int i = 0; i < kTilesHalf; ++i) {
-    const uint8_t* tile = sc + (kh * kTilesHalf + i) * 512;
-    sw[0][i] = *reinterpret_cast<const uint32_t*>(tile + fp4_tile_byte(r0));
-    sw[1][i] = *reinterpret_cast<const uint32_t*>(tile + fp4_tile_byte(r0 + 8));
-  }
-  const uint32_t pick = t & 2 ? 0x3232u : 0x1010u;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int cc = 4 * kh + c;
-    if (cc >= chunks) break;
-    uint32_t w[2], b[NT * (MODE == kDown ? 2 : 1)][4];
-    w[0] = *reinterpret_cast<const uint32_t*>(row0 + ((cc ^ g) << 4));
-    w[1] = *reinterpret_cast<const uint32_t*>(row0 + 8 * 128 + ((cc ^ g) << 4));
-#pragma unroll
-    for (int n = 0; n < NT * (MODE == kDown ? 2 : 1); ++n) {
-      const int token = 8 * (n % NT) + g;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if ((tokens >> token) & 1u)
-        v = *reinterpret_cast<const uint4*>(x0 + n % NT * 8 * x_stride(MODE) + n / NT * kUnitK * 2 + cc * 64);
-      b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w;
-    }
-    uint32_t a[2][4];  // of the two MMAs: (row g, row g + 8) x (first, second pair of k)
-    a[0][0] = e2m1x2_f16<0>(w[0]); a[0][1] = e2m1x2_f16<0>(w[1]);
-    a[0][2] = e2m1x2_f16<1>(w[0]); a[0][3] = e2m1x2_f16<1>(w[1]);
-    a[1][0] = e2m1x2_f16<2>(w[0]); a[1][1] = e2m1x2_f16<2>(w[1]);
-    a[1][2] = e2m1x2_f16<3>(w[0]); a[1][3] = e2m1x2_f16<3>(w[1]);
-    if constexpr (FMT == EXQ_FP4_E4M3) {
-      // the lane's 8 k lie in one block of 16: quads' first two lanes in the chunk's first, the others in its second
-      const uint32_t s0 = __byte_perm(e4m3x2_f16(sw[0][c >> 1] >> (16 * (c & 1))), 0u, pick);
-      const uint32_t s1 = __byte_perm(e4m3x2_f16(sw[1][c >> 1] >> (16 * (c & 1))), 0u, pick);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        a[j][0] = hmul2(a[j][0], s0); a[j][1] = hmul2(a[j][1], s1);
-        a[j][2] = hmul2(a[j][2], s0); a[j][3] = hmul2(a[j][3], s1);
-      }
-#pragma unroll
-      for (int n = 0; n < NT * (MODE == kDown ? 2 : 1); ++n) {
-        mma16816(acc[n % NT], a[0], b[n][0], b[n][1]);
-        mma16816(acc[n % NT], a[1], b[n][2], b[n][3]);
-      }
-    } else {
-      const float s0 = e8m0_f32((sw[0][0] >> (8 * c)) & 0xFFu), s1 = e8m0_f32((sw[1][0] >> (8 * c)) & 0xFFu);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(d, a[0], b[n][0], b[n][1]);
-        mma16816(d, a[1], b[n][2], b[n][3]);
-        if constexpr (MODE == kDown) {
-          mma16816(d, a[0], b[NT + n][0], b[NT + n][1]);
-          mma16816(d, a[1], b[NT + n][2], b[NT + n][3]);
-        }
-        acc[n][0] = fmaf(d[0], s0, acc[n][0]);
-        acc[n][1] = fmaf(d[1], s0, acc[n][1]);
-        acc[n][2] = fmaf(d[2], s1, acc[n][2]);
-        acc[n][3] = fmaf(d[3], s1, acc[n][3]);
-      }
-    }
-  }
-}
+// ---------------------------------------------------------------- experts
 
 // The experts' tables, by all threads of the CTA.
 __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned* used, bool report) {
   const int tid = threadIdx.x, pairs = a.M * a.top_k;
   if (tid < kMaxExperts / 32) used[tid] = 0u;
-  if (tid < kMaxPairs) e->tokens[tid] = 0u;
-  const int id = tid < pairs ? __ldcg(a.ids + tid) : -1;
-  const float w = tid < pairs ? __ldcg(a.weights + tid) : 0.f;
-  if (tid < kMaxPairs) e->ids[tid] = id;
+  for (int i = tid; i < kMaxPairs; i += kThreads) {
+    e->tokens[i] = 0u;
+    e->ids[i] = i < pairs ? __ldcg(a.ids + i) : -1;
+    e->weight[i] = i < pairs ? __ldcg(a.weights + i) : 0.f;
+  }
   __syncthreads();
-  const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.n_experts);
-  if (good) atomicOr(&used[id >> 5], 1u << (id & 31));
-  if (report && id != -1 && !good) atomicOr(&g_stream_err, kDevErrBadExpert);
-  if (tid < kMaxPairs) e->weight[tid] = w;
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int id = e->ids[i];
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_experts))
+      atomicOr(&used[id >> 5], 1u << (id & 31));
+    else if (report && id != -1)
+      atomicOr(&g_stream_err, kDevErrBadExpert);
+  }
   __syncthreads();
   if (tid == 0) {
     int n = 0;
     for (int i = 0; i < kMaxExperts / 32; ++i) n += __popc(used[i]);
     e->n = n;
+    e->most_tokens = 1;
   }
-  bool first = good;
-  float sum = 0.f;
-  if (good) {
+  float sum[2] = {0.f, 0.f};
+  int slot_of[2] = {-1, -1};
+  for (int i = tid, r = 0; i < pairs; i += kThreads, ++r) {
+    const int id = e->ids[i];
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_experts)) continue;
     int slot = __popc(used[id >> 5] & ((1u << (id & 31)) - 1u));
-    for (int i = 0; i < (id >> 5); ++i) slot += __popc(used[i]);
+    for (int w = 0; w < (id >> 5); ++w) slot += __popc(used[w]);
     e->expert[slot] = id;
-    const int t = tid / a.top_k;
+    const int t = i / a.top_k;
+    bool first = true;
     for (int p = t * a.top_k; p < (t + 1) * a.top_k; ++p)
       if (e->ids[p] == id) {
-        first = first && p >= tid;
-        sum += e->weight[p];
+        first = first && p >= i;
+        sum[r] += e->weight[p];
       }
     if (first) {
-      e->place[slot][t] = static_cast<uint8_t>(tid);
+      e->place[slot][t] = static_cast<uint8_t>(i);
       atomicOr(&e->tokens[slot], 1u << t);
+      slot_of[r] = slot;
     }
   }
   __syncthreads();
-  if (first) e->weight[tid] = sum;
+  for (int i = tid, r = 0; i < pairs; i += kThreads, ++r)
+    if (slot_of[r] >= 0) {
+      e->weight[i] = sum[r];
+      atomicMax(&e->most_tokens, __popc(e->tokens[slot_of[r]]));
+    }
   __syncthreads();
 }
+static_assert(kMaxPairs <= 2 * kThreads, "two places a thread");
 
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == EXQ_ACT_SILU) return v / (1.f + __expf(-v));
@@ -243,18 +268,59 @@ __device__ __forceinline__ float activate(float v, int act) {
   return 0.5f * v * (1.f + tanhf(u));
 }
 
-// The unit list of a call: n units, those of one tile consecutive.
-struct Units {
-  int tile_units;   // of a tile
-  long long n;
-};
-
-template <int MODE>
-__device__ __forceinline__ Units units_of(const Args& a, int experts) {
-  if constexpr (MODE == kGemv) return {a.k_units, static_cast<long long>(a.row_tiles) * a.k_units};
-  if constexpr (MODE == kUp) return {a.k_units, static_cast<long long>(experts) * a.row_tiles * a.k_units};
-  return {experts * a.k_units, static_cast<long long>(a.row_tiles) * experts * a.k_units};
+// bit number j (from 0) that is set
+__device__ __forceinline__ int nth_bit(unsigned m, int j) {
+  for (; j > 0; --j) m &= m - 1u;
+  return __ffs(static_cast<int>(m)) - 1;
 }
+
+// ---------------------------------------------------------------- units
+
+// How many units a call has, and a tile of it.
+template <int MODE>
+__device__ __forceinline__ long long units_of(const Args& a, int experts) {
+  return static_cast<long long>(a.row_tiles) * a.k_units * (MODE == kGemv ? 1 : experts);
+}
+
+// A unit's place: its expert (the index in Experts), tile of rows and k. The
+// division is made once a CTA; from unit to unit the place counts up.
+template <int MODE>
+struct Place {
+  int kc, slot, row;
+
+  __device__ __forceinline__ Place(const Args& a, int experts, long long u) {
+    const long long q = u / a.k_units;
+    kc = static_cast<int>(u - q * a.k_units);
+    slot = 0;
+    row = static_cast<int>(q);
+    if constexpr (MODE == kUp) {
+      slot = static_cast<int>(q / a.row_tiles);
+      row = static_cast<int>(q) - slot * a.row_tiles;
+    } else if constexpr (MODE == kDown) {
+      row = static_cast<int>(q / experts);
+      slot = static_cast<int>(q) - row * experts;
+    }
+  }
+
+  // the last unit of its tile
+  __device__ __forceinline__ bool ends(const Args& a, int experts) const {
+    return kc + 1 == a.k_units && (MODE != kDown || slot + 1 == experts);
+  }
+
+  __device__ __forceinline__ void next(const Args& a, int experts) {
+    if (++kc < a.k_units) return;
+    kc = 0;
+    if constexpr (MODE == kDown) {
+      if (++slot < experts) return;
+      slot = 0;
+      ++row;
+    } else {
+      if (++row < a.row_tiles || MODE == kGemv) return;
+      row = 0;
+      ++slot;
+    }
+  }
+};
 
 // The CTA that has unit u, of `ctas` that divide n units: CTA b has units
 // [b n / ctas, (b + 1) n / ctas).
@@ -262,249 +328,331 @@ __device__ __forceinline__ int owner(long long u, long long n, int ctas) {
   return static_cast<int>(((u + 1) * ctas - 1) / n);
 }
 
-template <int FMT, int MODE, int NT>
+// counts stages or buffers, and the parity of their barriers
+struct Turn {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+template <int FMT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1,
-                  const __grid_constant__ Args a) {
-  constexpr int kStages = stages(MODE, NT);
-  constexpr int kStageBytes = stage_bytes(MODE, NT);
-  constexpr int kParts = MODE == kUp ? 2 : 1;  // matrices of a unit, a stage each
-  constexpr int kTilesUnit = kUnitK / fp4_tile_k(FMT);
-  constexpr int kAccs = accs(MODE, NT) / 4;
+                  const __grid_constant__ CUtensorMap mx, const __grid_constant__ Args a) {
+  constexpr int kMatrices = MODE == kUp ? 2 : 1;  // of a unit, a stage each
+  constexpr int kTiles = unit_tiles(FMT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float4* meet = reinterpret_cast<float4*>(smem + kStages * kStageBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + meet_bytes(MODE, NT));
-  uint64_t* empty = full + kStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + kStages);
+  float* sums = reinterpret_cast<float*>(smem + kRing);                 // down: [tokens][rows]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sums + kRows * kMaxTokens);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* dfull = empty + kMaxStages;
+  uint64_t* dempty = dfull + kMaxBuffers;
+  uint64_t* done = dempty + kMaxBuffers;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last = abort_flag + 1;
-  unsigned* used = reinterpret_cast<unsigned*>(empty + kStages) + 4;
+  unsigned* used = reinterpret_cast<unsigned*>(tmem_slot + 4);
   Experts* ex = reinterpret_cast<Experts*>(used + kMaxExperts / 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), kConsumers);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   if constexpr (MODE == kUp) {
-    // ids and weights may come from the launch before; the down product may start its own set-up from here
+    // ids and weights may come from the launch before
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  int n_experts = 0;
+  if constexpr (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n_experts = 0, most_tokens = a.M;
   if constexpr (MODE != kGemv) {
     find_experts(a, ex, used, MODE == kUp && blockIdx.x == 0);
     n_experts = ex->n;
-  } else {
-    __syncthreads();
+    most_tokens = ex->most_tokens;
   }
-
-  const Units un = units_of<MODE>(a, n_experts);
+  const long long n_units = units_of<MODE>(a, n_experts);
   if constexpr (MODE == kDown) {
-    if (un.n == 0) {  // no token has an expert
+    if (n_units == 0) {  // no token has an expert
       asm volatile("griddepcontrol.wait;" ::: "memory");
       const long long n = static_cast<long long>(a.M) * a.rows;
       for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n;
            i += static_cast<long long>(gridDim.x) * kThreads)
-        a.out[i] = 0;
+        a.y[i] = 0;
     }
   }
-  const int ctas = static_cast<int>(un.n < gridDim.x ? un.n : gridDim.x);
+  const int ctas = static_cast<int>(n_units < gridDim.x ? n_units : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long u0 = blockIdx.x * un.n / ctas, u1 = (blockIdx.x + 1) * un.n / ctas;
+  const long long u0 = blockIdx.x * n_units / ctas;
+  const int n_mine = static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0);
+
+  // the ring and the buffers of sums go by the most tokens that a matrix of the call has
+  const int off_xs = kOffX + 1024 * most_tokens;
+  const int stage_bytes = (off_xs + (MODE == kGemv ? 2048 : (most_tokens + 3) / 4 * 4 * token_lines(FMT)) + 1023) / 1024 * 1024;
+  const int n_stages = min(kMaxStages, kRing / stage_bytes);
+  const int cols = (8 * most_tokens + 15) / 16 * 16;                    // of one sum
+  const int buffer_cols = cols * (MODE == kGemv ? 1 : 2);               // up: gate, up; down: the halves of a unit's k
+  const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), MODE == kDown ? 5 : 1);  // the MMAs; down: and the warps that read h's factors
+    }
+    for (int b = 0; b < kMaxBuffers; ++b) {
+      mbar_init(smem_u32(&dfull[b]), 1);
+      mbar_init(smem_u32(&dempty[b]), 4);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const unsigned everyone = (1u << a.M) - 1u;
 
-  if (warp == kConsumers) {
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (a.starve) {  // test hook: a starved producer issues nothing
-      if constexpr (MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
-      const int n_stages = static_cast<int>(u1 - u0) * kParts;
-      int x_from = 0;  // stages whose x rows are still to be issued (down: after the wait)
-      bool waited = MODE != kDown;
-      int issued = 0;
-      auto place = [&](int i, int& kc, int& slot, int& row, int& id) {
-        const long long u = u0 + i / kParts;
-        const long long q = u / a.k_units;
-        kc = static_cast<int>(u - q * a.k_units);
-        slot = 0;
-        id = 0;
-        if constexpr (MODE == kGemv) {
-          row = static_cast<int>(q);
-        } else if constexpr (MODE == kUp) {
-          slot = static_cast<int>(q / a.row_tiles);
-          row = static_cast<int>(q) - slot * a.row_tiles;
-          id = ex->expert[slot];
-        } else {
-          row = static_cast<int>(q / n_experts);
-          slot = static_cast<int>(q) - row * n_experts;
-          id = ex->expert[slot];
-        }
-      };
+      const int n = n_mine * kMatrices;
+      bool waited = MODE == kUp;  // for the launch that leaves x's parts
+      int issued = 0, x_from = 0;
+      Place<MODE> at(a, n_experts, u0), x_at = at;  // of the weights' and of x's next stage
+      Turn turn, x_turn;
       auto issue_x = [&](int i) {
-        int kc, slot, row, id;
-        place(i, kc, slot, row, id);
-        const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
-        if (lane < 8 * NT && ((tokens >> lane) & 1u)) {  // lane: the token
-          const uint32_t dst = smem_u32(smem + (i % kStages) * kStageBytes + kCodeBytes + kScaleRoom + lane * x_stride(MODE));
-          if constexpr (MODE == kDown)
-            bulk_load(dst, a.x + (static_cast<size_t>(ex->place[slot][lane]) * a.k_units + kc) * (kHPiece / 2), kHPiece,
-                      smem_u32(&full[i % kStages]));
-          else
-            bulk_load(dst, a.x + static_cast<size_t>(lane) * a.K + static_cast<size_t>(kc) * kUnitK,
-                      min(kUnitK, a.K - kc * kUnitK) * 2, smem_u32(&full[i % kStages]));
+        const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[x_at.slot];
+        uint8_t* st = smem + x_turn.i * stage_bytes;
+        const uint32_t bar = smem_u32(&full[x_turn.i]);
+        if (lane < __popc(tokens)) {  // lane: the number of the token among the unit's
+          const int token = MODE == kGemv ? lane : nth_bit(tokens, lane);
+          const int from = MODE == kDown ? ex->place[x_at.slot][token] : token;
+          tma_load_2d(smem_u32(st + kOffX + lane * 1024), &mx, x_at.kc * (kUnitK / 2), from * kParts, bar);
+          if constexpr (MODE != kGemv)
+            bulk_load(smem_u32(st + off_xs + lane * token_lines(FMT)),
+                      a.x_scales + (static_cast<size_t>(from) * a.k_units + x_at.kc) * token_lines(FMT), token_lines(FMT), bar);
         }
+        if constexpr (MODE == kGemv) {
+          if (lane == 0)
+            bulk_load(smem_u32(st + off_xs), a.x_scales + static_cast<size_t>(x_at.kc) * kTiles * 512,
+                      min(kTiles, a.k_tiles - x_at.kc * kTiles) * 512, bar);
+        }
+        if (i % kMatrices == kMatrices - 1) x_at.next(a, n_experts);
+        x_turn.next(n_stages);
+        ++x_from;
       };
-      for (int i = 0; i < n_stages; ++i) {
-        const int s = i % kStages;
-        if (!waited && i == kStages) {
+      for (int i = 0; i < n; ++i) {
+        if (!waited && i == n_stages) {
           asm volatile("griddepcontrol.wait;" ::: "memory");
           waited = true;
-          for (; x_from < i; ++x_from) issue_x(x_from);
+          while (x_from < i) issue_x(x_from);
         }
-        if (!mbar_wait_warp(smem_u32(&empty[s]), ((i / kStages) & 1) ^ 1, abort_flag, a.wait_limit, &g_stream_err)) break;
-        int kc, slot, row, id;
-        place(i, kc, slot, row, id);
-        const int part = i % kParts;
-        uint8_t* st = smem + s * kStageBytes;
-        const uint32_t bar = smem_u32(&full[s]);
+        if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
+        const int which = i % kMatrices;
         if (lane == 0) {
-          const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
-          const uint32_t xb = __popc(tokens) * (MODE == kDown ? kHPiece : min(kUnitK, a.K - kc * kUnitK) * 2);
-          const uint32_t sb = min(kTilesUnit, a.k_tiles - kc * kTilesUnit) * 512;
-          mbar_expect_tx(bar, kCodeBytes + sb + xb);
-          tma_load_2d(smem_u32(st), part == 0 ? &m0 : &m1, kc * (kUnitK / 2), id * a.rows + row * kRows, bar);
-          bulk_load(smem_u32(st + kCodeBytes),
-                    (part == 0 ? a.sc0 : a.sc1) + id * a.sc_stride +
-                        (static_cast<size_t>(row) * a.k_tiles + kc * kTilesUnit) * 512,
+          const int id = MODE == kGemv ? 0 : ex->expert[at.slot];
+          const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
+          uint8_t* st = smem + turn.i * stage_bytes;
+          const uint32_t bar = smem_u32(&full[turn.i]);
+          const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
+          mbar_expect_tx(bar, kOffScales + sb + tokens * 1024 + (MODE == kGemv ? sb : tokens * token_lines(FMT)));
+          tma_load_2d(smem_u32(st), which == 0 ? &m0 : &m1, at.kc * (kUnitK / 2), id * a.rows + at.row * kRows, bar);
+          bulk_load(smem_u32(st + kOffScales),
+                    (which == 0 ? a.sc0 : a.sc1) + id * a.sc_stride +
+                        (static_cast<size_t>(at.row) * a.k_tiles + at.kc * kTiles) * 512,
                     sb, bar);
         }
         __syncwarp();
-        if (waited) {
-          issue_x(i);
-          x_from = i + 1;
-        }
+        if (which == kMatrices - 1) at.next(a, n_experts);
+        turn.next(n_stages);
         issued = i + 1;
+        if (waited) issue_x(i);
       }
       if (!waited) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        for (; x_from < issued; ++x_from) issue_x(x_from);
+        while (x_from < issued) issue_x(x_from);
       }
       // every issued stage's copies land before the CTA may exit
-      for (int i = max(0, issued - kStages); i < issued; ++i)
+      for (int i = max(0, issued - n_stages); i < issued; ++i)
         for (int r = 0; r < a.wait_limit; ++r)
-          if (mbar_try_wait(smem_u32(&full[i % kStages]), (i / kStages) & 1)) break;
+          if (mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1)) break;
     }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
-  const int rg = warp & 7, kh = warp >> 3;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-  float acc[kAccs][4];       // of the tile
-  float run[NT][4];          // down: of the unit, before the factors
-  float share[NT][2];        // down: weight and factor of the expert for the lane's tokens
-  int slot_of_share = -1;
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      Place<MODE> at(a, n_experts, u0);
+      Turn turn, buf;
+      bool fresh = true;  // the next unit begins a buffer
+      bool ok = true;
+      for (int left = n_mine; left > 0 && ok; --left) {
+        const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
+        const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
+        const uint32_t d0 = tmem + buf.i * buffer_cols;
+        if (fresh && !mbar_wait(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
 #pragma unroll
-  for (int i = 0; i < kAccs; ++i)
+        for (int which = 0; which < kMatrices; ++which) {
+          if (!mbar_wait(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + turn.i * stage_bytes);
+          const uint32_t sa = tmem + kTmemScales;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+          for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
+          const uint64_t ad = codes_desc(st);
+          for (int g = 0; g < tokens; g += MODE == kGemv ? kMaxTokens : 4) {
+            // gemv: all tokens, their scales in tiles; else four, from their own lines
+            const uint32_t sb = sa + 16 + 4 * g;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) run[i][j] = 0.f;
-
-  int i = 0, tiles_done = 0;
-  for (long long u = u0; u < u1; ++u) {
-    const long long q = u / a.k_units;
-    const int kc = static_cast<int>(u - q * a.k_units);
-    int slot = 0, row;
-    if constexpr (MODE == kGemv) {
-      row = static_cast<int>(q);
-    } else if constexpr (MODE == kUp) {
-      slot = static_cast<int>(q / a.row_tiles);
-      row = static_cast<int>(q) - slot * a.row_tiles;
-    } else {
-      row = static_cast<int>(q / n_experts);
-      slot = static_cast<int>(q) - row * n_experts;
+            for (int j = 0; j < kTiles; ++j)
+              copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
+                                                    : lines_desc(st + off_xs + g * token_lines(FMT) + j * kLines, token_lines(FMT)));
+            const int m = MODE == kGemv ? tokens : min(4, tokens - g);
+            const uint32_t idesc = idesc_for(FMT, (8 * m + 15) / 16 * 16);
+            const uint64_t bd = codes_desc(st + kOffX + g * 1024);
+            for (int j = 0; j < n_k; ++j) {  // 64 k: 32 bytes of a row
+              // down: each half of 128 k has its own sums, and every unit its own
+              const uint32_t d = d0 + 8 * g + (MODE == kUp ? which * cols : MODE == kDown ? (j >> 1) * cols : 0);
+              const bool first = MODE == kDown ? (j & 1) == 0 : fresh && j == 0;
+              if constexpr (FMT == EXQ_FP4_E4M3) {
+                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 4 * j, !first);
+              } else {  // two scales of the tile's four: byte 0 or 2 of each word
+                const uint32_t id = (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
+                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * (j >> 1), !first);
+              }
+            }
+          }
+          commit(smem_u32(&empty[turn.i]));
+          turn.next(n_stages);
+        }
+        if (!ok) break;
+        fresh = MODE == kDown || left == 1 || at.ends(a, n_experts);
+        if (fresh) {
+          commit(smem_u32(&dfull[buf.i]));
+          buf.next(n_buffers);
+        }
+        at.next(a, n_experts);
+      }
+      // the MMAs are over before tensor memory is given back
+      commit(smem_u32(done));
+      for (int r = 0; r < a.wait_limit; ++r)
+        if (mbar_try_wait(smem_u32(done), 0)) break;
     }
-    const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
-    const int chunks = min(8, (a.K - kc * kUnitK) / 32);
-#pragma unroll
-    for (int part = 0; part < kParts; ++part, ++i) {
-      const int s = i % kStages;
-      if (mbar_wait_warp(smem_u32(&full[s]), (i / kStages) & 1, abort_flag, a.wait_limit, &g_stream_err))
-        consume<FMT, MODE, NT>(smem + s * kStageBytes, chunks, tokens, rg, kh, lane,
-                               MODE == kDown ? run : acc + part * NT);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ draining the sums
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    Place<MODE> at(a, n_experts, u0);
+    Turn turn, buf;
+    bool begins = true;  // down: the next unit is the first of a tile
+    for (int left = n_mine; left > 0; --left) {
+      const int slot = at.slot, row = at.row, kc = at.kc;
+      const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
+      const int n_tok = __popc(tokens);
+      const bool tile_ends = left == 1 || at.ends(a, n_experts);
+      at.next(a, n_experts);
+      float v[kMaxTokens * kMatrices];  // the row's values: token by token; up: gate's, then up's
       if constexpr (MODE == kDown) {
-        // weight, down's factor and that of h's half, all after the sum of products; an expert's sums go to its own
-        // tokens only: a NaN of its weights reaches no other
-        if (slot != slot_of_share) {
-          slot_of_share = slot;
-          const float fd = a.f2 ? __ldg(a.f2 + ex->expert[slot]) : 1.f;
+        if (begins)
+          for (int t = 0; t < a.M; ++t) sums[t * kRows + r] = 0.f;
+        begins = tile_ends;
+        // h's factors of the two halves of k, beside the scales of their first tiles
+        float f[2] = {0.f, 0.f};
+        if (mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err) && lane < n_tok) {
+          const uint8_t* line = smem + turn.i * stage_bytes + off_xs + lane * token_lines(FMT);
+          const float w = ex->weight[ex->place[slot][nth_bit(tokens, lane)]] * (a.f0 ? __ldg(a.f0 + ex->expert[slot]) : 1.f);
+          f[0] = w * *reinterpret_cast<const float*>(line + 4);
+          f[1] = w * *reinterpret_cast<const float*>(line + kTiles / 2 * kLines + 4);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[turn.i]));
+        turn.next(n_stages);
+        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
+        tc_fence_after();
+        if (ok) {
+          const uint32_t d = tmem + lanes + buf.i * buffer_cols;
+          const bool both = a.K - kc * kUnitK > kUnitK / 2;
+          unsigned m = tokens;
+          for (int j = 0; j < n_tok; j += 2) {
+            float c[2][16];
+            tmem_ld16(d + 8 * j, c[0]);
+            if (both) tmem_ld16(d + cols + 8 * j, c[1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int o = 0; o < 2; ++o) {
+              if (j + o >= n_tok) break;
+              float s = join_parts(c[0] + 8 * o) * __shfl_sync(0xffffffffu, f[0], j + o);
+              const float f1 = __shfl_sync(0xffffffffu, f[1], j + o);
+              if (both) s = fmaf(join_parts(c[1] + 8 * o), f1, s);
+              const int t = __ffs(static_cast<int>(m)) - 1;
+              m &= m - 1u;
+              sums[t * kRows + r] += s;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
+        buf.next(n_buffers);
+        if (!tile_ends) continue;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int token = 8 * n + t2 + c;
-              share[n][c] = (tokens >> token) & 1u ? ex->weight[ex->place[slot][token]] * fd : 0.f;
+        for (int t = 0; t < kMaxTokens; ++t) v[t] = t < a.M ? sums[t * kRows + r] : 0.f;
+      } else {
+        if (!tile_ends) continue;
+        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
+        if (ok) {
+          const uint32_t d = tmem + lanes + buf.i * buffer_cols;
+#pragma unroll
+          for (int w = 0; w < kMatrices; ++w)
+#pragma unroll
+            for (int j = 0; j < kMaxTokens; j += 2) {
+              if (j < n_tok) {
+                float c[16];
+                tmem_ld16(d + w * cols + 8 * j, c);
+                v[w * kMaxTokens + j] = join_parts(c);
+                v[w * kMaxTokens + j + 1] = join_parts(c + 8);
+              }
             }
         }
-        const uint8_t* x = smem + s * kStageBytes + kCodeBytes + kScaleRoom + kUnitK * 4 + 4 * kh;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int token = 8 * n + t2 + c;
-            if (4 * kh < chunks && ((tokens >> token) & 1u)) {
-              const float f = share[n][c] * *reinterpret_cast<const float*>(x + token * kHStride);
-              acc[n][c] = fmaf(run[n][c], f, acc[n][c]);
-              acc[n][2 + c] = fmaf(run[n][2 + c], f, acc[n][2 + c]);
-            }
-            run[n][c] = run[n][2 + c] = 0.f;
-          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
+        buf.next(n_buffers);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty[s]));
-    }
-    const bool tile_ends = (u + 1) % un.tile_units == 0 || u + 1 == u1;
-    if (!tile_ends) continue;
 
-    // the two halves of k: the second's sums through shared memory (two areas in turn, one barrier a tile)
-    float4* area = meet + (tiles_done & 1) * 8 * 32 * kAccs;
-    ++tiles_done;
-    if (kh == 1) {
-#pragma unroll
-      for (int n = 0; n < kAccs; ++n)
-        area[(rg * kAccs + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-    if (kh == 0) {
-#pragma unroll
-      for (int n = 0; n < kAccs; ++n) {
-        const float4 v = area[(rg * kAccs + n) * 32 + lane];
-        acc[n][0] += v.x; acc[n][1] += v.y; acc[n][2] += v.z; acc[n][3] += v.w;
-      }
-      const long long tile = u / un.tile_units;
-      const long long first = tile * un.tile_units, end = first + un.tile_units;
-      const int b0 = owner(first, un.n, ctas), b1 = owner(end - 1, un.n, ctas);
+      // ---- the tile, or this CTA's part of it
+      const int n_val = MODE == kDown ? a.M : n_tok;
+      const int tile = MODE == kUp ? slot * a.row_tiles + row : row;
+      const int tile_units = a.k_units * (MODE == kDown ? n_experts : 1);
+      const long long first = static_cast<long long>(tile) * tile_units, end = first + tile_units;
+      const int b0 = owner(first, n_units, ctas), b1 = owner(end - 1, n_units, ctas);
       bool mine = true;  // this CTA writes the result
       if (b0 != b1) {
         auto part_of = [&](int b) {  // a CTA's tile that began before it is its part 0
-          return reinterpret_cast<float4*>(a.part) +
-                 (static_cast<size_t>(b) * 2 + (first < b * un.n / ctas ? 0 : 1)) * (part_floats(MODE, NT) / 4);
+          return a.part + (static_cast<size_t>(b) * 2 + (first < b * n_units / ctas ? 0 : 1)) * part_floats(MODE) + r;
         };
-        float4* p = part_of(blockIdx.x);
+        float* p = part_of(blockIdx.x);
 #pragma unroll
-        for (int n = 0; n < kAccs; ++n)
-          __stcg(p + (rg * kAccs + n) * 32 + lane, make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]));
+        for (int w = 0; w < kMatrices; ++w)
+#pragma unroll
+          for (int j = 0; j < kMaxTokens; ++j)
+            if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w * kMaxTokens + j]);
         __threadfence();
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (threadIdx.x == 0) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 64) {
           int is_last = 0;
           if (!*abort_flag) {
             const unsigned before = atomicAdd(a.counters + tile, 1u);
@@ -514,94 +662,101 @@ __global__ void __launch_bounds__(kThreads, 1)
           __threadfence();
           *last = is_last;
         }
-        asm volatile("bar.sync 2, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         mine = *last != 0;
         if (mine) {
 #pragma unroll
-          for (int n = 0; n < kAccs; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+          for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
           for (int b = b0; b <= b1; ++b) {
-            const float4* o = part_of(b);
+            const float* o = part_of(b);
 #pragma unroll
-            for (int n = 0; n < kAccs; ++n) {
-              const float4 v = __ldcg(o + (rg * kAccs + n) * 32 + lane);
-              acc[n][0] += v.x; acc[n][1] += v.y; acc[n][2] += v.z; acc[n][3] += v.w;
-            }
+            for (int w = 0; w < kMatrices; ++w)
+#pragma unroll
+              for (int j = 0; j < kMaxTokens; ++j)
+                if (j < n_val) v[w * kMaxTokens + j] += __ldcg(o + (w * kMaxTokens + j) * kRows);
           }
         }
       }
-      // lane's results: rows r and r + 8, tokens t2 and t2 + 1 of each eight
-      const int r = row * kRows + rg * 16 + g;
+      if (!mine) continue;
+      const int n_row = row * kRows + r;
+      const bool in = n_row < a.rows;
       if constexpr (MODE == kUp) {
-        if (mine) {
-          const int id = ex->expert[slot];
-          const float fg = a.f0 ? __ldg(a.f0 + id) : 1.f, fu = a.f1 ? __ldg(a.f1 + id) : 1.f;
-          // h of the lane's two rows, and the largest of the tile for each token
-          float most[NT][2];
+        const int id = ex->expert[slot];
+        const float fx = FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f;  // of x's parts
+        const float fg = (a.f0 ? __ldg(a.f0 + id) : 1.f) * fx, fu = (a.f1 ? __ldg(a.f1 + id) : 1.f) * fx;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < kMaxTokens; ++j) {
+          if (j >= n_tok) break;
+          const float h = activate(v[j] * fg, a.act) * (v[kMaxTokens + j] * fu);
+          v[j] = in ? h : 0.f;
+          float m = fabsf(v[j]);
+          if (!isfinite(m)) m = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                acc[n][2 * j + c] = activate(acc[n][2 * j + c] * fg, a.act) * (acc[NT + n][2 * j + c] * fu);
-              float m = fmaxf(r < a.rows ? fabsf(acc[n][c]) : 0.f, r + 8 < a.rows ? fabsf(acc[n][2 + c]) : 0.f);
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-              if (g == 0) ex->most[rg][8 * n + t2 + c] = m;
-            }
-          asm volatile("bar.sync 2, 256;" ::: "memory");
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              most[n][c] = 0.f;
-#pragma unroll
-              for (int w = 0; w < 8; ++w) most[n][c] = fmaxf(most[n][c], ex->most[w][8 * n + t2 + c]);
-            }
-          if (!*abort_flag) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int token = 8 * n + t2 + c;
-                if (!((tokens >> token) & 1u)) continue;
-                // a power of two that brings the tile's largest to 1 .. 2 (exact; what is not finite stays)
-                const int e = min(max(static_cast<int>(__float_as_uint(most[n][c]) >> 23), 1), 253);
-                const float up = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                uint16_t* h = a.out + (static_cast<size_t>(ex->place[slot][token]) * a.h_units + (row >> 1)) * (kHPiece / 2);
-                if (g == 0 && rg == 0) reinterpret_cast<float*>(h + kUnitK * 2)[row & 1] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (r + 8 * j >= a.rows) continue;
-                  const float v = acc[n][2 * j + c] * up;
-                  const __half hi = __float2half_rn(v);
-                  const float rest = v - __half2float(hi);
-                  const int at = (row & 1) * kRows + rg * 16 + g + 8 * j;
-                  h[at] = __half_as_ushort(hi);
-                  h[kUnitK + at] = __half_as_ushort(__float2half_rn(isfinite(rest) ? rest : 0.f));
-                }
-              }
-          }
+          for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          if (lane == 0) ex->most[quarter][j] = m;
         }
-      } else if (mine && !*abort_flag) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        unsigned left_tokens = tokens;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < kMaxTokens; ++j) {
+          if (j >= n_tok) break;
+          const int token = __ffs(static_cast<int>(left_tokens)) - 1;
+          left_tokens &= left_tokens - 1u;
+          const float most = fmaxf(fmaxf(ex->most[0][j], ex->most[1][j]), fmaxf(ex->most[2][j], ex->most[3][j]));
+          const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126);  // tile's largest: 2^e ..
+          const float h = v[j] * pow2(-e);
+          // the block's scale: 16 or 32 rows, a lane each
+          float m = fabsf(h);
+          bool bad = !isfinite(h);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int token = 8 * n + t2 + c;
-            if (token >= a.M) continue;
-            uint16_t* y = a.out + static_cast<size_t>(token) * a.rows;
-            if (r < a.rows) y[r] = __half_as_ushort(__float2half_rn(acc[n][c] * a.factor));
-            if (r + 8 < a.rows) y[r + 8] = __half_as_ushort(__float2half_rn(acc[n][2 + c] * a.factor));
+          for (int d = 1; d < fp4_block(FMT); d <<= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), d) != 0;
           }
+          const int pe = bad ? 0 : part_exponent<FMT>(m, kHTop);
+          const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(pe, kHTop);
+          float q = bad ? 0.f : h * pow2(-pe);
+          const size_t pair = ex->place[slot][token];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            uint32_t code;
+            float val;
+            e2m1_nearest(q, code, val);
+            q = (q - val) * 8.f;
+            uint32_t word = code << (4 * (lane & 7));
+            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            if ((lane & 7) == 0 && in)
+              *reinterpret_cast<uint32_t*>(a.h_codes + (pair * kParts + p) * (a.rows / 2) + n_row / 2) = word;
+          }
+          // the scale lines: 8 of each tile, their first word the four blocks' bytes; beside the first tile's h's factor
+          uint8_t* lines = a.h_scales + (pair * a.h_units + (row >> 1)) * token_lines(FMT) + (row & 1) * (kTiles / 2) * kLines;
+          if constexpr (FMT == EXQ_FP4_E4M3) {
+            // a tile is 64 rows, a warp has 2 of its 4 blocks: a half word
+            const uint32_t b0 = __shfl_sync(0xffffffffu, byte, 0), b1 = __shfl_sync(0xffffffffu, byte, 16);
+            if (lane < 8)
+              *reinterpret_cast<uint16_t*>(lines + (quarter >> 1) * kLines + lane * 16 + (quarter & 1) * 2) = static_cast<uint16_t>(b0 | (b1 << 8));
+          } else if (lane < 8) {
+            lines[lane * 16 + quarter] = static_cast<uint8_t>(byte);
+          }
+          if (r == 0) *reinterpret_cast<float*>(lines + 4) = pow2(e) * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kHTop)) : 1.f);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // `most` is free again
+      } else if (!*abort_flag && in) {
+        const float f = MODE == kGemv ? a.factor * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f) : 1.f;
+#pragma unroll
+        for (int t = 0; t < kMaxTokens; ++t)
+          if (t < a.M) a.y[static_cast<size_t>(t) * a.rows + n_row] = __half_as_ushort(__float2half_rn(v[t] * f));
       }
     }
-#pragma unroll
-    for (int n = 0; n < kAccs; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 

@@ -100,7 +100,7 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uin
 size_t fp4_gemm_workspace_bytes(const exq_fp4_matrix& a, const exq_fp4_matrix& w, int sms);
 exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, uint16_t* y, void* workspace, int sms,
                            int device, cudaStream_t stream);
-size_t fp4_gemv_workspace_bytes(int M, int sms);
+size_t fp4_gemv_workspace_bytes(const exq_fp4_matrix& w, int M, int sms);
 bool fp4_gemv_fits(int rows);  // whether the row tiles have counters
 exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t* ids, float* weights, uint16_t* y,
                       void* workspace, int sms, int device, cudaStream_t stream);

@@ -114,6 +114,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One lane of a converged warp. The code around it stays the whole warp's: the
+// operands of tcgen05 instructions are uniform registers, and a loop that one
+// lane runs alone brings each of them there anew (150 clocks an MMA, where the
+// tensor core takes 46).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 constexpr int kFp4WaitLimit = 1 << 22;  // try_wait rounds before giving up
 
 // Bounded wait of one thread or of a whole warp (every lane tests; a vote

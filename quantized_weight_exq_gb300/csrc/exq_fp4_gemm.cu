@@ -187,14 +187,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = idesc_for(FMT, n_mma);
-      for (int i = 0; i < n_iter; ++i) {
-        const int s = i % kStages;
-        if (!mbar_wait(smem_u32(&full[s]), (i / kStages) & 1, abort_flag, p.wait_limit, &g_fp4_gemm_err)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + s * kStageBytes);
-        const int n_k = min(4, (p.K - (u0 + i) * BK + 63) / 64);  // MMAs with k of the matrices
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_for(FMT, n_mma);
+    for (int i = 0; i < n_iter; ++i) {
+      const int s = i % kStages;
+      if (!mbar_wait_warp(smem_u32(&full[s]), (i / kStages) & 1, abort_flag, p.wait_limit, &g_fp4_gemm_err)) break;
+      tc_fence_after();
+      const uint32_t st = smem_u32(smem) + s * kStageBytes;
+      const int n_k = min(4, (p.K - (u0 + i) * BK + 63) / 64);  // MMAs with k of the matrices
+      if (leader) {
 #pragma unroll
         for (int j = 0; j < kTilesUnit; ++j) {
           copy_scales(tmem + kTmemSA + 4 * j, scale_desc(st + kOffSA + j * 512));
@@ -202,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           copy_scales(tmem + kTmemSB + 8 * j + 4, scale_desc(st + kOffSB + kScaleTiles + j * 512));
         }
         const uint64_t ad = codes_desc(st), bd = codes_desc(st + kOffB);
-        for (int j = 0; j < n_k; ++j) {  // 64 k: 32 bytes of a row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
+          if (j >= n_k) break;
           if constexpr (FMT == EXQ_FP4_E4M3) {
             mma_scaled<FMT>(tmem, ad + 2 * j, bd + 2 * j, idesc, tmem + kTmemSA + 4 * j, tmem + kTmemSB + 8 * j,
                             (i | j) != 0);
@@ -214,8 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(smem_u32(&empty[s]));
       }
-      commit(smem_u32(done));
+      __syncwarp();
     }
+    if (leader) commit(smem_u32(done));
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     if (mbar_wait_warp(smem_u32(done), 0, abort_flag, p.wait_limit, &g_fp4_gemm_err) && !*abort_flag) {

@@ -488,67 +488,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      Place<MODE> at(a, n_experts, u0);
-      Turn turn, buf;
-      bool fresh = true;  // the next unit begins a buffer
-      bool ok = true;
-      for (int left = n_mine; left > 0 && ok; --left) {
-        const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
-        const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
-        const uint32_t d0 = tmem + buf.i * buffer_cols;
-        if (fresh && !mbar_wait(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
+    const bool leader = elect_one();
+    Place<MODE> at(a, n_experts, u0);
+    Turn turn, buf;
+    bool fresh = true;  // the next unit begins a buffer
+    bool ok = true;
+    const uint32_t sa = tmem + kTmemScales;
+    for (int left = n_mine; left > 0 && ok; --left) {
+      const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
+      const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
+      const uint32_t d0 = tmem + buf.i * buffer_cols;
+      if (fresh && !mbar_wait_warp(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
 #pragma unroll
-        for (int which = 0; which < kMatrices; ++which) {
-          if (!mbar_wait(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + turn.i * stage_bytes);
-          const uint32_t sa = tmem + kTmemScales;
+      for (int which = 0; which < kMatrices; ++which) {
+        if (!mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem) + turn.i * stage_bytes;
+        if (leader) {
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
-          const uint64_t ad = codes_desc(st);
-          for (int g = 0; g < tokens; g += MODE == kGemv ? kMaxTokens : 4) {
-            // gemv: all tokens, their scales in tiles; else four, from their own lines
-            const uint32_t sb = sa + 16 + 4 * g;
+        }
+        const uint64_t ad = codes_desc(st);
+        for (int g = 0; g < tokens; g += MODE == kGemv ? kMaxTokens : 4) {
+          // gemv: all tokens, their scales in tiles; else four, from their own lines
+          const uint32_t sb = sa + 16 + 4 * g;
+          const int m = MODE == kGemv ? tokens : min(4, tokens - g);
+          const uint32_t idesc = idesc_for(FMT, (8 * m + 15) / 16 * 16);
+          const uint64_t bd = codes_desc(st + kOffX + g * 1024);
+          const uint32_t d = d0 + 8 * g + which * cols;
+          if (leader) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
               copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
                                                     : lines_desc(st + off_xs + g * token_lines(FMT) + j * kLines, token_lines(FMT)));
-            const int m = MODE == kGemv ? tokens : min(4, tokens - g);
-            const uint32_t idesc = idesc_for(FMT, (8 * m + 15) / 16 * 16);
-            const uint64_t bd = codes_desc(st + kOffX + g * 1024);
-            for (int j = 0; j < n_k; ++j) {  // 64 k: 32 bytes of a row
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
+              if (j >= n_k) break;
               // down: each half of 128 k has its own sums, and every unit its own
-              const uint32_t d = d0 + 8 * g + (MODE == kUp ? which * cols : MODE == kDown ? (j >> 1) * cols : 0);
-              const bool first = MODE == kDown ? (j & 1) == 0 : fresh && j == 0;
+              const uint32_t dj = MODE == kDown && j >= 2 ? d + cols : d;
+              const bool first = MODE == kDown ? (j & 1) == 0 : j == 0 && fresh;
               if constexpr (FMT == EXQ_FP4_E4M3) {
-                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 4 * j, !first);
+                mma_scaled<FMT>(dj, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 4 * j, !first);
               } else {  // two scales of the tile's four: byte 0 or 2 of each word
                 const uint32_t id = (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
-                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * (j >> 1), !first);
+                mma_scaled<FMT>(dj, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * (j >> 1), !first);
               }
             }
           }
-          commit(smem_u32(&empty[turn.i]));
-          turn.next(n_stages);
+          __syncwarp();
         }
-        if (!ok) break;
-        fresh = MODE == kDown || left == 1 || at.ends(a, n_experts);
-        if (fresh) {
-          commit(smem_u32(&dfull[buf.i]));
-          buf.next(n_buffers);
-        }
-        at.next(a, n_experts);
+        if (leader) commit(smem_u32(&empty[turn.i]));
+        __syncwarp();
+        turn.next(n_stages);
       }
-      // the MMAs are over before tensor memory is given back
-      commit(smem_u32(done));
-      for (int r = 0; r < a.wait_limit; ++r)
-        if (mbar_try_wait(smem_u32(done), 0)) break;
+      if (!ok) break;
+      fresh = MODE == kDown || left == 1 || at.ends(a, n_experts);
+      if (fresh) {
+        if (leader) commit(smem_u32(&dfull[buf.i]));
+        __syncwarp();
+        buf.next(n_buffers);
+      }
+      at.next(a, n_experts);
     }
+    // the MMAs are over before tensor memory is given back
+    if (leader) commit(smem_u32(done));
     __syncwarp();
+    for (int r = 0; r < a.wait_limit; ++r)
+      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(done), 0))) break;
   } else {
     // ------------------------------------------------------------ draining the sums
     const int quarter = warp & 3, r = quarter * 32 + lane;

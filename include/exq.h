@@ -716,12 +716,14 @@ exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16
 size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M);
 
 /* exq_fp4_gemv -- device, asynchronous: y fp16 [M, w.rows] = x . w^T for a few
- * rows x fp16 [M, K] as they are (not quantised), 1 <= M <= 16; products and
- * sums in fp32, w.factor and one rounding at the end. The codes are read once.
+ * rows x fp16 [M, K], 1 <= M <= 16. x enters the product to 2^-23 of the
+ * largest of its block of 16 or 32 (and 2^-25), sums are fp32, w.factor and one
+ * rounding come at the end. An infinity or a NaN in a row of x makes that row
+ * of y NaN. The codes are read once.
  *   workspace  as above, 256-byte aligned; calls that may overlap on the GPU
  *              need separate ones.
  * w.rows % 8 == 0. Deterministic on the same device. EXQ_ERR_UNSUPPORTED for
- * M > 16 (use exq_fp4_gemm) or more than 4,194,176 rows; EXQ_ERR_INVALID_ARG for
+ * M > 16 (use exq_fp4_gemm), more than 4,194,176 rows or K > 2^25; EXQ_ERR_INVALID_ARG for
  * M < 1, bad pointers, sizes or workspace. */
 exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, int32_t M, uint16_t* y, void* workspace,
                         size_t ws_bytes, void* stream);
@@ -760,9 +762,9 @@ size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T);
  *   weights[t][j] = exp(logit - max) / sum (see renorm);
  *   y[t] = fp16_RNE(sum_j weights[t][j] * (act(x gate^T) * (x up^T)) down^T)
  * with the experts' products over x as it is and fp32 sums. What lies between
- * the products is held as the sum of two fp16 numbers times a power of two for
- * each 128 values (22 bits of the largest); weights and factors are applied in
- * fp32 after the sums.
+ * the products is held to 2^-23 of the largest of its block; weights and
+ * factors are applied in fp32 after the sums. An infinity or a NaN in a token
+ * makes its result NaN.
  *   ids      device int32 [T, top_k], weights device fp32 [T, top_k]: written
  *            when the layer has a router, read when it has none. An id of -1
  *            is an unused place; one that repeats counts each time; another
@@ -773,7 +775,7 @@ size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T);
  *   workspace  as for exq_fp4_gemv.
  * Only the chosen experts are read, each once. D % 32 == 0, I % 32 == 0, at
  * most 512 experts. Deterministic on the same device. EXQ_ERR_UNSUPPORTED for
- * T > 16, more than 512 experts, top_k > 16 or sizes whose tiles outnumber the counters;
+ * T > 16, more than 512 experts, top_k > 16, D or I > 2^25 or sizes whose tiles outnumber the counters;
  * EXQ_ERR_INVALID_ARG for anything else out of range. */
 exq_status exq_moe(const exq_moe_layer* layer, const uint16_t* x, int32_t T, int32_t* ids, float* weights, uint16_t* y,
                    void* workspace, size_t ws_bytes, void* stream);

@@ -409,6 +409,8 @@ namespace {
 // block size of a format, 0 for an unknown one
 int fp4_block_of(int format) { return format == EXQ_FP4_E4M3 ? 16 : format == EXQ_FP4_E8M0 ? 32 : 0; }
 
+constexpr int kFp4MostK = 1 << 25;  // of the few-row products: they count x's values in 32 bits
+
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 exq_status check_fp4(const exq_fp4_matrix* m) {
@@ -476,7 +478,7 @@ extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix
 
 extern "C" size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M) {
   const int sms = current_sms();
-  if (check_fp4(w) != EXQ_OK || w->rows <= 0 || w->rows % 8 || M < 1 || M > 16 || sms <= 0) return 0;
+  if (check_fp4(w) != EXQ_OK || w->rows <= 0 || w->rows % 8 || w->K > kFp4MostK || M < 1 || M > 16 || sms <= 0) return 0;
   return fp4_gemv_workspace_bytes(*w, M, sms);
 }
 
@@ -485,7 +487,7 @@ extern "C" exq_status exq_fp4_gemv(const exq_fp4_matrix* w, const uint16_t* x, i
   const exq_status st = check_fp4(w);
   if (st != EXQ_OK) return st;
   if (w->rows <= 0 || w->rows % 8 || M < 1 || !x || !y || !aligned16(x) || !aligned16(y)) return EXQ_ERR_INVALID_ARG;
-  if (M > 16 || !fp4_gemv_fits(w->rows)) return EXQ_ERR_UNSUPPORTED;
+  if (M > 16 || !fp4_gemv_fits(w->rows) || w->K > kFp4MostK) return EXQ_ERR_UNSUPPORTED;
   const int sms = current_sms();
   if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
   if (!workspace || !aligned256(workspace) || ws_bytes < fp4_gemv_workspace_bytes(*w, M, sms)) return EXQ_ERR_INVALID_ARG;
@@ -515,7 +517,7 @@ exq_status check_moe(const exq_moe_layer* l, int T) {
   if (l->top_k < 1 || l->top_k > n || (l->renorm != 0 && l->renorm != 1) ||
       (l->act != EXQ_ACT_SILU && l->act != EXQ_ACT_GELU_TANH) || !aligned16(l->router))
     return EXQ_ERR_INVALID_ARG;
-  if (T > 16 || l->top_k > 16 || n > 512 || !moe_fits(*l, T)) return EXQ_ERR_UNSUPPORTED;
+  if (T > 16 || l->top_k > 16 || n > 512 || D > kFp4MostK || I > kFp4MostK || !moe_fits(*l, T)) return EXQ_ERR_UNSUPPORTED;
   return EXQ_OK;
 }
 

@@ -16,8 +16,11 @@ struct PrepareArgs {
   const uint16_t* x;       // [T, D]
   // x's parts for the streaming kernel
   uint32_t* codes;         // [T * 8, D / 2] bytes
-  uint32_t* scales;        // tiles, or lines for each [token, unit]
-  int split_blocks, k_units;
+  uint32_t* scales;        // gemv: the parts' scale tiles
+  uint8_t* pieces;         // experts: [rows, units]
+  const float* h;          // instead of x: [T, D] in fp32,
+  unsigned* h_most;        // and each row's largest magnitude (zeroed by the launch that splits x)
+  int split_blocks, k_units, pairs;
   // routing, where the layer has a router
   const uint16_t* router;  // [E, D]
   float* logits;           // [T, E]
@@ -29,45 +32,61 @@ struct PrepareArgs {
 
 constexpr int kPrepareThreads = 256;
 
-// Rows of x as eight 4-bit rows each (see exq_fp4_stream.cuh): a thread takes 8
+// Rows as eight 4-bit rows each (see exq_fp4_stream.cuh): a thread takes 8
 // values, the 2 or 4 of a block find its scale together, and those of a scale
-// word write it to the 8 rows. Blocks past the row's end are written as blocks
-// of zeros as far as their scale tile goes: the MMAs read them.
-template <int FMT, bool TILES>
-__device__ __forceinline__ void split_x(const PrepareArgs& a) {
+// word write it to the 8 rows. What lies past the row's end is written as
+// zeros as far as its scale tile (the MMAs read it) or its unit (no copy
+// fills it up) goes. H: rows of h, divided by the power of two of each.
+template <int FMT, bool TILES, bool H>
+__device__ __forceinline__ void split_rows(const PrepareArgs& a) {
   constexpr int kBlockThreads = fp4_block(FMT) / 8, kWordThreads = 4 * kBlockThreads;
-  const int k_tiles = (a.D + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
-  const int row_threads = k_tiles * kWordThreads;
-  const int total = a.T * row_threads;
-  const int stride = a.split_blocks * kPrepareThreads;
-  const int padded = (total + 31) / 32 * 32;  // whole warps
-  for (int i = (blockIdx.x * kPrepareThreads) + threadIdx.x; i < padded; i += stride) {
+  constexpr int kTop = H ? kHTop : kXTop;
+  const int row_threads = TILES ? (a.D + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT) * kWordThreads : a.k_units * (kUnitK / 8);
+  const int total = a.T * row_threads;            // below 2^31: K is, by the entry points, at most 2^25
+  const int padded = (total + 31) / 32 * 32;      // whole warps
+  for (int i = static_cast<int>(blockIdx.x) * kPrepareThreads + threadIdx.x; i < padded; i += a.split_blocks * kPrepareThreads) {
     const int t = i / row_threads, c = i - t * row_threads;
     const bool in = i < total && c * 8 < a.D;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (in) x = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.D) + c);
-    const uint32_t h[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m2 = 0u;
+    float q[8] = {};
+    uint32_t m = 0u;  // bits of the block's largest magnitude in fp32
+    if (in) {
+      if constexpr (H) {
+        const float4* src = reinterpret_cast<const float4*>(a.h + static_cast<size_t>(t) * a.D + 8 * c);
+        const float4 u = __ldcg(src), v = __ldcg(src + 1);
+        const float r = pow2(-h_exponent(__ldcg(a.h_most + t)));
+        q[0] = u.x * r; q[1] = u.y * r; q[2] = u.z * r; q[3] = u.w * r;
+        q[4] = v.x * r; q[5] = v.y * r; q[6] = v.z * r; q[7] = v.w * r;
+      } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.D) + c);
+        const uint32_t h[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, h[j] & 0x7FFF7FFFu);
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+          q[2 * j] = v.x;
+          q[2 * j + 1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(q[j]) & 0x7FFFFFFFu);  // (infinity and NaN are above all others)
+    }
 #pragma unroll
     for (int d = 1; d < kBlockThreads; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const bool bad = m >= 0x7C00u;  // an infinity or a NaN: the block is NaN
-    const int e = bad ? 0 : part_exponent<FMT>(__half2float(__ushort_as_half(static_cast<unsigned short>(m))), kXTop);
-    const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(e, kXTop);
+    const bool bad = m >= 0x7F800000u;  // the block is NaN
+    const int e = bad ? 0 : part_exponent<FMT>(__uint_as_float(m), kTop);
+    const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(e, kTop);
     const float r = pow2(-e);
-    float q[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-      q[2 * j] = bad ? 0.f : v.x * r;
-      q[2 * j + 1] = bad ? 0.f : v.y * r;
-    }
+    for (int j = 0; j < 8; ++j) q[j] = bad ? 0.f : q[j] * r;
+    uint8_t* piece = nullptr;
+    if constexpr (!TILES) piece = a.pieces + (static_cast<size_t>(t) * a.k_units + c / (kUnitK / 8)) * piece_bytes(FMT);
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       const uint32_t word = e2m1x8(q);
-      if (in) a.codes[(static_cast<size_t>(t) * kParts + p) * (a.D / 8) + c] = word;
+      if constexpr (TILES) {
+        if (in) a.codes[(static_cast<size_t>(t) * kParts + p) * (a.D / 8) + c] = word;
+      } else {
+        if (i < total) *reinterpret_cast<uint32_t*>(piece + piece_word(p, 8 * c % kUnitK)) = word;
+      }
       const uint32_t v[4] = {e2m1x2_f16<0>(word), e2m1x2_f16<1>(word), e2m1x2_f16<2>(word), e2m1x2_f16<3>(word)};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -82,9 +101,9 @@ __device__ __forceinline__ void split_x(const PrepareArgs& a) {
     const int p = c % kWordThreads, tile = c / kWordThreads;
     if (i < total && p < kParts) {
       if constexpr (TILES)
-        a.scales[(tile * 512 + fp4_tile_byte(t * kParts + p)) / 4] = word;
+        a.scales[(static_cast<size_t>(tile) * 512 + fp4_tile_byte(t * kParts + p)) / 4] = word;
       else
-        a.scales[((static_cast<size_t>(t) * a.k_units * unit_tiles(FMT) + tile) * kLines + p * 16) / 4] = word;
+        *reinterpret_cast<uint32_t*>(piece + 1024 + tile % unit_tiles(FMT) * kLines + p * 16) = word;
     }
   }
 }
@@ -144,44 +163,52 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
 
   for (int t = warp; t < a.T; t += kPrepareThreads / 32) {
     constexpr int kPer = kMaxExperts / 32;
-    float v[kPer];  // lane's logits: experts lane, lane + 32, ...
-    unsigned gone = 0u;
+    // lane's logits (experts lane, lane + 32, ...) as unsigned keys that order as the numbers do, a NaN as -infinity, -0 as
+    // 0; above 0 for every number: 0 is what is not there or has been taken
+    float v[kPer];
+    unsigned keys[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = 32 * i + lane < a.E ? __ldcg(a.logits + t * a.E + 32 * i + lane) : 0.f;
+    for (int i = 0; i < kPer; ++i) {
+      if (32 * i >= a.E) break;
+      const bool there = 32 * i + lane < a.E;
+      v[i] = there ? __ldcg(a.logits + t * a.E + 32 * i + lane) : 0.f;
+      const unsigned b = v[i] != v[i] ? 0xFF800000u : v[i] == 0.f ? 0u : __float_as_uint(v[i]);
+      keys[i] = !there ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+    }
     float top = 0.f, total = 0.f, mine = 0.f;
     for (int j = 0; j < a.top_k; ++j) {
-      // the largest left: as unsigned keys that order as the numbers do, a NaN as -infinity
       unsigned key = 0u;
-      int at = 1 << 30;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (32 * i + lane >= a.E || (gone >> i & 1u)) continue;
-        const unsigned b = v[i] != v[i] ? 0xFF800000u : v[i] == 0.f ? 0u : __float_as_uint(v[i]);
-        const unsigned k = b & 0x80000000u ? ~b : b | 0x80000000u;  // above 0 for every number
-        if (k > key) { key = k; at = 32 * i + lane; }
+        if (32 * i >= a.E) break;
+        key = max(key, keys[i]);
       }
+      key = __reduce_max_sync(0xffffffffu, key);
+      unsigned at = 0xFFFFFFFFu;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) {
-        const unsigned k = __shfl_xor_sync(0xffffffffu, key, d);
-        const int o = __shfl_xor_sync(0xffffffffu, at, d);
-        if (k > key || (k == key && o < at)) { key = k; at = o; }
-      }
+      for (int i = kPer - 1; i >= 0; --i)
+        if (32 * i < a.E && keys[i] == key) at = 32 * i + lane;
+      at = __reduce_min_sync(0xffffffffu, at);
       float l = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (32 * i + lane == at) { gone |= 1u << i; l = v[i]; }
+      for (int i = 0; i < kPer; ++i) {
+        if (32 * i >= a.E) break;
+        if (32 * i + lane == at) { keys[i] = 0u; l = v[i]; }
+      }
       l = __shfl_sync(0xffffffffu, l, at & 31);
       if (j == 0) top = l;
       const float p = expf(l - top);
       if (lane == j) mine = p;
       total += p;
-      if (lane == 0) a.ids[t * a.top_k + j] = at;
+      if (lane == 0) a.ids[t * a.top_k + j] = static_cast<int>(at);
     }
     if (!a.renorm) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (32 * i >= a.E) break;
         if (32 * i + lane < a.E) s += expf(v[i] - top);
+      }
 #pragma unroll
       for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
       total = s;
@@ -195,19 +222,37 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
 template <int FMT, bool TILES, int TT>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) < a.split_blocks)
-    split_x<FMT, TILES>(a);
-  else if constexpr (TT > 0)
+  if (static_cast<int>(blockIdx.x) < a.split_blocks) {
+    if (!TILES && blockIdx.x == 0)
+      for (int i = threadIdx.x; i < a.pairs; i += kPrepareThreads) a.h_most[i] = 0u;
+    split_rows<FMT, TILES, false>(a);
+  } else if constexpr (TT > 0) {
     route<TT>(a);
+  }
+}
+
+// Between the experts' products: h's parts. (Places that nothing was written
+// to are split all the same; nobody reads them.)
+template <int FMT>
+__global__ void __launch_bounds__(kPrepareThreads) split_h_kernel(const __grid_constant__ PrepareArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the launch after this may start: what it reads before it waits is older than the launch before this
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  split_rows<FMT, false, true>(a);
 }
 
 // ---------------------------------------------------------------- launches
 
 int div_up(int a, int b) { return (a + b - 1) / b; }
 
+// blocks that split rows of D values, a thread 8 of them
+int split_blocks_for(int format, bool tiles, int rows, int D) {
+  const int k = tiles ? fp4_tile_k(format) : kUnitK;
+  return std::min(div_up(rows * div_up(D, k) * (k / 8), kPrepareThreads), 8192);
+}
+
 exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t stream) {
-  const int threads = p.T * div_up(p.D, fp4_tile_k(format)) * (fp4_tile_k(format) / 8);
-  p.split_blocks = div_up(threads, kPrepareThreads);
+  p.split_blocks = split_blocks_for(format, tiles, p.T, p.D);
   const bool e4m3 = format == EXQ_FP4_E4M3;
   constexpr int A = EXQ_FP4_E4M3, B = EXQ_FP4_E8M0;
   auto fn = tiles ? (e4m3 ? prepare_kernel<A, true, 0> : prepare_kernel<B, true, 0>)
@@ -217,6 +262,21 @@ exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t st
                        : (e4m3 ? prepare_kernel<A, false, 16> : prepare_kernel<B, false, 16>);
   fn<<<p.split_blocks + (p.router ? p.E : 0), kPrepareThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
+exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
+  p.split_blocks = split_blocks_for(format, false, p.T, p.D);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.split_blocks);
+  cfg.blockDim = dim3(kPrepareThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  auto fn = format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>;
+  return cudaLaunchKernelEx(&cfg, fn, p) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 
 // (each a programmatic dependent of the launch before it)
@@ -274,16 +334,16 @@ struct GemvPlan {
 };
 
 struct MoePlan {
-  size_t logits, x_codes, x_scales, h_codes, h_scales, part, end;
+  size_t logits, x, h, h_most, h_pieces, part, end;
   MoePlan(const exq_moe_layer& l, int T, int sms) {
     const int D = l.gate.K, I = l.gate.rows;
-    const size_t lines = token_lines(l.gate.format), pairs = static_cast<size_t>(T) * l.top_k;
+    const size_t piece = piece_bytes(l.gate.format), pairs = static_cast<size_t>(T) * l.top_k;
     logits = EXQ_FP4_COUNTER_BYTES;
-    x_codes = logits + round256(static_cast<size_t>(T) * l.gate.n_experts * 4);
-    x_scales = x_codes + round256(static_cast<size_t>(T) * kParts * D / 2);
-    h_codes = x_scales + round256(static_cast<size_t>(T) * div_up(D, kUnitK) * lines);
-    h_scales = h_codes + round256(pairs * kParts * I / 2);
-    part = h_scales + round256(pairs * div_up(I, kUnitK) * lines);
+    x = logits + round256(static_cast<size_t>(T) * l.gate.n_experts * 4);
+    h = x + round256(static_cast<size_t>(T) * div_up(D, kUnitK) * piece);
+    h_most = h + round256(pairs * I * 4);
+    h_pieces = h_most + round256(pairs * 4);
+    part = h_pieces + round256(pairs * div_up(I, kUnitK) * piece);
     end = part + std::max(part_bytes(kUp, sms), part_bytes(kDown, sms));
   }
 };
@@ -303,7 +363,7 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   const GemvPlan plan(w.format, w.K, M, sms);
   CUtensorMap mw, mx;
   if (!encode_codes(&mw, w.codes, w.rows, w.K, kRows) ||
-      !encode_codes(&mx, ws + plan.codes, static_cast<uint64_t>(M) * kParts, w.K, kParts))
+      !encode_codes(&mx, ws + plan.codes, static_cast<uint64_t>(M) * kParts, w.K, M * kParts))
     return EXQ_ERR_CUDA;
   PrepareArgs p{};
   p.x = x;
@@ -316,7 +376,7 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   Args a{};
   set_shape(a, w.format, w.rows, w.K);
   a.sc0 = w.scales;
-  a.x_scales = ws + plan.scales;
+  a.x = ws + plan.scales;
   a.y = y;
   a.M = M;
   a.factor = w.factor;
@@ -340,18 +400,18 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   const int E = l.gate.n_experts, D = l.gate.K, I = l.gate.rows, fmt = l.gate.format;
   unsigned* counters = reinterpret_cast<unsigned*>(ws);
   const uint64_t rows = static_cast<uint64_t>(E);
-  CUtensorMap mg, mu, md, mx, mh;
+  CUtensorMap mg, mu, md;
   if (!encode_codes(&mg, l.gate.codes, rows * I, D, kRows) || !encode_codes(&mu, l.up.codes, rows * I, D, kRows) ||
-      !encode_codes(&md, l.down.codes, rows * D, I, kRows) ||
-      !encode_codes(&mx, ws + plan.x_codes, static_cast<uint64_t>(T) * kParts, D, kParts) ||
-      !encode_codes(&mh, ws + plan.h_codes, static_cast<uint64_t>(T) * l.top_k * kParts, I, kParts))
+      !encode_codes(&md, l.down.codes, rows * D, I, kRows))
     return EXQ_ERR_CUDA;
 
   PrepareArgs p{};
   p.x = x;
-  p.codes = reinterpret_cast<uint32_t*>(ws + plan.x_codes);
-  p.scales = reinterpret_cast<uint32_t*>(ws + plan.x_scales);
+  p.pieces = ws + plan.x;
+  p.h = reinterpret_cast<float*>(ws + plan.h);
+  p.h_most = reinterpret_cast<unsigned*>(ws + plan.h_most);
   p.k_units = div_up(D, kUnitK);
+  p.pairs = T * l.top_k;
   p.router = l.router;
   p.logits = reinterpret_cast<float*>(ws + plan.logits);
   p.ids = ids;
@@ -370,10 +430,9 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.sc0 = l.gate.scales;
   a.sc1 = l.up.scales;
   a.sc_stride = exq_fp4_scale_bytes(fmt, I, D);
-  a.x_scales = ws + plan.x_scales;
-  a.h_codes = ws + plan.h_codes;
-  a.h_scales = ws + plan.h_scales;
-  a.h_units = div_up(I, kUnitK);
+  a.x = ws + plan.x;
+  a.h = reinterpret_cast<float*>(ws + plan.h);
+  a.h_most = reinterpret_cast<unsigned*>(ws + plan.h_most);
   a.f0 = l.gate.factors;
   a.f1 = l.up.factors;
   a.ids = ids;
@@ -384,17 +443,23 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.act = l.act;
   a.counters = counters;
   a.part = reinterpret_cast<float*>(ws + plan.part);
-  if ((st = launch_stream<kUp>(fmt, mg, mu, mx, a, sms, device, stream)) != EXQ_OK) return st;
+  if ((st = launch_stream<kUp>(fmt, mg, mu, mg, a, sms, device, stream)) != EXQ_OK) return st;
+
+  p.pieces = ws + plan.h_pieces;
+  p.T = T * l.top_k;
+  p.D = I;
+  p.k_units = div_up(I, kUnitK);
+  if ((st = launch_split_h(fmt, p, stream)) != EXQ_OK) return st;
 
   set_shape(a, fmt, D, I);
   a.sc0 = l.down.scales;
   a.sc1 = nullptr;
   a.sc_stride = exq_fp4_scale_bytes(fmt, D, I);
-  a.x_scales = ws + plan.h_scales;
+  a.x = ws + plan.h_pieces;
   a.f0 = l.down.factors;
   a.f1 = nullptr;
   a.y = y;
-  return launch_stream<kDown>(fmt, md, md, mh, a, sms, device, stream);
+  return launch_stream<kDown>(fmt, md, md, md, a, sms, device, stream);
 }
 
 unsigned take_fp4_stream_errors(cudaStream_t stream) {

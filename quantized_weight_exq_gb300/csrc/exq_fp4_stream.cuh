@@ -25,12 +25,12 @@
 // or 1 KB of scales). The units of a call, those of one output tile in a row,
 // are divided evenly over the CTAs, one an SM: no wave is left part-filled.
 //
-//   warp 0     producer: for each unit the codes as one 2-D box (128-byte
-//              rows, 128-byte swizzle), the scale tiles as one copy, and of
-//              each token its 8 rows of parts (1 KB: one swizzle atom) and
-//              their scales.
-//   warp 1     one lane copies scales to tensor memory and issues the MMAs
-//              (M = 128 rows of the matrix, N = 8 columns a token, K = 64).
+//   warp 0     brings a unit's codes, as one 2-D box (128-byte rows, 128-byte
+//              swizzle), and its scale tiles, as one copy.
+//   warp 6     brings the tokens' parts and their scales (a warp of its own:
+//              behind the weights' copies theirs cost 250 ns a unit).
+//   warp 1     copies scales to tensor memory and issues the MMAs (M = 128
+//              rows of the matrix, N = 8 columns a token, K = 64).
 //   warps 2-5  drain the sums: a lane is a row.
 //
 // A tile whose units lie in several CTAs goes through the workspace: each
@@ -49,24 +49,29 @@ enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 7 * 32;
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
 constexpr int kMaxPairs = 256;       // tokens x experts of each
 constexpr int kMaxExperts = 512;
 constexpr int kMaxStages = 10;
 
-// a stage: codes, scale tiles, the tokens' parts, their scales
+// a stage: codes, scale tiles, the tokens' parts and their scales
 constexpr int kOffScales = kRows * kUnitK / 2;
 constexpr int kOffX = kOffScales + 2048;
 static_assert(kOffX % 1024 == 0, "swizzle atoms");
-// An expert's tokens are picked one by one. Their scales of a unit are 8 lines
-// of 16 bytes (a line a row, its first word the scales) for each scale tile:
-// four such pieces, one a token, are what one copy to tensor memory takes, so
-// that MMAs are made for up to four tokens at a time.
+// The decode product takes all tokens: the parts are a matrix of 8 M rows with
+// its scale tiles. An expert's tokens are picked one by one: a token's parts
+// of a unit are a piece, written as shared memory has it: the 8 rows of 128
+// bytes, swizzled, then for each scale tile 8 lines of 16 bytes, a line a row,
+// its first word the scales. Four pieces' lines are what one copy to tensor
+// memory takes, so that MMAs are made for up to four tokens at a time.
 constexpr int kLines = 8 * 16;
+constexpr int kSlot = 2048;          // of a piece in a stage
 __host__ __device__ constexpr int unit_tiles(int fmt) { return kUnitK / fp4_tile_k(fmt); }
-__host__ __device__ constexpr int token_lines(int fmt) { return unit_tiles(fmt) * kLines; }
+__host__ __device__ constexpr int piece_bytes(int fmt) { return 1024 + unit_tiles(fmt) * kLines; }
+// byte of the word of 8 codes at k (a multiple of 8, in the unit) of part p
+__host__ __device__ constexpr int piece_word(int p, int k) { return p * 128 + (((k / 32) ^ p) * 16) + (k % 32) / 2; }
 
 constexpr int kSmemTotal = 226 * 1024;
 constexpr int kRest = 20 * 1024;     // barriers, the experts' tables, sums, alignment
@@ -80,8 +85,8 @@ constexpr int kMaxBuffers = 4;
 // An e4m3 scale has 18 powers of two: for fp16 the largest is 2^14 (times 2^-6
 // that is 2^8, e4m3's largest power), and a block whose scale would be under
 // the smallest takes that one, 2^-3: its eighth part counts 2^-25 then, half of
-// fp16's smallest number. What lies between the experts' products is brought
-// to [1, 2) first, for each 128 rows and token.
+// fp16's smallest number. What lies between an expert's products (h) is
+// divided by a power of two first that brings a token's largest to [1, 2).
 constexpr int kXTop = 14, kHTop = -1;          // exponents of the largest scales
 __host__ __device__ constexpr int e4m3_shift(int top) { return top - 8; }
 
@@ -89,10 +94,10 @@ struct Args {
   const uint8_t* sc0;      // scale tiles of the matrix, or of expert 0's gate or down
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
-  const uint8_t* x_scales; // gemv: scale tiles of the parts; else token_lines for each [token or pair, unit]
+  const uint8_t* x;        // gemv: scale tiles of the parts; else pieces [token or pair, unit]
   uint16_t* y;             // gemv [M, rows], down [M, rows]
-  uint8_t* h_codes;        // up: parts of h, [pairs * 8, rows / 2]
-  uint8_t* h_scales;       // up: token_lines for each [pair, h_units]
+  float* h;                // up: [pairs, rows]
+  unsigned* h_most;        // [pairs]: bits of the largest finite magnitude of h
   const float *f0, *f1;    // experts' factors of gate and up, or of down, or NULL
   const int32_t* ids;      // [M, top_k]
   const float* weights;
@@ -100,7 +105,7 @@ struct Args {
   float* part;             // [CTAs][2][part_floats]
   float factor;
   int rows, K, M;
-  int row_tiles, k_units, k_tiles, h_units;
+  int row_tiles, k_units, k_tiles;
   int top_k, n_experts, act;
   int wait_limit, starve;
 };
@@ -117,7 +122,6 @@ struct Experts {
   uint8_t place[kMaxPairs][kMaxTokens];       // the first, where an id repeats
   int ids[kMaxPairs];
   float weight[kMaxPairs];                    // by that place: those of an id that repeats are added up
-  float most[4][kMaxTokens];                  // up: the warps' largest h
 };
 static_assert(sizeof(Experts) + kRows * kMaxTokens * 4 + 512 + 1024 <= kRest, "shared memory budget");
 
@@ -139,13 +143,17 @@ __device__ __forceinline__ uint32_t part_scale_byte(int e, int top) {
   return p >= -6 ? static_cast<uint32_t>(p + 7) << 3 : 1u << (p + 9);
 }
 
+// h's power of two: e of [2^e, 2^(e + 1)) for the largest magnitude, given as bits
+__device__ __forceinline__ int h_exponent(unsigned most) { return min(max(static_cast<int>(most >> 23) - 127, -100), 126); }
+
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // ---------------------------------------------------------------- tcgen05
 
-__device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {  // K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+// K-major, 128-byte swizzle, 8-row groups `stride` bytes apart
+__device__ __forceinline__ uint64_t codes_desc(uint32_t addr, uint32_t stride) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (static_cast<uint64_t>(stride >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
 
@@ -361,6 +369,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   Experts* ex = reinterpret_cast<Experts*>(used + kMaxExperts / 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 2);  // the weights' and x's copies
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < kMaxBuffers; ++b) {
+      mbar_init(smem_u32(&dfull[b]), 1);
+      mbar_init(smem_u32(&dempty[b]), 4);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   if constexpr (MODE == kUp) {
     // ids and weights may come from the launch before
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -388,26 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_mine = static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0);
 
   // the ring and the buffers of sums go by the most tokens that a matrix of the call has
-  const int off_xs = kOffX + 1024 * most_tokens;
-  const int stage_bytes = (off_xs + (MODE == kGemv ? 2048 : (most_tokens + 3) / 4 * 4 * token_lines(FMT)) + 1023) / 1024 * 1024;
+  const int off_xs = kOffX + 1024 * most_tokens;                        // gemv: the parts' scale tiles
+  const int stage_bytes = MODE == kGemv ? off_xs + 2048 : kOffX + kSlot * ((most_tokens + 3) / 4 * 4);
   const int n_stages = min(kMaxStages, kRing / stage_bytes);
   const int cols = (8 * most_tokens + 15) / 16 * 16;                    // of one sum
-  const int buffer_cols = cols * (MODE == kGemv ? 1 : 2);               // up: gate, up; down: the halves of a unit's k
+  const int buffer_cols = cols * kMatrices;
   const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), MODE == kDown ? 5 : 1);  // the MMAs; down: and the warps that read h's factors
-    }
-    for (int b = 0; b < kMaxBuffers; ++b) {
-      mbar_init(smem_u32(&dfull[b]), 1);
-      mbar_init(smem_u32(&dempty[b]), 4);
-    }
-    mbar_init(smem_u32(done), 1);
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols) : "memory");
@@ -420,71 +428,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned everyone = (1u << a.M) - 1u;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (a.starve) {  // test hook: a starved producer issues nothing
-      if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
-    } else {
-      const int n = n_mine * kMatrices;
-      bool waited = MODE == kUp;  // for the launch that leaves x's parts
-      int issued = 0, x_from = 0;
-      Place<MODE> at(a, n_experts, u0), x_at = at;  // of the weights' and of x's next stage
-      Turn turn, x_turn;
-      auto issue_x = [&](int i) {
-        const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[x_at.slot];
-        uint8_t* st = smem + x_turn.i * stage_bytes;
-        const uint32_t bar = smem_u32(&full[x_turn.i]);
-        if (lane < __popc(tokens)) {  // lane: the number of the token among the unit's
-          const int token = MODE == kGemv ? lane : nth_bit(tokens, lane);
-          const int from = MODE == kDown ? ex->place[x_at.slot][token] : token;
-          tma_load_2d(smem_u32(st + kOffX + lane * 1024), &mx, x_at.kc * (kUnitK / 2), from * kParts, bar);
-          if constexpr (MODE != kGemv)
-            bulk_load(smem_u32(st + off_xs + lane * token_lines(FMT)),
-                      a.x_scales + (static_cast<size_t>(from) * a.k_units + x_at.kc) * token_lines(FMT), token_lines(FMT), bar);
+    // ------------------------------------------------------------ codes and scales of the matrix
+    const bool leader = elect_one();
+    int issued = 0;
+    if (!a.starve) {  // test hook: starved producers issue nothing
+      Place<MODE> at(a, n_experts, u0);
+      Turn turn;
+      bool ok = true;
+      for (int left = n_mine; left > 0 && ok; --left) {
+        const int id = MODE == kGemv ? 0 : ex->expert[at.slot];
+        const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
+        const size_t off = id * a.sc_stride + (static_cast<size_t>(at.row) * a.k_tiles + at.kc * kTiles) * 512;
+#pragma unroll
+        for (int which = 0; which < kMatrices; ++which) {
+          if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t st = smem_u32(smem) + turn.i * stage_bytes, bar = smem_u32(&full[turn.i]);
+            mbar_expect_tx(bar, kOffScales + sb);
+            tma_load_2d(st, which == 0 ? &m0 : &m1, at.kc * (kUnitK / 2), id * a.rows + at.row * kRows, bar);
+            bulk_load(st + kOffScales, (which == 0 ? a.sc0 : a.sc1) + off, sb, bar);
+          }
+          __syncwarp();
+          turn.next(n_stages);
+          ++issued;
         }
-        if constexpr (MODE == kGemv) {
-          if (lane == 0)
-            bulk_load(smem_u32(st + off_xs), a.x_scales + static_cast<size_t>(x_at.kc) * kTiles * 512,
-                      min(kTiles, a.k_tiles - x_at.kc * kTiles) * 512, bar);
-        }
-        if (i % kMatrices == kMatrices - 1) x_at.next(a, n_experts);
-        x_turn.next(n_stages);
-        ++x_from;
-      };
-      for (int i = 0; i < n; ++i) {
-        if (!waited && i == n_stages) {
-          asm volatile("griddepcontrol.wait;" ::: "memory");
-          waited = true;
-          while (x_from < i) issue_x(x_from);
-        }
-        if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
-        const int which = i % kMatrices;
-        if (lane == 0) {
-          const int id = MODE == kGemv ? 0 : ex->expert[at.slot];
-          const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
-          uint8_t* st = smem + turn.i * stage_bytes;
-          const uint32_t bar = smem_u32(&full[turn.i]);
-          const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
-          mbar_expect_tx(bar, kOffScales + sb + tokens * 1024 + (MODE == kGemv ? sb : tokens * token_lines(FMT)));
-          tma_load_2d(smem_u32(st), which == 0 ? &m0 : &m1, at.kc * (kUnitK / 2), id * a.rows + at.row * kRows, bar);
-          bulk_load(smem_u32(st + kOffScales),
-                    (which == 0 ? a.sc0 : a.sc1) + id * a.sc_stride +
-                        (static_cast<size_t>(at.row) * a.k_tiles + at.kc * kTiles) * 512,
-                    sb, bar);
-        }
-        __syncwarp();
-        if (which == kMatrices - 1) at.next(a, n_experts);
-        turn.next(n_stages);
-        issued = i + 1;
-        if (waited) issue_x(i);
+        at.next(a, n_experts);
       }
-      if (!waited) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        while (x_from < issued) issue_x(x_from);
+    }
+    // every issued stage's copies land before the CTA may exit
+    for (int i = max(0, issued - n_stages); i < issued; ++i)
+      for (int r = 0; r < a.wait_limit; ++r)
+        if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1))) break;
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ the tokens' parts
+    const bool leader = elect_one();
+    // they come from the launch before
+    if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!a.starve) {
+      Place<MODE> at(a, n_experts, u0);
+      Turn turn;
+      bool ok = true;
+      for (int left = n_mine; left > 0 && ok; --left) {
+        const unsigned tokens = MODE == kGemv ? 0u : ex->tokens[at.slot];
+        const int n_tok = MODE == kGemv ? a.M : __popc(tokens);
+        const uint8_t* src = nullptr;  // lane: the piece of a token of the unit
+        if (MODE != kGemv && lane < n_tok) {
+          const int token = nth_bit(tokens, lane);
+          src = a.x + (static_cast<size_t>(MODE == kDown ? ex->place[at.slot][token] : token) * a.k_units + at.kc) * piece_bytes(FMT);
+        }
+#pragma unroll
+        for (int which = 0; which < kMatrices; ++which) {
+          if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(smem) + turn.i * stage_bytes, bar = smem_u32(&full[turn.i]);
+          if constexpr (MODE == kGemv) {
+            if (leader) {
+              const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
+              mbar_expect_tx(bar, n_tok * 1024 + sb);
+              tma_load_2d(st + kOffX, &mx, at.kc * (kUnitK / 2), 0, bar);
+              bulk_load(st + off_xs, a.x + static_cast<size_t>(at.kc) * kTiles * 512, sb, bar);
+            }
+          } else {
+            if (leader) mbar_expect_tx(bar, n_tok * piece_bytes(FMT));
+            __syncwarp();
+            if (lane < n_tok) bulk_load(st + kOffX + lane * kSlot, src, piece_bytes(FMT), bar);
+          }
+          __syncwarp();
+          turn.next(n_stages);
+        }
+        at.next(a, n_experts);
       }
-      // every issued stage's copies land before the CTA may exit
-      for (int i = max(0, issued - n_stages); i < issued; ++i)
-        for (int r = 0; r < a.wait_limit; ++r)
-          if (mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1)) break;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -511,30 +529,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
         }
-        const uint64_t ad = codes_desc(st);
+        const uint64_t ad = codes_desc(st, 1024);
         for (int g = 0; g < tokens; g += MODE == kGemv ? kMaxTokens : 4) {
           // gemv: all tokens, their scales in tiles; else four, from their own lines
           const uint32_t sb = sa + 16 + 4 * g;
           const int m = MODE == kGemv ? tokens : min(4, tokens - g);
           const uint32_t idesc = idesc_for(FMT, (8 * m + 15) / 16 * 16);
-          const uint64_t bd = codes_desc(st + kOffX + g * 1024);
+          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, MODE == kGemv ? 1024 : kSlot);
           const uint32_t d = d0 + 8 * g + which * cols;
           if (leader) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
               copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
-                                                    : lines_desc(st + off_xs + g * token_lines(FMT) + j * kLines, token_lines(FMT)));
+                                                    : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
               if (j >= n_k) break;
-              // down: each half of 128 k has its own sums, and every unit its own
-              const uint32_t dj = MODE == kDown && j >= 2 ? d + cols : d;
-              const bool first = MODE == kDown ? (j & 1) == 0 : j == 0 && fresh;
+              const bool first = j == 0 && fresh;
               if constexpr (FMT == EXQ_FP4_E4M3) {
-                mma_scaled<FMT>(dj, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 4 * j, !first);
+                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 4 * j, !first);
               } else {  // two scales of the tile's four: byte 0 or 2 of each word
                 const uint32_t id = (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc;
-                mma_scaled<FMT>(dj, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * (j >> 1), !first);
+                mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa + 4 * (j >> 1), sb + 4 * (j >> 1), !first);
               }
             }
           }
@@ -545,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         turn.next(n_stages);
       }
       if (!ok) break;
-      fresh = MODE == kDown || left == 1 || at.ends(a, n_experts);
+      fresh = left == 1 || at.kc + 1 == a.k_units;  // the end of a tile, or (down) of an expert's share of it
       if (fresh) {
         if (leader) commit(smem_u32(&dfull[buf.i]));
         __syncwarp();
@@ -563,83 +579,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     Place<MODE> at(a, n_experts, u0);
-    Turn turn, buf;
-    bool begins = true;  // down: the next unit is the first of a tile
+    Turn buf;
+    bool begins = true;  // down: the next expert is the first of a tile
     for (int left = n_mine; left > 0; --left) {
-      const int slot = at.slot, row = at.row, kc = at.kc;
-      const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
-      const int n_tok = __popc(tokens);
+      const int slot = at.slot, row = at.row;
+      const bool segment_ends = left == 1 || at.kc + 1 == a.k_units;
       const bool tile_ends = left == 1 || at.ends(a, n_experts);
       at.next(a, n_experts);
+      if (!segment_ends) continue;
+      const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
+      const int n_tok = __popc(tokens);
+      float f = 0.f;  // down: lane's token's weight, times down's factor and h's
+      int place = 0;
+      if (MODE == kDown && lane < n_tok) {
+        place = ex->place[slot][nth_bit(tokens, lane)];
+        f = ex->weight[place] * (a.f0 ? __ldg(a.f0 + ex->expert[slot]) : 1.f);
+        if (FMT == EXQ_FP4_E4M3) f *= pow2(e4m3_shift(kHTop));
+      }
+      if (MODE == kDown && begins)
+        for (int t = 0; t < a.M; ++t) sums[t * kRows + r] = 0.f;
+      begins = tile_ends;
+      const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
+      tc_fence_after();
+      // (the largest h is known: parts made with it have come through the MMAs)
+      if (MODE == kDown && lane < n_tok) f *= pow2(h_exponent(__ldcg(a.h_most + place)));
       float v[kMaxTokens * kMatrices];  // the row's values: token by token; up: gate's, then up's
-      if constexpr (MODE == kDown) {
-        if (begins)
-          for (int t = 0; t < a.M; ++t) sums[t * kRows + r] = 0.f;
-        begins = tile_ends;
-        // h's factors of the two halves of k, beside the scales of their first tiles
-        float f[2] = {0.f, 0.f};
-        if (mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err) && lane < n_tok) {
-          const uint8_t* line = smem + turn.i * stage_bytes + off_xs + lane * token_lines(FMT);
-          const float w = ex->weight[ex->place[slot][nth_bit(tokens, lane)]] * (a.f0 ? __ldg(a.f0 + ex->expert[slot]) : 1.f);
-          f[0] = w * *reinterpret_cast<const float*>(line + 4);
-          f[1] = w * *reinterpret_cast<const float*>(line + kTiles / 2 * kLines + 4);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[turn.i]));
-        turn.next(n_stages);
-        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
-        tc_fence_after();
-        if (ok) {
-          const uint32_t d = tmem + lanes + buf.i * buffer_cols;
-          const bool both = a.K - kc * kUnitK > kUnitK / 2;
-          unsigned m = tokens;
-          for (int j = 0; j < n_tok; j += 2) {
-            float c[2][16];
-            tmem_ld16(d + 8 * j, c[0]);
-            if (both) tmem_ld16(d + cols + 8 * j, c[1]);
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              if (j + o >= n_tok) break;
-              float s = join_parts(c[0] + 8 * o) * __shfl_sync(0xffffffffu, f[0], j + o);
-              const float f1 = __shfl_sync(0xffffffffu, f[1], j + o);
-              if (both) s = fmaf(join_parts(c[1] + 8 * o), f1, s);
-              const int t = __ffs(static_cast<int>(m)) - 1;
-              m &= m - 1u;
-              sums[t * kRows + r] += s;
+      for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
+      if (ok) {
+        const uint32_t d = tmem + lanes + buf.i * buffer_cols;
+#pragma unroll
+        for (int w = 0; w < kMatrices; ++w)
+#pragma unroll
+          for (int j = 0; j < kMaxTokens; j += 2) {
+            if (j < n_tok) {
+              float c[16];
+              tmem_ld16(d + w * cols + 8 * j, c);
+              v[w * kMaxTokens + j] = join_parts(c);
+              v[w * kMaxTokens + j + 1] = join_parts(c + 8);
             }
           }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
+      buf.next(n_buffers);
+      if constexpr (MODE == kDown) {
+        // an expert's sums go to its own tokens only: a NaN of its weights reaches no other
+        unsigned m = tokens;
+#pragma unroll
+        for (int j = 0; j < kMaxTokens; ++j) {
+          if (j >= n_tok) break;
+          const float fj = __shfl_sync(0xffffffffu, f, j);
+          const int t = __ffs(static_cast<int>(m)) - 1;
+          m &= m - 1u;
+          sums[t * kRows + r] = fmaf(v[j], fj, sums[t * kRows + r]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
-        buf.next(n_buffers);
         if (!tile_ends) continue;
 #pragma unroll
         for (int t = 0; t < kMaxTokens; ++t) v[t] = t < a.M ? sums[t * kRows + r] : 0.f;
-      } else {
-        if (!tile_ends) continue;
-        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
-        if (ok) {
-          const uint32_t d = tmem + lanes + buf.i * buffer_cols;
-#pragma unroll
-          for (int w = 0; w < kMatrices; ++w)
-#pragma unroll
-            for (int j = 0; j < kMaxTokens; j += 2) {
-              if (j < n_tok) {
-                float c[16];
-                tmem_ld16(d + w * cols + 8 * j, c);
-                v[w * kMaxTokens + j] = join_parts(c);
-                v[w * kMaxTokens + j + 1] = join_parts(c + 8);
-              }
-            }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
-        buf.next(n_buffers);
       }
 
       // ---- the tile, or this CTA's part of it
@@ -693,65 +691,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id = ex->expert[slot];
         const float fx = FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f;  // of x's parts
         const float fg = (a.f0 ? __ldg(a.f0 + id) : 1.f) * fx, fu = (a.f1 ? __ldg(a.f1 + id) : 1.f) * fx;
+        unsigned m = tokens;
 #pragma unroll
         for (int j = 0; j < kMaxTokens; ++j) {
           if (j >= n_tok) break;
+          const int place = ex->place[slot][__ffs(static_cast<int>(m)) - 1];
+          m &= m - 1u;
           const float h = activate(v[j] * fg, a.act) * (v[kMaxTokens + j] * fu);
-          v[j] = in ? h : 0.f;
-          float m = fabsf(v[j]);
-          if (!isfinite(m)) m = 0.f;
-#pragma unroll
-          for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          if (lane == 0) ex->most[quarter][j] = m;
+          if (in) a.h[static_cast<size_t>(place) * a.rows + n_row] = h;
+          // magnitudes order as their bits do
+          const unsigned most = __reduce_max_sync(0xffffffffu, in && isfinite(h) ? __float_as_uint(fabsf(h)) : 0u);
+          if (lane == 0) atomicMax(a.h_most + place, most);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        unsigned left_tokens = tokens;
-#pragma unroll
-        for (int j = 0; j < kMaxTokens; ++j) {
-          if (j >= n_tok) break;
-          const int token = __ffs(static_cast<int>(left_tokens)) - 1;
-          left_tokens &= left_tokens - 1u;
-          const float most = fmaxf(fmaxf(ex->most[0][j], ex->most[1][j]), fmaxf(ex->most[2][j], ex->most[3][j]));
-          const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 126);  // tile's largest: 2^e ..
-          const float h = v[j] * pow2(-e);
-          // the block's scale: 16 or 32 rows, a lane each
-          float m = fabsf(h);
-          bool bad = !isfinite(h);
-#pragma unroll
-          for (int d = 1; d < fp4_block(FMT); d <<= 1) {
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), d) != 0;
-          }
-          const int pe = bad ? 0 : part_exponent<FMT>(m, kHTop);
-          const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(pe, kHTop);
-          float q = bad ? 0.f : h * pow2(-pe);
-          const size_t pair = ex->place[slot][token];
-#pragma unroll
-          for (int p = 0; p < kParts; ++p) {
-            uint32_t code;
-            float val;
-            e2m1_nearest(q, code, val);
-            q = (q - val) * 8.f;
-            uint32_t word = code << (4 * (lane & 7));
-            word |= __shfl_xor_sync(0xffffffffu, word, 1);
-            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            word |= __shfl_xor_sync(0xffffffffu, word, 4);
-            if ((lane & 7) == 0 && in)
-              *reinterpret_cast<uint32_t*>(a.h_codes + (pair * kParts + p) * (a.rows / 2) + n_row / 2) = word;
-          }
-          // the scale lines: 8 of each tile, their first word the four blocks' bytes; beside the first tile's h's factor
-          uint8_t* lines = a.h_scales + (pair * a.h_units + (row >> 1)) * token_lines(FMT) + (row & 1) * (kTiles / 2) * kLines;
-          if constexpr (FMT == EXQ_FP4_E4M3) {
-            // a tile is 64 rows, a warp has 2 of its 4 blocks: a half word
-            const uint32_t b0 = __shfl_sync(0xffffffffu, byte, 0), b1 = __shfl_sync(0xffffffffu, byte, 16);
-            if (lane < 8)
-              *reinterpret_cast<uint16_t*>(lines + (quarter >> 1) * kLines + lane * 16 + (quarter & 1) * 2) = static_cast<uint16_t>(b0 | (b1 << 8));
-          } else if (lane < 8) {
-            lines[lane * 16 + quarter] = static_cast<uint8_t>(byte);
-          }
-          if (r == 0) *reinterpret_cast<float*>(lines + 4) = pow2(e) * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kHTop)) : 1.f);
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // `most` is free again
       } else if (!*abort_flag && in) {
         const float f = MODE == kGemv ? a.factor * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f) : 1.f;
 #pragma unroll

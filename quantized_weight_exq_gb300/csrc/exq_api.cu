@@ -473,7 +473,7 @@ extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix
   if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
   const size_t need = fp4_gemm_workspace_bytes(*a, *w, sms);
   if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return EXQ_ERR_INVALID_ARG;
-  return launch_fp4_gemm(*a, *w, y, workspace, ws_bytes, sms, current_device(), static_cast<cudaStream_t>(stream));
+  return launch_fp4_gemm(*a, *w, y, workspace, sms, current_device(), static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M) {

@@ -1,8 +1,9 @@
-// Products of a few fp16 rows with matrices of the microscaled 4-bit format on
-// the block-scaled tcgen05 tensor cores: the decode product (one matrix) and
-// the two products of an expert layer.
+// Products of a few rows with matrices of the microscaled 4-bit format on the
+// block-scaled tcgen05 tensor cores: the decode product (one matrix) and the
+// two products of an expert layer, of up to 16 fp16 rows, and the product of
+// two 4-bit matrices where there are few tiles of it.
 //
-//   out[t][n] = sum_k x[t][k] w[n][k],   t < 16
+//   out[t][n] = sum_k x[t][k] w[n][k]
 //
 // Every code is read once, so the floor is the codes' and scales' bytes. At
 // 6.8 TB/s an SM gets 47 codes a clock: turning them into fp16 in registers
@@ -31,7 +32,7 @@
 //              behind the weights' copies theirs cost 250 ns a unit).
 //   warp 1     copies scales to tensor memory and issues the MMAs (M = 128
 //              rows of the matrix, N = 8 columns a token, K = 64).
-//   warps 2-5  drain the sums: a lane is a row.
+//   warps 2-5  drain the sums: a lane is a row of the matrix.
 //
 // A tile whose units lie in several CTAs goes through the workspace: each
 // writes its part, the last to arrive (a counter) adds them in CTA order, so
@@ -45,13 +46,14 @@ namespace fp4s {
 
 static __device__ unsigned g_stream_err;
 
-enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
+enum Mode { kGemv = 0, kUp = 1, kDown = 2, kFew = 3 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
 constexpr int kThreads = 7 * 32;
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
+constexpr int kFewRows = 128;        // rows of a 4-bit x in a tile
 constexpr int kMaxPairs = 256;       // tokens x experts of each
 constexpr int kMaxExperts = 512;
 constexpr int kMaxStages = 10;
@@ -94,8 +96,8 @@ struct Args {
   const uint8_t* sc0;      // scale tiles of the matrix, or of expert 0's gate or down
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
-  const uint8_t* x;        // gemv: scale tiles of the parts; else pieces [token or pair, unit]
-  uint16_t* y;             // gemv [M, rows], down [M, rows]
+  const uint8_t* x;        // gemv, few: scale tiles (of the parts, of x); else pieces [token or pair, unit]
+  uint16_t* y;             // [M, rows] (not up)
   float* h;                // up: [pairs, rows]
   unsigned* h_most;        // [pairs]: bits of the largest finite magnitude of h
   const float *f0, *f1;    // experts' factors of gate and up, or of down, or NULL
@@ -111,7 +113,9 @@ struct Args {
 };
 
 // floats of one CTA's part of a tile: a value for each row, token (and matrix)
-__host__ __device__ constexpr int part_floats(int mode) { return kRows * kMaxTokens * (mode == kUp ? 2 : 1); }
+__host__ __device__ constexpr int part_floats(int mode) {
+  return kRows * (mode == kFew ? kFewRows : kMaxTokens * (mode == kUp ? 2 : 1));
+}
 
 // The experts of a call, the same in every CTA: those that some token chose,
 // ascending, with the tokens of each and the place of (expert, token) in ids.
@@ -284,13 +288,14 @@ __device__ __forceinline__ int nth_bit(unsigned m, int j) {
 
 // ---------------------------------------------------------------- units
 
-// How many units a call has, and a tile of it.
-template <int MODE>
-__device__ __forceinline__ long long units_of(const Args& a, int experts) {
-  return static_cast<long long>(a.row_tiles) * a.k_units * (MODE == kGemv ? 1 : experts);
+// How many units a call has. `slots`: the experts, or (few) the tiles of x's
+// rows, or one.
+__device__ __forceinline__ long long units_of(const Args& a, int slots) {
+  return static_cast<long long>(a.row_tiles) * a.k_units * slots;
 }
 
-// A unit's place: its expert (the index in Experts), tile of rows and k. The
+// A unit's place: its expert (the index in Experts) or tile of x's rows, its
+// tile of the matrix's rows, and k. The
 // division is made once a CTA; from unit to unit the place counts up.
 template <int MODE>
 struct Place {
@@ -304,7 +309,7 @@ struct Place {
     if constexpr (MODE == kUp) {
       slot = static_cast<int>(q / a.row_tiles);
       row = static_cast<int>(q) - slot * a.row_tiles;
-    } else if constexpr (MODE == kDown) {
+    } else if constexpr (MODE == kDown || MODE == kFew) {
       row = static_cast<int>(q / experts);
       slot = static_cast<int>(q) - row * experts;
     }
@@ -318,7 +323,7 @@ struct Place {
   __device__ __forceinline__ void next(const Args& a, int experts) {
     if (++kc < a.k_units) return;
     kc = 0;
-    if constexpr (MODE == kDown) {
+    if constexpr (MODE == kDown || MODE == kFew) {
       if (++slot < experts) return;
       slot = 0;
       ++row;
@@ -347,6 +352,26 @@ struct Turn {
     }
   }
 };
+
+// v[j] += part j (of n) of CTAs b0 .. b1, in their order; four CTAs' loads are in flight at a time
+template <typename PartOf>
+__device__ __forceinline__ void add_parts(float (&v)[16], int n, int b0, int b1, PartOf part_of) {
+  for (int b = b0; b <= b1; b += 4) {
+    float t[4][16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* p = part_of(min(b + i, b1));
+#pragma unroll
+      for (int j = 0; j < 16; ++j) t[i][j] = j < n ? __ldcg(p + j * kRows) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i <= b1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += t[i][j];
+      }
+  }
+}
 
 template <int FMT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -387,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   if constexpr (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n_experts = 0, most_tokens = a.M;
-  if constexpr (MODE != kGemv) {
+  int n_experts = MODE == kFew ? (a.M + kFewRows - 1) / kFewRows : 1, most_tokens = a.M;
+  if constexpr (MODE == kUp || MODE == kDown) {
     find_experts(a, ex, used, MODE == kUp && blockIdx.x == 0);
     n_experts = ex->n;
     most_tokens = ex->most_tokens;
   }
-  const long long n_units = units_of<MODE>(a, n_experts);
+  const long long n_units = units_of(a, n_experts);
   if constexpr (MODE == kDown) {
     if (n_units == 0) {  // no token has an expert
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -409,10 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_mine = static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0);
 
   // the ring and the buffers of sums go by the most tokens that a matrix of the call has
-  const int off_xs = kOffX + 1024 * most_tokens;                        // gemv: the parts' scale tiles
-  const int stage_bytes = MODE == kGemv ? off_xs + 2048 : kOffX + kSlot * ((most_tokens + 3) / 4 * 4);
+  constexpr bool kTileScales = MODE == kGemv || MODE == kFew;           // x's scales come as tiles
+  const int x_rows = MODE == kFew ? min(kFewRows, (a.M + 7) / 8 * 8) : 8 * most_tokens;
+  const int off_xs = kOffX + 128 * x_rows;                              // where
+  const int stage_bytes = kTileScales ? off_xs + 2048 : kOffX + kSlot * ((most_tokens + 3) / 4 * 4);
   const int n_stages = min(kMaxStages, kRing / stage_bytes);
-  const int cols = (8 * most_tokens + 15) / 16 * 16;                    // of one sum
+  const int cols = (x_rows + 15) / 16 * 16;                             // of one sum
   const int buffer_cols = cols * kMatrices;
   const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
 
@@ -425,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const unsigned everyone = (1u << a.M) - 1u;
+  const unsigned everyone = MODE == kGemv ? (1u << a.M) - 1u : 0u;
 
   if (warp == 0) {
     // ------------------------------------------------------------ codes and scales of the matrix
@@ -436,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn turn;
       bool ok = true;
       for (int left = n_mine; left > 0 && ok; --left) {
-        const int id = MODE == kGemv ? 0 : ex->expert[at.slot];
+        const int id = kTileScales ? 0 : ex->expert[at.slot];
         const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
         const size_t off = id * a.sc_stride + (static_cast<size_t>(at.row) * a.k_tiles + at.kc * kTiles) * 512;
 #pragma unroll
@@ -466,16 +493,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ the tokens' parts
     const bool leader = elect_one();
     // they come from the launch before
-    if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (MODE == kGemv || MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!a.starve) {
       Place<MODE> at(a, n_experts, u0);
       Turn turn;
       bool ok = true;
       for (int left = n_mine; left > 0 && ok; --left) {
-        const unsigned tokens = MODE == kGemv ? 0u : ex->tokens[at.slot];
-        const int n_tok = MODE == kGemv ? a.M : __popc(tokens);
+        const unsigned tokens = kTileScales ? 0u : ex->tokens[at.slot];
+        const int n_tok = __popc(tokens);
         const uint8_t* src = nullptr;  // lane: the piece of a token of the unit
-        if (MODE != kGemv && lane < n_tok) {
+        if (lane < n_tok) {
           const int token = nth_bit(tokens, lane);
           src = a.x + (static_cast<size_t>(MODE == kDown ? ex->place[at.slot][token] : token) * a.k_units + at.kc) * piece_bytes(FMT);
         }
@@ -486,12 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t st = smem_u32(smem) + turn.i * stage_bytes, bar = smem_u32(&full[turn.i]);
-          if constexpr (MODE == kGemv) {
+          if constexpr (kTileScales) {
             if (leader) {
               const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
-              mbar_expect_tx(bar, n_tok * 1024 + sb);
-              tma_load_2d(st + kOffX, &mx, at.kc * (kUnitK / 2), 0, bar);
-              bulk_load(st + off_xs, a.x + static_cast<size_t>(at.kc) * kTiles * 512, sb, bar);
+              mbar_expect_tx(bar, x_rows * 128 + sb);
+              tma_load_2d(st + kOffX, &mx, at.kc * (kUnitK / 2), MODE == kFew ? at.slot * kFewRows : 0, bar);
+              bulk_load(st + off_xs, a.x + (static_cast<size_t>(at.slot) * a.k_tiles + at.kc * kTiles) * 512, sb, bar);
             }
           } else {
             if (leader) mbar_expect_tx(bar, n_tok * piece_bytes(FMT));
@@ -513,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint32_t sa = tmem + kTmemScales;
     for (int left = n_mine; left > 0 && ok; --left) {
-      const int tokens = MODE == kGemv ? a.M : __popc(ex->tokens[at.slot]);
+      const int tokens = kTileScales ? 1 : __popc(ex->tokens[at.slot]);  // (all of x at once)
       const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
       const uint32_t d0 = tmem + buf.i * buffer_cols;
       if (fresh && !mbar_wait_warp(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
@@ -530,17 +557,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
         }
         const uint64_t ad = codes_desc(st, 1024);
-        for (int g = 0; g < tokens; g += MODE == kGemv ? kMaxTokens : 4) {
-          // gemv: all tokens, their scales in tiles; else four, from their own lines
+        for (int g = 0; g < tokens; g += 4) {
+          // all of x, its scales in tiles; or four tokens, from their own lines
           const uint32_t sb = sa + 16 + 4 * g;
-          const int m = MODE == kGemv ? tokens : min(4, tokens - g);
-          const uint32_t idesc = idesc_for(FMT, (8 * m + 15) / 16 * 16);
-          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, MODE == kGemv ? 1024 : kSlot);
+          const uint32_t idesc = idesc_for(FMT, kTileScales ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
+          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, kTileScales ? 1024 : kSlot);
           const uint32_t d = d0 + 8 * g + which * cols;
           if (leader) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
-              copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
+              copy_scales(sb + 4 * j, kTileScales ? lines_desc(st + off_xs + j * 512, kLines)
                                                     : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
@@ -587,6 +613,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool tile_ends = left == 1 || at.ends(a, n_experts);
       at.next(a, n_experts);
       if (!segment_ends) continue;
+      const int n_row = row * kRows + r;
+      const bool in = n_row < a.rows;
+      // whose units the tile is made of
+      const int tile = MODE == kUp ? slot * a.row_tiles + row : MODE == kFew ? row * n_experts + slot : row;
+      const int tile_units = a.k_units * (MODE == kDown ? n_experts : 1);
+      const long long first = static_cast<long long>(tile) * tile_units;
+      const int b0 = owner(first, n_units, ctas), b1 = owner(first + tile_units - 1, n_units, ctas);
+      auto part_of = [&](int b) {  // a CTA's tile that began before it is its part 0
+        return a.part + (static_cast<size_t>(b) * 2 + (first < b * n_units / ctas ? 0 : 1)) * part_floats(MODE) + r;
+      };
+      // after this CTA's part is written: whether all are
+      auto last_of_tile = [&]() {
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 64) {
+          int is_last = 0;
+          if (!*abort_flag) {
+            const unsigned before = atomicAdd(a.counters + tile, 1u);
+            is_last = before == static_cast<unsigned>(b1 - b0);
+            if (is_last) a.counters[tile] = 0u;
+          }
+          __threadfence();
+          *last = is_last;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        return *last != 0;
+      };
+      if constexpr (MODE == kFew) {
+        const int m0 = slot * kFewRows, n_rows = min(kFewRows, a.M - m0);
+        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
+        tc_fence_after();
+        auto store = [&](int c, const float (&v)[16]) {
+          if (!in || *abort_flag) return;
+          uint16_t* dst = a.y + static_cast<size_t>(m0 + c) * a.rows + n_row;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < n_rows) dst[static_cast<size_t>(j) * a.rows] = __half_as_ushort(__float2half_rn(v[j] * a.factor));
+        };
+        float v[16];
+        for (int c = 0; c < n_rows; c += 16) {
+          if (!ok) break;
+          tmem_ld16(tmem + lanes + buf.i * buffer_cols + c, v);
+          if (b0 == b1) {
+            store(c, v);
+          } else {
+            float* p = part_of(blockIdx.x) + c * kRows;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < n_rows) __stcg(p + j * kRows, v[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
+        buf.next(n_buffers);
+        if (b0 != b1 && last_of_tile()) {
+          for (int c = 0; c < n_rows; c += 16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+            add_parts(v, n_rows - c, b0, b1, [&](int b) { return part_of(b) + c * kRows; });
+            store(c, v);
+          }
+        }
+        continue;
+      }
       const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
       const int n_tok = __popc(tokens);
       float f = 0.f;  // down: lane's token's weight, times down's factor and h's
@@ -603,9 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // (the largest h is known: parts made with it have come through the MMAs)
       if (MODE == kDown && lane < n_tok) f *= pow2(h_exponent(__ldcg(a.h_most + place)));
-      float v[kMaxTokens * kMatrices];  // the row's values: token by token; up: gate's, then up's
+      float v[kMatrices][kMaxTokens];  // the row's values: token by token; up: gate's and up's
 #pragma unroll
-      for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
+      for (int w = 0; w < kMatrices; ++w)
+#pragma unroll
+        for (int j = 0; j < kMaxTokens; ++j) v[w][j] = 0.f;
       if (ok) {
         const uint32_t d = tmem + lanes + buf.i * buffer_cols;
 #pragma unroll
@@ -615,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < n_tok) {
               float c[16];
               tmem_ld16(d + w * cols + 8 * j, c);
-              v[w * kMaxTokens + j] = join_parts(c);
-              v[w * kMaxTokens + j + 1] = join_parts(c + 8);
+              v[w][j] = join_parts(c);
+              v[w][j + 1] = join_parts(c + 8);
             }
           }
       }
@@ -633,60 +726,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float fj = __shfl_sync(0xffffffffu, f, j);
           const int t = __ffs(static_cast<int>(m)) - 1;
           m &= m - 1u;
-          sums[t * kRows + r] = fmaf(v[j], fj, sums[t * kRows + r]);
+          sums[t * kRows + r] = fmaf(v[0][j], fj, sums[t * kRows + r]);
         }
         if (!tile_ends) continue;
 #pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t) v[t] = t < a.M ? sums[t * kRows + r] : 0.f;
+        for (int t = 0; t < kMaxTokens; ++t) v[0][t] = t < a.M ? sums[t * kRows + r] : 0.f;
       }
 
       // ---- the tile, or this CTA's part of it
       const int n_val = MODE == kDown ? a.M : n_tok;
-      const int tile = MODE == kUp ? slot * a.row_tiles + row : row;
-      const int tile_units = a.k_units * (MODE == kDown ? n_experts : 1);
-      const long long first = static_cast<long long>(tile) * tile_units, end = first + tile_units;
-      const int b0 = owner(first, n_units, ctas), b1 = owner(end - 1, n_units, ctas);
-      bool mine = true;  // this CTA writes the result
       if (b0 != b1) {
-        auto part_of = [&](int b) {  // a CTA's tile that began before it is its part 0
-          return a.part + (static_cast<size_t>(b) * 2 + (first < b * n_units / ctas ? 0 : 1)) * part_floats(MODE) + r;
-        };
         float* p = part_of(blockIdx.x);
 #pragma unroll
         for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
           for (int j = 0; j < kMaxTokens; ++j)
-            if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w * kMaxTokens + j]);
-        __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (threadIdx.x == 64) {
-          int is_last = 0;
-          if (!*abort_flag) {
-            const unsigned before = atomicAdd(a.counters + tile, 1u);
-            is_last = before == static_cast<unsigned>(b1 - b0);
-            if (is_last) a.counters[tile] = 0u;
-          }
-          __threadfence();
-          *last = is_last;
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        mine = *last != 0;
-        if (mine) {
+            if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w][j]);
+        if (!last_of_tile()) continue;
 #pragma unroll
-          for (int j = 0; j < kMaxTokens * kMatrices; ++j) v[j] = 0.f;
-          for (int b = b0; b <= b1; ++b) {
-            const float* o = part_of(b);
+        for (int w = 0; w < kMatrices; ++w) {
 #pragma unroll
-            for (int w = 0; w < kMatrices; ++w)
-#pragma unroll
-              for (int j = 0; j < kMaxTokens; ++j)
-                if (j < n_val) v[w * kMaxTokens + j] += __ldcg(o + (w * kMaxTokens + j) * kRows);
-          }
+          for (int j = 0; j < kMaxTokens; ++j) v[w][j] = 0.f;
+          add_parts(v[w], n_val, b0, b1, [&](int b) { return part_of(b) + w * kMaxTokens * kRows; });
         }
       }
-      if (!mine) continue;
-      const int n_row = row * kRows + r;
-      const bool in = n_row < a.rows;
       if constexpr (MODE == kUp) {
         const int id = ex->expert[slot];
         const float fx = FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f;  // of x's parts
@@ -697,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= n_tok) break;
           const int place = ex->place[slot][__ffs(static_cast<int>(m)) - 1];
           m &= m - 1u;
-          const float h = activate(v[j] * fg, a.act) * (v[kMaxTokens + j] * fu);
+          const float h = activate(v[0][j] * fg, a.act) * (v[kMatrices - 1][j] * fu);
           if (in) a.h[static_cast<size_t>(place) * a.rows + n_row] = h;
           // magnitudes order as their bits do
           const unsigned most = __reduce_max_sync(0xffffffffu, in && isfinite(h) ? __float_as_uint(fabsf(h)) : 0u);
@@ -707,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = MODE == kGemv ? a.factor * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f) : 1.f;
 #pragma unroll
         for (int t = 0; t < kMaxTokens; ++t)
-          if (t < a.M) a.y[static_cast<size_t>(t) * a.rows + n_row] = __half_as_ushort(__float2half_rn(v[t] * f));
+          if (t < a.M) a.y[static_cast<size_t>(t) * a.rows + n_row] = __half_as_ushort(__float2half_rn(v[0][t] * f));
       }
     }
   }

@@ -732,7 +732,7 @@ def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
 
 FP4_COUNTER_BYTES = 128 << 10  # EXQ_FP4_COUNTER_BYTES
 
-_fp4_ws = {}  # (device index, stream handle) -> workspace of exq_fp4_gemv and exq_moe, its counters zero between calls
+_fp4_ws = {}  # (device index, stream handle) -> workspace of exq_fp4_gemm, exq_fp4_gemv and exq_moe, its counters zero between calls
 
 
 def _fp4_workspace(need: int, dev: int, stream, handle: int, where: str):
@@ -854,7 +854,7 @@ def _space(workspace, where: str):
 
 
 def exq_fp4_gemm(a: Fp4Matrix, w: Fp4Matrix, out=None, workspace=None, stream=None):
-    """a . w^T as fp16 [a.rows, w.rows], both in the 4-bit format."""
+    """a . w^T as fp16 [a.rows, w.rows], both in the 4-bit format. The workspace is as exq_fp4_gemv's; large products need none."""
     import torch
     where = "exq_fp4_gemm"
     dev = a.device
@@ -864,12 +864,13 @@ def exq_fp4_gemm(a: Fp4Matrix, w: Fp4Matrix, out=None, workspace=None, stream=No
     _fp16_rows(out, where)
     if out.shape != (a.rows, w.rows):
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    handle = _stream_ptr(stream, dev)
     if workspace is None:
         need = exq_fp4_gemm_workspace_size(a, w)
         if need:
-            workspace = _empty(need, torch.uint8, a.codes.device, stream)
+            workspace = _fp4_workspace(need, dev, stream, handle, where)
     ws, n = _space(workspace, where)
-    _check(_lib.exq_fp4_gemm(a._ref, w._ref, out.data_ptr(), ws, n, _stream_ptr(stream, dev)), where)
+    _check(_lib.exq_fp4_gemm(a._ref, w._ref, out.data_ptr(), ws, n, handle), where)
     return out
 
 

@@ -130,7 +130,9 @@ def _check_product(y, a, w, extra_roundings):
 
 
 GEMM_SHAPES = [(1, 8, 32), (1, 128, 64), (5, 8, 96), (128, 256, 256), (129, 264, 288), (300, 1000, 2080), (64, 512, 4096), (17, 1032, 160),
-               (513, 136, 1056), (256, 384, 64), (2, 2048, 5152), (390, 520, 512)]
+               (513, 136, 1056), (256, 384, 64), (2, 2048, 5152), (390, 520, 512), (128, 8, 8224), (1000, 24, 288),
+               # tiles of 256 x 256: fewer than the SM pairs and more, the last ones ragged
+               (2000, 2056, 96), (1030, 4104, 544), (300, 9000, 64), (2300, 2312, 352), (257, 20000, 32), (6000, 1288, 1312)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -266,7 +268,7 @@ def test_graph_and_other_stream(env, fmt):
     q = exq.exq_fp4_quantize(x, fmt)
     y1, y2, back = (torch.empty(s, dtype=torch.float16, device="cuda") for s in ((M, N), (M, N), (M, K)))
     ws1 = torch.zeros(exq.exq_fp4_gemv_workspace_size(w, M), dtype=torch.uint8, device="cuda")
-    ws2 = torch.empty(max(exq.exq_fp4_gemm_workspace_size(q, w), 16), dtype=torch.uint8, device="cuda")
+    ws2 = torch.zeros(max(exq.exq_fp4_gemm_workspace_size(q, w), 16), dtype=torch.uint8, device="cuda")
 
     def step():
         exq.exq_fp4_quantize(x, fmt, out=q)

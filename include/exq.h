@@ -688,29 +688,20 @@ exq_status exq_fp4_quantize(const uint16_t* x, const exq_fp4_matrix* out, void* 
  * fp16_RNE(fp32_RNE(value)); the same rules. */
 exq_status exq_fp4_dequantize(const exq_fp4_matrix* m, uint16_t* out, void* stream);
 
-/* The workspaces of exq_fp4_gemm, exq_fp4_gemv and exq_moe start with counters:
- * ZERO-FILL this many bytes before the first use. Every call that completes
- * leaves them zero, so that one workspace serves any sequence of calls of all
- * three on one stream; one that ended in EXQ_ERR_TIMEOUT may not: zero-fill
- * them again. */
-#define EXQ_FP4_COUNTER_BYTES ((size_t)128 << 10)
-
-/* Bytes of device workspace exq_fp4_gemm needs on the current device: where
- * there are few tiles of the product, counters and fp32 parts of it; else 0. */
-size_t exq_fp4_gemm_workspace_size(const exq_fp4_matrix* a, const exq_fp4_matrix* w);
-
 /* exq_fp4_gemm -- device, asynchronous: y fp16 [a.rows, w.rows],
  *   y[m][n] = fp16_RNE(a.factor * w.factor * sum_k a[m][k] w[n][k]),
  * on the block-scaled tcgen05 tensor cores, sums in fp32. a and w have one
- * format and one K; any a.rows (0 launches nothing), w.rows % 8 == 0.
- *   workspace  at least exq_fp4_gemm_workspace_size() bytes, 256-byte aligned
- *              (NULL when that is 0), as above. Calls that may overlap on the
- *              GPU need separate workspaces.
- * A row of a (w) with a NaN scale has a NaN row (column) of y, no other.
- * Deterministic: the same inputs give the same bits on the same device.
- * EXQ_ERR_INVALID_ARG for bad pointers, sizes, formats or a short workspace. */
-exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* workspace,
-                        size_t ws_bytes, void* stream);
+ * format and one K; any a.rows (0 launches nothing), w.rows % 8 == 0. It needs
+ * no workspace. A row of a (w) with a NaN scale has a NaN row (column) of y,
+ * no other. Deterministic: the same inputs give the same bits.
+ * EXQ_ERR_INVALID_ARG for bad pointers, sizes or formats. */
+exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* stream);
+
+/* The workspaces of exq_fp4_gemv and exq_moe start with counters: ZERO-FILL
+ * this many bytes before the first use. Every call that completes leaves them
+ * zero, so that one workspace serves any sequence of calls of either on one
+ * stream; one that ended in EXQ_ERR_TIMEOUT may not: zero-fill them again. */
+#define EXQ_FP4_COUNTER_BYTES ((size_t)128 << 10)
 
 /* Bytes of device workspace exq_fp4_gemv needs on the current device; 0 for an
  * invalid matrix or M outside 1..16. */

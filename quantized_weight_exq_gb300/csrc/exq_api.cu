@@ -458,22 +458,13 @@ extern "C" exq_status exq_fp4_dequantize(const exq_fp4_matrix* m, uint16_t* out,
   return launch_fp4_dequantize(*m, out, current_sms(), static_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t exq_fp4_gemm_workspace_size(const exq_fp4_matrix* a, const exq_fp4_matrix* w) {
-  const int sms = current_sms();
-  if (check_fp4_product(a, w) != EXQ_OK || a->rows == 0 || sms <= 0) return 0;
-  return fp4_gemm_workspace_bytes(*a, *w, sms);
-}
-
-extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* workspace,
-                                   size_t ws_bytes, void* stream) {
+extern "C" exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16_t* y, void* stream) {
   const exq_status st = check_fp4_product(a, w);
   if (st != EXQ_OK || a->rows == 0) return st;
   if (!y || !aligned16(y)) return EXQ_ERR_INVALID_ARG;
   const int sms = current_sms();
   if (sms <= 0 || current_cc() < 100) return EXQ_ERR_CUDA;
-  const size_t need = fp4_gemm_workspace_bytes(*a, *w, sms);
-  if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return EXQ_ERR_INVALID_ARG;
-  return launch_fp4_gemm(*a, *w, y, workspace, sms, current_device(), static_cast<cudaStream_t>(stream));
+  return launch_fp4_gemm(*a, *w, y, sms, current_device(), static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M) {

@@ -1,5 +1,5 @@
 // Product of two matrices of the microscaled 4-bit format on the block-scaled
-// tcgen05 tensor cores, for sizes that fill the GPU with tiles:
+// tcgen05 tensor cores:
 //   y[m][n] = fp16(f sum_k a[m][k] w[n][k]),   f = a.factor * w.factor.
 //
 // A pair of CTAs (a cluster of two, cta_group::2) computes 256 x 256 of y, 256
@@ -22,6 +22,10 @@
 //               one set of sums only: the warps take theirs as packed fp16 into
 //               registers at once, let the next tile's MMAs begin, and store
 //               while those run.
+//
+// Up to 128 rows of a change places with w: its rows are the MMA's 256, a's its
+// N (32 .. 128 columns). The product is then bound by the codes of w; a stage
+// is at most 28 KB and its MMAs short, so that more of them are on their way.
 #include <algorithm>
 #include <cstring>
 
@@ -34,36 +38,52 @@ __device__ unsigned g_fp4_gemm_err;
 
 constexpr int kTile = 256;   // rows and columns of a pair's tile
 constexpr int BK = 256;      // k of a stage: four MMAs
-constexpr int kStages = 5;
 constexpr int kThreads = 14 * 32;
 
-constexpr int kCodes = 128 * BK / 2;  // of one operand in a CTA
+constexpr int kCodes = 128 * BK / 2;  // of 128 rows
 constexpr int kScaleTiles = 2048;     // the scale tiles of 128 rows x 256 k: 4 (E4M3) or 2 (E8M0)
-constexpr int kOffB = kCodes;
-constexpr int kOffSA = 2 * kCodes;
-constexpr int kOffSB = kOffSA + kScaleTiles;
-constexpr int kStageBytes = kOffSB + 2 * kScaleTiles;
-static_assert(kStageBytes % 1024 == 0, "stage alignment");
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024;
+constexpr int kRing = 5 * (2 * kCodes + 3 * kScaleTiles);
+constexpr int kSmemBytes = kRing + 1024 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
-// tensor memory: 256 columns of sums, then the scales of each stage (a: 4
-// columns a tile, b: 8): with two places for five stages the way from one
-// stage's MMAs over the warps that write scales to another's took 1 us
-constexpr uint32_t kTmemScales = 256;
-constexpr uint32_t kScaleCols = 48;
+// Tensor memory: the sums, then the scales of each stage (the MMA's A: 4 columns
+// a tile, B: 8, or 4 for up to 128 rows). With two places for five stages the
+// way from one stage's MMAs over the warps that write scales to another's
+// took 1 us.
 constexpr uint32_t kTmemCols = 512;
-static_assert(kTmemScales + kStages * kScaleCols <= kTmemCols, "tensor memory budget");
+// SWAP: a's rows are the MMA's N
+__host__ __device__ constexpr uint32_t scales_at(bool swap) { return swap ? 128 : 256; }
+__host__ __device__ constexpr uint32_t scale_cols(bool swap) { return swap ? 32 : 48; }
+__host__ __device__ constexpr int most_stages(bool swap) { return swap ? 10 : 5; }
+constexpr int kMaxStages = most_stages(true);
+static_assert(scales_at(false) + most_stages(false) * scale_cols(false) <= kTmemCols, "tensor memory budget");
+static_assert(scales_at(true) + most_stages(true) * scale_cols(true) <= kTmemCols, "tensor memory budget");
+
+// One stage of a CTA: 128 rows of A, its half of B's rows, A's scale tiles, all of B's.
+struct Stage {
+  int b_rows, bytes, n;
+  __host__ __device__ constexpr int off_sa() const { return kCodes + b_rows * (BK / 2); }
+  __host__ __device__ constexpr int off_sb() const { return off_sa() + kScaleTiles; }
+};
+__host__ __device__ constexpr Stage stage_of(bool swap, int n_columns) {
+  Stage s{};
+  s.b_rows = n_columns / 2;
+  s.bytes = s.off_sb() + (swap ? 1 : 2) * kScaleTiles;
+  s.n = kRing / s.bytes < most_stages(swap) ? kRing / s.bytes : most_stages(swap);
+  return s;
+}
+static_assert(stage_of(false, 256).n == 5 && stage_of(false, 256).bytes % 1024 == 0 && stage_of(true, 32).bytes % 1024 == 0, "stages");
 
 struct Args {
-  const uint8_t *sa, *sb;
+  const uint8_t *sa, *sb;  // scale tiles of the MMA's A and B
   uint16_t* y;
   float factor;
-  int M, N, K;
-  int a_tiles, b_tiles;  // tiles of 128 rows
-  int k_tiles;           // scale tiles along K
+  int A, B, K;             // rows of both
+  int a_tiles, b_tiles;    // tiles of 128 rows
+  int k_tiles;             // scale tiles along K
   int k_units;
-  int m_pairs, n_tiles;  // tiles of 256 along M, and in all
+  int a_pairs, n_tiles;    // tiles of 256 rows of A, and of the product in all
+  int n_columns;           // of a tile: 256, or (SWAP) all of B, rounded up to 32
   int wait_limit, starve;
 };
 
@@ -73,9 +93,9 @@ __device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {
          (1ull << 46) | (2ull << 61);
 }
 
-// instruction descriptor of the block-scaled kinds: e2m1 operands, K-major, 256 x 256
-__host__ __device__ constexpr uint32_t idesc_of(int fmt) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTile >> 3) << 17) | ((fmt == EXQ_FP4_E8M0 ? 1u : 0u) << 23) |
+// instruction descriptor of the block-scaled kinds: e2m1 operands, K-major, 256 x n
+__host__ __device__ constexpr uint32_t idesc_of(int fmt, int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((fmt == EXQ_FP4_E8M0 ? 1u : 0u) << 23) |
          (static_cast<uint32_t>(kTile >> 4) << 24);
 }
 
@@ -130,6 +150,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // four scale tiles (16 bytes of each for the lane) to 16 columns of this warp's lanes
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&t)[4]) {
   asm volatile(
@@ -147,35 +176,37 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 struct Turn {  // counts stages, and the parity of their barriers
   int i = 0;
   uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == kStages) {
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
       i = 0;
       parity ^= 1u;
     }
   }
 };
 
-template <int FMT>
+template <int FMT, bool SWAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ Args p) {
   constexpr int kTilesUnit = BK / fp4_tile_k(FMT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* ready = empty + kStages;  // the first CTA's: a stage's codes and scales are there in both
-  uint64_t* dfull = ready + kStages;
-  uint64_t* dempty = dfull + 1;       // the first CTA's
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* ready = empty + kMaxStages;  // the first CTA's: a stage's codes and scales are there in both
+  uint64_t* dfull = ready + kMaxStages;
+  uint64_t* dempty = dfull + 1;          // the first CTA's
   uint64_t* done = dempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int n_columns = SWAP ? p.n_columns : kTile;
+  const Stage stage = SWAP ? stage_of(true, n_columns) : stage_of(false, kTile);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&ready[s]), 8);
@@ -205,8 +236,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Turn turn;
       bool ok = true;
       for (int t = pair; t < p.n_tiles && ok; t += pairs) {
-        const int nt = t / p.m_pairs, mt = t - nt * p.m_pairs;
-        const int a_tile = 2 * mt + rank, b_parts = min(2, p.b_tiles - 2 * nt);
+        const int bt = t / p.a_pairs, at = t - bt * p.a_pairs;
+        const int a_tile = 2 * at + rank, b_parts = SWAP ? 1 : min(2, p.b_tiles - 2 * bt);
         const bool has_a = a_tile < p.a_tiles;  // (else the rows are past the matrix: zero codes, any scales)
         for (int u = 0; u < p.k_units; ++u) {
           if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
@@ -214,32 +245,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           if (leader) {
-            const uint32_t st = smem_u32(smem) + turn.i * kStageBytes, bar = smem_u32(&full[turn.i]);
+            const uint32_t st = smem_u32(smem) + turn.i * stage.bytes, bar = smem_u32(&full[turn.i]);
             const uint32_t sbytes = min(kTilesUnit, p.k_tiles - u * kTilesUnit) * 512;
-            mbar_expect_tx(bar, 2 * kCodes + ((has_a ? 1 : 0) + b_parts) * sbytes);
+            mbar_expect_tx(bar, kCodes + stage.b_rows * (BK / 2) + ((has_a ? 1 : 0) + b_parts) * sbytes);
             tma_load_2d(st, &ma, u * (BK / 2), a_tile * 128, bar);
-            tma_load_2d(st + kOffB, &mb, u * (BK / 2), nt * kTile + rank * 128, bar);
+            tma_load_2d(st + kCodes, &mb, u * (BK / 2), bt * kTile + rank * stage.b_rows, bar);
             const size_t along = static_cast<size_t>(u) * kTilesUnit;
-            if (has_a) bulk_load(st + kOffSA, p.sa + (static_cast<size_t>(a_tile) * p.k_tiles + along) * 512, sbytes, bar);
+            if (has_a) bulk_load(st + stage.off_sa(), p.sa + (static_cast<size_t>(a_tile) * p.k_tiles + along) * 512, sbytes, bar);
             for (int h = 0; h < b_parts; ++h)
-              bulk_load(st + kOffSB + h * kScaleTiles,
-                        p.sb + (static_cast<size_t>(2 * nt + h) * p.k_tiles + along) * 512, sbytes, bar);
+              bulk_load(st + stage.off_sb() + h * kScaleTiles,
+                        p.sb + (static_cast<size_t>(2 * bt + h) * p.k_tiles + along) * 512, sbytes, bar);
           }
           __syncwarp();
-          turn.next();
+          turn.next(stage.n);
           ++issued;
         }
       }
     }
     // every issued stage's copies land before the CTA may exit
-    for (int i = max(0, issued - kStages); i < issued; ++i)
+    for (int i = max(0, issued - stage.n); i < issued; ++i)
       for (int r = 0; r < p.wait_limit; ++r)
-        if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % kStages]), (i / kStages) & 1))) break;
+        if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % stage.n]), (i / stage.n) & 1))) break;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs, by the first CTA
     if (rank == 0) {
       const bool leader = elect_one();
-      constexpr uint32_t idesc = idesc_of(FMT);
+      const uint32_t idesc = idesc_of(FMT, n_columns);
+      constexpr uint32_t kTileColsB = SWAP ? 4 : 8;
       Turn turn;
       uint32_t tile_parity = 1;
       bool ok = true;
@@ -253,24 +285,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(smem) + turn.i * kStageBytes;
-          const uint32_t sa = tmem + kTmemScales + turn.i * kScaleCols, sb = sa + 16;
+          const uint32_t st = smem_u32(smem) + turn.i * stage.bytes;
+          const uint32_t sa = tmem + scales_at(SWAP) + turn.i * scale_cols(SWAP), sb = sa + 16;
           const int n_k = min(4, (p.K - u * BK + 63) / 64);  // MMAs with k of the matrices
           if (leader) {
-            const uint64_t ad = codes_desc(st), bd = codes_desc(st + kOffB);
+            const uint64_t ad = codes_desc(st), bd = codes_desc(st + kCodes);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
               if (j >= n_k) break;
               if constexpr (FMT == EXQ_FP4_E4M3)
-                mma_pair<FMT>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + 8 * j, (u | j) != 0);
+                mma_pair<FMT>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + kTileColsB * j, (u | j) != 0);
               else  // two scales of the tile's four: byte 0 or 2 of each word
                 mma_pair<FMT>(tmem, ad + 2 * j, bd + 2 * j, (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc, sa + 4 * (j >> 1),
-                              sb + 8 * (j >> 1), (u | j) != 0);
+                              sb + kTileColsB * (j >> 1), (u | j) != 0);
             }
             commit_pair(smem_u32(&empty[turn.i]));
           }
           __syncwarp();
-          turn.next();
+          turn.next(stage.n);
         }
         if (leader) commit_pair(smem_u32(dfull));
         __syncwarp();
@@ -292,55 +324,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const uint8_t* st = smem + turn.i * kStageBytes + lane * 16;
+        const uint8_t* sa = smem + turn.i * stage.bytes + stage.off_sa() + lane * 16;
+        const uint8_t* sb = smem + turn.i * stage.bytes + stage.off_sb() + lane * 16;
         uint4 a[4], b[2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          a[j] = *reinterpret_cast<const uint4*>(st + kOffSA + j % kTilesUnit * 512);
-          // columns: tile 0 of the first and the second 128 rows, tile 1 of both, ...
-          b[0][j] = *reinterpret_cast<const uint4*>(st + kOffSB + (j & 1) * kScaleTiles + (j >> 1) * 512);
-          if (kTilesUnit == 4) b[1][j] = *reinterpret_cast<const uint4*>(st + kOffSB + (j & 1) * kScaleTiles + (2 + (j >> 1)) * 512);
+          a[j] = *reinterpret_cast<const uint4*>(sa + j % kTilesUnit * 512);
+          if constexpr (SWAP) {
+            b[0][j] = *reinterpret_cast<const uint4*>(sb + j % kTilesUnit * 512);
+          } else {
+            // columns: tile 0 of the first and the second 128 rows, tile 1 of both, ...
+            b[0][j] = *reinterpret_cast<const uint4*>(sb + (j & 1) * kScaleTiles + (j >> 1) * 512);
+            if (kTilesUnit == 4) b[1][j] = *reinterpret_cast<const uint4*>(sb + (j & 1) * kScaleTiles + (2 + (j >> 1)) * 512);
+          }
         }
         tc_fence_after();
-        const uint32_t to = tmem + lanes + kTmemScales + turn.i * kScaleCols;  // (the stage was free, so this is)
+        const uint32_t to = tmem + lanes + scales_at(SWAP) + turn.i * scale_cols(SWAP);  // (the stage was free, so this is)
         tmem_st16(to, a);
         tmem_st16(to + 16, b[0]);
-        if (kTilesUnit == 4) tmem_st16(to + 32, b[1]);
+        if (!SWAP && kTilesUnit == 4) tmem_st16(to + 32, b[1]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first(smem_u32(&ready[turn.i]));
-        turn.next();
+        turn.next(stage.n);
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 6) >> 2;
-    const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (n_columns / 2);
     uint32_t parity = 0;
     for (int t = pair; t < p.n_tiles; t += pairs) {
-      const int nt = t / p.m_pairs, mt = t - nt * p.m_pairs;
+      const int bt = t / p.a_pairs, at = t - bt * p.a_pairs;
       if (!mbar_wait_warp(smem_u32(dfull), parity, abort_flag, p.wait_limit, &g_fp4_gemm_err) || *abort_flag) break;
       parity ^= 1u;
       tc_fence_after();
-      uint32_t h[64];
+      const int row = at * kTile + rank * 128 + quarter * 32 + lane;
+      if constexpr (SWAP) {
+        uint32_t v[4][16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(from + 32 * c, r);
+        for (int c = 0; c < 4; ++c)
+          if (16 * c < n_columns / 2) tmem_ld16(from + 16 * c, v[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(smem_u32(dempty));
+        if (row < p.A) {
+          uint16_t* dst = p.y + static_cast<size_t>(half * (n_columns / 2)) * p.A + row;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          h[16 * c + j] = pack_half2(__uint_as_float(r[2 * j]) * p.factor, __uint_as_float(r[2 * j + 1]) * p.factor);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first(smem_u32(dempty));
-      const int m = mt * kTile + rank * 128 + quarter * 32 + lane, n0 = nt * kTile + half * 128;
-      if (m < p.M) {
-        uint16_t* dst = p.y + static_cast<size_t>(m) * p.N + n0;
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (n0 + 8 * j < p.N) *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            for (int j = 0; j < 16; ++j)
+              if (16 * c + j < n_columns / 2 && half * (n_columns / 2) + 16 * c + j < p.B)
+                dst[static_cast<size_t>(16 * c + j) * p.A] = __half_as_ushort(__float2half_rn(__uint_as_float(v[c][j]) * p.factor));
+        }
+      } else {
+        uint32_t h[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(from + 32 * c, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            h[16 * c + j] = pack_half2(__uint_as_float(r[2 * j]) * p.factor, __uint_as_float(r[2 * j + 1]) * p.factor);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(smem_u32(dempty));
+        const int n0 = bt * kTile + half * 128;
+        if (row < p.A) {
+          uint16_t* dst = p.y + static_cast<size_t>(row) * p.B + n0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (n0 + 8 * j < p.B) *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        }
       }
     }
   }
@@ -359,35 +416,41 @@ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-exq_status launch_fp4_gemm_tiles(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uint16_t* y, int sms, int device,
-                                 cudaStream_t stream) {
+exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uint16_t* y, int sms, int device,
+                           cudaStream_t stream) {
+  const bool swap = x.rows <= 128;
+  const exq_fp4_matrix &a = swap ? w : x, &b = swap ? x : w;
+  const int n_columns = swap ? div_up(x.rows, 32) * 32 : kTile;
   CUtensorMap ma, mb;
   if (!encode_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K / 2, a.rows, a.K / 2, BK / 2, 128,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K / 2, w.rows, w.K / 2, BK / 2, 128,
+      !encode_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, b.K / 2, b.rows, b.K / 2, BK / 2, n_columns / 2,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_128B))
     return EXQ_ERR_CUDA;
   Args p{};
   p.sa = a.scales;
-  p.sb = w.scales;
+  p.sb = b.scales;
   p.y = y;
-  p.factor = a.factor * w.factor;
-  p.M = a.rows;
-  p.N = w.rows;
+  p.factor = a.factor * b.factor;
+  p.A = a.rows;
+  p.B = b.rows;
   p.K = a.K;
   p.a_tiles = div_up(a.rows, 128);
-  p.b_tiles = div_up(w.rows, 128);
+  p.b_tiles = div_up(b.rows, 128);
   p.k_tiles = div_up(a.K, fp4_tile_k(a.format));
   p.k_units = div_up(a.K, BK);
-  p.m_pairs = div_up(a.rows, kTile);
-  p.n_tiles = p.m_pairs * div_up(w.rows, kTile);
+  p.a_pairs = div_up(a.rows, kTile);
+  p.n_tiles = p.a_pairs * div_up(b.rows, kTile);
+  p.n_columns = n_columns;
   const int starve = testing_starve_rounds();
   p.wait_limit = starve > 0 ? starve : kFp4WaitLimit;
   p.starve = starve > 0 ? 1 : 0;
 
-  auto fn = a.format == EXQ_FP4_E4M3 ? gemm_kernel<EXQ_FP4_E4M3> : gemm_kernel<EXQ_FP4_E8M0>;
-  static PerDevice attr[2];
-  if (!attr[a.format == EXQ_FP4_E4M3].once(device, [&] {
+  const bool e4m3 = a.format == EXQ_FP4_E4M3;
+  auto fn = e4m3 ? (swap ? gemm_kernel<EXQ_FP4_E4M3, true> : gemm_kernel<EXQ_FP4_E4M3, false>)
+                 : (swap ? gemm_kernel<EXQ_FP4_E8M0, true> : gemm_kernel<EXQ_FP4_E8M0, false>);
+  static PerDevice attr[4];
+  if (!attr[2 * e4m3 + swap].once(device, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) == cudaSuccess;
       }))
     return EXQ_ERR_CUDA;

@@ -1,9 +1,10 @@
 // fp16 rows to the microscaled 4-bit format and back.
 //
 // Both ways are bound by memory: 2 bytes a value on the one side, 9/16 (E4M3)
-// or 17/32 (E8M0) on the other. A thread takes 16 consecutive values (32 bytes
-// in two loads, 8 bytes of codes), so that a warp reads 1 KB in one piece; the
-// scale bytes of 4 blocks of a row leave as one 4-byte word of their tile.
+// or 17/32 (E8M0) on the other. A quantising thread takes 16 consecutive
+// values (one load of 32 bytes, 8 bytes of codes), so that a warp reads 1 KB in
+// one piece; the scale bytes of 4 blocks of a row leave as one 4-byte word of
+// their tile.
 #include "exq_fp4.cuh"
 
 namespace exq {
@@ -35,27 +36,49 @@ __device__ __forceinline__ uint32_t scale_byte(float a, float f, float inv6f) {
   return max(lo, 1u);
 }
 
+// Row and piece of an index that goes up by a fixed stride: a division at the
+// start only (of 64-bit numbers, 100 instructions).
+struct Walk {
+  long long row, d_row;
+  int piece, d_piece, per_row;
+  __device__ __forceinline__ Walk(long long i, long long stride, int n) : per_row(n) {
+    row = i / n;
+    piece = static_cast<int>(i - row * n);
+    d_row = stride / n;
+    d_piece = static_cast<int>(stride - d_row * n);
+  }
+  __device__ __forceinline__ void next() {
+    row += d_row;
+    piece += d_piece;
+    if (piece >= per_row) {
+      piece -= per_row;
+      ++row;
+    }
+  }
+};
+
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __restrict__ x, uint2* __restrict__ codes,
                                                             uint32_t* __restrict__ scales, int rows, int K, float f,
                                                             float inv6f) {
   constexpr int kPer = fp4_tile_k(FMT) / 16;  // threads of one scale word: 4 or 8
   const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
   const long long padded = static_cast<long long>((rows + 127) / 128) * 128;
-  const long long total = padded * words * kPer;
+  const int per_row = words * kPer;
+  const long long total = padded * per_row;
   const int pieces = K / 16;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    // total is a multiple of 32 (padded is one of 128): the warp is whole here
-    const long long row = i / (words * kPer);
-    const int piece = static_cast<int>(i - row * (words * kPer));
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  Walk at(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, stride, per_row);
+  // total is a multiple of 32 (padded is one of 128): the warp is whole here
+  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += stride, at.next()) {
+    const long long row = at.row;
+    const int piece = at.piece;
     const bool in = row < rows && piece < pieces;
     uint32_t h[8] = {};
     if (in) {
-      const uint4* src = x + (row * pieces + piece) * 2;
-      const uint4 p = __ldcs(src), q = __ldcs(src + 1);
-      h[0] = p.x; h[1] = p.y; h[2] = p.z; h[3] = p.w;
-      h[4] = q.x; h[5] = q.y; h[6] = q.z; h[7] = q.w;
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "=r"(h[4]), "=r"(h[5]), "=r"(h[6]), "=r"(h[7])
+                   : "l"(x + (row * pieces + piece) * 16));
     }
     // the largest magnitude, as bits: they order as the numbers do, infinity and NaN above
     uint32_t m2 = 0u;
@@ -137,34 +160,66 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint4* __restr
   }
 }
 
+// 32 codes of a row, their scales and where they go
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint2* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales,
-                                                              uint4* __restrict__ out, int rows, int K, float f) {
-  const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
-  const int pieces = K / 16;
-  const long long total = static_cast<long long>(rows) * pieces;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long row = i / pieces;
-    const int piece = static_cast<int>(i - row * pieces);
-    const int block = FMT == EXQ_FP4_E4M3 ? piece : piece >> 1;
-    const uint2 c = __ldcs(codes + i);
-    const uint32_t b = __ldg(scales + ((row >> 7) * words + (block >> 2)) * 512 + fp4_tile_byte(static_cast<int>(row & 127)) +
-                             (block & 3));
-    const float s = FMT == EXQ_FP4_E4M3 ? e4m3_f32(b) : e8m0_f32(b);
-    const uint32_t p[8] = {e2m1x2_f16<0>(c.x), e2m1x2_f16<1>(c.x), e2m1x2_f16<2>(c.x), e2m1x2_f16<3>(c.x),
-                           e2m1x2_f16<0>(c.y), e2m1x2_f16<1>(c.y), e2m1x2_f16<2>(c.y), e2m1x2_f16<3>(c.y)};
-    uint32_t o[8];
+struct Codes32 {
+  uint4 c;
+  uint32_t s;  // E4M3: the bytes of two blocks; E8M0: of one
+  uint16_t* to;
+  __device__ __forceinline__ void load(const uint4* codes, const uint8_t* scales, uint16_t* out, long long i, const Walk& at,
+                                       int words) {
+    c = __ldcs(codes + i);
+    const uint8_t* tile = scales + fp4_tile_byte(static_cast<int>(at.row & 127));
+    if constexpr (FMT == EXQ_FP4_E4M3)
+      s = __ldg(reinterpret_cast<const uint16_t*>(tile + ((at.row >> 7) * words + (at.piece >> 1)) * 512 + (at.piece & 1) * 2));
+    else
+      s = __ldg(tile + ((at.row >> 7) * words + (at.piece >> 2)) * 512 + (at.piece & 3));
+    to = out + 32 * i;
+  }
+  __device__ __forceinline__ void store(float f) const {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
-      // code times scale is exact (6 bits), the factor rounds once in fp32
-      const __half2 y = __floats2half2_rn(v.x * s * f, v.y * s * f);
-      o[j] = *reinterpret_cast<const uint32_t*>(&y);
+    for (int h = 0; h < 2; ++h) {
+      const float sc = FMT == EXQ_FP4_E4M3 ? e4m3_f32((s >> (8 * h)) & 0xFFu) : e8m0_f32(s);
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t v = w[2 * h + j];
+        const uint32_t p[4] = {e2m1x2_f16<0>(v), e2m1x2_f16<1>(v), e2m1x2_f16<2>(v), e2m1x2_f16<3>(v)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
+          // code times scale is exact (6 bits), the factor rounds once in fp32
+          const __half2 y = __floats2half2_rn(x.x * sc * f, x.y * sc * f);
+          o[4 * j + k] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * h), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                   "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
     }
-    __stcs(out + 2 * i, make_uint4(o[0], o[1], o[2], o[3]));
-    __stcs(out + 2 * i + 1, make_uint4(o[4], o[5], o[6], o[7]));
+  }
+};
+
+// A thread takes 32 codes at a time (16 bytes; 64 of results, in stores of 32
+// bytes, whole sectors), and has the next 32 on their way.
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint4* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales,
+                                                              uint16_t* __restrict__ out, int rows, int K, float f) {
+  const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
+  const int pieces = K / 32;
+  const long long total = static_cast<long long>(rows) * pieces, stride = static_cast<long long>(gridDim.x) * kThreads;
+  long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  Walk at(i, stride, pieces);
+  for (; i < total; i += 2 * stride) {
+    Codes32<FMT> a, b;
+    a.load(codes, scales, out, i, at, words);
+    at.next();
+    const bool two = i + stride < total;
+    if (two) b.load(codes, scales, out, i + stride, at, words);
+    at.next();
+    a.store(f);
+    if (two) b.store(f);
   }
 }
 
@@ -180,15 +235,15 @@ exq_status launch_fp4_quantize(const uint16_t* x, const exq_fp4_matrix& m, int s
   const long long threads = static_cast<long long>((m.rows + 127) / 128) * 128 * words * (fp4_tile_k(m.format) / 16);
   auto fn = m.format == EXQ_FP4_E4M3 ? quantize_kernel<EXQ_FP4_E4M3> : quantize_kernel<EXQ_FP4_E8M0>;
   fn<<<blocks_for(threads, sms), kThreads, 0, stream>>>(
-      reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(m.codes), reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K,
+      x, reinterpret_cast<uint2*>(m.codes), reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K,
       m.factor, 1.f / (6.f * m.factor));
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 
 exq_status launch_fp4_dequantize(const exq_fp4_matrix& m, uint16_t* out, int sms, cudaStream_t stream) {
   auto fn = m.format == EXQ_FP4_E4M3 ? dequantize_kernel<EXQ_FP4_E4M3> : dequantize_kernel<EXQ_FP4_E8M0>;
-  fn<<<blocks_for(static_cast<long long>(m.rows) * (m.K / 16), sms), kThreads, 0, stream>>>(
-      reinterpret_cast<const uint2*>(m.codes), m.scales, reinterpret_cast<uint4*>(out), m.rows, m.K, m.factor);
+  fn<<<blocks_for(static_cast<long long>(m.rows) * (m.K / 32), sms), kThreads, 0, stream>>>(
+      reinterpret_cast<const uint4*>(m.codes), m.scales, out, m.rows, m.K, m.factor);
   return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 

@@ -279,10 +279,10 @@ exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, fn, p) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 
-// (dependent: a programmatic dependent of the launch before it)
+// (each a programmatic dependent of the launch before it)
 template <int MODE>
 exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a,
-                         int ctas, bool dependent, int device, cudaStream_t stream) {
+                         int ctas, int device, cudaStream_t stream) {
   auto fn = format == EXQ_FP4_E4M3 ? stream_kernel<EXQ_FP4_E4M3, MODE> : stream_kernel<EXQ_FP4_E8M0, MODE>;
   static PerDevice attr[2];
   if (!attr[format == EXQ_FP4_E4M3].once(device, [&] {
@@ -298,7 +298,7 @@ exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, m0, m1, mx, a) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 
@@ -353,47 +353,6 @@ struct MoePlan {
 
 }  // namespace
 
-namespace {
-
-// What the two ways of a product of 4-bit matrices take, in clocks (measured at
-// 1.9 GHz): pairs of CTAs with tiles of 256 x 256, whole waves of them; or
-// units of 128 x 128 x 256 that are divided evenly, with parts to join.
-bool few_tiles(int M, int N, int K, int sms) {
-  const long long k_units = div_up(K, kUnitK), pairs = std::max(sms / 2, 1);
-  const long long tiles = static_cast<long long>(div_up(M, 256)) * div_up(N, 256);
-  const long long few = static_cast<long long>(div_up(M, kFewRows)) * div_up(N, kRows);
-  if (few > kTileCounters) return false;
-  const long long by_tiles = (tiles + pairs - 1) / pairs * (k_units * 560 + 1200) + 3000;
-  const long long by_units = (few * k_units + sms - 1) / sms * 800 + 9000;
-  return by_units < by_tiles;
-}
-
-}  // namespace
-
-size_t fp4_gemm_workspace_bytes(const exq_fp4_matrix& a, const exq_fp4_matrix& w, int sms) {
-  return few_tiles(a.rows, w.rows, a.K, sms) ? EXQ_FP4_COUNTER_BYTES + part_bytes(kFew, sms) : 0;
-}
-
-exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uint16_t* y, void* workspace, int sms,
-                           int device, cudaStream_t stream) {
-  if (!few_tiles(x.rows, w.rows, x.K, sms)) return launch_fp4_gemm_tiles(x, w, y, sms, device, stream);
-  CUtensorMap mw, mx;
-  if (!encode_codes(&mw, w.codes, w.rows, w.K, kRows) ||
-      !encode_codes(&mx, x.codes, x.rows, x.K, std::min(kFewRows, div_up(x.rows, 8) * 8)))
-    return EXQ_ERR_CUDA;
-  Args a{};
-  set_shape(a, w.format, w.rows, w.K);
-  a.sc0 = w.scales;
-  a.x = x.scales;
-  a.y = y;
-  a.M = x.rows;
-  a.factor = x.factor * w.factor;
-  a.counters = static_cast<unsigned*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + EXQ_FP4_COUNTER_BYTES);
-  const long long units = static_cast<long long>(a.row_tiles) * a.k_units * div_up(x.rows, kFewRows);
-  return launch_stream<kFew>(w.format, mw, mw, mx, a, static_cast<int>(std::min<long long>(units, sms)), false, device, stream);
-}
-
 size_t fp4_gemv_workspace_bytes(const exq_fp4_matrix& w, int M, int sms) { return GemvPlan(w.format, w.K, M, sms).end; }
 
 bool fp4_gemv_fits(int rows) { return div_up(rows, kRows) <= kTileCounters; }
@@ -424,7 +383,7 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   a.counters = static_cast<unsigned*>(workspace);
   a.part = reinterpret_cast<float*>(ws + plan.part);
   const long long units = static_cast<long long>(a.row_tiles) * a.k_units;
-  return launch_stream<kGemv>(w.format, mw, mw, mx, a, static_cast<int>(std::min<long long>(units, sms)), true, device, stream);
+  return launch_stream<kGemv>(w.format, mw, mw, mx, a, static_cast<int>(std::min<long long>(units, sms)), device, stream);
 }
 
 size_t moe_workspace_bytes(const exq_moe_layer& l, int T, int sms) { return MoePlan(l, T, sms).end; }
@@ -484,7 +443,7 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.act = l.act;
   a.counters = counters;
   a.part = reinterpret_cast<float*>(ws + plan.part);
-  if ((st = launch_stream<kUp>(fmt, mg, mu, mg, a, sms, true, device, stream)) != EXQ_OK) return st;
+  if ((st = launch_stream<kUp>(fmt, mg, mu, mg, a, sms, device, stream)) != EXQ_OK) return st;
 
   p.pieces = ws + plan.h_pieces;
   p.T = T * l.top_k;
@@ -500,7 +459,7 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.f0 = l.down.factors;
   a.f1 = nullptr;
   a.y = y;
-  return launch_stream<kDown>(fmt, md, md, md, a, sms, true, device, stream);
+  return launch_stream<kDown>(fmt, md, md, md, a, sms, device, stream);
 }
 
 unsigned take_fp4_stream_errors(cudaStream_t stream) {

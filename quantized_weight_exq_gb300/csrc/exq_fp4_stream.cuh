@@ -1,9 +1,8 @@
-// Products of a few rows with matrices of the microscaled 4-bit format on the
-// block-scaled tcgen05 tensor cores: the decode product (one matrix) and the
-// two products of an expert layer, of up to 16 fp16 rows, and the product of
-// two 4-bit matrices where there are few tiles of it.
+// Products of a few fp16 rows with matrices of the microscaled 4-bit format on
+// the block-scaled tcgen05 tensor cores: the decode product (one matrix) and
+// the two products of an expert layer.
 //
-//   out[t][n] = sum_k x[t][k] w[n][k]
+//   out[t][n] = sum_k x[t][k] w[n][k],   t < 16
 //
 // Every code is read once, so the floor is the codes' and scales' bytes. At
 // 6.8 TB/s an SM gets 47 codes a clock: turning them into fp16 in registers
@@ -46,14 +45,13 @@ namespace fp4s {
 
 static __device__ unsigned g_stream_err;
 
-enum Mode { kGemv = 0, kUp = 1, kDown = 2, kFew = 3 };
+enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
 constexpr int kThreads = 7 * 32;
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
-constexpr int kFewRows = 128;        // rows of a 4-bit x in a tile
 constexpr int kMaxPairs = 256;       // tokens x experts of each
 constexpr int kMaxExperts = 512;
 constexpr int kMaxStages = 10;
@@ -96,7 +94,7 @@ struct Args {
   const uint8_t* sc0;      // scale tiles of the matrix, or of expert 0's gate or down
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
-  const uint8_t* x;        // gemv, few: scale tiles (of the parts, of x); else pieces [token or pair, unit]
+  const uint8_t* x;        // gemv: scale tiles of the parts; else pieces [token or pair, unit]
   uint16_t* y;             // [M, rows] (not up)
   float* h;                // up: [pairs, rows]
   unsigned* h_most;        // [pairs]: bits of the largest finite magnitude of h
@@ -113,9 +111,7 @@ struct Args {
 };
 
 // floats of one CTA's part of a tile: a value for each row, token (and matrix)
-__host__ __device__ constexpr int part_floats(int mode) {
-  return kRows * (mode == kFew ? kFewRows : kMaxTokens * (mode == kUp ? 2 : 1));
-}
+__host__ __device__ constexpr int part_floats(int mode) { return kRows * kMaxTokens * (mode == kUp ? 2 : 1); }
 
 // The experts of a call, the same in every CTA: those that some token chose,
 // ascending, with the tokens of each and the place of (expert, token) in ids.
@@ -288,14 +284,12 @@ __device__ __forceinline__ int nth_bit(unsigned m, int j) {
 
 // ---------------------------------------------------------------- units
 
-// How many units a call has. `slots`: the experts, or (few) the tiles of x's
-// rows, or one.
+// How many units a call has. `slots`: the experts, or one.
 __device__ __forceinline__ long long units_of(const Args& a, int slots) {
   return static_cast<long long>(a.row_tiles) * a.k_units * slots;
 }
 
-// A unit's place: its expert (the index in Experts) or tile of x's rows, its
-// tile of the matrix's rows, and k. The
+// A unit's place: its expert (the index in Experts), tile of rows and k. The
 // division is made once a CTA; from unit to unit the place counts up.
 template <int MODE>
 struct Place {
@@ -309,7 +303,7 @@ struct Place {
     if constexpr (MODE == kUp) {
       slot = static_cast<int>(q / a.row_tiles);
       row = static_cast<int>(q) - slot * a.row_tiles;
-    } else if constexpr (MODE == kDown || MODE == kFew) {
+    } else if constexpr (MODE == kDown) {
       row = static_cast<int>(q / experts);
       slot = static_cast<int>(q) - row * experts;
     }
@@ -323,7 +317,7 @@ struct Place {
   __device__ __forceinline__ void next(const Args& a, int experts) {
     if (++kc < a.k_units) return;
     kc = 0;
-    if constexpr (MODE == kDown || MODE == kFew) {
+    if constexpr (MODE == kDown) {
       if (++slot < experts) return;
       slot = 0;
       ++row;
@@ -412,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   if constexpr (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n_experts = MODE == kFew ? (a.M + kFewRows - 1) / kFewRows : 1, most_tokens = a.M;
-  if constexpr (MODE == kUp || MODE == kDown) {
+  int n_experts = 1, most_tokens = a.M;
+  if constexpr (MODE != kGemv) {
     find_experts(a, ex, used, MODE == kUp && blockIdx.x == 0);
     n_experts = ex->n;
     most_tokens = ex->most_tokens;
@@ -434,12 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_mine = static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0);
 
   // the ring and the buffers of sums go by the most tokens that a matrix of the call has
-  constexpr bool kTileScales = MODE == kGemv || MODE == kFew;           // x's scales come as tiles
-  const int x_rows = MODE == kFew ? min(kFewRows, (a.M + 7) / 8 * 8) : 8 * most_tokens;
-  const int off_xs = kOffX + 128 * x_rows;                              // where
-  const int stage_bytes = kTileScales ? off_xs + 2048 : kOffX + kSlot * ((most_tokens + 3) / 4 * 4);
+  const int off_xs = kOffX + 1024 * most_tokens;                        // gemv: the parts' scale tiles
+  const int stage_bytes = MODE == kGemv ? off_xs + 2048 : kOffX + kSlot * ((most_tokens + 3) / 4 * 4);
   const int n_stages = min(kMaxStages, kRing / stage_bytes);
-  const int cols = (x_rows + 15) / 16 * 16;                             // of one sum
+  const int cols = (8 * most_tokens + 15) / 16 * 16;                    // of one sum
   const int buffer_cols = cols * kMatrices;
   const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
 
@@ -463,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn turn;
       bool ok = true;
       for (int left = n_mine; left > 0 && ok; --left) {
-        const int id = kTileScales ? 0 : ex->expert[at.slot];
+        const int id = MODE == kGemv ? 0 : ex->expert[at.slot];
         const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
         const size_t off = id * a.sc_stride + (static_cast<size_t>(at.row) * a.k_tiles + at.kc * kTiles) * 512;
 #pragma unroll
@@ -499,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn turn;
       bool ok = true;
       for (int left = n_mine; left > 0 && ok; --left) {
-        const unsigned tokens = kTileScales ? 0u : ex->tokens[at.slot];
+        const unsigned tokens = MODE == kGemv ? 0u : ex->tokens[at.slot];
         const int n_tok = __popc(tokens);
         const uint8_t* src = nullptr;  // lane: the piece of a token of the unit
         if (lane < n_tok) {
@@ -513,12 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t st = smem_u32(smem) + turn.i * stage_bytes, bar = smem_u32(&full[turn.i]);
-          if constexpr (kTileScales) {
+          if constexpr (MODE == kGemv) {
             if (leader) {
               const uint32_t sb = min(kTiles, a.k_tiles - at.kc * kTiles) * 512;
-              mbar_expect_tx(bar, x_rows * 128 + sb);
-              tma_load_2d(st + kOffX, &mx, at.kc * (kUnitK / 2), MODE == kFew ? at.slot * kFewRows : 0, bar);
-              bulk_load(st + off_xs, a.x + (static_cast<size_t>(at.slot) * a.k_tiles + at.kc * kTiles) * 512, sb, bar);
+              mbar_expect_tx(bar, a.M * 1024 + sb);
+              tma_load_2d(st + kOffX, &mx, at.kc * (kUnitK / 2), 0, bar);
+              bulk_load(st + off_xs, a.x + static_cast<size_t>(at.kc) * kTiles * 512, sb, bar);
             }
           } else {
             if (leader) mbar_expect_tx(bar, n_tok * piece_bytes(FMT));
@@ -540,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint32_t sa = tmem + kTmemScales;
     for (int left = n_mine; left > 0 && ok; --left) {
-      const int tokens = kTileScales ? 1 : __popc(ex->tokens[at.slot]);  // (all of x at once)
+      const int tokens = MODE == kGemv ? 1 : __popc(ex->tokens[at.slot]);  // (all of x at once)
       const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
       const uint32_t d0 = tmem + buf.i * buffer_cols;
       if (fresh && !mbar_wait_warp(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
@@ -560,13 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; g < tokens; g += 4) {
           // all of x, its scales in tiles; or four tokens, from their own lines
           const uint32_t sb = sa + 16 + 4 * g;
-          const uint32_t idesc = idesc_for(FMT, kTileScales ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
-          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, kTileScales ? 1024 : kSlot);
+          const uint32_t idesc = idesc_for(FMT, MODE == kGemv ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
+          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, MODE == kGemv ? 1024 : kSlot);
           const uint32_t d = d0 + 8 * g + which * cols;
           if (leader) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
-              copy_scales(sb + 4 * j, kTileScales ? lines_desc(st + off_xs + j * 512, kLines)
+              copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
                                                     : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
@@ -616,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_row = row * kRows + r;
       const bool in = n_row < a.rows;
       // whose units the tile is made of
-      const int tile = MODE == kUp ? slot * a.row_tiles + row : MODE == kFew ? row * n_experts + slot : row;
+      const int tile = MODE == kUp ? slot * a.row_tiles + row : row;
       const int tile_units = a.k_units * (MODE == kDown ? n_experts : 1);
       const long long first = static_cast<long long>(tile) * tile_units;
       const int b0 = owner(first, n_units, ctas), b1 = owner(first + tile_units - 1, n_units, ctas);
@@ -640,44 +632,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");
         return *last != 0;
       };
-      if constexpr (MODE == kFew) {
-        const int m0 = slot * kFewRows, n_rows = min(kFewRows, a.M - m0);
-        const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
-        tc_fence_after();
-        auto store = [&](int c, const float (&v)[16]) {
-          if (!in || *abort_flag) return;
-          uint16_t* dst = a.y + static_cast<size_t>(m0 + c) * a.rows + n_row;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < n_rows) dst[static_cast<size_t>(j) * a.rows] = __half_as_ushort(__float2half_rn(v[j] * a.factor));
-        };
-        float v[16];
-        for (int c = 0; c < n_rows; c += 16) {
-          if (!ok) break;
-          tmem_ld16(tmem + lanes + buf.i * buffer_cols + c, v);
-          if (b0 == b1) {
-            store(c, v);
-          } else {
-            float* p = part_of(blockIdx.x) + c * kRows;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < n_rows) __stcg(p + j * kRows, v[j]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&dempty[buf.i]));
-        buf.next(n_buffers);
-        if (b0 != b1 && last_of_tile()) {
-          for (int c = 0; c < n_rows; c += 16) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.f;
-            add_parts(v, n_rows - c, b0, b1, [&](int b) { return part_of(b) + c * kRows; });
-            store(c, v);
-          }
-        }
-        continue;
-      }
       const unsigned tokens = MODE == kGemv ? everyone : ex->tokens[slot];
       const int n_tok = __popc(tokens);
       float f = 0.f;  // down: lane's token's weight, times down's factor and h's

@@ -95,11 +95,8 @@ size_t paged_attn_workspace_bytes(const exq_kv_cache& c, const exq_kv_batch& bat
 // microscaled 4-bit floating point (arguments checked by the caller)
 exq_status launch_fp4_quantize(const uint16_t* x, const exq_fp4_matrix& m, int sms, cudaStream_t stream);
 exq_status launch_fp4_dequantize(const exq_fp4_matrix& m, uint16_t* out, int sms, cudaStream_t stream);
-exq_status launch_fp4_gemm(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uint16_t* y, void* workspace, int sms,
-                           int device, cudaStream_t stream);
-exq_status launch_fp4_gemm_tiles(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uint16_t* y, int sms, int device,
-                                 cudaStream_t stream);  // sizes that fill the GPU with tiles of 256 x 256
-size_t fp4_gemm_workspace_bytes(const exq_fp4_matrix& a, const exq_fp4_matrix& w, int sms);
+exq_status launch_fp4_gemm(const exq_fp4_matrix& a, const exq_fp4_matrix& w, uint16_t* y, int sms, int device,
+                           cudaStream_t stream);
 exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, uint16_t* y, void* workspace, int sms,
                            int device, cudaStream_t stream);
 size_t fp4_gemv_workspace_bytes(const exq_fp4_matrix& w, int M, int sms);

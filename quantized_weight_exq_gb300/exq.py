@@ -44,7 +44,7 @@ EXPORTED = (
     "exq_quantize_exl2", "exq_measure_exl2_workspace_size", "exq_measure_exl2", "exq_solve_exl2_bits",
     "exq_rope_freqs", "exq_rope_steps", "exq_rope", "exq_kv_append", "exq_paged_attn_workspace_size", "exq_paged_attn",
     "exq_kv_copy_pages", "exq_pages_alloc", "exq_pages_free", "exq_pages_fork", "exq_pages_compact",
-    "exq_fp4_scale_bytes", "exq_pack_fp4", "exq_fp4_quantize", "exq_fp4_dequantize", "exq_fp4_gemm_workspace_size", "exq_fp4_gemm",
+    "exq_fp4_scale_bytes", "exq_pack_fp4", "exq_fp4_quantize", "exq_fp4_dequantize", "exq_fp4_gemm",
     "exq_fp4_gemv_workspace_size", "exq_fp4_gemv", "exq_moe_workspace_size", "exq_moe",
     "exq_testing_starve",
 )
@@ -149,8 +149,7 @@ def _load():
         "exq_pack_fp4": (st, [P, P, i32, i32, i32, P, P]),
         "exq_fp4_quantize": (st, [P, P, P]),
         "exq_fp4_dequantize": (st, [P, P, P]),
-        "exq_fp4_gemm_workspace_size": (sz, [P, P]),
-        "exq_fp4_gemm": (st, [P, P, P, P, sz, P]),
+        "exq_fp4_gemm": (st, [P, P, P, P]),
         "exq_fp4_gemv_workspace_size": (sz, [P, i32]),
         "exq_fp4_gemv": (st, [P, P, i32, P, P, sz, P]),
         "exq_moe_workspace_size": (sz, [P, i32]),
@@ -732,24 +731,25 @@ def exq_kv_copy_pages(cache: KVCache, pairs, stream=None) -> None:
 
 FP4_COUNTER_BYTES = 128 << 10  # EXQ_FP4_COUNTER_BYTES
 
-_fp4_ws = {}  # (device index, stream handle) -> workspace of exq_fp4_gemm, exq_fp4_gemv and exq_moe, its counters zero between calls
+# (device index, stream handle) -> (workspace of exq_fp4_gemv and exq_moe, its address and bytes); its counters are zero between calls
+_fp4_ws = {}
 
 
 def _fp4_workspace(need: int, dev: int, stream, handle: int, where: str):
-    """The default workspace of the launch's stream, its counters zeroed in that stream's order; kept and grown across calls.
-    Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
+    """(address, bytes) of the default workspace of the launch's stream, its counters zeroed in that stream's order; kept and grown
+    across calls. Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
     import torch
     if stream is not None:
         with _on(stream, dev):
             return _fp4_workspace(need, dev, None, handle, where)
     if torch.cuda.is_current_stream_capturing():
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
-    buf = _fp4_ws.get((dev, handle))
-    if buf is None or buf.numel() < need:
-        buf = torch.empty(max(need, 4 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
+    kept = _fp4_ws.get((dev, handle))
+    if kept is None or kept[2] < need:
+        buf = torch.empty(max(need, 8 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
         buf[:FP4_COUNTER_BYTES].zero_()
-        _fp4_ws[dev, handle] = buf
-    return buf
+        kept = _fp4_ws[dev, handle] = buf, buf.data_ptr(), buf.numel()
+    return kept[1:]
 
 
 def exq_fp4_scale_bytes(format: int, rows: int, K: int) -> int:
@@ -774,10 +774,36 @@ class Fp4Matrix:
 
     def __init__(self, codes, scales, format: int, factor: float = 1.0):
         self.rows, self.K = _fp4_tensors("Fp4Matrix", codes, scales, (), format)
-        self.codes, self.scales, self.format, self.factor = codes, scales, format, factor
+        self._codes, self._scales, self.format, self.factor = codes, scales, format, factor
         self.device = codes.get_device()
         self._desc = exq_fp4_matrix(format, self.rows, self.K, factor, codes.data_ptr(), scales.data_ptr())
         self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def _made(cls, rows: int, K: int, format: int, factor: float, like, stream):
+        """One with memory of its own (codes, then scales), on the device of ``like``; its sizes are for the call that fills it to check."""
+        import torch
+        m = cls.__new__(cls)
+        n = rows * K // 2
+        buf = _empty(n + 512 * (-(-rows // 128) * -(-K // (64 if format == FP4_E4M3 else 128))), torch.uint8, like.device, stream)
+        m.rows, m.K, m.format, m.factor, m.device = rows, K, format, factor, like.get_device()
+        m._buf, m._codes, m._scales = buf, None, None
+        at = buf.data_ptr()
+        m._desc = exq_fp4_matrix(format, rows, K, factor, at, at + n)
+        m._ref = ctypes.byref(m._desc)
+        return m
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * self.K // 2].view(self.rows, self.K // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buf[self.rows * self.K // 2:]
+        return self._scales
 
 
 def exq_pack_fp4(codes: np.ndarray, scales: np.ndarray, format: int):
@@ -798,11 +824,18 @@ def fp4_matrix(codes: np.ndarray, scales: np.ndarray, format: int, factor: float
     return Fp4Matrix(*(torch.from_numpy(a).to(device) for a in exq_pack_fp4(codes, scales, format)), format, factor)
 
 
-def _fp16_rows(x, where: str):
-    """Refuses what is not a contiguous fp16 [rows, K]."""
+def _is_rows(x, half) -> bool:
+    return x.dtype is half and x.dim() == 2 and x.is_contiguous()
+
+
+def _result(out, rows: int, cols: int, dev: int, like, stream, where: str):
+    """``out``, which has to be a contiguous fp16 [rows, cols] on the device, or such a tensor."""
     import torch
-    if x.dtype != torch.float16 or x.dim() != 2 or not x.is_contiguous():
+    if out is None:
+        return _empty((rows, cols), torch.float16, like.device, stream)
+    if not _is_rows(out, torch.float16) or out.shape != (rows, cols) or out.get_device() != dev:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    return out
 
 
 def exq_fp4_quantize(x, format: int, factor: float = 1.0, out: Optional[Fp4Matrix] = None, stream=None) -> Fp4Matrix:
@@ -810,17 +843,14 @@ def exq_fp4_quantize(x, format: int, factor: float = 1.0, out: Optional[Fp4Matri
     replaced."""
     import torch
     where = "exq_fp4_quantize"
-    _fp16_rows(x, where)
-    rows, K = x.shape
     dev = x.get_device()
-    _here(where, dev, dev if out is None else out.device)
+    _here(where, dev)
+    if not _is_rows(x, torch.float16):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    rows, K = x.shape
     if out is None:
-        bytes_ = exq_fp4_scale_bytes(format, rows, K)
-        if rows and not bytes_:
-            raise ExqError(EXQ_ERR_INVALID_ARG, where)
-        out = Fp4Matrix(_empty((rows, K // 2), torch.uint8, x.device, stream), _empty(bytes_, torch.uint8, x.device, stream),
-                        format, factor)
-    elif out.rows != rows or out.K != K:
+        out = Fp4Matrix._made(rows, K, format, factor, x, stream)
+    elif out.rows != rows or out.K != K or out.device != dev:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     _check(_lib.exq_fp4_quantize(x.data_ptr(), out._ref, _stream_ptr(stream, dev)), where)
     return out
@@ -828,49 +858,28 @@ def exq_fp4_quantize(x, format: int, factor: float = 1.0, out: Optional[Fp4Matri
 
 def exq_fp4_dequantize(m: Fp4Matrix, out=None, stream=None):
     """The matrix as fp16 [rows, K]."""
-    import torch
     where = "exq_fp4_dequantize"
-    _here(where, m.device, m.device if out is None else out.get_device())
-    if out is None:
-        out = _empty((m.rows, m.K), torch.float16, m.codes.device, stream)
-    _fp16_rows(out, where)
-    if out.shape != (m.rows, m.K):
-        raise ExqError(EXQ_ERR_INVALID_ARG, where)
-    _check(_lib.exq_fp4_dequantize(m._ref, out.data_ptr(), _stream_ptr(stream, m.device)), where)
+    dev = m.device
+    _here(where, dev)
+    out = _result(out, m.rows, m.K, dev, m._codes if m._codes is not None else m._buf, stream, where)
+    _check(_lib.exq_fp4_dequantize(m._ref, out.data_ptr(), _stream_ptr(stream, dev)), where)
     return out
 
 
-def exq_fp4_gemm_workspace_size(a: Fp4Matrix, w: Fp4Matrix) -> int:
-    return int(_lib.exq_fp4_gemm_workspace_size(a._ref, w._ref))
-
-
-def _space(workspace, where: str):
-    """(address, bytes) of a workspace tensor."""
-    if workspace is None:
-        return None, 0
-    if not workspace.is_contiguous():
+def _space(workspace, dev: int, where: str):
+    """(address, bytes) of a caller's workspace."""
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def exq_fp4_gemm(a: Fp4Matrix, w: Fp4Matrix, out=None, workspace=None, stream=None):
-    """a . w^T as fp16 [a.rows, w.rows], both in the 4-bit format. The workspace is as exq_fp4_gemv's; large products need none."""
-    import torch
+def exq_fp4_gemm(a: Fp4Matrix, w: Fp4Matrix, out=None, stream=None):
+    """a . w^T as fp16 [a.rows, w.rows], both in the 4-bit format."""
     where = "exq_fp4_gemm"
     dev = a.device
-    _here(where, dev, w.device, dev if out is None else out.get_device(), dev if workspace is None else workspace.get_device())
-    if out is None:
-        out = _empty((a.rows, w.rows), torch.float16, a.codes.device, stream)
-    _fp16_rows(out, where)
-    if out.shape != (a.rows, w.rows):
-        raise ExqError(EXQ_ERR_INVALID_ARG, where)
-    handle = _stream_ptr(stream, dev)
-    if workspace is None:
-        need = exq_fp4_gemm_workspace_size(a, w)
-        if need:
-            workspace = _fp4_workspace(need, dev, stream, handle, where)
-    ws, n = _space(workspace, where)
-    _check(_lib.exq_fp4_gemm(a._ref, w._ref, out.data_ptr(), ws, n, handle), where)
+    _here(where, dev, w.device)
+    out = _result(out, a.rows, w.rows, dev, a._codes if a._codes is not None else a._buf, stream, where)
+    _check(_lib.exq_fp4_gemm(a._ref, w._ref, out.data_ptr(), _stream_ptr(stream, dev)), where)
     return out
 
 
@@ -885,18 +894,16 @@ def exq_fp4_gemv(w: Fp4Matrix, x, out=None, workspace=None, stream=None):
     import torch
     where = "exq_fp4_gemv"
     dev = w.device
-    _here(where, dev, x.get_device(), dev if out is None else out.get_device(), dev if workspace is None else workspace.get_device())
-    _fp16_rows(x, where)
-    M = x.shape[0]
-    if out is None:
-        out = _empty((M, w.rows), torch.float16, x.device, stream)
-    _fp16_rows(out, where)
-    if x.shape[1] != w.K or out.shape != (M, w.rows):
+    _here(where, dev, x.get_device())
+    if not _is_rows(x, torch.float16) or x.shape[1] != w.K:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    M = x.shape[0]
+    out = _result(out, M, w.rows, dev, x, stream, where)
     handle = _stream_ptr(stream, dev)
     if workspace is None:
-        workspace = _fp4_workspace(exq_fp4_gemv_workspace_size(w, M), dev, stream, handle, where)
-    ws, n = _space(workspace, where)
+        ws, n = _fp4_workspace(_lib.exq_fp4_gemv_workspace_size(w._ref, M), dev, stream, handle, where)
+    else:
+        ws, n = _space(workspace, dev, where)
     _check(_lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle), where)
     return out
 
@@ -948,26 +955,25 @@ def exq_moe(layer: MoeLayer, x, ids=None, weights=None, out=None, workspace=None
     import torch
     where = "exq_moe"
     dev = layer.device
-    _here(where, dev, x.get_device(), *(t.get_device() for t in (ids, weights, out, workspace) if t is not None))
-    _fp16_rows(x, where)
+    _here(where, dev, x.get_device())
+    if not _is_rows(x, torch.float16) or x.shape[1] != layer.D or (layer.router is None and (ids is None or weights is None)):
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
     T = x.shape[0]
-    if layer.router is None and (ids is None or weights is None):
-        raise ExqError(EXQ_ERR_INVALID_ARG, where)
-    if ids is None:
-        ids = _empty((T, layer.top_k), torch.int32, x.device, stream)
-    if weights is None:
-        weights = _empty((T, layer.top_k), torch.float32, x.device, stream)
-    if out is None:
-        out = _empty((T, layer.D), torch.float16, x.device, stream)
-    _fp16_rows(out, where)
     shape = (T, layer.top_k)
-    if (x.shape[1] != layer.D or out.shape != x.shape or ids.shape != shape or weights.shape != shape or ids.dtype != torch.int32
-            or weights.dtype != torch.float32 or not ids.is_contiguous() or not weights.is_contiguous()):
+    if ids is None:
+        ids = _empty(shape, torch.int32, x.device, stream)
+    elif ids.dtype is not torch.int32 or ids.shape != shape or not ids.is_contiguous() or ids.get_device() != dev:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    if weights is None:
+        weights = _empty(shape, torch.float32, x.device, stream)
+    elif weights.dtype is not torch.float32 or weights.shape != shape or not weights.is_contiguous() or weights.get_device() != dev:
+        raise ExqError(EXQ_ERR_INVALID_ARG, where)
+    out = _result(out, T, layer.D, dev, x, stream, where)
     handle = _stream_ptr(stream, dev)
     if workspace is None:
-        workspace = _fp4_workspace(exq_moe_workspace_size(layer, T), dev, stream, handle, where)
-    ws, n = _space(workspace, where)
+        ws, n = _fp4_workspace(_lib.exq_moe_workspace_size(layer._ref, T), dev, stream, handle, where)
+    else:
+        ws, n = _space(workspace, dev, where)
     _check(_lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle), where)
     return out, ids, weights
 

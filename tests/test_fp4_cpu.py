@@ -94,7 +94,7 @@ def test_gemm_validates_on_host(exq):
     bad = exq.EXQ_ERR_INVALID_ARG
 
     def call(a={}, w={}, y=0x50000):
-        return _call("exq_fp4_gemm", _matrix(exq, **{"rows": 5, **a}), _matrix(exq, **w), y, None, 0, None)
+        return _call("exq_fp4_gemm", _matrix(exq, **{"rows": 5, **a}), _matrix(exq, **w), y, None)
 
     for kw in MATRIX_BAD:
         assert call(a=kw) == bad and call(w=kw) == bad, kw

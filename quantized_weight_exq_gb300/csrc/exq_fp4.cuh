@@ -19,6 +19,24 @@ __host__ __device__ constexpr int fp4_tile_k(int fmt) { return 4 * fp4_block(fmt
 // byte of row r (0..127) in a scale tile; block j of the four is byte + j
 __host__ __device__ constexpr int fp4_tile_byte(int r) { return (r & 31) * 16 + (r >> 5) * 4; }
 
+// A launch that may begin while the one before it on the stream ends (a
+// programmatic dependent): its kernel calls griddepcontrol.wait before it reads
+// or writes memory.
+template <typename... P, typename... A>
+exq_status launch_dependent(void (*fn)(P...), int blocks, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- numbers
 
 // the two e2m1 codes of byte B of w, as fp16 (exact; the even k in the low half)

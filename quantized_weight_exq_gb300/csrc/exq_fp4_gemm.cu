@@ -8,24 +8,30 @@
 // L2 were that kernel's bound (220 us at 2048 x 28672 x 8192). The pairs stay
 // and take tile after tile.
 //
-//   warp 0      brings the codes (128-byte rows, 128-byte swizzle) and the
-//               scale tiles as they lie in memory (512 bytes for 128 rows x 4
-//               blocks).
-//   warps 2-5   write the scales to tensor memory, a place for each stage. The
-//               tensor core's own copy (tcgen05.cp) does not do here: one takes
-//               55 clocks whatever its size, the 12 of a stage 660, the four
-//               MMAs 512. From registers a stage takes 4 warps under 320.
+//   warp 0      brings the codes (128-byte rows, 128-byte swizzle),
+//   warp 18     the scale tiles as they lie in memory (512 bytes for 128 rows x
+//               4 blocks): one warp that issues all five copies of a stage is
+//               slower than the MMAs.
+//   warps 2-9   write the scales to tensor memory, a place for each stage, four
+//               warps every second one. The tensor core's own copy
+//               (tcgen05.cp) does not do here: one takes 55 clocks whatever its
+//               size, the 12 of a stage 660, the four MMAs 512. From registers
+//               a stage takes four warps 320, from barrier to barrier 500.
 //   warp 1      of the pair's first CTA: four MMAs (K = 64) a stage, fp32 sums
 //               in the tensor memory of both CTAs.
-//   warps 6-13  epilogue: 32 rows x 128 columns each. The sums fill half of
+//   warps 10-17 epilogue: 32 rows x 128 columns each. The sums fill half of
 //               tensor memory and the scales a part of the rest, so there is
 //               one set of sums only: the warps take theirs as packed fp16 into
 //               registers at once, let the next tile's MMAs begin, and store
 //               while those run.
 //
-// Up to 128 rows of a change places with w: its rows are the MMA's 256, a's its
-// N (32 .. 128 columns). The product is then bound by the codes of w; a stage
-// is at most 28 KB and its MMAs short, so that more of them are on their way.
+// Up to 128 rows of a change places with w: a CTA alone has 128 of its rows and
+// all of a's as the MMA's N (16 .. 128 columns). The product is then bound by
+// the codes of w: single MMAs of few columns take 46 clocks, a pair's 128
+// however few (64 x 8192 x 8192 took 15 us by pairs).
+//
+// The launch may begin while the one before it ends (its set-up takes 1 us):
+// nothing is read or written before griddepcontrol.wait.
 #include <algorithm>
 #include <cstring>
 
@@ -38,7 +44,7 @@ __device__ unsigned g_fp4_gemm_err;
 
 constexpr int kTile = 256;   // rows and columns of a pair's tile
 constexpr int BK = 256;      // k of a stage: four MMAs
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 19 * 32;
 
 constexpr int kCodes = 128 * BK / 2;  // of 128 rows
 constexpr int kScaleTiles = 2048;     // the scale tiles of 128 rows x 256 k: 4 (E4M3) or 2 (E8M0)
@@ -51,7 +57,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 // way from one stage's MMAs over the warps that write scales to another's
 // took 1 us.
 constexpr uint32_t kTmemCols = 512;
-// SWAP: a's rows are the MMA's N
+// SWAP: a's rows are the MMA's N; one CTA has a tile, not two
 __host__ __device__ constexpr uint32_t scales_at(bool swap) { return swap ? 128 : 256; }
 __host__ __device__ constexpr uint32_t scale_cols(bool swap) { return swap ? 32 : 48; }
 __host__ __device__ constexpr int most_stages(bool swap) { return swap ? 10 : 5; }
@@ -59,7 +65,7 @@ constexpr int kMaxStages = most_stages(true);
 static_assert(scales_at(false) + most_stages(false) * scale_cols(false) <= kTmemCols, "tensor memory budget");
 static_assert(scales_at(true) + most_stages(true) * scale_cols(true) <= kTmemCols, "tensor memory budget");
 
-// One stage of a CTA: 128 rows of A, its half of B's rows, A's scale tiles, all of B's.
+// One stage of a CTA: 128 rows of A, B's rows or its half of them, A's scale tiles, all of B's.
 struct Stage {
   int b_rows, bytes, n;
   __host__ __device__ constexpr int off_sa() const { return kCodes + b_rows * (BK / 2); }
@@ -67,12 +73,12 @@ struct Stage {
 };
 __host__ __device__ constexpr Stage stage_of(bool swap, int n_columns) {
   Stage s{};
-  s.b_rows = n_columns / 2;
+  s.b_rows = swap ? n_columns : n_columns / 2;
   s.bytes = s.off_sb() + (swap ? 1 : 2) * kScaleTiles;
   s.n = kRing / s.bytes < most_stages(swap) ? kRing / s.bytes : most_stages(swap);
   return s;
 }
-static_assert(stage_of(false, 256).n == 5 && stage_of(false, 256).bytes % 1024 == 0 && stage_of(true, 32).bytes % 1024 == 0, "stages");
+static_assert(stage_of(false, 256).n == 5 && stage_of(false, 256).bytes % 1024 == 0 && stage_of(true, 16).bytes % 1024 == 0, "stages");
 
 struct Args {
   const uint8_t *sa, *sb;  // scale tiles of the MMA's A and B
@@ -82,8 +88,9 @@ struct Args {
   int a_tiles, b_tiles;    // tiles of 128 rows
   int k_tiles;             // scale tiles along K
   int k_units;
-  int a_pairs, n_tiles;    // tiles of 256 rows of A, and of the product in all
-  int n_columns;           // of a tile: 256, or (SWAP) all of B, rounded up to 32
+  int a_rows, n_tiles;     // tiles of A (of 256 rows, SWAP: 128), and of the product in all
+  int n_columns;           // of a tile: 256, or (SWAP) all of B, rounded up to 16
+  int whole_sectors;       // y's rows begin on 32-byte boundaries
   int wait_limit, starve;
 };
 
@@ -93,31 +100,36 @@ __device__ __forceinline__ uint64_t codes_desc(uint32_t addr) {
          (1ull << 46) | (2ull << 61);
 }
 
-// instruction descriptor of the block-scaled kinds: e2m1 operands, K-major, 256 x n
-__host__ __device__ constexpr uint32_t idesc_of(int fmt, int n) {
+// instruction descriptor of the block-scaled kinds: e2m1 operands, K-major, m x n
+__host__ __device__ constexpr uint32_t idesc_of(int fmt, int m, int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((fmt == EXQ_FP4_E8M0 ? 1u : 0u) << 23) |
-         (static_cast<uint32_t>(kTile >> 4) << 24);
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-template <int FMT>
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                         uint32_t accumulate) {
-  if constexpr (FMT == EXQ_FP4_E4M3)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+// CTAS: how many work on one tile
+template <int FMT, int CTAS>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           uint32_t accumulate) {
+#define EXQ_MMA(ctas, kind)                                                                                         \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                    \
+               "tcgen05.mma.cta_group::" ctas ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),     \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                                        \
+               : "memory")
+  if constexpr (FMT == EXQ_FP4_E4M3 && CTAS == 2) EXQ_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (FMT == EXQ_FP4_E4M3) EXQ_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (CTAS == 2) EXQ_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  else EXQ_MMA("1", "mxf4.block_scale.scale_vec::2X");
+#undef EXQ_MMA
+}
+
+// arrives at the barrier, in both CTAs of a pair (mask 3), when the MMAs issued so far are over
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t bar, uint16_t mask = 3) {
+  if constexpr (CTAS == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"(mask) : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
-}
-
-// arrives at the barrier in both CTAs (mask 3) when the MMAs issued so far are over
-__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask = 3) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-               ::"r"(bar), "h"(mask) : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Arrives at the first CTA's barrier. What it tells of lies in tensor memory
@@ -125,7 +137,9 @@ __device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask = 3) {
 // shared memory by copies that a barrier has seen: no ordinary store has to be
 // ordered before it, and a release to the whole cluster, which drains them,
 // made the product more than twice as slow (367 us, 170 without).
+template <int CTAS>
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
+  if constexpr (CTAS == 1) return mbar_arrive(bar);
   asm volatile(
       "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar) : "memory");
@@ -185,10 +199,12 @@ struct Turn {  // counts stages, and the parity of their barriers
 };
 
 template <int FMT, bool SWAP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ Args p) {
   constexpr int kTilesUnit = BK / fp4_tile_k(FMT);
+  constexpr int CTAS = SWAP ? 1 : 2;
+  constexpr int kARows = 128 * CTAS;  // of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
@@ -201,44 +217,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int rank = blockIdx.x % CTAS, pair = blockIdx.x / CTAS, pairs = gridDim.x / CTAS;
   const int n_columns = SWAP ? p.n_columns : kTile;
   const Stage stage = SWAP ? stage_of(true, n_columns) : stage_of(false, kTile);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), 2);  // codes and scales
       mbar_init(smem_u32(&empty[s]), 1);
-      mbar_init(smem_u32(&ready[s]), 8);
+      mbar_init(smem_u32(&ready[s]), 4 * CTAS);
     }
     mbar_init(smem_u32(dfull), 1);
-    mbar_init(smem_u32(dempty), 16);
+    mbar_init(smem_u32(dempty), 8 * CTAS);
     mbar_init(smem_u32(done), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  if (warp == 0 && elect_one()) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&ma)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mb)) : "memory");
   }
+  if (warp == 1) {
+    if constexpr (CTAS == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if constexpr (CTAS == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ copies
+    // ------------------------------------------------------------ codes
     const bool leader = elect_one();
     int issued = 0;
-    if (!p.starve) {  // test hook: a starved producer issues nothing
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!p.starve) {  // test hook: starved producers issue nothing
       Turn turn;
       bool ok = true;
       for (int t = pair; t < p.n_tiles && ok; t += pairs) {
-        const int bt = t / p.a_pairs, at = t - bt * p.a_pairs;
-        const int a_tile = 2 * at + rank, b_parts = SWAP ? 1 : min(2, p.b_tiles - 2 * bt);
-        const bool has_a = a_tile < p.a_tiles;  // (else the rows are past the matrix: zero codes, any scales)
+        const int bt = t / p.a_rows, at = t - bt * p.a_rows;
+        const int a_row = at * kARows + rank * 128, b_row = bt * kTile + rank * stage.b_rows;
         for (int u = 0; u < p.k_units; ++u) {
           if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
             ok = false;
@@ -246,15 +274,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (leader) {
             const uint32_t st = smem_u32(smem) + turn.i * stage.bytes, bar = smem_u32(&full[turn.i]);
-            const uint32_t sbytes = min(kTilesUnit, p.k_tiles - u * kTilesUnit) * 512;
-            mbar_expect_tx(bar, kCodes + stage.b_rows * (BK / 2) + ((has_a ? 1 : 0) + b_parts) * sbytes);
-            tma_load_2d(st, &ma, u * (BK / 2), a_tile * 128, bar);
-            tma_load_2d(st + kCodes, &mb, u * (BK / 2), bt * kTile + rank * stage.b_rows, bar);
-            const size_t along = static_cast<size_t>(u) * kTilesUnit;
-            if (has_a) bulk_load(st + stage.off_sa(), p.sa + (static_cast<size_t>(a_tile) * p.k_tiles + along) * 512, sbytes, bar);
-            for (int h = 0; h < b_parts; ++h)
-              bulk_load(st + stage.off_sb() + h * kScaleTiles,
-                        p.sb + (static_cast<size_t>(2 * bt + h) * p.k_tiles + along) * 512, sbytes, bar);
+            mbar_expect_tx(bar, kCodes + stage.b_rows * (BK / 2));
+            tma_load_2d(st, &ma, u * (BK / 2), a_row, bar);
+            tma_load_2d(st + kCodes, &mb, u * (BK / 2), b_row, bar);
           }
           __syncwarp();
           turn.next(stage.n);
@@ -266,11 +288,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = max(0, issued - stage.n); i < issued; ++i)
       for (int r = 0; r < p.wait_limit; ++r)
         if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % stage.n]), (i / stage.n) & 1))) break;
+  } else if (warp == 18) {
+    // ------------------------------------------------------------ scales
+    const bool leader = elect_one();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.starve) {
+      Turn turn;
+      bool ok = true;
+      for (int t = pair; t < p.n_tiles && ok; t += pairs) {
+        const int bt = t / p.a_rows, at = t - bt * p.a_rows;
+        const int a_tile = CTAS * at + rank, b_parts = SWAP ? 1 : min(2, p.b_tiles - 2 * bt);
+        const bool has_a = a_tile < p.a_tiles;  // (else the rows are past the matrix: zero codes, any scales)
+        const uint8_t* sa = p.sa + static_cast<size_t>(a_tile) * p.k_tiles * 512;
+        const uint8_t* sb = p.sb + static_cast<size_t>(2 * bt) * p.k_tiles * 512;
+        const uint8_t* sb2 = sb + static_cast<size_t>(p.k_tiles) * 512;
+        for (int u = 0; u < p.k_units; ++u) {
+          if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t st = smem_u32(smem) + turn.i * stage.bytes, bar = smem_u32(&full[turn.i]);
+            const uint32_t bytes = min(kTilesUnit, p.k_tiles - u * kTilesUnit) * 512;
+            mbar_expect_tx(bar, ((has_a ? 1 : 0) + b_parts) * bytes);
+            if (has_a) bulk_load(st + stage.off_sa(), sa, bytes, bar);
+            bulk_load(st + stage.off_sb(), sb, bytes, bar);
+            if (!SWAP && b_parts == 2) bulk_load(st + stage.off_sb() + kScaleTiles, sb2, bytes, bar);
+          }
+          sa += kTilesUnit * 512;
+          sb += kTilesUnit * 512;
+          sb2 += kTilesUnit * 512;
+          __syncwarp();
+          turn.next(stage.n);
+        }
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs, by the first CTA
     if (rank == 0) {
       const bool leader = elect_one();
-      const uint32_t idesc = idesc_of(FMT, n_columns);
+      const uint32_t idesc = idesc_of(FMT, kARows, n_columns);
       constexpr uint32_t kTileColsB = SWAP ? 4 : 8;
       Turn turn;
       uint32_t tile_parity = 1;
@@ -294,32 +351,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
               if (j >= n_k) break;
               if constexpr (FMT == EXQ_FP4_E4M3)
-                mma_pair<FMT>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + kTileColsB * j, (u | j) != 0);
+                mma_scaled<FMT, CTAS>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + kTileColsB * j, (u | j) != 0);
               else  // two scales of the tile's four: byte 0 or 2 of each word
-                mma_pair<FMT>(tmem, ad + 2 * j, bd + 2 * j, (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc, sa + 4 * (j >> 1),
+                mma_scaled<FMT, CTAS>(tmem, ad + 2 * j, bd + 2 * j, (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc, sa + 4 * (j >> 1),
                               sb + kTileColsB * (j >> 1), (u | j) != 0);
             }
-            commit_pair(smem_u32(&empty[turn.i]));
+            commit<CTAS>(smem_u32(&empty[turn.i]));
           }
           __syncwarp();
           turn.next(stage.n);
         }
-        if (leader) commit_pair(smem_u32(dfull));
+        if (leader) commit<CTAS>(smem_u32(dfull));
         __syncwarp();
       }
       // the MMAs are over before tensor memory is given back
-      if (leader) commit_pair(smem_u32(done), 1);
+      if (leader) commit<CTAS>(smem_u32(done), 1);
       __syncwarp();
       for (int r = 0; r < p.wait_limit; ++r)
         if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(done), 0))) break;
     }
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     // ------------------------------------------------------------ scales to tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Turn turn;
+    // Stages by their place, not by their turn: four warps see every phase of the barriers they wait on. (A wait tells a
+    // phase from the one before, not from the one before that, and copies may land out of order.)
+    const int group = (warp - 2) >> 2;
     bool ok = true;
     for (int t = pair; t < p.n_tiles && ok; t += pairs) {
       for (int u = 0; u < p.k_units; ++u) {
+        if ((turn.i & 1) != group) {
+          turn.next(stage.n);
+          continue;
+        }
         if (!mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
           ok = false;
           break;
@@ -346,57 +410,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(smem_u32(&ready[turn.i]));
+        if (lane == 0) arrive_first<CTAS>(smem_u32(&ready[turn.i]));
         turn.next(stage.n);
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, half = (warp - 6) >> 2;
-    const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (n_columns / 2);
+    const int quarter = warp & 3, half = (warp - 10) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t parity = 0;
     for (int t = pair; t < p.n_tiles; t += pairs) {
-      const int bt = t / p.a_pairs, at = t - bt * p.a_pairs;
+      const int bt = t / p.a_rows, at = t - bt * p.a_rows;
       if (!mbar_wait_warp(smem_u32(dfull), parity, abort_flag, p.wait_limit, &g_fp4_gemm_err) || *abort_flag) break;
       parity ^= 1u;
       tc_fence_after();
-      const int row = at * kTile + rank * 128 + quarter * 32 + lane;
+      const int row = at * kARows + rank * 128 + quarter * 32 + lane;
       if constexpr (SWAP) {
+        // groups of 16 columns (rows of y), the two halves of the warps in turn
         uint32_t v[4][16];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (16 * c < n_columns / 2) tmem_ld16(from + 16 * c, v[c]);
+          if ((2 * c + half) * 16 < n_columns) tmem_ld16(tmem + lanes + (2 * c + half) * 16, v[c]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(smem_u32(dempty));
+        if (lane == 0) arrive_first<CTAS>(smem_u32(dempty));
         if (row < p.A) {
-          uint16_t* dst = p.y + static_cast<size_t>(half * (n_columns / 2)) * p.A + row;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int m0 = (2 * c + half) * 16;
+            uint16_t* dst = p.y + static_cast<size_t>(m0) * p.A + row;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (16 * c + j < n_columns / 2 && half * (n_columns / 2) + 16 * c + j < p.B)
-                dst[static_cast<size_t>(16 * c + j) * p.A] = __half_as_ushort(__float2half_rn(__uint_as_float(v[c][j]) * p.factor));
+            for (int j = 0; j < 16; ++j) {
+              if (m0 + j < p.B) *dst = __half_as_ushort(__float2half_rn(__uint_as_float(v[c][j]) * p.factor));
+              dst += p.A;
+            }
+          }
         }
       } else {
         uint32_t h[64];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
-          tmem_ld32(from + 32 * c, r);
+          tmem_ld32(tmem + lanes + half * 128 + 32 * c, r);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             h[16 * c + j] = pack_half2(__uint_as_float(r[2 * j]) * p.factor, __uint_as_float(r[2 * j + 1]) * p.factor);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(smem_u32(dempty));
+        if (lane == 0) arrive_first<CTAS>(smem_u32(dempty));
         const int n0 = bt * kTile + half * 128;
         if (row < p.A) {
           uint16_t* dst = p.y + static_cast<size_t>(row) * p.B + n0;
+          if (p.whole_sectors) {  // 32 bytes at a time: a lane's stores fill sectors (with 16 they take twice as long)
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (n0 + 8 * j < p.B) *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+              if (n0 + 16 * j < p.B)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * j), "r"(h[8 * j]),
+                             "r"(h[8 * j + 1]), "r"(h[8 * j + 2]), "r"(h[8 * j + 3]), "r"(h[8 * j + 4]), "r"(h[8 * j + 5]),
+                             "r"(h[8 * j + 6]), "r"(h[8 * j + 7]) : "memory");
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (n0 + 8 * j < p.B) *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+          }
         }
       }
     }
@@ -405,10 +482,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the other CTA's tensor memory and barriers are in use until here
+  if constexpr (CTAS == 2) cluster_sync();  // the other CTA's tensor memory and barriers are in use until here
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if constexpr (CTAS == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -420,11 +500,11 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
                            cudaStream_t stream) {
   const bool swap = x.rows <= 128;
   const exq_fp4_matrix &a = swap ? w : x, &b = swap ? x : w;
-  const int n_columns = swap ? div_up(x.rows, 32) * 32 : kTile;
+  const int n_columns = swap ? div_up(x.rows, 16) * 16 : kTile;
   CUtensorMap ma, mb;
   if (!encode_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K / 2, a.rows, a.K / 2, BK / 2, 128,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, b.K / 2, b.rows, b.K / 2, BK / 2, n_columns / 2,
+      !encode_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, b.K / 2, b.rows, b.K / 2, BK / 2, swap ? n_columns : kTile / 2,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_128B))
     return EXQ_ERR_CUDA;
   Args p{};
@@ -439,9 +519,10 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
   p.b_tiles = div_up(b.rows, 128);
   p.k_tiles = div_up(a.K, fp4_tile_k(a.format));
   p.k_units = div_up(a.K, BK);
-  p.a_pairs = div_up(a.rows, kTile);
-  p.n_tiles = p.a_pairs * div_up(b.rows, kTile);
+  p.a_rows = div_up(a.rows, swap ? 128 : kTile);
+  p.n_tiles = p.a_rows * div_up(b.rows, kTile);
   p.n_columns = n_columns;
+  p.whole_sectors = b.rows % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31u) == 0;
   const int starve = testing_starve_rounds();
   p.wait_limit = starve > 0 ? starve : kFp4WaitLimit;
   p.starve = starve > 0 ? 1 : 0;
@@ -455,10 +536,18 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
       }))
     return EXQ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * std::min(p.n_tiles, std::max(sms / 2, 1)));
+  cfg.gridDim = dim3(swap ? std::min(p.n_tiles, sms) : 2 * std::min(p.n_tiles, std::max(sms / 2, 1)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = swap ? 1 : 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fn, ma, mb, p) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
 }
 

@@ -12,6 +12,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Both kernels are launched while the one before them may still run, and let
+// the next do so; nothing is read or written before it is over.
+__device__ __forceinline__ void begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // magnitude (1..7) -> the tie between it and the code below
 __device__ __forceinline__ float tie_below(int c) {
   // 0.25 0.75 1.25 1.75 2.5 3.5 5
@@ -60,8 +67,9 @@ struct Walk {
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __restrict__ x, uint2* __restrict__ codes,
                                                             uint32_t* __restrict__ scales, int rows, int K, float f,
-                                                            float inv6f) {
+                                                            float inv6f, bool wide) {
   constexpr int kPer = fp4_tile_k(FMT) / 16;  // threads of one scale word: 4 or 8
+  begin();
   const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
   const long long padded = static_cast<long long>((rows + 127) / 128) * 128;
   const int per_row = words * kPer;
@@ -76,9 +84,16 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
     const bool in = row < rows && piece < pieces;
     uint32_t h[8] = {};
     if (in) {
-      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "=r"(h[4]), "=r"(h[5]), "=r"(h[6]), "=r"(h[7])
-                   : "l"(x + (row * pieces + piece) * 16));
+      const uint16_t* src = x + (row * pieces + piece) * 16;
+      if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]), "=r"(h[4]), "=r"(h[5]), "=r"(h[6]), "=r"(h[7])
+                     : "l"(src));
+      } else {
+        const uint4 p = __ldcs(reinterpret_cast<const uint4*>(src)), q = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
+        h[0] = p.x; h[1] = p.y; h[2] = p.z; h[3] = p.w;
+        h[4] = q.x; h[5] = q.y; h[6] = q.z; h[7] = q.w;
+      }
     }
     // the largest magnitude, as bits: they order as the numbers do, infinity and NaN above
     uint32_t m2 = 0u;
@@ -176,7 +191,7 @@ struct Codes32 {
       s = __ldg(tile + ((at.row >> 7) * words + (at.piece >> 2)) * 512 + (at.piece & 3));
     to = out + 32 * i;
   }
-  __device__ __forceinline__ void store(float f) const {
+  __device__ __forceinline__ void store(float f, bool wide) const {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -194,8 +209,13 @@ struct Codes32 {
           o[4 * j + k] = *reinterpret_cast<const uint32_t*>(&y);
         }
       }
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * h), "r"(o[0]), "r"(o[1]), "r"(o[2]),
-                   "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+      if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * h), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                     "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+      } else {
+        __stcs(reinterpret_cast<uint4*>(to + 16 * h), make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4*>(to + 16 * h) + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      }
     }
   }
 };
@@ -205,7 +225,8 @@ struct Codes32 {
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint4* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
-                                                              uint16_t* __restrict__ out, int rows, int K, float f) {
+                                                              uint16_t* __restrict__ out, int rows, int K, float f, bool wide) {
+  begin();
   const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
   const int pieces = K / 32;
   const long long total = static_cast<long long>(rows) * pieces, stride = static_cast<long long>(gridDim.x) * kThreads;
@@ -218,10 +239,13 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint4* __res
     const bool two = i + stride < total;
     if (two) b.load(codes, scales, out, i + stride, at, words);
     at.next();
-    a.store(f);
-    if (two) b.store(f);
+    a.store(f, wide);
+    if (two) b.store(f, wide);
   }
 }
+
+// whether rows of 32-byte pieces from here can be read and written by the piece (16 bytes are what is asked of callers)
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 int blocks_for(long long threads, int sms) {
   const long long b = (threads + kThreads - 1) / kThreads;
@@ -234,17 +258,15 @@ exq_status launch_fp4_quantize(const uint16_t* x, const exq_fp4_matrix& m, int s
   const int words = (m.K + fp4_tile_k(m.format) - 1) / fp4_tile_k(m.format);
   const long long threads = static_cast<long long>((m.rows + 127) / 128) * 128 * words * (fp4_tile_k(m.format) / 16);
   auto fn = m.format == EXQ_FP4_E4M3 ? quantize_kernel<EXQ_FP4_E4M3> : quantize_kernel<EXQ_FP4_E8M0>;
-  fn<<<blocks_for(threads, sms), kThreads, 0, stream>>>(
-      x, reinterpret_cast<uint2*>(m.codes), reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K,
-      m.factor, 1.f / (6.f * m.factor));
-  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+  return launch_dependent(fn, blocks_for(threads, sms), kThreads, 0, stream, x, reinterpret_cast<uint2*>(m.codes),
+                          reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K, m.factor, 1.f / (6.f * m.factor), aligned32(x));
 }
 
 exq_status launch_fp4_dequantize(const exq_fp4_matrix& m, uint16_t* out, int sms, cudaStream_t stream) {
   auto fn = m.format == EXQ_FP4_E4M3 ? dequantize_kernel<EXQ_FP4_E4M3> : dequantize_kernel<EXQ_FP4_E8M0>;
-  fn<<<blocks_for(static_cast<long long>(m.rows) * (m.K / 32), sms), kThreads, 0, stream>>>(
-      reinterpret_cast<const uint4*>(m.codes), m.scales, out, m.rows, m.K, m.factor);
-  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+  return launch_dependent(fn, blocks_for(static_cast<long long>(m.rows) * (m.K / 32), sms), kThreads, 0, stream,
+                          reinterpret_cast<const uint4*>(m.codes), static_cast<const uint8_t*>(m.scales), out, m.rows, m.K,
+                          m.factor, aligned32(out));
 }
 
 }  // namespace exq

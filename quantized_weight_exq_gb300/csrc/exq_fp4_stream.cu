@@ -221,6 +221,8 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
 // expert layer's routing (the others).
 template <int FMT, bool TILES, int TT>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (not sooner: the launch after this reads weights, which may come from the one before this, without another wait)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (static_cast<int>(blockIdx.x) < a.split_blocks) {
     if (!TILES && blockIdx.x == 0)
@@ -260,26 +262,15 @@ exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t st
             : p.T == 1 ? (e4m3 ? prepare_kernel<A, false, 1> : prepare_kernel<B, false, 1>)
             : p.T <= 4 ? (e4m3 ? prepare_kernel<A, false, 4> : prepare_kernel<B, false, 4>)
                        : (e4m3 ? prepare_kernel<A, false, 16> : prepare_kernel<B, false, 16>);
-  fn<<<p.split_blocks + (p.router ? p.E : 0), kPrepareThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+  return launch_dependent(fn, p.split_blocks + (p.router ? p.E : 0), kPrepareThreads, 0, stream, p);
 }
 
 exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
   p.split_blocks = split_blocks_for(format, false, p.T, p.D);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.split_blocks);
-  cfg.blockDim = dim3(kPrepareThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  auto fn = format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>;
-  return cudaLaunchKernelEx(&cfg, fn, p) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+  return launch_dependent(format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>, p.split_blocks,
+                          kPrepareThreads, 0, stream, p);
 }
 
-// (each a programmatic dependent of the launch before it)
 template <int MODE>
 exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a,
                          int ctas, int device, cudaStream_t stream) {
@@ -289,17 +280,7 @@ exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal) == cudaSuccess;
       }))
     return EXQ_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(fp4s::kThreads);
-  cfg.dynamicSmemBytes = kSmemTotal;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, m0, m1, mx, a) == cudaSuccess ? EXQ_OK : EXQ_ERR_CUDA;
+  return launch_dependent(fn, ctas, fp4s::kThreads, kSmemTotal, stream, m0, m1, mx, a);
 }
 
 bool encode_codes(CUtensorMap* map, const void* codes, uint64_t rows, int K, int box_rows) {

@@ -132,7 +132,9 @@ def _check_product(y, a, w, extra_roundings):
 GEMM_SHAPES = [(1, 8, 32), (1, 128, 64), (5, 8, 96), (128, 256, 256), (129, 264, 288), (300, 1000, 2080), (64, 512, 4096), (17, 1032, 160),
                (513, 136, 1056), (256, 384, 64), (2, 2048, 5152), (390, 520, 512), (128, 8, 8224), (1000, 24, 288),
                # tiles of 256 x 256: fewer than the SM pairs and more, the last ones ragged
-               (2000, 2056, 96), (1030, 4104, 544), (300, 9000, 64), (2300, 2312, 352), (257, 20000, 32), (6000, 1288, 1312)]
+               (2000, 2056, 96), (1030, 4104, 544), (300, 9000, 64), (2300, 2312, 352), (257, 20000, 32), (6000, 1288, 1312),
+               # up to 128 rows: more tiles of 128 columns than SMs, odd counts of stages
+               (128, 40008, 1312), (7, 20488, 2336), (100, 30000, 800), (33, 19464, 256)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -246,6 +248,36 @@ def test_large_product(env, fmt):
     tol = 0.5 * ulp16(ref) * (1 + 2.0 ** -8) + (K / 16 + 16) * 2.0 ** -23 * size
     err = np.abs(y.cpu().numpy().astype(np.float64) - ref)
     assert (err[np.abs(ref) < 65504] <= tol[np.abs(ref) < 65504]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_every_pointer_on_a_16_byte_boundary(env, fmt):
+    # contiguous views that begin 16 bytes into their memory
+    exq, torch = env
+    rng = np.random.default_rng(12)
+
+    def off(t):
+        n = 16 // t.element_size()
+        buf = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        view = buf[n:].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 32 == 16
+        return view
+
+    for M, N, K in ((5, 40, 96), (300, 264, 416)):
+        x = _activations(rng, M, K, 1)
+        w, wv = _quantised(exq, torch, rng, N, K, fmt)
+        w = exq.Fp4Matrix(off(w.codes), off(w.scales), fmt)
+        xd = off(torch.from_numpy(x).cuda())
+        q = exq.Fp4Matrix(off(torch.zeros(M, K // 2, dtype=torch.uint8, device="cuda")),
+                          off(torch.zeros(exq.exq_fp4_scale_bytes(fmt, M, K), dtype=torch.uint8, device="cuda")), fmt)
+        half = lambda *s: off(torch.zeros(s, dtype=torch.float16, device="cuda"))  # noqa: E731
+        codes, scales = _check_quantised(exq.exq_fp4_quantize(xd, fmt, out=q), x, fmt, 1.0)
+        values = O.fp4_values(codes, scales, fmt)
+        np.testing.assert_array_equal(exq.exq_fp4_dequantize(q, out=half(M, K)).cpu().numpy(), _f32_product(values, 1.0))
+        _check_product(exq.exq_fp4_gemm(q, w, out=half(M, N)), values, wv, 16)
+        rows = min(M, 16)
+        _check_product(exq.exq_fp4_gemv(w, off(xd[:rows]), out=half(rows, N)), x[:rows].astype(np.float64), wv, 16)
 
 
 def test_empty(env):

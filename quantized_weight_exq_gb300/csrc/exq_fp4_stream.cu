@@ -30,7 +30,7 @@ struct PrepareArgs {
   int T, D, E, top_k, renorm;
 };
 
-constexpr int kPrepareThreads = 256;
+constexpr int kPrepareThreads = 512;
 
 // Rows as eight 4-bit rows each (see exq_fp4_stream.cuh): a thread takes 8
 // values, the 2 or 4 of a block find its scale together, and those of a scale
@@ -124,11 +124,12 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
   for (int k = threadIdx.x * 8; k < a.D; k += kPrepareThreads * 8) {
     const uint4 w = __ldg(reinterpret_cast<const uint4*>(wr + k));
     const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+    uint4 x[TT];  // all on their way at once (rows past the last are the last)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) x[t] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(min(t, a.T - 1)) * a.D + k));
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      if (t >= a.T) break;
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.D + k));
-      const uint32_t xv[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t xv[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&wv[j]));
@@ -175,7 +176,7 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
       const unsigned b = v[i] != v[i] ? 0xFF800000u : v[i] == 0.f ? 0u : __float_as_uint(v[i]);
       keys[i] = !there ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
     }
-    float top = 0.f, total = 0.f, mine = 0.f;
+    float mine = -INFINITY;  // lane j: the j-th logit
     for (int j = 0; j < a.top_k; ++j) {
       unsigned key = 0u;
 #pragma unroll
@@ -196,24 +197,23 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
         if (32 * i + lane == at) { keys[i] = 0u; l = v[i]; }
       }
       l = __shfl_sync(0xffffffffu, l, at & 31);
-      if (j == 0) top = l;
-      const float p = expf(l - top);
-      if (lane == j) mine = p;
-      total += p;
+      if (lane == j) mine = l;
       if (lane == 0) a.ids[t * a.top_k + j] = static_cast<int>(at);
     }
+    const float top = __shfl_sync(0xffffffffu, mine, 0);
+    const float p = lane < a.top_k ? expf(mine - top) : 0.f;
+    float total = p;
     if (!a.renorm) {
-      float s = 0.f;
+      total = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         if (32 * i >= a.E) break;
-        if (32 * i + lane < a.E) s += expf(v[i] - top);
+        if (32 * i + lane < a.E) total += expf(v[i] - top);
       }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      total = s;
     }
-    if (lane < a.top_k) a.weights[t * a.top_k + lane] = mine / total;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane < a.top_k) a.weights[t * a.top_k + lane] = p / total;
   }
 }
 
@@ -247,6 +247,13 @@ __global__ void __launch_bounds__(kPrepareThreads) split_h_kernel(const __grid_c
 
 int div_up(int a, int b) { return (a + b - 1) / b; }
 
+// A small kernel runs on SMs whose shared memory is set up as the streaming
+// kernel wants it: else an SM has to fall idle before that one's CTA may start
+// (the experts' down product began 10 us after up's end, not 3).
+bool beside_streaming(void (*fn)(PrepareArgs)) {
+  return cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+}
+
 // blocks that split rows of D values, a thread 8 of them
 int split_blocks_for(int format, bool tiles, int rows, int D) {
   const int k = tiles ? fp4_tile_k(format) : kUnitK;
@@ -261,14 +268,17 @@ exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t st
             : !p.router ? (e4m3 ? prepare_kernel<A, false, 0> : prepare_kernel<B, false, 0>)
             : p.T == 1 ? (e4m3 ? prepare_kernel<A, false, 1> : prepare_kernel<B, false, 1>)
             : p.T <= 4 ? (e4m3 ? prepare_kernel<A, false, 4> : prepare_kernel<B, false, 4>)
+            : p.T <= 8 ? (e4m3 ? prepare_kernel<A, false, 8> : prepare_kernel<B, false, 8>)
                        : (e4m3 ? prepare_kernel<A, false, 16> : prepare_kernel<B, false, 16>);
+  if (!beside_streaming(fn)) return EXQ_ERR_CUDA;
   return launch_dependent(fn, p.split_blocks + (p.router ? p.E : 0), kPrepareThreads, 0, stream, p);
 }
 
 exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
   p.split_blocks = split_blocks_for(format, false, p.T, p.D);
-  return launch_dependent(format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>, p.split_blocks,
-                          kPrepareThreads, 0, stream, p);
+  auto fn = format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>;
+  if (!beside_streaming(fn)) return EXQ_ERR_CUDA;
+  return launch_dependent(fn, p.split_blocks, kPrepareThreads, 0, stream, p);
 }
 
 template <int MODE>
@@ -424,7 +434,12 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.act = l.act;
   a.counters = counters;
   a.part = reinterpret_cast<float*>(ws + plan.part);
-  if ((st = launch_stream<kUp>(fmt, mg, mu, mg, a, sms, device, stream)) != EXQ_OK) return st;
+  a.down_scales = l.down.scales;
+  a.down_stride = exq_fp4_scale_bytes(fmt, D, I);
+  a.down_row_tiles = div_up(D, kRows);
+  a.down_k_units = div_up(I, kUnitK);
+  a.down_k_tiles = div_up(I, fp4_tile_k(fmt));
+  if ((st = launch_stream<kUp>(fmt, mg, mu, md, a, sms, device, stream)) != EXQ_OK) return st;
 
   p.pieces = ws + plan.h_pieces;
   p.T = T * l.top_k;

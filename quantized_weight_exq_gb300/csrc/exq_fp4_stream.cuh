@@ -73,7 +73,7 @@ __host__ __device__ constexpr int piece_bytes(int fmt) { return 1024 + unit_tile
 // byte of the word of 8 codes at k (a multiple of 8, in the unit) of part p
 __host__ __device__ constexpr int piece_word(int p, int k) { return p * 128 + (((k / 32) ^ p) * 16) + (k % 32) / 2; }
 
-constexpr int kSmemTotal = 226 * 1024;
+constexpr int kSmemTotal = 222 * 1024;  // (room is left for a CTA of the small kernels before and after)
 constexpr int kRest = 20 * 1024;     // barriers, the experts' tables, sums, alignment
 constexpr int kRing = kSmemTotal - kRest;
 
@@ -107,8 +107,17 @@ struct Args {
   int rows, K, M;
   int row_tiles, k_units, k_tiles;
   int top_k, n_experts, act;
+  // up: the down product that follows
+  const uint8_t* down_scales;
+  size_t down_stride;
+  int down_row_tiles, down_k_units, down_k_tiles;
   int wait_limit, starve;
 };
+
+// Between the last of up's codes and the first of down's the SMs wait for sums,
+// for h's parts and for a set-up, some 10 us. Up's CTAs ask for down's first
+// units meanwhile, as far as L2 (this many a CTA: 44 MB in all).
+constexpr int kAhead = 16;
 
 // floats of one CTA's part of a tile: a value for each row, token (and matrix)
 __host__ __device__ constexpr int part_floats(int mode) { return kRows * kMaxTokens * (mode == kUp ? 2 : 1); }
@@ -235,6 +244,7 @@ __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned
   __syncthreads();
   if (tid == 0) {
     int n = 0;
+#pragma unroll
     for (int i = 0; i < kMaxExperts / 32; ++i) n += __popc(used[i]);
     e->n = n;
     e->most_tokens = 1;
@@ -245,15 +255,19 @@ __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned
     const int id = e->ids[i];
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_experts)) continue;
     int slot = __popc(used[id >> 5] & ((1u << (id & 31)) - 1u));
-    for (int w = 0; w < (id >> 5); ++w) slot += __popc(used[w]);
+#pragma unroll
+    for (int w = 0; w < kMaxExperts / 32; ++w) slot += w < (id >> 5) ? __popc(used[w]) : 0;
     e->expert[slot] = id;
     const int t = i / a.top_k;
     bool first = true;
-    for (int p = t * a.top_k; p < (t + 1) * a.top_k; ++p)
-      if (e->ids[p] == id) {
-        first = first && p >= i;
-        sum[r] += e->weight[p];
-      }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int p = min(t * a.top_k + j, kMaxPairs - 1);
+      const bool same = e->ids[p] == id && j < a.top_k;
+      const float w = e->weight[p];
+      first = first && (!same || p >= i);
+      sum[r] += same ? w : 0.f;
+    }
     if (first) {
       e->place[slot][t] = static_cast<uint8_t>(i);
       atomicOr(&e->tokens[slot], 1u << t);
@@ -304,7 +318,7 @@ struct Place {
       slot = static_cast<int>(q / a.row_tiles);
       row = static_cast<int>(q) - slot * a.row_tiles;
     } else if constexpr (MODE == kDown) {
-      row = static_cast<int>(q / experts);
+      row = static_cast<int>(q / max(experts, 1));  // (without experts there is no unit)
       slot = static_cast<int>(q) - row * experts;
     }
   }
@@ -401,6 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   if constexpr (MODE == kUp) {
     // ids and weights may come from the launch before
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -423,9 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const int ctas = static_cast<int>(n_units < gridDim.x ? n_units : gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long u0 = blockIdx.x * n_units / ctas;
-  const int n_mine = static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0);
+  const long long u0 = ctas > 0 ? blockIdx.x * n_units / ctas : 0;
+  const int n_mine = static_cast<int>(blockIdx.x) < ctas ? static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0) : 0;
 
   // the ring and the buffers of sums go by the most tokens that a matrix of the call has
   const int off_xs = kOffX + 1024 * most_tokens;                        // gemv: the parts' scale tiles
@@ -435,11 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int buffer_cols = cols * kMatrices;
   const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
 
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -475,6 +488,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         at.next(a, n_experts);
+      }
+      if constexpr (MODE == kUp) {
+        Args d;
+        d.row_tiles = a.down_row_tiles;
+        d.k_units = a.down_k_units;
+        const long long n_down = units_of(d, n_experts);
+        const int down_ctas = static_cast<int>(n_down < gridDim.x ? n_down : gridDim.x);
+        if (static_cast<int>(blockIdx.x) < down_ctas) {
+          const long long d0 = blockIdx.x * n_down / down_ctas;
+          const int n = min(kAhead, static_cast<int>((blockIdx.x + 1) * n_down / down_ctas - d0));
+          Place<kDown> to(d, n_experts, d0);
+          for (int i = 0; i < n; ++i) {
+            if (leader) {
+              const int id = ex->expert[to.slot];
+              asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&mx)),
+                           "r"(to.kc * (kUnitK / 2)), "r"(id * a.K + to.row * kRows) : "memory");
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(
+                               a.down_scales + id * a.down_stride + (static_cast<size_t>(to.row) * a.down_k_tiles + to.kc * kTiles) * 512)),
+                           "r"(min(kTiles, a.down_k_tiles - to.kc * kTiles) * 512) : "memory");
+            }
+            __syncwarp();
+            to.next(d, n_experts);
+          }
+        }
       }
     }
     // every issued stage's copies land before the CTA may exit
@@ -549,17 +586,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
         }
         const uint64_t ad = codes_desc(st, 1024);
-        for (int g = 0; g < tokens; g += 4) {
-          // all of x, its scales in tiles; or four tokens, from their own lines
-          const uint32_t sb = sa + 16 + 4 * g;
-          const uint32_t idesc = idesc_for(FMT, MODE == kGemv ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
-          const uint64_t bd = codes_desc(st + kOffX + g * kSlot, MODE == kGemv ? 1024 : kSlot);
-          const uint32_t d = d0 + 8 * g + which * cols;
-          if (leader) {
+        if (leader) {
+          // x's scales: of all of x, in tiles; or of four tokens at a time, from their own lines. All before the MMAs: a
+          // copy behind an MMA waits for it, and an MMA behind a copy, 280 clocks each time.
+          for (int g = 0; g < tokens; g += 4) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
-              copy_scales(sb + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
-                                                    : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
+              copy_scales(sa + 16 + 4 * g + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
+                                                                 : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
+          }
+          for (int g = 0; g < tokens; g += 4) {
+            const uint32_t sb = sa + 16 + 4 * g, d = d0 + 8 * g + which * cols;
+            const uint32_t idesc = idesc_for(FMT, MODE == kGemv ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
+            const uint64_t bd = codes_desc(st + kOffX + g * kSlot, MODE == kGemv ? 1024 : kSlot);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
               if (j >= n_k) break;
@@ -572,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          __syncwarp();
         }
+        __syncwarp();
         if (leader) commit(smem_u32(&empty[turn.i]));
         __syncwarp();
         turn.next(n_stages);

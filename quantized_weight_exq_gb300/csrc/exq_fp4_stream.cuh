@@ -29,8 +29,13 @@
 //              swizzle), and its scale tiles, as one copy.
 //   warp 6     brings the tokens' parts and their scales (a warp of its own:
 //              behind the weights' copies theirs cost 250 ns a unit).
-//   warp 1     copies scales to tensor memory and issues the MMAs (M = 128
-//              rows of the matrix, N = 8 columns a token, K = 64).
+//   warps 7-10 write a unit's scales to tensor memory, from shared memory by
+//              way of registers. (The tensor core's own copy, tcgen05.cp, takes
+//              55 clocks a tile and keeps MMAs waiting: 720 clocks a unit for
+//              E4M3, of the 800 in which its codes arrive, and more for several
+//              tokens of an expert.)
+//   warp 1     issues the MMAs (M = 128 rows of the matrix, N = 8 columns a
+//              token, K = 64).
 //   warps 2-5  drain the sums: a lane is a row of the matrix.
 //
 // A tile whose units lie in several CTAs goes through the workspace: each
@@ -49,7 +54,7 @@ enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
-constexpr int kThreads = 7 * 32;
+constexpr int kThreads = 11 * 32;
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
 constexpr int kMaxPairs = 256;       // tokens x experts of each
@@ -64,8 +69,8 @@ static_assert(kOffX % 1024 == 0, "swizzle atoms");
 // its scale tiles. An expert's tokens are picked one by one: a token's parts
 // of a unit are a piece, written as shared memory has it: the 8 rows of 128
 // bytes, swizzled, then for each scale tile 8 lines of 16 bytes, a line a row,
-// its first word the scales. Four pieces' lines are what one copy to tensor
-// memory takes, so that MMAs are made for up to four tokens at a time.
+// its first word the scales. Four pieces' lines are 32, a lane each, so that
+// MMAs are made for up to four tokens at a time.
 constexpr int kLines = 8 * 16;
 constexpr int kSlot = 2048;          // of a piece in a stage
 __host__ __device__ constexpr int unit_tiles(int fmt) { return kUnitK / fp4_tile_k(fmt); }
@@ -78,7 +83,6 @@ constexpr int kRest = 20 * 1024;     // barriers, the experts' tables, sums, ali
 constexpr int kRing = kSmemTotal - kRest;
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemScales = 432;         // 16 columns of the matrix's, then 16 for each four tokens
 constexpr int kMaxBuffers = 4;
 
 // Scale of a block of x: 2^(e - 1) for a largest magnitude in [2^e, 2^(e + 1)).
@@ -166,11 +170,6 @@ __device__ __forceinline__ uint64_t codes_desc(uint32_t addr, uint32_t stride) {
          (1ull << 46) | (2ull << 61);
 }
 
-// 32 lines of 16 bytes, groups of 8 lines `stride` bytes apart, no swizzle
-__device__ __forceinline__ uint64_t lines_desc(uint32_t addr, uint32_t stride) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46);
-}
-
 __device__ __forceinline__ uint32_t idesc_for(int fmt, int n) {  // e2m1 operands, K-major, M = 128
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          ((fmt == EXQ_FP4_E8M0 ? 1u : 0u) << 23) | (static_cast<uint32_t>(kRows >> 4) << 24);
@@ -191,8 +190,13 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// four scale tiles (16 bytes of each for the lane) to 16 columns of this warp's lanes
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&t)[4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(t[0].x), "r"(t[0].y), "r"(t[0].z), "r"(t[0].w), "r"(t[1].x), "r"(t[1].y), "r"(t[1].z), "r"(t[1].w),
+        "r"(t[2].x), "r"(t[2].y), "r"(t[2].z), "r"(t[2].w), "r"(t[3].x), "r"(t[3].y), "r"(t[3].z), "r"(t[3].w)
+      : "memory");
 }
 
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -346,6 +350,7 @@ struct Place {
 // The CTA that has unit u, of `ctas` that divide n units: CTA b has units
 // [b n / ctas, (b + 1) n / ctas).
 __device__ __forceinline__ int owner(long long u, long long n, int ctas) {
+  if (n * ctas < (1LL << 31)) return (static_cast<int>(u + 1) * ctas - 1) / static_cast<int>(n);
   return static_cast<int>(((u + 1) * ctas - 1) / n);
 }
 
@@ -392,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sums = reinterpret_cast<float*>(smem + kRing);                 // down: [tokens][rows]
   uint64_t* full = reinterpret_cast<uint64_t*>(sums + kRows * kMaxTokens);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* dfull = empty + kMaxStages;
+  uint64_t* ready = empty + kMaxStages;  // and the scales are in tensor memory
+  uint64_t* dfull = ready + kMaxStages;
   uint64_t* dempty = dfull + kMaxBuffers;
   uint64_t* done = dempty + kMaxBuffers;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -406,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&full[s]), 2);  // the weights' and x's copies
       mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&ready[s]), 4);
     }
     for (int b = 0; b < kMaxBuffers; ++b) {
       mbar_init(smem_u32(&dfull[b]), 1);
@@ -451,7 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_stages = min(kMaxStages, kRing / stage_bytes);
   const int cols = (8 * most_tokens + 15) / 16 * 16;                    // of one sum
   const int buffer_cols = cols * kMatrices;
-  const int n_buffers = min(kMaxBuffers, static_cast<int>(kTmemScales) / buffer_cols);
+  // tensor memory: the buffers, then places for the scales of stages (16 columns of the matrix's, 16 for each four tokens);
+  // three of them at least, while there are two buffers or one
+  const int groups = MODE == kGemv ? 1 : (most_tokens + 3) / 4;
+  const int scale_cols = 16 + 16 * groups;
+  const int n_buffers = max(1, min(kMaxBuffers, (static_cast<int>(kTmemCols) - 3 * scale_cols) / buffer_cols));
+  const int n_places = min(n_stages, (static_cast<int>(kTmemCols) - n_buffers * buffer_cols) / scale_cols);
 
   tc_fence_before();
   __syncthreads();
@@ -564,10 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();
     Place<MODE> at(a, n_experts, u0);
-    Turn turn, buf;
+    Turn turn, buf, place;
     bool fresh = true;  // the next unit begins a buffer
     bool ok = true;
-    const uint32_t sa = tmem + kTmemScales;
     for (int left = n_mine; left > 0 && ok; --left) {
       const int tokens = MODE == kGemv ? 1 : __popc(ex->tokens[at.slot]);  // (all of x at once)
       const int n_k = min(4, (a.K - at.kc * kUnitK + 63) / 64);  // MMAs with k of the matrices
@@ -575,26 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (fresh && !mbar_wait_warp(smem_u32(&dempty[buf.i]), buf.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
 #pragma unroll
       for (int which = 0; which < kMatrices; ++which) {
-        if (!mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
+        if (!mbar_wait_warp(smem_u32(&ready[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t st = smem_u32(smem) + turn.i * stage_bytes;
-        if (leader) {
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) copy_scales(sa + 4 * j, lines_desc(st + kOffScales + j * 512, kLines));
-        }
+        const uint32_t sa = tmem + n_buffers * buffer_cols + place.i * scale_cols;
         const uint64_t ad = codes_desc(st, 1024);
         if (leader) {
-          // x's scales: of all of x, in tiles; or of four tokens at a time, from their own lines. All before the MMAs: a
-          // copy behind an MMA waits for it, and an MMA behind a copy, 280 clocks each time.
-          for (int g = 0; g < tokens; g += 4) {
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-              copy_scales(sa + 16 + 4 * g + 4 * j, MODE == kGemv ? lines_desc(st + off_xs + j * 512, kLines)
-                                                                 : lines_desc(st + kOffX + g * kSlot + 1024 + j * kLines, kSlot));
-          }
           for (int g = 0; g < tokens; g += 4) {
             const uint32_t sb = sa + 16 + 4 * g, d = d0 + 8 * g + which * cols;
             const uint32_t idesc = idesc_for(FMT, MODE == kGemv ? cols : (8 * min(4, tokens - g) + 15) / 16 * 16);
@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) commit(smem_u32(&empty[turn.i]));
         __syncwarp();
         turn.next(n_stages);
+        place.next(n_places);
       }
       if (!ok) break;
       fresh = left == 1 || at.kc + 1 == a.k_units;  // the end of a tile, or (down) of an expert's share of it
@@ -631,6 +632,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     for (int r = 0; r < a.wait_limit; ++r)
       if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(done), 0))) break;
+  } else if (warp >= 7) {
+    // ------------------------------------------------------------ scales to tensor memory
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Place<MODE> at(a, n_experts, u0);
+    Turn turn, place, old;  // old: the stage whose MMAs read this place last
+    int n = 0;
+    bool ok = true;
+    for (int left = n_mine; left > 0 && ok; --left) {
+      const int tokens = MODE == kGemv ? 1 : __popc(ex->tokens[at.slot]);
+#pragma unroll
+      for (int which = 0; which < kMatrices; ++which) {
+        if (!mbar_wait_warp(smem_u32(&full[turn.i]), turn.parity, abort_flag, a.wait_limit, &g_stream_err)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* st = smem + turn.i * stage_bytes;
+        uint4 t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = *reinterpret_cast<const uint4*>(st + kOffScales + j % kTiles * 512 + lane * 16);
+        if (n_places < n_stages) {
+          if (n >= n_places) {
+            if (!mbar_wait_warp(smem_u32(&empty[old.i]), old.parity, abort_flag, a.wait_limit, &g_stream_err)) {
+              ok = false;
+              break;
+            }
+            old.next(n_stages);
+          }
+          ++n;
+        }
+        tc_fence_after();
+        const uint32_t to = tmem + lanes + n_buffers * buffer_cols + place.i * scale_cols;
+        tmem_st16(to, t);
+        for (int g = 0; g < tokens; g += 4) {
+          // all of x's, in tiles; or those of four tokens, a line a lane
+          const uint8_t* from = MODE == kGemv ? st + off_xs + lane * 16
+                                              : st + kOffX + (g + (lane >> 3)) * kSlot + 1024 + (lane & 7) * 16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[j] = *reinterpret_cast<const uint4*>(from + j % kTiles * (MODE == kGemv ? 512 : kLines));
+          tmem_st16(to + 16 + 4 * g, t);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ready[turn.i]));
+        turn.next(n_stages);
+        place.next(n_places);
+      }
+      at.next(a, n_experts);
+    }
   } else {
     // ------------------------------------------------------------ draining the sums
     const int quarter = warp & 3, r = quarter * 32 + lane;
@@ -652,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long first = static_cast<long long>(tile) * tile_units;
       const int b0 = owner(first, n_units, ctas), b1 = owner(first + tile_units - 1, n_units, ctas);
       auto part_of = [&](int b) {  // a CTA's tile that began before it is its part 0
-        return a.part + (static_cast<size_t>(b) * 2 + (first < b * n_units / ctas ? 0 : 1)) * part_floats(MODE) + r;
+        return a.part + (static_cast<size_t>(b) * 2 + (b == b0 ? 1 : 0)) * part_floats(MODE) + r;
       };
       // after this CTA's part is written: whether all are
       auto last_of_tile = [&]() {

@@ -31,6 +31,7 @@ struct PrepareArgs {
 };
 
 constexpr int kPrepareThreads = 512;
+constexpr int kSplitThreads = 128;   // of h: their registers fit beside a CTA of the streaming kernel, which need not wait for them
 
 // Rows as eight 4-bit rows each (see exq_fp4_stream.cuh): a thread takes 8
 // values, the 2 or 4 of a block find its scale together, and those of a scale
@@ -39,12 +40,13 @@ constexpr int kPrepareThreads = 512;
 // fills it up) goes. H: rows of h, divided by the power of two of each.
 template <int FMT, bool TILES, bool H>
 __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
+  constexpr int kThreads = H ? kSplitThreads : kPrepareThreads;
   constexpr int kBlockThreads = fp4_block(FMT) / 8, kWordThreads = 4 * kBlockThreads;
   constexpr int kTop = H ? kHTop : kXTop;
   const int row_threads = TILES ? (a.D + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT) * kWordThreads : a.k_units * (kUnitK / 8);
   const int total = a.T * row_threads;            // below 2^31: K is, by the entry points, at most 2^25
   const int padded = (total + 31) / 32 * 32;      // whole warps
-  for (int i = static_cast<int>(blockIdx.x) * kPrepareThreads + threadIdx.x; i < padded; i += a.split_blocks * kPrepareThreads) {
+  for (int i = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x; i < padded; i += a.split_blocks * kThreads) {
     const int t = i / row_threads, c = i - t * row_threads;
     const bool in = i < total && c * 8 < a.D;
     float q[8] = {};
@@ -108,9 +110,15 @@ __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
   }
 }
 
+// a logit as an unsigned key that orders as the numbers do, a NaN as -infinity, -0 as 0
+__device__ __forceinline__ unsigned order_key(float v) {
+  const unsigned b = v != v ? 0xFF800000u : v == 0.f ? 0u : __float_as_uint(v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
 // Routing: one CTA an expert: its row against every token, fp32 sums of exact products
 // (a thread's share in order of k, then a tree). The last CTA to finish picks
-// each token's experts, a warp a token. The router is small (128 experts x
+// each token's experts. The router is small (128 experts x
 // 4096: 1 MB): what counts is the way from launch to result.
 template <int TT>
 __device__ __forceinline__ void route(const PrepareArgs& a) {
@@ -162,54 +170,39 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
   __syncthreads();
   if (!is_last) return;
 
+  // Each expert's place is the number of those before it: larger ones, and equal ones of a lower index. All experts of some
+  // tokens are compared with all at once, which for up to 128 of them is sooner done than top_k searches one after the other
+  // (3 us, with the loads of code that runs once).
+  constexpr int kHeld = 1024;
+  __shared__ unsigned held[kHeld];    // keys of a batch of tokens
+  __shared__ float chosen[16][16];
+  const int batch = max(1, min(a.T, kHeld / a.E));
+  for (int t0 = 0; t0 < a.T; t0 += batch) {
+    const int n = min(batch, a.T - t0) * a.E;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPrepareThreads) held[i] = order_key(__ldcg(a.logits + t0 * a.E + i));
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPrepareThreads) {
+      const int t = i / a.E, e = i - t * a.E;
+      const unsigned key = held[i];
+      const unsigned* others = held + t * a.E;
+      int place = 0;
+#pragma unroll 8
+      for (int o = 0; o < a.E; ++o) place += others[o] > key || (others[o] == key && o < e) ? 1 : 0;
+      if (place < a.top_k) {
+        a.ids[(t0 + t) * a.top_k + place] = e;
+        chosen[t0 + t][place] = __ldcg(a.logits + (t0 + t) * a.E + e);
+      }
+    }
+  }
+  __syncthreads();
   for (int t = warp; t < a.T; t += kPrepareThreads / 32) {
-    constexpr int kPer = kMaxExperts / 32;
-    // lane's logits (experts lane, lane + 32, ...) as unsigned keys that order as the numbers do, a NaN as -infinity, -0 as
-    // 0; above 0 for every number: 0 is what is not there or has been taken
-    float v[kPer];
-    unsigned keys[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (32 * i >= a.E) break;
-      const bool there = 32 * i + lane < a.E;
-      v[i] = there ? __ldcg(a.logits + t * a.E + 32 * i + lane) : 0.f;
-      const unsigned b = v[i] != v[i] ? 0xFF800000u : v[i] == 0.f ? 0u : __float_as_uint(v[i]);
-      keys[i] = !there ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
-    }
-    float mine = -INFINITY;  // lane j: the j-th logit
-    for (int j = 0; j < a.top_k; ++j) {
-      unsigned key = 0u;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (32 * i >= a.E) break;
-        key = max(key, keys[i]);
-      }
-      key = __reduce_max_sync(0xffffffffu, key);
-      unsigned at = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i)
-        if (32 * i < a.E && keys[i] == key) at = 32 * i + lane;
-      at = __reduce_min_sync(0xffffffffu, at);
-      float l = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (32 * i >= a.E) break;
-        if (32 * i + lane == at) { keys[i] = 0u; l = v[i]; }
-      }
-      l = __shfl_sync(0xffffffffu, l, at & 31);
-      if (lane == j) mine = l;
-      if (lane == 0) a.ids[t * a.top_k + j] = static_cast<int>(at);
-    }
-    const float top = __shfl_sync(0xffffffffu, mine, 0);
-    const float p = lane < a.top_k ? expf(mine - top) : 0.f;
+    const float top = chosen[t][0];
+    const float p = lane < a.top_k ? expf(chosen[t][lane] - top) : 0.f;
     float total = p;
     if (!a.renorm) {
       total = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (32 * i >= a.E) break;
-        if (32 * i + lane < a.E) total += expf(v[i] - top);
-      }
+      for (int e = lane; e < a.E; e += 32) total += expf(__ldcg(a.logits + t * a.E + e) - top);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
@@ -236,7 +229,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 // Between the experts' products: h's parts. (Places that nothing was written
 // to are split all the same; nobody reads them.)
 template <int FMT>
-__global__ void __launch_bounds__(kPrepareThreads) split_h_kernel(const __grid_constant__ PrepareArgs a) {
+__global__ void __launch_bounds__(kSplitThreads) split_h_kernel(const __grid_constant__ PrepareArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the launch after this may start: what it reads before it waits is older than the launch before this
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -255,13 +248,13 @@ bool beside_streaming(void (*fn)(PrepareArgs)) {
 }
 
 // blocks that split rows of D values, a thread 8 of them
-int split_blocks_for(int format, bool tiles, int rows, int D) {
+int split_blocks_for(int format, bool tiles, int rows, int D, int threads) {
   const int k = tiles ? fp4_tile_k(format) : kUnitK;
-  return std::min(div_up(rows * div_up(D, k) * (k / 8), kPrepareThreads), 8192);
+  return std::min(div_up(rows * div_up(D, k) * (k / 8), threads), 8192);
 }
 
 exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t stream) {
-  p.split_blocks = split_blocks_for(format, tiles, p.T, p.D);
+  p.split_blocks = split_blocks_for(format, tiles, p.T, p.D, kPrepareThreads);
   const bool e4m3 = format == EXQ_FP4_E4M3;
   constexpr int A = EXQ_FP4_E4M3, B = EXQ_FP4_E8M0;
   auto fn = tiles ? (e4m3 ? prepare_kernel<A, true, 0> : prepare_kernel<B, true, 0>)
@@ -275,22 +268,31 @@ exq_status launch_prepare(int format, bool tiles, PrepareArgs p, cudaStream_t st
 }
 
 exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
-  p.split_blocks = split_blocks_for(format, false, p.T, p.D);
+  p.split_blocks = split_blocks_for(format, false, p.T, p.D, kSplitThreads);
   auto fn = format == EXQ_FP4_E4M3 ? split_h_kernel<EXQ_FP4_E4M3> : split_h_kernel<EXQ_FP4_E8M0>;
   if (!beside_streaming(fn)) return EXQ_ERR_CUDA;
-  return launch_dependent(fn, p.split_blocks, kPrepareThreads, 0, stream, p);
+  return launch_dependent(fn, p.split_blocks, kSplitThreads, 0, stream, p);
+}
+
+template <int FMT, int MODE, int NT>
+exq_status launch_stream(const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a, int ctas,
+                         int device, cudaStream_t stream) {
+  auto fn = stream_kernel<FMT, MODE, NT>;
+  static PerDevice attr;
+  if (!attr.once(device, [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal) == cudaSuccess;
+      }))
+    return EXQ_ERR_CUDA;
+  return launch_dependent(fn, ctas, fp4s::kThreads, kSmemTotal, stream, m0, m1, mx, a);
 }
 
 template <int MODE>
 exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a,
                          int ctas, int device, cudaStream_t stream) {
-  auto fn = format == EXQ_FP4_E4M3 ? stream_kernel<EXQ_FP4_E4M3, MODE> : stream_kernel<EXQ_FP4_E8M0, MODE>;
-  static PerDevice attr[2];
-  if (!attr[format == EXQ_FP4_E4M3].once(device, [&] {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal) == cudaSuccess;
-      }))
-    return EXQ_ERR_CUDA;
-  return launch_dependent(fn, ctas, fp4s::kThreads, kSmemTotal, stream, m0, m1, mx, a);
+  constexpr int A = EXQ_FP4_E4M3, B = EXQ_FP4_E8M0;
+  auto go = format == EXQ_FP4_E4M3 ? (a.M == 1 ? launch_stream<A, MODE, 1> : a.M <= 8 ? launch_stream<A, MODE, 8> : launch_stream<A, MODE, 16>)
+                                   : (a.M == 1 ? launch_stream<B, MODE, 1> : a.M <= 8 ? launch_stream<B, MODE, 8> : launch_stream<B, MODE, 16>);
+  return go(m0, m1, mx, a, ctas, device, stream);
 }
 
 bool encode_codes(CUtensorMap* map, const void* codes, uint64_t rows, int K, int box_rows) {

@@ -366,31 +366,40 @@ struct Turn {
   }
 };
 
-// v[j] += part j (of n) of CTAs b0 .. b1, in their order; four CTAs' loads are in flight at a time
-template <typename PartOf>
-__device__ __forceinline__ void add_parts(float (&v)[16], int n, int b0, int b1, PartOf part_of) {
-  for (int b = b0; b <= b1; b += 4) {
-    float t[4][16];
+// v[w][j] += part j (of n) of matrix w of CTAs b0 .. b1, in their order; several parts' loads are in flight at a time
+template <int W, int N, typename PartOf>
+__device__ __forceinline__ void add_parts(float (&v)[W][N], int n, int b0, int b1, PartOf part_of) {
+  constexpr int kAtOnce = W * N > 32 ? 2 : W * N > 8 ? 4 / W : 8;
+  for (int b = b0; b <= b1; b += kAtOnce) {
+    float t[kAtOnce][W][N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const float* p = part_of(min(b + i, b1));
 #pragma unroll
-      for (int j = 0; j < 16; ++j) t[i][j] = j < n ? __ldcg(p + j * kRows) : 0.f;
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int j = 0; j < N; ++j) t[i][w][j] = j < n ? __ldcg(p + (w * kMaxTokens + j) * kRows) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kAtOnce; ++i)
       if (b + i <= b1) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += t[i][j];
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[w][j] += t[i][w][j];
       }
   }
 }
 
-template <int FMT, int MODE>
+// NT: rows of x, at most. (What drains the sums is unrolled over them, and in a
+// short call most of its code is fetched for the first time: one row's is a
+// sixteenth of sixteen's.)
+template <int FMT, int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1,
                   const __grid_constant__ CUtensorMap mx, const __grid_constant__ Args a) {
   constexpr int kMatrices = MODE == kUp ? 2 : 1;  // of a unit, a stage each
+  constexpr int kVals = NT < 2 ? 2 : NT;           // values of a lane (two tokens' come at a time)
   constexpr int kTiles = unit_tiles(FMT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -422,6 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0 && elect_one()) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&m0)) : "memory");
+    if constexpr (MODE == kUp) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&m1)) : "memory");
+    if constexpr (MODE != kDown) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&mx)) : "memory");
+  }
+  __syncwarp();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols) : "memory");
@@ -737,17 +752,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // (the largest h is known: parts made with it have come through the MMAs)
       if (MODE == kDown && lane < n_tok) f *= pow2(h_exponent(__ldcg(a.h_most + place)));
-      float v[kMatrices][kMaxTokens];  // the row's values: token by token; up: gate's and up's
+      float v[kMatrices][kVals];  // the row's values: token by token; up: gate's and up's
 #pragma unroll
       for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
-        for (int j = 0; j < kMaxTokens; ++j) v[w][j] = 0.f;
+        for (int j = 0; j < kVals; ++j) v[w][j] = 0.f;
       if (ok) {
         const uint32_t d = tmem + lanes + buf.i * buffer_cols;
 #pragma unroll
         for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
-          for (int j = 0; j < kMaxTokens; j += 2) {
+          for (int j = 0; j < kVals; j += 2) {
             if (j < n_tok) {
               float c[16];
               tmem_ld16(d + w * cols + 8 * j, c);
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // an expert's sums go to its own tokens only: a NaN of its weights reaches no other
         unsigned m = tokens;
 #pragma unroll
-        for (int j = 0; j < kMaxTokens; ++j) {
+        for (int j = 0; j < NT; ++j) {
           if (j >= n_tok) break;
           const float fj = __shfl_sync(0xffffffffu, f, j);
           const int t = __ffs(static_cast<int>(m)) - 1;
@@ -773,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!tile_ends) continue;
 #pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t) v[0][t] = t < a.M ? sums[t * kRows + r] : 0.f;
+        for (int t = 0; t < NT; ++t) v[0][t] = t < a.M ? sums[t * kRows + r] : 0.f;
       }
 
       // ---- the tile, or this CTA's part of it
@@ -783,15 +798,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
-          for (int j = 0; j < kMaxTokens; ++j)
+          for (int j = 0; j < NT; ++j)
             if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w][j]);
         if (!last_of_tile()) continue;
 #pragma unroll
-        for (int w = 0; w < kMatrices; ++w) {
+        for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
-          for (int j = 0; j < kMaxTokens; ++j) v[w][j] = 0.f;
-          add_parts(v[w], n_val, b0, b1, [&](int b) { return part_of(b) + w * kMaxTokens * kRows; });
-        }
+          for (int j = 0; j < kVals; ++j) v[w][j] = 0.f;
+        add_parts(v, n_val, b0, b1, part_of);
       }
       if constexpr (MODE == kUp) {
         const int id = ex->expert[slot];
@@ -799,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float fg = (a.f0 ? __ldg(a.f0 + id) : 1.f) * fx, fu = (a.f1 ? __ldg(a.f1 + id) : 1.f) * fx;
         unsigned m = tokens;
 #pragma unroll
-        for (int j = 0; j < kMaxTokens; ++j) {
+        for (int j = 0; j < NT; ++j) {
           if (j >= n_tok) break;
           const int place = ex->place[slot][__ffs(static_cast<int>(m)) - 1];
           m &= m - 1u;
@@ -812,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (!*abort_flag && in) {
         const float f = MODE == kGemv ? a.factor * (FMT == EXQ_FP4_E4M3 ? pow2(e4m3_shift(kXTop)) : 1.f) : 1.f;
 #pragma unroll
-        for (int t = 0; t < kMaxTokens; ++t)
+        for (int t = 0; t < NT; ++t)
           if (t < a.M) a.y[static_cast<size_t>(t) * a.rows + n_row] = __half_as_ushort(__float2half_rn(v[0][t] * f));
       }
     }

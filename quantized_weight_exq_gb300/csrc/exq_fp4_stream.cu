@@ -41,7 +41,7 @@ constexpr int kSplitThreads = 128;   // of h: their registers fit beside a CTA o
 template <int FMT, bool TILES, bool H>
 __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
   constexpr int kThreads = H ? kSplitThreads : kPrepareThreads;
-  constexpr int kBlockThreads = fp4_block(FMT) / 8, kWordThreads = 4 * kBlockThreads;
+  constexpr int kWordThreads = fp4_tile_k(FMT) / 8;
   constexpr int kTop = H ? kHTop : kXTop;
   const int row_threads = TILES ? (a.D + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT) * kWordThreads : a.k_units * (kUnitK / 8);
   const int total = a.T * row_threads;            // below 2^31: K is, by the entry points, at most 2^25
@@ -50,7 +50,6 @@ __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
     const int t = i / row_threads, c = i - t * row_threads;
     const bool in = i < total && c * 8 < a.D;
     float q[8] = {};
-    uint32_t m = 0u;  // bits of the block's largest magnitude in fp32
     if (in) {
       if constexpr (H) {
         const float4* src = reinterpret_cast<const float4*>(a.h + static_cast<size_t>(t) * a.D + 8 * c);
@@ -59,47 +58,21 @@ __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
         q[0] = u.x * r; q[1] = u.y * r; q[2] = u.z * r; q[3] = u.w * r;
         q[4] = v.x * r; q[5] = v.y * r; q[6] = v.z * r; q[7] = v.w * r;
       } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.D) + c);
-        const uint32_t h[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-          q[2 * j] = v.x;
-          q[2 * j + 1] = v.y;
-        }
+        to_f32(__ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.D) + c), q);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(q[j]) & 0x7FFFFFFFu);  // (infinity and NaN are above all others)
     }
-#pragma unroll
-    for (int d = 1; d < kBlockThreads; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const bool bad = m >= 0x7F800000u;  // the block is NaN
-    const int e = bad ? 0 : part_exponent<FMT>(__uint_as_float(m), kTop);
-    const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(e, kTop);
-    const float r = pow2(-e);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = bad ? 0.f : q[j] * r;
+    uint32_t words[kParts], word;
+    split8<FMT>(q, kTop, c, words, word);
     uint8_t* piece = nullptr;
     if constexpr (!TILES) piece = a.pieces + (static_cast<size_t>(t) * a.k_units + c / (kUnitK / 8)) * piece_bytes(FMT);
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
-      const uint32_t word = e2m1x8(q);
       if constexpr (TILES) {
-        if (in) a.codes[(static_cast<size_t>(t) * kParts + p) * (a.D / 8) + c] = word;
+        if (in) a.codes[(static_cast<size_t>(t) * kParts + p) * (a.D / 8) + c] = words[p];
       } else {
-        if (i < total) *reinterpret_cast<uint32_t*>(piece + piece_word(p, 8 * c % kUnitK)) = word;
-      }
-      const uint32_t v[4] = {e2m1x2_f16<0>(word), e2m1x2_f16<1>(word), e2m1x2_f16<2>(word), e2m1x2_f16<3>(word)};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-        q[2 * j] = (q[2 * j] - d.x) * 8.f;
-        q[2 * j + 1] = (q[2 * j + 1] - d.y) * 8.f;
+        if (i < total) *reinterpret_cast<uint32_t*>(piece + piece_word(p, 8 * c % kUnitK)) = words[p];
       }
     }
-    uint32_t word = byte << (8 * ((c / kBlockThreads) & 3));
-#pragma unroll
-    for (int d = kBlockThreads; d < kWordThreads; d <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, d);
     const int p = c % kWordThreads, tile = c / kWordThreads;
     if (i < total && p < kParts) {
       if constexpr (TILES)
@@ -355,21 +328,26 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const GemvPlan plan(w.format, w.K, M, sms);
   CUtensorMap mw, mx;
-  if (!encode_codes(&mw, w.codes, w.rows, w.K, kRows) ||
-      !encode_codes(&mx, ws + plan.codes, static_cast<uint64_t>(M) * kParts, w.K, M * kParts))
+  if (!encode_codes(&mw, w.codes, w.rows, w.K, kRows)) return EXQ_ERR_CUDA;
+  if (M == 1)
+    mx = mw;  // not used
+  else if (!encode_codes(&mx, ws + plan.codes, static_cast<uint64_t>(M) * kParts, w.K, M * kParts))
     return EXQ_ERR_CUDA;
-  PrepareArgs p{};
-  p.x = x;
-  p.codes = reinterpret_cast<uint32_t*>(ws + plan.codes);
-  p.scales = reinterpret_cast<uint32_t*>(ws + plan.scales);
-  p.T = M;
-  p.D = w.K;
-  const exq_status st = launch_prepare(w.format, true, p, stream);
-  if (st != EXQ_OK) return st;
+  if (M > 1) {
+    PrepareArgs p{};
+    p.x = x;
+    p.codes = reinterpret_cast<uint32_t*>(ws + plan.codes);
+    p.scales = reinterpret_cast<uint32_t*>(ws + plan.scales);
+    p.T = M;
+    p.D = w.K;
+    const exq_status st = launch_prepare(w.format, true, p, stream);
+    if (st != EXQ_OK) return st;
+  }
   Args a{};
   set_shape(a, w.format, w.rows, w.K);
   a.sc0 = w.scales;
   a.x = ws + plan.scales;
+  a.row = x;
   a.y = y;
   a.M = M;
   a.factor = w.factor;

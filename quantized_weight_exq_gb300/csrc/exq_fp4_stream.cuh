@@ -28,7 +28,9 @@
 //   warp 0     brings a unit's codes, as one 2-D box (128-byte rows, 128-byte
 //              swizzle), and its scale tiles, as one copy.
 //   warp 6     brings the tokens' parts and their scales (a warp of its own:
-//              behind the weights' copies theirs cost 250 ns a unit).
+//              behind the weights' copies theirs cost 250 ns a unit). One row
+//              it splits itself, a unit at a time, while the codes arrive, and
+//              warp 11 with it; for more a launch before this one does.
 //   warps 7-10 write a unit's scales to tensor memory, from shared memory by
 //              way of registers. (The tensor core's own copy, tcgen05.cp, takes
 //              55 clocks a tile and keeps MMAs waiting: 720 clocks a unit for
@@ -54,7 +56,7 @@ enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
-constexpr int kThreads = 11 * 32;
+constexpr int kThreads = 12 * 32;
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
 constexpr int kMaxPairs = 256;       // tokens x experts of each
@@ -99,6 +101,7 @@ struct Args {
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
   const uint8_t* x;        // gemv: scale tiles of the parts; else pieces [token or pair, unit]
+  const uint16_t* row;     // gemv of one row: x itself
   uint16_t* y;             // [M, rows] (not up)
   float* h;                // up: [pairs, rows]
   unsigned* h_most;        // [pairs]: bits of the largest finite magnitude of h
@@ -161,6 +164,50 @@ __device__ __forceinline__ int h_exponent(unsigned most) { return min(max(static
 
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Eight values of a row as words of codes of the parts, and the scale word
+// that they share with the 8 (E4M3) or 16 threads of four blocks; `c` counts
+// the threads along the row. By whole warps.
+template <int FMT>
+__device__ __forceinline__ void split8(float (&q)[8], int top, int c, uint32_t (&words)[kParts], uint32_t& scales) {
+  constexpr int kBlockThreads = fp4_block(FMT) / 8, kWordThreads = 4 * kBlockThreads;
+  uint32_t m = 0u;  // bits of the block's largest magnitude (infinity and NaN are above all others)
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(q[j]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 1; d < kBlockThreads; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool bad = m >= 0x7F800000u;  // the block is NaN
+  const int e = bad ? 0 : part_exponent<FMT>(__uint_as_float(m), top);
+  const uint32_t byte = bad ? (FMT == EXQ_FP4_E4M3 ? 0x7Fu : 0xFFu) : part_scale_byte<FMT>(e, top);
+  const float r = pow2(-e);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = bad ? 0.f : q[j] * r;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    words[p] = e2m1x8(q);
+    const uint32_t v[4] = {e2m1x2_f16<0>(words[p]), e2m1x2_f16<1>(words[p]), e2m1x2_f16<2>(words[p]), e2m1x2_f16<3>(words[p])};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+      q[2 * j] = (q[2 * j] - d.x) * 8.f;
+      q[2 * j + 1] = (q[2 * j + 1] - d.y) * 8.f;
+    }
+  }
+  scales = byte << (8 * ((c / kBlockThreads) & 3));
+#pragma unroll
+  for (int d = kBlockThreads; d < kWordThreads; d <<= 1) scales |= __shfl_xor_sync(0xffffffffu, scales, d);
+}
+
+// eight fp16 numbers
+__device__ __forceinline__ void to_f32(uint4 x, float (&q)[8]) {
+  const uint32_t h[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    q[2 * j] = v.x;
+    q[2 * j + 1] = v.y;
+  }
+}
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -232,19 +279,17 @@ __device__ __forceinline__ float join_parts(const float* d) {
 __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned* used, bool report) {
   const int tid = threadIdx.x, pairs = a.M * a.top_k;
   if (tid < kMaxExperts / 32) used[tid] = 0u;
-  for (int i = tid; i < kMaxPairs; i += kThreads) {
-    e->tokens[i] = 0u;
-    e->ids[i] = i < pairs ? __ldcg(a.ids + i) : -1;
-    e->weight[i] = i < pairs ? __ldcg(a.weights + i) : 0.f;
+  const int id = tid < pairs ? __ldcg(a.ids + tid) : -1;
+  const float weight = tid < pairs ? __ldcg(a.weights + tid) : 0.f;
+  if (tid < kMaxPairs) {
+    e->tokens[tid] = 0u;
+    e->ids[tid] = id;
+    e->weight[tid] = weight;
   }
   __syncthreads();
-  for (int i = tid; i < pairs; i += kThreads) {
-    const int id = e->ids[i];
-    if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n_experts))
-      atomicOr(&used[id >> 5], 1u << (id & 31));
-    else if (report && id != -1)
-      atomicOr(&g_stream_err, kDevErrBadExpert);
-  }
+  const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.n_experts);
+  if (good) atomicOr(&used[id >> 5], 1u << (id & 31));
+  if (report && id != -1 && !good) atomicOr(&g_stream_err, kDevErrBadExpert);
   __syncthreads();
   if (tid == 0) {
     int n = 0;
@@ -253,40 +298,36 @@ __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned
     e->n = n;
     e->most_tokens = 1;
   }
-  float sum[2] = {0.f, 0.f};
-  int slot_of[2] = {-1, -1};
-  for (int i = tid, r = 0; i < pairs; i += kThreads, ++r) {
-    const int id = e->ids[i];
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.n_experts)) continue;
-    int slot = __popc(used[id >> 5] & ((1u << (id & 31)) - 1u));
+  bool first = good;
+  float sum = 0.f;
+  int slot = 0;
+  if (good) {
+    slot = __popc(used[id >> 5] & ((1u << (id & 31)) - 1u));
 #pragma unroll
     for (int w = 0; w < kMaxExperts / 32; ++w) slot += w < (id >> 5) ? __popc(used[w]) : 0;
     e->expert[slot] = id;
-    const int t = i / a.top_k;
-    bool first = true;
+    const int t = tid / a.top_k;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int p = min(t * a.top_k + j, kMaxPairs - 1);
       const bool same = e->ids[p] == id && j < a.top_k;
       const float w = e->weight[p];
-      first = first && (!same || p >= i);
-      sum[r] += same ? w : 0.f;
+      first = first && (!same || p >= tid);
+      sum += same ? w : 0.f;
     }
     if (first) {
-      e->place[slot][t] = static_cast<uint8_t>(i);
+      e->place[slot][t] = static_cast<uint8_t>(tid);
       atomicOr(&e->tokens[slot], 1u << t);
-      slot_of[r] = slot;
     }
   }
   __syncthreads();
-  for (int i = tid, r = 0; i < pairs; i += kThreads, ++r)
-    if (slot_of[r] >= 0) {
-      e->weight[i] = sum[r];
-      atomicMax(&e->most_tokens, __popc(e->tokens[slot_of[r]]));
-    }
+  if (first) {
+    e->weight[tid] = sum;
+    atomicMax(&e->most_tokens, __popc(e->tokens[slot]));
+  }
   __syncthreads();
 }
-static_assert(kMaxPairs <= 2 * kThreads, "two places a thread");
+static_assert(kMaxPairs <= kThreads, "a place a thread");
 
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == EXQ_ACT_SILU) return v / (1.f + __expf(-v));
@@ -446,6 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ids and weights may come from the launch before
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
+  constexpr bool kOneRow = MODE == kGemv && NT == 1;
+  if constexpr (kOneRow) asm volatile("griddepcontrol.wait;" ::: "memory");  // w may come from the launch before
   if constexpr (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int n_experts = 1, most_tokens = a.M;
   if constexpr (MODE != kGemv) {
@@ -545,12 +588,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = max(0, issued - n_stages); i < issued; ++i)
       for (int r = 0; r < a.wait_limit; ++r)
         if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1))) break;
-  } else if (warp == 6) {
+  } else if (warp == 6 || warp == 11) {
     // ------------------------------------------------------------ the tokens' parts
     const bool leader = elect_one();
     // they come from the launch before
-    if constexpr (MODE == kGemv || MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!a.starve) {
+    if constexpr (MODE != kUp && !kOneRow) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (kOneRow && !a.starve) {
+      // Each warp takes the units of every second place. (Every second unit
+      // would not do: with an odd number of stages a warp would come to a place
+      // every second time round, and a barrier's parity would tell it nothing.)
+      constexpr int kWordThreads = fp4_tile_k(FMT) / 8;
+      const int group = warp == 6 ? 0 : 1;
+      Place<MODE> at(a, n_experts, u0);
+      Turn turn;
+      int left = n_mine;
+      auto step = [&]() {
+        do {
+          at.next(a, n_experts);
+          turn.next(n_stages);
+          --left;
+        } while (left > 0 && (turn.i & 1) != group);
+      };
+      auto load = [&]() {
+        const int k = at.kc * kUnitK + 8 * lane;
+        return left > 0 && k < a.K ? __ldg(reinterpret_cast<const uint4*>(a.row + k)) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (group == 1) step();
+      uint4 next = load();
+      while (left > 0) {
+        const Turn mine = turn;
+        float q[8];
+        to_f32(next, q);
+        step();
+        next = load();
+        uint32_t words[kParts], scales;
+        split8<FMT>(q, kXTop, lane, words, scales);
+        if (!mbar_wait_warp(smem_u32(&empty[mine.i]), mine.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
+        uint8_t* st = smem + mine.i * stage_bytes;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint32_t*>(st + kOffX + piece_word(p, 8 * lane)) = words[p];
+        if (lane % kWordThreads < kParts)  // a line of the scale tile for each part
+          *reinterpret_cast<uint32_t*>(st + off_xs + lane / kWordThreads * 512 + lane % kWordThreads * 16) = scales;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor core reads it
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&full[mine.i]));
+      }
+    } else if (!a.starve && warp == 6) {
       Place<MODE> at(a, n_experts, u0);
       Turn turn;
       bool ok = true;

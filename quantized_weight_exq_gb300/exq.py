@@ -772,9 +772,12 @@ class Fp4Matrix:
     """A matrix [rows, K] in the 4-bit format on the GPU: codes uint8 [rows, K / 2], scales uint8 [exq_fp4_scale_bytes] in tiles
     (exq_pack_fp4, exq_fp4_quantize), and the factor of an E4M3 one."""
 
+    __slots__ = "rows", "K", "format", "factor", "device", "_buf", "_codes", "_scales", "_desc", "_ref", "_space"
+
     def __init__(self, codes, scales, format: int, factor: float = 1.0):
         self.rows, self.K = _fp4_tensors("Fp4Matrix", codes, scales, (), format)
-        self._codes, self._scales, self.format, self.factor = codes, scales, format, factor
+        self._buf, self._codes, self._scales, self.format, self.factor = None, codes, scales, format, factor
+        self._space = {}
         self.device = codes.get_device()
         self._desc = exq_fp4_matrix(format, self.rows, self.K, factor, codes.data_ptr(), scales.data_ptr())
         self._ref = ctypes.byref(self._desc)
@@ -785,12 +788,14 @@ class Fp4Matrix:
         import torch
         m = cls.__new__(cls)
         n = rows * K // 2
-        buf = _empty(n + 512 * (-(-rows // 128) * -(-K // (64 if format == FP4_E4M3 else 128))), torch.uint8, like.device, stream)
+        size = n + 512 * (-(-rows // 128) * -(-K // (64 if format == FP4_E4M3 else 128)))
+        m._buf = buf = (torch.empty(size, dtype=torch.uint8, device=like.device) if stream is None
+                        else _empty(size, torch.uint8, like.device, stream))
         m.rows, m.K, m.format, m.factor, m.device = rows, K, format, factor, like.get_device()
-        m._buf, m._codes, m._scales = buf, None, None
+        m._codes = m._scales = m._space = None
         at = buf.data_ptr()
-        m._desc = exq_fp4_matrix(format, rows, K, factor, at, at + n)
-        m._ref = ctypes.byref(m._desc)
+        m._desc = d = exq_fp4_matrix(format, rows, K, factor, at, at + n)
+        m._ref = ctypes.byref(d)
         return m
 
     @property
@@ -832,6 +837,8 @@ def _result(out, rows: int, cols: int, dev: int, like, stream, where: str):
     """``out``, which has to be a contiguous fp16 [rows, cols] on the device, or such a tensor."""
     import torch
     if out is None:
+        if stream is None:
+            return torch.empty((rows, cols), dtype=torch.float16, device=like.device)
         return _empty((rows, cols), torch.float16, like.device, stream)
     if not _is_rows(out, torch.float16) or out.shape != (rows, cols) or out.get_device() != dev:
         raise ExqError(EXQ_ERR_INVALID_ARG, where)
@@ -901,7 +908,12 @@ def exq_fp4_gemv(w: Fp4Matrix, x, out=None, workspace=None, stream=None):
     out = _result(out, M, w.rows, dev, x, stream, where)
     handle = _stream_ptr(stream, dev)
     if workspace is None:
-        ws, n = _fp4_workspace(_lib.exq_fp4_gemv_workspace_size(w._ref, M), dev, stream, handle, where)
+        if w._space is None:
+            w._space = {}
+        need = w._space.get(M)  # what M rows need, of a matrix of this shape
+        if need is None:
+            need = w._space[M] = _lib.exq_fp4_gemv_workspace_size(w._ref, M)
+        ws, n = _fp4_workspace(need, dev, stream, handle, where)
     else:
         ws, n = _space(workspace, dev, where)
     _check(_lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle), where)
@@ -943,6 +955,7 @@ class MoeLayer:
         self._desc = exq_moe_layer(gate._desc, up._desc, down._desc, None if router is None else router.data_ptr(), top_k,
                                    int(renorm), act)
         self._ref = ctypes.byref(self._desc)
+        self._space = {}
 
 
 def exq_moe_workspace_size(layer: MoeLayer, T: int) -> int:
@@ -971,7 +984,10 @@ def exq_moe(layer: MoeLayer, x, ids=None, weights=None, out=None, workspace=None
     out = _result(out, T, layer.D, dev, x, stream, where)
     handle = _stream_ptr(stream, dev)
     if workspace is None:
-        ws, n = _fp4_workspace(_lib.exq_moe_workspace_size(layer._ref, T), dev, stream, handle, where)
+        need = layer._space.get(T)
+        if need is None:
+            need = layer._space[T] = _lib.exq_moe_workspace_size(layer._ref, T)
+        ws, n = _fp4_workspace(need, dev, stream, handle, where)
     else:
         ws, n = _space(workspace, dev, where)
     _check(_lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle), where)

@@ -247,25 +247,46 @@ exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
   return launch_dependent(fn, p.split_blocks, kSplitThreads, 0, stream, p);
 }
 
-template <int FMT, int MODE, int NT>
+// Whether the streaming kernel splits the rows itself: one always, and up to
+// eight of x where a CTA has few units. The launch that splits them takes 0.5
+// to 3.5 us; splitting a row in every CTA takes each of its units up to 60 ns
+// longer. Here and by a launch: 4 x 1024 x 8192 (7 row units a CTA) 7.7 and
+// 11.2 us, 2 x 8192 x 4096 (13) 10.1 and 10.8, 6 x 4096 x 4096 (20) 8.9 and
+// 9.6, 3 x 8192 x 4096 (20) 10.6 and 10.9, 4 x 8192 x 4096 (27) 11.5 and 10.9,
+// 2 x 8192 x 8192 (27) 14.3 and 13.7, 8 x 28672 x 8192 (377) 52 and 29. One
+// token of 8 of 128 experts of 1536 x 4096: 36.9 and 39.5 us; two and more
+// tokens of other layers gained as often as they lost.
+bool splits(int mode, int M, long long units, int ctas) {
+  return M == 1 || (mode == kGemv && M <= 8 && M * units <= 20ll * ctas);
+}
+
+template <int FMT, int MODE, int NT, bool HERE>
 exq_status launch_stream(const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a, int ctas,
                          int device, cudaStream_t stream) {
-  auto fn = stream_kernel<FMT, MODE, NT>;
+  auto fn = stream_kernel<FMT, MODE, NT, HERE>;
   static PerDevice attr;
   if (!attr.once(device, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal) == cudaSuccess;
       }))
     return EXQ_ERR_CUDA;
-  return launch_dependent(fn, ctas, fp4s::kThreads, kSmemTotal, stream, m0, m1, mx, a);
+  return launch_dependent(fn, ctas, threads_of(NT, HERE), kSmemTotal, stream, m0, m1, mx, a);
+}
+
+template <int FMT, int MODE>
+exq_status launch_stream(bool here, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a, int ctas,
+                         int device, cudaStream_t stream) {
+  auto go = a.M == 1 ? launch_stream<FMT, MODE, 1, MODE != kUp> : a.M <= 8 ? launch_stream<FMT, MODE, 8, false>
+                                                                           : launch_stream<FMT, MODE, 16, false>;
+  if constexpr (MODE == kGemv)
+    if (here && a.M > 1) go = launch_stream<FMT, MODE, 8, true>;
+  return go(m0, m1, mx, a, ctas, device, stream);
 }
 
 template <int MODE>
-exq_status launch_stream(int format, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx, const Args& a,
-                         int ctas, int device, cudaStream_t stream) {
-  constexpr int A = EXQ_FP4_E4M3, B = EXQ_FP4_E8M0;
-  auto go = format == EXQ_FP4_E4M3 ? (a.M == 1 ? launch_stream<A, MODE, 1> : a.M <= 8 ? launch_stream<A, MODE, 8> : launch_stream<A, MODE, 16>)
-                                   : (a.M == 1 ? launch_stream<B, MODE, 1> : a.M <= 8 ? launch_stream<B, MODE, 8> : launch_stream<B, MODE, 16>);
-  return go(m0, m1, mx, a, ctas, device, stream);
+exq_status launch_stream(int format, bool here, const CUtensorMap& m0, const CUtensorMap& m1, const CUtensorMap& mx,
+                         const Args& a, int ctas, int device, cudaStream_t stream) {
+  return format == EXQ_FP4_E4M3 ? launch_stream<EXQ_FP4_E4M3, MODE>(here, m0, m1, mx, a, ctas, device, stream)
+                                : launch_stream<EXQ_FP4_E8M0, MODE>(here, m0, m1, mx, a, ctas, device, stream);
 }
 
 bool encode_codes(CUtensorMap* map, const void* codes, uint64_t rows, int K, int box_rows) {
@@ -329,11 +350,14 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   const GemvPlan plan(w.format, w.K, M, sms);
   CUtensorMap mw, mx;
   if (!encode_codes(&mw, w.codes, w.rows, w.K, kRows)) return EXQ_ERR_CUDA;
-  if (M == 1)
+  const long long units = static_cast<long long>(div_up(w.rows, kRows)) * div_up(w.K, kUnitK);
+  const int ctas = static_cast<int>(std::min<long long>(units, sms));
+  const bool here = splits(kGemv, M, units, ctas);
+  if (here)
     mx = mw;  // not used
   else if (!encode_codes(&mx, ws + plan.codes, static_cast<uint64_t>(M) * kParts, w.K, M * kParts))
     return EXQ_ERR_CUDA;
-  if (M > 1) {
+  if (!here) {
     PrepareArgs p{};
     p.x = x;
     p.codes = reinterpret_cast<uint32_t*>(ws + plan.codes);
@@ -347,14 +371,13 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   set_shape(a, w.format, w.rows, w.K);
   a.sc0 = w.scales;
   a.x = ws + plan.scales;
-  a.row = x;
+  a.rows_of_x = x;
   a.y = y;
   a.M = M;
   a.factor = w.factor;
   a.counters = static_cast<unsigned*>(workspace);
   a.part = reinterpret_cast<float*>(ws + plan.part);
-  const long long units = static_cast<long long>(a.row_tiles) * a.k_units;
-  return launch_stream<kGemv>(w.format, mw, mw, mx, a, static_cast<int>(std::min<long long>(units, sms)), device, stream);
+  return launch_stream<kGemv>(w.format, here, mw, mw, mx, a, ctas, device, stream);
 }
 
 size_t moe_workspace_bytes(const exq_moe_layer& l, int T, int sms) { return MoePlan(l, T, sms).end; }
@@ -419,13 +442,16 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.down_row_tiles = div_up(D, kRows);
   a.down_k_units = div_up(I, kUnitK);
   a.down_k_tiles = div_up(I, fp4_tile_k(fmt));
-  if ((st = launch_stream<kUp>(fmt, mg, mu, md, a, sms, device, stream)) != EXQ_OK) return st;
+  if ((st = launch_stream<kUp>(fmt, false, mg, mu, md, a, sms, device, stream)) != EXQ_OK) return st;
 
-  p.pieces = ws + plan.h_pieces;
-  p.T = T * l.top_k;
-  p.D = I;
-  p.k_units = div_up(I, kUnitK);
-  if ((st = launch_split_h(fmt, p, stream)) != EXQ_OK) return st;
+  const bool here = splits(kDown, T, 0, sms);
+  if (!here) {
+    p.pieces = ws + plan.h_pieces;
+    p.T = T * l.top_k;
+    p.D = I;
+    p.k_units = div_up(I, kUnitK);
+    if ((st = launch_split_h(fmt, p, stream)) != EXQ_OK) return st;
+  }
 
   set_shape(a, fmt, D, I);
   a.sc0 = l.down.scales;
@@ -435,7 +461,7 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   a.f0 = l.down.factors;
   a.f1 = nullptr;
   a.y = y;
-  return launch_stream<kDown>(fmt, md, md, md, a, sms, device, stream);
+  return launch_stream<kDown>(fmt, here, md, md, md, a, sms, device, stream);
 }
 
 unsigned take_fp4_stream_errors(cudaStream_t stream) {

@@ -28,9 +28,10 @@
 //   warp 0     brings a unit's codes, as one 2-D box (128-byte rows, 128-byte
 //              swizzle), and its scale tiles, as one copy.
 //   warp 6     brings the tokens' parts and their scales (a warp of its own:
-//              behind the weights' copies theirs cost 250 ns a unit). One row
-//              it splits itself, a unit at a time, while the codes arrive, and
-//              warp 11 with it; for more a launch before this one does.
+//              behind the weights' copies theirs cost 250 ns a unit).
+//              Few rows are split here, and there is no launch before this one
+//              that does it: by warps 6 and 11-13, a row of a unit each; if x
+//              is one row, by warps 6 and 11, a unit each.
 //   warps 7-10 write a unit's scales to tensor memory, from shared memory by
 //              way of registers. (The tensor core's own copy, tcgen05.cp, takes
 //              55 clocks a tile and keeps MMAs waiting: 720 clocks a unit for
@@ -56,7 +57,8 @@ enum Mode { kGemv = 0, kUp = 1, kDown = 2 };
 
 constexpr int kRows = 128;           // rows of a unit: the MMA's M
 constexpr int kUnitK = 256;          // k of a unit: 128 bytes of codes a row
-constexpr int kThreads = 12 * 32;
+// of a CTA: the warps above
+__host__ __device__ constexpr int threads_of(int NT, bool here) { return 32 * (!here ? 11 : NT == 1 ? 12 : 14); }
 constexpr int kParts = 8;            // 4-bit rows of a row of x
 constexpr int kMaxTokens = 16;
 constexpr int kMaxPairs = 256;       // tokens x experts of each
@@ -101,7 +103,7 @@ struct Args {
   const uint8_t* sc1;      // of expert 0's up
   size_t sc_stride;        // from expert to expert
   const uint8_t* x;        // gemv: scale tiles of the parts; else pieces [token or pair, unit]
-  const uint16_t* row;     // gemv of one row: x itself
+  const uint16_t* rows_of_x;  // gemv that splits x: [M, K]
   uint16_t* y;             // [M, rows] (not up)
   float* h;                // up: [pairs, rows]
   unsigned* h_most;        // [pairs]: bits of the largest finite magnitude of h
@@ -327,7 +329,7 @@ __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned
   }
   __syncthreads();
 }
-static_assert(kMaxPairs <= kThreads, "a place a thread");
+static_assert(kMaxPairs <= threads_of(1, false), "a place a thread");
 
 __device__ __forceinline__ float activate(float v, int act) {
   if (act == EXQ_ACT_SILU) return v / (1.f + __expf(-v));
@@ -435,13 +437,14 @@ __device__ __forceinline__ void add_parts(float (&v)[W][N], int n, int b0, int b
 // NT: rows of x, at most. (What drains the sums is unrolled over them, and in a
 // short call most of its code is fetched for the first time: one row's is a
 // sixteenth of sixteen's.)
-template <int FMT, int MODE, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+// HERE: x's rows, or the one row of h of an expert, are split in this kernel.
+template <int FMT, int MODE, int NT, bool HERE>
+__global__ void __launch_bounds__(threads_of(NT, HERE), 1)
     stream_kernel(const __grid_constant__ CUtensorMap m0, const __grid_constant__ CUtensorMap m1,
                   const __grid_constant__ CUtensorMap mx, const __grid_constant__ Args a) {
   constexpr int kMatrices = MODE == kUp ? 2 : 1;  // of a unit, a stage each
   constexpr int kVals = NT < 2 ? 2 : NT;           // values of a lane (two tokens' come at a time)
-  constexpr int kTiles = unit_tiles(FMT);
+  constexpr int kTiles = unit_tiles(FMT), kThreads = threads_of(NT, HERE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sums = reinterpret_cast<float*>(smem + kRing);                 // down: [tokens][rows]
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 2);  // the weights' and x's copies
+      mbar_init(smem_u32(&full[s]), 1 + (HERE && NT > 1 ? 4 : 1));  // the weights' copies and x's parts
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&ready[s]), 4);
     }
@@ -487,8 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ids and weights may come from the launch before
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  constexpr bool kOneRow = MODE == kGemv && NT == 1;
-  if constexpr (kOneRow) asm volatile("griddepcontrol.wait;" ::: "memory");  // w may come from the launch before
+  if constexpr (MODE == kGemv && HERE) asm volatile("griddepcontrol.wait;" ::: "memory");  // w may come from the launch before
   if constexpr (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int n_experts = 1, most_tokens = a.M;
   if constexpr (MODE != kGemv) {
@@ -588,52 +590,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = max(0, issued - n_stages); i < issued; ++i)
       for (int r = 0; r < a.wait_limit; ++r)
         if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1))) break;
-  } else if (warp == 6 || warp == 11) {
-    // ------------------------------------------------------------ the tokens' parts
-    const bool leader = elect_one();
-    // they come from the launch before
-    if constexpr (MODE != kUp && !kOneRow) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (kOneRow && !a.starve) {
-      // Each warp takes the units of every second place. (Every second unit
-      // would not do: with an odd number of stages a warp would come to a place
-      // every second time round, and a barrier's parity would tell it nothing.)
+  } else if (HERE && (warp == 6 || warp > 10)) {
+    // ------------------------------------------------------------ rows to parts
+    if constexpr (MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // for h
+    if (!a.starve) {
       constexpr int kWordThreads = fp4_tile_k(FMT) / 8;
-      const int group = warp == 6 ? 0 : 1;
+      constexpr int kMost = (NT + 3) / 4;  // rows of a unit for a warp
+      const int group = warp == 6 ? 0 : warp - 10;
       Place<MODE> at(a, n_experts, u0);
       Turn turn;
       int left = n_mine;
+      // Of one row each warp takes the units of every second place. (Every second unit would not do: with an odd number of
+      // stages a warp would come to a place every second time round, and a barrier's parity would tell it nothing.)
       auto step = [&]() {
         do {
           at.next(a, n_experts);
           turn.next(n_stages);
           --left;
-        } while (left > 0 && (turn.i & 1) != group);
+        } while (NT == 1 && left > 0 && (turn.i & 1) != group);
       };
+      int before = 0;  // rows of the units before: they go to the warps in turn
+      uint4 next[kMost][MODE == kGemv ? 1 : 2];  // (taken apart when it is there, not here)
+      unsigned most[kMost];
+      int mine = 0;    // the first row of this warp, of the unit that `next` is of
       auto load = [&]() {
+        mine = NT == 1 ? 0 : (group - before) & 3;
+        before += a.M;
         const int k = at.kc * kUnitK + 8 * lane;
-        return left > 0 && k < a.K ? __ldg(reinterpret_cast<const uint4*>(a.row + k)) : make_uint4(0u, 0u, 0u, 0u);
-      };
-      if (group == 1) step();
-      uint4 next = load();
-      while (left > 0) {
-        const Turn mine = turn;
-        float q[8];
-        to_f32(next, q);
-        step();
-        next = load();
-        uint32_t words[kParts], scales;
-        split8<FMT>(q, kXTop, lane, words, scales);
-        if (!mbar_wait_warp(smem_u32(&empty[mine.i]), mine.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
-        uint8_t* st = smem + mine.i * stage_bytes;
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint32_t*>(st + kOffX + piece_word(p, 8 * lane)) = words[p];
-        if (lane % kWordThreads < kParts)  // a line of the scale tile for each part
-          *reinterpret_cast<uint32_t*>(st + off_xs + lane / kWordThreads * 512 + lane % kWordThreads * 16) = scales;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor core reads it
+        for (int i = 0; i < kMost; ++i) {
+          const int t = mine + 4 * i;
+          const bool in = t < a.M && k < a.K;
+          const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (MODE == kGemv) {
+            next[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(a.rows_of_x + static_cast<size_t>(t) * a.K + k)) : none;
+          } else {
+            const int pair = ex->place[at.slot][0];  // (of one token)
+            const uint4* src = reinterpret_cast<const uint4*>(a.h + static_cast<size_t>(pair) * a.K + k);
+            next[i][0] = in ? __ldcg(src) : none;
+            next[i][1] = in ? __ldcg(src + 1) : none;
+            most[i] = __ldcg(a.h_most + pair);
+          }
+        }
+      };
+      if (NT == 1 && group == 1) step();
+      if (left > 0) load();
+      while (left > 0) {
+        float q[kMost][8];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          if constexpr (MODE == kGemv) {
+            to_f32(next[i][0], q[i]);
+          } else {
+            const float r = pow2(-h_exponent(most[i]));
+            const uint32_t b[8] = {next[i][0].x, next[i][0].y, next[i][0].z, next[i][0].w,
+                                   next[i][1].x, next[i][1].y, next[i][1].z, next[i][1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[i][j] = __uint_as_float(b[j]) * r;
+          }
+        }
+        const int t0 = mine;
+        const Turn now = turn;
+        step();
+        if (left > 0) load();
+        if (!mbar_wait_warp(smem_u32(&empty[now.i]), now.parity ^ 1u, abort_flag, a.wait_limit, &g_stream_err)) break;
+        uint8_t* st = smem + now.i * stage_bytes;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          const int t = t0 + 4 * i;
+          if (t >= a.M) break;
+          uint32_t words[kParts], scales;
+          split8<FMT>(q[i], MODE == kDown ? kHTop : kXTop, lane, words, scales);
+          uint8_t* piece = st + kOffX + t * 1024;
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) *reinterpret_cast<uint32_t*>(piece + piece_word(p, 8 * lane)) = words[p];
+          const int p = lane % kWordThreads, tile = lane / kWordThreads;  // a line of the scale tile for each part
+          if (p < kParts)
+            *reinterpret_cast<uint32_t*>(MODE == kGemv ? st + off_xs + tile * 512 + fp4_tile_byte(t * kParts + p)
+                                                       : piece + 1024 + tile * kLines + p * 16) = scales;
+        }
+        if (t0 < a.M) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the tensor core reads it
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&full[mine.i]));
+        if (lane == 0) mbar_arrive(smem_u32(&full[now.i]));
       }
-    } else if (!a.starve && warp == 6) {
+    }
+  } else if (!HERE && warp == 6) {
+    // ------------------------------------------------------------ the tokens' parts
+    const bool leader = elect_one();
+    // they come from the launch before
+    if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!a.starve) {
       Place<MODE> at(a, n_experts, u0);
       Turn turn;
       bool ok = true;
@@ -730,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     for (int r = 0; r < a.wait_limit; ++r)
       if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(done), 0))) break;
-  } else if (warp >= 7) {
+  } else if (warp >= 7 && warp <= 10) {
     // ------------------------------------------------------------ scales to tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Place<MODE> at(a, n_experts, u0);
@@ -779,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       at.next(a, n_experts);
     }
-  } else {
+  } else if (warp < 6) {
     // ------------------------------------------------------------ draining the sums
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;

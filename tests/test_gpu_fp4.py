@@ -171,6 +171,19 @@ def test_gemv(env, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(8, 4104, 4384), (6, 4744, 4896), (1, 4744, 9760)])
+def test_gemv_of_many_units(env, fmt, M, N, K):
+    # CTAs with several units, of two rows of tiles
+    exq, torch = env
+    rng = np.random.default_rng(M + N + K + fmt)
+    w, wv = _quantised(exq, torch, rng, N, K, fmt, 0.37 if fmt == 1 else 1.0)
+    x = _activations(rng, M, K, 2)
+    y = exq.exq_fp4_gemv(w, torch.from_numpy(x).cuda())
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    _check_product(y, x.astype(np.float64), wv, 160)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_small_numbers_in_gemv(env, fmt):
     # fp16 subnormals times the smallest scales: nothing is flushed
     exq, torch = env

@@ -410,6 +410,7 @@ namespace {
 int fp4_block_of(int format) { return format == EXQ_FP4_E4M3 ? 16 : format == EXQ_FP4_E8M0 ? 32 : 0; }
 
 constexpr int kFp4MostK = 1 << 25;  // of the few-row products: they count x's values in 32 bits
+constexpr int kFp4Most = 0x7FFFFF00;  // rows and K: rounded up to tiles they are numbers of 32 bits
 
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
@@ -417,6 +418,7 @@ exq_status check_fp4(const exq_fp4_matrix* m) {
   if (!m || !fp4_block_of(m->format) || m->rows < 0 || m->K <= 0 || m->K % 32) return EXQ_ERR_INVALID_ARG;
   if (m->format == EXQ_FP4_E8M0 ? m->factor != 1.f : !(m->factor >= 0x1p-60f && m->factor <= 0x1p60f))
     return EXQ_ERR_INVALID_ARG;
+  if (m->rows > kFp4Most || m->K > kFp4Most) return EXQ_ERR_UNSUPPORTED;
   if (m->rows == 0) return EXQ_OK;  // its memory is not looked at
   if (!m->codes || !m->scales || !aligned16(m->codes) || !aligned16(m->scales)) return EXQ_ERR_INVALID_ARG;
   return EXQ_OK;

@@ -5,7 +5,7 @@
 //   out[t][n] = sum_k x[t][k] w[n][k],   t < 16
 //
 // Every code is read once, so the floor is the codes' and scales' bytes. At
-// 6.8 TB/s an SM gets 47 codes a clock: turning them into fp16 in registers
+// 6.8 TB/s an SM gets some 40 codes a clock: turning them into fp16 in registers
 // costs more instructions than it has (a first kernel on mma.sync reached 2.4
 // TB/s, its integer pipe full). So the codes are never turned into anything:
 // the tensor cores multiply them as they are, and x is brought to their form.

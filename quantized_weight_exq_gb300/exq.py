@@ -1073,7 +1073,10 @@ def exq_quantize_exl2(W, bits, perm=None, stream=None) -> Weight:
 
 
 def exq_get_last_device_error(stream=None) -> int:
-    return int(_lib.exq_get_last_device_error(_stream_ptr(stream)))
+    st = int(_lib.exq_get_last_device_error(_stream_ptr(stream)))
+    if st == EXQ_ERR_TIMEOUT:  # calls that gave up may have left counters: the next ones of the 4-bit products get new workspaces
+        _fp4_ws.clear()
+    return st
 
 
 def exq_testing_starve(wait_rounds: int) -> None:

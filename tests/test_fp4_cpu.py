@@ -85,6 +85,10 @@ def test_quantisers_validate_on_host(exq):
         assert _call("exq_fp4_quantize", x, _matrix(exq), None) == bad
         assert _call("exq_fp4_dequantize", _matrix(exq), x, None) == bad
     assert _call("exq_fp4_quantize", 0x30000, None, None) == bad and _call("exq_fp4_dequantize", None, 0x30000, None) == bad
+    for kw in (dict(rows=0x7FFFFF01), dict(rows=0x7FFFFFFF), dict(K=0x7FFFFF20), dict(K=0x7FFFFFE0)):  # past 32 bits, in whole tiles
+        assert _call("exq_fp4_quantize", 0x30000, _matrix(exq, **kw), None) == exq.EXQ_ERR_UNSUPPORTED, kw
+        assert _call("exq_fp4_dequantize", _matrix(exq, **kw), 0x30000, None) == exq.EXQ_ERR_UNSUPPORTED, kw
+        assert _call("exq_fp4_gemm", _matrix(exq, **kw), _matrix(exq), 0x50000, None) == exq.EXQ_ERR_UNSUPPORTED, kw
     empty = _matrix(exq, rows=0, codes=None, scales=None)
     assert _call("exq_fp4_quantize", None, empty, None) == exq.EXQ_OK
     assert _call("exq_fp4_dequantize", empty, None, None) == exq.EXQ_OK

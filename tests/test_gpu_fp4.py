@@ -383,3 +383,41 @@ def test_waits_run_out_then_recover(env):
     _check_product(exq.exq_fp4_gemv(w, x, workspace=ws), xv.astype(np.float64), wv, 16)
     _check_product(exq.exq_fp4_gemm(a, w), av, wv, 16)
     assert exq.exq_get_last_device_error() == exq.EXQ_OK
+
+
+def test_default_workspace_after_waits_run_out(env):
+    # counters that a call left behind when it gave up are not the next call's
+    exq, torch = env
+    rng = np.random.default_rng(3)
+    w, wv = _quantised(exq, torch, rng, 512, 2048, 1)
+    xv = _activations(rng, 3, 2048, 1)
+    x = torch.from_numpy(xv).cuda()
+    exq.exq_fp4_gemv(w, x)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    exq.exq_testing_starve(64)
+    try:
+        exq.exq_fp4_gemv(w, x)
+        for kept in exq.exq._fp4_ws.values():
+            kept[0][:exq.FP4_COUNTER_BYTES].fill_(1)
+        assert exq.exq_get_last_device_error() == exq.EXQ_ERR_TIMEOUT
+    finally:
+        exq.exq_testing_starve(0)
+    _check_product(exq.exq_fp4_gemv(w, x), xv.astype(np.float64), wv, 16)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 2, 7, 16])
+def test_what_is_not_finite_in_gemv(env, fmt, M):
+    # a row of x with an infinity or a NaN has a NaN row of y, at any place of a block and of a unit; no other changes
+    exq, torch = env
+    rng = np.random.default_rng(M + fmt)
+    w, _ = _quantised(exq, torch, rng, 136, 544, fmt)
+    x = torch.from_numpy(_activations(rng, M, 544, 1)).cuda()
+    clean = exq.exq_fp4_gemv(w, x)
+    assert not torch.isnan(clean).any()
+    for at, v in ((0, float("inf")), (255, float("nan")), (256, float("-inf")), (543, float("nan"))):
+        spoilt, want = x.clone(), clean.clone()
+        spoilt[M - 1, at] = v
+        want[M - 1] = float("nan")
+        torch.testing.assert_close(exq.exq_fp4_gemv(w, spoilt), want, rtol=0, atol=0, equal_nan=True)

@@ -120,12 +120,20 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
       }
     }
   }
+  // the warp's sums: the lanes halve what tokens they have from step to step (one token at a time takes five shuffles each)
+  int d = 16;
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
+  for (int n = TT / 2; n; n >>= 1, d >>= 1) {
+    const bool upper = lane & d;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], d);
-    if (lane == 0) sums[warp][t] = acc[t];
+    for (int t = 0; t < n; ++t) {
+      const float give = upper ? acc[t] : acc[t + n], keep = upper ? acc[t + n] : acc[t];
+      acc[t] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+    }
   }
+#pragma unroll
+  for (; d; d >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], d);
+  if (lane % (32 / TT) == 0) sums[warp][lane / (32 / TT)] = acc[0];
   __syncthreads();
   if (threadIdx.x < a.T) {
     float v = 0.f;

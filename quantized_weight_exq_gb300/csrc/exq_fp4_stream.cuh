@@ -255,16 +255,19 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// 16 columns of this warp's lanes, there after wait_ld of the same registers: several may be on their way
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
-  uint32_t u[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void wait_ld(float (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])::"memory");
 }
 
 // a token's sum from those of its parts
@@ -409,19 +412,32 @@ struct Turn {
   }
 };
 
-// v[w][j] += part j (of n) of matrix w of CTAs b0 .. b1, in their order; several parts' loads are in flight at a time
-template <int W, int N, typename PartOf>
+// v[w][j] becomes the sum of part j (of n) of matrix w of CTAs b0 .. b1, in their order; several parts' loads are in flight at a
+// time. OWN: this CTA's part is what v has; else it is read like the others, which takes fewer registers: the few-row product is
+// to leave room for the next call's small kernel (13 x 4096 x 11008: 13.0 us with 128 registers, 15.5 with 140), and with
+// sixteen tokens an expert's products lost by it what they gained.
+template <bool OWN, int W, int N, typename PartOf>
 __device__ __forceinline__ void add_parts(float (&v)[W][N], int n, int b0, int b1, PartOf part_of) {
   constexpr int kAtOnce = W * N > 32 ? 2 : W * N > 8 ? 4 / W : 8;
+  const int me = OWN ? static_cast<int>(blockIdx.x) : -1;
+  float own[W][N];
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (OWN) own[w][j] = v[w][j];
+      v[w][j] = 0.f;
+    }
   for (int b = b0; b <= b1; b += kAtOnce) {
     float t[kAtOnce][W][N];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
+      const bool load = !OWN || b + i != me;
       const float* p = part_of(min(b + i, b1));
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
-        for (int j = 0; j < N; ++j) t[i][w][j] = j < n ? __ldcg(p + (w * kMaxTokens + j) * kRows) : 0.f;
+        for (int j = 0; j < N; ++j) t[i][w][j] = load && j < n ? __ldcg(p + (w * kMaxTokens + j) * kRows) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
@@ -429,7 +445,7 @@ __device__ __forceinline__ void add_parts(float (&v)[W][N], int n, int b0, int b
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[w][j] += t[i][w][j];
+          for (int j = 0; j < N; ++j) v[w][j] += OWN && b + i == me ? own[w][j] : t[i][w][j];
       }
   }
 }
@@ -444,6 +460,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
                   const __grid_constant__ CUtensorMap mx, const __grid_constant__ Args a) {
   constexpr int kMatrices = MODE == kUp ? 2 : 1;  // of a unit, a stage each
   constexpr int kVals = NT < 2 ? 2 : NT;           // values of a lane (two tokens' come at a time)
+  constexpr bool kOwn = MODE != kGemv && NT <= 8;
   constexpr int kTiles = unit_tiles(FMT), kThreads = threads_of(NT, HERE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -848,6 +865,23 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       auto part_of = [&](int b) {  // a CTA's tile that began before it is its part 0
         return a.part + (static_cast<size_t>(b) * 2 + (b == b0 ? 1 : 0)) * part_floats(MODE) + r;
       };
+      // Whether the tile's other parts are all there, asked while the MMAs still run: those of the CTAs that began with this tile
+      // were their first work. The part then stays in
+      // registers. (5 tokens of 8 of 128 experts: 85.6 us, by the workspace 87.5.)
+      auto others_there = [&]() {
+        if (threadIdx.x == 64) {
+          unsigned n;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(a.counters + tile) : "memory");
+          const int all = n == static_cast<unsigned>(b1 - b0) && !*abort_flag;
+          if (all) a.counters[tile] = 0u;
+          __threadfence();
+          *last = all;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const bool all = *last != 0;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        return all;
+      };
       // after this CTA's part is written: whether all are
       auto last_of_tile = [&]() {
         __threadfence();
@@ -877,6 +911,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       if (MODE == kDown && begins)
         for (int t = 0; t < a.M; ++t) sums[t * kRows + r] = 0.f;
       begins = tile_ends;
+      const bool alone = MODE == kUp && kOwn && left == 1 && b0 != b1 && others_there();
       const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
       tc_fence_after();
       // (the largest h is known: parts made with it have come through the MMAs)
@@ -889,16 +924,19 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       if (ok) {
         const uint32_t d = tmem + lanes + buf.i * buffer_cols;
 #pragma unroll
-        for (int w = 0; w < kMatrices; ++w)
+        for (int j = 0; j < kVals; j += 2) {
+          if (j < n_tok) {
+            float c[kMatrices][16];
 #pragma unroll
-          for (int j = 0; j < kVals; j += 2) {
-            if (j < n_tok) {
-              float c[16];
-              tmem_ld16(d + w * cols + 8 * j, c);
-              v[w][j] = join_parts(c);
-              v[w][j + 1] = join_parts(c + 8);
+            for (int w = 0; w < kMatrices; ++w) tmem_ld16(d + w * cols + 8 * j, c[w]);
+#pragma unroll
+            for (int w = 0; w < kMatrices; ++w) {
+              wait_ld(c[w]);
+              v[w][j] = join_parts(c[w]);
+              v[w][j + 1] = join_parts(c[w] + 8);
             }
           }
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -923,18 +961,16 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       // ---- the tile, or this CTA's part of it
       const int n_val = MODE == kDown ? a.M : n_tok;
       if (b0 != b1) {
-        float* p = part_of(blockIdx.x);
+        if (!alone) {
+          float* p = part_of(blockIdx.x);
 #pragma unroll
-        for (int w = 0; w < kMatrices; ++w)
+          for (int w = 0; w < kMatrices; ++w)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w][j]);
-        if (!last_of_tile()) continue;
-#pragma unroll
-        for (int w = 0; w < kMatrices; ++w)
-#pragma unroll
-          for (int j = 0; j < kVals; ++j) v[w][j] = 0.f;
-        add_parts(v, n_val, b0, b1, part_of);
+            for (int j = 0; j < NT; ++j)
+              if (j < n_val) __stcg(p + (w * kMaxTokens + j) * kRows, v[w][j]);
+          if (!last_of_tile()) continue;
+        }
+        add_parts<kOwn>(v, n_val, b0, b1, part_of);
       }
       if constexpr (MODE == kUp) {
         const int id = ex->expert[slot];

@@ -44,6 +44,11 @@
 // A tile whose units lie in several CTAs goes through the workspace: each
 // writes its part, the last to arrive (a counter) adds them in CTA order, so
 // that the result does not depend on who it is.
+//
+// One row of 28672 x 8192, E8M0: 25.7 us (4.9 TB/s; 6.4 while it streams), of
+// 4096 x 4096: 7.8 us, which is set-up, the first bytes' way and the last sums';
+// sixteen rows of 28672 x 8192, E4M3: 30 us. Experts: 5 tokens of 8 of 128 of
+// 1536 x 4096, E4M3, 85.9 us (4.4 TB/s, 7 while gate and up stream).
 #pragma once
 
 #include "exq_fp4.cuh"
@@ -866,8 +871,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
         return a.part + (static_cast<size_t>(b) * 2 + (b == b0 ? 1 : 0)) * part_floats(MODE) + r;
       };
       // Whether the tile's other parts are all there, asked while the MMAs still run: those of the CTAs that began with this tile
-      // were their first work. The part then stays in
-      // registers. (5 tokens of 8 of 128 experts: 85.6 us, by the workspace 87.5.)
+      // were their first work. The part then stays in registers. (5 tokens of 8 of 128 experts: 85.9 us, by the workspace 87.5.)
       auto others_there = [&]() {
         if (threadIdx.x == 64) {
           unsigned n;

@@ -1,4 +1,4 @@
-"""GB300-native dequantize-fused quantized matmul (GPTQ 4-bit and EXL2).
+"""GB300-native quantized matmul: dequantize-fused (GPTQ 4-bit and EXL2), and microscaled 4-bit floating point with its experts.
 
 The compute path is the C-ABI library ``libexq.so`` (CUDA kernels for
 sm_103a plus C++ host packers); ``exq`` is its ctypes binding. Build it with

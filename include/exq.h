@@ -649,7 +649,8 @@ exq_status exq_solve_exl2_bits(const double* err, int32_t S, int64_t budget, uin
  *    first 128 rows come first, in order of K. Where a tile reaches over the
  *    matrix its bytes are zero (exq_pack_fp4 and exq_fp4_quantize write them).
  * K % 32 == 0 (a row's codes are then a multiple of 16 bytes). Calls with more
- * than 2,147,483,392 rows or a larger K are EXQ_ERR_UNSUPPORTED. */
+ * than 2,147,483,392 rows or a larger K are EXQ_ERR_UNSUPPORTED. What a call
+ * writes may not overlap what it reads. */
 typedef enum { EXQ_FP4_E4M3 = 1, EXQ_FP4_E8M0 = 2 } exq_fp4_format;
 
 typedef struct {

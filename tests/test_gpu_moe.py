@@ -269,3 +269,53 @@ def test_waits_run_out_then_recover(env):
     ws[:exq.FP4_COUNTER_BYTES].zero_()
     assert torch.equal(exq.exq_moe(layer, x, workspace=ws)[0], want)
     assert exq.exq_get_last_device_error() == exq.EXQ_OK
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("T", [1, 2, 13])
+def test_steps_of_a_decode_loop(env, fmt, T):
+    # each call reads what the one before it wrote, weights among it, and begins while that one ends: the bits are those of
+    # calls with a synchronise between them, from the host and from a graph
+    exq, torch = env
+    D = 512
+    ex = Experts(exq, torch, fmt, 12, D, 288, 21)
+    layer = exq.MoeLayer(*ex.parts, top_k=3, router=torch.from_numpy(ex.router).cuda())
+    x0 = torch.from_numpy(ex.x[:T]).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    dense = [torch.randn(D, D, generator=gen, device="cuda").half() / 16 for _ in range(6)]
+    w = exq.exq_fp4_quantize(dense[0], fmt)
+    ws = torch.zeros(max(exq.exq_moe_workspace_size(layer, T), exq.exq_fp4_gemv_workspace_size(w, T)), dtype=torch.uint8, device="cuda")
+    ys = [torch.empty(T, D, dtype=torch.float16, device="cuda") for _ in range(3 * len(dense))]
+    ids, weights = torch.empty(T, 3, dtype=torch.int32, device="cuda"), torch.empty(T, 3, dtype=torch.float32, device="cuda")
+
+    def steps(between):
+        x = x0
+        for i, d in enumerate(dense):
+            a, b, c = ys[3 * i:3 * i + 3]
+            exq.exq_fp4_quantize(d, fmt, out=w), between()
+            exq.exq_fp4_gemv(w, x, out=a, workspace=ws), between()
+            exq.exq_moe(layer, a, ids, weights, out=b, workspace=ws), between()
+            exq.exq_fp4_quantize(b, fmt, out=rows), between()
+            exq.exq_fp4_gemm(rows, w, out=c), between()
+            x = torch.add(x0, c, alpha=2.0 ** -10, out=xs[i])
+
+    xs = torch.empty(len(dense), T, D, dtype=torch.float16, device="cuda")
+    rows = exq.exq_fp4_quantize(x0, fmt)
+    steps(torch.cuda.synchronize)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    want = [y.view(torch.int16).clone() for y in ys]
+    assert all(torch.isfinite(y).all() and y.any() for y in ys)
+    for _ in range(20):
+        for y in ys:
+            y.fill_(float("nan"))
+        steps(lambda: None)
+        assert all(torch.equal(y.view(torch.int16), v) for y, v in zip(ys, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps(lambda: None)
+    for _ in range(20):
+        for y in ys:
+            y.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(y.view(torch.int16), v) for y, v in zip(ys, want))
+    assert not ws[:exq.FP4_COUNTER_BYTES].any()

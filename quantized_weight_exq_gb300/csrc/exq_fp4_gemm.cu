@@ -28,7 +28,10 @@
 // Up to 128 rows of a change places with w: a CTA alone has 128 of its rows and
 // all of a's as the MMA's N (16 .. 128 columns). The product is then bound by
 // the codes of w: single MMAs of few columns take 46 clocks, a pair's 128
-// however few (64 x 8192 x 8192 took 15 us by pairs).
+// however few (64 x 8192 x 8192 took 15 us by pairs). Where tiles are fewer
+// than the SMs a cluster of two to eight CTAs divides a tile's k: each leaves
+// its sums in its shared memory, where its MMAs' operands were, and each adds
+// some columns of all, in order of k.
 //
 // The launch may begin while the one before it ends (its set-up takes 1 us):
 // nothing is read or written before griddepcontrol.wait.
@@ -95,6 +98,7 @@ struct Args {
   int k_units;
   int a_rows, n_tiles;     // tiles of A (of 256 rows, SWAP: 128), and of the product in all
   int n_columns;           // of a tile: 256, or (SWAP) all of B, rounded up to 16
+  int split;               // SWAP: CTAs (a cluster) that have a share of a tile's k each
   int whole_sectors;       // y's rows begin on 32-byte boundaries
   int wait_limit, starve;
 };
@@ -148,6 +152,14 @@ __device__ __forceinline__ void arrive_first(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar) : "memory");
+}
+
+// four fp32 numbers at this address of the cluster's CTA `rank` (several loads are to be on their way: no memory clobber)
+__device__ __forceinline__ float4 peer_load(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank));
+  return v;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -222,7 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % CTAS, pair = blockIdx.x / CTAS, pairs = gridDim.x / CTAS;
+  const int rank = blockIdx.x % CTAS, per_tile = SWAP ? p.split : CTAS;
+  const int pair = blockIdx.x / per_tile, pairs = gridDim.x / per_tile;
+  const int share = SWAP ? blockIdx.x % per_tile : 0;
+  const int u0 = SWAP ? share * p.k_units / p.split : 0, u1 = SWAP ? (share + 1) * p.k_units / p.split : p.k_units;
   const int n_columns = SWAP ? p.n_columns : kTile;
   const Stage stage = SWAP ? stage_of(true, n_columns) : stage_of(false, kTile);
 
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = pair; t < p.n_tiles && ok; t += pairs) {
         const int bt = t / p.a_rows, at = t - bt * p.a_rows;
         const int a_row = at * kARows + rank * 128, b_row = bt * kTile + rank * stage.b_rows;
-        for (int u = 0; u < p.k_units; ++u) {
+        for (int u = u0; u < u1; ++u) {
           if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
             ok = false;
             break;
@@ -307,7 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* sa = p.sa + static_cast<size_t>(a_tile) * p.k_tiles * 512;
         const uint8_t* sb = p.sb + static_cast<size_t>(2 * bt) * p.k_tiles * 512;
         const uint8_t* sb2 = sb + static_cast<size_t>(p.k_tiles) * 512;
-        for (int u = 0; u < p.k_units; ++u) {
+        if constexpr (SWAP) {
+          sa += static_cast<size_t>(u0) * kTilesUnit * 512;
+          sb += static_cast<size_t>(u0) * kTilesUnit * 512;
+        }
+        for (int u = u0; u < u1; ++u) {
           if (!mbar_wait_warp(smem_u32(&empty[turn.i]), turn.parity ^ 1u, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
             ok = false;
             break;
@@ -341,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp(smem_u32(dempty), tile_parity, abort_flag, p.wait_limit, &g_fp4_gemm_err)) break;
         tile_parity ^= 1u;
         tc_fence_after();
-        for (int u = 0; u < p.k_units; ++u) {
+        for (int u = u0; u < u1; ++u) {
           if (!mbar_wait_warp(smem_u32(&ready[turn.i]), turn.parity, abort_flag, p.wait_limit, &g_fp4_gemm_err)) {
             ok = false;
             break;
@@ -356,10 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {  // 64 k: 32 bytes of a row
               if (j >= n_k) break;
               if constexpr (FMT == EXQ_FP4_E4M3)
-                mma_scaled<FMT, CTAS>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + kTileColsB * j, (u | j) != 0);
+                mma_scaled<FMT, CTAS>(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sb + kTileColsB * j, u != u0 || j != 0);
               else  // two scales of the tile's four: byte 0 or 2 of each word
                 mma_scaled<FMT, CTAS>(tmem, ad + 2 * j, bd + 2 * j, (j & 1) ? idesc | (2u << 4) | (2u << 29) : idesc, sa + 4 * (j >> 1),
-                              sb + kTileColsB * (j >> 1), (u | j) != 0);
+                              sb + kTileColsB * (j >> 1), u != u0 || j != 0);
             }
             commit<CTAS>(smem_u32(&empty[turn.i]));
           }
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp - 2) >> 2;
     bool ok = true;
     for (int t = pair; t < p.n_tiles && ok; t += pairs) {
-      for (int u = 0; u < p.k_units; ++u) {
+      for (int u = u0; u < u1; ++u) {
         if ((turn.i & 1) != group) {
           turn.next(stage.n);
           continue;
@@ -439,7 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first<CTAS>(smem_u32(dempty));
-        if (row < p.A) {
+        if (p.split > 1) {  // the ring is free: sums [columns][rows], for the cluster
+          float* sums = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if ((2 * c + half) * 16 < n_columns) sums[((2 * c + half) * 16 + j) * 128] = __uint_as_float(v[c][j]);
+        } else if (row < p.A) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int m0 = (2 * c + half) * 16;
@@ -485,6 +511,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncwarp();
+  if constexpr (SWAP) {
+    if (p.split > 1) {
+      // Each CTA adds some columns of all, in order of k; the last barrier keeps shared memory until it is read.
+      cluster_sync();
+      const int row = pair * 128 + 4 * lane, m0 = share * n_columns / p.split, m1 = (share + 1) * n_columns / p.split;
+      if (warp >= 10 && row < p.A && !*abort_flag) {
+        for (int m = m0 + warp - 10; m < min(m1, p.B); m += 32) {  // four columns at a time, every eighth one
+          float4 v[4] = {};
+          for (int r = 0; r < p.split; ++r) {
+            float4 t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (m + 8 * i < m1) t[i] = peer_load(smem_u32(smem) + (m + 8 * i) * 512 + lane * 16, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (m + 8 * i < m1) v[i] = make_float4(v[i].x + t[i].x, v[i].y + t[i].y, v[i].z + t[i].z, v[i].w + t[i].w);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (m + 8 * i < min(m1, p.B))
+              *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(m + 8 * i) * p.A + row) =
+                  make_uint2(pack_half2(v[i].x * p.factor, v[i].y * p.factor), pack_half2(v[i].z * p.factor, v[i].w * p.factor));
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (CTAS == 2) cluster_sync();  // the other CTA's tensor memory and barriers are in use until here
@@ -498,6 +552,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// CTAs for a tile of up to 128 rows: as many as there are SMs for, in a cluster
+// (of four and eight fewer fit), with four units of k each and more, eight
+// where the sums to join are many. By one CTA and by these: 64 x 8192 x 8192
+// (2) 12.6 and 11.5 us, 64 x 4096 x 11008 (4) 14.4 and 10.0, 64 x 1024 x 8192
+// (8) 11.5 and 7.3, 32 x 4096 x 4096 (4) 7.7 and 6.8; 128 x 4096 x 4096 8.2,
+// with four 9.1.
+int split_of(int n_tiles, int n_columns, int k_units, int sms) {
+  const int least = n_columns > 64 ? 8 : 4;
+  for (int split = 8; split > 1; split /= 2)
+    if (static_cast<long long>(n_tiles) * split <= (split == 2 ? sms : split == 4 ? sms * 6 / 7 : sms * 2 / 3) && k_units >= least * split)
+      return split;
+  return 1;
+}
 
 }  // namespace
 
@@ -527,6 +595,7 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
   p.a_rows = div_up(a.rows, swap ? 128 : kTile);
   p.n_tiles = p.a_rows * div_up(b.rows, kTile);
   p.n_columns = n_columns;
+  p.split = swap ? split_of(p.n_tiles, n_columns, p.k_units, sms) : 1;
   p.whole_sectors = b.rows % 16 == 0 && (reinterpret_cast<uintptr_t>(y) & 31u) == 0;
   const int starve = testing_starve_rounds();
   p.wait_limit = starve > 0 ? starve : kFp4WaitLimit;
@@ -541,7 +610,7 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
       }))
     return EXQ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(swap ? std::min(p.n_tiles, sms) : 2 * std::min(p.n_tiles, std::max(sms / 2, 1)));
+  cfg.gridDim = dim3(swap ? std::min(p.n_tiles * p.split, sms) : 2 * std::min(p.n_tiles, std::max(sms / 2, 1)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
@@ -549,7 +618,7 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = swap ? 1 : 2;
+  at[1].val.clusterDim.x = swap ? p.split : 2;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;

@@ -134,7 +134,9 @@ GEMM_SHAPES = [(1, 8, 32), (1, 128, 64), (5, 8, 96), (128, 256, 256), (129, 264,
                # tiles of 256 x 256: fewer than the SM pairs and more, the last ones ragged
                (2000, 2056, 96), (1030, 4104, 544), (300, 9000, 64), (2300, 2312, 352), (257, 20000, 32), (6000, 1288, 1312),
                # up to 128 rows: more tiles of 128 columns than SMs, odd counts of stages
-               (128, 40008, 1312), (7, 20488, 2336), (100, 30000, 800), (33, 19464, 256)]
+               (128, 40008, 1312), (7, 20488, 2336), (100, 30000, 800), (33, 19464, 256),
+               # up to 128 rows, few tiles: shares of k in clusters of two, four and eight
+               (64, 8192, 1056), (128, 9600, 2080), (17, 4096, 4128), (50, 4104, 8224), (1, 520, 8192), (112, 1536, 8480), (16, 136, 2048)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

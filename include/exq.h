@@ -638,7 +638,7 @@ exq_status exq_solve_exl2_bits(const double* err, int32_t S, int64_t budget, uin
 
 /* A matrix [rows, K] of e2m1 codes (bit 3 the sign; magnitudes 0, 0.5, 1, 1.5,
  * 2, 3, 4, 6 for codes 0..7) with one scale byte for each block along K:
- *  E4M3  blocks of 16, the scale an e4m3 number (without sign), and one fp32
+ *  E4M3  blocks of 16, the scale an e4m3 number (without sign), and one
  *        factor for the whole matrix: value = e2m1(code) * scale * factor
  *  E8M0  blocks of 32, the scale 2^(byte - 127): value = e2m1(code) * scale
  * A NaN scale (e4m3 0x7f, e8m0 0xff) makes its block NaN. Layout:
@@ -657,7 +657,7 @@ typedef struct {
   int32_t format; /* exq_fp4_format                                            */
   int32_t rows;
   int32_t K;
-  float factor;   /* E4M3: of the whole matrix, 2^-60 .. 2^60; E8M0: 1            */
+  double factor;  /* E4M3: of the whole matrix, 2^-60 .. 2^60; E8M0: 1            */
   uint8_t* codes; /* device [rows, K/2]                                        */
   uint8_t* scales;/* device, exq_fp4_scale_bytes(format, rows, K)              */
 } exq_fp4_matrix;
@@ -680,19 +680,21 @@ exq_status exq_pack_fp4(const uint8_t* codes, const uint8_t* scales, int32_t for
  *        448, at least 2^-9 (0 for a block of zeros)
  *  E8M0  s = 2^(floor(log2 a) - 2) (2^-127 for a block of zeros)
  * and each code is the e2m1 number nearest to x / (s factor), ties to the even
- * code, at most 6 in magnitude, with x's sign. Both are decided exactly, not
- * on rounded quotients. A block that holds a NaN or an infinity gets the NaN
+ * code, at most 6 in magnitude, with x's sign. Both are decided on the
+ * quotients in 64 bits (6 factor, s factor and the quotients each rounded to
+ * nearest); of a factor that is a number of 32 bits these are no nearer to a
+ * tie, or farther from it, than the exact ones. A block that holds a NaN or an infinity gets the NaN
  * scale and codes 0. rows = 0 launches nothing.
  * EXQ_ERR_INVALID_ARG for bad pointers (16 bytes), sizes or a factor out of range. */
 exq_status exq_fp4_quantize(const uint16_t* x, const exq_fp4_matrix* out, void* stream);
 
 /* exq_fp4_dequantize -- device, asynchronous: out fp16 [rows, K],
- * fp16_RNE(fp32_RNE(value)); the same rules. */
+ * fp16_RNE(fp32_RNE(e2m1(code) * scale * fp32_RNE(factor))); the same rules. */
 exq_status exq_fp4_dequantize(const exq_fp4_matrix* m, uint16_t* out, void* stream);
 
 /* exq_fp4_gemm -- device, asynchronous: y fp16 [a.rows, w.rows],
- *   y[m][n] = fp16_RNE(a.factor * w.factor * sum_k a[m][k] w[n][k]),
- * on the block-scaled tcgen05 tensor cores, sums in fp32. a and w have one
+ *   y[m][n] = fp16_RNE(fp32_RNE(a.factor * w.factor) * sum_k a[m][k] w[n][k]),
+ * on the block-scaled tcgen05 tensor cores, sums (of code times scale) in fp32. a and w have one
  * format and one K; any a.rows (0 launches nothing), w.rows % 8 == 0. It needs
  * no workspace. A row of a (w) with a NaN scale has a NaN row (column) of y,
  * no other. Deterministic: the same inputs give the same bits.
@@ -711,8 +713,8 @@ size_t exq_fp4_gemv_workspace_size(const exq_fp4_matrix* w, int32_t M);
 
 /* exq_fp4_gemv -- device, asynchronous: y fp16 [M, w.rows] = x . w^T for a few
  * rows x fp16 [M, K], 1 <= M <= 16. x enters the product to 2^-23 of the
- * largest of its block of 16 or 32 (and 2^-25), sums are fp32, w.factor and one
- * rounding come at the end. An infinity or a NaN in a row of x makes that row
+ * largest of its block of 16 or 32 (and 2^-25), sums are fp32, w.factor in fp32
+ * and one rounding come at the end. An infinity or a NaN in a row of x makes that row
  * of y NaN. The codes are read once.
  *   workspace  as above, 256-byte aligned; calls that may overlap on the GPU
  *              need separate ones.

@@ -21,7 +21,7 @@ def fp4_scale_values(scales, fmt):
 def fp4_values(codes, scales, fmt, factor=1.0):
     """codes [rows, K] (0..15) and scale bytes [rows, K / block] -> float64 [rows, K]."""
     s = np.repeat(fp4_scale_values(scales, fmt), FP4_BLOCK[fmt], axis=-1)
-    return E2M1[codes] * s * np.float64(np.float32(factor))
+    return E2M1[codes] * s * np.float64(factor)
 
 
 def _nearest(v, grid):
@@ -32,14 +32,15 @@ def _nearest(v, grid):
 
 
 def fp4_quantize(x, fmt, factor=1.0):
-    """fp16 [rows, K] -> (codes [rows, K], scale bytes [rows, K / block])."""
+    """fp16 [rows, K] -> (codes [rows, K], scale bytes [rows, K / block]); the factor is a number of 64 bits, as are the quotients
+    that decide (6 factor and scale times factor are rounded to 64 bits before them)."""
     x = np.asarray(x, dtype=np.float16).astype(np.float64)
     rows, K = x.shape
     b = x.reshape(rows, -1, FP4_BLOCK[fmt])
     finite = np.isfinite(b).all(-1)
     b = np.where(finite[..., None], b, 0.0)
     a = np.abs(b).max(-1)
-    f = np.float64(np.float32(factor))
+    f = np.float64(factor)
     if fmt == FP4_E4M3:
         byte = np.where(a > 0, np.maximum(_nearest(np.minimum(a / (6 * f), 448.0), E4M3[:127]), 1), 0)
         scale = E4M3[byte] * f

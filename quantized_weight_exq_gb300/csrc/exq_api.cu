@@ -416,7 +416,7 @@ bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) 
 
 exq_status check_fp4(const exq_fp4_matrix* m) {
   if (!m || !fp4_block_of(m->format) || m->rows < 0 || m->K <= 0 || m->K % 32) return EXQ_ERR_INVALID_ARG;
-  if (m->format == EXQ_FP4_E8M0 ? m->factor != 1.f : !(m->factor >= 0x1p-60f && m->factor <= 0x1p60f))
+  if (m->format == EXQ_FP4_E8M0 ? m->factor != 1. : !(m->factor >= 0x1p-60 && m->factor <= 0x1p60))
     return EXQ_ERR_INVALID_ARG;
   if (m->rows > kFp4Most || m->K > kFp4Most) return EXQ_ERR_UNSUPPORTED;
   if (m->rows == 0) return EXQ_OK;  // its memory is not looked at

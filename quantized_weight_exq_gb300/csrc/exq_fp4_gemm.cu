@@ -584,7 +584,7 @@ exq_status launch_fp4_gemm(const exq_fp4_matrix& x, const exq_fp4_matrix& w, uin
   p.sa = a.scales;
   p.sb = b.scales;
   p.y = y;
-  p.factor = a.factor * b.factor;
+  p.factor = static_cast<float>(a.factor * b.factor);
   p.A = a.rows;
   p.B = b.rows;
   p.K = a.K;

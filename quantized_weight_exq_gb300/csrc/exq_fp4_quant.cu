@@ -4,7 +4,8 @@
 // or 17/32 (E8M0) on the other. A quantising thread takes 16 consecutive
 // values (one load of 32 bytes, 8 bytes of codes), so that a warp reads 1 KB in
 // one piece; the scale bytes of 4 blocks of a row leave as one 4-byte word of
-// their tile. 28672 x 8192, E8M0: 92 us there and 94 back, 6.4 TB/s.
+// their tile. 28672 x 8192, E8M0: 90 us there and 94 back, 6.4 TB/s; E4M3: 111
+// there, 130 where many values are ties (a factor of 0.025).
 #include "exq_fp4.cuh"
 
 namespace exq {
@@ -25,20 +26,50 @@ __device__ __forceinline__ float tie_below(int c) {
   return c <= 4 ? 0.5f * c - 0.25f : c == 5 ? 2.5f : c == 6 ? 3.5f : 5.0f;
 }
 
+// A number of 64 bits as the sum of three of 32: 24, 24 and 5 bits.
+struct Divisor {
+  float h, m, l;
+};
+
+// What an E4M3 matrix's factor f is to the quantiser. s f is rounded to 64
+// bits: a scale s is one of 8 numbers in [1, 2) times a power of two, with which
+// the product scales exactly.
+struct Factor {
+  float f, inv6f;
+  Divisor six;       // 6 f
+  Divisor times[8];  // (1 + i / 8) f
+};
+
+// Whether v / d, rounded to 64 bits, goes to the number above the tie t and not
+// to the one below, which is `odd` or even; t has at most 5 bits, v / d is within
+// 2^-18 of it. The quotient rounds to t where it is within half a step of t,
+// whose last bit is even: v - t d is compared with half a step times d. (Below a
+// power of two a step is half as long, but no tie above an odd number is one.)
+// In fp32, whose units are many: e has the sign of v - t d, and is v - t d where
+// that is below 2^-33 of v. The first difference has 11 bits (t h has 29, and 18
+// cancel), the second is rounded only where the third cannot change its sign,
+// the third only where it is far above the last bits of d. (Of an f of 32 bits a
+// difference is zero or above 2^-34 of v: the exact quotient decides.)
+__device__ __forceinline__ bool rounds_up(float v, float t, const Divisor& d, bool odd) {
+  const float e = __fmaf_rn(-t, d.l, __fmaf_rn(-t, d.m, __fmaf_rn(-t, d.h, v)));
+  const float half = __uint_as_float((__float_as_uint(t) & 0x7F800000u) - (53u << 23));
+  const float w = odd ? half : -half;
+  const float over = __fmaf_rn(w, d.m, __fmaf_rn(w, d.h, e));
+  return odd ? over >= 0.f : over > 0.f;
+}
+
 // The e4m3 byte nearest to a / (6 f), ties to even, at least 1 for a > 0. The
-// quotient by a rounded reciprocal is off by less than 2^-21 of itself: where
-// the two ends of that range give one byte it is the right one, else the two
-// are neighbours and the sign of a - 6 f mid, exact in one fma (6 mid has at
-// most 7 bits), decides.
-__device__ __forceinline__ uint32_t scale_byte(float a, float f, float inv6f) {
+// quotient in 32 bits by a rounded reciprocal is off by less than 2^-21 of
+// itself: where the two ends of that range give one byte it is the right one,
+// else the two are neighbours and what lies between them decides.
+__device__ __forceinline__ uint32_t scale_byte(float a, const Factor& f) {
   if (a == 0.f) return 0u;
-  const float u = a * inv6f;
+  const float u = a * f.inv6f;
   const uint32_t both = e4m3x2(u * (1.f + 0x1p-20f), u * (1.f - 0x1p-20f));
   uint32_t lo = both & 0xFFu, hi = both >> 8;
   if (lo != hi) {
     const float mid = 0.5f * (e4m3_f32(lo) + e4m3_f32(hi));
-    const float d = __fmaf_rn(-6.f * mid, f, a);
-    lo = d > 0.f ? hi : d < 0.f ? lo : (lo & 1u) ? hi : lo;
+    if (rounds_up(a, mid, f.six, lo & 1u)) lo = hi;
   }
   return max(lo, 1u);
 }
@@ -64,10 +95,11 @@ struct Walk {
   }
 };
 
+// (Six blocks an SM, 40 registers: with 44 E4M3 takes 122 us, not 111.)
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __restrict__ x, uint2* __restrict__ codes,
-                                                            uint32_t* __restrict__ scales, int rows, int K, float f,
-                                                            float inv6f, bool wide) {
+__global__ void __launch_bounds__(kThreads, 6) quantize_kernel(const uint16_t* __restrict__ x, uint2* __restrict__ codes,
+                                                            uint32_t* __restrict__ scales, int rows, int K, bool wide,
+                                                            const __grid_constant__ Factor f) {
   constexpr int kPer = fp4_tile_k(FMT) / 16;  // threads of one scale word: 4 or 8
   begin();
   const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);
@@ -113,9 +145,9 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
       v[2 * j + 1] = t.y;
     }
     if constexpr (FMT == EXQ_FP4_E4M3) {
-      byte = finite ? scale_byte(a, f, inv6f) : 0x7Fu;
+      byte = finite ? scale_byte(a, f) : 0x7Fu;
       const float s = e4m3_f32(byte);
-      const float r = a > 0.f ? 1.f / (s * f) : 0.f;
+      const float r = a > 0.f ? 1.f / (s * f.f) : 0.f;
       // as for the scale: a code that both ends of the quotient's range give is right
       const float rl = r * (1.f - 0x1p-20f), rh = r * (1.f + 0x1p-20f);
       float lo[8], hi[8];
@@ -128,15 +160,16 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
       c1 = e2m1x8(lo);
       uint32_t d1 = c1 ^ e2m1x8(hi);
       if (d0 | d1) {
-        // the code is the lower one's or the next: the sign of |x| - tie s f, exact in one fma
+        // the code is the lower one's or the next
+        const uint32_t bits = __float_as_uint(s);
+        const Divisor& d = f.times[(bits >> 20) & 7u];
+        const float power = __uint_as_float(bits & 0x7F800000u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int sh = 4 * (j & 7);
-          const uint32_t d = ((j < 8 ? d0 : d1) >> sh) & 0xFu;
-          if (d) {
+          if (((j < 8 ? d0 : d1) >> sh) & 0xFu) {
             const uint32_t c = ((j < 8 ? c0 : c1) >> sh) & 7u;
-            const float e = __fmaf_rn(-tie_below(static_cast<int>(c) + 1) * s, f, fabsf(v[j]));
-            if (e > 0.f || (e == 0.f && (c & 1u))) (j < 8 ? c0 : c1) += 1u << sh;
+            if (rounds_up(fabsf(v[j]), tie_below(static_cast<int>(c) + 1) * power, d, c & 1u)) (j < 8 ? c0 : c1) += 1u << sh;
           }
         }
       }
@@ -247,6 +280,14 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint4* __res
 // whether rows of 32-byte pieces from here can be read and written by the piece (16 bytes are what is asked of callers)
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+Divisor split(double d) {
+  Divisor r;
+  r.h = static_cast<float>(d);
+  r.m = static_cast<float>(d - r.h);
+  r.l = static_cast<float>(d - r.h - r.m);
+  return r;
+}
+
 int blocks_for(long long threads, int sms) {
   const long long b = (threads + kThreads - 1) / kThreads;
   return static_cast<int>(b < 16LL * sms ? b : 16LL * sms);
@@ -258,15 +299,20 @@ exq_status launch_fp4_quantize(const uint16_t* x, const exq_fp4_matrix& m, int s
   const int words = (m.K + fp4_tile_k(m.format) - 1) / fp4_tile_k(m.format);
   const long long threads = static_cast<long long>((m.rows + 127) / 128) * 128 * words * (fp4_tile_k(m.format) / 16);
   auto fn = m.format == EXQ_FP4_E4M3 ? quantize_kernel<EXQ_FP4_E4M3> : quantize_kernel<EXQ_FP4_E8M0>;
+  Factor f;
+  f.f = static_cast<float>(m.factor);
+  f.inv6f = static_cast<float>(1. / (6. * m.factor));
+  f.six = split(6. * m.factor);
+  for (int i = 0; i < 8; ++i) f.times[i] = split((1. + i / 8.) * m.factor);
   return launch_dependent(fn, blocks_for(threads, sms), kThreads, 0, stream, x, reinterpret_cast<uint2*>(m.codes),
-                          reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K, m.factor, 1.f / (6.f * m.factor), aligned32(x));
+                          reinterpret_cast<uint32_t*>(m.scales), m.rows, m.K, aligned32(x), f);
 }
 
 exq_status launch_fp4_dequantize(const exq_fp4_matrix& m, uint16_t* out, int sms, cudaStream_t stream) {
   auto fn = m.format == EXQ_FP4_E4M3 ? dequantize_kernel<EXQ_FP4_E4M3> : dequantize_kernel<EXQ_FP4_E8M0>;
   return launch_dependent(fn, blocks_for(static_cast<long long>(m.rows) * (m.K / 32), sms), kThreads, 0, stream,
                           reinterpret_cast<const uint4*>(m.codes), static_cast<const uint8_t*>(m.scales), out, m.rows, m.K,
-                          m.factor, aligned32(out));
+                          static_cast<float>(m.factor), aligned32(out));
 }
 
 }  // namespace exq

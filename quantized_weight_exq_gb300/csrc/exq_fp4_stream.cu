@@ -382,7 +382,7 @@ exq_status launch_fp4_gemv(const exq_fp4_matrix& w, const uint16_t* x, int M, ui
   a.rows_of_x = x;
   a.y = y;
   a.M = M;
-  a.factor = w.factor;
+  a.factor = static_cast<float>(w.factor);
   a.counters = static_cast<unsigned*>(workspace);
   a.part = reinterpret_cast<float*>(ws + plan.part);
   return launch_stream<kGemv>(w.format, here, mw, mw, mx, a, ctas, device, stream);

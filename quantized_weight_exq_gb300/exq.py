@@ -92,7 +92,7 @@ class exq_kv_batch(ctypes.Structure):
 
 class exq_fp4_matrix(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("format", "rows", "K")] + [
-        ("factor", ctypes.c_float), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+        ("factor", ctypes.c_double), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class exq_fp4_experts(ctypes.Structure):
@@ -770,7 +770,8 @@ def _fp4_tensors(where: str, codes, scales, lead: tuple, format: int):
 
 class Fp4Matrix:
     """A matrix [rows, K] in the 4-bit format on the GPU: codes uint8 [rows, K / 2], scales uint8 [exq_fp4_scale_bytes] in tiles
-    (exq_pack_fp4, exq_fp4_quantize), and the factor of an E4M3 one."""
+    (exq_pack_fp4, exq_fp4_quantize), and the factor of an E4M3 one, a float of 64 bits as the caller gave it (the quantiser decides
+    with it; where values are multiplied by it, it is rounded to 32 bits)."""
 
     __slots__ = "rows", "K", "format", "factor", "device", "_buf", "_codes", "_scales", "_desc", "_ref", "_space"
 

@@ -173,3 +173,14 @@ def test_units_have_one_owner():
         u = np.arange(n, dtype=np.int64)
         owner = ((u + 1) * ctas - 1) // n
         np.testing.assert_array_equal(owner, np.searchsorted(start, u, side="right") - 1)
+
+
+def test_factor_has_64_bits(exq):
+    # the caller's number, not the nearest of 32 bits: 0.025 * 1.25 is 2^-5 in 64 bits only
+    assert exq.exq_fp4_matrix(1, 1, 32, 0.025, None, None).factor == 0.025
+    x = np.zeros((1, 32), np.float16)
+    x[0, :16:2], x[0, 1] = 0.0390625, 0.1875                     # a tie (1.25 * 2^-5) of a block whose scale is 1.25
+    codes, scales = O.fp4_quantize(x, 1, 0.025)
+    assert O.fp4_scale_values(scales, 1)[0, 0] == 1.25 and codes[0, 0] == 2
+    codes, _ = O.fp4_quantize(x, 1, np.nextafter(0.025, 0))      # the next number down: above the tie
+    assert codes[0, 0] == 3

@@ -423,3 +423,37 @@ def test_what_is_not_finite_in_gemv(env, fmt, M):
         spoilt[M - 1, at] = v
         want[M - 1] = float("nan")
         torch.testing.assert_close(exq.exq_fp4_gemv(w, spoilt), want, rtol=0, atol=0, equal_nan=True)
+
+
+def _blocks_at_ties(factor):
+    """E4M3 blocks of every fp16 number as the largest, with the numbers at and next to the ties of its scale and factor."""
+    top = np.arange(0x7C00, dtype=np.uint16).view(np.float16)
+    x = np.zeros((top.size, 16), np.float16)
+    x[:, 0] = top
+    s = O.fp4_scale_values(O.fp4_quantize(np.repeat(x, 2, 1), 1, factor)[1], 1)[:, :1]
+    with np.errstate(over="ignore"):
+        near = np.clip(s * factor * [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], 0, 65504).astype(np.float16)
+    near = np.minimum(near, top[:, None])
+    x[:, 1:8] = near
+    x[:, 8:15] = -np.minimum(np.nextafter(near, np.float16(65504)), top[:, None])
+    return np.concatenate([x, -x], 1)
+
+
+@pytest.mark.parametrize("factor", [0.025, 0.0125, 0.05, 0.1, 0.2, 0.3, 1 / 6, 0.7, 1 / 3, 2.5e-5, 1e10, 0.021 + 0.001 * 4])
+def test_quantize_with_a_factor_of_64_bits(env, factor):
+    # such factors times a scale are, in 64 bits, numbers that fp16 values are ties of: rounded to 32 bits first they are not
+    exq, torch = env
+    x = _blocks_at_ties(factor)
+    m = exq.exq_fp4_quantize(torch.from_numpy(x).cuda(), 1, factor)
+    assert m.factor == factor
+    codes, scales = _check_quantised(m, x, 1, factor)
+    if factor not in (2.5e-5, 1e10):  # (one has no ties, the other 32 bits)
+        rounded = O.fp4_quantize(x, 1, float(np.float32(factor)))
+        assert (rounded[0] != codes).any() or (rounded[1] != scales).any()  # the test can tell
+    np.testing.assert_array_equal(exq.exq_fp4_dequantize(m).cpu().numpy(), _f32_product(O.fp4_values(codes, scales, 1), factor))
+    rng = np.random.default_rng(int(factor * 1e4) % 1000)
+    x = _activations(rng, 64, 8192)
+    _check_quantised(exq.exq_fp4_quantize(torch.from_numpy(x).cuda(), 1, factor, out=None), x, 1, factor)
+    out = exq.Fp4Matrix(torch.zeros(64, 4096, dtype=torch.uint8, device="cuda"),
+                        torch.zeros(exq.exq_fp4_scale_bytes(1, 64, 8192), dtype=torch.uint8, device="cuda"), 1, factor)
+    _check_quantised(exq.exq_fp4_quantize(torch.from_numpy(x).cuda(), 1, out=out), x, 1, factor)

@@ -704,7 +704,10 @@ exq_status exq_fp4_gemm(const exq_fp4_matrix* a, const exq_fp4_matrix* w, uint16
 /* The workspaces of exq_fp4_gemv and exq_moe start with counters: ZERO-FILL
  * this many bytes before the first use. Every call that completes leaves them
  * zero, so that one workspace serves any sequence of calls of either on one
- * stream; one that ended in EXQ_ERR_TIMEOUT may not: zero-fill them again. */
+ * stream; one that ended in EXQ_ERR_TIMEOUT may not: zero-fill them again. A
+ * call is up to four launches that pass data through the workspace: another
+ * call with the same one, by another host thread, may not begin before it has
+ * returned. */
 #define EXQ_FP4_COUNTER_BYTES ((size_t)128 << 10)
 
 /* Bytes of device workspace exq_fp4_gemv needs on the current device; 0 for an

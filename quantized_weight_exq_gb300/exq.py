@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 from dataclasses import dataclass, field
 from pathlib import Path
 from typing import Optional
@@ -733,11 +734,18 @@ FP4_COUNTER_BYTES = 128 << 10  # EXQ_FP4_COUNTER_BYTES
 
 # (device index, stream handle) -> (workspace of exq_fp4_gemv and exq_moe, its address and bytes); its counters are zero between calls
 _fp4_ws = {}
+_fp4_locks = {}
+
+
+def _fp4_lock(dev: int, handle: int):
+    """Held by the host thread that has the default workspace of a stream, from before it is looked up until the call's launches
+    are all made: they pass data through it, and another thread's may not come between them, nor another workspace be put in its place."""
+    return _fp4_locks.get((dev, handle)) or _fp4_locks.setdefault((dev, handle), threading.RLock())
 
 
 def _fp4_workspace(need: int, dev: int, stream, handle: int, where: str):
-    """(address, bytes) of the default workspace of the launch's stream, its counters zeroed in that stream's order; kept and grown
-    across calls. Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
+    """(memory, address, bytes) of the default workspace of the launch's stream, its counters zeroed in that stream's order; kept and
+    grown across calls, under _fp4_lock. Refused while the stream is captured: a graph needs a workspace that lives as long as it does."""
     import torch
     if stream is not None:
         with _on(stream, dev):
@@ -749,7 +757,7 @@ def _fp4_workspace(need: int, dev: int, stream, handle: int, where: str):
         buf = torch.empty(max(need, 8 << 20), dtype=torch.uint8, device=f"cuda:{dev}")
         buf[:FP4_COUNTER_BYTES].zero_()
         kept = _fp4_ws[dev, handle] = buf, buf.data_ptr(), buf.numel()
-    return kept[1:]
+    return kept
 
 
 def exq_fp4_scale_bytes(format: int, rows: int, K: int) -> int:
@@ -897,7 +905,8 @@ def exq_fp4_gemv_workspace_size(w: Fp4Matrix, M: int) -> int:
 
 def exq_fp4_gemv(w: Fp4Matrix, x, out=None, workspace=None, stream=None):
     """x . w^T as fp16 [M, w.rows] for up to 16 rows x fp16 [M, K], which are not quantised. Without ``workspace`` one is kept for
-    each stream that calls are launched on. A call that a graph captures needs one of its own, its first FP4_COUNTER_BYTES zero,
+    each stream that calls are launched on (calls of several host threads on one stream take turns). One that is given is for one
+    call at a time: threads that share it take turns themselves. A call that a graph captures needs one of its own, its first FP4_COUNTER_BYTES zero,
     for as long as the graph is replayed."""
     import torch
     where = "exq_fp4_gemv"
@@ -914,10 +923,13 @@ def exq_fp4_gemv(w: Fp4Matrix, x, out=None, workspace=None, stream=None):
         need = w._space.get(M)  # what M rows need, of a matrix of this shape
         if need is None:
             need = w._space[M] = _lib.exq_fp4_gemv_workspace_size(w._ref, M)
-        ws, n = _fp4_workspace(need, dev, stream, handle, where)
+        with _fp4_lock(dev, handle):
+            _kept, ws, n = _fp4_workspace(need, dev, stream, handle, where)
+            status = _lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle)
     else:
         ws, n = _space(workspace, dev, where)
-    _check(_lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle), where)
+        status = _lib.exq_fp4_gemv(w._ref, x.data_ptr(), M, out.data_ptr(), ws, n, handle)
+    _check(status, where)
     return out
 
 
@@ -988,10 +1000,13 @@ def exq_moe(layer: MoeLayer, x, ids=None, weights=None, out=None, workspace=None
         need = layer._space.get(T)
         if need is None:
             need = layer._space[T] = _lib.exq_moe_workspace_size(layer._ref, T)
-        ws, n = _fp4_workspace(need, dev, stream, handle, where)
+        with _fp4_lock(dev, handle):
+            _kept, ws, n = _fp4_workspace(need, dev, stream, handle, where)
+            status = _lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle)
     else:
         ws, n = _space(workspace, dev, where)
-    _check(_lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle), where)
+        status = _lib.exq_moe(layer._ref, x.data_ptr(), T, ids.data_ptr(), weights.data_ptr(), out.data_ptr(), ws, n, handle)
+    _check(status, where)
     return out, ids, weights
 
 
@@ -1076,7 +1091,9 @@ def exq_quantize_exl2(W, bits, perm=None, stream=None) -> Weight:
 def exq_get_last_device_error(stream=None) -> int:
     st = int(_lib.exq_get_last_device_error(_stream_ptr(stream)))
     if st == EXQ_ERR_TIMEOUT:  # calls that gave up may have left counters: the next ones of the 4-bit products get new workspaces
-        _fp4_ws.clear()
+        for key in list(_fp4_ws):
+            with _fp4_lock(*key):
+                _fp4_ws.pop(key, None)
     return st
 
 

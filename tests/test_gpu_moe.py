@@ -319,3 +319,43 @@ def test_steps_of_a_decode_loop(env, fmt, T):
         graph.replay()
         assert all(torch.equal(y.view(torch.int16), v) for y, v in zip(ys, want))
     assert not ws[:exq.FP4_COUNTER_BYTES].any()
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_threads_on_one_stream(env, fmt):
+    # host threads whose calls of several launches share a stream's default workspace: the bits are those of calls one by one
+    import threading
+    exq, torch = env
+    ex = Experts(exq, torch, fmt, 12, 512, 288, 23 + fmt)
+    layer = exq.MoeLayer(*ex.parts, top_k=3, router=torch.from_numpy(ex.router).cuda())
+    gen = torch.Generator(device="cuda").manual_seed(fmt)
+    w = exq.exq_fp4_quantize(torch.randn(2056, 1024, generator=gen, device="cuda").half() / 16, fmt)
+    xs = [torch.randn(m, 1024, generator=gen, device="cuda").half() for m in (16, 9, 16, 3)]
+    ts = [torch.randn(t, 512, generator=gen, device="cuda").half() for t in (16, 5, 1, 13)]
+    jobs = [lambda x=x: [exq.exq_fp4_gemv(w, x)] for x in xs] + [lambda x=x: exq.exq_moe(layer, x) for x in ts]
+    exq.exq._fp4_ws.clear()  # so that it grows again while the threads run
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in job()] for job in jobs]
+    torch.cuda.synchronize()
+    exq.exq._fp4_ws.clear()
+    got, errors = [[] for _ in jobs], []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(50):
+                got[i].append(jobs[i]())
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and exq.exq_get_last_device_error() == exq.EXQ_OK
+    for results, ref in zip(got, want):
+        assert len(results) == 50
+        for r in results:
+            assert all(torch.equal(a, b) for a, b in zip(r, ref))

@@ -761,9 +761,11 @@ size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T);
  *   weights[t][j] = exp(logit - max) / sum (see renorm);
  *   y[t] = fp16_RNE(sum_j weights[t][j] * (act(x gate^T) * (x up^T)) down^T)
  * with the experts' products over x as it is and fp32 sums. What lies between
- * the products is held to 2^-23 of the largest of its block; weights and
- * factors are applied in fp32 after the sums. An infinity or a NaN in a token
- * makes its result NaN.
+ * the products, h, is held to 2^-23 of the largest of its block of 16 or 32,
+ * with e4m3 scales plus 2^-40 of the token's largest h of that expert (2^-140 if
+ * that is below 2^-100); weights and factors are applied in fp32 after the sums.
+ * An infinity or a NaN in a token makes its result NaN, and so does an h beyond
+ * fp32's range.
  *   ids      device int32 [T, top_k], weights device fp32 [T, top_k]: written
  *            when the layer has a router, read when it has none. An id of -1
  *            is an unused place; one that repeats counts each time; another

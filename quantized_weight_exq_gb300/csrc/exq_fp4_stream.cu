@@ -54,7 +54,7 @@ __device__ __forceinline__ void split_rows(const PrepareArgs& a) {
       if constexpr (H) {
         const float4* src = reinterpret_cast<const float4*>(a.h + static_cast<size_t>(t) * a.D + 8 * c);
         const float4 u = __ldcg(src), v = __ldcg(src + 1);
-        const float r = pow2(-h_exponent(__ldcg(a.h_most + t)));
+        const float r = h_scale(__ldcg(a.h_most + t));
         q[0] = u.x * r; q[1] = u.y * r; q[2] = u.z * r; q[3] = u.w * r;
         q[4] = v.x * r; q[5] = v.y * r; q[6] = v.z * r; q[7] = v.w * r;
       } else {

@@ -99,7 +99,8 @@ constexpr int kMaxBuffers = 4;
 // that is 2^8, e4m3's largest power), and a block whose scale would be under
 // the smallest takes that one, 2^-3: its eighth part counts 2^-25 then, half of
 // fp16's smallest number. What lies between an expert's products (h) is
-// divided by a power of two first that brings a token's largest to [1, 2).
+// divided by a power of two first that brings a token's largest to [1, 2) (below
+// 2^-100: by 2^-100): the smallest scale is 2^-18 then, and 2^-40 is left of it.
 constexpr int kXTop = 14, kHTop = -1;          // exponents of the largest scales
 __host__ __device__ constexpr int e4m3_shift(int top) { return top - 8; }
 
@@ -167,10 +168,16 @@ __device__ __forceinline__ uint32_t part_scale_byte(int e, int top) {
 }
 
 // h's power of two: e of [2^e, 2^(e + 1)) for the largest magnitude, given as bits
-__device__ __forceinline__ int h_exponent(unsigned most) { return min(max(static_cast<int>(most >> 23) - 127, -100), 126); }
+__device__ __forceinline__ int h_exponent(unsigned most) { return max(static_cast<int>(most >> 23) - 127, -100); }
 
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// what h is multiplied by: 2^-e, for e = 127 a subnormal number
+__device__ __forceinline__ float h_scale(unsigned most) {
+  const int e = h_exponent(most);
+  return e == 127 ? __uint_as_float(0x00400000u) : pow2(-e);
+}
 
 // Eight values of a row as words of codes of the parts, and the scale word
 // that they share with the 8 (E4M3) or 16 threads of four blocks; `c` counts
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
           if constexpr (MODE == kGemv) {
             to_f32(next[i][0], q[i]);
           } else {
-            const float r = pow2(-h_exponent(most[i]));
+            const float r = h_scale(most[i]);
             const uint32_t b[8] = {next[i][0].x, next[i][0].y, next[i][0].z, next[i][0].w,
                                    next[i][1].x, next[i][1].y, next[i][1].z, next[i][1].w};
 #pragma unroll
@@ -910,7 +917,6 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       if (MODE == kDown && lane < n_tok) {
         place = ex->place[slot][nth_bit(tokens, lane)];
         f = ex->weight[place] * (a.f0 ? __ldg(a.f0 + ex->expert[slot]) : 1.f);
-        if (FMT == EXQ_FP4_E4M3) f *= pow2(e4m3_shift(kHTop));
       }
       if (MODE == kDown && begins)
         for (int t = 0; t < a.M; ++t) sums[t * kRows + r] = 0.f;
@@ -919,7 +925,8 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
       const bool ok = mbar_wait_warp(smem_u32(&dfull[buf.i]), buf.parity, abort_flag, a.wait_limit, &g_stream_err);
       tc_fence_after();
       // (the largest h is known: parts made with it have come through the MMAs)
-      if (MODE == kDown && lane < n_tok) f *= pow2(h_exponent(__ldcg(a.h_most + place)));
+      if (MODE == kDown && lane < n_tok)
+        f *= pow2(h_exponent(__ldcg(a.h_most + place)) + (FMT == EXQ_FP4_E4M3 ? e4m3_shift(kHTop) : 0));
       float v[kMatrices][kVals];  // the row's values: token by token; up: gate's and up's
 #pragma unroll
       for (int w = 0; w < kMatrices; ++w)

@@ -359,3 +359,92 @@ def test_threads_on_one_stream(env, fmt):
         assert len(results) == 50
         for r in results:
             assert all(torch.equal(a, b) for a, b in zip(r, ref))
+
+
+def _layer_of(exq, torch, fmt, parts, top_k, act=0):
+    """A layer from (codes [E, rows, K], scale bytes, factors or None) of gate, up and down, and their values in 64 bits."""
+    made, values = [], []
+    for codes, scales, factors in parts:
+        codes, scales = codes.astype(np.uint8), scales.astype(np.uint8)
+        packed = [exq.exq_pack_fp4(c, s, fmt) for c, s in zip(codes, scales)]
+        made.append(exq.Fp4Experts(torch.from_numpy(np.stack([p for p, _ in packed])).cuda(), torch.from_numpy(np.stack([t for _, t in packed])).cuda(),
+                                   fmt, None if factors is None else torch.from_numpy(np.float32(factors)).cuda()))
+        values.append(np.stack([O.fp4_values(c, s, fmt, 1.0 if factors is None else factors[e]) for e, (c, s) in enumerate(zip(codes, scales))]))
+    return exq.MoeLayer(*made, top_k=top_k, act=act), values
+
+
+def _power(fmt, e):
+    """(a scale byte and a factor that are 2^e together, the factor None for E8M0)"""
+    return (0x38, 2.0 ** e) if fmt == 1 else (127 + e, None)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("T", [1, 2, 12])
+def test_h_up_to_the_largest_numbers(env, fmt, T):
+    # h up to 1.92 * 2^127, brought back by down's scales and the tokens' weights
+    exq, torch = env
+    rng = np.random.default_rng(T + fmt)
+    D, I, block = 32, 96, O.FP4_BLOCK[fmt]
+    gate, up = np.zeros((1, I, D)), np.zeros((1, I, D))
+    gate[0, :, 0], up[0, :, 0] = 3, rng.integers(1, 3, I)      # 1.5; 0.5 or 1
+    up[0, 5, 0] = 2
+    up[0, :, 0] += 8 * rng.integers(0, 2, I)
+    down = rng.integers(0, 16, (1, D, I))
+    (sg, fg), (su, fu), (sd, fd) = (_power(fmt, e) for e in (63, 63, -100))
+    parts = [(c, np.full((1, c.shape[1], c.shape[2] // block), s), None if f is None else [f])
+             for c, s, f in ((gate, sg, fg), (up, su, fu), (down, sd, fd))]
+    layer, (gv, uv, dv) = _layer_of(exq, torch, fmt, parts, 1)
+    x = np.zeros((T, D), np.float16)
+    x[:, 0] = np.resize([1.29, 1.6, 1.25, 1.15], T)
+    weights = np.full((T, 1), 2.0 ** -24, np.float32)
+    y, _, _ = exq.exq_moe(layer, torch.from_numpy(x).cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.from_numpy(weights).cuda())
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    for t in range(T):
+        h = (gv[0] @ x[t].astype(np.float64)) * (uv[0] @ x[t].astype(np.float64))  # (SiLU of what is so large is itself)
+        assert 2.0 ** 126 < np.abs(h).max() < 2.0 ** 128 and (t % 4 == 3 or np.abs(h).max() > 2.0 ** 127)
+        ref, size = dv[0] @ h * 2.0 ** -24, np.abs(dv[0]) @ np.abs(h) * 2.0 ** -24
+        assert 1 < np.abs(ref).max() < 65504
+        # gate's and up's sums have one term: h is off by its own rounding, 2^-24, and by 2^-23 of its block's largest (at most
+        # twice itself); then the sums' roundings and the result's
+        tol = 0.5 * ulp16(ref) * (1 + 2.0 ** -8) + ((I / 16 + 170) * 2.0 ** -23 + 2.0 ** -24 + 2.0 ** -22) * size
+        assert (np.abs(y[t].cpu().numpy().astype(np.float64) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("T", [1, 3])
+def test_h_of_mixed_sizes(env, fmt, T):
+    # one channel of h far above the other blocks, which alone reach the result: each is held to 2^-23 of its block's largest,
+    # with e4m3 scales plus 2^-40 of the token's
+    exq, torch = env
+    rng = np.random.default_rng(T + fmt)
+    D, I, block = 32, 160, O.FP4_BLOCK[fmt]
+    gate = rng.integers(1, 8, (1, I, D)) + 8 * rng.integers(0, 2, (1, I, D))
+    up = rng.integers(1, 8, (1, I, D)) + 8 * rng.integers(0, 2, (1, I, D))
+    down = rng.integers(0, 16, (1, D, I))
+    gate[:, 0] &= 7
+    up[:, 0] &= 7
+    down[:, :, :block] = 0
+    su = np.full((1, I, D // block), 0x28 if fmt == 1 else 120)  # 2^-2, 2^-7
+    for j in range(block, I, block):                             # blocks of h from 2^-9 to 2^-16 down (e4m3: of normal scales), or 2^-60
+        su[0, j:j + block] = 0x10 - 8 * (j // block % 2) if fmt == 1 else 120 - 15 * (j // block)
+    sg = np.full_like(su, 0x38 if fmt == 1 else 127)
+    su[0, 0], sg[0, 0] = (0x78, 0x78) if fmt == 1 else (150, 127)  # channel 0: 2^8 and 2^8, or 2^23
+    sd = np.full((1, D, I // block), 0x38 if fmt == 1 else 127 + 20)
+    f = [[1.0] if fmt == 1 else None] * 3
+    layer, (gv, uv, dv) = _layer_of(exq, torch, fmt, list(zip((gate, up, down), (sg, su, sd), f)), 1)
+    x = np.abs(rng.standard_normal((T, D))).astype(np.float16)
+    w = np.ones((T, 1), np.float32)
+    y, _, _ = exq.exq_moe(layer, torch.from_numpy(x).cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.from_numpy(w).cuda())
+    for t in range(T):
+        xt = x[t].astype(np.float64)
+        g, u = gv[0] @ xt, uv[0] @ xt
+        h = O.moe_activate(g, 0) * u
+        largest = np.repeat(np.abs(h).reshape(-1, block).max(1), block)
+        assert np.abs(h).max() > 2.0 ** 16 * np.abs(h[block:]).max()
+        eg, eu = (np.abs(m[0]) @ np.abs(xt) * ((D / 16 + 170) * 2.0 ** -23) for m in (gv, uv))
+        off = 1.13 * eg * (np.abs(u) + eu) + np.abs(O.moe_activate(g, 0)) * eu + 2.0 ** -20 * np.abs(h) + 2.0 ** -23 * largest
+        if fmt == 1:
+            off += 2.0 ** -40 * np.abs(h).max()
+        ref = dv[0] @ h
+        tol = 0.5 * ulp16(ref) * (1 + 2.0 ** -8) + np.abs(dv[0]) @ (off + (I / 16 + 170) * 2.0 ** -23 * np.abs(h))
+        assert (np.abs(y[t].cpu().numpy().astype(np.float64) - ref) <= tol).all()

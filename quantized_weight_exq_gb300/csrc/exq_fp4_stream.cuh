@@ -346,10 +346,13 @@ __device__ __forceinline__ void find_experts(const Args& a, Experts* e, unsigned
 }
 static_assert(kMaxPairs <= threads_of(1, false), "a place a thread");
 
+// v times the logistic function of v, or of 2 u, which is (1 + tanh u) / 2: where u is
+// very negative 1 + tanh u is a difference of two numbers near 1, and this is not.
+// (__expf is off by 2 + |1.2 t| of its last bits: less than 2^-16 as far as t = -88,
+// below which the result is zero.)
 __device__ __forceinline__ float activate(float v, int act) {
-  if (act == EXQ_ACT_SILU) return v / (1.f + __expf(-v));
-  const float u = 0.7978845608028654f * (v + 0.044715f * v * v * v);
-  return 0.5f * v * (1.f + tanhf(u));
+  const float t = act == EXQ_ACT_SILU ? v : 1.5957691216057308f * (v + 0.044715f * v * v * v);
+  return v / (1.f + __expf(-t));
 }
 
 // bit number j (from 0) that is set

@@ -448,3 +448,34 @@ def test_h_of_mixed_sizes(env, fmt, T):
         ref = dv[0] @ h
         tol = 0.5 * ulp16(ref) * (1 + 2.0 ** -8) + np.abs(dv[0]) @ (off + (I / 16 + 170) * 2.0 ** -23 * np.abs(h))
         assert (np.abs(y[t].cpu().numpy().astype(np.float64) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("T", [1, 4, 16])
+def test_gelu_of_what_it_hardly_lets_through(env, fmt, T):
+    # a token whose gate is -6 to -2 everywhere: the result is small, and as precise as another
+    exq, torch = env
+    rng = np.random.default_rng(T + fmt)
+    E, D, I, block = 4, 32, 64, O.FP4_BLOCK[fmt]
+    gate, up = np.zeros((E, I, D)), np.zeros((E, I, D))
+    gate[:, :, 0] = 8 + np.array([4, 5, 6, 7])[:, None]          # -2, -3, -4, -6
+    up[:, :, 0] = rng.integers(2, 8, (E, I))
+    down = rng.integers(1, 8, (E, D, I))                         # of one sign: no sum cancels
+    factors = 2.0 ** np.array([0, 4, 8, 28])                     # of down: results in fp16's range
+    scale = lambda rows, K: np.full((E, rows, K // block), 0x38 if fmt == 1 else 127)  # noqa: E731
+    parts = [(gate, scale(I, D), None), (up, scale(I, D), None), (down, scale(D, I), factors)]
+    if fmt == 2:
+        parts[2] = (down, scale(D, I) + np.int64(np.log2(factors))[:, None, None], None)
+    layer, (gv, uv, dv) = _layer_of(exq, torch, fmt, parts, 1, act=1)
+    for first in range(E if T == 1 else 1):
+        ids = ((first + np.arange(T)) % E).astype(np.int32)[:, None]
+        x = np.zeros((T, D), np.float16)
+        x[:, 0] = 1
+        y, _, _ = exq.exq_moe(layer, torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), torch.ones(T, 1, device="cuda"))
+        for t in range(T):
+            e = ids[t, 0]
+            g, u = gv[e, :, 0], uv[e, :, 0]
+            ref = dv[e] @ (g / (1 + np.exp(-2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3))) * u)
+            # the exponent is 25 at most, off by four roundings of 2^-24 of itself (6e-6), its exponential by 31 * 2^-23 (4e-6): 2^-16
+            tol = 0.5 * ulp16(ref) * (1 + 2.0 ** -8) + (2.0 ** -16 + (I / 16 + 170) * 2.0 ** -23) * np.abs(ref)
+            assert (np.abs(y[t].cpu().numpy().astype(np.float64) - ref) <= tol).all(), (e, y[t], ref)

@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last = abort_flag + 1;
+  volatile int* there = last + 1;  // (a word of its own: `last` may still be read, of the tile before)
   unsigned* used = reinterpret_cast<unsigned*>(tmem_slot + 4);
   Experts* ex = reinterpret_cast<Experts*>(used + kMaxExperts / 32);
 
@@ -889,12 +890,10 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
           const int all = n == static_cast<unsigned>(b1 - b0) && !*abort_flag;
           if (all) a.counters[tile] = 0u;
           __threadfence();
-          *last = all;
+          *there = all;  // once: of the CTA's last tile
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        const bool all = *last != 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        return all;
+        return *there != 0;
       };
       // after this CTA's part is written: whether all are
       auto last_of_tile = [&]() {

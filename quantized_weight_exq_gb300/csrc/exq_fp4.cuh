@@ -172,6 +172,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return false;
 }
 
+// Waits for the copies of the last n of the stages 0 .. issued - 1 that this warp has issued: all have landed before the CTA may
+// exit. Each warp that issues copies waits for its own: after a timeout one may be ahead of another, and a stage that lacks the
+// other's share does not complete. What is waited then is still a thousand times what a copy takes.
+__device__ __forceinline__ void await_issued(const uint64_t* full, int issued, int n, int limit) {
+  for (int i = max(0, issued - n); i < issued; ++i)
+    for (int r = 0; r < min(limit, 1 << 16); ++r)
+      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % n]), (i / n) & 1))) break;
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"

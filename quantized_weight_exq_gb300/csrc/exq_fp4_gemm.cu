@@ -304,13 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    // every issued stage's copies land before the CTA may exit
-    for (int i = max(0, issued - stage.n); i < issued; ++i)
-      for (int r = 0; r < p.wait_limit; ++r)
-        if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % stage.n]), (i / stage.n) & 1))) break;
+    await_issued(full, issued, stage.n, p.wait_limit);
   } else if (warp == 18) {
     // ------------------------------------------------------------ scales
     const bool leader = elect_one();
+    int issued = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!p.starve) {
       Turn turn;
@@ -344,9 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           sb2 += kTilesUnit * 512;
           __syncwarp();
           turn.next(stage.n);
+          ++issued;
         }
       }
     }
+    await_issued(full, issued, stage.n, p.wait_limit);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs, by the first CTA
     if (rank == 0) {

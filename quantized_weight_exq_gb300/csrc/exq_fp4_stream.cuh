@@ -619,10 +619,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
         }
       }
     }
-    // every issued stage's copies land before the CTA may exit
-    for (int i = max(0, issued - n_stages); i < issued; ++i)
-      for (int r = 0; r < a.wait_limit; ++r)
-        if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&full[i % n_stages]), (i / n_stages) & 1))) break;
+    await_issued(full, issued, n_stages, a.wait_limit);
   } else if (HERE && (warp == 6 || warp > 10)) {
     // ------------------------------------------------------------ rows to parts
     if constexpr (MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // for h
@@ -710,6 +707,7 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
   } else if (!HERE && warp == 6) {
     // ------------------------------------------------------------ the tokens' parts
     const bool leader = elect_one();
+    int issued = 0;
     // they come from the launch before
     if constexpr (MODE != kUp) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!a.starve) {
@@ -745,10 +743,12 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
           }
           __syncwarp();
           turn.next(n_stages);
+          ++issued;
         }
         at.next(a, n_experts);
       }
     }
+    await_issued(full, issued, n_stages, a.wait_limit);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one();

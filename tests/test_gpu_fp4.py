@@ -457,3 +457,26 @@ def test_quantize_with_a_factor_of_64_bits(env, factor):
     out = exq.Fp4Matrix(torch.zeros(64, 4096, dtype=torch.uint8, device="cuda"),
                         torch.zeros(exq.exq_fp4_scale_bytes(1, 64, 8192), dtype=torch.uint8, device="cuda"), 1, factor)
     _check_quantised(exq.exq_fp4_quantize(torch.from_numpy(x).cuda(), 1, out=out), x, 1, factor)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,units", [(2, 10), (3, 6), (4, 5), (5, 4), (6, 3), (7, 2), (8, 2)])
+def test_gemv_splits_rows_of_several_units(env, fmt, M, units):
+    # few rows that the product's own warps split (M * units of a CTA at most 20), with several units a CTA: the rows of a unit
+    # go to the four warps in turn from unit to unit, and ten units are more than there are stages
+    exq, torch = env
+    rng = np.random.default_rng(10 * M + fmt)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    K = 13 * 256 - 224
+    N = (units * sms - 5) // 13 * 128 - 120
+    count = -(-N // 128) * -(-K // 256)
+    assert (units - 1) * sms < count <= units * sms and M * count <= 20 * sms
+    w, wv = _quantised(exq, torch, rng, N, K, fmt, 0.37 if fmt == 1 else 1.0)
+    x = _activations(rng, M, K, 2)
+    xd = torch.from_numpy(x).cuda()
+    y = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+    ws = torch.zeros(exq.exq_fp4_gemv_workspace_size(w, M), dtype=torch.uint8, device="cuda")
+    exq.exq_fp4_gemv(w, xd, out=y, workspace=ws)
+    assert exq.exq_get_last_device_error() == exq.EXQ_OK
+    assert not ws[:exq.FP4_COUNTER_BYTES].any()
+    _check_product(y, x.astype(np.float64), wv, 160)

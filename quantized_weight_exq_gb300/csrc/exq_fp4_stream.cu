@@ -257,15 +257,18 @@ exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
 
 // Whether the streaming kernel splits the rows itself: one always, and up to
 // eight of x where a CTA has few units. The launch that splits them takes 0.5
-// to 3.5 us; splitting a row in every CTA takes each of its units up to 60 ns
-// longer. Here and by a launch: 4 x 1024 x 8192 (7 row units a CTA) 7.7 and
-// 11.2 us, 2 x 8192 x 4096 (13) 10.1 and 10.8, 6 x 4096 x 4096 (20) 8.9 and
-// 9.6, 3 x 8192 x 4096 (20) 10.6 and 10.9, 4 x 8192 x 4096 (27) 11.5 and 10.9,
-// 2 x 8192 x 8192 (27) 14.3 and 13.7, 8 x 28672 x 8192 (377) 52 and 29. One
-// token of 8 of 128 experts of 1536 x 4096: 36.9 and 39.5 us; two and more
-// tokens of other layers gained as often as they lost.
+// to 1 us; splitting a row in every CTA takes each of its units up to 60 ns
+// longer. Both sides, us, here and by a launch, at (units, rows times units) of a
+// CTA: 4 x 4096 x 3584 (2.9, 12) 8.2 and 9.2, 2 x 4096 x 11008 (9.1, 18) 11.2 and
+// 11.7, 6 x 4096 x 4096 (3.4, 20.2) 8.7 and 9.3, 4 x 4096 x 6656 (5.5, 22) 10.0 and
+// 10.8, 8 x 2048 x 6912 (2.8, 23) 9.4 and 10.2, 3 x 11008 x 3584 (7.9, 23.8) 11.7
+// and 11.8; 2 x 8192 x 6144 (10.1, 20.2) 12.0 and 11.9, 2 x 11008 x 5120 (11.3, 23)
+// 13.2 and 12.7, 3 x 8192 x 5120 (8.4, 25) 11.6 and 11.4, 4 x 8192 x 4096 (6.7,
+// 27) 11.2 and 10.8, 8 x 8192 x 5120 (8.4, 67) 14.9 and 12.0. One token of 8 of
+// 128 experts of 1536 x 4096: 36.9 and 39.5 us; two and more tokens of other
+// layers gained as often as they lost.
 bool splits(int mode, int M, long long units, int ctas) {
-  return M == 1 || (mode == kGemv && M <= 8 && M * units <= 20ll * ctas);
+  return M == 1 || (mode == kGemv && M <= 8 && units <= 10ll * ctas && M * units <= 24ll * ctas);
 }
 
 template <int FMT, int MODE, int NT, bool HERE>

@@ -460,9 +460,9 @@ def test_quantize_with_a_factor_of_64_bits(env, factor):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,units", [(2, 10), (3, 6), (4, 5), (5, 4), (6, 3), (7, 2), (8, 2)])
+@pytest.mark.parametrize("M,units", [(2, 10), (3, 6), (4, 5), (5, 4), (6, 3), (7, 2), (8, 2), (3, 8), (6, 4), (7, 3), (8, 3)])
 def test_gemv_splits_rows_of_several_units(env, fmt, M, units):
-    # few rows that the product's own warps split (M * units of a CTA at most 20), with several units a CTA: the rows of a unit
+    # few rows that the product's own warps split (a CTA has at most 10 units and 24 rows of units), with several units a CTA: the rows of a unit
     # go to the four warps in turn from unit to unit, and ten units are more than there are stages
     exq, torch = env
     rng = np.random.default_rng(10 * M + fmt)
@@ -470,7 +470,7 @@ def test_gemv_splits_rows_of_several_units(env, fmt, M, units):
     K = 13 * 256 - 224
     N = (units * sms - 5) // 13 * 128 - 120
     count = -(-N // 128) * -(-K // 256)
-    assert (units - 1) * sms < count <= units * sms and M * count <= 20 * sms
+    assert (units - 1) * sms < count <= units * sms and units <= 10 and M * count <= 24 * sms
     w, wv = _quantised(exq, torch, rng, N, K, fmt, 0.37 if fmt == 1 else 1.0)
     x = _activations(rng, M, K, 2)
     xd = torch.from_numpy(x).cuda()

@@ -93,15 +93,3 @@ def moe_activate(g, act):
         if act == 0:
             return g / (1 + np.exp(-g))
         return 0.5 * g * (1 + np.tanh(np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)))
-
-
-def moe_experts(x, ids, weights, gate, up, down, act=0):
-    """y [T, D]; gate, up, down are functions from an expert's index to its float64 matrix. ids outside the experts are skipped."""
-    x = np.asarray(x, np.float64)
-    y = np.zeros_like(x)
-    for t in range(x.shape[0]):
-        for e, w in zip(ids[t], weights[t]):
-            if e >= 0:
-                h = moe_activate(gate(e) @ x[t], act) * (up(e) @ x[t])
-                y[t] += float(w) * (down(e) @ h)
-    return y

@@ -144,20 +144,9 @@ __device__ __forceinline__ bool elect_one() {
 
 constexpr int kFp4WaitLimit = 1 << 22;  // try_wait rounds before giving up
 
-// Bounded wait of one thread or of a whole warp (every lane tests; a vote
-// keeps the lanes together). False, with the timeout recorded in *err and
-// *abort_flag set for the CTA's other roles, if the phase does not complete.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int limit,
-                                          unsigned* err) {
-  for (int i = 0; i < limit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  atomicOr(err, kDevErrTimeout);
-  *abort_flag = 1;
-  return false;
-}
-
+// Bounded wait of a whole warp (every lane tests; a vote keeps the lanes
+// together). False, with the timeout recorded in *err and *abort_flag set for the
+// CTA's other roles, if the phase does not complete.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int limit,
                                                unsigned* err) {
   for (int i = 0; i < limit; ++i) {

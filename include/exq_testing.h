@@ -1,8 +1,8 @@
 /*
- * exq_testing.h -- test hook of libexq for failure detection. It has no
- * counterpart in the ExLlamaV2 pages: it exists so that a test can watch a
- * bounded device-side wait give up without faulting, trapping or hanging
- * the GPU.
+ * exq_testing.h -- test hooks of libexq. They have no counterpart in the
+ * ExLlamaV2 pages: one lets a test watch a bounded device-side wait give up
+ * without faulting, trapping or hanging the GPU, the others show it arithmetic
+ * that kernels do.
  */
 #ifndef EXQ_TESTING_H
 #define EXQ_TESTING_H
@@ -26,6 +26,14 @@ extern "C" {
  * wait_rounds = 0 turns the hook off (the default). Host-side, process-wide,
  * thread-safe; it affects launches made after it returns. */
 void exq_testing_starve(int32_t wait_rounds);
+
+/* How the few-row product and the experts divide a call's units over CTAs, as
+ * their kernels compute it: CTA cta (0 .. ctas) of ctas has the units from
+ * exq_testing_first_unit(cta) up to that of cta + 1; exq_testing_unit_owner is
+ * the CTA that has `unit`, 0 <= unit < n_units, 1 <= ctas <= n_units. -1 for
+ * anything else. Host-side. */
+int64_t exq_testing_first_unit(int32_t cta, int64_t n_units, int32_t ctas);
+int32_t exq_testing_unit_owner(int64_t unit, int64_t n_units, int32_t ctas);
 
 #ifdef __cplusplus
 }

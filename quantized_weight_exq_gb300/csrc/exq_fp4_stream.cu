@@ -475,6 +475,14 @@ exq_status launch_moe(const exq_moe_layer& l, const uint16_t* x, int T, int32_t*
   return launch_stream<kDown>(fmt, here, md, md, md, a, sms, device, stream);
 }
 
+extern "C" int64_t exq_testing_first_unit(int32_t cta, int64_t n_units, int32_t ctas) {
+  return ctas >= 1 && cta >= 0 && cta <= ctas && n_units >= ctas ? first_unit(cta, n_units, ctas) : -1;
+}
+
+extern "C" int32_t exq_testing_unit_owner(int64_t unit, int64_t n_units, int32_t ctas) {
+  return ctas >= 1 && unit >= 0 && unit < n_units && n_units >= ctas ? owner(unit, n_units, ctas) : -1;
+}
+
 unsigned take_fp4_stream_errors(cudaStream_t stream) {
   unsigned v = 0, zero = 0;
   if (cudaMemcpyFromSymbolAsync(&v, g_stream_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return ~0u;

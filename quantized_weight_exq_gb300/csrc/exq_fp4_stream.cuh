@@ -408,9 +408,11 @@ struct Place {
   }
 };
 
-// The CTA that has unit u, of `ctas` that divide n units: CTA b has units
-// [b n / ctas, (b + 1) n / ctas).
-__device__ __forceinline__ int owner(long long u, long long n, int ctas) {
+// CTA b of `ctas` that divide n units has those from first_unit(b) up to
+// first_unit(b + 1); `owner` is the one that has unit u.
+__host__ __device__ __forceinline__ long long first_unit(int b, long long n, int ctas) { return b * n / ctas; }
+
+__host__ __device__ __forceinline__ int owner(long long u, long long n, int ctas) {
   if (n * ctas < (1LL << 31)) return (static_cast<int>(u + 1) * ctas - 1) / static_cast<int>(n);
   return static_cast<int>(((u + 1) * ctas - 1) / n);
 }
@@ -542,8 +544,8 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
     }
   }
   const int ctas = static_cast<int>(n_units < gridDim.x ? n_units : gridDim.x);
-  const long long u0 = ctas > 0 ? blockIdx.x * n_units / ctas : 0;
-  const int n_mine = static_cast<int>(blockIdx.x) < ctas ? static_cast<int>((blockIdx.x + 1) * n_units / ctas - u0) : 0;
+  const long long u0 = ctas > 0 ? first_unit(blockIdx.x, n_units, ctas) : 0;
+  const int n_mine = static_cast<int>(blockIdx.x) < ctas ? static_cast<int>(first_unit(blockIdx.x + 1, n_units, ctas) - u0) : 0;
 
   // the ring and the buffers of sums go by the most tokens that a matrix of the call has
   const int off_xs = kOffX + 1024 * most_tokens;                        // gemv: the parts' scale tiles
@@ -601,8 +603,8 @@ __global__ void __launch_bounds__(threads_of(NT, HERE), 1)
         const long long n_down = units_of(d, n_experts);
         const int down_ctas = static_cast<int>(n_down < gridDim.x ? n_down : gridDim.x);
         if (static_cast<int>(blockIdx.x) < down_ctas) {
-          const long long d0 = blockIdx.x * n_down / down_ctas;
-          const int n = min(kAhead, static_cast<int>((blockIdx.x + 1) * n_down / down_ctas - d0));
+          const long long d0 = first_unit(blockIdx.x, n_down, down_ctas);
+          const int n = min(kAhead, static_cast<int>(first_unit(blockIdx.x + 1, n_down, down_ctas) - d0));
           Place<kDown> to(d, n_experts, d0);
           for (int i = 0; i < n; ++i) {
             if (leader) {

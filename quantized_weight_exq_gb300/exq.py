@@ -47,7 +47,7 @@ EXPORTED = (
     "exq_kv_copy_pages", "exq_pages_alloc", "exq_pages_free", "exq_pages_fork", "exq_pages_compact",
     "exq_fp4_scale_bytes", "exq_pack_fp4", "exq_fp4_quantize", "exq_fp4_dequantize", "exq_fp4_gemm",
     "exq_fp4_gemv_workspace_size", "exq_fp4_gemv", "exq_moe_workspace_size", "exq_moe",
-    "exq_testing_starve",
+    "exq_testing_starve", "exq_testing_first_unit", "exq_testing_unit_owner",
 )
 
 # most layers one exq_gemv_multi call takes (EXQ_GEMV_MAX_LAYERS)
@@ -158,6 +158,8 @@ def _load():
         "exq_status_string": (ctypes.c_char_p, [st]),
         "exq_get_last_device_error": (st, [P]),
         "exq_testing_starve": (None, [i32]),
+        "exq_testing_first_unit": (i64, [i32, i64, i32]),
+        "exq_testing_unit_owner": (i32, [i64, i64, i32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

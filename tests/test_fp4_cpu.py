@@ -184,3 +184,19 @@ def test_factor_has_64_bits(exq):
     assert O.fp4_scale_values(scales, 1)[0, 0] == 1.25 and codes[0, 0] == 2
     codes, _ = O.fp4_quantize(x, 1, np.nextafter(0.025, 0))      # the next number down: above the tie
     assert codes[0, 0] == 3
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 148, 152])
+def test_units_of_the_kernels_have_one_owner(exq, ctas):
+    # the kernels' own arithmetic, on both sides of where it changes to 64 bits (units times CTAs = 2^31)
+    lib = exq.exq._lib
+    rng = np.random.default_rng(ctas)
+    border = 2 ** 31 // ctas
+    for n in {ctas, ctas + 1, 3 * ctas - 1, 7168, 8 * 32767, border - 1, border, border + 1, 2 ** 31 - 257, 2 ** 33, *rng.integers(ctas, 10 ** 6, 20).tolist()}:
+        start = [lib.exq_testing_first_unit(b, n, ctas) for b in range(ctas + 1)]
+        assert start[0] == 0 and start[-1] == n and all(a < b for a, b in zip(start, start[1:]))
+        for b in range(ctas):
+            for u in {start[b], start[b + 1] - 1, (start[b] + start[b + 1]) // 2}:
+                assert lib.exq_testing_unit_owner(u, n, ctas) == b
+    assert lib.exq_testing_first_unit(0, ctas - 1, ctas) == -1 and lib.exq_testing_first_unit(ctas + 1, ctas, ctas) == -1
+    assert lib.exq_testing_unit_owner(ctas, ctas, ctas) == -1 and lib.exq_testing_unit_owner(0, 0, 0) == -1

@@ -682,8 +682,7 @@ exq_status exq_pack_fp4(const uint8_t* codes, const uint8_t* scales, int32_t for
  * and each code is the e2m1 number nearest to x / (s factor), ties to the even
  * code, at most 6 in magnitude, with x's sign. Both are decided on the
  * quotients in 64 bits (6 factor, s factor and the quotients each rounded to
- * nearest); of a factor that is a number of 32 bits these are no nearer to a
- * tie, or farther from it, than the exact ones. A block that holds a NaN or an infinity gets the NaN
+ * nearest), which for a factor of 32 bits is what the exact ones give. A block that holds a NaN or an infinity gets the NaN
  * scale and codes 0. rows = 0 launches nothing.
  * EXQ_ERR_INVALID_ARG for bad pointers (16 bytes), sizes or a factor out of range. */
 exq_status exq_fp4_quantize(const uint16_t* x, const exq_fp4_matrix* out, void* stream);

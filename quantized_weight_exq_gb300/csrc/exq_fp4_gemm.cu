@@ -36,8 +36,9 @@
 // The launch may begin while the one before it ends (its set-up takes 1 us):
 // nothing is read or written before griddepcontrol.wait.
 //
-// 2048 x 28672 x 8192: E4M3 149 us (6.5 PFLOPS), E8M0 143; 1777 x 11008 x 4096
-// 36 us (with the quantiser of a). Bound by what an SM takes in: 38 KB for 512
+// 2048 x 28672 x 8192: E4M3 149 us (6.5 PFLOPS), E8M0 143, in runs of some 20 ms;
+// after a second of nothing else the power limit has the SMs at 1.63 GHz, and E4M3
+// takes 164. 1777 x 11008 x 4096 36 us (with the quantiser of a). Bound by what an SM takes in: 38 KB for 512
 // clocks of MMAs are 74 bytes a clock, and copies alone reach 54 to 56. (A
 // quarter of the codes brought by multicast inside the pair: 2 % less time.)
 #include <algorithm>

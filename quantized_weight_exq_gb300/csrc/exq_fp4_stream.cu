@@ -153,7 +153,8 @@ __device__ __forceinline__ void route(const PrepareArgs& a) {
 
   // Each expert's place is the number of those before it: larger ones, and equal ones of a lower index. All experts of some
   // tokens are compared with all at once, which for up to 128 of them is sooner done than top_k searches one after the other
-  // (3 us, with the loads of code that runs once).
+  // (3 us, with the loads of code that runs once). Beyond that these comparisons, T E^2 in one CTA, are most of a small layer: 16
+  // tokens' routing adds 6, 16, 50 and 177 us with 64, 128, 256 and 512 experts, one token's 2, 3, 5 and 13 (D = 2048).
   constexpr int kHeld = 1024;
   __shared__ unsigned held[kHeld];    // keys of a batch of tokens
   __shared__ float chosen[16][16];

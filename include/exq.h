@@ -757,7 +757,8 @@ size_t exq_moe_workspace_size(const exq_moe_layer* layer, int32_t T);
  * [T, D], 1 <= T <= 16:
  *   logits = x . router^T (fp32); ids[t] = the top_k largest, largest first,
  *   ties (and NaNs, which count as -infinity) to the lowest index;
- *   weights[t][j] = exp(logit - max) / sum (see renorm);
+ *   weights[t][j] = exp(logit - max) / sum (see renorm; NaN where a NaN is
+ *   among the logits that the sum goes over);
  *   y[t] = fp16_RNE(sum_j weights[t][j] * (act(x gate^T) * (x up^T)) down^T)
  * with the experts' products over x as it is and fp32 sums. What lies between
  * the products, h, is held to 2^-23 of the largest of its block of 16 or 32,

@@ -98,8 +98,8 @@ struct Walk {
 // (Six blocks an SM, 40 registers: with 44 E4M3 takes 122 us, not 111.)
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 6) quantize_kernel(const uint16_t* __restrict__ x, uint2* __restrict__ codes,
-                                                            uint32_t* __restrict__ scales, int rows, int K, bool wide,
-                                                            const __grid_constant__ Factor f) {
+                                                               uint32_t* __restrict__ scales, int rows, int K, bool wide,
+                                                               const __grid_constant__ Factor f) {
   constexpr int kPer = fp4_tile_k(FMT) / 16;  // threads of one scale word: 4 or 8
   begin();
   const int words = (K + fp4_tile_k(FMT) - 1) / fp4_tile_k(FMT);

@@ -258,9 +258,9 @@ exq_status launch_split_h(int format, PrepareArgs p, cudaStream_t stream) {
 
 // Whether the streaming kernel splits the rows itself: one always, and up to
 // eight of x where a CTA has few units. The launch that splits them takes 0.5
-// to 1 us; splitting a row in every CTA takes each of its units up to 60 ns
+// to 3.5 us; splitting a row in every CTA takes each of its units up to 60 ns
 // longer. Both sides, us, here and by a launch, at (units, rows times units) of a
-// CTA: 4 x 4096 x 3584 (2.9, 12) 8.2 and 9.2, 2 x 4096 x 11008 (9.1, 18) 11.2 and
+// CTA: 4 x 1024 x 8192 (1.7, 7) 7.7 and 11.2, 4 x 4096 x 3584 (2.9, 12) 8.2 and 9.2, 2 x 4096 x 11008 (9.1, 18) 11.2 and
 // 11.7, 6 x 4096 x 4096 (3.4, 20.2) 8.7 and 9.3, 4 x 4096 x 6656 (5.5, 22) 10.0 and
 // 10.8, 8 x 2048 x 6912 (2.8, 23) 9.4 and 10.2, 3 x 11008 x 3584 (7.9, 23.8) 11.7
 // and 11.8; 2 x 8192 x 6144 (10.1, 20.2) 12.0 and 11.9, 2 x 11008 x 5120 (11.3, 23)

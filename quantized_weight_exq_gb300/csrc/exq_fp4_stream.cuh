@@ -45,7 +45,7 @@
 // writes its part, the last to arrive (a counter) adds them in CTA order, so
 // that the result does not depend on who it is.
 //
-// One row of 28672 x 8192, E8M0: 25.7 us (4.9 TB/s; 6.4 while it streams), of
+// One row of 28672 x 8192, E8M0: 25.5 us (4.9 TB/s; 6.4 while it streams), of
 // 4096 x 4096: 7.9 us, which is set-up, the first bytes' way and the last sums';
 // sixteen rows of 28672 x 8192, E4M3: 29 us. Experts: 5 tokens of 8 of 128 of
 // 1536 x 4096, E4M3, 84.4 us (4.4 TB/s, 7 while gate and up stream).
